@@ -6,7 +6,10 @@ PyTorch (device memory, pinned host memory, streams) and passes their
 addresses.  There is no CPU fallback: without the built library every call
 raises.
 
+    embed             rows of an embedding table, scaled (and embed_backward)
     route_topk        softmax -> top-k -> renormalised weights
+    route_balance     route_topk with a balance loss and per-expert counts
+                      (and route_backward, the logits' gradient)
     dispatch_permute  expert-major, capacity-bounded permutation (BF16 / E4M3)
     Pool              paged stash: push / pop / reset / overflow read-out,
                       calibration and lazy growth (over an Arena)
@@ -28,9 +31,10 @@ FLAG_RECORD_OVERFLOW = 0x4
 FLAG_BAD_COUNT = 0x8
 FLAG_BAD_INDEX = 0x10
 FLAG_CORRUPT = 0x20
-DTYPE_BF16, DTYPE_E4M3 = 0, 1
+DTYPE_BF16, DTYPE_E4M3, DTYPE_F32 = 0, 1, 2
 
-__all__ = ["route_topk", "dispatch_permute", "dispatch_scratch_bytes", "combine_unpermute", "combine_backward",
+__all__ = ["embed", "embed_backward", "embed_scratch_bytes", "route_balance", "route_balance_scratch_bytes",
+           "route_backward", "route_topk", "dispatch_permute", "dispatch_scratch_bytes", "combine_unpermute", "combine_backward",
            "dispatch_backward", "cast_e4m3", "Pool", "Arena", "APError", "lib", "launch_count"]
 
 
@@ -67,6 +71,191 @@ def route_topk(logits: torch.Tensor, k: int, idx: torch.Tensor | None = None, w:
         w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
     check(lib().ap_route_topk(_p(logits), T, E, k, _p(idx), _p(w), _stream(stream)), "route_topk")
     return idx, w
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor that belongs to the stream the call runs on, so that its memory is not handed
+    out again before that stream is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _groups(T: int, group_tokens: int) -> int:
+    return -(-T // (group_tokens or T)) if T else 0
+
+
+def _mask(mask: torch.Tensor | None, T: int):
+    if mask is None:
+        return
+    if mask.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"mask must be bool or uint8, got {mask.dtype}")
+    _need(mask, mask.dtype, "mask")
+    if mask.shape != (T,):
+        raise ValueError(f"mask must be [{T}], got {list(mask.shape)}")
+
+
+def _shape(t: torch.Tensor | None, shape: tuple, name: str):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def route_balance_scratch_bytes(T: int, E: int, group_tokens: int = 0) -> int:
+    n = ctypes.c_int64(0)
+    check(lib().ap_route_balance_scratch_bytes(T, E, group_tokens, ctypes.byref(n)), "route_balance_scratch_bytes")
+    return n.value
+
+
+def route_balance(logits: torch.Tensor, k: int, coef: float = 1.0, group_tokens: int = 0,
+                  mask: torch.Tensor | None = None, out: dict | None = None, stream=None) -> dict:
+    """``route_topk`` with the balance loss of each group of ``group_tokens``
+    tokens (0: all tokens are one group): a dict of ``idx`` ([T, k] int32) and
+    ``w`` ([T, k] float32) as route_topk's, ``counts`` ([G, E] int32, pairs per
+    expert), ``prob`` ([G, E] float32, mean softmax probability), ``slope``
+    ([G, E] float32, d loss / d p, for ``route_backward``), ``loss`` (float32
+    scalar tensor, ``coef`` x the mean over groups of E sum_e share_e prob_e)
+    and ``scratch``.  ``mask`` ([T] bool or uint8): tokens that count.  Pass
+    ``out`` (such a dict) to reuse buffers."""
+    _need(logits, torch.float32, "logits")
+    T, E = logits.shape
+    _mask(mask, T)
+    G = _groups(T, group_tokens)
+    dev = logits.device
+    o = dict(out) if out is not None else {}
+    for name, shape, dtype in (("idx", (T, k), torch.int32), ("w", (T, k), torch.float32),
+                               ("counts", (G, E), torch.int32), ("prob", (G, E), torch.float32),
+                               ("slope", (G, E), torch.float32), ("loss", (), torch.float32)):
+        if name in o:
+            _need(o[name], dtype, name)
+            _shape(o[name], shape, name)
+        else:
+            o[name] = _empty(shape, dtype, dev, stream)
+    sb = route_balance_scratch_bytes(T, E, group_tokens)
+    if "scratch" not in o or o["scratch"].numel() < sb:
+        o["scratch"] = _empty(sb, torch.uint8, dev, stream)
+    check(lib().ap_route_balance(_p(logits), T, E, k, group_tokens, _p(mask), coef, _p(o["idx"]), _p(o["w"]),
+                                 _p(o["counts"]), _p(o["prob"]), _p(o["slope"]), _p(o["loss"]), _p(o["scratch"]),
+                                 o["scratch"].numel(), _stream(stream)), "route_balance")
+    return o
+
+
+def route_backward(logits: torch.Tensor, idx: torch.Tensor | None = None, w: torch.Tensor | None = None,
+                   dw: torch.Tensor | None = None, slope: torch.Tensor | None = None,
+                   dloss: torch.Tensor | None = None, group_tokens: int = 0, mask: torch.Tensor | None = None,
+                   dlogits: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """dlogits [T, E] float32 from the gradient ``dw`` of the routing weights
+    (with the forward pass's ``idx`` and ``w``) and from the balance loss (with
+    its ``slope`` and, if not 1, ``dloss``); either may be left out."""
+    _need(logits, torch.float32, "logits")
+    T, E = logits.shape
+    _mask(mask, T)
+    k = 1
+    if dw is not None:
+        if idx is None or w is None:
+            raise ValueError("dw needs idx and w")
+        _need(dw, torch.float32, "dw")
+        _need(idx, torch.int32, "idx")
+        _need(w, torch.float32, "w")
+        k = dw.shape[1]
+        for t, name in ((dw, "dw"), (idx, "idx"), (w, "w")):
+            _shape(t, (T, k), name)
+    if slope is not None:
+        _need(slope, torch.float32, "slope")
+        _shape(slope, (_groups(T, group_tokens), E), "slope")
+    if dloss is not None:
+        _need(dloss, torch.float32, "dloss")
+        if dloss.numel() != 1:
+            raise ValueError("dloss must hold one value")
+    if dlogits is None:
+        dlogits = _empty((T, E), torch.float32, logits.device, stream)
+    else:
+        _need(dlogits, torch.float32, "dlogits")
+        _shape(dlogits, (T, E), "dlogits")
+    check(lib().ap_route_backward(_p(logits), T, E, k, _p(idx) if dw is not None else None,
+                                  _p(w) if dw is not None else None, _p(dw), _p(slope), _p(dloss), group_tokens,
+                                  _p(mask), _p(dlogits), _p(status), _stream(stream)), "route_backward")
+    return dlogits
+
+
+_ROW_TYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+
+def _need_rows(t: torch.Tensor, name: str):
+    """[n, H] BF16 or FP32 rows, each contiguous; the rows may lie apart."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _ROW_TYPES:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be [rows, H] with contiguous rows that do not overlap")
+
+
+def _pitch(t: torch.Tensor) -> int:
+    return max(t.stride(0), t.shape[1])
+
+
+def _need_ids(ids: torch.Tensor) -> int:
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+    _need(ids, ids.dtype, "ids")
+    if ids.dim() != 1:
+        raise ValueError("ids must be [T]")
+    return ids.shape[0]
+
+
+def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, dtype: torch.dtype | None = None,
+          out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[t] = scale * table[ids[t]]: [T, H] of ``dtype`` (default: the
+    table's) for a BF16 or FP32 table [V, H] and int32 or int64 ids [T].  Rows
+    of table and out may lie apart.  An id outside [0, V) gives zeros and sets
+    FLAG_BAD_INDEX in ``status``."""
+    _need_rows(table, "table")
+    T = _need_ids(ids)
+    V, H = table.shape
+    if out is None:
+        out = _empty((T, H), dtype if dtype is not None else table.dtype, table.device, stream)
+    _need_rows(out, "out")
+    _shape(out, (T, H), "out")
+    check(lib().ap_embed(_p(table), V, _pitch(table), _ROW_TYPES[table.dtype], _p(ids), ids.element_size(), T, H,
+                         scale, _p(out), _pitch(out), _ROW_TYPES[out.dtype], _p(status), _stream(stream)), "embed")
+    return out
+
+
+def embed_scratch_bytes(T: int, V: int, H: int) -> int:
+    n = ctypes.c_int64(0)
+    check(lib().ap_embed_scratch_bytes(T, V, H, ctypes.byref(n)), "embed_scratch_bytes")
+    return n.value
+
+
+def embed_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1.0, padding_idx: int | None = None,
+                   dtable: torch.Tensor | None = None, accumulate: bool = False, dtype: torch.dtype = torch.float32,
+                   scratch: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """Gradient of ``embed``'s table: dtable [V, H], for every id the sum of its
+    tokens' rows of dout [T, H] times ``scale`` (FP32 sums), written whole or,
+    with ``accumulate``, added to ``dtable``.  Tokens whose id is
+    ``padding_idx`` add nothing.  ``scratch``: a uint8 tensor of
+    ``embed_scratch_bytes(T, V, H)`` bytes to reuse."""
+    _need_rows(dout, "dout")
+    T = _need_ids(ids)
+    if dout.shape[0] != T:
+        raise ValueError(f"dout has {dout.shape[0]} rows for {T} ids")
+    H = dout.shape[1]
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate needs dtable")
+        dtable = _empty((V, H), dtype, dout.device, stream)
+    _need_rows(dtable, "dtable")
+    _shape(dtable, (V, H), "dtable")
+    sb = embed_scratch_bytes(T, V, H)
+    if scratch is None or scratch.numel() < sb:
+        scratch = _empty(sb, torch.uint8, dout.device, stream)
+    check(lib().ap_embed_backward(_p(dout), _pitch(dout), _ROW_TYPES[dout.dtype], _p(ids), ids.element_size(), T, H, V,
+                                  -1 if padding_idx is None else padding_idx, scale, int(accumulate), _p(dtable),
+                                  _pitch(dtable), _ROW_TYPES[dtable.dtype], _p(scratch), scratch.numel(), _p(status),
+                                  _stream(stream)), "embed_backward")
+    return dtable
 
 
 def launch_count() -> int:

@@ -13,6 +13,7 @@ LIB_PATH = os.path.join(HERE, "libap.so")
 
 P = ctypes.c_void_p
 i32, i64, u32, u64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64
+f32 = ctypes.c_float
 
 
 class PoolConfig(ctypes.Structure):
@@ -45,6 +46,12 @@ SIGNATURES = {
     "ap_combine_unpermute": (i32, [P, i64, i32, P, P, i64, i32, P, P, P]),
     "ap_combine_backward": (i32, [P, P, i64, i32, P, P, i64, i32, P, P, P, P]),
     "ap_dispatch_backward": (i32, [P, i64, i32, P, i64, i32, P, P, P]),
+    "ap_route_balance_scratch_bytes": (i32, [i64, i32, i64, P]),
+    "ap_route_balance": (i32, [P, i64, i32, i32, i64, P, f32, P, P, P, P, P, P, P, i64, P]),
+    "ap_route_backward": (i32, [P, i64, i32, i32, P, P, P, P, P, i64, P, P, P, P]),
+    "ap_embed": (i32, [P, i64, i64, i32, P, i32, i64, i32, f32, P, i64, i32, P, P]),
+    "ap_embed_scratch_bytes": (i32, [i64, i64, i32, P]),
+    "ap_embed_backward": (i32, [P, i64, i32, P, i32, i64, i32, i64, i64, f32, i32, P, i64, i32, P, i64, P, P]),
     "ap_pool_required_bytes": (i32, [P, P, P, P]),
     "ap_pool_init": (i32, [P, P, P, P, P, P]),
     "ap_pool_reset": (i32, [P, P]),

@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libap.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
-SOURCES = ["common.cu", "route.cu", "dispatch.cu", "combine.cu", "stash.cu", "noalloc.cu", "arena.cu"]
+SOURCES = ["common.cu", "route.cu", "dispatch.cu", "combine.cu", "stash.cu", "noalloc.cu", "arena.cu",
+           "balance.cu", "embed.cu"]
 # bench-only synthetic compute (whole-SM busy blocks for the overlap measurement), not part of libap.so
 BENCH_SOURCES = ["bench/busy.cu", "bench/green.cu"]
 BENCH_LIB = os.path.join(HERE, "libap_bench.so")

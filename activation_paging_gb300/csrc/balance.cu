@@ -1,0 +1,473 @@
+// Routing with its balance loss, and the gradient of the router's logits.
+//
+// Forward.  For a group g of tokens with n counting tokens, softmax rows p and
+// chosen pairs counted in c:
+//   loss = coef / G * sum_g E * sum_e c[g,e] / (n k) * (sum_t p[t,e] / n).
+// The counts are constants of the loss, so d loss / d p[t,e] = slope[g,e] =
+// coef * E * c[g,e] / (G k n^2) is one number per group and expert, and all
+// that the backward pass needs.
+// One pass over the logits (k_route_balance): a warp routes a token as
+// k_route_topk does and adds the token's softmax row to sums that stay in
+// registers (lane l holds experts l, l + 32, ...); a block adds its warps up
+// and writes one row of sums and counts.  A second kernel (k_balance_finish)
+// adds the blocks' rows in block order and forms prob, slope and the loss.
+// Every order is fixed by the sizes, so equal inputs give equal bits.
+//
+// Backward.  With q = p * (slope - <p, slope>) and the selected softmax w:
+//   dlogits = dloss * q + scatter(w * (dw - <w, dw>)).
+// One pass: a warp holds a token's row in registers, recomputes its softmax,
+// and adds the k selected terms through shared memory.
+#include "route_topk.cuh"
+
+namespace ap {
+namespace {
+
+constexpr int kBalThreads = 256;
+constexpr int kBalWarps = kBalThreads / kWarp;
+constexpr int kBalBlocks = 608; // row-sum blocks of all groups together, at most (one group per block beyond)
+
+struct BalancePlan {
+    int64_t S, G, blocks; // tokens per group, groups, blocks per group
+    int64_t off_n, off_lp, off_p, off_c, bytes;
+};
+
+// The split and the layout of the work space: one row of E sums, E counts and
+// one token count per block, one loss term per 32 experts of a group, and the
+// counter of finished blocks of the second kernel.
+BalancePlan balance_plan(int64_t T, int32_t E, int64_t group_tokens)
+{
+    BalancePlan p = {};
+    p.S = group_tokens > 0 && group_tokens < T ? group_tokens : (T > 0 ? T : 1);
+    p.G = (T + p.S - 1) / p.S;
+    p.blocks = 1;
+    if (p.G > 0) {
+        const int64_t most = (p.S + kBalWarps - 1) / kBalWarps;
+        p.blocks = kBalBlocks / p.G;
+        if (p.blocks > most) p.blocks = most;
+        if (p.blocks < 1) p.blocks = 1;
+    }
+    auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+    const int64_t rows = p.G * p.blocks;
+    p.off_n = 256;
+    p.off_lp = p.off_n + up(rows * 4);
+    p.off_p = p.off_lp + up(p.G * ((E + 31) / 32) * 4);
+    p.off_c = p.off_p + up(rows * E * 4);
+    p.bytes = p.off_c + up(rows * E * 4);
+    return p;
+}
+
+template <int NV>
+__global__ void __launch_bounds__(kBalThreads)
+    k_route_balance(const float *__restrict__ logits, int64_t T, int E, int k, int64_t S, int blocks,
+                    const uint8_t *__restrict__ mask, int32_t *__restrict__ idx, float *__restrict__ w,
+                    int32_t *__restrict__ part_n, float *__restrict__ part_p, int32_t *__restrict__ part_c,
+                    uint32_t *done)
+{
+    pdl_begin();
+    extern __shared__ float s_mem[];
+    float *s_sum = s_mem;                                            // [warps][E]
+    int *s_cnt = reinterpret_cast<int *>(s_mem + kBalWarps * E);     // [E]
+    __shared__ int s_n;
+    const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *done = 0;
+    if (threadIdx.x == 0) s_n = 0;
+    for (int e = threadIdx.x; e < E; e += kBalThreads) s_cnt[e] = 0;
+    __syncthreads();
+
+    const int64_t g = blockIdx.x / blocks;
+    const int b = (int)(blockIdx.x - g * blocks);
+    const int64_t t_end = (g + 1) * S < T ? (g + 1) * S : T;
+    float acc[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) acc[i] = 0.f;
+    int n = 0;
+    for (int64_t t = g * S + (int64_t)b * kBalWarps + wid; t < t_end; t += (int64_t)blocks * kBalWarps) {
+        const float *row = logits + t * E;
+        float v[NV];
+        uint32_t key[NV];
+        int ex[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int ei = lane + kWarp * i;
+            const bool ok = ei < E;
+            v[i] = ok ? __ldcs(row + ei) : -INFINITY;
+            key[i] = ok ? order_key(v[i]) : 0u;
+            ex[i] = ok ? ei : kNoExpert;
+        }
+        int e;
+        float wt, top;
+        select_token<NV>(key, ex, k, lane, &e, &wt, &top);
+        const bool some = top != -INFINITY; // warp-uniform
+        if (lane < k) {
+            idx[t * k + lane] = e;
+            w[t * k + lane] = some ? wt : 0.f;
+        }
+        if (some && (!mask || mask[t])) {
+            float z[NV], sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                z[i] = expf(v[i] - top); // -infinity (no such expert, or one masked out) gives 0
+                sum += z[i];
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            const float inv = __fdiv_rn(1.0f, sum);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) acc[i] += z[i] * inv;
+            if (lane < k) atomicAdd(&s_cnt[e], 1);
+            ++n;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int ei = lane + kWarp * i;
+        if (ei < E) s_sum[wid * E + ei] = acc[i];
+    }
+    if (lane == 0 && n) atomicAdd(&s_n, n);
+    __syncthreads();
+    const int64_t at = (int64_t)blockIdx.x * E;
+    for (int e = threadIdx.x; e < E; e += kBalThreads) {
+        float sum = 0.f;
+#pragma unroll
+        for (int q = 0; q < kBalWarps; ++q) sum += s_sum[q * E + e];
+        part_p[at + e] = sum;
+        part_c[at + e] = s_cnt[e];
+    }
+    if (threadIdx.x == 0) part_n[blockIdx.x] = s_n;
+}
+
+// One block per group and 32 experts: warp r adds the rows r, r + 8, ... of its
+// group's blocks, the eight warps' sums are added in warp order, and the last
+// block to finish adds the loss terms up in block order.
+__global__ void __launch_bounds__(kBalThreads)
+    k_balance_finish(int E, int k, int64_t G, int blocks, float coef, const int32_t *__restrict__ part_n,
+                     const float *__restrict__ part_p, const int32_t *__restrict__ part_c, float *loss_part,
+                     int32_t *__restrict__ counts, float *__restrict__ prob, float *__restrict__ slope,
+                     float *__restrict__ loss, uint32_t *done)
+{
+    pdl_begin();
+    __shared__ float s_p[kBalWarps][kWarp];
+    __shared__ int s_c[kBalWarps][kWarp];
+    __shared__ bool s_last;
+    const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
+    const int pieces = (E + kWarp - 1) / kWarp;
+    const int64_t g = blockIdx.x / pieces;
+    const int e = (int)(blockIdx.x - g * pieces) * kWarp + lane;
+    float sum = 0.f;
+    int cnt = 0;
+    if (e < E)
+        for (int b = wid; b < blocks; b += kBalWarps) {
+            sum += part_p[(g * blocks + b) * E + e];
+            cnt += part_c[(g * blocks + b) * E + e];
+        }
+    s_p[wid][lane] = sum;
+    s_c[wid][lane] = cnt;
+    __syncthreads();
+    if (wid == 0) {
+        int n = 0;
+        for (int b = lane; b < blocks; b += kWarp) n += part_n[g * blocks + b];
+        n = __reduce_add_sync(0xffffffffu, n);
+        sum = 0.f;
+        cnt = 0;
+#pragma unroll
+        for (int q = 0; q < kBalWarps; ++q) {
+            sum += s_p[q][lane];
+            cnt += s_c[q][lane];
+        }
+        const float nf = (float)(n > 0 ? n : 1);
+        const float sl = coef * (float)E / ((float)G * (float)k) * (float)cnt / (nf * nf);
+        float term = 0.f;
+        if (e < E) {
+            counts[g * E + e] = cnt;
+            prob[g * E + e] = __fdiv_rn(sum, nf);
+            slope[g * E + e] = sl;
+            term = sl * sum;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xffffffffu, term, off);
+        if (lane == 0) {
+            loss_part[blockIdx.x] = term;
+            __threadfence();
+            s_last = atomicAdd(done, 1u) == gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    float total = 0.f;
+    for (int64_t i = threadIdx.x; i < gridDim.x; i += kBalThreads) total += __ldcg(loss_part + i);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    if (lane == 0) s_p[0][wid] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        total = 0.f;
+#pragma unroll
+        for (int q = 0; q < kBalWarps; ++q) total += s_p[0][q];
+        *loss = total;
+    }
+}
+
+__global__ void k_zero_word(float *p)
+{
+    pdl_begin();
+    *p = 0.f;
+}
+
+template <int VEC> struct Floats;
+template <> struct Floats<4> { using T = float4; };
+template <> struct Floats<1> { using T = float; };
+
+// A warp per token; lane l holds the vectors l, l + 32, ... of VEC experts
+// each (N of them).  The selected terms are added through a row of shared
+// memory per warp, zero between tokens.
+template <int VEC, int N>
+__global__ void __launch_bounds__(kBalThreads)
+    k_route_backward(const float *logits, int64_t T, int E, int k, const int32_t *__restrict__ idx,
+                     const float *__restrict__ w, const float *__restrict__ dw, const float *__restrict__ slope,
+                     const float *__restrict__ dloss, int64_t S, const uint8_t *__restrict__ mask, float *dlogits,
+                     uint32_t *d_status)
+{
+    pdl_begin();
+    using V = typename Floats<VEC>::T;
+    extern __shared__ float s_mem[];
+    const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
+    float *s_add = s_mem + wid * ((E + 3) & ~3);
+    for (int e = lane; e < E; e += kWarp) s_add[e] = 0.f;
+    __syncwarp();
+    const float gl = slope ? (dloss ? *dloss : 1.0f) : 0.f;
+    const int nvec = E / VEC;
+    const int64_t warps = (int64_t)gridDim.x * kBalWarps;
+    for (int64_t t = (int64_t)blockIdx.x * kBalWarps + wid; t < T; t += warps) {
+        float d[N][VEC];
+        const bool on = slope && (!mask || mask[t]); // warp-uniform
+        if (on) {
+            const V *row = reinterpret_cast<const V *>(logits + t * E);
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int s = lane + kWarp * i;
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) d[i][c] = -INFINITY;
+                if (s < nvec) {
+                    const V v = row[s];
+                    memcpy(d[i], &v, sizeof(V));
+                }
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) top = fmaxf(top, d[i][c]);
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const V *srow = reinterpret_cast<const V *>(slope + t / S * E);
+            float sl[N][VEC], sum = 0.f, dot = 0.f;
+            const bool some = top != -INFINITY;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int s = lane + kWarp * i;
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) sl[i][c] = 0.f;
+                if (s < nvec) {
+                    const V v = srow[s];
+                    memcpy(sl[i], &v, sizeof(V));
+                }
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    d[i][c] = some ? expf(d[i][c] - top) : 0.f;
+                    sum += d[i][c];
+                    dot += d[i][c] * sl[i][c];
+                }
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                dot += __shfl_xor_sync(0xffffffffu, dot, off);
+            }
+            const float inv = some ? __fdiv_rn(1.0f, sum) : 0.f;
+            const float mean = dot * inv;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) d[i][c] = gl * (d[i][c] * inv) * (sl[i][c] - mean);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) d[i][c] = 0.f;
+        }
+        int e = -1;
+        if (dw) {
+            float wj = 0.f, dj = 0.f;
+            if (lane < k) {
+                e = idx[t * k + lane];
+                wj = w[t * k + lane];
+                dj = dw[t * k + lane];
+                if (e < 0 || e >= E) {
+                    if (d_status) atomicOr(d_status, AP_FLAG_BAD_INDEX);
+                    e = -1;
+                }
+            }
+            float dot = wj * dj;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+            if (e >= 0) s_add[e] = wj * (dj - dot);
+            __syncwarp();
+        }
+        V *out = reinterpret_cast<V *>(dlogits + t * E);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int s = lane + kWarp * i;
+            if (s < nvec) {
+                float a[VEC];
+                const V v = reinterpret_cast<const V *>(s_add)[s];
+                memcpy(a, &v, sizeof(V));
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) a[c] += d[i][c];
+                V o;
+                memcpy(&o, a, sizeof(V));
+                out[s] = o;
+            }
+        }
+        if (dw) {
+            __syncwarp();
+            if (e >= 0) s_add[e] = 0.f;
+            __syncwarp();
+        }
+    }
+}
+
+template <int VEC, int N>
+void launch_route_backward(const float *logits, int64_t T, int E, int k, const int32_t *idx, const float *w,
+                           const float *dw, const float *slope, const float *dloss, int64_t S, const uint8_t *mask,
+                           float *dlogits, uint32_t *d_status, cudaStream_t st)
+{
+    const size_t smem = (size_t)kBalWarps * ((E + 3) & ~3) * 4;
+    const int64_t want = (T + kBalWarps - 1) / kBalWarps;
+    const int64_t most = (int64_t)sm_count() * 16;
+    launch(k_route_backward<VEC, N>, (int)(want < most ? want : most), kBalThreads, smem, st, logits, T, E, k, idx, w,
+           dw, slope, dloss, S, mask, dlogits, d_status);
+}
+
+bool balance_sizes_ok(int64_t T, int32_t E, int32_t k, int64_t group_tokens)
+{
+    return T >= 0 && T < (int64_t(1) << 31) && E >= 1 && E <= 1024 && k >= 1 && k <= E && k <= 32 && group_tokens >= 0;
+}
+
+} // namespace
+} // namespace ap
+
+extern "C" ap_status ap_route_balance_scratch_bytes(int64_t T, int32_t E, int64_t group_tokens, int64_t *bytes)
+{
+    using namespace ap;
+    if (!bytes || !balance_sizes_ok(T, E, 1, group_tokens))
+        return fail(AP_EINVAL, "route_balance_scratch_bytes: bad sizes T=%lld E=%d group_tokens=%lld", (long long)T, E,
+                    (long long)group_tokens);
+    *bytes = balance_plan(T, E, group_tokens).bytes;
+    return AP_OK;
+}
+
+extern "C" ap_status ap_route_balance(const float *logits, int64_t T, int32_t E, int32_t k, int64_t group_tokens,
+                                      const uint8_t *mask, float coef, int32_t *idx, float *w, int32_t *counts,
+                                      float *prob, float *slope, float *loss, void *scratch, int64_t scratch_bytes,
+                                      void *stream)
+{
+    AP_NVTX_RANGE("ap_route_balance");
+    using namespace ap;
+    if (!balance_sizes_ok(T, E, k, group_tokens))
+        return fail(AP_EINVAL, "route_balance: bad sizes T=%lld E=%d k=%d group_tokens=%lld", (long long)T, E, k,
+                    (long long)group_tokens);
+    if (!loss) return fail(AP_EINVAL, "route_balance: NULL pointer");
+    cudaStream_t st = (cudaStream_t)stream;
+    if (T == 0) {
+        launch(k_zero_word, 1, 1, 0, st, loss);
+        AP_CHECK_LAUNCH("route_balance launch");
+        return AP_OK;
+    }
+    if (!logits || !idx || !w || !counts || !prob || !slope || !scratch)
+        return fail(AP_EINVAL, "route_balance: NULL pointer");
+    const BalancePlan p = balance_plan(T, E, group_tokens);
+    if (reinterpret_cast<uintptr_t>(scratch) & 15) return fail(AP_EINVAL, "route_balance: scratch not 16-byte aligned");
+    if (scratch_bytes < p.bytes)
+        return fail(AP_EINVAL, "route_balance: scratch of %lld bytes, %lld needed", (long long)scratch_bytes,
+                    (long long)p.bytes);
+    const int64_t pieces = (E + kWarp - 1) / kWarp;
+    if (p.G * p.blocks > INT32_MAX || p.G * pieces > INT32_MAX)
+        return fail(AP_EINVAL, "route_balance: %lld groups of %d experts are more than one launch takes",
+                    (long long)p.G, E);
+    char *sc = static_cast<char *>(scratch);
+    uint32_t *done = reinterpret_cast<uint32_t *>(sc);
+    int32_t *part_n = reinterpret_cast<int32_t *>(sc + p.off_n);
+    float *loss_part = reinterpret_cast<float *>(sc + p.off_lp);
+    float *part_p = reinterpret_cast<float *>(sc + p.off_p);
+    int32_t *part_c = reinterpret_cast<int32_t *>(sc + p.off_c);
+    const int grid = (int)(p.G * p.blocks);
+    const size_t smem = (size_t)(kBalWarps + 1) * E * 4;
+    auto go = [&](auto *kernel) {
+        launch(kernel, grid, kBalThreads, smem, st, logits, T, E, k, p.S, (int)p.blocks, mask, idx, w, part_n, part_p,
+               part_c, done);
+    };
+    if (E <= 32)
+        go(k_route_balance<1>);
+    else if (E <= 64)
+        go(k_route_balance<2>);
+    else if (E <= 128)
+        go(k_route_balance<4>);
+    else if (E <= 256)
+        go(k_route_balance<8>);
+    else if (E <= 512)
+        go(k_route_balance<16>);
+    else
+        go(k_route_balance<32>);
+    AP_CHECK_LAUNCH("route_balance launch");
+    launch(k_balance_finish, (int)(p.G * pieces), kBalThreads, 0, st, E, k, p.G, (int)p.blocks, coef, part_n, part_p,
+           part_c, loss_part, counts, prob, slope, loss, done);
+    AP_CHECK_LAUNCH("route_balance finish launch");
+    return AP_OK;
+}
+
+extern "C" ap_status ap_route_backward(const float *logits, int64_t T, int32_t E, int32_t k, const int32_t *idx,
+                                       const float *w, const float *dw, const float *slope, const float *dloss,
+                                       int64_t group_tokens, const uint8_t *mask, float *dlogits, uint32_t *d_status,
+                                       void *stream)
+{
+    AP_NVTX_RANGE("ap_route_backward");
+    using namespace ap;
+    if (!balance_sizes_ok(T, E, k, group_tokens))
+        return fail(AP_EINVAL, "route_backward: bad sizes T=%lld E=%d k=%d group_tokens=%lld", (long long)T, E, k,
+                    (long long)group_tokens);
+    if (T == 0) return AP_OK;
+    if (!dlogits || (slope && !logits) || (dw && (!idx || !w)))
+        return fail(AP_EINVAL, "route_backward: NULL pointer");
+    const int64_t S = group_tokens > 0 && group_tokens < T ? group_tokens : T;
+    cudaStream_t st = (cudaStream_t)stream;
+    const uintptr_t al = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(slope) |
+                         reinterpret_cast<uintptr_t>(dlogits);
+    const bool vec = E % 4 == 0 && (al & 15) == 0;
+#define AP_ROUTE_BWD(VEC, N) \
+    launch_route_backward<VEC, N>(logits, T, E, k, idx, w, dw, slope, dloss, S, mask, dlogits, d_status, st)
+    if (vec) {
+        if (E <= 128)
+            AP_ROUTE_BWD(4, 1);
+        else if (E <= 256)
+            AP_ROUTE_BWD(4, 2);
+        else if (E <= 512)
+            AP_ROUTE_BWD(4, 4);
+        else
+            AP_ROUTE_BWD(4, 8);
+    } else {
+        if (E <= 32)
+            AP_ROUTE_BWD(1, 1);
+        else if (E <= 64)
+            AP_ROUTE_BWD(1, 2);
+        else if (E <= 128)
+            AP_ROUTE_BWD(1, 4);
+        else if (E <= 256)
+            AP_ROUTE_BWD(1, 8);
+        else if (E <= 512)
+            AP_ROUTE_BWD(1, 16);
+        else
+            AP_ROUTE_BWD(1, 32);
+    }
+#undef AP_ROUTE_BWD
+    AP_CHECK_LAUNCH("route_backward launch");
+    return AP_OK;
+}

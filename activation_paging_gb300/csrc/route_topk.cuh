@@ -39,21 +39,16 @@ __device__ __forceinline__ bool before(uint32_t ka, int ea, uint32_t kb, int eb)
 // Each lane sorts its NV candidates (odd-even transposition, constant
 // indices), then k rounds each take the warp-wide best head with two
 // redux.sync reductions (max key, then min id among equal keys); the winning
-// lane shifts its list.  All 32 lanes call it; lane j < k receives the j-th
-// expert in *e and its renormalised weight in *wt.
+// lane shifts its list.  All 32 lanes call it with their candidates (a lane
+// without one holds key 0 and id kNoExpert); lane j < k receives the j-th
+// expert in *e and its renormalised weight in *wt, every lane the largest
+// logit in *top.
+constexpr int kNoExpert = 0x7fffffff;
+
 template <int NV>
-__device__ __forceinline__ void route_token(const float *__restrict__ row, int E, int k, int lane, int *e, float *wt)
+__device__ __forceinline__ void select_token(uint32_t (&key)[NV], int (&ex)[NV], int k, int lane, int *e, float *wt,
+                                             float *top)
 {
-    constexpr int kNone = 0x7fffffff;
-    uint32_t key[NV];
-    int ex[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int ei = lane + kWarp * i;
-        const bool ok = ei < E;
-        key[i] = ok ? order_key(__ldcs(row + ei)) : 0u; // 0 sorts below every finite logit
-        ex[i] = ok ? ei : kNone;
-    }
 #pragma unroll
     for (int r = 0; r < NV; ++r) {
 #pragma unroll
@@ -72,7 +67,7 @@ __device__ __forceinline__ void route_token(const float *__restrict__ row, int E
     int my_e = 0;
     for (int j = 0; j < k; ++j) {
         const uint32_t m = __reduce_max_sync(0xffffffffu, key[0]);
-        const int emin = __reduce_min_sync(0xffffffffu, key[0] == m ? ex[0] : kNone);
+        const int emin = __reduce_min_sync(0xffffffffu, key[0] == m ? ex[0] : kNoExpert);
         if (key[0] == m && ex[0] == emin) {
 #pragma unroll
             for (int i = 0; i + 1 < NV; ++i) {
@@ -80,7 +75,7 @@ __device__ __forceinline__ void route_token(const float *__restrict__ row, int E
                 ex[i] = ex[i + 1];
             }
             key[NV - 1] = 0u;
-            ex[NV - 1] = kNone;
+            ex[NV - 1] = kNoExpert;
         }
         if (lane == j) {
             my_key = m;
@@ -94,6 +89,24 @@ __device__ __forceinline__ void route_token(const float *__restrict__ row, int E
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     *e = my_e;
     *wt = __fdiv_rn(z, s);
+    *top = mv;
+}
+
+// Loads one token's row and selects from it.
+template <int NV>
+__device__ __forceinline__ void route_token(const float *__restrict__ row, int E, int k, int lane, int *e, float *wt)
+{
+    uint32_t key[NV];
+    int ex[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int ei = lane + kWarp * i;
+        const bool ok = ei < E;
+        key[i] = ok ? order_key(__ldcs(row + ei)) : 0u; // 0 sorts below every finite logit
+        ex[i] = ok ? ei : kNoExpert;
+    }
+    float top;
+    select_token<NV>(key, ex, k, lane, e, wt, &top);
 }
 
 } // namespace

@@ -55,9 +55,11 @@ typedef int32_t ap_status;
 #define AP_FLAG_BAD_INDEX 0x10u      /* an expert id or row index out of range   */
 #define AP_FLAG_CORRUPT 0x20u        /* a page id read back out of range         */
 
-/* payload types of dispatch_permute */
+/* payload types of dispatch_permute (BF16, E4M3); table, row and gradient
+ * types of embed and embed_backward (BF16, F32) */
 #define AP_DTYPE_BF16 0
 #define AP_DTYPE_E4M3 1
+#define AP_DTYPE_F32 2
 
 /* Human-readable name of a status code (static string). */
 const char *ap_status_str(ap_status s);
@@ -224,6 +226,108 @@ ap_status ap_combine_backward(const void *dout, const void *y, int64_t y_rows,
 ap_status ap_dispatch_backward(const void *dxd, int64_t rows, int32_t H,
                                const int32_t *dest, int64_t T, int32_t k,
                                void *dx, uint32_t *d_status, void *stream);
+
+/* ============================================================================
+ * route_balance
+ *
+ * Routing with its balance loss (no counterpart on the pages).  idx and w are
+ * exactly those of ap_route_topk.  The T tokens
+ * form G = ceil(T / group_tokens) groups of group_tokens consecutive tokens
+ * (a batch's sequences; the last group may be shorter; group_tokens = 0: one
+ * group of all T).  A token counts when mask is NULL or mask[t] != 0 and its
+ * row holds a number above -infinity.  For group g with n_g such tokens, their
+ * softmax rows p[t] over the E experts and their chosen pairs:
+ *   counts[g, e] = pairs (t, j) with idx[t, j] = e
+ *   prob[g, e]   = sum_t p[t, e] / n_g
+ *   loss         = coef / G * sum_g E * sum_e counts[g, e] / (n_g k) * prob[g, e]
+ *   slope[g, e]  = coef * E * counts[g, e] / (G * k * n_g^2), which is
+ *                  d loss / d p[t, e] for every such token t of group g
+ * (counts are constants of the loss, as usual).  A group without such a token
+ * has counts, prob and slope 0 and adds nothing to the loss.  Masked tokens
+ * are routed all the same; what their logits hold reaches no sum.  Sums are
+ * single precision in an order that depends on the sizes alone, so equal
+ * inputs give equal bits.  For a loss over the counts of several calls or
+ * GPUs, add up counts and form slope from the sums; prob and loss are this
+ * call's.
+ *
+ *   logits  [T, E] float32, row-major (device, read).  Finite, or -infinity
+ *           for an expert that the token must not choose: its p is 0, and w
+ *           is 0 if fewer than k experts are left (all -infinity: w is 0)
+ *   mask    [T] bytes (device, read) or NULL
+ *   idx, w  [T, k] as ap_route_topk (device, written)
+ *   counts  [G, E] int32, prob, slope [G, E] float32 (device, written)
+ *   loss    [1] float32 (device, written)
+ *   scratch device work space of ap_route_balance_scratch_bytes() bytes,
+ *           16-byte aligned; its contents need no initialisation
+ * T = 0 writes loss = 0 (G = 0).  Limits: as ap_route_topk, group_tokens >= 0.
+ * ========================================================================== */
+ap_status ap_route_balance_scratch_bytes(int64_t T, int32_t E, int64_t group_tokens, int64_t *bytes);
+ap_status ap_route_balance(const float *logits, int64_t T, int32_t E, int32_t k, int64_t group_tokens,
+                           const uint8_t *mask, float coef, int32_t *idx, float *w, int32_t *counts, float *prob,
+                           float *slope, float *loss, void *scratch, int64_t scratch_bytes, void *stream);
+
+/* Gradient of the router's logits from both uses of them (the derivatives of
+ * the definitions above):
+ *   dlogits[t, e] = sum_j [idx[t, j] = e] w[t, j] (dw[t, j] - sum_i w[t, i] dw[t, i])
+ *                 + dloss * p[t, e] (slope[g, e] - sum_e' p[t, e'] slope[g, e'])
+ * with g the group of t; the second term is 0 for a token that does not count.
+ *   idx, w   [T, k] (device, read): the forward pass's; ids distinct in a row.
+ *            An id outside [0, E) adds nothing and sets AP_FLAG_BAD_INDEX in
+ *            *d_status (may be NULL)
+ *   dw       [T, k] float32 (device, read), e.g. of ap_combine_backward, or
+ *            NULL: no first term (idx and w may then be NULL)
+ *   slope    [G, E] float32 (device, read) or NULL: no second term
+ *   dloss    [1] float32 (device, read) or NULL: 1
+ *   dlogits  [T, E] float32 (device, written whole); may be logits itself
+ * logits, mask, group_tokens and limits as ap_route_balance. */
+ap_status ap_route_backward(const float *logits, int64_t T, int32_t E, int32_t k, const int32_t *idx, const float *w,
+                            const float *dw, const float *slope, const float *dloss, int64_t group_tokens,
+                            const uint8_t *mask, float *dlogits, uint32_t *d_status, void *stream);
+
+/* ============================================================================
+ * embed
+ *
+ * Token rows from an embedding table (no counterpart on the pages: the rows x
+ * that the dispatch takes begin here):
+ *   out[t] = round(scale * table[ids[t]])   (one float32 multiply, one
+ *                                            rounding to out_dtype)
+ * An id outside [0, V) gives a row of zeros and sets AP_FLAG_BAD_INDEX in
+ * *d_status (may be NULL).
+ *
+ *   table   [V, H] of table_dtype, rows table_ld elements apart (device, read)
+ *   ids     [T] int32 (id_bytes = 4) or int64 (id_bytes = 8) (device, read)
+ *   out     [T, H] of out_dtype, rows out_ld elements apart (device, written)
+ * Types: AP_DTYPE_BF16 or AP_DTYPE_F32.  Limits: V >= 1, V < 2^31, H >= 1,
+ * 0 <= T < 2^31, row distances >= H, pointers aligned to their elements.
+ * 16-byte aligned rows are fastest.
+ * ========================================================================== */
+ap_status ap_embed(const void *table, int64_t V, int64_t table_ld, int32_t table_dtype, const void *ids,
+                   int32_t id_bytes, int64_t T, int32_t H, float scale, void *out, int64_t out_ld, int32_t out_dtype,
+                   uint32_t *d_status, void *stream);
+
+/* Gradient of the table: for every id v
+ *   sum[v]    = sum of dout[t] over the tokens t with ids[t] = v (float32)
+ *   dtable[v] = round(scale * sum[v])               (accumulate = 0: all V
+ *               rows are written, zeros where no token has the id)
+ *   dtable[v] = round(dtable[v] + scale * sum[v])   (accumulate = 1: only rows
+ *               of ids that occur are touched)
+ * Tokens with ids[t] = padding_idx (-1: none) add nothing; neither do tokens
+ * with an id outside [0, V), which set AP_FLAG_BAD_INDEX in *d_status (may be
+ * NULL).  The tokens are sorted by id and each id's rows are added up in an
+ * order that depends on the ids and sizes alone, without floating-point
+ * atomics: equal inputs give equal bits.
+ *
+ *   dout    [T, H] of dout_dtype, rows dout_ld elements apart (device, read)
+ *   dtable  [V, H] of dtable_dtype, rows dtable_ld apart (device, written;
+ *           accumulate = 1: read too).  Elements between rows stay untouched
+ *   scratch device work space of ap_embed_scratch_bytes() bytes, 16-byte
+ *           aligned; its contents need no initialisation
+ * T = 0 is the empty sum.  ids, types and limits as ap_embed. */
+ap_status ap_embed_scratch_bytes(int64_t T, int64_t V, int32_t H, int64_t *bytes);
+ap_status ap_embed_backward(const void *dout, int64_t dout_ld, int32_t dout_dtype, const void *ids, int32_t id_bytes,
+                            int64_t T, int32_t H, int64_t V, int64_t padding_idx, float scale, int32_t accumulate,
+                            void *dtable, int64_t dtable_ld, int32_t dtable_dtype, void *scratch,
+                            int64_t scratch_bytes, uint32_t *d_status, void *stream);
 
 /* ============================================================================
  * Paged activation stash (torchtitan pull 5541, "AI-Generated Details":
