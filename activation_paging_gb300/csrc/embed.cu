@@ -6,12 +6,13 @@
 //   1. The tokens are sorted by id (stable radix sort, least significant digit
 //      first; ids that do not count sort last), so an id's tokens are one run
 //      in token order.
-//   2. k_embed_sum: a warp takes kChunk sorted tokens and a piece of the
-//      columns, adds rows up in single precision, and finishes each run that
-//      lies inside its chunk in dtable.  A run that crosses chunks leaves one
-//      partial row in each: `head` where it began earlier, `tail` where it
-//      begins and goes on.
-//   3. k_embed_join adds the partial rows of each such run in chunk order.
+//   2. k_embed_sum: a block takes a tile of 8 * rows sorted tokens and a slice
+//      of the columns, each warp `rows` tokens of it.  Rows add up in single
+//      precision; a run inside one warp goes straight to dtable, the warps'
+//      partial rows of a run that spans warps are joined in shared memory,
+//      and a run that spans tiles leaves one partial row per tile: `head`
+//      where it began in an earlier tile, `tail` where it begins and goes on.
+//   3. k_embed_join adds the partial rows of each such run in tile order.
 // No floating-point atomics: every sum has one order, fixed by ids and sizes.
 #include <cuda_bf16.h>
 
@@ -33,6 +34,47 @@ __device__ __forceinline__ float to_f(bf16_t v) { return __bfloat162float(v); }
 template <typename E> __device__ __forceinline__ E from_f(float v);
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ bf16_t from_f<bf16_t>(float v) { return __float2bfloat16_rn(v); }
+
+// Loads a pack now, if `on`: the compiler keeps the load where it stands
+// (it would move one whose value is used under a condition down to that use,
+// and a batch of loads would wait for memory one after the other).
+template <typename P> __device__ __forceinline__ void load_now(P &v, const P *p, bool on)
+{
+    if constexpr (sizeof(P) == 16) {
+        uint4 r = {0, 0, 0, 0};
+        asm volatile("{ .reg .pred q; setp.ne.u32 q, %5, 0; @q ld.global.v4.u32 {%0, %1, %2, %3}, [%4]; }"
+                     : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)
+                     : "l"(p), "r"((uint32_t)on));
+        memcpy(&v, &r, 16);
+    } else if constexpr (sizeof(P) == 8) {
+        uint2 r = {0, 0};
+        asm volatile("{ .reg .pred q; setp.ne.u32 q, %3, 0; @q ld.global.v2.u32 {%0, %1}, [%2]; }"
+                     : "+r"(r.x), "+r"(r.y)
+                     : "l"(p), "r"((uint32_t)on));
+        memcpy(&v, &r, 8);
+    } else if constexpr (sizeof(P) == 4) {
+        uint32_t r = 0;
+        asm volatile("{ .reg .pred q; setp.ne.u32 q, %2, 0; @q ld.global.u32 %0, [%1]; }"
+                     : "+r"(r)
+                     : "l"(p), "r"((uint32_t)on));
+        memcpy(&v, &r, 4);
+    } else if constexpr (sizeof(P) == 2) {
+        uint16_t r = 0;
+        asm volatile("{ .reg .pred q; setp.ne.u32 q, %2, 0; @q ld.global.u16 %0, [%1]; }"
+                     : "+h"(r)
+                     : "l"(p), "r"((uint32_t)on));
+        memcpy(&v, &r, 2);
+    } else {
+        static_assert(sizeof(P) == 32, "pack size");
+        struct Half {
+            uint4 r;
+        };
+        Half h[2];
+        load_now(h[0], reinterpret_cast<const Half *>(p), on);
+        load_now(h[1], reinterpret_cast<const Half *>(p) + 1, on);
+        memcpy(&v, h, 32);
+    }
+}
 
 __device__ __forceinline__ int64_t load_id(const void *ids, bool wide, int64_t t)
 {
@@ -77,9 +119,7 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---- sort of the tokens by id ----------------------------------------------------
-constexpr int kSortThreads = 256;
-constexpr int kSortItems = 8;
-constexpr int kSortTile = kSortThreads * kSortItems;
+// Sorted tokens as (id, token); ids that do not count hold V and come last.
 constexpr int kMaxDigitBits = 10;
 
 // Sort key of a token: its id, or V for one that does not count.
@@ -95,13 +135,183 @@ __device__ __forceinline__ uint32_t sort_key(const void *ids, bool wide, int64_t
     return (uint32_t)id;
 }
 
-// Digit counts of each tile: hist[d * tiles + tile].  The first pass (keys ==
+// Ranks the warp's 32 tokens of one step among its tokens of the same digit
+// (d = -1: no token): the count so far plus the equal lanes below.
+__device__ __forceinline__ uint32_t warp_rank(uint16_t *cnt, int d)
+{
+    const uint32_t same = __match_any_sync(0xffffffffu, d);
+    uint32_t rank = 0;
+    if (d >= 0) rank = cnt[d] + __popc(same & lanemask_lt());
+    __syncwarp();
+    if (d >= 0 && (same >> lane_id()) == 1u) cnt[d] = (uint16_t)(rank + 1); // the last lane of its digit
+    __syncwarp();
+    return rank;
+}
+
+// Sets the bit of every id that occurs, one lane for each id of the warp.  All lanes call it.
+__device__ __forceinline__ void mark_seen(uint32_t *seen, uint32_t key, int64_t V)
+{
+    const uint32_t same = __match_any_sync(0xffffffffu, key);
+    if ((same >> lane_id()) == 1u && key != (uint32_t)V) atomicOr(seen + (key >> 5), 1u << (key & 31));
+}
+
+// One cluster sorts up to kClusterMax tokens in one launch, in registers and
+// (distributed) shared memory.  Block r holds tokens r * per .. r * per + per - 1
+// of the current order, warp q of it a run of 32 * ITEMS.  A pass: every warp
+// ranks its tokens per digit; a thread per digit adds the warps up; the
+// blocks exchange their digit totals; every token goes to its new place in
+// the block that holds it, in the last pass to memory.  Six dependent
+// launches of the form below cost 35 us at any length up to some thousand
+// tokens; this one costs its passes alone.
+constexpr int kClThreads = 1024;
+constexpr int kClWarps = kClThreads / kWarp;
+constexpr int kClItemsMax = 16;
+constexpr int kClBlocks = 8; // the largest portable cluster
+constexpr int64_t kClusterMax = (int64_t)kClBlocks * kClThreads * kClItemsMax;
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// Address of the same shared variable in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ uint32_t cluster_load(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint2 v)
+{
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+
+template <int ITEMS>
+__global__ void __launch_bounds__(kClThreads, 1)
+    k_sort_cluster(const void *__restrict__ ids, bool wide, int T, int per, int64_t V, int64_t pad, int passes,
+                   int bits, uint2 *__restrict__ sorted, uint32_t *__restrict__ seen, uint32_t *d_status)
+{
+    pdl_begin_after(); // the sums kernel reads ids and rows ahead of its own wait
+    extern __shared__ uint2 s_pairs[]; // [kClThreads * ITEMS], then the warps' counts [kClWarps][D]
+    __shared__ uint32_t s_tot[1 << kMaxDigitBits], s_base[1 << kMaxDigitBits], s_warp[kClWarps];
+    const int D = 1 << bits;
+    uint16_t *cnt = reinterpret_cast<uint16_t *>(s_pairs + kClThreads * ITEMS);
+    const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
+    const uint32_t me = blockIdx.x, blocks = gridDim.x; // the grid is one cluster
+    const int first = (int)me * per;
+    const int n = T - first < per ? T - first : per; // this block's tokens (may be <= 0)
+    const int l0 = wid * (ITEMS * kWarp) + lane;
+    uint16_t *mine = cnt + wid * D;
+    if (seen) // cleared before the first barrier of the cluster, set in the last pass
+        for (int64_t i = (int64_t)me * kClThreads + threadIdx.x; i < (V + 31) / 32; i += (int64_t)blocks * kClThreads)
+            seen[i] = 0;
+    for (int pass = 0; pass < passes; ++pass) {
+        const int shift = pass * bits;
+        uint32_t *words = reinterpret_cast<uint32_t *>(cnt);
+        for (int i = threadIdx.x; i < kClWarps * D / 2; i += kClThreads) words[i] = 0;
+        uint2 pair[ITEMS];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int l = l0 + i * kWarp;
+            if (l < n) {
+                if (pass == 0)
+                    pair[i] = make_uint2(sort_key(ids, wide, first + l, V, pad, d_status), (uint32_t)(first + l));
+                else
+                    pair[i] = s_pairs[l];
+            }
+        }
+        __syncthreads();
+        uint32_t rank[ITEMS];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            rank[i] = warp_rank(mine, l0 + i * kWarp < n ? (int)((pair[i].x >> shift) & (D - 1)) : -1);
+        __syncthreads();
+        if ((int)threadIdx.x < D) {
+            uint32_t c[kClWarps], sum = 0;
+#pragma unroll
+            for (int q = 0; q < kClWarps; ++q) c[q] = cnt[q * D + threadIdx.x];
+#pragma unroll
+            for (int q = 0; q < kClWarps; ++q) {
+                cnt[q * D + threadIdx.x] = (uint16_t)sum;
+                sum += c[q];
+            }
+            s_tot[threadIdx.x] = sum;
+        }
+        cluster_sync(); // the totals are there, and no block needs its s_pairs any more
+        uint32_t before = 0, all = 0;
+        if ((int)threadIdx.x < D) {
+            const uint32_t at = smem_addr(&s_tot[threadIdx.x]);
+            uint32_t c[kClBlocks];
+#pragma unroll
+            for (uint32_t r = 0; r < kClBlocks; ++r) c[r] = r < blocks ? cluster_load(cluster_addr(at, r)) : 0u;
+#pragma unroll
+            for (uint32_t r = 0; r < kClBlocks; ++r) {
+                if (r < me) before += c[r];
+                all += c[r];
+            }
+        }
+        uint32_t x = all; // exclusive sum over the digits
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        if (lane == 31) s_warp[wid] = x;
+        __syncthreads();
+        if (wid == 0) {
+            const uint32_t v = s_warp[lane];
+            uint32_t z = v;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, z, off);
+                if (lane >= off) z += y;
+            }
+            s_warp[lane] = z - v;
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < D) s_base[threadIdx.x] = s_warp[wid] + x - all + before;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const bool in = l0 + i * kWarp < n;
+            if (seen && pass + 1 == passes) mark_seen(seen, in ? pair[i].x : (uint32_t)V, V);
+            if (!in) continue;
+            const int d = (int)((pair[i].x >> shift) & (D - 1));
+            const uint32_t at = s_base[d] + mine[d] + rank[i];
+            if (pass + 1 == passes) {
+                sorted[at] = pair[i];
+            } else {
+                const uint32_t to = at / (uint32_t)per;
+                cluster_store(cluster_addr(smem_addr(s_pairs + (at - to * per)), to), pair[i]);
+            }
+        }
+        cluster_sync(); // the pairs are in place; no block leaves while another reads its totals
+    }
+}
+
+// Longer inputs: three launches per digit, over tiles of kSortTile tokens.
+constexpr int kSortThreads = 256;
+constexpr int kSortItems = 8;
+constexpr int kSortTile = kSortThreads * kSortItems;
+
+// Digit counts of each tile: hist[d * tiles + tile].  The first pass (in ==
 // NULL) reads the ids.
 __global__ void __launch_bounds__(kSortThreads)
-    k_sort_count(const uint32_t *__restrict__ keys, const void *__restrict__ ids, bool wide, int64_t T, int64_t V,
-                 int64_t pad, int shift, int bits, uint32_t *__restrict__ hist, uint32_t *d_status)
+    k_sort_count(const uint2 *__restrict__ in, const void *__restrict__ ids, bool wide, int64_t T, int64_t V,
+                 int64_t pad, int shift, int bits, uint32_t *__restrict__ hist, uint32_t *__restrict__ seen,
+                 uint32_t *d_status)
 {
     pdl_begin();
+    if (seen) // the first pass clears what the last one sets
+        for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < (V + 31) / 32;
+             i += (int64_t)gridDim.x * kSortThreads)
+            seen[i] = 0;
     __shared__ uint32_t s_hist[1 << kMaxDigitBits];
     const int D = 1 << bits;
     for (int d = threadIdx.x; d < D; d += kSortThreads) s_hist[d] = 0;
@@ -110,7 +320,7 @@ __global__ void __launch_bounds__(kSortThreads)
     for (int i = 0; i < kSortItems; ++i) {
         const int64_t t = t0 + i * kSortThreads + threadIdx.x;
         if (t < T) {
-            const uint32_t key = keys ? keys[t] : sort_key(ids, wide, t, V, pad, d_status);
+            const uint32_t key = in ? in[t].x : sort_key(ids, wide, t, V, pad, d_status);
             atomicAdd(&s_hist[(key >> shift) & (D - 1)], 1u);
         }
     }
@@ -150,11 +360,12 @@ __global__ void __launch_bounds__(1024) k_sort_scan(uint32_t *hist, int64_t n)
 // Moves every token of a tile to its place, keeping the order within a digit:
 // warp q ranks its kSortItems * 32 consecutive tokens, 32 at a time.
 __global__ void __launch_bounds__(kSortThreads)
-    k_sort_scatter(const uint32_t *__restrict__ keys, const uint32_t *__restrict__ toks, const void *__restrict__ ids,
-                   bool wide, int64_t T, int64_t V, int64_t pad, int shift, int bits,
-                   const uint32_t *__restrict__ hist, uint32_t *__restrict__ keys_out, uint32_t *__restrict__ toks_out)
+    k_sort_scatter(const uint2 *__restrict__ in, const void *__restrict__ ids, bool wide, int64_t T, int64_t V,
+                   int64_t pad, int shift, int bits, const uint32_t *__restrict__ hist, uint2 *__restrict__ out,
+                   uint32_t *__restrict__ seen)
 {
-    pdl_begin();
+    pdl_begin_after(); // as k_sort_cluster
+
     constexpr int W = kSortThreads / kWarp;
     __shared__ uint16_t s_cnt[W][1 << kMaxDigitBits];
     const int D = 1 << bits;
@@ -162,19 +373,17 @@ __global__ void __launch_bounds__(kSortThreads)
     for (int d = threadIdx.x; d < W * D; d += kSortThreads) s_cnt[d / D][d % D] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * kSortTile + wid * (kSortItems * kWarp) + lane;
-    uint32_t key[kSortItems], rank[kSortItems];
+    uint2 pair[kSortItems];
+    uint32_t rank[kSortItems];
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
         const int64_t t = t0 + i * kWarp;
-        const bool in = t < T;
-        key[i] = in ? (keys ? keys[t] : sort_key(ids, wide, t, V, pad, nullptr)) : 0u;
-        // tokens past the end match nobody inside
-        const int d = in ? (int)((key[i] >> shift) & (D - 1)) : -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, d);
-        if (in) rank[i] = s_cnt[wid][d] + __popc(same & lanemask_lt());
-        __syncwarp();
-        if (in && (same >> lane) == 1u) s_cnt[wid][d] = (uint16_t)(rank[i] + 1); // the last of its digit
-        __syncwarp();
+        int d = -1;
+        if (t < T) {
+            pair[i] = in ? in[t] : make_uint2(sort_key(ids, wide, t, V, pad, nullptr), (uint32_t)t);
+            d = (int)((pair[i].x >> shift) & (D - 1));
+        }
+        rank[i] = warp_rank(s_cnt[wid], d);
     }
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += kSortThreads) {
@@ -189,180 +398,379 @@ __global__ void __launch_bounds__(kSortThreads)
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
-        const int64_t t = t0 + i * kWarp;
-        if (t >= T) continue;
-        const int d = (int)((key[i] >> shift) & (D - 1));
-        const uint32_t at = hist[(int64_t)d * gridDim.x + blockIdx.x] + s_cnt[wid][d] + rank[i];
-        keys_out[at] = key[i];
-        toks_out[at] = toks ? toks[t] : (uint32_t)t;
+        const bool in = t0 + i * kWarp < T;
+        if (seen) mark_seen(seen, in ? pair[i].x : (uint32_t)V, V);
+        if (!in) continue;
+        const int d = (int)((pair[i].x >> shift) & (D - 1));
+        out[hist[(int64_t)d * gridDim.x + blockIdx.x] + s_cnt[wid][d] + rank[i]] = pair[i];
     }
 }
 
 // ---- sums of the runs ------------------------------------------------------------
-constexpr int kChunk = 32;
+constexpr int kSumThreads = 256;
+constexpr int kSumWarps = kSumThreads / kWarp;
+constexpr int kSumRowsMax = 16;
+constexpr int64_t kPrefetchBytes = 48 << 20;
 
-// First position in [0, n) of the sorted keys that is >= key.
-__device__ __forceinline__ int64_t lower_bound(const uint32_t *keys, int64_t n, uint32_t key)
-{
-    int64_t lo = 0, hi = n;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (keys[mid] < key)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo;
-}
+// Where a lane's VE * NG elements of a slice lie: NG groups of VE, 32 lanes apart.
+template <int VE, int NG> struct Slice {
+    int s0, nstep; // first vector of the lane, vectors in a row
+    __device__ bool in(int g) const { return s0 + g * kWarp < nstep; }
+    __device__ int at(int g) const { return s0 + g * kWarp; }
+};
 
-template <typename TG, int VE>
-__device__ __forceinline__ void finish_row(TG *row, int s, const float *acc, float scale, bool accumulate)
+template <typename TG, int VE, int NG>
+__device__ __forceinline__ void finish_row(TG *row, const Slice<VE, NG> &sl, const float (&acc)[NG][VE],
+                                           const Pack<TG, VE> (&old)[NG], float scale, bool add)
 {
-    using PG = Pack<TG, VE>;
-    PG *p = reinterpret_cast<PG *>(row) + s;
-    PG o;
-    if (accumulate) {
-        const PG old = *p;
 #pragma unroll
-        for (int i = 0; i < VE; ++i) o.v[i] = from_f<TG>(__fadd_rn(to_f(old.v[i]), __fmul_rn(scale, acc[i])));
-    } else {
+    for (int g = 0; g < NG; ++g) {
+        if (!sl.in(g)) continue;
+        Pack<TG, VE> o;
 #pragma unroll
-        for (int i = 0; i < VE; ++i) o.v[i] = from_f<TG>(__fmul_rn(scale, acc[i]));
-    }
-    *p = o;
-}
-
-// Rows of ids that do not occur, set to zero: a warp takes kFillRows rows.
-constexpr int kFillRows = 8;
-template <typename TG, int VE>
-__global__ void __launch_bounds__(256)
-    k_embed_fill(const uint32_t *__restrict__ keys, int64_t T, int64_t V, int H, TG *__restrict__ dtable, int64_t ld)
-{
-    pdl_begin();
-    using PG = Pack<TG, VE>;
-    const int lane = (int)lane_id();
-    const int nstep = H / VE;
-    PG zero;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) zero.v[i] = from_f<TG>(0.f);
-    const int64_t warps = (int64_t)gridDim.x * (blockDim.x / kWarp);
-    for (int64_t r0 = ((int64_t)blockIdx.x * (blockDim.x / kWarp) + threadIdx.x / kWarp) * kFillRows; r0 < V;
-         r0 += warps * kFillRows) {
-        int64_t at = lower_bound(keys, T, (uint32_t)r0);
-        for (int64_t r = r0; r < r0 + kFillRows && r < V; ++r) {
-            if (at < T && keys[at] == (uint32_t)r) {
-                at = lower_bound(keys, T, (uint32_t)r + 1);
-                continue;
-            }
-            PG *row = reinterpret_cast<PG *>(dtable + r * ld);
-            for (int s = lane; s < nstep; s += kWarp) row[s] = zero;
+        for (int i = 0; i < VE; ++i) {
+            const float v = __fmul_rn(scale, acc[g][i]);
+            o.v[i] = from_f<TG>(add ? __fadd_rn(to_f(old[g].v[i]), v) : v);
         }
+        reinterpret_cast<Pack<TG, VE> *>(row)[sl.at(g)] = o;
     }
 }
 
-template <typename TD, typename TG, int VE, int U>
-__global__ void __launch_bounds__(256)
-    k_embed_sum(const TD *__restrict__ dout, int64_t dout_ld, const uint32_t *__restrict__ keys,
-                const uint32_t *__restrict__ toks, int64_t T, int64_t V, int H, float scale, bool accumulate,
-                TG *__restrict__ dtable, int64_t ld, float *__restrict__ partial, int64_t part_ld)
+template <typename E, int VE, int NG>
+__device__ __forceinline__ void load_row(Pack<E, VE> (&v)[NG], const E *row, const Slice<VE, NG> &sl, bool on = true)
 {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) load_now(v[g], reinterpret_cast<const Pack<E, VE> *>(row) + sl.at(g), on && sl.in(g));
+}
+
+// The same from shared memory.
+template <int VE, int NG>
+__device__ __forceinline__ void load_part(Pack<float, VE> (&v)[NG], const float *row, const Slice<VE, NG> &sl)
+{
+#pragma unroll
+    for (int g = 0; g < NG; ++g) v[g] = reinterpret_cast<const Pack<float, VE> *>(row)[sl.at(g)];
+}
+
+template <int VE, int NG> __device__ __forceinline__ void zero(float (&a)[NG][VE])
+{
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < VE; ++i) a[g][i] = 0.f;
+}
+
+template <typename E, int VE, int NG>
+__device__ __forceinline__ void add_row(float (&a)[NG][VE], const Pack<E, VE> (&v)[NG])
+{
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < VE; ++i) a[g][i] = __fadd_rn(a[g][i], to_f(v[g].v[i]));
+}
+
+template <int VE, int NG>
+__device__ __forceinline__ void store_part(float *row, const Slice<VE, NG> &sl, const float (&a)[NG][VE])
+{
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        if (!sl.in(g)) continue;
+        Pack<float, VE> o;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) o.v[i] = a[g][i];
+        reinterpret_cast<Pack<float, VE> *>(row)[sl.at(g)] = o;
+    }
+}
+
+// Asks for `bytes` bytes from p in L2 (a hint; the 16-byte granules that hold them).
+__device__ __forceinline__ void prefetch_l2(const void *p, int64_t bytes)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15;
+    const uintptr_t e = (reinterpret_cast<uintptr_t>(p) + bytes + 15) & ~(uintptr_t)15;
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"((uint32_t)(e - a)) : "memory");
+}
+
+// While the sort runs on a few SMs, the rows of dout (and, to be added to, the
+// rows of dtable that the ids name) start on their way to L2: at most
+// kPrefetchBytes, about what the sort's time lets HBM deliver.
+template <typename TD, typename TG, bool ADD>
+__device__ __forceinline__ void prefetch_inputs(const TD *dout, int64_t dout_ld, const void *ids, bool wide, int64_t T,
+                                                int64_t V, int64_t pad, int H, const TG *dtable, int64_t ld)
+{
+    const int64_t rb = (int64_t)H * sizeof(TD), gb = ADD ? (int64_t)H * sizeof(TG) : 0;
+    const int64_t most = kPrefetchBytes / (rb + gb);
+    const int64_t n = T < most ? T : most;
+    for (int64_t t = (int64_t)threadIdx.x * gridDim.x + blockIdx.x; t < n; t += (int64_t)gridDim.x * kSumThreads) {
+        const int64_t id = load_id(ids, wide, t);
+        if (id < 0 || id >= V || id == pad) continue;
+        prefetch_l2(dout + t * dout_ld, rb);
+        if (ADD) prefetch_l2(dtable + id * ld, gb);
+    }
+}
+
+// How the aligned form of the sums stages a row: 512 bytes of dout and the same
+// columns of dtable, copied to shared memory kStages rows ahead.
+constexpr int kStages = 8;
+constexpr int kDoutBytes = kWarp * 16;
+template <typename TD, typename TG, bool ADD>
+constexpr int kOldBytes = ADD ? kDoutBytes / (int)sizeof(TD) * (int)sizeof(TG) : 0;
+template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
+constexpr int kSumSmem = kSumWarps * ((RING ? kStages * (kDoutBytes + kOldBytes<TD, TG, ADD>) : 0) +
+                                      2 * kWarp * VE * NG * 4);
+
+__device__ __forceinline__ void copy_async16(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// RING (rows of both in 16-byte granules): every warp keeps kStages rows on
+// their way to shared memory, over the ends of items, so that the sums never
+// wait for one row's latency; loads into registers left 3.3 TB/s at 32768 x
+// 7168 rows, bound by what a warp's registers hold in flight.
+// Otherwise the rows go through registers, four at a time.
+template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
+__global__ void __launch_bounds__(kSumThreads, 2)
+    k_embed_sum(const TD *__restrict__ dout, int64_t dout_ld, const uint2 *__restrict__ sorted, int64_t T, int64_t V,
+                int H, float scale, int rows, TG *__restrict__ dtable, int64_t ld, float *__restrict__ partial,
+                int64_t part_ld, const uint32_t *__restrict__ seen, int fill_rows, const void *__restrict__ ids,
+                bool wide, int64_t pad)
+{
+    prefetch_inputs<TD, TG, ADD>(dout, dout_ld, ids, wide, T, V, pad, H, dtable, ld);
     pdl_begin();
-    using PD = Pack<TD, VE>;
-    using PF = Pack<float, VE>;
-    const int lane = (int)lane_id();
+    constexpr uint32_t kHead = 1, kThrough = 2, kTail = 4;
+    constexpr int kCols = kWarp * VE * NG;
+    constexpr int kOld = kOldBytes<TD, TG, ADD>;
+    constexpr int kStage = kDoutBytes + kOld;
+    extern __shared__ __align__(16) uint8_t s_mem[];
+    __shared__ uint32_t s_flags[kSumWarps];
+    const int lane = (int)lane_id(), w = threadIdx.x / kWarp;
+    auto s_part = [&](int q, int slot) { return reinterpret_cast<float *>(s_mem) + (q * 2 + slot) * kCols; };
+    uint8_t *ring = s_mem + kSumWarps * 2 * kCols * 4 + w * (kStages * kStage);
+    const uint32_t none = (uint32_t)V;
     const int nstep = H / VE;
-    const int pieces = (nstep + kWarp - 1) / kWarp;
-    const int64_t chunks = (T + kChunk - 1) / kChunk;
-    const int64_t items = chunks * pieces;
-    const int64_t warps = (int64_t)gridDim.x * (blockDim.x / kWarp);
-    for (int64_t it = (int64_t)blockIdx.x * (blockDim.x / kWarp) + threadIdx.x / kWarp; it < items; it += warps) {
-        const int64_t c = it / pieces;
-        const int s = (int)(it - c * pieces) * kWarp + lane;
-        const int64_t i0 = c * kChunk;
-        const int n = (int)(T - i0 < kChunk ? T - i0 : kChunk);
-        const uint32_t none = (uint32_t)V;
-        const uint32_t my_key = lane < n ? keys[i0 + lane] : none;
-        const uint32_t my_tok = lane < n ? toks[i0 + lane] : 0u;
-        const uint32_t before = i0 > 0 ? keys[i0 - 1] : none;
-        const uint32_t after = i0 + n < T ? keys[i0 + n] : none;
-        const int live = __popc(__ballot_sync(0xffffffffu, my_key != none)); // the ids that count come first
-        float acc[VE];
+    const int slices = (nstep + kWarp * NG - 1) / (kWarp * NG);
+    const int64_t tiles = (T + rows * kSumWarps - 1) / (rows * kSumWarps);
+    const int64_t sums = tiles * slices;
+    const Slice<VE, NG> mine{lane, kWarp * NG}; // within a slice, for s_part
+    // a warp's tokens of an item, with the ids before and after them
+    struct Rows {
+        uint2 my;
+        uint32_t before, ends, direct; // ends: rows that end a run; direct: of those, runs of this warp alone
+        int64_t tile;
+        int n, live, col0, cols;
+        bool began; // the first run began before these rows
+    };
+    auto rows_of = [&](int64_t it) {
+        Rows x;
+        x.tile = it / slices;
+        x.col0 = (int)(it - x.tile * slices) * kCols;
+        x.cols = H - x.col0 < kCols ? H - x.col0 : kCols;
+        const int64_t i0 = (x.tile * kSumWarps + w) * rows;
+        x.n = T - i0 >= rows ? rows : T > i0 ? (int)(T - i0) : 0;
+        x.my = lane < x.n ? sorted[i0 + lane] : make_uint2(none, 0u);
+        x.before = x.n > 0 && i0 > 0 ? sorted[i0 - 1].x : none;
+        const uint32_t after = i0 + x.n < T ? sorted[i0 + x.n].x : none;
+        uint32_t next = __shfl_down_sync(0xffffffffu, x.my.x, 1);
+        if (lane == x.n - 1) next = after;
+        x.live = __popc(__ballot_sync(0xffffffffu, x.my.x != none)); // ids that count come first
+        x.ends = __ballot_sync(0xffffffffu, x.my.x != none && next != x.my.x);
+        x.began = x.live > 0 && x.before == __shfl_sync(0xffffffffu, x.my.x, 0);
+        x.direct = x.ends & ~(x.began ? (x.ends & (0u - x.ends)) : 0u);
+        return x;
+    };
+    // row r of x into its stage of the ring (one group per row, empty past the end)
+    auto fetch = [&](const Rows &x, int r) {
+        if (r < x.live) {
+            const uint32_t to = smem_addr(ring + (r % kStages) * kStage) + lane * 16;
+            const uint32_t tok = __shfl_sync(0xffffffffu, x.my.y, r), key = __shfl_sync(0xffffffffu, x.my.x, r);
+            if (lane * 16 < x.cols * (int)sizeof(TD))
+                copy_async16(to, reinterpret_cast<const uint8_t *>(dout + (int64_t)tok * dout_ld + x.col0) + lane * 16);
+            if (ADD && (x.direct >> r & 1)) {
+                const uint8_t *from = reinterpret_cast<const uint8_t *>(dtable + (int64_t)key * ld + x.col0);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) acc[i] = 0.f;
-        bool head = true; // still in the chunk's first run
-        for (int r0 = 0; r0 < live; r0 += U) {
-            PD v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t tok = __shfl_sync(0xffffffffu, my_tok, (r0 + u) & 31);
-                if (r0 + u < live && s < nstep)
-                    v[u] = reinterpret_cast<const PD *>(dout + (int64_t)tok * dout_ld)[s];
+                for (int b = 0; b < kOld; b += kWarp * 16)
+                    if (b + lane * 16 < x.cols * (int)sizeof(TG)) copy_async16(to + kDoutBytes + b, from + b + lane * 16);
             }
+        }
+        copy_commit();
+    };
+    Rows ahead;
+    if (blockIdx.x < sums) {
+        ahead = rows_of(blockIdx.x);
+        if (RING)
+            for (int r = 0; r < kStages; ++r) fetch(ahead, r);
+    }
+    for (int64_t it = blockIdx.x; it < sums; it += gridDim.x) {
+        const Rows cur = ahead;
+        const int64_t tile = cur.tile;
+        const int live = cur.live;
+        const uint32_t ends = cur.ends, direct = cur.direct;
+        const bool began = cur.began;
+        const Slice<VE, NG> sl{cur.col0 / VE + lane, nstep};
+        const bool more = it + gridDim.x < sums;
+        if (more) ahead = rows_of(it + gridDim.x);
+        float acc[NG][VE];
+        zero(acc);
+        // row r is added: where it ends a run, the sum goes to dtable, or to the warps that join it
+        auto take = [&](int r, const Pack<TD, VE>(&v)[NG], const Pack<TG, VE>(&old)[NG]) {
+            add_row(acc, v);
+            if (!(ends >> r & 1)) return;
+            if (direct >> r & 1) {
+                const uint32_t key = __shfl_sync(0xffffffffu, cur.my.x, r);
+                finish_row(dtable + (int64_t)key * ld, sl, acc, old, scale, ADD);
+            } else {
+                store_part(s_part(w, 0), mine, acc);
+            }
+            zero(acc);
+        };
+        if constexpr (RING) {
+            for (int r = 0; r < live; ++r) {
+                copy_wait<kStages - 1>();
+                __syncwarp();
+                const uint8_t *at = ring + (r % kStages) * kStage;
+                Pack<TD, VE> v[NG];
+                Pack<TG, VE> old[NG];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = r0 + u;
-                if (r >= live) break;
-                const uint32_t key = __shfl_sync(0xffffffffu, my_key, r);
-                const uint32_t next = r + 1 < n ? __shfl_sync(0xffffffffu, my_key, (r + 1) & 31) : after;
-                if (s < nstep) {
-#pragma unroll
-                    for (int i = 0; i < VE; ++i) acc[i] = __fadd_rn(acc[i], to_f(v[u].v[i]));
+                for (int g = 0; g < NG; ++g) {
+                    v[g] = reinterpret_cast<const Pack<TD, VE> *>(at)[mine.at(g)];
+                    if (ADD) old[g] = reinterpret_cast<const Pack<TG, VE> *>(at + kDoutBytes)[mine.at(g)];
                 }
-                const bool goes_on = r + 1 == n && next == key;
-                if (r + 1 < n && next == key) continue;
-                const bool began_before = head && before == key;
-                if (s < nstep) {
-                    if (!began_before && !goes_on) {
-                        finish_row<TG, VE>(dtable + (int64_t)key * ld, s, acc, scale, accumulate);
-                    } else {
-                        PF o;
+                __syncwarp();
+                fetch(cur, r + kStages);
+                take(r, v, old);
+            }
+            // the rows past `live` left empty groups: the next item's first rows follow them
+            if (more)
+                for (int r = 0; r < kStages; ++r) fetch(ahead, r);
+        } else {
+            constexpr int U = 4;
+            for (int r0 = 0; r0 < live; r0 += U) {
+                Pack<TD, VE> v[U][NG];
+                Pack<TG, VE> old[U][NG];
 #pragma unroll
-                        for (int i = 0; i < VE; ++i) o.v[i] = acc[i];
-                        reinterpret_cast<PF *>(partial + (2 * c + (began_before ? 0 : 1)) * part_ld)[s] = o;
+                for (int u = 0; u < U; ++u) {
+                    const uint32_t tok = __shfl_sync(0xffffffffu, cur.my.y, (r0 + u) & 31);
+                    load_row(v[u], dout + (int64_t)tok * dout_ld, sl, r0 + u < live);
+                }
+                if (ADD) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const uint32_t key = __shfl_sync(0xffffffffu, cur.my.x, (r0 + u) & 31);
+                        load_row(old[u], dtable + (int64_t)key * ld, sl, r0 + u < live && (direct >> (r0 + u) & 1));
                     }
                 }
-                head = false;
 #pragma unroll
-                for (int i = 0; i < VE; ++i) acc[i] = 0.f;
+                for (int u = 0; u < U; ++u)
+                    if (r0 + u < live) take(r0 + u, v[u], old[u]);
             }
+        }
+        uint32_t flags = 0;
+        if (began) flags |= kHead;
+        if (live > 0 && !(ends >> (live - 1) & 1)) { // the last run goes on
+            const bool through = began && ends == 0;
+            flags |= through ? kThrough : kTail;
+            store_part(s_part(w, through ? 0 : 1), mine, acc);
+        }
+        if (lane == 0) s_flags[w] = flags;
+        __syncthreads();
+        // runs that span warps: the warp in which one begins joins it, the last warp joins what entered the tile
+        auto join_from = [&](int q) { // adds heads from warp q on; true if the run ends in this tile
+            for (; q < kSumWarps; ++q) {
+                Pack<float, VE> p[NG];
+                load_part(p, s_part(q, 0), mine);
+                add_row(acc, p);
+                if (!(s_flags[q] & kThrough)) return true;
+            }
+            return false;
+        };
+        if (flags & kTail) {
+            const uint32_t key = __shfl_sync(0xffffffffu, cur.my.x, live - 1);
+            if (join_from(w + 1)) {
+                Pack<TG, VE> old[NG];
+                if (ADD) load_row(old, dtable + (int64_t)key * ld, sl);
+                finish_row(dtable + (int64_t)key * ld, sl, acc, old, scale, ADD);
+            } else {
+                store_part(partial + (2 * tile + 1) * part_ld, sl, acc);
+            }
+        }
+        if (w == kSumWarps - 1 && (s_flags[0] & kHead)) {
+            zero(acc);
+            (void)join_from(0);
+            store_part(partial + 2 * tile * part_ld, sl, acc);
+        }
+        __syncthreads();
+    }
+    if (ADD) return;
+    // rows of ids that do not occur: zeros
+    Pack<TG, VE> z;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) z.v[i] = from_f<TG>(0.f);
+    for (int64_t r0 = (int64_t)blockIdx.x * fill_rows; r0 < V; r0 += (int64_t)gridDim.x * fill_rows) {
+        const int64_t r1 = r0 + fill_rows < V ? r0 + fill_rows : V;
+        for (int64_t r = r0 + w; r < r1; r += kSumWarps) {
+            if (seen && (__ldg(seen + (r >> 5)) >> (r & 31) & 1)) continue;
+            Pack<TG, VE> *row = reinterpret_cast<Pack<TG, VE> *>(dtable + r * ld);
+            for (int s = lane; s < nstep; s += kWarp) row[s] = z;
         }
     }
 }
 
-// Chunk c's tail run, where it goes on into later chunks: its tail and their
-// heads, added in chunk order.  One block per chunk.
-template <typename TG, int VE>
-__global__ void __launch_bounds__(256)
-    k_embed_join(const uint32_t *__restrict__ keys, int64_t T, int64_t V, int H, float scale, bool accumulate,
+// Runs that span tiles: the tail of the tile in which one begins and the heads
+// of the tiles it goes on through, added in tile order.  A warp takes a tile
+// and a slice; most find nothing to do.
+template <typename TG, int VE, int NG, bool ADD>
+__global__ void __launch_bounds__(kSumThreads)
+    k_embed_join(const uint2 *__restrict__ sorted, int64_t T, int64_t V, int H, float scale, int tile_rows,
                  TG *__restrict__ dtable, int64_t ld, const float *__restrict__ partial, int64_t part_ld)
 {
     pdl_begin();
-    using PF = Pack<float, VE>;
-    const int64_t chunks = (T + kChunk - 1) / kChunk;
+    constexpr int U = 8;
     const int nstep = H / VE;
-    for (int64_t c = blockIdx.x; c + 1 < chunks; c += gridDim.x) {
-        const int64_t i0 = c * kChunk, i1 = i0 + kChunk;
-        const uint32_t key = keys[i1 - 1];
-        if (key == (uint32_t)V || keys[i1] != key) continue;
-        if (i0 > 0 && keys[i0 - 1] == key) continue; // an earlier chunk's
-        const int64_t last = (lower_bound(keys, T, key + 1) - 1) / kChunk;
-        for (int s = threadIdx.x; s < nstep; s += blockDim.x) {
-            PF a = reinterpret_cast<const PF *>(partial + (2 * c + 1) * part_ld)[s];
-            for (int64_t q = c + 1; q <= last; ++q) {
-                const PF b = reinterpret_cast<const PF *>(partial + 2 * q * part_ld)[s];
+    const int slices = (nstep + kWarp * NG - 1) / (kWarp * NG);
+    const int64_t tiles = (T + tile_rows - 1) / tile_rows;
+    const int64_t items = (tiles - 1) * slices;
+    const int64_t warps = (int64_t)gridDim.x * kSumWarps;
+    for (int64_t it = (int64_t)blockIdx.x * kSumWarps + threadIdx.x / kWarp; it < items; it += warps) {
+        const int64_t c = it / slices;
+        const int64_t i0 = c * tile_rows, i1 = i0 + tile_rows;
+        const uint32_t key = sorted[i1 - 1].x;
+        if (key == (uint32_t)V || sorted[i1].x != key) continue;
+        if (i0 > 0 && sorted[i0 - 1].x == key) continue; // an earlier tile's
+        const Slice<VE, NG> sl{(int)(it - c * slices) * kWarp * NG + (int)lane_id(), nstep};
+        Pack<TG, VE> old[NG];
+        if (ADD) load_row(old, dtable + (int64_t)key * ld, sl);
+        float acc[NG][VE];
+        zero(acc);
+        Pack<float, VE> p[U][NG];
+        load_row(p[0], partial + (2 * c + 1) * part_ld, sl);
+        add_row(acc, p[0]);
+        for (int64_t q0 = c + 1; q0 < tiles; q0 += U) {
+            bool on[U];
 #pragma unroll
-                for (int i = 0; i < VE; ++i) a.v[i] = __fadd_rn(a.v[i], b.v[i]);
+            for (int u = 0; u < U; ++u) {
+                on[u] = q0 + u < tiles && sorted[(q0 + u) * tile_rows].x == key;
             }
-            finish_row<TG, VE>(dtable + (int64_t)key * ld, s, a.v, scale, accumulate);
+#pragma unroll
+            for (int u = 0; u < U; ++u) load_row(p[u], partial + 2 * (q0 + u) * part_ld, sl, on[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (on[u]) add_row(acc, p[u]);
+            if (!on[U - 1]) break;
         }
+        finish_row(dtable + (int64_t)key * ld, sl, acc, old, scale, ADD);
     }
 }
 
 // ---- host ------------------------------------------------------------------------
 struct EmbedPlan {
     int passes, bits; // radix passes and bits per digit
-    int64_t tiles, chunks, part_ld;
-    int64_t off_k1, off_t0, off_t1, off_hist, off_part, bytes; // (keys 0 at offset 0)
+    int rows;         // sorted tokens per warp of the sums
+    int64_t tiles, sum_tiles, part_ld;
+    int64_t off_b, off_hist, off_seen, off_part, bytes; // (sorted tokens, one of two buffers, at offset 0)
 };
 
 EmbedPlan embed_plan(int64_t T, int64_t V, int32_t H)
@@ -372,17 +780,67 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int32_t H)
     while (bits < 32 && (V >> bits)) ++bits; // keys 0 .. V
     p.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
     p.bits = (bits + p.passes - 1) / p.passes;
-    p.tiles = (T + kSortTile - 1) / kSortTile;
-    p.chunks = (T + kChunk - 1) / kChunk;
+    p.tiles = T > kClusterMax ? (T + kSortTile - 1) / kSortTile : 0;
+    // few tokens: short tiles, so that more blocks share them (at 777 x 1001 and 8192 x 2048 each the fastest)
+    p.rows = T >= 4096 ? kSumRowsMax : T >= 1024 ? 8 : 4;
+    p.sum_tiles = (T + p.rows * kSumWarps - 1) / (p.rows * kSumWarps);
     p.part_ld = ((int64_t)H + 7) / 8 * 8;
     auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
-    p.off_k1 = up(T * 4);
-    p.off_t0 = p.off_k1 + up(T * 4);
-    p.off_t1 = p.off_t0 + up(T * 4);
-    p.off_hist = p.off_t1 + up(T * 4);
-    p.off_part = p.off_hist + up((p.tiles << p.bits) * 4);
-    p.bytes = p.off_part + up(2 * p.chunks * p.part_ld * 4);
+    p.off_b = up(T * 8);
+    p.off_hist = p.off_b + (p.tiles ? up(T * 8) : 0);
+    p.off_seen = p.off_hist + up((p.tiles << p.bits) * 4);
+    p.off_part = p.off_seen + up((V + 31) / 32 * 4);
+    p.bytes = p.off_part + up(2 * p.sum_tiles * p.part_ld * 4);
     return p;
+}
+
+template <int ITEMS>
+ap_status sort_cluster(const void *ids, bool wide, int64_t T, int64_t V, int64_t pad, const EmbedPlan &p, int blocks,
+                       uint2 *sorted, uint32_t *seen, uint32_t *d_status, cudaStream_t st)
+{
+    const size_t smem = (size_t)kClThreads * ITEMS * sizeof(uint2) + ((size_t)kClWarps << p.bits) * 2;
+    static const cudaError_t attr = cudaFuncSetAttribute(
+        (const void *)k_sort_cluster<ITEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (int)(kClThreads * ITEMS * sizeof(uint2) + ((size_t)kClWarps << kMaxDigitBits) * 2));
+    if (attr != cudaSuccess) return cuda_fail(attr, "embed_backward sort");
+    launch_cluster(k_sort_cluster<ITEMS>, blocks, kClThreads, smem, blocks, st, ids, wide, (int)T,
+                   (int)((T + blocks - 1) / blocks), V, pad, p.passes, p.bits, sorted, seen, d_status);
+    AP_CHECK_LAUNCH("embed_backward sort launch");
+    return AP_OK;
+}
+
+// Sorts the tokens into one of the two buffers at `sc`; *sorted is set to it.
+// seen (may be NULL): a bit for every id that occurs.
+ap_status sort_tokens(const void *ids, bool wide, int64_t T, int64_t V, int64_t pad, const EmbedPlan &p, char *sc,
+                      uint2 **sorted, uint32_t *seen, uint32_t *d_status, cudaStream_t st)
+{
+    uint2 *buf[2] = {reinterpret_cast<uint2 *>(sc), reinterpret_cast<uint2 *>(sc + p.off_b)};
+    *sorted = buf[0];
+    if (T == 0) return AP_OK;
+    if (!p.tiles) {
+        int blocks = 1;
+        while (blocks < kClBlocks && (int64_t)blocks * kClThreads < T) blocks *= 2;
+        const int64_t each = ((T + blocks - 1) / blocks + kClThreads - 1) / kClThreads; // tokens per thread
+        if (each <= 1) return sort_cluster<1>(ids, wide, T, V, pad, p, blocks, buf[0], seen, d_status, st);
+        if (each <= 2) return sort_cluster<2>(ids, wide, T, V, pad, p, blocks, buf[0], seen, d_status, st);
+        if (each <= 4) return sort_cluster<4>(ids, wide, T, V, pad, p, blocks, buf[0], seen, d_status, st);
+        if (each <= 8) return sort_cluster<8>(ids, wide, T, V, pad, p, blocks, buf[0], seen, d_status, st);
+        return sort_cluster<16>(ids, wide, T, V, pad, p, blocks, buf[0], seen, d_status, st);
+    }
+    uint32_t *hist = reinterpret_cast<uint32_t *>(sc + p.off_hist);
+    for (int q = 0; q < p.passes; ++q) {
+        const uint2 *in = q ? buf[(q - 1) & 1] : nullptr;
+        launch(k_sort_count, (int)p.tiles, kSortThreads, 0, st, in, ids, wide, T, V, pad, q * p.bits, p.bits, hist,
+               q == 0 ? seen : nullptr, d_status);
+        AP_CHECK_LAUNCH("embed_backward count launch");
+        launch(k_sort_scan, 1, 1024, 0, st, hist, p.tiles << p.bits);
+        AP_CHECK_LAUNCH("embed_backward scan launch");
+        launch(k_sort_scatter, (int)p.tiles, kSortThreads, 0, st, in, ids, wide, T, V, pad, q * p.bits, p.bits, hist,
+               buf[q & 1], q + 1 == p.passes ? seen : nullptr);
+        AP_CHECK_LAUNCH("embed_backward scatter launch");
+        *sorted = buf[q & 1];
+    }
+    return AP_OK;
 }
 
 bool row_type(int32_t d) { return d == AP_DTYPE_BF16 || d == AP_DTYPE_F32; }
@@ -422,45 +880,62 @@ void embed_typed(const void *table, int64_t V, int64_t ld, int32_t tt, const voi
         launch_embed<TI, TO, 1, 4>(table, V, ld, ids, wide, T, H, scale, out, out_ld, d_status, st);
 }
 
-template <typename TD, typename TG, int VE>
-ap_status embed_sums(const TD *dout, int64_t dout_ld, const uint32_t *keys, const uint32_t *toks, int64_t T, int64_t V,
-                     int H, float scale, bool accumulate, TG *dtable, int64_t ld, float *partial, int64_t part_ld,
-                     cudaStream_t st)
+// What the sums kernels take besides their types.
+struct SumArgs {
+    const void *dout;
+    int64_t dout_ld;
+    const uint2 *sorted;
+    int64_t T, V;
+    int H;
+    float scale;
+    void *dtable;
+    int64_t ld;
+    float *partial;
+    const uint32_t *seen;
+    const void *ids;
+    bool wide;
+    int64_t pad;
+};
+
+template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
+ap_status embed_sums(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
 {
-    if (!accumulate) {
-        static const int resident = resident_grid((const void *)k_embed_fill<TG, VE>, 256);
-        launch(k_embed_fill<TG, VE>, grid_for((V + kFillRows - 1) / kFillRows, resident), 256, 0, st, keys, T, V, H,
-               dtable, ld);
-        AP_CHECK_LAUNCH("embed_backward fill launch");
-    }
-    if (T == 0) return AP_OK;
-    constexpr int U = VE == 1 ? 16 : 8;
-    const int64_t chunks = (T + kChunk - 1) / kChunk;
-    static const int resident = resident_grid((const void *)k_embed_sum<TD, TG, VE, U>, 256);
-    const int64_t items = chunks * ((H / VE + kWarp - 1) / kWarp);
-    launch(k_embed_sum<TD, TG, VE, U>, grid_for(items, resident), 256, 0, st, dout, dout_ld, keys, toks, T, V, H,
-           scale, accumulate, dtable, ld, partial, part_ld);
+    TG *dtable = static_cast<TG *>(a.dtable);
+    const int slices = (a.H / VE + kWarp * NG - 1) / (kWarp * NG);
+    const auto kernel = k_embed_sum<TD, TG, VE, NG, ADD, RING>;
+    constexpr int smem = kSumSmem<TD, TG, VE, NG, ADD, RING>;
+    static const cudaError_t attr = cudaFuncSetAttribute((const void *)kernel,
+                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (attr != cudaSuccess) return cuda_fail(attr, "embed_backward sum");
+    static const int resident = resident_grid((const void *)kernel, kSumThreads, smem);
+    // zeros are written 128 KB at a time or so
+    const int64_t gb = (int64_t)a.H * sizeof(TG);
+    const int fill_rows = (int)(gb >= (128 << 10) / kSumWarps ? kSumWarps : (128 << 10) / gb);
+    int64_t want = p.sum_tiles * slices;
+    if (!ADD && (a.V + fill_rows - 1) / fill_rows > want) want = (a.V + fill_rows - 1) / fill_rows;
+    launch(kernel, (int)(want < resident ? want : resident), kSumThreads, smem, st,
+           static_cast<const TD *>(a.dout), a.dout_ld, a.sorted, a.T, a.V, a.H, a.scale, p.rows, dtable, a.ld,
+           a.partial, p.part_ld, a.seen, fill_rows, a.ids, a.wide, a.pad);
     AP_CHECK_LAUNCH("embed_backward sum launch");
-    if (chunks > 1) {
-        static const int resident_j = resident_grid((const void *)k_embed_join<TG, VE>, 256);
-        launch(k_embed_join<TG, VE>, (int)(chunks - 1 < resident_j ? chunks - 1 : resident_j), 256, 0, st, keys, T, V,
-               H, scale, accumulate, dtable, ld, partial, part_ld);
+    if (p.sum_tiles > 1) {
+        static const int resident_j = resident_grid((const void *)k_embed_join<TG, VE, NG, ADD>, kSumThreads);
+        launch(k_embed_join<TG, VE, NG, ADD>, grid_for((p.sum_tiles - 1) * slices, resident_j), kSumThreads, 0, st,
+               a.sorted, a.T, a.V, a.H, a.scale, p.rows * kSumWarps, dtable, a.ld, a.partial, p.part_ld);
         AP_CHECK_LAUNCH("embed_backward join launch");
     }
     return AP_OK;
 }
 
 template <typename TD, typename TG>
-ap_status embed_backward_typed(const void *dout, int64_t dout_ld, int32_t dt, const uint32_t *keys,
-                               const uint32_t *toks, int64_t T, int64_t V, int H, float scale, bool accumulate,
-                               void *dtable, int64_t ld, int32_t gt, float *partial, int64_t part_ld, cudaStream_t st)
+ap_status embed_backward_typed(const SumArgs &a, int32_t dt, int32_t gt, bool add, const EmbedPlan &p, cudaStream_t st)
 {
-    constexpr int VE = sizeof(TD) == 2 ? 8 : 4;
-    const TD *d = static_cast<const TD *>(dout);
-    TG *g = static_cast<TG *>(dtable);
-    if (H % VE == 0 && vec_ok(dout, dout_ld, dt, VE) && vec_ok(dtable, ld, gt, VE))
-        return embed_sums<TD, TG, VE>(d, dout_ld, keys, toks, T, V, H, scale, accumulate, g, ld, partial, part_ld, st);
-    return embed_sums<TD, TG, 1>(d, dout_ld, keys, toks, T, V, H, scale, accumulate, g, ld, partial, part_ld, st);
+    constexpr int VE = sizeof(TD) == 2 && sizeof(TG) == 2 ? 8 : 4;
+    constexpr int NG = sizeof(TD) == 2 && sizeof(TG) == 4 ? 2 : 1; // 512 bytes of dout a row and slice
+    constexpr int V16 = sizeof(TD) == 2 || sizeof(TG) == 2 ? 8 : 4;
+    if (a.H % V16 == 0 && vec_ok(a.dout, a.dout_ld, dt, V16) && vec_ok(a.dtable, a.ld, gt, V16))
+        return add ? embed_sums<TD, TG, VE, NG, true, true>(a, p, st)
+                   : embed_sums<TD, TG, VE, NG, false, true>(a, p, st);
+    return add ? embed_sums<TD, TG, 1, 4, true, false>(a, p, st) : embed_sums<TD, TG, 1, 4, false, false>(a, p, st);
 }
 
 bool embed_sizes_ok(int64_t T, int64_t V, int32_t H)
@@ -542,30 +1017,16 @@ extern "C" ap_status ap_embed_backward(const void *dout, int64_t dout_ld, int32_
                     (long long)p.bytes);
     cudaStream_t st = (cudaStream_t)stream;
     char *sc = static_cast<char *>(scratch);
-    uint32_t *key[2] = {reinterpret_cast<uint32_t *>(sc), reinterpret_cast<uint32_t *>(sc + p.off_k1)};
-    uint32_t *tok[2] = {reinterpret_cast<uint32_t *>(sc + p.off_t0), reinterpret_cast<uint32_t *>(sc + p.off_t1)};
-    uint32_t *hist = reinterpret_cast<uint32_t *>(sc + p.off_hist);
-    float *partial = reinterpret_cast<float *>(sc + p.off_part);
-    const bool wide = id_bytes == 8;
-    for (int q = 0; T > 0 && q < p.passes; ++q) {
-        const uint32_t *kin = q ? key[(q - 1) & 1] : nullptr, *tin = q ? tok[(q - 1) & 1] : nullptr;
-        launch(k_sort_count, (int)p.tiles, kSortThreads, 0, st, kin, ids, wide, T, V, padding_idx, q * p.bits, p.bits,
-               hist, d_status);
-        AP_CHECK_LAUNCH("embed_backward count launch");
-        launch(k_sort_scan, 1, 1024, 0, st, hist, p.tiles << p.bits);
-        AP_CHECK_LAUNCH("embed_backward scan launch");
-        launch(k_sort_scatter, (int)p.tiles, kSortThreads, 0, st, kin, tin, ids, wide, T, V, padding_idx, q * p.bits,
-               p.bits, hist, key[q & 1], tok[q & 1]);
-        AP_CHECK_LAUNCH("embed_backward scatter launch");
-    }
-    const uint32_t *keys = key[(p.passes - 1) & 1], *toks = tok[(p.passes - 1) & 1];
-#define AP_EMBED_BWD(TD, TG)                                                                                         \
-    embed_backward_typed<TD, TG>(dout, dout_ld, dout_dtype, keys, toks, T, V, H, scale, accumulate != 0, dtable,      \
-                                 dtable_ld, dtable_dtype, partial, p.part_ld, st)
-    const bool fd = dout_dtype == AP_DTYPE_F32, fg = dtable_dtype == AP_DTYPE_F32;
-    if (fd && fg) return AP_EMBED_BWD(float, float);
-    if (fd) return AP_EMBED_BWD(float, bf16_t);
-    if (fg) return AP_EMBED_BWD(bf16_t, float);
-    return AP_EMBED_BWD(bf16_t, bf16_t);
-#undef AP_EMBED_BWD
+    uint32_t *seen = reinterpret_cast<uint32_t *>(sc + p.off_seen);
+    uint2 *sorted = nullptr;
+    const ap_status ss = sort_tokens(ids, id_bytes == 8, T, V, padding_idx, p, sc, &sorted, accumulate ? nullptr : seen,
+                                     d_status, st);
+    if (ss != AP_OK) return ss;
+    const SumArgs a = {dout,   dout_ld, sorted, T, V, H, scale, dtable, dtable_ld,
+                       reinterpret_cast<float *>(sc + p.off_part), T > 0 ? seen : nullptr, ids, id_bytes == 8, padding_idx};
+    const bool fd = dout_dtype == AP_DTYPE_F32, fg = dtable_dtype == AP_DTYPE_F32, add = accumulate != 0;
+    if (fd && fg) return embed_backward_typed<float, float>(a, dout_dtype, dtable_dtype, add, p, st);
+    if (fd) return embed_backward_typed<float, bf16_t>(a, dout_dtype, dtable_dtype, add, p, st);
+    if (fg) return embed_backward_typed<bf16_t, float>(a, dout_dtype, dtable_dtype, add, p, st);
+    return embed_backward_typed<bf16_t, bf16_t>(a, dout_dtype, dtable_dtype, add, p, st);
 }
