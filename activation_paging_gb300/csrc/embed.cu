@@ -135,15 +135,33 @@ __device__ __forceinline__ uint32_t sort_key(const void *ids, bool wide, int64_t
     return (uint32_t)id;
 }
 
-// Ranks the warp's 32 tokens of one step among its tokens of the same digit
-// (d = -1: no token): the count so far plus the equal lanes below.
-__device__ __forceinline__ uint32_t warp_rank(uint16_t *cnt, int d)
+// Lanes of the warp whose digit equals this lane's (one vote per bit; a lane
+// without a token, in = false, gets none).  __match_any_sync takes about 60
+// cycles of an SM for each warp: 2000 cycles for one digit of 1024 tokens,
+// where the votes take 350.
+__device__ __forceinline__ uint32_t same_digit(uint32_t d, bool in, int bits)
 {
-    const uint32_t same = __match_any_sync(0xffffffffu, d);
+    uint32_t m = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+    for (int b = 0; b < kMaxDigitBits; ++b) {
+        if (b < bits) {
+            const bool one = d >> b & 1;
+            const uint32_t v = __ballot_sync(0xffffffffu, one);
+            m &= one ? v : ~v;
+        }
+    }
+    return m;
+}
+
+// Ranks the warp's 32 tokens of one step among its tokens of the same digit:
+// the count so far plus the equal lanes below.
+__device__ __forceinline__ uint32_t warp_rank(uint16_t *cnt, uint32_t d, bool in, int bits)
+{
+    const uint32_t same = same_digit(d, in, bits);
     uint32_t rank = 0;
-    if (d >= 0) rank = cnt[d] + __popc(same & lanemask_lt());
+    if (in) rank = cnt[d] + __popc(same & lanemask_lt());
     __syncwarp();
-    if (d >= 0 && (same >> lane_id()) == 1u) cnt[d] = (uint16_t)(rank + 1); // the last lane of its digit
+    if (in && (same >> lane_id()) == 1u) cnt[d] = (uint16_t)(rank + 1); // the last lane of its digit
     __syncwarp();
     return rank;
 }
@@ -158,16 +176,17 @@ __device__ __forceinline__ void mark_seen(uint32_t *seen, uint32_t key, int64_t 
 // One cluster sorts up to kClusterMax tokens in one launch, in registers and
 // (distributed) shared memory.  Block r holds tokens r * per .. r * per + per - 1
 // of the current order, warp q of it a run of 32 * ITEMS.  A pass: every warp
-// ranks its tokens per digit; a thread per digit adds the warps up; the
-// blocks exchange their digit totals; every token goes to its new place in
-// the block that holds it, in the last pass to memory.  Six dependent
-// launches of the form below cost 35 us at any length up to some thousand
-// tokens; this one costs its passes alone.
+// ranks its tokens per digit; the warps' counts are added up per digit; every
+// block gives its totals to all blocks; every token goes to its new place in
+// the block that holds it, in the last pass to memory.  The phases wait for
+// one another (about 4 us for two passes over 8192 tokens, of which the two
+// or three barriers of the cluster take a half); three launches per digit, as
+// below, cost 35 us.
 constexpr int kClThreads = 1024;
 constexpr int kClWarps = kClThreads / kWarp;
-constexpr int kClItemsMax = 16;
-constexpr int kClBlocks = 8; // the largest portable cluster
-constexpr int64_t kClusterMax = (int64_t)kClBlocks * kClThreads * kClItemsMax;
+constexpr int kClItemsMax = 8;
+constexpr int kClBlocksMax = 16; // 8 is the largest portable cluster, and what is used where 16 do not fit
+constexpr int64_t kClusterMax = (int64_t)kClBlocksMax * kClThreads * kClItemsMax;
 
 __device__ __forceinline__ void cluster_sync()
 {
@@ -181,15 +200,19 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t rank)
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
     return a;
 }
-__device__ __forceinline__ uint32_t cluster_load(uint32_t addr)
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t v)
 {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void cluster_store(uint32_t addr, uint2 v)
 {
     asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+
+// Dynamic shared memory: the block's tokens, the warps' counts, the blocks' totals.
+constexpr size_t cluster_smem(int items, int bits, int blocks)
+{
+    return (size_t)kClThreads * items * 8 + ((size_t)(kClWarps + blocks) << bits) * 2;
 }
 
 template <int ITEMS>
@@ -198,23 +221,34 @@ __global__ void __launch_bounds__(kClThreads, 1)
                    int bits, uint2 *__restrict__ sorted, uint32_t *__restrict__ seen, uint32_t *d_status)
 {
     pdl_begin_after(); // the sums kernel reads ids and rows ahead of its own wait
-    extern __shared__ uint2 s_pairs[]; // [kClThreads * ITEMS], then the warps' counts [kClWarps][D]
-    __shared__ uint32_t s_tot[1 << kMaxDigitBits], s_base[1 << kMaxDigitBits], s_warp[kClWarps];
-    const int D = 1 << bits;
-    uint16_t *cnt = reinterpret_cast<uint16_t *>(s_pairs + kClThreads * ITEMS);
+    // Counts and totals are 16 bits, two digits to a word (bits >= 1, a block holds at most 8192 tokens).
+    extern __shared__ uint2 s_pairs[];                                            // [kClThreads * ITEMS]
+    uint16_t *cnt = reinterpret_cast<uint16_t *>(s_pairs + kClThreads * ITEMS);   // [kClWarps][D]
+    __shared__ uint32_t s_base[1 << kMaxDigitBits], s_warp[kClWarps], s_group[kClThreads];
+    const int D = 1 << bits, D2 = D / 2;
+    uint16_t *tot = cnt + kClWarps * D; // [blocks][D]
+    uint32_t *cnt2 = reinterpret_cast<uint32_t *>(cnt), *tot2 = reinterpret_cast<uint32_t *>(tot);
     const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
     const uint32_t me = blockIdx.x, blocks = gridDim.x; // the grid is one cluster
     const int first = (int)me * per;
     const int n = T - first < per ? T - first : per; // this block's tokens (may be <= 0)
     const int l0 = wid * (ITEMS * kWarp) + lane;
     uint16_t *mine = cnt + wid * D;
+    auto sync_all = [&] {
+        if (blocks > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+    };
+    // the warps' counts of a pair of digits are added up by `groups` threads, each over `each` warps
+    const int groups = D2 >= kClThreads ? 1 : kClThreads / D2 < kClWarps ? kClThreads / D2 : kClWarps;
+    const int each = kClWarps / groups;
+    const int pair_of = (int)threadIdx.x & (D2 - 1), group = (int)threadIdx.x / D2;
     if (seen) // cleared before the first barrier of the cluster, set in the last pass
         for (int64_t i = (int64_t)me * kClThreads + threadIdx.x; i < (V + 31) / 32; i += (int64_t)blocks * kClThreads)
             seen[i] = 0;
     for (int pass = 0; pass < passes; ++pass) {
         const int shift = pass * bits;
-        uint32_t *words = reinterpret_cast<uint32_t *>(cnt);
-        for (int i = threadIdx.x; i < kClWarps * D / 2; i += kClThreads) words[i] = 0;
         uint2 pair[ITEMS];
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
@@ -226,34 +260,41 @@ __global__ void __launch_bounds__(kClThreads, 1)
                     pair[i] = s_pairs[l];
             }
         }
-        __syncthreads();
+        for (int i = lane; i < D2; i += kWarp) cnt2[wid * D2 + i] = 0; // the warp's own counts
+        __syncwarp();
         uint32_t rank[ITEMS];
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i)
-            rank[i] = warp_rank(mine, l0 + i * kWarp < n ? (int)((pair[i].x >> shift) & (D - 1)) : -1);
-        __syncthreads();
-        if ((int)threadIdx.x < D) {
-            uint32_t c[kClWarps], sum = 0;
-#pragma unroll
-            for (int q = 0; q < kClWarps; ++q) c[q] = cnt[q * D + threadIdx.x];
-#pragma unroll
-            for (int q = 0; q < kClWarps; ++q) {
-                cnt[q * D + threadIdx.x] = (uint16_t)sum;
-                sum += c[q];
-            }
-            s_tot[threadIdx.x] = sum;
+        for (int i = 0; i < ITEMS; ++i) {
+            const bool in = l0 + i * kWarp < n;
+            rank[i] = warp_rank(mine, in ? pair[i].x >> shift & (D - 1) : 0u, in, bits);
         }
-        cluster_sync(); // the totals are there, and no block needs its s_pairs any more
+        __syncthreads();
+        uint32_t sum = 0;
+        if (group < groups) {
+            for (int q = 0; q < each; ++q) sum += cnt2[(group * each + q) * D2 + pair_of];
+            s_group[group * D2 + pair_of] = sum;
+        }
+        __syncthreads();
+        if (group < groups) {
+            uint32_t base = 0;
+            for (int g = 0; g < group; ++g) base += s_group[g * D2 + pair_of];
+            for (int q = 0; q < each; ++q) {
+                uint32_t *c = &cnt2[(group * each + q) * D2 + pair_of];
+                const uint32_t v = *c;
+                *c = base;
+                base += v;
+            }
+            if (group == groups - 1) // base is the block's total: to every block
+                for (uint32_t r = 0; r < blocks; ++r)
+                    cluster_store(cluster_addr(smem_addr(&tot2[me * D2 + pair_of]), r), base);
+        }
+        sync_all(); // the totals are there, and no block needs its s_pairs any more
         uint32_t before = 0, all = 0;
         if ((int)threadIdx.x < D) {
-            const uint32_t at = smem_addr(&s_tot[threadIdx.x]);
-            uint32_t c[kClBlocks];
-#pragma unroll
-            for (uint32_t r = 0; r < kClBlocks; ++r) c[r] = r < blocks ? cluster_load(cluster_addr(at, r)) : 0u;
-#pragma unroll
-            for (uint32_t r = 0; r < kClBlocks; ++r) {
-                if (r < me) before += c[r];
-                all += c[r];
+            for (uint32_t r = 0; r < blocks; ++r) {
+                const uint32_t c = tot[r * D + threadIdx.x];
+                if (r < me) before += c;
+                all += c;
             }
         }
         uint32_t x = all; // exclusive sum over the digits
@@ -264,34 +305,28 @@ __global__ void __launch_bounds__(kClThreads, 1)
         }
         if (lane == 31) s_warp[wid] = x;
         __syncthreads();
-        if (wid == 0) {
-            const uint32_t v = s_warp[lane];
-            uint32_t z = v;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, z, off);
-                if (lane >= off) z += y;
-            }
-            s_warp[lane] = z - v;
-        }
+        uint32_t lower = lane < wid ? s_warp[lane] : 0u; // the digits of the warps below
+        lower = __reduce_add_sync(0xffffffffu, lower);
+        if ((int)threadIdx.x < D) s_base[threadIdx.x] = lower + x - all + before;
         __syncthreads();
-        if ((int)threadIdx.x < D) s_base[threadIdx.x] = s_warp[wid] + x - all + before;
-        __syncthreads();
+        const bool last = pass + 1 == passes;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const bool in = l0 + i * kWarp < n;
-            if (seen && pass + 1 == passes) mark_seen(seen, in ? pair[i].x : (uint32_t)V, V);
+            if (seen && last) mark_seen(seen, in ? pair[i].x : (uint32_t)V, V);
             if (!in) continue;
             const int d = (int)((pair[i].x >> shift) & (D - 1));
             const uint32_t at = s_base[d] + mine[d] + rank[i];
-            if (pass + 1 == passes) {
+            if (last) {
                 sorted[at] = pair[i];
             } else {
                 const uint32_t to = at / (uint32_t)per;
                 cluster_store(cluster_addr(smem_addr(s_pairs + (at - to * per)), to), pair[i]);
             }
         }
-        cluster_sync(); // the pairs are in place; no block leaves while another reads its totals
+        // the pairs are in place, and nobody reads the totals any more; nothing
+        // of another block is touched after the last pass's barrier above
+        if (!last) sync_all();
     }
 }
 
@@ -378,12 +413,12 @@ __global__ void __launch_bounds__(kSortThreads)
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
         const int64_t t = t0 + i * kWarp;
-        int d = -1;
+        uint32_t d = 0;
         if (t < T) {
             pair[i] = in ? in[t] : make_uint2(sort_key(ids, wide, t, V, pad, nullptr), (uint32_t)t);
-            d = (int)((pair[i].x >> shift) & (D - 1));
+            d = (pair[i].x >> shift) & (D - 1);
         }
-        rank[i] = warp_rank(s_cnt[wid], d);
+        rank[i] = warp_rank(s_cnt[wid], d, t < T, bits);
     }
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += kSortThreads) {
@@ -780,7 +815,7 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int32_t H)
     while (bits < 32 && (V >> bits)) ++bits; // keys 0 .. V
     p.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
     p.bits = (bits + p.passes - 1) / p.passes;
-    p.tiles = T > kClusterMax ? (T + kSortTile - 1) / kSortTile : 0;
+    p.tiles = T > kClusterMax / 2 ? (T + kSortTile - 1) / kSortTile : 0; // (half: clusters of 8)
     // few tokens: short tiles, so that more blocks share them (at 777 x 1001 and 8192 x 2048 each the fastest)
     p.rows = T >= 4096 ? kSumRowsMax : T >= 1024 ? 8 : 4;
     p.sum_tiles = (T + p.rows * kSumWarps - 1) / (p.rows * kSumWarps);
@@ -798,15 +833,44 @@ template <int ITEMS>
 ap_status sort_cluster(const void *ids, bool wide, int64_t T, int64_t V, int64_t pad, const EmbedPlan &p, int blocks,
                        uint2 *sorted, uint32_t *seen, uint32_t *d_status, cudaStream_t st)
 {
-    const size_t smem = (size_t)kClThreads * ITEMS * sizeof(uint2) + ((size_t)kClWarps << p.bits) * 2;
-    static const cudaError_t attr = cudaFuncSetAttribute(
-        (const void *)k_sort_cluster<ITEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        (int)(kClThreads * ITEMS * sizeof(uint2) + ((size_t)kClWarps << kMaxDigitBits) * 2));
+    static const cudaError_t attr = [] {
+        const void *k = (const void *)k_sort_cluster<ITEMS>;
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)cluster_smem(ITEMS, kMaxDigitBits, kClBlocksMax));
+        return e != cudaSuccess ? e : cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    }();
     if (attr != cudaSuccess) return cuda_fail(attr, "embed_backward sort");
-    launch_cluster(k_sort_cluster<ITEMS>, blocks, kClThreads, smem, blocks, st, ids, wide, (int)T,
-                   (int)((T + blocks - 1) / blocks), V, pad, p.passes, p.bits, sorted, seen, d_status);
+    launch_cluster(k_sort_cluster<ITEMS>, blocks, kClThreads, cluster_smem(ITEMS, p.bits, blocks), blocks, st, ids,
+                   wide, (int)T, (int)((T + blocks - 1) / blocks), V, pad, p.passes, p.bits, sorted, seen, d_status);
     AP_CHECK_LAUNCH("embed_backward sort launch");
     return AP_OK;
+}
+
+// The largest cluster that this GPU takes with the sort's largest shared memory.
+int cluster_blocks()
+{
+    static const int most = [] {
+        const void *k = (const void *)k_sort_cluster<kClItemsMax>;
+        const size_t smem = cluster_smem(kClItemsMax, kMaxDigitBits, kClBlocksMax);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kClBlocksMax;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = kClBlocksMax;
+        cfg.blockDim = kClThreads;
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        const bool ok =
+            cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess &&
+            cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess && n > 0;
+        if (!ok) (void)cudaGetLastError();
+        return ok ? kClBlocksMax : kClBlocksMax / 2;
+    }();
+    return most;
 }
 
 // Sorts the tokens into one of the two buffers at `sc`; *sorted is set to it.
@@ -817,15 +881,15 @@ ap_status sort_tokens(const void *ids, bool wide, int64_t T, int64_t V, int64_t 
     uint2 *buf[2] = {reinterpret_cast<uint2 *>(sc), reinterpret_cast<uint2 *>(sc + p.off_b)};
     *sorted = buf[0];
     if (T == 0) return AP_OK;
-    if (!p.tiles) {
+    const int most = T > kClThreads ? cluster_blocks() : 1;
+    if (T <= (int64_t)most * kClThreads * kClItemsMax) {
         int blocks = 1;
-        while (blocks < kClBlocks && (int64_t)blocks * kClThreads < T) blocks *= 2;
+        while (blocks < most && (int64_t)blocks * kClThreads < T) blocks *= 2;
         const int64_t each = ((T + blocks - 1) / blocks + kClThreads - 1) / kClThreads; // tokens per thread
         if (each <= 1) return sort_cluster<1>(ids, wide, T, V, pad, p, blocks, buf[0], seen, d_status, st);
         if (each <= 2) return sort_cluster<2>(ids, wide, T, V, pad, p, blocks, buf[0], seen, d_status, st);
         if (each <= 4) return sort_cluster<4>(ids, wide, T, V, pad, p, blocks, buf[0], seen, d_status, st);
-        if (each <= 8) return sort_cluster<8>(ids, wide, T, V, pad, p, blocks, buf[0], seen, d_status, st);
-        return sort_cluster<16>(ids, wide, T, V, pad, p, blocks, buf[0], seen, d_status, st);
+        return sort_cluster<8>(ids, wide, T, V, pad, p, blocks, buf[0], seen, d_status, st);
     }
     uint32_t *hist = reinterpret_cast<uint32_t *>(sc + p.off_hist);
     for (int q = 0; q < p.passes; ++q) {
