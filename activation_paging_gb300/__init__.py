@@ -19,6 +19,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -43,8 +44,10 @@ def lib():
 
 
 def _stream(stream) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle without a Stream object (a third of a call's host time)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _p(t):
@@ -86,21 +89,23 @@ def _groups(T: int, group_tokens: int) -> int:
     return -(-T // (group_tokens or T)) if T else 0
 
 
+def _need_shape(t: torch.Tensor, dtype, shape: tuple, name: str) -> int:
+    """_need, the shape too; returns the address."""
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype, name)
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
 def _mask(mask: torch.Tensor | None, T: int):
     if mask is None:
-        return
+        return None
     if mask.dtype not in (torch.bool, torch.uint8):
         raise ValueError(f"mask must be bool or uint8, got {mask.dtype}")
-    _need(mask, mask.dtype, "mask")
-    if mask.shape != (T,):
-        raise ValueError(f"mask must be [{T}], got {list(mask.shape)}")
+    return _need_shape(mask, mask.dtype, (T,), "mask")
 
 
-def _shape(t: torch.Tensor | None, shape: tuple, name: str):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-
-
+@functools.lru_cache(maxsize=1024)
 def route_balance_scratch_bytes(T: int, E: int, group_tokens: int = 0) -> int:
     n = ctypes.c_int64(0)
     check(lib().ap_route_balance_scratch_bytes(T, E, group_tokens, ctypes.byref(n)), "route_balance_scratch_bytes")
@@ -116,26 +121,25 @@ def route_balance(logits: torch.Tensor, k: int, coef: float = 1.0, group_tokens:
     ([G, E] float32, d loss / d p, for ``route_backward``), ``loss`` (float32
     scalar tensor, ``coef`` x the mean over groups of E sum_e share_e prob_e)
     and ``scratch``.  ``mask`` ([T] bool or uint8): tokens that count.  Pass
-    ``out`` (such a dict) to reuse buffers."""
+    ``out`` (such a dict, whole or in part) to reuse buffers."""
     _need(logits, torch.float32, "logits")
     T, E = logits.shape
-    _mask(mask, T)
+    m = _mask(mask, T)
     G = _groups(T, group_tokens)
-    dev = logits.device
-    o = dict(out) if out is not None else {}
-    for name, shape, dtype in (("idx", (T, k), torch.int32), ("w", (T, k), torch.float32),
-                               ("counts", (G, E), torch.int32), ("prob", (G, E), torch.float32),
-                               ("slope", (G, E), torch.float32), ("loss", (), torch.float32)):
-        if name in o:
-            _need(o[name], dtype, name)
-            _shape(o[name], shape, name)
-        else:
-            o[name] = _empty(shape, dtype, dev, stream)
     sb = route_balance_scratch_bytes(T, E, group_tokens)
+    o = dict(out) if out is not None else {}
+    pairs, sums = (T, k), (G, E)
+    for name, shape, dtype in (("idx", pairs, torch.int32), ("w", pairs, torch.float32), ("counts", sums, torch.int32),
+                               ("prob", sums, torch.float32), ("slope", sums, torch.float32),
+                               ("loss", (), torch.float32)):
+        if name in o:
+            _need_shape(o[name], dtype, shape, name)
+        else:
+            o[name] = _empty(shape, dtype, logits.device, stream)
     if "scratch" not in o or o["scratch"].numel() < sb:
-        o["scratch"] = _empty(sb, torch.uint8, dev, stream)
-    check(lib().ap_route_balance(_p(logits), T, E, k, group_tokens, _p(mask), coef, _p(o["idx"]), _p(o["w"]),
-                                 _p(o["counts"]), _p(o["prob"]), _p(o["slope"]), _p(o["loss"]), _p(o["scratch"]),
+        o["scratch"] = _empty(sb, torch.uint8, logits.device, stream)
+    check(lib().ap_route_balance(_p(logits), T, E, k, group_tokens, m, coef, _p(o["idx"]), _p(o["w"]), _p(o["counts"]),
+                                 _p(o["prob"]), _p(o["slope"]), _p(o["loss"]), _p(o["scratch"]),
                                  o["scratch"].numel(), _stream(stream)), "route_balance")
     return o
 
@@ -149,59 +153,62 @@ def route_backward(logits: torch.Tensor, idx: torch.Tensor | None = None, w: tor
     its ``slope`` and, if not 1, ``dloss``); either may be left out."""
     _need(logits, torch.float32, "logits")
     T, E = logits.shape
-    _mask(mask, T)
-    k = 1
+    m = _mask(mask, T)
+    k, pi, pw, pdw, ps, pl = 1, None, None, None, None, None
     if dw is not None:
         if idx is None or w is None:
             raise ValueError("dw needs idx and w")
-        _need(dw, torch.float32, "dw")
-        _need(idx, torch.int32, "idx")
-        _need(w, torch.float32, "w")
         k = dw.shape[1]
-        for t, name in ((dw, "dw"), (idx, "idx"), (w, "w")):
-            _shape(t, (T, k), name)
+        pdw = _need_shape(dw, torch.float32, (T, k), "dw")
+        pi = _need_shape(idx, torch.int32, (T, k), "idx")
+        pw = _need_shape(w, torch.float32, (T, k), "w")
     if slope is not None:
-        _need(slope, torch.float32, "slope")
-        _shape(slope, (_groups(T, group_tokens), E), "slope")
+        ps = _need_shape(slope, torch.float32, (_groups(T, group_tokens), E), "slope")
     if dloss is not None:
         _need(dloss, torch.float32, "dloss")
         if dloss.numel() != 1:
             raise ValueError("dloss must hold one value")
+        pl = dloss.data_ptr()
     if dlogits is None:
         dlogits = _empty((T, E), torch.float32, logits.device, stream)
     else:
-        _need(dlogits, torch.float32, "dlogits")
-        _shape(dlogits, (T, E), "dlogits")
-    check(lib().ap_route_backward(_p(logits), T, E, k, _p(idx) if dw is not None else None,
-                                  _p(w) if dw is not None else None, _p(dw), _p(slope), _p(dloss), group_tokens,
-                                  _p(mask), _p(dlogits), _p(status), _stream(stream)), "route_backward")
+        _need_shape(dlogits, torch.float32, (T, E), "dlogits")
+    check(lib().ap_route_backward(_p(logits), T, E, k, pi, pw, pdw, ps, pl, group_tokens, m, _p(dlogits), _p(status),
+                                  _stream(stream)), "route_backward")
     return dlogits
 
 
 _ROW_TYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
 
-def _need_rows(t: torch.Tensor, name: str):
-    """[n, H] BF16 or FP32 rows, each contiguous; the rows may lie apart."""
+def _rows(t: torch.Tensor, name: str):
+    """(n, H, distance of rows, type) of BF16 or FP32 rows [n, H], each contiguous; they may lie apart."""
+    kind = _ROW_TYPES.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _ROW_TYPES:
-        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{name} must be [rows, H] with contiguous rows that do not overlap")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, H]")
+    (n, H), (pitch, step) = t.shape, t.stride()
+    if pitch < H:
+        if n > 1:
+            raise ValueError(f"{name} must have rows that do not overlap")
+        pitch = H
+    if step != 1 and H > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return n, H, pitch, kind
 
 
-def _pitch(t: torch.Tensor) -> int:
-    return max(t.stride(0), t.shape[1])
-
-
-def _need_ids(ids: torch.Tensor) -> int:
-    if ids.dtype not in (torch.int32, torch.int64):
+def _ids(ids: torch.Tensor):
+    """(T, bytes of an id)"""
+    size = 8 if ids.dtype == torch.int64 else 4 if ids.dtype == torch.int32 else 0
+    if not size:
         raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
     _need(ids, ids.dtype, "ids")
     if ids.dim() != 1:
         raise ValueError("ids must be [T]")
-    return ids.shape[0]
+    return ids.shape[0], size
 
 
 def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, dtype: torch.dtype | None = None,
@@ -210,18 +217,19 @@ def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, dtype: tor
     table's) for a BF16 or FP32 table [V, H] and int32 or int64 ids [T].  Rows
     of table and out may lie apart.  An id outside [0, V) gives zeros and sets
     FLAG_BAD_INDEX in ``status``."""
-    _need_rows(table, "table")
-    T = _need_ids(ids)
-    V, H = table.shape
+    V, H, ld, kind = _rows(table, "table")
+    T, size = _ids(ids)
     if out is None:
         out = _empty((T, H), dtype if dtype is not None else table.dtype, table.device, stream)
-    _need_rows(out, "out")
-    _shape(out, (T, H), "out")
-    check(lib().ap_embed(_p(table), V, _pitch(table), _ROW_TYPES[table.dtype], _p(ids), ids.element_size(), T, H,
-                         scale, _p(out), _pitch(out), _ROW_TYPES[out.dtype], _p(status), _stream(stream)), "embed")
+    n, h, out_ld, out_kind = _rows(out, "out")
+    if n != T or h != H:
+        raise ValueError(f"out must be {[T, H]}, got {[n, h]}")
+    check(lib().ap_embed(_p(table), V, ld, kind, _p(ids), size, T, H, scale, _p(out), out_ld, out_kind, _p(status),
+                         _stream(stream)), "embed")
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def embed_scratch_bytes(T: int, V: int, H: int) -> int:
     n = ctypes.c_int64(0)
     check(lib().ap_embed_scratch_bytes(T, V, H, ctypes.byref(n)), "embed_scratch_bytes")
@@ -237,24 +245,26 @@ def embed_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: float =
     with ``accumulate``, added to ``dtable``.  Tokens whose id is
     ``padding_idx`` add nothing.  ``scratch``: a uint8 tensor of
     ``embed_scratch_bytes(T, V, H)`` bytes to reuse."""
-    _need_rows(dout, "dout")
-    T = _need_ids(ids)
-    if dout.shape[0] != T:
-        raise ValueError(f"dout has {dout.shape[0]} rows for {T} ids")
-    H = dout.shape[1]
+    n, H, ld, kind = _rows(dout, "dout")
+    T, size = _ids(ids)
+    if n != T:
+        raise ValueError(f"dout has {n} rows for {T} ids")
     if dtable is None:
         if accumulate:
             raise ValueError("accumulate needs dtable")
         dtable = _empty((V, H), dtype, dout.device, stream)
-    _need_rows(dtable, "dtable")
-    _shape(dtable, (V, H), "dtable")
+    v, h, g_ld, g_kind = _rows(dtable, "dtable")
+    if v != V or h != H:
+        raise ValueError(f"dtable must be {[V, H]}, got {[v, h]}")
     sb = embed_scratch_bytes(T, V, H)
-    if scratch is None or scratch.numel() < sb:
+    if scratch is None:
         scratch = _empty(sb, torch.uint8, dout.device, stream)
-    check(lib().ap_embed_backward(_p(dout), _pitch(dout), _ROW_TYPES[dout.dtype], _p(ids), ids.element_size(), T, H, V,
-                                  -1 if padding_idx is None else padding_idx, scale, int(accumulate), _p(dtable),
-                                  _pitch(dtable), _ROW_TYPES[dtable.dtype], _p(scratch), scratch.numel(), _p(status),
-                                  _stream(stream)), "embed_backward")
+    else:
+        _need(scratch, torch.uint8, "scratch")
+    check(lib().ap_embed_backward(_p(dout), ld, kind, _p(ids), size, T, H, V,
+                                  -1 if padding_idx is None else padding_idx, scale, 1 if accumulate else 0, _p(dtable),
+                                  g_ld, g_kind, _p(scratch), scratch.numel(), _p(status), _stream(stream)),
+          "embed_backward")
     return dtable
 
 

@@ -22,17 +22,23 @@
 namespace ap {
 namespace {
 
-constexpr int kBalThreads = 256;
+constexpr int kBalThreads = 256; // of the backward kernel
 constexpr int kBalWarps = kBalThreads / kWarp;
-constexpr int kBalBlocks = 608; // row-sum blocks of all groups together, at most (one group per block beyond)
+constexpr int kBalBlocks = 304;  // row-sum blocks of all groups together, at most (one group per block beyond)
+constexpr int kFinThreads = 1024;
+constexpr int kFinWarps = kFinThreads / kWarp;
+constexpr int kFinCols = 8; // experts of a block: 64 bytes of a row of sums and counts
+
+// Warps of a row-sum block: 16 while a lane's logits and sums fit 64 registers, else 8.
+constexpr int bal_warps(int E) { return E <= 256 ? 16 : 8; }
 
 struct BalancePlan {
     int64_t S, G, blocks; // tokens per group, groups, blocks per group
-    int64_t off_n, off_lp, off_p, off_c, bytes;
+    int64_t off_n, off_lp, off_p, bytes;
 };
 
-// The split and the layout of the work space: one row of E sums, E counts and
-// one token count per block, one loss term per 32 experts of a group, and the
+// The split and the layout of the work space: one row of E sums and counts and
+// one token count per block, one loss term per kFinCols experts of a group, and the
 // counter of finished blocks of the second kernel.
 BalancePlan balance_plan(int64_t T, int32_t E, int64_t group_tokens)
 {
@@ -41,7 +47,8 @@ BalancePlan balance_plan(int64_t T, int32_t E, int64_t group_tokens)
     p.G = (T + p.S - 1) / p.S;
     p.blocks = 1;
     if (p.G > 0) {
-        const int64_t most = (p.S + kBalWarps - 1) / kBalWarps;
+        const int64_t warps = bal_warps(E);
+        const int64_t most = (p.S + warps - 1) / warps;
         p.blocks = kBalBlocks / p.G;
         if (p.blocks > most) p.blocks = most;
         if (p.blocks < 1) p.blocks = 1;
@@ -50,160 +57,202 @@ BalancePlan balance_plan(int64_t T, int32_t E, int64_t group_tokens)
     const int64_t rows = p.G * p.blocks;
     p.off_n = 256;
     p.off_lp = p.off_n + up(rows * 4);
-    p.off_p = p.off_lp + up(p.G * ((E + 31) / 32) * 4);
-    p.off_c = p.off_p + up(rows * E * 4);
-    p.bytes = p.off_c + up(rows * E * 4);
+    p.off_p = p.off_lp + up(p.G * ((E + kFinCols - 1) / kFinCols) * 4);
+    p.bytes = p.off_p + up(rows * E * 8);
     return p;
 }
 
-template <int NV>
-__global__ void __launch_bounds__(kBalThreads)
+template <int VEC> struct Floats;
+template <> struct Floats<4> { using T = float4; };
+template <> struct Floats<1> { using T = float; };
+
+// exp(x) for x <= 0 as 2^(x log2 e): relative error (2.2 |x| + 4) 2^-24, where
+// expf takes twice the instructions for (|x| + 4) 2^-24.
+__device__ __forceinline__ float exp_neg(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+    return y;
+}
+
+// Lane l holds the vectors l, l + 32, ... of VEC experts each (N of them).
+template <int VEC, int N, int W>
+__global__ void __launch_bounds__(W *kWarp)
     k_route_balance(const float *__restrict__ logits, int64_t T, int E, int k, int64_t S, int blocks,
                     const uint8_t *__restrict__ mask, int32_t *__restrict__ idx, float *__restrict__ w,
-                    int32_t *__restrict__ part_n, float *__restrict__ part_p, int32_t *__restrict__ part_c,
-                    uint32_t *done)
+                    int32_t *__restrict__ part_n, float2 *__restrict__ part, uint32_t *done)
 {
     pdl_begin();
-    extern __shared__ float s_mem[];
-    float *s_sum = s_mem;                                            // [warps][E]
-    int *s_cnt = reinterpret_cast<int *>(s_mem + kBalWarps * E);     // [E]
+    using Vec = typename Floats<VEC>::T;
+    extern __shared__ __align__(16) float s_mem[];
+    float *s_sum = s_mem;                                // [W][E]
+    int *s_cnt = reinterpret_cast<int *>(s_mem + W * E); // [E]
+    __shared__ __align__(16) TopkSlots s_slots[W];
     __shared__ int s_n;
     const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
     if (blockIdx.x == 0 && threadIdx.x == 0) *done = 0;
     if (threadIdx.x == 0) s_n = 0;
-    for (int e = threadIdx.x; e < E; e += kBalThreads) s_cnt[e] = 0;
+    for (int e = threadIdx.x; e < E; e += W * kWarp) s_cnt[e] = 0;
     __syncthreads();
 
+    const int nvec = E / VEC;
     const int64_t g = blockIdx.x / blocks;
     const int b = (int)(blockIdx.x - g * blocks);
     const int64_t t_end = (g + 1) * S < T ? (g + 1) * S : T;
-    float acc[NV];
+    float acc[N][VEC];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) acc[i] = 0.f;
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) acc[i][c] = 0.f;
     int n = 0;
-    for (int64_t t = g * S + (int64_t)b * kBalWarps + wid; t < t_end; t += (int64_t)blocks * kBalWarps) {
-        const float *row = logits + t * E;
-        float v[NV];
-        uint32_t key[NV];
-        int ex[NV];
+    for (int64_t t = g * S + (int64_t)b * W + wid; t < t_end; t += (int64_t)blocks * W) {
+        const Vec *row = reinterpret_cast<const Vec *>(logits + t * E);
+        float v[N][VEC];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int ei = lane + kWarp * i;
-            const bool ok = ei < E;
-            v[i] = ok ? __ldcs(row + ei) : -INFINITY;
-            key[i] = ok ? order_key(v[i]) : 0u;
-            ex[i] = ok ? ei : kNoExpert;
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) v[i][c] = -INFINITY;
+            if (lane + kWarp * i < nvec) {
+                const Vec x = __ldcs(row + lane + kWarp * i);
+                memcpy(v[i], &x, sizeof(Vec));
+            }
         }
+        const bool counts = !mask || mask[t];
         int e;
         float wt, top;
-        select_token<NV>(key, ex, k, lane, &e, &wt, &top);
+        select_token_slots<VEC, N>(v, E, k, lane, s_slots[wid], &e, &wt, &top);
         const bool some = top != -INFINITY; // warp-uniform
         if (lane < k) {
             idx[t * k + lane] = e;
             w[t * k + lane] = some ? wt : 0.f;
         }
-        if (some && (!mask || mask[t])) {
-            float z[NV], sum = 0.f;
+        if (some && counts) {
+            float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                z[i] = expf(v[i] - top); // -infinity (no such expert, or one masked out) gives 0
-                sum += z[i];
-            }
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    v[i][c] = exp_neg(v[i][c] - top); // -infinity (no such expert, or one masked out) gives 0
+                    sum += v[i][c];
+                }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            const float inv = __fdiv_rn(1.0f, sum);
+            const float inv = __frcp_rn(sum);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) acc[i] += z[i] * inv;
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) acc[i][c] += v[i][c] * inv;
             if (lane < k) atomicAdd(&s_cnt[e], 1);
             ++n;
         }
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int ei = lane + kWarp * i;
-        if (ei < E) s_sum[wid * E + ei] = acc[i];
-    }
+    for (int i = 0; i < N; ++i)
+        if (lane + kWarp * i < nvec) {
+            Vec x;
+            memcpy(&x, acc[i], sizeof(Vec));
+            reinterpret_cast<Vec *>(s_sum + wid * E)[lane + kWarp * i] = x;
+        }
     if (lane == 0 && n) atomicAdd(&s_n, n);
     __syncthreads();
     const int64_t at = (int64_t)blockIdx.x * E;
-    for (int e = threadIdx.x; e < E; e += kBalThreads) {
+    for (int e = threadIdx.x; e < E; e += W * kWarp) {
         float sum = 0.f;
 #pragma unroll
-        for (int q = 0; q < kBalWarps; ++q) sum += s_sum[q * E + e];
-        part_p[at + e] = sum;
-        part_c[at + e] = s_cnt[e];
+        for (int q = 0; q < W; ++q) sum += s_sum[q * E + e];
+        part[at + e] = make_float2(sum, __int_as_float(s_cnt[e]));
     }
     if (threadIdx.x == 0) part_n[blockIdx.x] = s_n;
 }
 
-// One block per group and 32 experts: warp r adds the rows r, r + 8, ... of its
-// group's blocks, the eight warps' sums are added in warp order, and the last
-// block to finish adds the loss terms up in block order.
-__global__ void __launch_bounds__(kBalThreads)
+// One block per group and kFinCols experts.  Thread (r, c) adds rows r, r + 128,
+// ... of its group's blocks in column c; the 128 sums of a column are added in
+// a fixed tree; the last block to finish adds the loss terms up in block order.
+__global__ void __launch_bounds__(kFinThreads)
     k_balance_finish(int E, int k, int64_t G, int blocks, float coef, const int32_t *__restrict__ part_n,
-                     const float *__restrict__ part_p, const int32_t *__restrict__ part_c, float *loss_part,
-                     int32_t *__restrict__ counts, float *__restrict__ prob, float *__restrict__ slope,
-                     float *__restrict__ loss, uint32_t *done)
+                     const float2 *__restrict__ part, float *loss_part, int32_t *__restrict__ counts,
+                     float *__restrict__ prob, float *__restrict__ slope, float *__restrict__ loss, uint32_t *done)
 {
     pdl_begin();
-    __shared__ float s_p[kBalWarps][kWarp];
-    __shared__ int s_c[kBalWarps][kWarp];
+    constexpr int kRows = kFinThreads / kFinCols;
+    __shared__ float2 s_part[kFinCols][kFinWarps];
+    __shared__ int s_n;
+    __shared__ float s_term[kFinCols], s_tot[kFinWarps];
     __shared__ bool s_last;
     const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
-    const int pieces = (E + kWarp - 1) / kWarp;
+    const int pieces = (E + kFinCols - 1) / kFinCols;
     const int64_t g = blockIdx.x / pieces;
-    const int e = (int)(blockIdx.x - g * pieces) * kWarp + lane;
+    const int col0 = (int)(blockIdx.x - g * pieces) * kFinCols;
+    const int c = lane % kFinCols, e = col0 + c, r0 = threadIdx.x / kFinCols;
     float sum = 0.f;
     int cnt = 0;
-    if (e < E)
-        for (int b = wid; b < blocks; b += kBalWarps) {
-            sum += part_p[(g * blocks + b) * E + e];
-            cnt += part_c[(g * blocks + b) * E + e];
-        }
-    s_p[wid][lane] = sum;
-    s_c[wid][lane] = cnt;
-    __syncthreads();
-    if (wid == 0) {
+    if (wid == kFinWarps - 1) {
         int n = 0;
+#pragma unroll 10
         for (int b = lane; b < blocks; b += kWarp) n += part_n[g * blocks + b];
         n = __reduce_add_sync(0xffffffffu, n);
-        sum = 0.f;
-        cnt = 0;
+        if (lane == 0) s_n = n;
+    }
+    constexpr int U = 3; // all of 304 blocks in flight
+    for (int b0 = r0; b0 < blocks; b0 += U * kRows) {
+        float2 r[U];
 #pragma unroll
-        for (int q = 0; q < kBalWarps; ++q) {
-            sum += s_p[q][lane];
-            cnt += s_c[q][lane];
-        }
-        const float nf = (float)(n > 0 ? n : 1);
-        const float sl = coef * (float)E / ((float)G * (float)k) * (float)cnt / (nf * nf);
-        float term = 0.f;
-        if (e < E) {
-            counts[g * E + e] = cnt;
-            prob[g * E + e] = __fdiv_rn(sum, nf);
-            slope[g * E + e] = sl;
-            term = sl * sum;
+        for (int u = 0; u < U; ++u) {
+            const int b = b0 + u * kRows;
+            r[u] = e < E && b < blocks ? part[(g * blocks + b) * E + e] : make_float2(0.f, 0.f);
         }
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xffffffffu, term, off);
+        for (int u = 0; u < U; ++u) {
+            sum += r[u].x;
+            cnt += __float_as_int(r[u].y);
+        }
+    }
+#pragma unroll
+    for (int off = kFinCols; off < kWarp; off <<= 1) { // the lanes of the same column
+        sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        cnt += __shfl_xor_sync(0xffffffffu, cnt, off);
+    }
+    if (lane < kFinCols) s_part[c][wid] = make_float2(sum, __int_as_float(cnt));
+    __syncthreads();
+    if (wid < kFinCols) { // warp q finishes column q
+        const float2 x = s_part[wid][lane];
+        sum = x.x;
+        cnt = __reduce_add_sync(0xffffffffu, __float_as_int(x.y));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         if (lane == 0) {
-            loss_part[blockIdx.x] = term;
-            __threadfence();
-            s_last = atomicAdd(done, 1u) == gridDim.x - 1;
+            const float nf = (float)(s_n > 0 ? s_n : 1);
+            const float sl = coef * (float)E / ((float)G * (float)k) * (float)cnt / (nf * nf);
+            if (col0 + wid < E) {
+                counts[g * E + col0 + wid] = cnt;
+                prob[g * E + col0 + wid] = __fdiv_rn(sum, nf);
+                slope[g * E + col0 + wid] = sl;
+            }
+            s_term[wid] = col0 + wid < E ? sl * sum : 0.f;
         }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float term = 0.f;
+#pragma unroll
+        for (int q = 0; q < kFinCols; ++q) term += s_term[q];
+        loss_part[blockIdx.x] = term;
+        __threadfence();
+        s_last = atomicAdd(done, 1u) == gridDim.x - 1;
     }
     __syncthreads();
     if (!s_last) return;
     __threadfence();
     float total = 0.f;
-    for (int64_t i = threadIdx.x; i < gridDim.x; i += kBalThreads) total += __ldcg(loss_part + i);
+    for (int64_t i = threadIdx.x; i < gridDim.x; i += kFinThreads) total += __ldcg(loss_part + i);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    if (lane == 0) s_p[0][wid] = total;
+    if (lane == 0) s_tot[wid] = total;
     __syncthreads();
     if (threadIdx.x == 0) {
         total = 0.f;
 #pragma unroll
-        for (int q = 0; q < kBalWarps; ++q) total += s_p[0][q];
+        for (int q = 0; q < kFinWarps; ++q) total += s_tot[q];
         *loss = total;
     }
 }
@@ -213,10 +262,6 @@ __global__ void k_zero_word(float *p)
     pdl_begin();
     *p = 0.f;
 }
-
-template <int VEC> struct Floats;
-template <> struct Floats<4> { using T = float4; };
-template <> struct Floats<1> { using T = float; };
 
 // A warp per token; lane l holds the vectors l, l + 32, ... of VEC experts
 // each (N of them).  The selected terms are added through a row of shared
@@ -389,7 +434,7 @@ extern "C" ap_status ap_route_balance(const float *logits, int64_t T, int32_t E,
     if (scratch_bytes < p.bytes)
         return fail(AP_EINVAL, "route_balance: scratch of %lld bytes, %lld needed", (long long)scratch_bytes,
                     (long long)p.bytes);
-    const int64_t pieces = (E + kWarp - 1) / kWarp;
+    const int64_t pieces = (E + kFinCols - 1) / kFinCols;
     if (p.G * p.blocks > INT32_MAX || p.G * pieces > INT32_MAX)
         return fail(AP_EINVAL, "route_balance: %lld groups of %d experts are more than one launch takes",
                     (long long)p.G, E);
@@ -397,29 +442,39 @@ extern "C" ap_status ap_route_balance(const float *logits, int64_t T, int32_t E,
     uint32_t *done = reinterpret_cast<uint32_t *>(sc);
     int32_t *part_n = reinterpret_cast<int32_t *>(sc + p.off_n);
     float *loss_part = reinterpret_cast<float *>(sc + p.off_lp);
-    float *part_p = reinterpret_cast<float *>(sc + p.off_p);
-    int32_t *part_c = reinterpret_cast<int32_t *>(sc + p.off_c);
+    float2 *part = reinterpret_cast<float2 *>(sc + p.off_p);
     const int grid = (int)(p.G * p.blocks);
-    const size_t smem = (size_t)(kBalWarps + 1) * E * 4;
+    const int warps = bal_warps(E);
+    const size_t smem = (size_t)(warps + 1) * E * 4;
     auto go = [&](auto *kernel) {
-        launch(kernel, grid, kBalThreads, smem, st, logits, T, E, k, p.S, (int)p.blocks, mask, idx, w, part_n, part_p,
-               part_c, done);
+        launch(kernel, grid, warps * kWarp, smem, st, logits, T, E, k, p.S, (int)p.blocks, mask, idx, w, part_n, part,
+               done);
     };
-    if (E <= 32)
-        go(k_route_balance<1>);
+    // vectors where every lane gets one (fewer lanes with experts leave no bound from the lanes' maxima)
+    if (E >= 128 && E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0) {
+        if (E <= 128)
+            go(k_route_balance<4, 1, 16>);
+        else if (E <= 256)
+            go(k_route_balance<4, 2, 16>);
+        else if (E <= 512)
+            go(k_route_balance<4, 4, 8>);
+        else
+            go(k_route_balance<4, 8, 8>);
+    } else if (E <= 32)
+        go(k_route_balance<1, 1, 16>);
     else if (E <= 64)
-        go(k_route_balance<2>);
+        go(k_route_balance<1, 2, 16>);
     else if (E <= 128)
-        go(k_route_balance<4>);
+        go(k_route_balance<1, 4, 16>);
     else if (E <= 256)
-        go(k_route_balance<8>);
+        go(k_route_balance<1, 8, 16>);
     else if (E <= 512)
-        go(k_route_balance<16>);
+        go(k_route_balance<1, 16, 8>);
     else
-        go(k_route_balance<32>);
+        go(k_route_balance<1, 32, 8>);
     AP_CHECK_LAUNCH("route_balance launch");
-    launch(k_balance_finish, (int)(p.G * pieces), kBalThreads, 0, st, E, k, p.G, (int)p.blocks, coef, part_n, part_p,
-           part_c, loss_part, counts, prob, slope, loss, done);
+    launch(k_balance_finish, (int)(p.G * pieces), kFinThreads, 0, st, E, k, p.G, (int)p.blocks, coef, part_n, part,
+           loss_part, counts, prob, slope, loss, done);
     AP_CHECK_LAUNCH("route_balance finish launch");
     return AP_OK;
 }

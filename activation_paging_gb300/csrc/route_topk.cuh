@@ -11,6 +11,7 @@
 #pragma once
 
 #include <float.h>
+#include <math.h>
 
 #include "ap_common.cuh"
 
@@ -90,6 +91,109 @@ __device__ __forceinline__ void select_token(uint32_t (&key)[NV], int (&ex)[NV],
     *e = my_e;
     *wt = __fdiv_rn(z, s);
     *top = mv;
+}
+
+// The largest of the lanes' values (NaN aside).
+__device__ __forceinline__ float reduce_max(float v)
+{
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+
+// Shared memory of one warp for select_token_slots.
+struct TopkSlots {
+    float val[kWarp + 4];
+    int id[kWarp];
+    float sel_val[kWarp];
+    int sel_id[kWarp];
+};
+
+// The same selection in about half the instructions for rows of 128 and more
+// experts, with a little shared memory.  The k-th largest of the lanes' maxima
+// bounds the k-th largest logit from below, so only logits that reach it can
+// be chosen: little more than k of them as a rule.  They are moved to one lane
+// each, ranked by counting, and put in rank order.  Where more than 32 reach
+// it (ties, or many large logits in one lane) or fewer than k do (NaN,
+// -infinity), the rounds above run instead.  Results are select_token's, bit
+// for bit.  v[i][c]: the logit of expert (lane + 32 i) * VEC + c, -infinity
+// beyond E.
+template <int VEC, int N>
+__device__ __forceinline__ void select_token_slots(const float (&v)[N][VEC], int E, int k, int lane, TopkSlots &s,
+                                                   int *e, float *wt, float *top)
+{
+    float cur = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) cur = fmaxf(cur, v[i][c]);
+    const float first = reduce_max(cur);
+    float least = first;
+    for (int j = 1; j < k; ++j) {
+        cur = cur == least ? -INFINITY : cur;
+        least = reduce_max(cur);
+    }
+    uint32_t has[N][VEC];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            has[i][c] = __ballot_sync(0xffffffffu, v[i][c] >= least);
+            n += __popc(has[i][c]);
+        }
+    if (least == -INFINITY || n < k || n > kWarp) { // warp-uniform
+        uint32_t key[N * VEC];
+        int ex[N * VEC];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                const int id = (lane + kWarp * i) * VEC + c;
+                key[i * VEC + c] = id < E ? order_key(v[i][c]) : 0u;
+                ex[i * VEC + c] = id < E ? id : kNoExpert;
+            }
+        select_token<N * VEC>(key, ex, k, lane, e, wt, top);
+        return;
+    }
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            if (v[i][c] >= least) {
+                const int to = at + __popc(has[i][c] & lanemask_lt());
+                s.val[to] = v[i][c];
+                s.id[to] = (lane + kWarp * i) * VEC + c;
+            }
+            at += __popc(has[i][c]);
+        }
+    if (lane < 4) s.val[n + lane] = -INFINITY;
+    __syncwarp();
+    const float mine = s.val[lane];
+    const int my_id = s.id[lane];
+    int rank = -1; // itself counts once
+    for (int c = 0; c < n; c += 4) {
+        const float4 o = *reinterpret_cast<const float4 *>(&s.val[c]);
+        rank += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
+    }
+    if (__reduce_add_sync(0xffffffffu, lane < n ? (unsigned)rank : 0u) != (unsigned)(n * (n - 1) / 2)) { // ties
+        rank = 0;
+        for (int c = 0; c < n; ++c) rank += s.val[c] > mine || (s.val[c] == mine && s.id[c] < my_id);
+    }
+    if (lane < n && rank < k) {
+        s.sel_val[rank] = mine;
+        s.sel_id[rank] = my_id;
+    }
+    __syncwarp();
+    const float z = (lane < k) ? expf(s.sel_val[lane] - first) : 0.f;
+    float sum = z;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    *e = s.sel_id[lane < k ? lane : 0];
+    *wt = __fdiv_rn(z, sum);
+    *top = first;
+    __syncwarp(); // the slots are free for the next token
 }
 
 // Loads one token's row and selects from it.
