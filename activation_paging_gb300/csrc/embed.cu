@@ -444,8 +444,9 @@ __global__ void __launch_bounds__(kSortThreads)
 // ---- sums of the runs ------------------------------------------------------------
 constexpr int kSumThreads = 256;
 constexpr int kSumWarps = kSumThreads / kWarp;
-constexpr int kSumRowsMax = 16;
-constexpr int64_t kPrefetchBytes = 48 << 20;
+constexpr int kSumRowsMax = 32;
+constexpr int64_t kPrefetchBytes = 64 << 20;
+constexpr int64_t kWantItems = 256;
 
 // Where a lane's VE * NG elements of a slice lie: NG groups of VE, 32 lanes apart.
 template <int VE, int NG> struct Slice {
@@ -816,8 +817,10 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int32_t H)
     p.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
     p.bits = (bits + p.passes - 1) / p.passes;
     p.tiles = T > kClusterMax / 2 ? (T + kSortTile - 1) / kSortTile : 0; // (half: clusters of 8)
-    // few tokens: short tiles, so that more blocks share them (at 777 x 1001 and 8192 x 2048 each the fastest)
-    p.rows = T >= 4096 ? kSumRowsMax : T >= 1024 ? 8 : 4;
+    // the longest tiles that still give a block to nearly every SM twice (pieces of 256 columns)
+    const int64_t pieces = ((int64_t)H + 255) / 256;
+    p.rows = kSumRowsMax;
+    while (p.rows > 4 && T * pieces < kWantItems * p.rows * kSumWarps) p.rows /= 2;
     p.sum_tiles = (T + p.rows * kSumWarps - 1) / (p.rows * kSumWarps);
     p.part_ld = ((int64_t)H + 7) / 8 * 8;
     auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
