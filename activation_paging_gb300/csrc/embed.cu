@@ -546,6 +546,7 @@ __device__ __forceinline__ void prefetch_inputs(const TD *dout, int64_t dout_ld,
 // How the aligned form of the sums stages a row: 512 bytes of dout and the same
 // columns of dtable, copied to shared memory kStages rows ahead.
 constexpr int kStages = 8;
+constexpr int kBatch = 4; // rows taken from the ring at a time
 constexpr int kDoutBytes = kWarp * 16;
 template <typename TD, typename TG, bool ADD>
 constexpr int kOldBytes = ADD ? kDoutBytes / (int)sizeof(TD) * (int)sizeof(TG) : 0;
@@ -572,11 +573,10 @@ template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
 __global__ void __launch_bounds__(kSumThreads, 2)
     k_embed_sum(const TD *__restrict__ dout, int64_t dout_ld, const uint2 *__restrict__ sorted, int64_t T, int64_t V,
                 int H, float scale, int rows, TG *__restrict__ dtable, int64_t ld, float *__restrict__ partial,
-                int64_t part_ld, const uint32_t *__restrict__ seen, int fill_rows, const void *__restrict__ ids,
-                bool wide, int64_t pad)
+                int64_t part_ld, const void *__restrict__ ids, bool wide, int64_t pad)
 {
     prefetch_inputs<TD, TG, ADD>(dout, dout_ld, ids, wide, T, V, pad, H, dtable, ld);
-    pdl_begin();
+    pdl_begin_after(); // the join's zeros need the sort complete
     constexpr uint32_t kHead = 1, kThrough = 2, kTail = 4;
     constexpr int kCols = kWarp * VE * NG;
     constexpr int kOld = kOldBytes<TD, TG, ADD>;
@@ -599,6 +599,8 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         int64_t tile;
         int n, live, col0, cols;
         bool began; // the first run began before these rows
+        const TD *src; // the lane's token's columns of dout
+        TG *dst;       // and of dtable
     };
     auto rows_of = [&](int64_t it) {
         Rows x;
@@ -616,17 +618,28 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         x.ends = __ballot_sync(0xffffffffu, x.my.x != none && next != x.my.x);
         x.began = x.live > 0 && x.before == __shfl_sync(0xffffffffu, x.my.x, 0);
         x.direct = x.ends & ~(x.began ? (x.ends & (0u - x.ends)) : 0u);
+        x.src = dout + (int64_t)x.my.y * dout_ld + x.col0;
+        x.dst = dtable + (int64_t)x.my.x * ld + x.col0;
         return x;
     };
-    // row r of x into its stage of the ring (one group per row, empty past the end)
-    auto fetch = [&](const Rows &x, int r) {
-        if (r < x.live) {
-            const uint32_t to = smem_addr(ring + (r % kStages) * kStage) + lane * 16;
-            const uint32_t tok = __shfl_sync(0xffffffffu, x.my.y, r), key = __shfl_sync(0xffffffffu, x.my.x, r);
-            if (lane * 16 < x.cols * (int)sizeof(TD))
-                copy_async16(to, reinterpret_cast<const uint8_t *>(dout + (int64_t)tok * dout_ld + x.col0) + lane * 16);
+    // the column slice of row r, of dout and of dtable
+    auto src_of = [&](const Rows &x, int r) {
+        return reinterpret_cast<const TD *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x.src), r));
+    };
+    auto dst_of = [&](const Rows &x, int r) {
+        return reinterpret_cast<TG *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x.dst), r));
+    };
+    // kBatch rows of x from r0 on into their stages of the ring: one group, empty past the end
+    auto fetch = [&](const Rows &x, int r0) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int r = r0 + u;
+            if (r >= x.live) break;
+            const uint32_t to = smem_addr(ring) + (r0 % kStages + u) * kStage + lane * 16;
+            const uint8_t *from = reinterpret_cast<const uint8_t *>(src_of(x, r));
+            if (lane * 16 < x.cols * (int)sizeof(TD)) copy_async16(to, from + lane * 16);
             if (ADD && (x.direct >> r & 1)) {
-                const uint8_t *from = reinterpret_cast<const uint8_t *>(dtable + (int64_t)key * ld + x.col0);
+                from = reinterpret_cast<const uint8_t *>(dst_of(x, r));
 #pragma unroll
                 for (int b = 0; b < kOld; b += kWarp * 16)
                     if (b + lane * 16 < x.cols * (int)sizeof(TG)) copy_async16(to + kDoutBytes + b, from + b + lane * 16);
@@ -638,7 +651,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
     if (blockIdx.x < sums) {
         ahead = rows_of(blockIdx.x);
         if (RING)
-            for (int r = 0; r < kStages; ++r) fetch(ahead, r);
+            for (int r = 0; r < kStages; r += kBatch) fetch(ahead, r);
     }
     for (int64_t it = blockIdx.x; it < sums; it += gridDim.x) {
         const Rows cur = ahead;
@@ -647,6 +660,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         const uint32_t ends = cur.ends, direct = cur.direct;
         const bool began = cur.began;
         const Slice<VE, NG> sl{cur.col0 / VE + lane, nstep};
+        const Slice<VE, NG> here{lane, cur.cols / VE}; // the same from the slice's first column
         const bool more = it + gridDim.x < sums;
         if (more) ahead = rows_of(it + gridDim.x);
         float acc[NG][VE];
@@ -655,33 +669,39 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         auto take = [&](int r, const Pack<TD, VE>(&v)[NG], const Pack<TG, VE>(&old)[NG]) {
             add_row(acc, v);
             if (!(ends >> r & 1)) return;
-            if (direct >> r & 1) {
-                const uint32_t key = __shfl_sync(0xffffffffu, cur.my.x, r);
-                finish_row(dtable + (int64_t)key * ld, sl, acc, old, scale, ADD);
-            } else {
+            if (direct >> r & 1)
+                finish_row(dst_of(cur, r), here, acc, old, scale, ADD);
+            else
                 store_part(s_part(w, 0), mine, acc);
-            }
             zero(acc);
         };
         if constexpr (RING) {
-            for (int r = 0; r < live; ++r) {
-                copy_wait<kStages - 1>();
+            for (int r0 = 0; r0 < live; r0 += kBatch) {
+                copy_wait<kStages / kBatch - 1>();
                 __syncwarp();
-                const uint8_t *at = ring + (r % kStages) * kStage;
-                Pack<TD, VE> v[NG];
-                Pack<TG, VE> old[NG];
+                const uint8_t *at = ring + r0 % kStages * kStage;
+                Pack<TD, VE> v[kBatch][NG];
+                Pack<TG, VE> old[kBatch][NG];
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    v[g] = reinterpret_cast<const Pack<TD, VE> *>(at)[mine.at(g)];
-                    if (ADD) old[g] = reinterpret_cast<const Pack<TG, VE> *>(at + kDoutBytes)[mine.at(g)];
+                for (int u = 0; u < kBatch; ++u) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        v[u][g] = reinterpret_cast<const Pack<TD, VE> *>(at + u * kStage)[mine.at(g)];
+                    if (ADD && (direct >> r0 >> u & 1)) {
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+                            old[u][g] = reinterpret_cast<const Pack<TG, VE> *>(at + u * kStage + kDoutBytes)[mine.at(g)];
+                    }
                 }
                 __syncwarp();
-                fetch(cur, r + kStages);
-                take(r, v, old);
+                fetch(cur, r0 + kStages);
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    if (r0 + u < live) take(r0 + u, v[u], old[u]);
             }
             // the rows past `live` left empty groups: the next item's first rows follow them
             if (more)
-                for (int r = 0; r < kStages; ++r) fetch(ahead, r);
+                for (int r = 0; r < kStages; r += kBatch) fetch(ahead, r);
         } else {
             constexpr int U = 4;
             for (int r0 = 0; r0 < live; r0 += U) {
@@ -689,14 +709,13 @@ __global__ void __launch_bounds__(kSumThreads, 2)
                 Pack<TG, VE> old[U][NG];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const uint32_t tok = __shfl_sync(0xffffffffu, cur.my.y, (r0 + u) & 31);
-                    load_row(v[u], dout + (int64_t)tok * dout_ld, sl, r0 + u < live);
+                    load_row(v[u], src_of(cur, (r0 + u) & 31), here, r0 + u < live);
                 }
                 if (ADD) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        const uint32_t key = __shfl_sync(0xffffffffu, cur.my.x, (r0 + u) & 31);
-                        load_row(old[u], dtable + (int64_t)key * ld, sl, r0 + u < live && (direct >> (r0 + u) & 1));
+                        load_row(old[u], dst_of(cur, (r0 + u) & 31), here,
+                                 r0 + u < live && (direct >> (r0 + u) & 1));
                     }
                 }
 #pragma unroll
@@ -724,11 +743,11 @@ __global__ void __launch_bounds__(kSumThreads, 2)
             return false;
         };
         if (flags & kTail) {
-            const uint32_t key = __shfl_sync(0xffffffffu, cur.my.x, live - 1);
+            TG *row = dst_of(cur, live - 1);
+            Pack<TG, VE> old[NG];
+            if (ADD) load_row(old, row, here); // on its way while the parts are added
             if (join_from(w + 1)) {
-                Pack<TG, VE> old[NG];
-                if (ADD) load_row(old, dtable + (int64_t)key * ld, sl);
-                finish_row(dtable + (int64_t)key * ld, sl, acc, old, scale, ADD);
+                finish_row(row, here, acc, old, scale, ADD);
             } else {
                 store_part(partial + (2 * tile + 1) * part_ld, sl, acc);
             }
@@ -740,65 +759,87 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         }
         __syncthreads();
     }
-    if (ADD) return;
-    // rows of ids that do not occur: zeros
+}
+
+// Zeros the rows of items [first, last) that no id names; an item is `rows`
+// rows (a power of two, at most 32), taken by one warp.
+template <typename TG, int VE>
+__device__ __forceinline__ void fill_rows(int64_t first, int64_t last, int rows, int64_t V, int nstep,
+                                          TG *__restrict__ dtable, int64_t ld, const uint32_t *__restrict__ seen)
+{
     Pack<TG, VE> z;
 #pragma unroll
     for (int i = 0; i < VE; ++i) z.v[i] = from_f<TG>(0.f);
-    for (int64_t r0 = (int64_t)blockIdx.x * fill_rows; r0 < V; r0 += (int64_t)gridDim.x * fill_rows) {
-        const int64_t r1 = r0 + fill_rows < V ? r0 + fill_rows : V;
-        for (int64_t r = r0 + w; r < r1; r += kSumWarps) {
-            if (seen && (__ldg(seen + (r >> 5)) >> (r & 31) & 1)) continue;
-            Pack<TG, VE> *row = reinterpret_cast<Pack<TG, VE> *>(dtable + r * ld);
-            for (int s = lane; s < nstep; s += kWarp) row[s] = z;
+    const int64_t warps = (int64_t)gridDim.x * kSumWarps;
+    int64_t it = first + blockIdx.x + (int64_t)gridDim.x * (threadIdx.x / kWarp);
+    uint32_t word = seen && it < last ? __ldcg(seen + (it * rows >> 5)) : 0u;
+    for (; it < last; it += warps) {
+        const int64_t r0 = it * rows;
+        const uint32_t bits = word >> (r0 & 31);
+        if (seen && it + warps < last) word = __ldcg(seen + ((it + warps) * rows >> 5));
+        const int n = V - r0 < rows ? (int)(V - r0) : rows;
+        for (int r = 0; r < n; ++r) {
+            if (bits >> r & 1) continue;
+            Pack<TG, VE> *row = reinterpret_cast<Pack<TG, VE> *>(dtable + (r0 + r) * ld);
+#pragma unroll 4
+            for (int s = (int)lane_id(); s < nstep; s += kWarp) row[s] = z;
         }
     }
 }
 
 // Runs that span tiles: the tail of the tile in which one begins and the heads
 // of the tiles it goes on through, added in tile order.  A warp takes a tile
-// and a slice; most find nothing to do.
+// and a slice; most find nothing to do.  A gradient that is written whole gets
+// its zeros here, by warps that need not wait for the sums (`early`: part of
+// them before the sums are complete; the sort is complete then, since the sums
+// kernel lets this one start only after its own wait).
 template <typename TG, int VE, int NG, bool ADD>
 __global__ void __launch_bounds__(kSumThreads)
     k_embed_join(const uint2 *__restrict__ sorted, int64_t T, int64_t V, int H, float scale, int tile_rows,
-                 TG *__restrict__ dtable, int64_t ld, const float *__restrict__ partial, int64_t part_ld)
+                 TG *__restrict__ dtable, int64_t ld, const float *__restrict__ partial, int64_t part_ld,
+                 const uint32_t *__restrict__ seen, int rows_per_fill, bool early)
 {
-    pdl_begin();
     constexpr int U = 8;
     const int nstep = H / VE;
+    const int64_t fills = ADD ? 0 : (V + rows_per_fill - 1) / rows_per_fill;
+    const int64_t ahead = early ? fills / 8 : 0;
+    if (!ADD) fill_rows<TG, VE>(0, ahead, rows_per_fill, V, nstep, dtable, ld, seen);
+    pdl_begin();
     const int slices = (nstep + kWarp * NG - 1) / (kWarp * NG);
     const int64_t tiles = (T + tile_rows - 1) / tile_rows;
-    const int64_t items = (tiles - 1) * slices;
+    const int64_t items = (tiles - 1) * slices; // (negative without tokens)
     const int64_t warps = (int64_t)gridDim.x * kSumWarps;
-    for (int64_t it = (int64_t)blockIdx.x * kSumWarps + threadIdx.x / kWarp; it < items; it += warps) {
+    for (int64_t it = blockIdx.x + (int64_t)gridDim.x * (threadIdx.x / kWarp); it < items; it += warps) {
         const int64_t c = it / slices;
         const int64_t i0 = c * tile_rows, i1 = i0 + tile_rows;
         const uint32_t key = sorted[i1 - 1].x;
-        if (key == (uint32_t)V || sorted[i1].x != key) continue;
-        if (i0 > 0 && sorted[i0 - 1].x == key) continue; // an earlier tile's
+        const uint32_t before = i0 > 0 ? sorted[i0 - 1].x : (uint32_t)V;
+        bool on[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) on[u] = c + 1 + u < tiles && sorted[i1 + u * tile_rows].x == key;
+        if (key == (uint32_t)V || !on[0] || before == key) continue; // none, or an earlier tile's
         const Slice<VE, NG> sl{(int)(it - c * slices) * kWarp * NG + (int)lane_id(), nstep};
         Pack<TG, VE> old[NG];
+        Pack<float, VE> tail[NG], p[U][NG];
         if (ADD) load_row(old, dtable + (int64_t)key * ld, sl);
+        load_row(tail, partial + (2 * c + 1) * part_ld, sl);
         float acc[NG][VE];
         zero(acc);
-        Pack<float, VE> p[U][NG];
-        load_row(p[0], partial + (2 * c + 1) * part_ld, sl);
-        add_row(acc, p[0]);
-        for (int64_t q0 = c + 1; q0 < tiles; q0 += U) {
-            bool on[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                on[u] = q0 + u < tiles && sorted[(q0 + u) * tile_rows].x == key;
-            }
+        for (int64_t q0 = c + 1;;) {
 #pragma unroll
             for (int u = 0; u < U; ++u) load_row(p[u], partial + 2 * (q0 + u) * part_ld, sl, on[u]);
+            if (q0 == c + 1) add_row(acc, tail);
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (on[u]) add_row(acc, p[u]);
             if (!on[U - 1]) break;
+            q0 += U;
+#pragma unroll
+            for (int u = 0; u < U; ++u) on[u] = q0 + u < tiles && sorted[(q0 + u) * tile_rows].x == key;
         }
         finish_row(dtable + (int64_t)key * ld, sl, acc, old, scale, ADD);
     }
+    if (!ADD) fill_rows<TG, VE>(ahead, fills, rows_per_fill, V, nstep, dtable, ld, seen);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -975,19 +1016,21 @@ ap_status embed_sums(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
                                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (attr != cudaSuccess) return cuda_fail(attr, "embed_backward sum");
     static const int resident = resident_grid((const void *)kernel, kSumThreads, smem);
-    // zeros are written 128 KB at a time or so
-    const int64_t gb = (int64_t)a.H * sizeof(TG);
-    const int fill_rows = (int)(gb >= (128 << 10) / kSumWarps ? kSumWarps : (128 << 10) / gb);
-    int64_t want = p.sum_tiles * slices;
-    if (!ADD && (a.V + fill_rows - 1) / fill_rows > want) want = (a.V + fill_rows - 1) / fill_rows;
-    launch(kernel, (int)(want < resident ? want : resident), kSumThreads, smem, st,
-           static_cast<const TD *>(a.dout), a.dout_ld, a.sorted, a.T, a.V, a.H, a.scale, p.rows, dtable, a.ld,
-           a.partial, p.part_ld, a.seen, fill_rows, a.ids, a.wide, a.pad);
-    AP_CHECK_LAUNCH("embed_backward sum launch");
-    if (p.sum_tiles > 1) {
+    const int64_t items = p.sum_tiles * slices;
+    if (items > 0) {
+        launch(kernel, (int)(items < resident ? items : resident), kSumThreads, smem, st,
+               static_cast<const TD *>(a.dout), a.dout_ld, a.sorted, a.T, a.V, a.H, a.scale, p.rows, dtable, a.ld,
+               a.partial, p.part_ld, a.ids, a.wide, a.pad);
+        AP_CHECK_LAUNCH("embed_backward sum launch");
+    }
+    if (!ADD || p.sum_tiles > 1) {
         static const int resident_j = resident_grid((const void *)k_embed_join<TG, VE, NG, ADD>, kSumThreads);
-        launch(k_embed_join<TG, VE, NG, ADD>, grid_for((p.sum_tiles - 1) * slices, resident_j), kSumThreads, 0, st,
-               a.sorted, a.T, a.V, a.H, a.scale, p.rows * kSumWarps, dtable, a.ld, a.partial, p.part_ld);
+        int rows = 32; // zeros: about 16 KB a warp at a time
+        while (rows > 1 && rows * (int64_t)a.H * (int64_t)sizeof(TG) > (16 << 10)) rows /= 2;
+        int64_t warps = (p.sum_tiles - 1) * slices;
+        if (!ADD && (a.V + rows - 1) / rows > warps) warps = (a.V + rows - 1) / rows;
+        launch(k_embed_join<TG, VE, NG, ADD>, grid_for(warps, resident_j), kSumThreads, 0, st, a.sorted, a.T, a.V, a.H,
+               a.scale, p.rows * kSumWarps, dtable, a.ld, a.partial, p.part_ld, a.seen, rows, a.T > 0);
         AP_CHECK_LAUNCH("embed_backward join launch");
     }
     return AP_OK;
