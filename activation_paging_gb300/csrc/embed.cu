@@ -455,6 +455,24 @@ template <int VE, int NG> struct Slice {
     __device__ int at(int g) const { return s0 + g * kWarp; }
 };
 
+// Two single-precision operations in one instruction, each rounded as its own.
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 template <typename TG, int VE, int NG>
 __device__ __forceinline__ void finish_row(TG *row, const Slice<VE, NG> &sl, const float (&acc)[NG][VE],
                                            const Pack<TG, VE> (&old)[NG], float scale, bool add)
@@ -463,10 +481,17 @@ __device__ __forceinline__ void finish_row(TG *row, const Slice<VE, NG> &sl, con
     for (int g = 0; g < NG; ++g) {
         if (!sl.in(g)) continue;
         Pack<TG, VE> o;
+        if constexpr (VE == 1) {
+            const float v = __fmul_rn(scale, acc[g][0]);
+            o.v[0] = from_f<TG>(add ? __fadd_rn(to_f(old[g].v[0]), v) : v);
+        } else {
 #pragma unroll
-        for (int i = 0; i < VE; ++i) {
-            const float v = __fmul_rn(scale, acc[g][i]);
-            o.v[i] = from_f<TG>(add ? __fadd_rn(to_f(old[g].v[i]), v) : v);
+            for (int i = 0; i < VE; i += 2) {
+                float2 x = mul2(make_float2(scale, scale), make_float2(acc[g][i], acc[g][i + 1]));
+                if (add) x = add2(make_float2(to_f(old[g].v[i]), to_f(old[g].v[i + 1])), x);
+                o.v[i] = from_f<TG>(x.x);
+                o.v[i + 1] = from_f<TG>(x.y);
+            }
         }
         reinterpret_cast<Pack<TG, VE> *>(row)[sl.at(g)] = o;
     }
@@ -499,9 +524,18 @@ template <typename E, int VE, int NG>
 __device__ __forceinline__ void add_row(float (&a)[NG][VE], const Pack<E, VE> (&v)[NG])
 {
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
+    for (int g = 0; g < NG; ++g) {
+        if constexpr (VE == 1) {
+            a[g][0] = __fadd_rn(a[g][0], to_f(v[g].v[0]));
+        } else {
 #pragma unroll
-        for (int i = 0; i < VE; ++i) a[g][i] = __fadd_rn(a[g][i], to_f(v[g].v[i]));
+            for (int i = 0; i < VE; i += 2) {
+                const float2 x = add2(make_float2(a[g][i], a[g][i + 1]), make_float2(to_f(v[g].v[i]), to_f(v[g].v[i + 1])));
+                a[g][i] = x.x;
+                a[g][i + 1] = x.y;
+            }
+        }
+    }
 }
 
 template <int VE, int NG>
@@ -554,26 +588,47 @@ template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
 constexpr int kSumSmem = kSumWarps * ((RING ? kStages * (kDoutBytes + kOldBytes<TD, TG, ADD>) : 0) +
                                       2 * kWarp * VE * NG * 4);
 
-__device__ __forceinline__ void copy_async16(uint32_t to, const void *from)
+// A bulk copy of `bytes` bytes (all in 16-byte granules) to shared memory, which completes on the barrier.
+__device__ __forceinline__ void copy_bulk(uint32_t to, const void *from, uint32_t bytes, uint32_t bar)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+                 "l"(from), "r"(bytes), "r"(bar)
+                 : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait()
+__device__ __forceinline__ void bar_init(uint32_t bar)
 {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Waits for the copies of a phase, at most kWaitLimit tries; false if they did not come.
+constexpr int kWaitLimit = 1 << 18;
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
+{
+    for (int i = 0; i < kWaitLimit; ++i) {
+        uint32_t done;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(done)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+        if (done) return true;
+    }
+    return false;
 }
 
 // RING (rows of both in 16-byte granules): every warp keeps kStages rows on
 // their way to shared memory, over the ends of items, so that the sums never
-// wait for one row's latency; loads into registers left 3.3 TB/s at 32768 x
-// 7168 rows, bound by what a warp's registers hold in flight.
+// wait for one row's latency.  A lane copies the row of its own token, so a
+// batch of rows costs two instructions.  Loads into registers left 3.3 TB/s
+// at 32768 x 7168 rows, bound by what a warp's registers hold in flight.
 // Otherwise the rows go through registers, four at a time.
 template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
 __global__ void __launch_bounds__(kSumThreads, 2)
     k_embed_sum(const TD *__restrict__ dout, int64_t dout_ld, const uint2 *__restrict__ sorted, int64_t T, int64_t V,
                 int H, float scale, int rows, TG *__restrict__ dtable, int64_t ld, float *__restrict__ partial,
-                int64_t part_ld, const void *__restrict__ ids, bool wide, int64_t pad)
+                int64_t part_ld, const void *__restrict__ ids, bool wide, int64_t pad, uint32_t *d_status)
 {
     prefetch_inputs<TD, TG, ADD>(dout, dout_ld, ids, wide, T, V, pad, H, dtable, ld);
     pdl_begin_after(); // the join's zeros need the sort complete
@@ -583,6 +638,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
     constexpr int kStage = kDoutBytes + kOld;
     extern __shared__ __align__(16) uint8_t s_mem[];
     __shared__ uint32_t s_flags[kSumWarps];
+    __shared__ uint64_t s_bar[kSumWarps][kStages / kBatch]; // one for each batch of the ring
     const int lane = (int)lane_id(), w = threadIdx.x / kWarp;
     auto s_part = [&](int q, int slot) { return reinterpret_cast<float *>(s_mem) + (q * 2 + slot) * kCols; };
     uint8_t *ring = s_mem + kSumWarps * 2 * kCols * 4 + w * (kStages * kStage);
@@ -623,30 +679,33 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         return x;
     };
     // the column slice of row r, of dout and of dtable
-    auto src_of = [&](const Rows &x, int r) {
+    [[maybe_unused]] auto src_of = [&](const Rows &x, int r) {
         return reinterpret_cast<const TD *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x.src), r));
     };
     auto dst_of = [&](const Rows &x, int r) {
         return reinterpret_cast<TG *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x.dst), r));
     };
-    // kBatch rows of x from r0 on into their stages of the ring: one group, empty past the end
+    // kBatch rows of x from r0 on into their stages of the ring: a lane copies its own token's row
     auto fetch = [&](const Rows &x, int r0) {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int r = r0 + u;
-            if (r >= x.live) break;
-            const uint32_t to = smem_addr(ring) + (r0 % kStages + u) * kStage + lane * 16;
-            const uint8_t *from = reinterpret_cast<const uint8_t *>(src_of(x, r));
-            if (lane * 16 < x.cols * (int)sizeof(TD)) copy_async16(to, from + lane * 16);
-            if (ADD && (x.direct >> r & 1)) {
-                from = reinterpret_cast<const uint8_t *>(dst_of(x, r));
-#pragma unroll
-                for (int b = 0; b < kOld; b += kWarp * 16)
-                    if (b + lane * 16 < x.cols * (int)sizeof(TG)) copy_async16(to + kDoutBytes + b, from + b + lane * 16);
-            }
+        const int rows_left = x.live - r0;
+        if (rows_left <= 0) return;
+        const uint32_t bar = smem_addr(&s_bar[w][r0 / kBatch % (kStages / kBatch)]);
+        const uint32_t db = x.cols * sizeof(TD), gb = x.cols * sizeof(TG);
+        const uint32_t mask = (rows_left >= kBatch ? (1u << kBatch) - 1 : (1u << rows_left) - 1) << r0;
+        if (lane == 0) bar_expect(bar, __popc(mask) * db + (ADD ? __popc(x.direct & mask) * gb : 0u));
+        __syncwarp();
+        if (mask >> lane & 1) {
+            const uint32_t to = smem_addr(ring) + (uint32_t)(lane % kStages) * kStage;
+            copy_bulk(to, x.src, db, bar);
+            if (ADD && (x.direct >> lane & 1)) copy_bulk(to + kDoutBytes, x.dst, gb, bar);
         }
-        copy_commit();
     };
+    uint32_t phases = 0; // parity of each barrier's phase
+    if (RING) {
+        if (lane < kStages / kBatch) bar_init(smem_addr(&s_bar[w][lane]));
+        asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+    }
     Rows ahead;
     if (blockIdx.x < sums) {
         ahead = rows_of(blockIdx.x);
@@ -677,8 +736,10 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         };
         if constexpr (RING) {
             for (int r0 = 0; r0 < live; r0 += kBatch) {
-                copy_wait<kStages / kBatch - 1>();
-                __syncwarp();
+                const int slot = r0 / kBatch % (kStages / kBatch);
+                if (!bar_wait(smem_addr(&s_bar[w][slot]), phases >> slot & 1) && d_status)
+                    atomicOr(d_status, AP_FLAG_CORRUPT);
+                phases ^= 1u << slot;
                 const uint8_t *at = ring + r0 % kStages * kStage;
                 Pack<TD, VE> v[kBatch][NG];
                 Pack<TG, VE> old[kBatch][NG];
@@ -699,7 +760,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
                 for (int u = 0; u < kBatch; ++u)
                     if (r0 + u < live) take(r0 + u, v[u], old[u]);
             }
-            // the rows past `live` left empty groups: the next item's first rows follow them
+            // the whole ring is free: the next item's first rows
             if (more)
                 for (int r = 0; r < kStages; r += kBatch) fetch(ahead, r);
         } else {
@@ -1003,6 +1064,7 @@ struct SumArgs {
     const void *ids;
     bool wide;
     int64_t pad;
+    uint32_t *d_status;
 };
 
 template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
@@ -1020,7 +1082,7 @@ ap_status embed_sums(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
     if (items > 0) {
         launch(kernel, (int)(items < resident ? items : resident), kSumThreads, smem, st,
                static_cast<const TD *>(a.dout), a.dout_ld, a.sorted, a.T, a.V, a.H, a.scale, p.rows, dtable, a.ld,
-               a.partial, p.part_ld, a.ids, a.wide, a.pad);
+               a.partial, p.part_ld, a.ids, a.wide, a.pad, a.d_status);
         AP_CHECK_LAUNCH("embed_backward sum launch");
     }
     if (!ADD || p.sum_tiles > 1) {
@@ -1133,7 +1195,7 @@ extern "C" ap_status ap_embed_backward(const void *dout, int64_t dout_ld, int32_
                                      d_status, st);
     if (ss != AP_OK) return ss;
     const SumArgs a = {dout,   dout_ld, sorted, T, V, H, scale, dtable, dtable_ld,
-                       reinterpret_cast<float *>(sc + p.off_part), T > 0 ? seen : nullptr, ids, id_bytes == 8, padding_idx};
+                       reinterpret_cast<float *>(sc + p.off_part), T > 0 ? seen : nullptr, ids, id_bytes == 8, padding_idx, d_status};
     const bool fd = dout_dtype == AP_DTYPE_F32, fg = dtable_dtype == AP_DTYPE_F32, add = accumulate != 0;
     if (fd && fg) return embed_backward_typed<float, float>(a, dout_dtype, dtable_dtype, add, p, st);
     if (fd) return embed_backward_typed<float, bf16_t>(a, dout_dtype, dtable_dtype, add, p, st);
