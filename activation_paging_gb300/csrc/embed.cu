@@ -586,7 +586,7 @@ template <typename TD, typename TG, bool ADD>
 constexpr int kOldBytes = ADD ? kDoutBytes / (int)sizeof(TD) * (int)sizeof(TG) : 0;
 template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
 constexpr int kSumSmem = kSumWarps * ((RING ? kStages * (kDoutBytes + kOldBytes<TD, TG, ADD>) : 0) +
-                                      2 * kWarp * VE * NG * 4);
+                                      kWarp * VE * NG * 4);
 
 // A bulk copy of `bytes` bytes (all in 16-byte granules) to shared memory, which completes on the barrier.
 __device__ __forceinline__ void copy_bulk(uint32_t to, const void *from, uint32_t bytes, uint32_t bar)
@@ -640,8 +640,8 @@ __global__ void __launch_bounds__(kSumThreads, 2)
     __shared__ uint32_t s_flags[kSumWarps];
     __shared__ uint64_t s_bar[kSumWarps][kStages / kBatch]; // one for each batch of the ring
     const int lane = (int)lane_id(), w = threadIdx.x / kWarp;
-    auto s_part = [&](int q, int slot) { return reinterpret_cast<float *>(s_mem) + (q * 2 + slot) * kCols; };
-    uint8_t *ring = s_mem + kSumWarps * 2 * kCols * 4 + w * (kStages * kStage);
+    auto s_part = [&](int q) { return reinterpret_cast<float *>(s_mem) + q * kCols; }; // a warp's head
+    uint8_t *ring = s_mem + kSumWarps * kCols * 4 + w * (kStages * kStage);
     const uint32_t none = (uint32_t)V;
     const int nstep = H / VE;
     const int slices = (nstep + kWarp * NG - 1) / (kWarp * NG);
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
             if (direct >> r & 1)
                 finish_row(dst_of(cur, r), here, acc, old, scale, ADD);
             else
-                store_part(s_part(w, 0), mine, acc);
+                store_part(s_part(w), mine, acc);
             zero(acc);
         };
         if constexpr (RING) {
@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         if (live > 0 && !(ends >> (live - 1) & 1)) { // the last run goes on
             const bool through = began && ends == 0;
             flags |= through ? kThrough : kTail;
-            store_part(s_part(w, through ? 0 : 1), mine, acc);
+            if (through) store_part(s_part(w), mine, acc); // (a tail stays in the warp's registers)
         }
         if (lane == 0) s_flags[w] = flags;
         __syncthreads();
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         auto join_from = [&](int q) { // adds heads from warp q on; true if the run ends in this tile
             for (; q < kSumWarps; ++q) {
                 Pack<float, VE> p[NG];
-                load_part(p, s_part(q, 0), mine);
+                load_part(p, s_part(q), mine);
                 add_row(acc, p);
                 if (!(s_flags[q] & kThrough)) return true;
             }
