@@ -256,15 +256,16 @@ def embed_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: float =
     v, h, g_ld, g_kind = _rows(dtable, "dtable")
     if v != V or h != H:
         raise ValueError(f"dtable must be {[V, H]}, got {[v, h]}")
-    sb = embed_scratch_bytes(T, V, H)
-    if scratch is None:
-        scratch = _empty(sb, torch.uint8, dout.device, stream)
-    else:
+    if scratch is not None:
         _need(scratch, torch.uint8, "scratch")
+    else:
+        sb = embed_scratch_bytes(T, V, H)
+        if sb:
+            scratch = _empty(sb, torch.uint8, dout.device, stream)
     check(lib().ap_embed_backward(_p(dout), ld, kind, _p(ids), size, T, H, V,
                                   -1 if padding_idx is None else padding_idx, scale, 1 if accumulate else 0, _p(dtable),
-                                  g_ld, g_kind, _p(scratch), scratch.numel(), _p(status), _stream(stream)),
-          "embed_backward")
+                                  g_ld, g_kind, _p(scratch), scratch.numel() if scratch is not None else 0, _p(status),
+                                  _stream(stream)), "embed_backward")
     return dtable
 
 

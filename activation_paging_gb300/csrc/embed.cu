@@ -215,21 +215,23 @@ constexpr size_t cluster_smem(int items, int bits, int blocks)
     return (size_t)kClThreads * items * 8 + ((size_t)(kClWarps + blocks) << bits) * 2;
 }
 
-template <int ITEMS>
-__global__ void __launch_bounds__(kClThreads, 1)
-    k_sort_cluster(const void *__restrict__ ids, bool wide, int T, int per, int64_t V, int64_t pad, int passes,
-                   int bits, uint2 *__restrict__ sorted, uint32_t *__restrict__ seen, uint32_t *d_status)
+// The passes, by one block or (CLUSTER) by all blocks of the cluster that is
+// the grid.  smem: the block's tokens, the warps' counts, the blocks' totals
+// (cluster_smem bytes).  out(at, pair) takes every sorted token; no block
+// touches another's memory after the barrier that precedes it.
+template <int ITEMS, bool CLUSTER, typename Out>
+__device__ __forceinline__ void sort_passes(const void *__restrict__ ids, bool wide, int T, int per, int64_t V,
+                                            int64_t pad, int passes, int bits, uint2 *s_pairs, uint32_t *d_status,
+                                            Out out)
 {
-    pdl_begin_after(); // the sums kernel reads ids and rows ahead of its own wait
     // Counts and totals are 16 bits, two digits to a word (bits >= 1, a block holds at most 8192 tokens).
-    extern __shared__ uint2 s_pairs[];                                            // [kClThreads * ITEMS]
     uint16_t *cnt = reinterpret_cast<uint16_t *>(s_pairs + kClThreads * ITEMS);   // [kClWarps][D]
     __shared__ uint32_t s_base[1 << kMaxDigitBits], s_warp[kClWarps], s_group[kClThreads];
     const int D = 1 << bits, D2 = D / 2;
     uint16_t *tot = cnt + kClWarps * D; // [blocks][D]
     uint32_t *cnt2 = reinterpret_cast<uint32_t *>(cnt), *tot2 = reinterpret_cast<uint32_t *>(tot);
     const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
-    const uint32_t me = blockIdx.x, blocks = gridDim.x; // the grid is one cluster
+    const uint32_t me = CLUSTER ? blockIdx.x : 0, blocks = CLUSTER ? gridDim.x : 1;
     const int first = (int)me * per;
     const int n = T - first < per ? T - first : per; // this block's tokens (may be <= 0)
     const int l0 = wid * (ITEMS * kWarp) + lane;
@@ -244,9 +246,6 @@ __global__ void __launch_bounds__(kClThreads, 1)
     const int groups = D2 >= kClThreads ? 1 : kClThreads / D2 < kClWarps ? kClThreads / D2 : kClWarps;
     const int each = kClWarps / groups;
     const int pair_of = (int)threadIdx.x & (D2 - 1), group = (int)threadIdx.x / D2;
-    if (seen) // cleared before the first barrier of the cluster, set in the last pass
-        for (int64_t i = (int64_t)me * kClThreads + threadIdx.x; i < (V + 31) / 32; i += (int64_t)blocks * kClThreads)
-            seen[i] = 0;
     for (int pass = 0; pass < passes; ++pass) {
         const int shift = pass * bits;
         uint2 pair[ITEMS];
@@ -271,29 +270,39 @@ __global__ void __launch_bounds__(kClThreads, 1)
         __syncthreads();
         uint32_t sum = 0;
         if (group < groups) {
+#pragma unroll 8
             for (int q = 0; q < each; ++q) sum += cnt2[(group * each + q) * D2 + pair_of];
             s_group[group * D2 + pair_of] = sum;
         }
         __syncthreads();
         if (group < groups) {
             uint32_t base = 0;
+#pragma unroll 4
             for (int g = 0; g < group; ++g) base += s_group[g * D2 + pair_of];
+#pragma unroll 8
             for (int q = 0; q < each; ++q) {
                 uint32_t *c = &cnt2[(group * each + q) * D2 + pair_of];
                 const uint32_t v = *c;
                 *c = base;
                 base += v;
             }
-            if (group == groups - 1) // base is the block's total: to every block
-                for (uint32_t r = 0; r < blocks; ++r)
-                    cluster_store(cluster_addr(smem_addr(&tot2[me * D2 + pair_of]), r), base);
+            if (group == groups - 1) { // base is the block's total: to every block
+                if (CLUSTER) {
+#pragma unroll 4
+                    for (uint32_t r = 0; r < blocks; ++r)
+                        cluster_store(cluster_addr(smem_addr(&tot2[me * D2 + pair_of]), r), base);
+                } else {
+                    tot2[pair_of] = base;
+                }
+            }
         }
         sync_all(); // the totals are there, and no block needs its s_pairs any more
         uint32_t before = 0, all = 0;
         if ((int)threadIdx.x < D) {
+#pragma unroll 8
             for (uint32_t r = 0; r < blocks; ++r) {
                 const uint32_t c = tot[r * D + threadIdx.x];
-                if (r < me) before += c;
+                if ((int)r < (int)me) before += c;
                 all += c;
             }
         }
@@ -313,21 +322,39 @@ __global__ void __launch_bounds__(kClThreads, 1)
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const bool in = l0 + i * kWarp < n;
-            if (seen && last) mark_seen(seen, in ? pair[i].x : (uint32_t)V, V);
-            if (!in) continue;
             const int d = (int)((pair[i].x >> shift) & (D - 1));
-            const uint32_t at = s_base[d] + mine[d] + rank[i];
+            const uint32_t at = in ? s_base[d] + mine[d] + rank[i] : 0u;
             if (last) {
-                sorted[at] = pair[i];
-            } else {
+                out(at, pair[i], in); // (all lanes)
+            } else if (in) {
                 const uint32_t to = at / (uint32_t)per;
-                cluster_store(cluster_addr(smem_addr(s_pairs + (at - to * per)), to), pair[i]);
+                if (CLUSTER)
+                    cluster_store(cluster_addr(smem_addr(s_pairs + (at - to * per)), to), pair[i]);
+                else
+                    s_pairs[at] = pair[i];
             }
         }
-        // the pairs are in place, and nobody reads the totals any more; nothing
-        // of another block is touched after the last pass's barrier above
+        // the pairs are in place, and nobody reads the totals any more
         if (!last) sync_all();
     }
+}
+
+template <int ITEMS>
+__global__ void __launch_bounds__(kClThreads, 1)
+    k_sort_cluster(const void *__restrict__ ids, bool wide, int T, int per, int64_t V, int64_t pad, int passes,
+                   int bits, uint2 *__restrict__ sorted, uint32_t *__restrict__ seen, uint32_t *d_status)
+{
+    pdl_begin_after(); // the sums kernel reads ids and rows ahead of its own wait
+    extern __shared__ __align__(16) uint8_t s_mem[];
+    if (seen) // cleared before the first barrier of the cluster, set in the last pass
+        for (int64_t i = (int64_t)blockIdx.x * kClThreads + threadIdx.x; i < (V + 31) / 32;
+             i += (int64_t)gridDim.x * kClThreads)
+            seen[i] = 0;
+    sort_passes<ITEMS, true>(ids, wide, T, per, V, pad, passes, bits, reinterpret_cast<uint2 *>(s_mem), d_status,
+                             [&](uint32_t at, uint2 pair, bool in) {
+                                 if (seen) mark_seen(seen, in ? pair.x : (uint32_t)V, V);
+                                 if (in) sorted[at] = pair;
+                             });
 }
 
 // Longer inputs: three launches per digit, over tiles of kSortTile tokens.
@@ -624,28 +651,26 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
 // batch of rows costs two instructions.  Loads into registers left 3.3 TB/s
 // at 32768 x 7168 rows, bound by what a warp's registers hold in flight.
 // Otherwise the rows go through registers, four at a time.
-template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
-__global__ void __launch_bounds__(kSumThreads, 2)
-    k_embed_sum(const TD *__restrict__ dout, int64_t dout_ld, const uint2 *__restrict__ sorted, int64_t T, int64_t V,
-                int H, float scale, int rows, TG *__restrict__ dtable, int64_t ld, float *__restrict__ partial,
-                int64_t part_ld, const void *__restrict__ ids, bool wide, int64_t pad, uint32_t *d_status)
+// The items (tile, slice) of a grid of blocks of W warps; s_mem: kSumSmem bytes.
+template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING, int W>
+__device__ __forceinline__ void sum_items(const TD *__restrict__ dout, int64_t dout_ld, const uint2 *sorted, int64_t T,
+                                          int64_t V, int H, float scale, int rows, TG *__restrict__ dtable, int64_t ld,
+                                          float *__restrict__ partial, int64_t part_ld, uint8_t *s_mem,
+                                          uint32_t *d_status)
 {
-    prefetch_inputs<TD, TG, ADD>(dout, dout_ld, ids, wide, T, V, pad, H, dtable, ld);
-    pdl_begin_after(); // the join's zeros need the sort complete
     constexpr uint32_t kHead = 1, kThrough = 2, kTail = 4;
     constexpr int kCols = kWarp * VE * NG;
     constexpr int kOld = kOldBytes<TD, TG, ADD>;
     constexpr int kStage = kDoutBytes + kOld;
-    extern __shared__ __align__(16) uint8_t s_mem[];
-    __shared__ uint32_t s_flags[kSumWarps];
-    __shared__ uint64_t s_bar[kSumWarps][kStages / kBatch]; // one for each batch of the ring
+    __shared__ uint32_t s_flags[W];
+    __shared__ uint64_t s_bar[W][kStages / kBatch]; // one for each batch of the ring
     const int lane = (int)lane_id(), w = threadIdx.x / kWarp;
     auto s_part = [&](int q) { return reinterpret_cast<float *>(s_mem) + q * kCols; }; // a warp's head
-    uint8_t *ring = s_mem + kSumWarps * kCols * 4 + w * (kStages * kStage);
+    uint8_t *ring = s_mem + W * kCols * 4 + w * (kStages * kStage);
     const uint32_t none = (uint32_t)V;
     const int nstep = H / VE;
     const int slices = (nstep + kWarp * NG - 1) / (kWarp * NG);
-    const int64_t tiles = (T + rows * kSumWarps - 1) / (rows * kSumWarps);
+    const int64_t tiles = (T + rows * W - 1) / (rows * W);
     const int64_t sums = tiles * slices;
     const Slice<VE, NG> mine{lane, kWarp * NG}; // within a slice, for s_part
     // a warp's tokens of an item, with the ids before and after them
@@ -663,7 +688,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         x.tile = it / slices;
         x.col0 = (int)(it - x.tile * slices) * kCols;
         x.cols = H - x.col0 < kCols ? H - x.col0 : kCols;
-        const int64_t i0 = (x.tile * kSumWarps + w) * rows;
+        const int64_t i0 = (x.tile * W + w) * rows;
         x.n = T - i0 >= rows ? rows : T > i0 ? (int)(T - i0) : 0;
         x.my = lane < x.n ? sorted[i0 + lane] : make_uint2(none, 0u);
         x.before = x.n > 0 && i0 > 0 ? sorted[i0 - 1].x : none;
@@ -795,7 +820,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         __syncthreads();
         // runs that span warps: the warp in which one begins joins it, the last warp joins what entered the tile
         auto join_from = [&](int q) { // adds heads from warp q on; true if the run ends in this tile
-            for (; q < kSumWarps; ++q) {
+            for (; q < W; ++q) {
                 Pack<float, VE> p[NG];
                 load_part(p, s_part(q), mine);
                 add_row(acc, p);
@@ -813,7 +838,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
                 store_part(partial + (2 * tile + 1) * part_ld, sl, acc);
             }
         }
-        if (w == kSumWarps - 1 && (s_flags[0] & kHead)) {
+        if (w == W - 1 && (s_flags[0] & kHead)) {
             zero(acc);
             (void)join_from(0);
             store_part(partial + 2 * tile * part_ld, sl, acc);
@@ -822,22 +847,36 @@ __global__ void __launch_bounds__(kSumThreads, 2)
     }
 }
 
+template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
+__global__ void __launch_bounds__(kSumThreads, 2)
+    k_embed_sum(const TD *__restrict__ dout, int64_t dout_ld, const uint2 *__restrict__ sorted, int64_t T, int64_t V,
+                int H, float scale, int rows, TG *__restrict__ dtable, int64_t ld, float *__restrict__ partial,
+                int64_t part_ld, const void *__restrict__ ids, bool wide, int64_t pad, uint32_t *d_status)
+{
+    prefetch_inputs<TD, TG, ADD>(dout, dout_ld, ids, wide, T, V, pad, H, dtable, ld);
+    pdl_begin_after(); // the join's zeros need the sort complete
+    extern __shared__ __align__(16) uint8_t s_mem[];
+    sum_items<TD, TG, VE, NG, ADD, RING, kSumWarps>(dout, dout_ld, sorted, T, V, H, scale, rows, dtable, ld, partial,
+                                                    part_ld, s_mem, d_status);
+}
+
 // Zeros the rows of items [first, last) that no id names; an item is `rows`
-// rows (a power of two, at most 32), taken by one warp.
-template <typename TG, int VE>
+// rows (a power of two, at most 32), taken by one warp of W in a block.
+// seen_from(r0): bit i says whether row r0 + i is named, for r0 a multiple of `rows`.
+template <typename TG, int VE, int W, typename Seen>
 __device__ __forceinline__ void fill_rows(int64_t first, int64_t last, int rows, int64_t V, int nstep,
-                                          TG *__restrict__ dtable, int64_t ld, const uint32_t *__restrict__ seen)
+                                          TG *__restrict__ dtable, int64_t ld, Seen seen_from)
 {
     Pack<TG, VE> z;
 #pragma unroll
     for (int i = 0; i < VE; ++i) z.v[i] = from_f<TG>(0.f);
-    const int64_t warps = (int64_t)gridDim.x * kSumWarps;
+    const int64_t warps = (int64_t)gridDim.x * W;
     int64_t it = first + blockIdx.x + (int64_t)gridDim.x * (threadIdx.x / kWarp);
-    uint32_t word = seen && it < last ? __ldcg(seen + (it * rows >> 5)) : 0u;
+    uint32_t next = it < last ? seen_from(it * rows) : 0u;
     for (; it < last; it += warps) {
         const int64_t r0 = it * rows;
-        const uint32_t bits = word >> (r0 & 31);
-        if (seen && it + warps < last) word = __ldcg(seen + ((it + warps) * rows >> 5));
+        const uint32_t bits = next;
+        if (it + warps < last) next = seen_from((it + warps) * rows); // on its way while these rows are written
         const int n = V - r0 < rows ? (int)(V - r0) : rows;
         for (int r = 0; r < n; ++r) {
             if (bits >> r & 1) continue;
@@ -864,7 +903,8 @@ __global__ void __launch_bounds__(kSumThreads)
     const int nstep = H / VE;
     const int64_t fills = ADD ? 0 : (V + rows_per_fill - 1) / rows_per_fill;
     const int64_t ahead = early ? fills / 8 : 0;
-    if (!ADD) fill_rows<TG, VE>(0, ahead, rows_per_fill, V, nstep, dtable, ld, seen);
+    auto seen_from = [&](int64_t r0) { return seen ? __ldcg(seen + (r0 >> 5)) >> (r0 & 31) : 0u; };
+    if (!ADD) fill_rows<TG, VE, kSumWarps>(0, ahead, rows_per_fill, V, nstep, dtable, ld, seen_from);
     pdl_begin();
     const int slices = (nstep + kWarp * NG - 1) / (kWarp * NG);
     const int64_t tiles = (T + tile_rows - 1) / tile_rows;
@@ -900,7 +940,46 @@ __global__ void __launch_bounds__(kSumThreads)
         }
         finish_row(dtable + (int64_t)key * ld, sl, acc, old, scale, ADD);
     }
-    if (!ADD) fill_rows<TG, VE>(ahead, fills, rows_per_fill, V, nstep, dtable, ld, seen);
+    if (!ADD) fill_rows<TG, VE, kSumWarps>(ahead, fills, rows_per_fill, V, nstep, dtable, ld, seen_from);
+}
+
+// Up to kSmallTokens tokens in one launch: every block sorts them for itself,
+// then sums its slices of the columns (one tile, nothing to join elsewhere)
+// and zeros its share of the rows that no id names.  Half the launches and no
+// work space: 13 us of host time where the three launches above take 19.
+constexpr int64_t kSmallTokens = kClThreads;
+template <typename TD, typename TG, int VE, int NG, bool ADD>
+__global__ void __launch_bounds__(kClThreads, 1)
+    k_embed_small(const TD *__restrict__ dout, int64_t dout_ld, const void *__restrict__ ids, bool wide, int T,
+                  int64_t V, int64_t pad, int H, float scale, int passes, int bits, int rows, TG *__restrict__ dtable,
+                  int64_t ld, int rows_per_fill, uint32_t *d_status)
+{
+    pdl_begin();
+    extern __shared__ __align__(16) uint8_t s_mem[];
+    uint2 *sorted = reinterpret_cast<uint2 *>(s_mem);
+    sort_passes<1, false>(ids, wide, T, T, V, pad, passes, bits, sorted, blockIdx.x == 0 ? d_status : nullptr,
+                          [&](uint32_t at, uint2 pair, bool in) {
+                              if (in) sorted[at] = pair;
+                          });
+    __syncthreads();
+    // the counts of the sort are no longer needed: the sums' shared memory
+    sum_items<TD, TG, VE, NG, ADD, false, kClWarps>(dout, dout_ld, sorted, T, V, H, scale, rows, dtable, ld, nullptr, 0,
+                                                    s_mem + kClThreads * sizeof(uint2), nullptr);
+    if (ADD) return;
+    auto seen_from = [&](int64_t r0) { // a lane looks for one row
+        const uint32_t key = (uint32_t)(r0 + lane_id());
+        int lo = 0, hi = T;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (sorted[mid].x < key)
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        return __ballot_sync(0xffffffffu, lo < T && sorted[lo].x == key);
+    };
+    fill_rows<TG, VE, kClWarps>(0, (V + rows_per_fill - 1) / rows_per_fill, rows_per_fill, V, H / VE, dtable, ld,
+                                seen_from);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -925,6 +1004,11 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int32_t H)
     while (p.rows > 4 && T * pieces < kWantItems * p.rows * kSumWarps) p.rows /= 2;
     p.sum_tiles = (T + p.rows * kSumWarps - 1) / (p.rows * kSumWarps);
     p.part_ld = ((int64_t)H + 7) / 8 * 8;
+    if (T <= kSmallTokens) { // one tile, no work space
+        p.rows = T > 0 ? (int)((T + kClWarps - 1) / kClWarps) : 1;
+        p.sum_tiles = T > 0;
+        return p;
+    }
     auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
     p.off_b = up(T * 8);
     p.off_hist = p.off_b + (p.tiles ? up(T * 8) : 0);
@@ -1067,6 +1151,14 @@ struct SumArgs {
     uint32_t *d_status;
 };
 
+// Rows of zeros that a warp writes at a time: about 16 KB.
+int fill_rows_of(int64_t row_bytes)
+{
+    int rows = 32;
+    while (rows > 1 && rows * row_bytes > (16 << 10)) rows /= 2;
+    return rows;
+}
+
 template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
 ap_status embed_sums(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
 {
@@ -1087,8 +1179,7 @@ ap_status embed_sums(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
     }
     if (!ADD || p.sum_tiles > 1) {
         static const int resident_j = resident_grid((const void *)k_embed_join<TG, VE, NG, ADD>, kSumThreads);
-        int rows = 32; // zeros: about 16 KB a warp at a time
-        while (rows > 1 && rows * (int64_t)a.H * (int64_t)sizeof(TG) > (16 << 10)) rows /= 2;
+        const int rows = fill_rows_of((int64_t)a.H * sizeof(TG));
         int64_t warps = (p.sum_tiles - 1) * slices;
         if (!ADD && (a.V + rows - 1) / rows > warps) warps = (a.V + rows - 1) / rows;
         launch(k_embed_join<TG, VE, NG, ADD>, grid_for(warps, resident_j), kSumThreads, 0, st, a.sorted, a.T, a.V, a.H,
@@ -1098,9 +1189,38 @@ ap_status embed_sums(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
     return AP_OK;
 }
 
+template <typename TD, typename TG, int VE, int NG, bool ADD>
+ap_status embed_small(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
+{
+    const auto kernel = k_embed_small<TD, TG, VE, NG, ADD>;
+    constexpr size_t sums = kClThreads * sizeof(uint2) + (size_t)kClWarps * kWarp * VE * NG * 4;
+    constexpr size_t most = cluster_smem(1, kMaxDigitBits, 1) > sums ? cluster_smem(1, kMaxDigitBits, 1) : sums;
+    static const cudaError_t attr =
+        cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (attr != cudaSuccess) return cuda_fail(attr, "embed_backward");
+    const size_t sort = cluster_smem(1, p.bits, 1);
+    const int rows = fill_rows_of((int64_t)a.H * sizeof(TG));
+    int64_t grid = (a.H / VE + kWarp * NG - 1) / (kWarp * NG);
+    if (!ADD) { // enough blocks for the zeros
+        const int64_t fill = (a.V + (int64_t)rows * kClWarps - 1) / ((int64_t)rows * kClWarps);
+        if (fill > grid) grid = fill;
+    }
+    const int64_t resident = sm_count();
+    launch(kernel, (int)(grid < resident ? grid : resident), kClThreads, sort > sums ? sort : sums, st,
+           static_cast<const TD *>(a.dout), a.dout_ld, a.ids, a.wide, (int)a.T, a.V, a.pad, a.H, a.scale, p.passes,
+           p.bits, p.rows, static_cast<TG *>(a.dtable), a.ld, rows, a.d_status);
+    AP_CHECK_LAUNCH("embed_backward launch");
+    return AP_OK;
+}
+
 template <typename TD, typename TG>
 ap_status embed_backward_typed(const SumArgs &a, int32_t dt, int32_t gt, bool add, const EmbedPlan &p, cudaStream_t st)
 {
+    if (a.T <= kSmallTokens) { // narrow slices: few rows, many blocks
+        if (a.H % 4 == 0 && vec_ok(a.dout, a.dout_ld, dt, 4) && vec_ok(a.dtable, a.ld, gt, 4))
+            return add ? embed_small<TD, TG, 4, 1, true>(a, p, st) : embed_small<TD, TG, 4, 1, false>(a, p, st);
+        return add ? embed_small<TD, TG, 1, 2, true>(a, p, st) : embed_small<TD, TG, 1, 2, false>(a, p, st);
+    }
     constexpr int VE = sizeof(TD) == 2 && sizeof(TG) == 2 ? 8 : 4;
     constexpr int NG = sizeof(TD) == 2 && sizeof(TG) == 4 ? 2 : 1; // 512 bytes of dout a row and slice
     constexpr int V16 = sizeof(TD) == 2 || sizeof(TG) == 2 ? 8 : 4;
@@ -1179,23 +1299,29 @@ extern "C" ap_status ap_embed_backward(const void *dout, int64_t dout_ld, int32_
         return fail(AP_EINVAL, "embed_backward: bad types (dout %d, dtable %d, ids of %d bytes, accumulate %d)",
                     dout_dtype, dtable_dtype, id_bytes, accumulate);
     if (T == 0 && accumulate) return AP_OK;
-    if (!dtable || (T > 0 && (!dout || !ids || !scratch))) return fail(AP_EINVAL, "embed_backward: NULL pointer");
+    const EmbedPlan p = embed_plan(T, V, H);
+    if (!dtable || (T > 0 && (!dout || !ids)) || (p.bytes > 0 && !scratch))
+        return fail(AP_EINVAL, "embed_backward: NULL pointer");
     if (reinterpret_cast<uintptr_t>(dout) % size_of(dout_dtype) || reinterpret_cast<uintptr_t>(ids) % id_bytes ||
         reinterpret_cast<uintptr_t>(dtable) % size_of(dtable_dtype) || (reinterpret_cast<uintptr_t>(scratch) & 15))
         return fail(AP_EINVAL, "embed_backward: pointer not aligned");
-    const EmbedPlan p = embed_plan(T, V, H);
-    if (T > 0 && scratch_bytes < p.bytes)
+    if (scratch_bytes < p.bytes)
         return fail(AP_EINVAL, "embed_backward: scratch of %lld bytes, %lld needed", (long long)scratch_bytes,
                     (long long)p.bytes);
     cudaStream_t st = (cudaStream_t)stream;
     char *sc = static_cast<char *>(scratch);
-    uint32_t *seen = reinterpret_cast<uint32_t *>(sc + p.off_seen);
-    uint2 *sorted = nullptr;
-    const ap_status ss = sort_tokens(ids, id_bytes == 8, T, V, padding_idx, p, sc, &sorted, accumulate ? nullptr : seen,
-                                     d_status, st);
-    if (ss != AP_OK) return ss;
-    const SumArgs a = {dout,   dout_ld, sorted, T, V, H, scale, dtable, dtable_ld,
-                       reinterpret_cast<float *>(sc + p.off_part), T > 0 ? seen : nullptr, ids, id_bytes == 8, padding_idx, d_status};
+    SumArgs a = {dout, dout_ld, nullptr, T, V, H, scale, dtable, dtable_ld, nullptr, nullptr, ids, id_bytes == 8,
+                 padding_idx, d_status};
+    if (T > kSmallTokens) {
+        uint32_t *seen = reinterpret_cast<uint32_t *>(sc + p.off_seen);
+        uint2 *sorted = nullptr;
+        const ap_status ss = sort_tokens(ids, id_bytes == 8, T, V, padding_idx, p, sc, &sorted,
+                                         accumulate ? nullptr : seen, d_status, st);
+        if (ss != AP_OK) return ss;
+        a.sorted = sorted;
+        a.partial = reinterpret_cast<float *>(sc + p.off_part);
+        a.seen = seen;
+    }
     const bool fd = dout_dtype == AP_DTYPE_F32, fg = dtable_dtype == AP_DTYPE_F32, add = accumulate != 0;
     if (fd && fg) return embed_backward_typed<float, float>(a, dout_dtype, dtable_dtype, add, p, st);
     if (fd) return embed_backward_typed<float, bf16_t>(a, dout_dtype, dtable_dtype, add, p, st);

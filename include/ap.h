@@ -321,7 +321,8 @@ ap_status ap_embed(const void *table, int64_t V, int64_t table_ld, int32_t table
  *   dtable  [V, H] of dtable_dtype, rows dtable_ld apart (device, written;
  *           accumulate = 1: read too).  Elements between rows stay untouched
  *   scratch device work space of ap_embed_scratch_bytes() bytes, 16-byte
- *           aligned; its contents need no initialisation
+ *           aligned; its contents need no initialisation.  Few tokens need 0
+ *           bytes (NULL)
  * T = 0 is the empty sum.  ids, types and limits as ap_embed. */
 ap_status ap_embed_scratch_bytes(int64_t T, int64_t V, int32_t H, int64_t *bytes);
 ap_status ap_embed_backward(const void *dout, int64_t dout_ld, int32_t dout_dtype, const void *ids, int32_t id_bytes,

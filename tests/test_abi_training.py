@@ -84,9 +84,9 @@ def test_embed_refusals(lib):
 
 def test_embed_backward_refusals(lib):
     n = ctypes.c_int64()
-    assert lib.ap_embed_scratch_bytes(1000, 5000, 64, ctypes.byref(n)) == 0
+    assert lib.ap_embed_scratch_bytes(5000, 5000, 64, ctypes.byref(n)) == 0
 
-    def call(dout=P, dld=64, dt=0, ids=P, ib=4, T=1000, H=64, V=5000, pad=-1, acc=0, dtable=P, gld=64, gt=2, scratch=P,
+    def call(dout=P, dld=64, dt=0, ids=P, ib=4, T=5000, H=64, V=5000, pad=-1, acc=0, dtable=P, gld=64, gt=2, scratch=P,
              sb=n.value):
         return lib.ap_embed_backward(dout, dld, dt, ids, ib, T, H, V, pad, 1.0, acc, dtable, gld, gt, scratch, sb,
                                      None, None)
@@ -128,6 +128,7 @@ def test_scratch_sizes(lib):
     assert emb(0, 1, 1) % 256 == 0
     assert emb(1, 1, 1) <= emb(1000, 1, 1) <= emb(100000, 1, 1)
     assert emb(1000, 100, 64) <= emb(1000, 100, 4096)
+    assert emb(5000, 100, 64) < emb(5000, 100, 4096)
     assert lib.ap_route_balance_scratch_bytes(10, 8, 0, None) == -1
     assert lib.ap_route_balance_scratch_bytes(10, 0, 0, ctypes.byref(n)) == -1
     assert lib.ap_embed_scratch_bytes(10, 8, 0, ctypes.byref(n)) == -1
