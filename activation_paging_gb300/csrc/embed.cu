@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(256)
         PI r[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (ok && s0 + u * kWarp < nstep) r[u] = src[s0 + u * kWarp];
+            load_now(r[u], src + s0 + u * kWarp, ok && s0 + u * kWarp < nstep);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s0 + u * kWarp >= nstep) continue;
@@ -217,12 +217,11 @@ constexpr size_t cluster_smem(int items, int bits, int blocks)
 
 // The passes, by one block or (CLUSTER) by all blocks of the cluster that is
 // the grid.  smem: the block's tokens, the warps' counts, the blocks' totals
-// (cluster_smem bytes).  out(at, pair) takes every sorted token; no block
-// touches another's memory after the barrier that precedes it.
-template <int ITEMS, bool CLUSTER, typename Out>
-__device__ __forceinline__ void sort_passes(const void *__restrict__ ids, bool wide, int T, int per, int64_t V,
-                                            int64_t pad, int passes, int bits, uint2 *s_pairs, uint32_t *d_status,
-                                            Out out)
+// (cluster_smem bytes).  key_of(t) gives token t's key, out(at, pair, in) takes
+// every sorted token (all lanes call it); no block touches another's memory
+// after the barrier that precedes it.
+template <int ITEMS, bool CLUSTER, typename Key, typename Out>
+__device__ __forceinline__ void sort_passes(int T, int per, int passes, int bits, uint2 *s_pairs, Key key_of, Out out)
 {
     // Counts and totals are 16 bits, two digits to a word (bits >= 1, a block holds at most 8192 tokens).
     uint16_t *cnt = reinterpret_cast<uint16_t *>(s_pairs + kClThreads * ITEMS);   // [kClWarps][D]
@@ -254,7 +253,7 @@ __device__ __forceinline__ void sort_passes(const void *__restrict__ ids, bool w
             const int l = l0 + i * kWarp;
             if (l < n) {
                 if (pass == 0)
-                    pair[i] = make_uint2(sort_key(ids, wide, first + l, V, pad, d_status), (uint32_t)(first + l));
+                    pair[i] = make_uint2(key_of(first + l), (uint32_t)(first + l));
                 else
                     pair[i] = s_pairs[l];
             }
@@ -325,7 +324,7 @@ __device__ __forceinline__ void sort_passes(const void *__restrict__ ids, bool w
             const int d = (int)((pair[i].x >> shift) & (D - 1));
             const uint32_t at = in ? s_base[d] + mine[d] + rank[i] : 0u;
             if (last) {
-                out(at, pair[i], in); // (all lanes)
+                out(at, pair[i], in);
             } else if (in) {
                 const uint32_t to = at / (uint32_t)per;
                 if (CLUSTER)
@@ -350,11 +349,13 @@ __global__ void __launch_bounds__(kClThreads, 1)
         for (int64_t i = (int64_t)blockIdx.x * kClThreads + threadIdx.x; i < (V + 31) / 32;
              i += (int64_t)gridDim.x * kClThreads)
             seen[i] = 0;
-    sort_passes<ITEMS, true>(ids, wide, T, per, V, pad, passes, bits, reinterpret_cast<uint2 *>(s_mem), d_status,
-                             [&](uint32_t at, uint2 pair, bool in) {
-                                 if (seen) mark_seen(seen, in ? pair.x : (uint32_t)V, V);
-                                 if (in) sorted[at] = pair;
-                             });
+    sort_passes<ITEMS, true>(
+        T, per, passes, bits, reinterpret_cast<uint2 *>(s_mem),
+        [&](int t) { return sort_key(ids, wide, t, V, pad, d_status); },
+        [&](uint32_t at, uint2 pair, bool in) {
+            if (seen) mark_seen(seen, in ? pair.x : (uint32_t)V, V);
+            if (in) sorted[at] = pair;
+        });
 }
 
 // Longer inputs: three launches per digit, over tiles of kSortTile tokens.
@@ -550,17 +551,16 @@ template <int VE, int NG> __device__ __forceinline__ void zero(float (&a)[NG][VE
 template <typename E, int VE, int NG>
 __device__ __forceinline__ void add_row(float (&a)[NG][VE], const Pack<E, VE> (&v)[NG])
 {
+    if constexpr (VE * NG == 1) {
+        a[0][0] = __fadd_rn(a[0][0], to_f(v[0].v[0]));
+    } else {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        if constexpr (VE == 1) {
-            a[g][0] = __fadd_rn(a[g][0], to_f(v[g].v[0]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < VE; i += 2) {
-                const float2 x = add2(make_float2(a[g][i], a[g][i + 1]), make_float2(to_f(v[g].v[i]), to_f(v[g].v[i + 1])));
-                a[g][i] = x.x;
-                a[g][i + 1] = x.y;
-            }
+        for (int i = 0; i < VE * NG; i += 2) {
+            const int j = i + 1;
+            const float2 x = add2(make_float2(a[i / VE][i % VE], a[j / VE][j % VE]),
+                                  make_float2(to_f(v[i / VE].v[i % VE]), to_f(v[j / VE].v[j % VE])));
+            a[i / VE][i % VE] = x.x;
+            a[j / VE][j % VE] = x.y;
         }
     }
 }
@@ -596,7 +596,7 @@ __device__ __forceinline__ void prefetch_inputs(const TD *dout, int64_t dout_ld,
     const int64_t rb = (int64_t)H * sizeof(TD), gb = ADD ? (int64_t)H * sizeof(TG) : 0;
     const int64_t most = kPrefetchBytes / (rb + gb);
     const int64_t n = T < most ? T : most;
-    for (int64_t t = (int64_t)threadIdx.x * gridDim.x + blockIdx.x; t < n; t += (int64_t)gridDim.x * kSumThreads) {
+    for (int64_t t = (int64_t)threadIdx.x * gridDim.x + blockIdx.x; t < n; t += (int64_t)gridDim.x * blockDim.x) {
         const int64_t id = load_id(ids, wide, t);
         if (id < 0 || id >= V || id == pad) continue;
         prefetch_l2(dout + t * dout_ld, rb);
@@ -604,16 +604,23 @@ __device__ __forceinline__ void prefetch_inputs(const TD *dout, int64_t dout_ld,
     }
 }
 
-// How the aligned form of the sums stages a row: 512 bytes of dout and the same
-// columns of dtable, copied to shared memory kStages rows ahead.
+// How the sums take their rows through a ring in shared memory.
+//   kAligned:  every row and slice starts on a 16-byte boundary
+//   kAnywhere: rows start anywhere: the 16-byte granules that hold a slice are
+//              copied, and read from its first byte on
+enum Route { kAligned, kAnywhere };
+
+// A row's stage of the ring: 512 bytes of dout and the same columns of dtable,
+// each with room for the granules at its ends, copied kStages rows ahead.
 constexpr int kStages = 8;
 constexpr int kBatch = 4; // rows taken from the ring at a time
 constexpr int kDoutBytes = kWarp * 16;
-template <typename TD, typename TG, bool ADD>
-constexpr int kOldBytes = ADD ? kDoutBytes / (int)sizeof(TD) * (int)sizeof(TG) : 0;
-template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
-constexpr int kSumSmem = kSumWarps * ((RING ? kStages * (kDoutBytes + kOldBytes<TD, TG, ADD>) : 0) +
-                                      kWarp * VE * NG * 4);
+template <typename TD, Route R> constexpr int kDoutStage = kDoutBytes + (R == kAnywhere ? 16 : 0);
+template <typename TD, typename TG, bool ADD, Route R>
+constexpr int kStageBytes = kDoutStage<TD, R> +
+                            (ADD ? kDoutBytes / (int)sizeof(TD) * (int)sizeof(TG) + (R == kAnywhere ? 16 : 0) : 0);
+template <typename TD, typename TG, int VE, int NG, bool ADD, Route R>
+constexpr int kSumSmem = kSumWarps * (kStages * kStageBytes<TD, TG, ADD, R> + kWarp * VE * NG * 4);
 
 // A bulk copy of `bytes` bytes (all in 16-byte granules) to shared memory, which completes on the barrier.
 __device__ __forceinline__ void copy_bulk(uint32_t to, const void *from, uint32_t bytes, uint32_t bar)
@@ -645,34 +652,68 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
     return false;
 }
 
-// RING (rows of both in 16-byte granules): every warp keeps kStages rows on
-// their way to shared memory, over the ends of items, so that the sums never
-// wait for one row's latency.  A lane copies the row of its own token, so a
-// batch of rows costs two instructions.  Loads into registers left 3.3 TB/s
-// at 32768 x 7168 rows, bound by what a warp's registers hold in flight.
-// Otherwise the rows go through registers, four at a time.
-// The items (tile, slice) of a grid of blocks of W warps; s_mem: kSumSmem bytes.
-template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING, int W>
-__device__ __forceinline__ void sum_items(const TD *__restrict__ dout, int64_t dout_ld, const uint2 *sorted, int64_t T,
-                                          int64_t V, int H, float scale, int rows, TG *__restrict__ dtable, int64_t ld,
-                                          float *__restrict__ partial, int64_t part_ld, uint8_t *s_mem,
-                                          uint32_t *d_status)
+// The granules of [p, p + bytes) inside [lo, hi), the buffer that holds it: a
+// buffer's first and last granules may be cut by its ends.
+struct Granules {
+    uintptr_t first, last; // of the whole granules
+    uintptr_t base;        // p's granule, where the stage begins
+};
+__device__ __forceinline__ Granules granules(uintptr_t p, uint32_t bytes, uintptr_t lo, uintptr_t hi)
 {
+    Granules g;
+    g.base = p & ~(uintptr_t)15;
+    g.first = g.base < lo ? g.base + 16 : g.base;
+    g.last = (p + bytes + 15) & ~(uintptr_t)15;
+    if (g.last > hi) g.last -= 16;
+    if (g.last < g.first) g.last = g.first;
+    return g;
+}
+
+// The elements of [p, p + bytes) that lie in no whole granule, by one lane.
+template <typename E>
+__device__ __forceinline__ void copy_ends(uint8_t *stage, const Granules &g, uintptr_t p, uint32_t bytes)
+{
+    if (g.first == g.base && g.last >= p + bytes) return;
+    for (uintptr_t q = p; q < p + bytes; q += sizeof(E)) {
+        if (q >= g.first && q + sizeof(E) <= g.last) {
+            q = g.last - sizeof(E); // on behind the granules
+            continue;
+        }
+        *reinterpret_cast<E *>(stage + (q - g.base)) = *reinterpret_cast<const E *>(q);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); // before a later bulk copy to the same place
+}
+
+// A block takes tiles of kSumWarps * rows sorted tokens and slices of the columns.
+// Through the ring every warp keeps kStages rows on their way to shared
+// memory, over the ends of items, so that the sums do not wait for one row's
+// latency.  A lane copies the row of its own token.  Loads into registers left
+// 3.3 TB/s at 32768 x 7168 rows, bound by what a warp's registers hold in
+// flight.
+template <typename TD, typename TG, int VE, int NG, bool ADD, Route R>
+__global__ void __launch_bounds__(kSumThreads, 2)
+    k_embed_sum(const TD *__restrict__ dout, int64_t dout_ld, const uint2 *__restrict__ sorted, int64_t T, int64_t V,
+                int H, float scale, int rows, uint32_t slices, uint32_t sums, TG *__restrict__ dtable, int64_t ld,
+                float *__restrict__ partial, int64_t part_ld, const void *__restrict__ ids, bool wide, int64_t pad,
+                uint32_t *d_status)
+{
+    prefetch_inputs<TD, TG, ADD>(dout, dout_ld, ids, wide, T, V, pad, H, dtable, ld);
+    pdl_begin_after(); // the join's zeros need the sort complete
+    extern __shared__ __align__(16) uint8_t s_mem[];
     constexpr uint32_t kHead = 1, kThrough = 2, kTail = 4;
     constexpr int kCols = kWarp * VE * NG;
-    constexpr int kOld = kOldBytes<TD, TG, ADD>;
-    constexpr int kStage = kDoutBytes + kOld;
-    __shared__ uint32_t s_flags[W];
-    __shared__ uint64_t s_bar[W][kStages / kBatch]; // one for each batch of the ring
+    constexpr int kDout = kDoutStage<TD, R>, kStage = kStageBytes<TD, TG, ADD, R>;
+    static_assert(kCols * sizeof(TD) == kDoutBytes, "a slice fills its stage");
+    __shared__ uint32_t s_flags[kSumWarps];
+    __shared__ uint64_t s_bar[kSumWarps][kStages / kBatch]; // one for each batch of the ring
     const int lane = (int)lane_id(), w = threadIdx.x / kWarp;
     auto s_part = [&](int q) { return reinterpret_cast<float *>(s_mem) + q * kCols; }; // a warp's head
-    uint8_t *ring = s_mem + W * kCols * 4 + w * (kStages * kStage);
+    uint8_t *ring = s_mem + kSumWarps * kCols * 4 + w * (kStages * kStage);
     const uint32_t none = (uint32_t)V;
     const int nstep = H / VE;
-    const int slices = (nstep + kWarp * NG - 1) / (kWarp * NG);
-    const int64_t tiles = (T + rows * W - 1) / (rows * W);
-    const int64_t sums = tiles * slices;
     const Slice<VE, NG> mine{lane, kWarp * NG}; // within a slice, for s_part
+    [[maybe_unused]] const uintptr_t dout_end = reinterpret_cast<uintptr_t>(dout + (T - 1) * dout_ld + H);
+    [[maybe_unused]] const uintptr_t dtable_end = reinterpret_cast<uintptr_t>(dtable + (V - 1) * ld + H);
     // a warp's tokens of an item, with the ids before and after them
     struct Rows {
         uint2 my;
@@ -683,12 +724,12 @@ __device__ __forceinline__ void sum_items(const TD *__restrict__ dout, int64_t d
         const TD *src; // the lane's token's columns of dout
         TG *dst;       // and of dtable
     };
-    auto rows_of = [&](int64_t it) {
+    auto rows_of = [&](uint32_t it) {
         Rows x;
         x.tile = it / slices;
-        x.col0 = (int)(it - x.tile * slices) * kCols;
+        x.col0 = (int)(it - (uint32_t)x.tile * slices) * kCols;
         x.cols = H - x.col0 < kCols ? H - x.col0 : kCols;
-        const int64_t i0 = (x.tile * W + w) * rows;
+        const int64_t i0 = (x.tile * kSumWarps + w) * rows;
         x.n = T - i0 >= rows ? rows : T > i0 ? (int)(T - i0) : 0;
         x.my = lane < x.n ? sorted[i0 + lane] : make_uint2(none, 0u);
         x.before = x.n > 0 && i0 > 0 ? sorted[i0 - 1].x : none;
@@ -703,10 +744,7 @@ __device__ __forceinline__ void sum_items(const TD *__restrict__ dout, int64_t d
         x.dst = dtable + (int64_t)x.my.x * ld + x.col0;
         return x;
     };
-    // the column slice of row r, of dout and of dtable
-    [[maybe_unused]] auto src_of = [&](const Rows &x, int r) {
-        return reinterpret_cast<const TD *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x.src), r));
-    };
+    // the column slice of row r of dtable
     auto dst_of = [&](const Rows &x, int r) {
         return reinterpret_cast<TG *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x.dst), r));
     };
@@ -717,27 +755,44 @@ __device__ __forceinline__ void sum_items(const TD *__restrict__ dout, int64_t d
         const uint32_t bar = smem_addr(&s_bar[w][r0 / kBatch % (kStages / kBatch)]);
         const uint32_t db = x.cols * sizeof(TD), gb = x.cols * sizeof(TG);
         const uint32_t mask = (rows_left >= kBatch ? (1u << kBatch) - 1 : (1u << rows_left) - 1) << r0;
-        if (lane == 0) bar_expect(bar, __popc(mask) * db + (ADD ? __popc(x.direct & mask) * gb : 0u));
-        __syncwarp();
-        if (mask >> lane & 1) {
-            const uint32_t to = smem_addr(ring) + (uint32_t)(lane % kStages) * kStage;
-            copy_bulk(to, x.src, db, bar);
-            if (ADD && (x.direct >> lane & 1)) copy_bulk(to + kDoutBytes, x.dst, gb, bar);
+        const bool on = mask >> lane & 1, both = ADD && on && (x.direct >> lane & 1);
+        uint8_t *stage = ring + lane % kStages * kStage;
+        const uint32_t to = smem_addr(stage);
+        if constexpr (R == kAligned) {
+            if (lane == 0) bar_expect(bar, __popc(mask) * db + (ADD ? __popc(x.direct & mask) * gb : 0u));
+            __syncwarp();
+            if (on) copy_bulk(to, x.src, db, bar);
+            if (both) copy_bulk(to + kDout, x.dst, gb, bar);
+        } else {
+            const uintptr_t src = reinterpret_cast<uintptr_t>(x.src), dst = reinterpret_cast<uintptr_t>(x.dst);
+            Granules s = {}, d = {};
+            if (on) s = granules(src, db, reinterpret_cast<uintptr_t>(dout), dout_end);
+            if (both) d = granules(dst, gb, reinterpret_cast<uintptr_t>(dtable), dtable_end);
+            const uint32_t sn = (uint32_t)(s.last - s.first), dn = (uint32_t)(d.last - d.first);
+            const uint32_t all = __reduce_add_sync(0xffffffffu, sn + dn);
+            if (lane == 0) bar_expect(bar, all);
+            if (on) copy_ends<TD>(stage, s, src, db);
+            if (both) copy_ends<TG>(stage + kDout, d, dst, gb);
+            __syncwarp();
+            if (sn) copy_bulk(to + (uint32_t)(s.first - s.base), reinterpret_cast<const void *>(s.first), sn, bar);
+            if (dn) copy_bulk(to + kDout + (uint32_t)(d.first - d.base), reinterpret_cast<const void *>(d.first), dn, bar);
         }
     };
+    // where row r's slice begins in its stage
+    [[maybe_unused]] auto start_of = [&](const void *p, int r) -> uint32_t {
+        if (R != kAnywhere) return 0;
+        return __shfl_sync(0xffffffffu, (uint32_t)reinterpret_cast<uintptr_t>(p), r) & 15;
+    };
     uint32_t phases = 0; // parity of each barrier's phase
-    if (RING) {
-        if (lane < kStages / kBatch) bar_init(smem_addr(&s_bar[w][lane]));
-        asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-    }
+    if (lane < kStages / kBatch) bar_init(smem_addr(&s_bar[w][lane]));
+    asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
     Rows ahead;
     if (blockIdx.x < sums) {
         ahead = rows_of(blockIdx.x);
-        if (RING)
-            for (int r = 0; r < kStages; r += kBatch) fetch(ahead, r);
+        for (int r = 0; r < kStages; r += kBatch) fetch(ahead, r);
     }
-    for (int64_t it = blockIdx.x; it < sums; it += gridDim.x) {
+    for (uint32_t it = blockIdx.x; it < sums; it += gridDim.x) {
         const Rows cur = ahead;
         const int64_t tile = cur.tile;
         const int live = cur.live;
@@ -759,56 +814,37 @@ __device__ __forceinline__ void sum_items(const TD *__restrict__ dout, int64_t d
                 store_part(s_part(w), mine, acc);
             zero(acc);
         };
-        if constexpr (RING) {
-            for (int r0 = 0; r0 < live; r0 += kBatch) {
-                const int slot = r0 / kBatch % (kStages / kBatch);
-                if (!bar_wait(smem_addr(&s_bar[w][slot]), phases >> slot & 1) && d_status)
-                    atomicOr(d_status, AP_FLAG_CORRUPT);
-                phases ^= 1u << slot;
-                const uint8_t *at = ring + r0 % kStages * kStage;
-                Pack<TD, VE> v[kBatch][NG];
-                Pack<TG, VE> old[kBatch][NG];
+        for (int r0 = 0; r0 < live; r0 += kBatch) {
+            const int slot = r0 / kBatch % (kStages / kBatch);
+            if (!bar_wait(smem_addr(&s_bar[w][slot]), phases >> slot & 1) && d_status)
+                atomicOr(d_status, AP_FLAG_CORRUPT);
+            phases ^= 1u << slot;
+            const uint8_t *at = ring + r0 % kStages * kStage;
+            Pack<TD, VE> v[kBatch][NG];
+            Pack<TG, VE> old[kBatch][NG];
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
+            for (int u = 0; u < kBatch; ++u) {
+                const uint8_t *row = at + u * kStage;
+                const uint32_t from = start_of(cur.src, r0 + u);
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    v[u][g] = reinterpret_cast<const Pack<TD, VE> *>(row + from)[mine.at(g)];
+                if (ADD && (direct >> r0 >> u & 1)) {
+                    const uint32_t from2 = start_of(cur.dst, r0 + u);
 #pragma unroll
                     for (int g = 0; g < NG; ++g)
-                        v[u][g] = reinterpret_cast<const Pack<TD, VE> *>(at + u * kStage)[mine.at(g)];
-                    if (ADD && (direct >> r0 >> u & 1)) {
-#pragma unroll
-                        for (int g = 0; g < NG; ++g)
-                            old[u][g] = reinterpret_cast<const Pack<TG, VE> *>(at + u * kStage + kDoutBytes)[mine.at(g)];
-                    }
+                        old[u][g] = reinterpret_cast<const Pack<TG, VE> *>(row + kDout + from2)[mine.at(g)];
                 }
-                __syncwarp();
-                fetch(cur, r0 + kStages);
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u)
-                    if (r0 + u < live) take(r0 + u, v[u], old[u]);
             }
-            // the whole ring is free: the next item's first rows
-            if (more)
-                for (int r = 0; r < kStages; r += kBatch) fetch(ahead, r);
-        } else {
-            constexpr int U = 4;
-            for (int r0 = 0; r0 < live; r0 += U) {
-                Pack<TD, VE> v[U][NG];
-                Pack<TG, VE> old[U][NG];
+            __syncwarp();
+            fetch(cur, r0 + kStages);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    load_row(v[u], src_of(cur, (r0 + u) & 31), here, r0 + u < live);
-                }
-                if (ADD) {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        load_row(old[u], dst_of(cur, (r0 + u) & 31), here,
-                                 r0 + u < live && (direct >> (r0 + u) & 1));
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (r0 + u < live) take(r0 + u, v[u], old[u]);
-            }
+            for (int u = 0; u < kBatch; ++u)
+                if (r0 + u < live) take(r0 + u, v[u], old[u]);
         }
+        // the whole ring is free: the next item's first rows
+        if (more)
+            for (int r = 0; r < kStages; r += kBatch) fetch(ahead, r);
         uint32_t flags = 0;
         if (began) flags |= kHead;
         if (live > 0 && !(ends >> (live - 1) & 1)) { // the last run goes on
@@ -820,7 +856,7 @@ __device__ __forceinline__ void sum_items(const TD *__restrict__ dout, int64_t d
         __syncthreads();
         // runs that span warps: the warp in which one begins joins it, the last warp joins what entered the tile
         auto join_from = [&](int q) { // adds heads from warp q on; true if the run ends in this tile
-            for (; q < W; ++q) {
+            for (; q < kSumWarps; ++q) {
                 Pack<float, VE> p[NG];
                 load_part(p, s_part(q), mine);
                 add_row(acc, p);
@@ -838,26 +874,13 @@ __device__ __forceinline__ void sum_items(const TD *__restrict__ dout, int64_t d
                 store_part(partial + (2 * tile + 1) * part_ld, sl, acc);
             }
         }
-        if (w == W - 1 && (s_flags[0] & kHead)) {
+        if (w == kSumWarps - 1 && (s_flags[0] & kHead)) {
             zero(acc);
             (void)join_from(0);
             store_part(partial + 2 * tile * part_ld, sl, acc);
         }
         __syncthreads();
     }
-}
-
-template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
-__global__ void __launch_bounds__(kSumThreads, 2)
-    k_embed_sum(const TD *__restrict__ dout, int64_t dout_ld, const uint2 *__restrict__ sorted, int64_t T, int64_t V,
-                int H, float scale, int rows, TG *__restrict__ dtable, int64_t ld, float *__restrict__ partial,
-                int64_t part_ld, const void *__restrict__ ids, bool wide, int64_t pad, uint32_t *d_status)
-{
-    prefetch_inputs<TD, TG, ADD>(dout, dout_ld, ids, wide, T, V, pad, H, dtable, ld);
-    pdl_begin_after(); // the join's zeros need the sort complete
-    extern __shared__ __align__(16) uint8_t s_mem[];
-    sum_items<TD, TG, VE, NG, ADD, RING, kSumWarps>(dout, dout_ld, sorted, T, V, H, scale, rows, dtable, ld, partial,
-                                                    part_ld, s_mem, d_status);
 }
 
 // Zeros the rows of items [first, last) that no id names; an item is `rows`
@@ -943,40 +966,157 @@ __global__ void __launch_bounds__(kSumThreads)
     if (!ADD) fill_rows<TG, VE, kSumWarps>(ahead, fills, rows_per_fill, V, nstep, dtable, ld, seen_from);
 }
 
-// Up to kSmallTokens tokens in one launch: every block sorts them for itself,
-// then sums its slices of the columns (one tile, nothing to join elsewhere)
-// and zeros its share of the rows that no id names.  Half the launches and no
-// work space: 13 us of host time where the three launches above take 19.
+// Up to kSmallTokens tokens in one launch, without work space: every block
+// sorts all of them for itself in shared memory (up to kRankTokens by counting
+// the tokens before each, else by radix passes) and then adds up its share of
+// the runs over its slice of the columns: run q belongs to group q % groups.
+// A run is cut into pieces of kPiece rows, one warp each; the pieces of a
+// longer run meet in shared memory and are added in order.  Without an old
+// gradient the rows that no id names are shared out over all blocks.
 constexpr int64_t kSmallTokens = kClThreads;
-template <typename TD, typename TG, int VE, int NG, bool ADD>
+constexpr int kRankTokens = 256;
+constexpr int kPiece = 16;
+// pieces of runs longer than one piece: a run of n > 16 has at most 2 n / 17
+constexpr int kLongPieces = 2 * (int)kSmallTokens / (kPiece + 1) + 1;
+constexpr int kSmallCols = 128;
+
+template <typename TD, typename TG, int VE, bool ADD>
 __global__ void __launch_bounds__(kClThreads, 1)
     k_embed_small(const TD *__restrict__ dout, int64_t dout_ld, const void *__restrict__ ids, bool wide, int T,
-                  int64_t V, int64_t pad, int H, float scale, int passes, int bits, int rows, TG *__restrict__ dtable,
-                  int64_t ld, int rows_per_fill, uint32_t *d_status)
+                  int64_t V, int64_t pad, int H, float scale, int passes, int bits, int slices, int groups,
+                  TG *__restrict__ dtable, int64_t ld, int rows_per_fill, uint32_t *d_status)
 {
     pdl_begin();
+    constexpr int NG = kSmallCols / kWarp / VE;
     extern __shared__ __align__(16) uint8_t s_mem[];
     uint2 *sorted = reinterpret_cast<uint2 *>(s_mem);
-    sort_passes<1, false>(ids, wide, T, T, V, pad, passes, bits, sorted, blockIdx.x == 0 ? d_status : nullptr,
-                          [&](uint32_t at, uint2 pair, bool in) {
-                              if (in) sorted[at] = pair;
-                          });
+    float *s_part = reinterpret_cast<float *>(s_mem + kClThreads * sizeof(uint2)); // after the sort: [kLongPieces][128]
+    __shared__ uint32_t s_piece[kSmallTokens], s_count[kClWarps];
+    __shared__ int s_head[kClWarps];
+    const int lane = (int)lane_id(), wid = threadIdx.x / kWarp, tid = threadIdx.x;
+    const uint32_t none = (uint32_t)V;
+    const uint32_t key =
+        tid < T ? sort_key(ids, wide, tid, V, pad, blockIdx.x == 0 ? d_status : nullptr) : none;
+    if (key != none && tid % gridDim.x == blockIdx.x) { // its rows start towards L2 while the tokens are sorted
+        prefetch_l2(dout + tid * dout_ld, (int64_t)H * sizeof(TD));
+        if (ADD) prefetch_l2(dtable + key * ld, (int64_t)H * sizeof(TG));
+    }
+    if (T <= kRankTokens) {
+        uint32_t *s_key = s_piece; // (free until the pieces are listed)
+        if (tid < kRankTokens) s_key[tid] = key;
+        __syncthreads();
+        // four threads count a token's predecessors: smaller keys, and equal ones of lower tokens
+        const int t = tid / 4;
+        const uint32_t mine = s_key[t];
+        uint32_t rank = 0;
+        for (int c = tid & 3; c < T; c += 4) {
+            const uint32_t other = s_key[c];
+            rank += other < mine || (other == mine && c < t);
+        }
+        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+        if (t < T && (tid & 3) == 0) sorted[rank] = make_uint2(mine, (uint32_t)t);
+    } else {
+        sort_passes<1, false>(
+            T, T, passes, bits, sorted, [&](int) { return key; }, // (a thread's first token is its own)
+            [&](uint32_t at, uint2 pair, bool in) {
+                if (in) sorted[at] = pair;
+            });
+    }
     __syncthreads();
-    // the counts of the sort are no longer needed: the sums' shared memory
-    sum_items<TD, TG, VE, NG, ADD, false, kClWarps>(dout, dout_ld, sorted, T, V, H, scale, rows, dtable, ld, nullptr, 0,
-                                                    s_mem + kClThreads * sizeof(uint2), nullptr);
+    // the pieces of this block's runs: first token, and for the pieces of longer runs their place in s_part
+    const int group = blockIdx.x / slices;
+    const uint32_t k = tid < T ? sorted[tid].x : none;
+    const bool live = k != none;
+    const bool head = live && (tid == 0 || sorted[tid - 1].x != k);
+    const uint32_t heads = __ballot_sync(0xffffffffu, head);
+    if (lane == 0) {
+        s_head[wid] = heads ? wid * kWarp + 31 - __clz(heads) : -1;
+        s_count[wid] = __popc(heads);
+    }
+    __syncthreads();
+    int start = __reduce_max_sync(0xffffffffu, lane < wid ? s_head[lane] : -1);
+    int run = (int)__reduce_add_sync(0xffffffffu, lane < wid ? s_count[lane] : 0u);
+    const uint32_t upto = heads & (lanemask_lt() | 1u << lane);
+    if (upto) start = wid * kWarp + 31 - __clz(upto);
+    run += __popc(upto) - 1;
+    const bool piece = live && (tid - start) % kPiece == 0 && run % groups == group;
+    const bool part = piece && (tid != start || (tid + kPiece < T && sorted[tid + kPiece].x == k)); // of a longer run
+    const uint32_t pieces = __ballot_sync(0xffffffffu, piece), parts = __ballot_sync(0xffffffffu, part);
+    __syncthreads(); // s_count is read
+    if (lane == 0) s_count[wid] = __popc(pieces) | __popc(parts) << 16;
+    __syncthreads();
+    uint32_t at = __reduce_add_sync(0xffffffffu, lane < wid ? s_count[lane] : 0u);
+    const int count = (int)(__reduce_add_sync(0xffffffffu, s_count[lane]) & 0xffffu);
+    constexpr uint32_t kPart = 1u << 31, kFirst = 1u << 30;
+    if (piece)
+        s_piece[(at & 0xffffu) + __popc(pieces & lanemask_lt())] =
+            (uint32_t)tid | ((at >> 16) + __popc(parts & lanemask_lt())) << 16 | (part ? kPart : 0u) |
+            (tid == start ? kFirst : 0u);
+    __syncthreads();
+
+    const Slice<VE, NG> mine{lane, kSmallCols / VE};
+    if (group < groups) {
+        const int slice = blockIdx.x % slices;
+        const int col0 = slice * kSmallCols, cols = H - col0 < kSmallCols ? H - col0 : kSmallCols;
+        const Slice<VE, NG> here{lane, cols / VE};
+        for (int j = wid; j < count; j += kClWarps) {
+            const uint32_t info = s_piece[j];
+            const int i = (int)(info & 0xffffu);
+            const uint2 my = i + lane < T ? sorted[i + lane] : make_uint2(none, 0u);
+            const uint32_t id = __shfl_sync(0xffffffffu, my.x, 0);
+            const int n = __popc(__ballot_sync(0xffffffffu, lane < kPiece && my.x == id));
+            TG *row = dtable + id * ld + col0;
+            Pack<TG, VE> old[NG];
+            if (ADD) load_row(old, row, here, !(info & kPart));
+            float acc[NG][VE];
+            zero(acc);
+            constexpr int U = 8;
+            for (int r0 = 0; r0 < n; r0 += U) {
+                Pack<TD, VE> v[U][NG];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const uint32_t tok = __shfl_sync(0xffffffffu, my.y, r0 + u);
+                    load_row(v[u], dout + tok * dout_ld + col0, here, r0 + u < n);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (r0 + u < n) add_row(acc, v[u]);
+            }
+            if (info & kPart)
+                store_part(s_part + (info >> 16 & 0x3fff) * kSmallCols, mine, acc);
+            else
+                finish_row(row, here, acc, old, scale, ADD);
+        }
+        __syncthreads();
+        for (int j = wid; j < count; j += kClWarps) { // longer runs, by the warp of their first piece
+            const uint32_t info = s_piece[j];
+            if ((info & (kPart | kFirst)) != (kPart | kFirst)) continue;
+            TG *row = dtable + sorted[info & 0xffffu].x * ld + col0;
+            Pack<TG, VE> old[NG];
+            if (ADD) load_row(old, row, here);
+            float acc[NG][VE];
+            zero(acc);
+            for (int q = j; q < count && (q == j || (s_piece[q] & (kPart | kFirst)) == kPart); ++q) {
+                Pack<float, VE> p[NG];
+                load_part(p, s_part + (s_piece[q] >> 16 & 0x3fff) * kSmallCols, mine);
+                add_row(acc, p);
+            }
+            finish_row(row, here, acc, old, scale, ADD);
+        }
+    }
     if (ADD) return;
     auto seen_from = [&](int64_t r0) { // a lane looks for one row
-        const uint32_t key = (uint32_t)(r0 + lane_id());
+        const uint32_t want = (uint32_t)(r0 + lane);
         int lo = 0, hi = T;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if (sorted[mid].x < key)
+            if (sorted[mid].x < want)
                 lo = mid + 1;
             else
                 hi = mid;
         }
-        return __ballot_sync(0xffffffffu, lo < T && sorted[lo].x == key);
+        return __ballot_sync(0xffffffffu, lo < T && sorted[lo].x == want);
     };
     fill_rows<TG, VE, kClWarps>(0, (V + rows_per_fill - 1) / rows_per_fill, rows_per_fill, V, H / VE, dtable, ld,
                                 seen_from);
@@ -1004,11 +1144,7 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int32_t H)
     while (p.rows > 4 && T * pieces < kWantItems * p.rows * kSumWarps) p.rows /= 2;
     p.sum_tiles = (T + p.rows * kSumWarps - 1) / (p.rows * kSumWarps);
     p.part_ld = ((int64_t)H + 7) / 8 * 8;
-    if (T <= kSmallTokens) { // one tile, no work space
-        p.rows = T > 0 ? (int)((T + kClWarps - 1) / kClWarps) : 1;
-        p.sum_tiles = T > 0;
-        return p;
-    }
+    if (T <= kSmallTokens) return p; // no work space
     auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
     p.off_b = up(T * 8);
     p.off_hist = p.off_b + (p.tiles ? up(T * 8) : 0);
@@ -1127,10 +1263,13 @@ void embed_typed(const void *table, int64_t V, int64_t ld, int32_t tt, const voi
                  float scale, void *out, int64_t out_ld, int32_t ot, uint32_t *d_status, cudaStream_t st)
 {
     constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
+    constexpr int UA = 4; // vectors of a lane in flight (16384 x 2048: 13.3 us, with 2 of them 14.5, with 1 20.5)
     if (H % VE == 0 && vec_ok(table, ld, tt, VE) && vec_ok(out, out_ld, ot, VE))
-        launch_embed<TI, TO, VE, 2>(table, V, ld, ids, wide, T, H, scale, out, out_ld, d_status, st);
+        launch_embed<TI, TO, VE, UA>(table, V, ld, ids, wide, T, H, scale, out, out_ld, d_status, st);
+    else if (H % 2 == 0 && vec_ok(table, ld, tt, 2) && vec_ok(out, out_ld, ot, 2))
+        launch_embed<TI, TO, 2, 8>(table, V, ld, ids, wide, T, H, scale, out, out_ld, d_status, st);
     else
-        launch_embed<TI, TO, 1, 4>(table, V, ld, ids, wide, T, H, scale, out, out_ld, d_status, st);
+        launch_embed<TI, TO, 1, 16>(table, V, ld, ids, wide, T, H, scale, out, out_ld, d_status, st);
 }
 
 // What the sums kernels take besides their types.
@@ -1159,13 +1298,13 @@ int fill_rows_of(int64_t row_bytes)
     return rows;
 }
 
-template <typename TD, typename TG, int VE, int NG, bool ADD, bool RING>
+template <typename TD, typename TG, int VE, int NG, bool ADD, Route R>
 ap_status embed_sums(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
 {
     TG *dtable = static_cast<TG *>(a.dtable);
     const int slices = (a.H / VE + kWarp * NG - 1) / (kWarp * NG);
-    const auto kernel = k_embed_sum<TD, TG, VE, NG, ADD, RING>;
-    constexpr int smem = kSumSmem<TD, TG, VE, NG, ADD, RING>;
+    const auto kernel = k_embed_sum<TD, TG, VE, NG, ADD, R>;
+    constexpr int smem = kSumSmem<TD, TG, VE, NG, ADD, R>;
     static const cudaError_t attr = cudaFuncSetAttribute((const void *)kernel,
                                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (attr != cudaSuccess) return cuda_fail(attr, "embed_backward sum");
@@ -1173,8 +1312,8 @@ ap_status embed_sums(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
     const int64_t items = p.sum_tiles * slices;
     if (items > 0) {
         launch(kernel, (int)(items < resident ? items : resident), kSumThreads, smem, st,
-               static_cast<const TD *>(a.dout), a.dout_ld, a.sorted, a.T, a.V, a.H, a.scale, p.rows, dtable, a.ld,
-               a.partial, p.part_ld, a.ids, a.wide, a.pad, a.d_status);
+               static_cast<const TD *>(a.dout), a.dout_ld, a.sorted, a.T, a.V, a.H, a.scale, p.rows,
+               (uint32_t)slices, (uint32_t)items, dtable, a.ld, a.partial, p.part_ld, a.ids, a.wide, a.pad, a.d_status);
         AP_CHECK_LAUNCH("embed_backward sum launch");
     }
     if (!ADD || p.sum_tiles > 1) {
@@ -1189,26 +1328,29 @@ ap_status embed_sums(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
     return AP_OK;
 }
 
-template <typename TD, typename TG, int VE, int NG, bool ADD>
+template <typename TD, typename TG, int VE, bool ADD>
 ap_status embed_small(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
 {
-    const auto kernel = k_embed_small<TD, TG, VE, NG, ADD>;
-    constexpr size_t sums = kClThreads * sizeof(uint2) + (size_t)kClWarps * kWarp * VE * NG * 4;
-    constexpr size_t most = cluster_smem(1, kMaxDigitBits, 1) > sums ? cluster_smem(1, kMaxDigitBits, 1) : sums;
+    const auto kernel = k_embed_small<TD, TG, VE, ADD>;
+    constexpr size_t parts = kClThreads * sizeof(uint2) + (size_t)kLongPieces * kSmallCols * 4;
+    constexpr size_t most = cluster_smem(1, kMaxDigitBits, 1) > parts ? cluster_smem(1, kMaxDigitBits, 1) : parts;
     static const cudaError_t attr =
         cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (attr != cudaSuccess) return cuda_fail(attr, "embed_backward");
-    const size_t sort = cluster_smem(1, p.bits, 1);
+    // as many groups of runs as fill the SMs once, each of some 32 tokens at least
+    const int sms = sm_count();
+    const int64_t slices = (a.H + kSmallCols - 1) / kSmallCols;
+    int64_t groups = a.T > 32 ? (a.T + 31) / 32 : 1;
+    if (groups * slices > sms) groups = sms / slices > 0 ? sms / slices : 1;
     const int rows = fill_rows_of((int64_t)a.H * sizeof(TG));
-    int64_t grid = (a.H / VE + kWarp * NG - 1) / (kWarp * NG);
+    int64_t grid = groups * slices;
     if (!ADD) { // enough blocks for the zeros
         const int64_t fill = (a.V + (int64_t)rows * kClWarps - 1) / ((int64_t)rows * kClWarps);
-        if (fill > grid) grid = fill;
+        if (grid < (fill < sms ? fill : sms)) grid = fill < sms ? fill : sms;
     }
-    const int64_t resident = sm_count();
-    launch(kernel, (int)(grid < resident ? grid : resident), kClThreads, sort > sums ? sort : sums, st,
-           static_cast<const TD *>(a.dout), a.dout_ld, a.ids, a.wide, (int)a.T, a.V, a.pad, a.H, a.scale, p.passes,
-           p.bits, p.rows, static_cast<TG *>(a.dtable), a.ld, rows, a.d_status);
+    launch(kernel, (int)(grid > 0 ? grid : 1), kClThreads, most, st, static_cast<const TD *>(a.dout), a.dout_ld, a.ids,
+           a.wide, (int)a.T, a.V, a.pad, a.H, a.scale, p.passes, p.bits, (int)slices, (int)groups,
+           static_cast<TG *>(a.dtable), a.ld, rows, a.d_status);
     AP_CHECK_LAUNCH("embed_backward launch");
     return AP_OK;
 }
@@ -1216,18 +1358,24 @@ ap_status embed_small(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
 template <typename TD, typename TG>
 ap_status embed_backward_typed(const SumArgs &a, int32_t dt, int32_t gt, bool add, const EmbedPlan &p, cudaStream_t st)
 {
-    if (a.T <= kSmallTokens) { // narrow slices: few rows, many blocks
+    const bool even = a.H % 2 == 0 && vec_ok(a.dout, a.dout_ld, dt, 2) && vec_ok(a.dtable, a.ld, gt, 2);
+    if (a.T <= kSmallTokens) {
         if (a.H % 4 == 0 && vec_ok(a.dout, a.dout_ld, dt, 4) && vec_ok(a.dtable, a.ld, gt, 4))
-            return add ? embed_small<TD, TG, 4, 1, true>(a, p, st) : embed_small<TD, TG, 4, 1, false>(a, p, st);
-        return add ? embed_small<TD, TG, 1, 2, true>(a, p, st) : embed_small<TD, TG, 1, 2, false>(a, p, st);
+            return add ? embed_small<TD, TG, 4, true>(a, p, st) : embed_small<TD, TG, 4, false>(a, p, st);
+        if (even) return add ? embed_small<TD, TG, 2, true>(a, p, st) : embed_small<TD, TG, 2, false>(a, p, st);
+        return add ? embed_small<TD, TG, 1, true>(a, p, st) : embed_small<TD, TG, 1, false>(a, p, st);
     }
+    constexpr int N = kDoutBytes / kWarp / (int)sizeof(TD); // a lane's columns of a slice
     constexpr int VE = sizeof(TD) == 2 && sizeof(TG) == 2 ? 8 : 4;
-    constexpr int NG = sizeof(TD) == 2 && sizeof(TG) == 4 ? 2 : 1; // 512 bytes of dout a row and slice
     constexpr int V16 = sizeof(TD) == 2 || sizeof(TG) == 2 ? 8 : 4;
     if (a.H % V16 == 0 && vec_ok(a.dout, a.dout_ld, dt, V16) && vec_ok(a.dtable, a.ld, gt, V16))
-        return add ? embed_sums<TD, TG, VE, NG, true, true>(a, p, st)
-                   : embed_sums<TD, TG, VE, NG, false, true>(a, p, st);
-    return add ? embed_sums<TD, TG, 1, 4, true, false>(a, p, st) : embed_sums<TD, TG, 1, 4, false, false>(a, p, st);
+        return add ? embed_sums<TD, TG, VE, N / VE, true, kAligned>(a, p, st)
+                   : embed_sums<TD, TG, VE, N / VE, false, kAligned>(a, p, st);
+    if (even)
+        return add ? embed_sums<TD, TG, 2, N / 2, true, kAnywhere>(a, p, st)
+                   : embed_sums<TD, TG, 2, N / 2, false, kAnywhere>(a, p, st);
+    return add ? embed_sums<TD, TG, 1, N, true, kAnywhere>(a, p, st)
+               : embed_sums<TD, TG, 1, N, false, kAnywhere>(a, p, st);
 }
 
 bool embed_sizes_ok(int64_t T, int64_t V, int32_t H)

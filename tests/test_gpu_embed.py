@@ -149,6 +149,17 @@ def test_runs_that_end_at_and_cross_tiles(lengths):
         check_backward(ids, 3 * len(lengths) + 4, 37, "f32", "f32", accumulate)
 
 
+@pytest.mark.parametrize("dout,grad", [("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
+@pytest.mark.parametrize("H,extra,shift", [(1, 0, 0), (3, 0, 1), (37, 0, 0), (130, 2, 0), (257, 0, 1), (264, 0, 2),
+                                           (514, 0, 0), (1001, 3, 0), (2056, 0, 0)])
+def test_many_tokens_with_rows_that_start_anywhere(H, extra, shift, dout, grad):
+    """Long enough for the staged sums: rows on and off 16-byte boundaries, buffers that begin and end inside one."""
+    ids = zipf_ids(H, 3000, 700)
+    ids[::7] = 699
+    for accumulate in (True, False):
+        check_backward(ids, 700, H, dout, grad, accumulate, 5, extra, shift)
+
+
 @pytest.mark.parametrize("accumulate", [True, False])
 def test_padding_and_bad_ids(accumulate):
     T, V = 700, 60
