@@ -120,27 +120,37 @@ def route_balance(logits: torch.Tensor, k: int, coef: float = 1.0, group_tokens:
     expert), ``prob`` ([G, E] float32, mean softmax probability), ``slope``
     ([G, E] float32, d loss / d p, for ``route_backward``), ``loss`` (float32
     scalar tensor, ``coef`` x the mean over groups of E sum_e share_e prob_e)
-    and ``scratch``.  ``mask`` ([T] bool or uint8): tokens that count.  Pass
+    and, for many tokens, ``scratch``.  ``mask`` ([T] bool or uint8): tokens that count.  Pass
     ``out`` (such a dict, whole or in part) to reuse buffers."""
     _need(logits, torch.float32, "logits")
     T, E = logits.shape
     m = _mask(mask, T)
     G = _groups(T, group_tokens)
     sb = route_balance_scratch_bytes(T, E, group_tokens)
-    o = dict(out) if out is not None else {}
-    pairs, sums = (T, k), (G, E)
-    for name, shape, dtype in (("idx", pairs, torch.int32), ("w", pairs, torch.float32), ("counts", sums, torch.int32),
-                               ("prob", sums, torch.float32), ("slope", sums, torch.float32),
-                               ("loss", (), torch.float32)):
-        if name in o:
-            _need_shape(o[name], dtype, shape, name)
-        else:
-            o[name] = _empty(shape, dtype, logits.device, stream)
-    if "scratch" not in o or o["scratch"].numel() < sb:
-        o["scratch"] = _empty(sb, torch.uint8, logits.device, stream)
-    check(lib().ap_route_balance(_p(logits), T, E, k, group_tokens, m, coef, _p(o["idx"]), _p(o["w"]), _p(o["counts"]),
-                                 _p(o["prob"]), _p(o["slope"]), _p(o["loss"]), _p(o["scratch"]),
-                                 o["scratch"].numel(), _stream(stream)), "route_balance")
+    pairs, sums, dev = (T, k), (G, E), logits.device
+    if out is None and stream is None:
+        o = {"idx": torch.empty(pairs, dtype=torch.int32, device=dev),
+             "w": torch.empty(pairs, dtype=torch.float32, device=dev),
+             "counts": torch.empty(sums, dtype=torch.int32, device=dev),
+             "prob": torch.empty(sums, dtype=torch.float32, device=dev),
+             "slope": torch.empty(sums, dtype=torch.float32, device=dev),
+             "loss": torch.empty((), dtype=torch.float32, device=dev)}
+    else:
+        o = dict(out) if out is not None else {}
+        for name, shape, dtype in (("idx", pairs, torch.int32), ("w", pairs, torch.float32),
+                                   ("counts", sums, torch.int32), ("prob", sums, torch.float32),
+                                   ("slope", sums, torch.float32), ("loss", (), torch.float32)):
+            if name in o:
+                _need_shape(o[name], dtype, shape, name)
+            else:
+                o[name] = _empty(shape, dtype, dev, stream)
+    scratch = o.get("scratch")
+    if sb and (scratch is None or scratch.numel() < sb):
+        scratch = o["scratch"] = _empty(sb, torch.uint8, dev, stream)
+    check(lib().ap_route_balance(logits.data_ptr(), T, E, k, group_tokens, m, coef, o["idx"].data_ptr(),
+                                 o["w"].data_ptr(), o["counts"].data_ptr(), o["prob"].data_ptr(),
+                                 o["slope"].data_ptr(), o["loss"].data_ptr(), _p(scratch),
+                                 scratch.numel() if scratch is not None else 0, _stream(stream)), "route_balance")
     return o
 
 

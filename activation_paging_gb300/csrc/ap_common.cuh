@@ -149,6 +149,35 @@ __device__ __forceinline__ unsigned lanemask_lt()
     return m;
 }
 
+// ---- thread-block clusters ---------------------------------------------------
+// Barrier of the cluster: what its blocks wrote before is visible after.  The
+// first one a kernel waits for also says that every block has started, which
+// must be so before its shared memory is touched.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync()
+{
+    cluster_arrive();
+    cluster_wait();
+}
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// Address of the same shared variable in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint2 v)
+{
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+
+
 // Streaming (evict-first) global loads/stores for data touched once.
 __device__ __forceinline__ int4 ld_stream(const int4 *p) { return __ldcs(p); }
 __device__ __forceinline__ void st_stream(int4 *p, int4 v) { __stcs(p, v); }

@@ -37,31 +37,6 @@ struct BalancePlan {
     int64_t off_n, off_lp, off_p, bytes;
 };
 
-// The split and the layout of the work space: one row of E sums and counts and
-// one token count per block, one loss term per kFinCols experts of a group, and the
-// counter of finished blocks of the second kernel.
-BalancePlan balance_plan(int64_t T, int32_t E, int64_t group_tokens)
-{
-    BalancePlan p = {};
-    p.S = group_tokens > 0 && group_tokens < T ? group_tokens : (T > 0 ? T : 1);
-    p.G = (T + p.S - 1) / p.S;
-    p.blocks = 1;
-    if (p.G > 0) {
-        const int64_t warps = bal_warps(E);
-        const int64_t most = (p.S + warps - 1) / warps;
-        p.blocks = kBalBlocks / p.G;
-        if (p.blocks > most) p.blocks = most;
-        if (p.blocks < 1) p.blocks = 1;
-    }
-    auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
-    const int64_t rows = p.G * p.blocks;
-    p.off_n = 256;
-    p.off_lp = p.off_n + up(rows * 4);
-    p.off_p = p.off_lp + up(p.G * ((E + kFinCols - 1) / kFinCols) * 4);
-    p.bytes = p.off_p + up(rows * E * 8);
-    return p;
-}
-
 template <int VEC> struct Floats;
 template <> struct Floats<4> { using T = float4; };
 template <> struct Floats<1> { using T = float; };
@@ -75,37 +50,20 @@ __device__ __forceinline__ float exp_neg(float x)
     return y;
 }
 
-// Lane l holds the vectors l, l + 32, ... of VEC experts each (N of them).
-template <int VEC, int N, int W>
-__global__ void __launch_bounds__(W *kWarp)
-    k_route_balance(const float *__restrict__ logits, int64_t T, int E, int k, int64_t S, int blocks,
-                    const uint8_t *__restrict__ mask, int32_t *__restrict__ idx, float *__restrict__ w,
-                    int32_t *__restrict__ part_n, float2 *__restrict__ part, uint32_t *done)
+// Routes the tokens t, t + step, ... below t_end of one group and adds the
+// softmax rows of those that count to acc, their pairs to s_cnt; returns how
+// many counted.  Lane l holds the vectors l, l + 32, ... of VEC experts each
+// (N of them).
+template <int VEC, int N>
+__device__ __forceinline__ int route_tokens(const float *__restrict__ logits, int64_t t, int64_t t_end, int64_t step,
+                                            int E, int k, const uint8_t *__restrict__ mask, int32_t *__restrict__ idx,
+                                            float *__restrict__ w, TopkSlots &slots, int *s_cnt, float (&acc)[N][VEC])
 {
-    pdl_begin();
     using Vec = typename Floats<VEC>::T;
-    extern __shared__ __align__(16) float s_mem[];
-    float *s_sum = s_mem;                                // [W][E]
-    int *s_cnt = reinterpret_cast<int *>(s_mem + W * E); // [E]
-    __shared__ __align__(16) TopkSlots s_slots[W];
-    __shared__ int s_n;
-    const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *done = 0;
-    if (threadIdx.x == 0) s_n = 0;
-    for (int e = threadIdx.x; e < E; e += W * kWarp) s_cnt[e] = 0;
-    __syncthreads();
-
+    const int lane = (int)lane_id();
     const int nvec = E / VEC;
-    const int64_t g = blockIdx.x / blocks;
-    const int b = (int)(blockIdx.x - g * blocks);
-    const int64_t t_end = (g + 1) * S < T ? (g + 1) * S : T;
-    float acc[N][VEC];
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) acc[i][c] = 0.f;
     int n = 0;
-    for (int64_t t = g * S + (int64_t)b * W + wid; t < t_end; t += (int64_t)blocks * W) {
+    for (; t < t_end; t += step) {
         const Vec *row = reinterpret_cast<const Vec *>(logits + t * E);
         float v[N][VEC];
 #pragma unroll
@@ -120,7 +78,7 @@ __global__ void __launch_bounds__(W *kWarp)
         const bool counts = !mask || mask[t];
         int e;
         float wt, top;
-        select_token_slots<VEC, N>(v, E, k, lane, s_slots[wid], &e, &wt, &top);
+        select_token_slots<VEC, N>(v, E, k, lane, slots, &e, &wt, &top);
         const bool some = top != -INFINITY; // warp-uniform
         if (lane < k) {
             idx[t * k + lane] = e;
@@ -146,14 +104,58 @@ __global__ void __launch_bounds__(W *kWarp)
             ++n;
         }
     }
+    return n;
+}
+
+// Zero sums, counts and token count; then, after the tokens, the warp's sums
+// into its row of s_sum.
+template <int VEC, int N> __device__ __forceinline__ void zero_sums(float (&acc)[N][VEC])
+{
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        if (lane + kWarp * i < nvec) {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) acc[i][c] = 0.f;
+}
+template <int VEC, int N>
+__device__ __forceinline__ void store_sums(float *row, const float (&acc)[N][VEC], int E)
+{
+    using Vec = typename Floats<VEC>::T;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if ((int)lane_id() + kWarp * i < E / VEC) {
             Vec x;
             memcpy(&x, acc[i], sizeof(Vec));
-            reinterpret_cast<Vec *>(s_sum + wid * E)[lane + kWarp * i] = x;
+            reinterpret_cast<Vec *>(row)[lane_id() + kWarp * i] = x;
         }
-    if (lane == 0 && n) atomicAdd(&s_n, n);
+}
+
+template <int VEC, int N, int W>
+__global__ void __launch_bounds__(W *kWarp)
+    k_route_balance(const float *__restrict__ logits, int64_t T, int E, int k, int64_t S, int blocks,
+                    const uint8_t *__restrict__ mask, int32_t *__restrict__ idx, float *__restrict__ w,
+                    int32_t *__restrict__ part_n, float2 *__restrict__ part, uint32_t *done)
+{
+    pdl_begin();
+    extern __shared__ __align__(16) float s_mem[];
+    float *s_sum = s_mem;                                // [W][E]
+    int *s_cnt = reinterpret_cast<int *>(s_mem + W * E); // [E]
+    __shared__ __align__(16) TopkSlots s_slots[W];
+    __shared__ int s_n;
+    const int wid = threadIdx.x / kWarp;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *done = 0;
+    if (threadIdx.x == 0) s_n = 0;
+    for (int e = threadIdx.x; e < E; e += W * kWarp) s_cnt[e] = 0;
+    __syncthreads();
+
+    const int64_t g = blockIdx.x / blocks;
+    const int b = (int)(blockIdx.x - g * blocks);
+    const int64_t t_end = (g + 1) * S < T ? (g + 1) * S : T;
+    float acc[N][VEC];
+    zero_sums(acc);
+    const int n = route_tokens<VEC, N>(logits, g * S + (int64_t)b * W + wid, t_end, (int64_t)blocks * W, E, k, mask, idx,
+                                       w, s_slots[wid], s_cnt, acc);
+    store_sums(s_sum + wid * E, acc, E);
+    if (lane_id() == 0 && n) atomicAdd(&s_n, n);
     __syncthreads();
     const int64_t at = (int64_t)blockIdx.x * E;
     for (int e = threadIdx.x; e < E; e += W * kWarp) {
@@ -163,6 +165,135 @@ __global__ void __launch_bounds__(W *kWarp)
         part[at + e] = make_float2(sum, __int_as_float(s_cnt[e]));
     }
     if (threadIdx.x == 0) part_n[blockIdx.x] = s_n;
+}
+
+// What one expert of a group comes to: its row entries, and its loss term.
+__device__ __forceinline__ float balance_entry(float sum, int cnt, int n, int E, int k, int64_t G, float coef,
+                                               int32_t *counts, float *prob, float *slope)
+{
+    const float nf = (float)(n > 0 ? n : 1);
+    const float sl = coef * (float)E / ((float)G * (float)k) * (float)cnt / (nf * nf);
+    *counts = cnt;
+    *prob = __fdiv_rn(sum, nf);
+    *slope = sl;
+    return sl * sum;
+}
+
+// Few tokens: one launch, no work space.  One cluster takes all groups: with
+// at most as many groups as blocks, a group has `per` blocks, whose sums go to
+// its first block's shared memory; with more, a block takes every gridDim-th
+// group.  Loss terms are added in expert, group and block order.
+constexpr int kClusterBlocks = 8; // the largest portable cluster
+// 8 SMs route 1000 tokens of 128 experts in 15 us, all of them in 8 us, but the
+// second launch and the work space cost 6 us of host time; 800 tokens of 1000
+// experts took 37 us.
+constexpr int64_t kClusterTokens = 1024, kClusterLogits = 1 << 18;
+bool one_cluster(int64_t T, int32_t E) { return T <= kClusterTokens && T * E <= kClusterLogits; }
+template <int VEC, int N, int W>
+__global__ void __launch_bounds__(W *kWarp)
+    k_balance_cluster(const float *__restrict__ logits, int T, int E, int k, int S, int G, int per,
+                      const uint8_t *__restrict__ mask, float coef, int32_t *__restrict__ idx, float *__restrict__ w,
+                      int32_t *__restrict__ counts, float *__restrict__ prob, float *__restrict__ slope,
+                      float *__restrict__ loss)
+{
+    cluster_arrive();
+    pdl_begin();
+    extern __shared__ __align__(16) float s_mem[];
+    float *s_sum = s_mem;                                                            // [W][E]
+    int *s_cnt = reinterpret_cast<int *>(s_mem + W * E);                             // [E]
+    float2 *s_part = reinterpret_cast<float2 *>(s_mem + (W + 1) * E + ((W + 1) * E & 1)); // [per][E] of the group's blocks
+    __shared__ __align__(16) TopkSlots s_slots[W];
+    __shared__ int s_n, s_ns[kClusterBlocks];
+    __shared__ float s_term[W], s_loss[kClusterBlocks];
+    const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
+    const int me = blockIdx.x, first = me / per * per; // the grid is one cluster
+    float block_loss = 0.f;                            // (of thread 0)
+    auto finish = [&](int g, int parts) { // the group's entries from the sums of its blocks, all in s_part
+        int n = 0;
+        for (int r = 0; r < parts; ++r) n += s_ns[r];
+        float term = 0.f;
+        for (int e = threadIdx.x; e < E; e += W * kWarp) {
+            float sum = 0.f;
+            int cnt = 0;
+            for (int r = 0; r < parts; ++r) {
+                sum += s_part[r * E + e].x;
+                cnt += __float_as_int(s_part[r * E + e].y);
+            }
+            const int64_t at = (int64_t)g * E + e;
+            term += balance_entry(sum, cnt, n, E, k, G, coef, counts + at, prob + at, slope + at);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xffffffffu, term, off);
+        if (lane == 0) s_term[wid] = term;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int q = 0; q < W; ++q) block_loss += s_term[q];
+    };
+    cluster_wait(); // all blocks have started: their shared memory may be written
+    for (int g = me / per; g < G; g += gridDim.x / per) {
+        if (threadIdx.x == 0) s_n = 0;
+        for (int e = threadIdx.x; e < E; e += W * kWarp) s_cnt[e] = 0;
+        __syncthreads();
+        const int64_t t_end = (int64_t)(g + 1) * S < T ? (int64_t)(g + 1) * S : T;
+        float acc[N][VEC];
+        zero_sums(acc);
+        const int n = route_tokens<VEC, N>(logits, (int64_t)g * S + (me - first) * W + wid, t_end, (int64_t)per * W, E, k,
+                                           mask, idx, w, s_slots[wid], s_cnt, acc);
+        store_sums(s_sum + wid * E, acc, E);
+        if (lane == 0 && n) atomicAdd(&s_n, n);
+        __syncthreads();
+        for (int e = threadIdx.x; e < E; e += W * kWarp) {
+            float sum = 0.f;
+#pragma unroll
+            for (int q = 0; q < W; ++q) sum += s_sum[q * E + e];
+            cluster_store(cluster_addr(smem_addr(&s_part[(me - first) * E + e]), first),
+                          make_uint2(__float_as_uint(sum), (uint32_t)s_cnt[e]));
+        }
+        if (threadIdx.x == 0) cluster_store(cluster_addr(smem_addr(&s_ns[me - first]), first), (uint32_t)s_n);
+        if (per == 1) {
+            __syncthreads();
+            finish(g, 1);
+            __syncthreads();
+        }
+    }
+    if (per > 1) {
+        cluster_sync();
+        if (me == first && me / per < G) finish(me / per, per);
+    }
+    if (threadIdx.x == 0)
+        cluster_store(cluster_addr(smem_addr(&s_loss[me]), 0), __float_as_uint(block_loss));
+    cluster_sync(); // (no block's shared memory is touched after this)
+    if (me == 0 && threadIdx.x == 0) {
+        float total = 0.f;
+        for (unsigned r = 0; r < gridDim.x; ++r) total += s_loss[r];
+        *loss = total;
+    }
+}
+
+// The split and the layout of the work space: one row of E sums and counts and
+// one token count per block, one loss term per kFinCols experts of a group, and the
+// counter of finished blocks of the second kernel.
+BalancePlan balance_plan(int64_t T, int32_t E, int64_t group_tokens)
+{
+    BalancePlan p = {};
+    p.S = group_tokens > 0 && group_tokens < T ? group_tokens : (T > 0 ? T : 1);
+    p.G = (T + p.S - 1) / p.S;
+    p.blocks = 1;
+    if (p.G > 0) {
+        const int64_t warps = bal_warps(E);
+        const int64_t most = (p.S + warps - 1) / warps;
+        p.blocks = kBalBlocks / p.G;
+        if (p.blocks > most) p.blocks = most;
+        if (p.blocks < 1) p.blocks = 1;
+    }
+    if (one_cluster(T, E)) return p; // no work space
+    auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+    const int64_t rows = p.G * p.blocks;
+    p.off_n = 256;
+    p.off_lp = p.off_n + up(rows * 4);
+    p.off_p = p.off_lp + up(p.G * ((E + kFinCols - 1) / kFinCols) * 4);
+    p.bytes = p.off_p + up(rows * E * 8);
+    return p;
 }
 
 // One block per group and kFinCols experts.  Thread (r, c) adds rows r, r + 128,
@@ -221,14 +352,10 @@ __global__ void __launch_bounds__(kFinThreads)
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         if (lane == 0) {
-            const float nf = (float)(s_n > 0 ? s_n : 1);
-            const float sl = coef * (float)E / ((float)G * (float)k) * (float)cnt / (nf * nf);
-            if (col0 + wid < E) {
-                counts[g * E + col0 + wid] = cnt;
-                prob[g * E + col0 + wid] = __fdiv_rn(sum, nf);
-                slope[g * E + col0 + wid] = sl;
-            }
-            s_term[wid] = col0 + wid < E ? sl * sum : 0.f;
+            const int64_t at = g * E + col0 + wid;
+            s_term[wid] = col0 + wid < E
+                              ? balance_entry(sum, cnt, s_n, E, k, G, coef, counts + at, prob + at, slope + at)
+                              : 0.f;
         }
     }
     __syncthreads();
@@ -380,6 +507,27 @@ __global__ void __launch_bounds__(kBalThreads)
     }
 }
 
+template <int VEC, int N, int W>
+ap_status launch_balance_cluster(const float *logits, int T, int E, int k, int S, int G, const uint8_t *mask, float coef,
+                                 int32_t *idx, float *w, int32_t *counts, float *prob, float *slope, float *loss,
+                                 cudaStream_t st)
+{
+    const auto kernel = k_balance_cluster<VEC, N, W>;
+    constexpr int kMaxE = VEC * N * kWarp;
+    constexpr auto smem_of = [](int e, int per) { return (size_t)((W + 1) * e + 1 + 2 * per * e) * 4; };
+    // one token a warp, in blocks of a portable cluster, while the groups and the warps want them
+    int blocks = 1;
+    while (blocks < kClusterBlocks && (blocks * W < T || blocks < G)) blocks *= 2;
+    const int per = G <= blocks ? blocks / G : 1;
+    static const cudaError_t attr = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                         (int)smem_of(kMaxE, kClusterBlocks));
+    if (attr != cudaSuccess) return cuda_fail(attr, "route_balance");
+    launch_cluster(kernel, blocks, W * kWarp, smem_of(E, per), blocks, st, logits, T, E, k, S, G, per, mask, coef, idx,
+                   w, counts, prob, slope, loss);
+    AP_CHECK_LAUNCH("route_balance launch");
+    return AP_OK;
+}
+
 template <int VEC, int N>
 void launch_route_backward(const float *logits, int64_t T, int E, int k, const int32_t *idx, const float *w,
                            const float *dw, const float *slope, const float *dloss, int64_t S, const uint8_t *mask,
@@ -427,13 +575,33 @@ extern "C" ap_status ap_route_balance(const float *logits, int64_t T, int32_t E,
         AP_CHECK_LAUNCH("route_balance launch");
         return AP_OK;
     }
-    if (!logits || !idx || !w || !counts || !prob || !slope || !scratch)
-        return fail(AP_EINVAL, "route_balance: NULL pointer");
     const BalancePlan p = balance_plan(T, E, group_tokens);
+    if (!logits || !idx || !w || !counts || !prob || !slope || (p.bytes > 0 && !scratch))
+        return fail(AP_EINVAL, "route_balance: NULL pointer");
     if (reinterpret_cast<uintptr_t>(scratch) & 15) return fail(AP_EINVAL, "route_balance: scratch not 16-byte aligned");
     if (scratch_bytes < p.bytes)
         return fail(AP_EINVAL, "route_balance: scratch of %lld bytes, %lld needed", (long long)scratch_bytes,
                     (long long)p.bytes);
+    // vectors where every lane gets one (fewer lanes with experts leave no bound from the lanes' maxima)
+    const bool vec = E >= 128 && E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
+    if (one_cluster(T, E)) {
+#define AP_BALANCE(VEC, N, W)                                                                                         \
+    launch_balance_cluster<VEC, N, W>(logits, (int)T, E, k, (int)p.S, (int)p.G, mask, coef, idx, w, counts, prob, slope, \
+                                      loss, st)
+        if (vec) {
+            if (E <= 128) return AP_BALANCE(4, 1, 16);
+            if (E <= 256) return AP_BALANCE(4, 2, 16);
+            if (E <= 512) return AP_BALANCE(4, 4, 8);
+            return AP_BALANCE(4, 8, 8);
+        }
+        if (E <= 32) return AP_BALANCE(1, 1, 16);
+        if (E <= 64) return AP_BALANCE(1, 2, 16);
+        if (E <= 128) return AP_BALANCE(1, 4, 16);
+        if (E <= 256) return AP_BALANCE(1, 8, 16);
+        if (E <= 512) return AP_BALANCE(1, 16, 8);
+        return AP_BALANCE(1, 32, 8);
+#undef AP_BALANCE
+    }
     const int64_t pieces = (E + kFinCols - 1) / kFinCols;
     if (p.G * p.blocks > INT32_MAX || p.G * pieces > INT32_MAX)
         return fail(AP_EINVAL, "route_balance: %lld groups of %d experts are more than one launch takes",
@@ -450,8 +618,7 @@ extern "C" ap_status ap_route_balance(const float *logits, int64_t T, int32_t E,
         launch(kernel, grid, warps * kWarp, smem, st, logits, T, E, k, p.S, (int)p.blocks, mask, idx, w, part_n, part,
                done);
     };
-    // vectors where every lane gets one (fewer lanes with experts leave no bound from the lanes' maxima)
-    if (E >= 128 && E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0) {
+    if (vec) {
         if (E <= 128)
             go(k_route_balance<4, 1, 16>);
         else if (E <= 256)

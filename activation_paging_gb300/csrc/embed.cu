@@ -188,27 +188,6 @@ constexpr int kClItemsMax = 8;
 constexpr int kClBlocksMax = 16; // 8 is the largest portable cluster, and what is used where 16 do not fit
 constexpr int64_t kClusterMax = (int64_t)kClBlocksMax * kClThreads * kClItemsMax;
 
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// Address of the same shared variable in block `rank` of the cluster.
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t rank)
-{
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
-    return a;
-}
-__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t v)
-{
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void cluster_store(uint32_t addr, uint2 v)
-{
-    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
-}
-
 // Dynamic shared memory: the block's tokens, the warps' counts, the blocks' totals.
 constexpr size_t cluster_smem(int items, int bits, int blocks)
 {
@@ -219,7 +198,8 @@ constexpr size_t cluster_smem(int items, int bits, int blocks)
 // the grid.  smem: the block's tokens, the warps' counts, the blocks' totals
 // (cluster_smem bytes).  key_of(t) gives token t's key, out(at, pair, in) takes
 // every sorted token (all lanes call it); no block touches another's memory
-// after the barrier that precedes it.
+// after the barrier that precedes it.  CLUSTER: the caller has arrived at the
+// cluster's barrier once.
 template <int ITEMS, bool CLUSTER, typename Key, typename Out>
 __device__ __forceinline__ void sort_passes(int T, int per, int passes, int bits, uint2 *s_pairs, Key key_of, Out out)
 {
@@ -273,6 +253,7 @@ __device__ __forceinline__ void sort_passes(int T, int per, int passes, int bits
             for (int q = 0; q < each; ++q) sum += cnt2[(group * each + q) * D2 + pair_of];
             s_group[group * D2 + pair_of] = sum;
         }
+        if (CLUSTER && pass == 0) cluster_wait(); // all blocks have started (the caller's arrive)
         __syncthreads();
         if (group < groups) {
             uint32_t base = 0;
@@ -343,6 +324,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
     k_sort_cluster(const void *__restrict__ ids, bool wide, int T, int per, int64_t V, int64_t pad, int passes,
                    int bits, uint2 *__restrict__ sorted, uint32_t *__restrict__ seen, uint32_t *d_status)
 {
+    cluster_arrive();
     pdl_begin_after(); // the sums kernel reads ids and rows ahead of its own wait
     extern __shared__ __align__(16) uint8_t s_mem[];
     if (seen) // cleared before the first barrier of the cluster, set in the last pass

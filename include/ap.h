@@ -258,7 +258,8 @@ ap_status ap_dispatch_backward(const void *dxd, int64_t rows, int32_t H,
  *   counts  [G, E] int32, prob, slope [G, E] float32 (device, written)
  *   loss    [1] float32 (device, written)
  *   scratch device work space of ap_route_balance_scratch_bytes() bytes,
- *           16-byte aligned; its contents need no initialisation
+ *           16-byte aligned; its contents need no initialisation.  Few tokens
+ *           need 0 bytes (NULL)
  * T = 0 writes loss = 0 (G = 0).  Limits: as ap_route_topk, group_tokens >= 0.
  * ========================================================================== */
 ap_status ap_route_balance_scratch_bytes(int64_t T, int32_t E, int64_t group_tokens, int64_t *bytes);
