@@ -63,8 +63,11 @@ __device__ __forceinline__ int route_tokens(const float *__restrict__ logits, in
     const int lane = (int)lane_id();
     const int nvec = E / VEC;
     int n = 0;
-    for (; t < t_end; t += step) {
-        const Vec *row = reinterpret_cast<const Vec *>(logits + t * E);
+    const float *next = logits + t * E;
+    idx += t * k + lane;
+    w += t * k + lane;
+    for (; t < t_end; t += step, next += step * E, idx += step * k, w += step * k) {
+        const Vec *row = reinterpret_cast<const Vec *>(next);
         float v[N][VEC];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -81,8 +84,8 @@ __device__ __forceinline__ int route_tokens(const float *__restrict__ logits, in
         select_token_slots<VEC, N>(v, E, k, lane, slots, &e, &wt, &top);
         const bool some = top != -INFINITY; // warp-uniform
         if (lane < k) {
-            idx[t * k + lane] = e;
-            w[t * k + lane] = some ? wt : 0.f;
+            *idx = e;
+            *w = some ? wt : 0.f;
         }
         if (some && counts) {
             float sum = 0.f;
@@ -430,7 +433,7 @@ __global__ void __launch_bounds__(kBalThreads)
             }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const V *srow = reinterpret_cast<const V *>(slope + t / S * E);
+            const V *srow = reinterpret_cast<const V *>(slope + (S < T ? (uint32_t)t / (uint32_t)S : 0u) * (int64_t)E);
             float sl[N][VEC], sum = 0.f, dot = 0.f;
             const bool some = top != -INFINITY;
 #pragma unroll
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(kBalThreads)
                 }
 #pragma unroll
                 for (int c = 0; c < VEC; ++c) {
-                    d[i][c] = some ? expf(d[i][c] - top) : 0.f;
+                    d[i][c] = some ? exp_neg(d[i][c] - top) : 0.f;
                     sum += d[i][c];
                     dot += d[i][c] * sl[i][c];
                 }
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(kBalThreads)
                 sum += __shfl_xor_sync(0xffffffffu, sum, off);
                 dot += __shfl_xor_sync(0xffffffffu, dot, off);
             }
-            const float inv = some ? __fdiv_rn(1.0f, sum) : 0.f;
+            const float inv = some ? __frcp_rn(sum) : 0.f;
             const float mean = dot * inv;
 #pragma unroll
             for (int i = 0; i < N; ++i)

@@ -101,12 +101,10 @@ __device__ __forceinline__ float reduce_max(float v)
     return m;
 }
 
-// Shared memory of one warp for select_token_slots.
+// Shared memory of one warp for select_token_slots: (logit, id) pairs.
 struct TopkSlots {
-    float val[kWarp + 4];
-    int id[kWarp];
-    float sel_val[kWarp];
-    int sel_id[kWarp];
+    float2 cand[kWarp + 2];
+    float2 sel[kWarp];
 };
 
 // The same selection in about half the instructions for rows of 128 and more
@@ -129,19 +127,23 @@ __device__ __forceinline__ void select_token_slots(const float (&v)[N][VEC], int
         for (int c = 0; c < VEC; ++c) cur = fmaxf(cur, v[i][c]);
     const float first = reduce_max(cur);
     float least = first;
+#pragma unroll 4
     for (int j = 1; j < k; ++j) {
         cur = cur == least ? -INFINITY : cur;
         least = reduce_max(cur);
     }
-    uint32_t has[N][VEC];
-    int n = 0;
+    int own = 0; // of this lane, then with those of the lanes below
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-            has[i][c] = __ballot_sync(0xffffffffu, v[i][c] >= least);
-            n += __popc(has[i][c]);
-        }
+        for (int c = 0; c < VEC; ++c) own += v[i][c] >= least;
+    int upto = own;
+#pragma unroll
+    for (int off = 1; off < kWarp; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += o;
+    }
+    const int n = __shfl_sync(0xffffffffu, upto, kWarp - 1);
     if (least == -INFINITY || n < k || n > kWarp) { // warp-uniform
         uint32_t key[N * VEC];
         int ex[N * VEC];
@@ -156,41 +158,35 @@ __device__ __forceinline__ void select_token_slots(const float (&v)[N][VEC], int
         select_token<N * VEC>(key, ex, k, lane, e, wt, top);
         return;
     }
-    int at = 0;
+    float2 *at = s.cand + (upto - own);
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-            if (v[i][c] >= least) {
-                const int to = at + __popc(has[i][c] & lanemask_lt());
-                s.val[to] = v[i][c];
-                s.id[to] = (lane + kWarp * i) * VEC + c;
-            }
-            at += __popc(has[i][c]);
-        }
-    if (lane < 4) s.val[n + lane] = -INFINITY;
+        for (int c = 0; c < VEC; ++c)
+            if (v[i][c] >= least) *at++ = make_float2(v[i][c], __int_as_float((lane + kWarp * i) * VEC + c));
+    if (lane == 0) s.cand[n] = make_float2(-INFINITY, 0.f);
     __syncwarp();
-    const float mine = s.val[lane];
-    const int my_id = s.id[lane];
+    const float2 mine = s.cand[lane];
     int rank = -1; // itself counts once
-    for (int c = 0; c < n; c += 4) {
-        const float4 o = *reinterpret_cast<const float4 *>(&s.val[c]);
-        rank += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
+    for (int c = 0; c < n; c += 2) {
+        const float4 o = *reinterpret_cast<const float4 *>(&s.cand[c]);
+        rank += (o.x >= mine.x) + (o.z >= mine.x);
     }
     if (__reduce_add_sync(0xffffffffu, lane < n ? (unsigned)rank : 0u) != (unsigned)(n * (n - 1) / 2)) { // ties
         rank = 0;
-        for (int c = 0; c < n; ++c) rank += s.val[c] > mine || (s.val[c] == mine && s.id[c] < my_id);
+        for (int c = 0; c < n; ++c) {
+            const float2 o = s.cand[c];
+            rank += o.x > mine.x || (o.x == mine.x && __float_as_int(o.y) < __float_as_int(mine.y));
+        }
     }
-    if (lane < n && rank < k) {
-        s.sel_val[rank] = mine;
-        s.sel_id[rank] = my_id;
-    }
+    if (lane < n && rank < k) s.sel[rank] = mine;
     __syncwarp();
-    const float z = (lane < k) ? expf(s.sel_val[lane] - first) : 0.f;
+    const float2 chosen = s.sel[lane < k ? lane : 0];
+    const float z = (lane < k) ? expf(chosen.x - first) : 0.f;
     float sum = z;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    *e = s.sel_id[lane < k ? lane : 0];
+    *e = __float_as_int(chosen.y);
     *wt = __fdiv_rn(z, sum);
     *top = first;
     __syncwarp(); // the slots are free for the next token
