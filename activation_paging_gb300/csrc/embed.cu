@@ -488,46 +488,107 @@ template <int VE, int NG> struct Slice {
     __device__ int at(int g) const { return s0 + g * kWarp; }
 };
 
-// Two single-precision operations in one instruction, each rounded as its own.
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
+// A lane's sums, two single-precision values to a register pair, for
+// instructions that work on two values at once (each rounded as its own).
+// Element e of the lane (group e / VE, place e % VE) is half of pair e / 2.
+using f2 = unsigned long long;
+template <int VE, int NG> struct Sums {
+    static_assert(VE * NG % 2 == 0, "pairs");
+    f2 p[VE * NG / 2];
+};
+
+__device__ __forceinline__ f2 pack2(uint32_t lo, uint32_t hi)
 {
-    float2 d;
-    asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
     return d;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+__device__ __forceinline__ float2 unpack2(f2 a)
 {
     float2 d;
-    asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+    return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b)
+{
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 
-template <typename TG, int VE, int NG>
-__device__ __forceinline__ void finish_row(TG *row, const Slice<VE, NG> &sl, const float (&acc)[NG][VE],
-                                           const Pack<TG, VE> (&old)[NG], float scale, bool add)
+// Pair q of a lane's elements, in single precision.
+template <typename E, int VE, int NG> __device__ __forceinline__ f2 pair_of(const Pack<E, VE> (&v)[NG], int q)
+{
+    const int e = 2 * q;
+    if constexpr (VE == 1) {
+        return pack2(__float_as_uint(to_f(v[e].v[0])), __float_as_uint(to_f(v[e + 1].v[0])));
+    } else if constexpr (sizeof(E) == 4) {
+        f2 d;
+        memcpy(&d, &v[e / VE].v[e % VE], 8);
+        return d;
+    } else { // two BF16 values are the upper halves of two single-precision ones
+        uint32_t w;
+        memcpy(&w, &v[e / VE].v[e % VE], 4);
+        return pack2(w << 16, w & 0xffff0000u);
+    }
+}
+
+template <int VE, int NG> __device__ __forceinline__ void zero(Sums<VE, NG> &a)
 {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        if (!sl.in(g)) continue;
-        Pack<TG, VE> o;
-        if constexpr (VE == 1) {
-            const float v = __fmul_rn(scale, acc[g][0]);
-            o.v[0] = from_f<TG>(add ? __fadd_rn(to_f(old[g].v[0]), v) : v);
-        } else {
+    for (int q = 0; q < VE * NG / 2; ++q) a.p[q] = 0;
+}
+
+template <typename E, int VE, int NG>
+__device__ __forceinline__ void add_row(Sums<VE, NG> &a, const Pack<E, VE> (&v)[NG])
+{
 #pragma unroll
-            for (int i = 0; i < VE; i += 2) {
-                float2 x = mul2(make_float2(scale, scale), make_float2(acc[g][i], acc[g][i + 1]));
-                if (add) x = add2(make_float2(to_f(old[g].v[i]), to_f(old[g].v[i + 1])), x);
-                o.v[i] = from_f<TG>(x.x);
-                o.v[i + 1] = from_f<TG>(x.y);
-            }
-        }
-        reinterpret_cast<Pack<TG, VE> *>(row)[sl.at(g)] = o;
+    for (int q = 0; q < VE * NG / 2; ++q) a.p[q] = add2(a.p[q], pair_of<E, VE, NG>(v, q));
+}
+
+// The elements as packs of type E.
+template <typename E, int VE, int NG> __device__ __forceinline__ void unpack(Pack<E, VE> (&o)[NG], const Sums<VE, NG> &a)
+{
+#pragma unroll
+    for (int e = 0; e < VE * NG; e += 2) {
+        const float2 x = unpack2(a.p[e / 2]);
+        o[e / VE].v[e % VE] = from_f<E>(x.x);
+        o[(e + 1) / VE].v[(e + 1) % VE] = from_f<E>(x.y);
     }
+}
+
+template <typename TG, int VE, int NG>
+__device__ __forceinline__ void finish_row(TG *row, const Slice<VE, NG> &sl, const Sums<VE, NG> &acc,
+                                           const Pack<TG, VE> (&old)[NG], float scale, bool add)
+{
+    const f2 scale2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
+    Sums<VE, NG> x;
+#pragma unroll
+    for (int q = 0; q < VE * NG / 2; ++q) {
+        x.p[q] = mul2(scale2, acc.p[q]);
+        if (add) x.p[q] = add2(pair_of<TG, VE, NG>(old, q), x.p[q]);
+    }
+    Pack<TG, VE> o[NG];
+    unpack(o, x);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+        if (sl.in(g)) reinterpret_cast<Pack<TG, VE> *>(row)[sl.at(g)] = o[g];
+}
+
+template <int VE, int NG>
+__device__ __forceinline__ void store_part(float *row, const Slice<VE, NG> &sl, const Sums<VE, NG> &a)
+{
+    Pack<float, VE> o[NG];
+    unpack(o, a);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+        if (sl.in(g)) reinterpret_cast<Pack<float, VE> *>(row)[sl.at(g)] = o[g];
 }
 
 template <typename E, int VE, int NG>
@@ -543,44 +604,6 @@ __device__ __forceinline__ void load_part(Pack<float, VE> (&v)[NG], const float 
 {
 #pragma unroll
     for (int g = 0; g < NG; ++g) v[g] = reinterpret_cast<const Pack<float, VE> *>(row)[sl.at(g)];
-}
-
-template <int VE, int NG> __device__ __forceinline__ void zero(float (&a)[NG][VE])
-{
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int i = 0; i < VE; ++i) a[g][i] = 0.f;
-}
-
-template <typename E, int VE, int NG>
-__device__ __forceinline__ void add_row(float (&a)[NG][VE], const Pack<E, VE> (&v)[NG])
-{
-    if constexpr (VE * NG == 1) {
-        a[0][0] = __fadd_rn(a[0][0], to_f(v[0].v[0]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < VE * NG; i += 2) {
-            const int j = i + 1;
-            const float2 x = add2(make_float2(a[i / VE][i % VE], a[j / VE][j % VE]),
-                                  make_float2(to_f(v[i / VE].v[i % VE]), to_f(v[j / VE].v[j % VE])));
-            a[i / VE][i % VE] = x.x;
-            a[j / VE][j % VE] = x.y;
-        }
-    }
-}
-
-template <int VE, int NG>
-__device__ __forceinline__ void store_part(float *row, const Slice<VE, NG> &sl, const float (&a)[NG][VE])
-{
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        if (!sl.in(g)) continue;
-        Pack<float, VE> o;
-#pragma unroll
-        for (int i = 0; i < VE; ++i) o.v[i] = a[g][i];
-        reinterpret_cast<Pack<float, VE> *>(row)[sl.at(g)] = o;
-    }
 }
 
 // Asks for `bytes` bytes from p in L2 (a hint; the 16-byte granules that hold them).
@@ -807,24 +830,18 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         const Slice<VE, NG> here{lane, cur.cols / VE}; // the same from the slice's first column
         const bool more = it + gridDim.x < sums;
         if (more) ahead = rows_of(it + gridDim.x);
-        float acc[NG][VE];
+        Sums<VE, NG> acc;
         zero(acc);
-        // row r is added: where it ends a run, the sum goes to dtable, or to the warps that join it
-        auto take = [&](int r, const Pack<TD, VE>(&v)[NG], const Pack<TG, VE>(&old)[NG]) {
-            add_row(acc, v);
-            if (!(ends >> r & 1)) return;
-            if (direct >> r & 1)
-                finish_row(dst_of(cur, r), here, acc, old, scale, ADD);
-            else
-                store_part(s_part(w), mine, acc);
-            zero(acc);
-        };
         for (int r0 = 0; r0 < live; r0 += kBatch) {
             const int slot = r0 / kBatch % (kStages / kBatch);
             if (!bar_wait(smem_addr(&s_bar[w][slot]), phases >> slot & 1) && d_status)
                 atomicOr(d_status, AP_FLAG_CORRUPT);
             phases ^= 1u << slot;
             const uint8_t *at = ring + r0 % kStages * kStage;
+            // the batch's rows, those that end a run, and of them those of this warp alone: in uniform registers,
+            // by a reduction, so that the branches on them are uniform
+            const uint32_t all = live - r0 >= kBatch ? (1u << kBatch) - 1 : (1u << (live - r0)) - 1;
+            const uint32_t bits = __reduce_or_sync(0xffffffffu, (ends >> r0 & all) | (direct >> r0 & all) << 8 | all << 16);
             Pack<TD, VE> v[kBatch][NG];
             Pack<TG, VE> old[kBatch][NG];
 #pragma unroll
@@ -834,7 +851,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
                     v[u][g] = reinterpret_cast<const Pack<TD, VE> *>(row + from)[mine.at(g)];
-                if (ADD && (direct >> r0 >> u & 1)) {
+                if (ADD && (bits >> (u + 8) & 1)) {
                     const uint32_t from2 = start_of(cur.dst, r0 + u);
 #pragma unroll
                     for (int g = 0; g < NG; ++g)
@@ -844,8 +861,16 @@ __global__ void __launch_bounds__(kSumThreads, 2)
             __syncwarp();
             fetch(cur, r0 + kStages);
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (r0 + u < live) take(r0 + u, v[u], old[u]);
+            for (int u = 0; u < kBatch; ++u) {
+                if (bits >> (u + 16) & 1) add_row(acc, v[u]);
+                if (bits >> u & 1) { // the sum goes to dtable, or to the warps that join it
+                    if (bits >> (u + 8) & 1)
+                        finish_row(dst_of(cur, r0 + u), here, acc, old[u], scale, ADD);
+                    else
+                        store_part(s_part(w), mine, acc);
+                    zero(acc);
+                }
+            }
         }
         // the whole ring is free: the next item's first rows
         if (more)
@@ -952,7 +977,7 @@ __global__ void __launch_bounds__(kSumThreads)
         Pack<float, VE> tail[NG], p[U][NG];
         if (ADD) load_row(old, dtable + (int64_t)key * ld, sl);
         load_row(tail, partial + (2 * c + 1) * part_ld, sl);
-        float acc[NG][VE];
+        Sums<VE, NG> acc;
         zero(acc);
         for (int64_t q0 = c + 1;;) {
 #pragma unroll
@@ -1074,7 +1099,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
             TG *row = dtable + id * ld + col0;
             Pack<TG, VE> old[NG];
             if (ADD) load_row(old, row, here, !(info & kPart));
-            float acc[NG][VE];
+            Sums<VE, NG> acc;
             zero(acc);
             constexpr int U = 8;
             for (int r0 = 0; r0 < n; r0 += U) {
@@ -1100,7 +1125,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
             TG *row = dtable + sorted[info & 0xffffu].x * ld + col0;
             Pack<TG, VE> old[NG];
             if (ADD) load_row(old, row, here);
-            float acc[NG][VE];
+            Sums<VE, NG> acc;
             zero(acc);
             for (int q = j; q < count && (q == j || (s_piece[q] & (kPart | kFirst)) == kPart); ++q) {
                 Pack<float, VE> p[NG];
