@@ -962,15 +962,15 @@ __device__ __forceinline__ void fill_rows(int64_t first, int64_t last, int rows,
 // find nothing to do); its warps add up an eighth of the heads each, in tile
 // order, and the first one adds their sums to the tail in warp order.
 // A gradient that is written whole gets its zeros here, by warps that need not
-// wait for the sums (`early`: part of them before the sums are complete; the
-// sort is complete then, since the sums kernel lets this one start only after
-// its own wait).
+// wait for the sums (an eighth of them before the sums are complete; the sort
+// is complete then, since the sums kernel lets this one start only after its
+// own wait).
 template <typename TG, int VE, int NG, bool ADD>
 __global__ void __launch_bounds__(kSumThreads)
     k_embed_join(const uint2 *__restrict__ sorted, int64_t T, int64_t V, int H, float scale, int tile_rows,
                  uint32_t slices, uint32_t items, TG *__restrict__ dtable, int64_t ld,
                  const float *__restrict__ partial, int64_t part_ld, const uint32_t *__restrict__ seen,
-                 int rows_per_fill, bool early)
+                 int rows_per_fill)
 {
     constexpr int U = 4;
     constexpr int kCols = kWarp * VE * NG;
@@ -979,8 +979,8 @@ __global__ void __launch_bounds__(kSumThreads)
     const int lane = (int)lane_id(), w = threadIdx.x / kWarp;
     const Slice<VE, NG> mine{lane, kWarp * NG};
     const int64_t fills = ADD ? 0 : (V + rows_per_fill - 1) / rows_per_fill;
-    const int64_t ahead = early ? fills / 8 : 0;
-    auto seen_from = [&](int64_t r0) { return seen ? __ldcg(seen + (r0 >> 5)) >> (r0 & 31) : 0u; };
+    const int64_t ahead = fills / 8;
+    auto seen_from = [&](int64_t r0) { return __ldcg(seen + (r0 >> 5)) >> (r0 & 31); };
     if (!ADD) fill_rows<TG, VE, kSumWarps>(0, ahead, rows_per_fill, V, nstep, dtable, ld, seen_from);
     pdl_begin();
     for (uint32_t it = blockIdx.x; it < items; it += gridDim.x) { // (block-uniform)
@@ -1272,8 +1272,7 @@ ap_status sort_tokens(const void *ids, bool wide, int64_t T, int64_t V, int64_t 
 {
     uint2 *buf[2] = {reinterpret_cast<uint2 *>(sc), reinterpret_cast<uint2 *>(sc + p.off_b)};
     *sorted = buf[0];
-    if (T == 0) return AP_OK;
-    const int most = T > kClThreads ? cluster_blocks() : 1;
+    const int most = cluster_blocks();
     if (T <= (int64_t)most * kClThreads * kClItemsMax) {
         int blocks = 1;
         while (blocks < most && (int64_t)blocks * kClThreads < T) blocks *= 2;
@@ -1376,24 +1375,23 @@ ap_status embed_sums(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
                                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (attr != cudaSuccess) return cuda_fail(attr, "embed_backward sum");
     static const int resident = resident_grid((const void *)kernel, kSumThreads, smem);
-    const int64_t items = p.sum_tiles * slices;
-    if (items > 0) {
-        launch(kernel, (int)(items < resident ? items : resident), kSumThreads, smem, st,
-               static_cast<const TD *>(a.dout), a.dout_ld, a.sorted, a.T, a.V, a.H, a.scale, p.rows,
-               (uint32_t)slices, (uint32_t)items, dtable, a.ld, a.partial, p.part_ld, a.ids, a.wide, a.pad, a.d_status);
-        AP_CHECK_LAUNCH("embed_backward sum launch");
-    }
-    if (!ADD || p.sum_tiles > 1) {
-        static const int resident_j = resident_grid((const void *)k_embed_join<TG, VE, NG, ADD>, kSumThreads);
-        const int rows = fill_rows_of((int64_t)a.H * sizeof(TG));
-        const int64_t joins = (p.sum_tiles - 1) * slices;
-        int64_t grid = joins;
-        if (!ADD && (a.V + rows - 1) / rows > grid * kSumWarps) grid = ((a.V + rows - 1) / rows + kSumWarps - 1) / kSumWarps;
-        launch(k_embed_join<TG, VE, NG, ADD>, (int)(grid < resident_j ? grid : resident_j), kSumThreads, 0, st, a.sorted,
-               a.T, a.V, a.H, a.scale, p.rows * kSumWarps, (uint32_t)slices, (uint32_t)joins, dtable, a.ld, a.partial,
-               p.part_ld, a.seen, rows, a.T > 0);
-        AP_CHECK_LAUNCH("embed_backward join launch");
-    }
+    // (more than kSmallTokens tokens: several tiles)
+    const int64_t items = p.sum_tiles * slices, joins = (p.sum_tiles - 1) * slices;
+    if (items > INT32_MAX)
+        return fail(AP_EINVAL, "embed_backward: %lld tokens of %d columns are more than one launch takes", (long long)a.T,
+                    a.H);
+    launch(kernel, (int)(items < resident ? items : resident), kSumThreads, smem, st, static_cast<const TD *>(a.dout),
+           a.dout_ld, a.sorted, a.T, a.V, a.H, a.scale, p.rows, (uint32_t)slices, (uint32_t)items, dtable, a.ld,
+           a.partial, p.part_ld, a.ids, a.wide, a.pad, a.d_status);
+    AP_CHECK_LAUNCH("embed_backward sum launch");
+    static const int resident_j = resident_grid((const void *)k_embed_join<TG, VE, NG, ADD>, kSumThreads);
+    const int rows = fill_rows_of((int64_t)a.H * sizeof(TG));
+    const int64_t fills = ADD ? 0 : ((a.V + rows - 1) / rows + kSumWarps - 1) / kSumWarps; // blocks the zeros can use
+    const int64_t grid = joins > fills ? joins : fills;
+    launch(k_embed_join<TG, VE, NG, ADD>, (int)(grid < resident_j ? grid : resident_j), kSumThreads, 0, st, a.sorted, a.T,
+           a.V, a.H, a.scale, p.rows * kSumWarps, (uint32_t)slices, (uint32_t)joins, dtable, a.ld, a.partial, p.part_ld,
+           a.seen, rows);
+    AP_CHECK_LAUNCH("embed_backward join launch");
     return AP_OK;
 }
 
