@@ -1,8 +1,10 @@
 // Embedding lookup with a scale, and the gradient of the table.
 //
-// Lookup: out[t] = round(scale * table[ids[t]]), one warp per piece of a row.
+// Lookup: out[t] = round(scale * table[ids[t]]), one warp per piece of a row;
+// bound by HBM (16384 x 2048 BF16 rows of a 151936-row table: 95 MB in 18 us).
 //
 // Gradient: dtable[v] (+)= scale * sum over the tokens with id v of dout[t].
+// Up to 1024 tokens take one launch (k_embed_small), more take three:
 //   1. The tokens are sorted by id (stable radix sort, least significant digit
 //      first; ids that do not count sort last), so an id's tokens are one run
 //      in token order.
@@ -12,8 +14,14 @@
 //      partial rows of a run that spans warps are joined in shared memory,
 //      and a run that spans tiles leaves one partial row per tile: `head`
 //      where it began in an earlier tile, `tail` where it begins and goes on.
-//   3. k_embed_join adds the partial rows of each such run in tile order.
+//   3. k_embed_join adds the partial rows of each such run in tile order, and
+//      zeros the rows that no id names where the gradient is written whole.
 // No floating-point atomics: every sum has one order, fixed by ids and sizes.
+// Each row of dout is read once, each row of dtable that an id names read and
+// written once, beside the partial rows (at most 2 of single precision for
+// every 256 rows).  Sums are bound by HBM where there is much to add (32768 x
+// 7168, 30% padding: 154 us, 828 MB); at 8192 x 2048 the sort takes 8 us of
+// the 25, the sums 14 (of which 4 to start and to join), the join 3.
 #include <cuda_bf16.h>
 
 #include "ap_common.cuh"
@@ -201,10 +209,10 @@ __device__ __forceinline__ void mark_seen(uint32_t *seen, uint32_t key, int64_t 
 // of the current order, warp q of it a run of 32 * ITEMS.  A pass: every warp
 // ranks its tokens per digit; the warps' counts are added up per digit; every
 // block gives its totals to all blocks; every token goes to its new place in
-// the block that holds it, in the last pass to memory.  The phases wait for
-// one another (about 4 us for two passes over 8192 tokens, of which the two
-// or three barriers of the cluster take a half); three launches per digit, as
-// below, cost 35 us.
+// the block that holds it, in the last pass to memory.  Bound by the waits of
+// its phases on one another (two passes: 8 us at 8192 tokens, 13 us at 16384
+// and 32768, 34 us at 131072; a barrier of the cluster takes about 0.7 us);
+// three launches per digit, as below, took 35 us at 8192.
 constexpr int kClThreads = 1024;
 constexpr int kClWarps = kClThreads / kWarp;
 constexpr int kClItemsMax = 8;
@@ -1041,7 +1049,7 @@ __global__ void __launch_bounds__(kSumThreads)
 // longer run meet in shared memory and are added in order.  Without an old
 // gradient the rows that no id names are shared out over all blocks.
 constexpr int64_t kSmallTokens = kClThreads;
-constexpr int kRankTokens = 256;
+constexpr int kRankTokens = 256; // 6.3 us at 256 x 2048 by counting, 8.4 us by radix passes
 constexpr int kPiece = 16;
 // pieces of runs longer than one piece: a run of n > 16 has at most 2 n / 17
 constexpr int kLongPieces = 2 * (int)kSmallTokens / (kPiece + 1) + 1;
@@ -1205,13 +1213,15 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int32_t H)
     p.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
     p.bits = (bits + p.passes - 1) / p.passes;
     p.tiles = T > kClusterMax / 2 ? (T + kSortTile - 1) / kSortTile : 0; // (half: clusters of 8)
-    // the longest tiles that still give a block to nearly every SM twice (pieces of 256 columns)
+    // the longest tiles that still give kWantItems blocks work (pieces of 256 columns): half as long, they take 169 us
+    // for 156 at 32768 x 7168 and 29.2 for 28.3 at 8192 x 2048, since the warps of a block wait for one another per tile
     const int64_t pieces = ((int64_t)H + 255) / 256;
     p.rows = kSumRowsMax;
     while (p.rows > 4 && T * pieces < kWantItems * p.rows * kSumWarps) p.rows /= 2;
     p.sum_tiles = (T + p.rows * kSumWarps - 1) / (p.rows * kSumWarps);
     p.part_ld = ((int64_t)H + 7) / 8 * 8;
-    if (T <= kSmallTokens) return p; // no work space
+    // no work space: one launch, 11.2 us at 1024 x 2048 where three take 13.0, and 7 us of host time for 18
+    if (T <= kSmallTokens) return p;
     auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
     p.off_b = up(T * 8);
     p.off_hist = p.off_b + (p.tiles ? up(T * 8) : 0);
@@ -1273,7 +1283,7 @@ ap_status sort_tokens(const void *ids, bool wide, int64_t T, int64_t V, int64_t 
     uint2 *buf[2] = {reinterpret_cast<uint2 *>(sc), reinterpret_cast<uint2 *>(sc + p.off_b)};
     *sorted = buf[0];
     const int most = cluster_blocks();
-    if (T <= (int64_t)most * kClThreads * kClItemsMax) {
+    if (T <= (int64_t)most * kClThreads * kClItemsMax) { // 131072 x 512: 87 us in all, with the passes below 137
         int blocks = 1;
         while (blocks < most && (int64_t)blocks * kClThreads < T) blocks *= 2;
         const int64_t each = ((T + blocks - 1) / blocks + kClThreads - 1) / kClThreads; // tokens per thread
@@ -1329,7 +1339,9 @@ void embed_typed(const void *table, int64_t V, int64_t ld, int32_t tt, const voi
                  float scale, void *out, int64_t out_ld, int32_t ot, uint32_t *d_status, cudaStream_t st)
 {
     constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
-    constexpr int UA = 4; // vectors of a lane in flight: 32768 x 7168 rows 117 us (2: 126 us), 16384 x 2048 18.4 us (2: 17.7)
+    // The widest elements that the rows' alignment allows: 16384 rows of 2048, 2046 and 2047 BF16 take 18.3, 20.2 and
+    // 27.1 us.  UA vectors of a lane in flight: 32768 x 7168 rows 117 us (2: 126 us), 16384 x 2048 18.4 us (2: 17.7).
+    constexpr int UA = 4;
     if (H % VE == 0 && vec_ok(table, ld, tt, VE) && vec_ok(out, out_ld, ot, VE))
         launch_embed<TI, TO, VE, UA>(table, V, ld, ids, wide, T, H, scale, out, out_ld, d_status, st);
     else if (H % 2 == 0 && vec_ok(table, ld, tt, 2) && vec_ok(out, out_ld, ot, 2))
@@ -1432,6 +1444,8 @@ ap_status embed_backward_typed(const SumArgs &a, int32_t dt, int32_t gt, bool ad
         if (even) return add ? embed_small<TD, TG, 2, true>(a, p, st) : embed_small<TD, TG, 2, false>(a, p, st);
         return add ? embed_small<TD, TG, 1, true>(a, p, st) : embed_small<TD, TG, 1, false>(a, p, st);
     }
+    // 8192 rows of 1008 (16-byte boundaries), 1002 (pairs) and 1001 columns: 17.8, 19.6 and 20.3 us; element-wise loads
+    // through registers took 36.8 us for the last
     constexpr int N = kDoutBytes / kWarp / (int)sizeof(TD); // a lane's columns of a slice
     constexpr int VE = sizeof(TD) == 2 && sizeof(TG) == 2 ? 8 : 4;
     constexpr int V16 = sizeof(TD) == 2 || sizeof(TG) == 2 ? 8 : 4;
