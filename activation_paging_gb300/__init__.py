@@ -230,10 +230,14 @@ def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, dtype: tor
     V, H, ld, kind = _rows(table, "table")
     T, size = _ids(ids)
     if out is None:
-        out = _empty((T, H), dtype if dtype is not None else table.dtype, table.device, stream)
-    n, h, out_ld, out_kind = _rows(out, "out")
-    if n != T or h != H:
-        raise ValueError(f"out must be {[T, H]}, got {[n, h]}")
+        out_ld, out_kind = H, kind if dtype is None else _ROW_TYPES.get(dtype)
+        if out_kind is None:
+            raise ValueError(f"dtype must be bfloat16 or float32, got {dtype}")
+        out = _empty((T, H), table.dtype if dtype is None else dtype, table.device, stream)
+    else:
+        n, h, out_ld, out_kind = _rows(out, "out")
+        if n != T or h != H:
+            raise ValueError(f"out must be {[T, H]}, got {[n, h]}")
     check(lib().ap_embed(_p(table), V, ld, kind, _p(ids), size, T, H, scale, _p(out), out_ld, out_kind, _p(status),
                          _stream(stream)), "embed")
     return out

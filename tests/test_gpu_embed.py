@@ -261,6 +261,7 @@ def test_binding_refuses():
         lambda: ap.embed(tab.t(), ids),
         lambda: ap.embed(tab, ids.short()),
         lambda: ap.embed(tab, ids[:, None]),
+        lambda: ap.embed(tab, ids, dtype=torch.float16),
         lambda: ap.embed(tab, ids, out=torch.zeros(2, 8, device="cuda")),
         lambda: ap.embed_backward(tab, ids, 9),                    # four rows, three ids
         lambda: ap.embed_backward(tab[:3], ids, 9, accumulate=True),
