@@ -158,12 +158,11 @@ __device__ __forceinline__ uint32_t sort_key(const void *ids, bool wide, int64_t
                                              uint32_t *d_status)
 {
     const int64_t id = load_id(ids, wide, t);
-    if (id == pad) return (uint32_t)V;
-    if (id < 0 || id >= V) {
+    if (id < 0 || id >= V) { // (pad = -1 is none: an id of -1 is a bad one)
         if (d_status) atomicOr(d_status, AP_FLAG_BAD_INDEX);
         return (uint32_t)V;
     }
-    return (uint32_t)id;
+    return id == pad ? (uint32_t)V : (uint32_t)id;
 }
 
 // Lanes of the warp whose digit equals this lane's (one vote per bit; a lane

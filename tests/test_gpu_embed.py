@@ -174,6 +174,24 @@ def test_padding_and_bad_ids(accumulate):
     check_backward(np.full(300, -7), V, 64, accumulate=accumulate)            # only bad ids
 
 
+@pytest.mark.parametrize("T", [16, 17, 255, 256, 257, 1023, 1024, 1025, 131072, 131073])
+def test_lengths_where_the_form_changes(T):
+    """One piece of a run or two, ranking by counting or by passes, one launch or three, one cluster or passes over
+    memory; a quarter of the tokens share an id, the others are spread."""
+    ids = inputs.rng(T, 25).integers(0, 900, T)
+    ids[::4] = 901
+    check_backward(ids, 902, 12, "bf16", "f32", True)
+    check_backward(ids, 902, 12, "f32", "bf16", False, pad=901)
+
+
+@pytest.mark.parametrize("T", [40, 2000])
+def test_an_id_of_minus_one_is_a_bad_one(T):
+    ids = zipf_ids(T, T, 50).astype(np.int64)
+    ids[7] = -1
+    check_backward(ids, 50, 24)          # no padding: flagged
+    check_backward(ids, 50, 24, pad=3)
+
+
 @pytest.mark.parametrize("accumulate", [True, False])
 def test_no_tokens(accumulate):
     check_backward(np.zeros(0, np.int64), 9, 24, accumulate=accumulate)
