@@ -89,6 +89,68 @@ __device__ __forceinline__ int64_t load_id(const void *ids, bool wide, int64_t t
     return wide ? static_cast<const int64_t *>(ids)[t] : (int64_t) static_cast<const int32_t *>(ids)[t];
 }
 
+// A lane's sums, two single-precision values to a register pair, for
+// instructions that work on two values at once (each rounded as its own).
+// Element e of the lane (group e / VE, place e % VE) is half of pair e / 2.
+using f2 = unsigned long long;
+template <int VE, int NG> struct Sums {
+    static_assert(VE * NG % 2 == 0, "pairs");
+    f2 p[VE * NG / 2];
+};
+
+__device__ __forceinline__ f2 pack2(uint32_t lo, uint32_t hi)
+{
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(f2 a)
+{
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+    return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b)
+{
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Pair q of a lane's elements, in single precision.
+template <typename E, int VE, int NG> __device__ __forceinline__ f2 pair_of(const Pack<E, VE> (&v)[NG], int q)
+{
+    const int e = 2 * q;
+    if constexpr (VE == 1) {
+        return pack2(__float_as_uint(to_f(v[e].v[0])), __float_as_uint(to_f(v[e + 1].v[0])));
+    } else if constexpr (sizeof(E) == 4) {
+        f2 d;
+        memcpy(&d, &v[e / VE].v[e % VE], 8);
+        return d;
+    } else { // two BF16 values are the upper halves of two single-precision ones
+        uint32_t w;
+        memcpy(&w, &v[e / VE].v[e % VE], 4);
+        return pack2(w << 16, w & 0xffff0000u);
+    }
+}
+
+// The elements as packs of type E.
+template <typename E, int VE, int NG> __device__ __forceinline__ void unpack(Pack<E, VE> (&o)[NG], const Sums<VE, NG> &a)
+{
+#pragma unroll
+    for (int e = 0; e < VE * NG; e += 2) {
+        const float2 x = unpack2(a.p[e / 2]);
+        o[e / VE].v[e % VE] = from_f<E>(x.x);
+        o[(e + 1) / VE].v[(e + 1) % VE] = from_f<E>(x.y);
+    }
+}
+
 // Stores a pack that is not read again here: evicted first, so that the rows
 // of the table stay in L2.
 template <typename P> __device__ __forceinline__ void store_stream(P *p, const P &v)
@@ -124,11 +186,14 @@ __global__ void __launch_bounds__(256)
     const int lane = (int)lane_id();
     const int nstep = H / VE;
     const int pieces = (nstep + U * kWarp - 1) / (U * kWarp);
-    const int64_t items = T * pieces;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x / kWarp);
-    for (int64_t it = (int64_t)blockIdx.x * (blockDim.x / kWarp) + threadIdx.x / kWarp; it < items; it += warps) {
-        const int64_t t = it / pieces;
-        const int s0 = (int)(it - t * pieces) * U * kWarp + lane;
+    const int64_t first = (int64_t)blockIdx.x * (blockDim.x / kWarp) + threadIdx.x / kWarp;
+    int64_t t = first / pieces; // (t, piece) steps by `warps` pieces, divided once
+    int piece = (int)(first - t * pieces);
+    const int64_t step_t = warps / pieces;
+    const int step_piece = (int)(warps - step_t * pieces);
+    while (t < T) {
+        const int s0 = piece * U * kWarp + lane;
         const int64_t id = load_id(ids, wide, t);
         const bool ok = id >= 0 && id < V;
         if (!ok && s0 == 0 && d_status) atomicOr(d_status, AP_FLAG_BAD_INDEX);
@@ -136,15 +201,30 @@ __global__ void __launch_bounds__(256)
         PO *dst = reinterpret_cast<PO *>(out + t * out_ld);
         PI r[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            load_now(r[u], src + s0 + u * kWarp, ok && s0 + u * kWarp < nstep);
+        for (int u = 0; u < U; ++u) load_now(r[u], src + s0 + u * kWarp, ok && s0 + u * kWarp < nstep); // (else zeros)
+        const float by = ok ? scale : 0.f;
+        const f2 by2 = pack2(__float_as_uint(by), __float_as_uint(by));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (s0 + u * kWarp >= nstep) continue;
             PO o;
+            if constexpr (VE == 1) {
+                o.v[0] = from_f<TO>(__fmul_rn(to_f(r[u].v[0]), by));
+            } else {
+                const PI in[1] = {r[u]};
+                PO to[1];
+                Sums<VE, 1> x;
 #pragma unroll
-            for (int i = 0; i < VE; ++i) o.v[i] = from_f<TO>(ok ? __fmul_rn(to_f(r[u].v[i]), scale) : 0.f);
-            store_stream(dst + s0 + u * kWarp, o);
+                for (int q = 0; q < VE / 2; ++q) x.p[q] = mul2(pair_of<TI, VE, 1>(in, q), by2);
+                unpack(to, x);
+                o = to[0];
+            }
+            if (s0 + u * kWarp < nstep) store_stream(dst + s0 + u * kWarp, o);
+        }
+        t += step_t;
+        piece += step_piece;
+        if (piece >= pieces) {
+            piece -= pieces;
+            ++t;
         }
     }
 }
@@ -512,57 +592,6 @@ template <int VE, int NG> struct Slice {
     __device__ int at(int g) const { return s0 + g * kWarp; }
 };
 
-// A lane's sums, two single-precision values to a register pair, for
-// instructions that work on two values at once (each rounded as its own).
-// Element e of the lane (group e / VE, place e % VE) is half of pair e / 2.
-using f2 = unsigned long long;
-template <int VE, int NG> struct Sums {
-    static_assert(VE * NG % 2 == 0, "pairs");
-    f2 p[VE * NG / 2];
-};
-
-__device__ __forceinline__ f2 pack2(uint32_t lo, uint32_t hi)
-{
-    f2 d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-    return d;
-}
-__device__ __forceinline__ float2 unpack2(f2 a)
-{
-    float2 d;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
-    return d;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b)
-{
-    f2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b)
-{
-    f2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-// Pair q of a lane's elements, in single precision.
-template <typename E, int VE, int NG> __device__ __forceinline__ f2 pair_of(const Pack<E, VE> (&v)[NG], int q)
-{
-    const int e = 2 * q;
-    if constexpr (VE == 1) {
-        return pack2(__float_as_uint(to_f(v[e].v[0])), __float_as_uint(to_f(v[e + 1].v[0])));
-    } else if constexpr (sizeof(E) == 4) {
-        f2 d;
-        memcpy(&d, &v[e / VE].v[e % VE], 8);
-        return d;
-    } else { // two BF16 values are the upper halves of two single-precision ones
-        uint32_t w;
-        memcpy(&w, &v[e / VE].v[e % VE], 4);
-        return pack2(w << 16, w & 0xffff0000u);
-    }
-}
-
 template <int VE, int NG> __device__ __forceinline__ void zero(Sums<VE, NG> &a)
 {
 #pragma unroll
@@ -574,17 +603,6 @@ __device__ __forceinline__ void add_row(Sums<VE, NG> &a, const Pack<E, VE> (&v)[
 {
 #pragma unroll
     for (int q = 0; q < VE * NG / 2; ++q) a.p[q] = add2(a.p[q], pair_of<E, VE, NG>(v, q));
-}
-
-// The elements as packs of type E.
-template <typename E, int VE, int NG> __device__ __forceinline__ void unpack(Pack<E, VE> (&o)[NG], const Sums<VE, NG> &a)
-{
-#pragma unroll
-    for (int e = 0; e < VE * NG; e += 2) {
-        const float2 x = unpack2(a.p[e / 2]);
-        o[e / VE].v[e % VE] = from_f<E>(x.x);
-        o[(e + 1) / VE].v[(e + 1) % VE] = from_f<E>(x.y);
-    }
 }
 
 template <typename TG, int VE, int NG>
