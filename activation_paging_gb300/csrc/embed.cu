@@ -955,16 +955,31 @@ __global__ void __launch_bounds__(kSumThreads, 2)
     }
 }
 
+// n zeros from p on, by a warp: 16 bytes a lane between the boundaries, single elements up to the first and from the
+// last on.
+template <typename TG> __device__ __forceinline__ void zero_span(TG *p, int n)
+{
+    constexpr int kPer = 16 / (int)sizeof(TG);
+    const int lane = (int)lane_id();
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15) / (int)sizeof(TG);
+    const int to = off ? kPer - off : 0, head = to < n ? to : n;
+    const int mid = (n - head) / kPer, rest = n - head - mid * kPer;
+    if (lane < head) p[lane] = from_f<TG>(0.f);
+    uint4 *q = reinterpret_cast<uint4 *>(p + head);
+#pragma unroll 4
+    for (int s = lane; s < mid; s += kWarp) q[s] = make_uint4(0, 0, 0, 0);
+    if (lane < rest) p[n - rest + lane] = from_f<TG>(0.f);
+}
+
 // Zeros the rows of items [first, last) that no id names; an item is `rows`
-// rows (a power of two, at most 32), taken by one warp of W in a block.
+// rows (a power of two, at most 32), taken by one warp of W in a block.  Rows
+// without a gap between them are one span: 139243 rows of 481 FP32 values take
+// 45 us, 78 row by row in single elements.
 // seen_from(r0): bit i says whether row r0 + i is named, for r0 a multiple of `rows`.
-template <typename TG, int VE, int W, typename Seen>
-__device__ __forceinline__ void fill_rows(int64_t first, int64_t last, int rows, int64_t V, int nstep,
+template <typename TG, int W, typename Seen>
+__device__ __forceinline__ void fill_rows(int64_t first, int64_t last, int rows, int64_t V, int H,
                                           TG *__restrict__ dtable, int64_t ld, Seen seen_from)
 {
-    Pack<TG, VE> z;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) z.v[i] = from_f<TG>(0.f);
     const int64_t warps = (int64_t)gridDim.x * W;
     int64_t it = first + blockIdx.x + (int64_t)gridDim.x * (threadIdx.x / kWarp);
     uint32_t next = it < last ? seen_from(it * rows) : 0u;
@@ -973,11 +988,15 @@ __device__ __forceinline__ void fill_rows(int64_t first, int64_t last, int rows,
         const uint32_t bits = next;
         if (it + warps < last) next = seen_from((it + warps) * rows); // on its way while these rows are written
         const int n = V - r0 < rows ? (int)(V - r0) : rows;
-        for (int r = 0; r < n; ++r) {
-            if (bits >> r & 1) continue;
-            Pack<TG, VE> *row = reinterpret_cast<Pack<TG, VE> *>(dtable + (r0 + r) * ld);
-#pragma unroll 4
-            for (int s = (int)lane_id(); s < nstep; s += kWarp) row[s] = z;
+        for (int r = 0; r < n;) {
+            const uint32_t from = bits >> r;
+            int e = r + 1;
+            if (!(from & 1)) {
+                if (ld == H) e = from ? r + __ffs(from) - 1 : n;
+                if (e > n) e = n;
+                zero_span(dtable + (r0 + r) * ld, (e - r) * H);
+            }
+            r = e;
         }
     }
 }
@@ -1006,7 +1025,7 @@ __global__ void __launch_bounds__(kSumThreads)
     const int64_t fills = ADD ? 0 : (V + rows_per_fill - 1) / rows_per_fill;
     const int64_t ahead = fills / 8;
     auto seen_from = [&](int64_t r0) { return __ldcg(seen + (r0 >> 5)) >> (r0 & 31); };
-    if (!ADD) fill_rows<TG, VE, kSumWarps>(0, ahead, rows_per_fill, V, nstep, dtable, ld, seen_from);
+    if (!ADD) fill_rows<TG, kSumWarps>(0, ahead, rows_per_fill, V, H, dtable, ld, seen_from);
     pdl_begin();
     for (uint32_t it = blockIdx.x; it < items; it += gridDim.x) { // (block-uniform)
         const int64_t c = it / slices;
@@ -1055,7 +1074,7 @@ __global__ void __launch_bounds__(kSumThreads)
         }
         __syncthreads();
     }
-    if (!ADD) fill_rows<TG, VE, kSumWarps>(ahead, fills, rows_per_fill, V, nstep, dtable, ld, seen_from);
+    if (!ADD) fill_rows<TG, kSumWarps>(ahead, fills, rows_per_fill, V, H, dtable, ld, seen_from);
 }
 
 // Up to kSmallTokens tokens in one launch, without work space: every block
@@ -1210,8 +1229,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
         }
         return __ballot_sync(0xffffffffu, lo < T && sorted[lo].x == want);
     };
-    fill_rows<TG, VE, kClWarps>(0, (V + rows_per_fill - 1) / rows_per_fill, rows_per_fill, V, H / VE, dtable, ld,
-                                seen_from);
+    fill_rows<TG, kClWarps>(0, (V + rows_per_fill - 1) / rows_per_fill, rows_per_fill, V, H, dtable, ld, seen_from);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -1356,8 +1374,9 @@ void embed_typed(const void *table, int64_t V, int64_t ld, int32_t tt, const voi
                  float scale, void *out, int64_t out_ld, int32_t ot, uint32_t *d_status, cudaStream_t st)
 {
     constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
-    // The widest elements that the rows' alignment allows: 16384 rows of 2048, 2046 and 2047 BF16 take 18.3, 20.2 and
-    // 27.1 us.  UA vectors of a lane in flight: 32768 x 7168 rows 117 us (2: 126 us), 16384 x 2048 18.4 us (2: 17.7).
+    // The widest elements that the rows' alignment allows: 16384 rows of 2048, 2046 and 2047 BF16 take 18.5, 18.6 and
+    // 24.6 us.  UA vectors of a lane in flight: 32768 x 7168 rows 114.3 us (2: 115.3, 8: 114.8), 16384 x 2048 18.5 us
+    // (2: 18.2, 8: 18.2).
     constexpr int UA = 4;
     if (H % VE == 0 && vec_ok(table, ld, tt, VE) && vec_ok(out, out_ld, ot, VE))
         launch_embed<TI, TO, VE, UA>(table, V, ld, ids, wide, T, H, scale, out, out_ld, d_status, st);
@@ -1385,11 +1404,12 @@ struct SumArgs {
     uint32_t *d_status;
 };
 
-// Rows of zeros that a warp writes at a time: about 16 KB.
-int fill_rows_of(int64_t row_bytes)
+// Rows of zeros that a warp writes at a time: at most 16 KB, and fewer where that leaves blocks without any (one token,
+// 3263 x 108 FP32: 3.8 us, 9.6 with 32 rows a warp and 32 warps a block).
+int fill_rows_of(int64_t V, int64_t row_bytes, int64_t blocks)
 {
     int rows = 32;
-    while (rows > 1 && rows * row_bytes > (16 << 10)) rows /= 2;
+    while (rows > 1 && (rows * row_bytes > (16 << 10) || V < rows * blocks)) rows /= 2;
     return rows;
 }
 
@@ -1414,8 +1434,8 @@ ap_status embed_sums(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
            a.partial, p.part_ld, a.ids, a.wide, a.pad, a.d_status);
     AP_CHECK_LAUNCH("embed_backward sum launch");
     static const int resident_j = resident_grid((const void *)k_embed_join<TG, VE, NG, ADD>, kSumThreads);
-    const int rows = fill_rows_of((int64_t)a.H * sizeof(TG));
-    const int64_t fills = ADD ? 0 : ((a.V + rows - 1) / rows + kSumWarps - 1) / kSumWarps; // blocks the zeros can use
+    const int rows = fill_rows_of(a.V, (int64_t)a.H * sizeof(TG), resident_j);
+    const int64_t fills = ADD ? 0 : (a.V + rows - 1) / rows; // blocks the zeros can use
     const int64_t grid = joins > fills ? joins : fills;
     launch(k_embed_join<TG, VE, NG, ADD>, (int)(grid < resident_j ? grid : resident_j), kSumThreads, 0, st, a.sorted, a.T,
            a.V, a.H, a.scale, p.rows * kSumWarps, (uint32_t)slices, (uint32_t)joins, dtable, a.ld, a.partial, p.part_ld,
@@ -1438,11 +1458,11 @@ ap_status embed_small(const SumArgs &a, const EmbedPlan &p, cudaStream_t st)
     const int64_t slices = (a.H + kSmallCols - 1) / kSmallCols;
     int64_t groups = a.T > 32 ? (a.T + 31) / 32 : 1;
     if (groups * slices > sms) groups = sms / slices > 0 ? sms / slices : 1;
-    const int rows = fill_rows_of((int64_t)a.H * sizeof(TG));
+    const int rows = fill_rows_of(a.V, (int64_t)a.H * sizeof(TG), sms);
     int64_t grid = groups * slices;
     if (!ADD) { // enough blocks for the zeros
-        const int64_t fill = (a.V + (int64_t)rows * kClWarps - 1) / ((int64_t)rows * kClWarps);
-        if (grid < (fill < sms ? fill : sms)) grid = fill < sms ? fill : sms;
+        const int64_t fills = (a.V + rows - 1) / rows;
+        if (grid < (fills < sms ? fills : sms)) grid = fills < sms ? fills : sms;
     }
     launch(kernel, (int)(grid > 0 ? grid : 1), kClThreads, most, st, static_cast<const TD *>(a.dout), a.dout_ld, a.ids,
            a.wide, (int)a.T, a.V, a.pad, a.H, a.scale, p.passes, p.bits, (int)slices, (int)groups,

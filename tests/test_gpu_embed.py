@@ -192,6 +192,15 @@ def test_an_id_of_minus_one_is_a_bad_one(T):
     check_backward(ids, 50, 24, pad=3)
 
 
+@pytest.mark.parametrize("grad", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [6, 3000])
+@pytest.mark.parametrize("H,extra,shift", [(1, 0, 0), (2, 0, 1), (5, 0, 3), (7, 1, 1), (8, 0, 0), (101, 0, 5), (9001, 0, 1)])
+def test_zeros_between_named_rows(H, extra, shift, T, grad):
+    """A gradient written whole: spans of rows that no id names, from none to many rows, start and end anywhere."""
+    check_backward(np.resize([0, 5, 6, 31, 32, 69], T), 70, H, "f32", grad, False, None, extra, shift)
+    check_backward(np.resize([1, 3, 68], T), 70, H, "f32", grad, False, None, extra, shift)
+
+
 @pytest.mark.parametrize("accumulate", [True, False])
 def test_no_tokens(accumulate):
     check_backward(np.zeros(0, np.int64), 9, 24, accumulate=accumulate)
