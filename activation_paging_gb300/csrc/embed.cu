@@ -175,6 +175,48 @@ template <typename P> __device__ __forceinline__ void store_stream(P *p, const P
 }
 
 // ---- lookup --------------------------------------------------------------------
+// A warp takes a piece of an output row: U vectors a lane.
+struct Pieces {
+    int64_t t, step_t; // row and piece of the warp; they step by as many pieces as there are warps, divided once
+    int piece, step_piece, pieces;
+    __device__ explicit Pieces(int n) : pieces(n)
+    {
+        const int64_t warps = (int64_t)gridDim.x * (blockDim.x / kWarp);
+        const int64_t first = (int64_t)blockIdx.x * (blockDim.x / kWarp) + threadIdx.x / kWarp;
+        t = first / n;
+        piece = (int)(first - t * n);
+        step_t = warps / n;
+        step_piece = (int)(warps - step_t * n);
+    }
+    __device__ void next()
+    {
+        t += step_t;
+        piece += step_piece;
+        if (piece >= pieces) {
+            piece -= pieces;
+            ++t;
+        }
+    }
+};
+
+template <typename TO, typename TI, int VE>
+__device__ __forceinline__ Pack<TO, VE> scaled(const Pack<TI, VE> &v, float by)
+{
+    if constexpr (VE == 1) {
+        return {from_f<TO>(__fmul_rn(to_f(v.v[0]), by))};
+    } else {
+        const Pack<TI, VE> in[1] = {v};
+        const f2 by2 = pack2(__float_as_uint(by), __float_as_uint(by));
+        Pack<TO, VE> to[1];
+        Sums<VE, 1> x;
+#pragma unroll
+        for (int q = 0; q < VE / 2; ++q) x.p[q] = mul2(pair_of<TI, VE, 1>(in, q), by2);
+        unpack(to, x);
+        return to[0];
+    }
+}
+
+// Rows on the boundaries of VE elements.
 template <typename TI, typename TO, int VE, int U>
 __global__ void __launch_bounds__(256)
     k_embed(const TI *__restrict__ table, int64_t V, int64_t ld, const void *__restrict__ ids, bool wide, int64_t T,
@@ -183,49 +225,93 @@ __global__ void __launch_bounds__(256)
     pdl_begin();
     using PI = Pack<TI, VE>;
     using PO = Pack<TO, VE>;
-    const int lane = (int)lane_id();
     const int nstep = H / VE;
-    const int pieces = (nstep + U * kWarp - 1) / (U * kWarp);
-    const int64_t warps = (int64_t)gridDim.x * (blockDim.x / kWarp);
-    const int64_t first = (int64_t)blockIdx.x * (blockDim.x / kWarp) + threadIdx.x / kWarp;
-    int64_t t = first / pieces; // (t, piece) steps by `warps` pieces, divided once
-    int piece = (int)(first - t * pieces);
-    const int64_t step_t = warps / pieces;
-    const int step_piece = (int)(warps - step_t * pieces);
-    while (t < T) {
-        const int s0 = piece * U * kWarp + lane;
-        const int64_t id = load_id(ids, wide, t);
+    for (Pieces at((nstep + U * kWarp - 1) / (U * kWarp)); at.t < T; at.next()) {
+        const int s0 = at.piece * U * kWarp + (int)lane_id();
+        const int64_t id = load_id(ids, wide, at.t);
         const bool ok = id >= 0 && id < V;
         if (!ok && s0 == 0 && d_status) atomicOr(d_status, AP_FLAG_BAD_INDEX);
         const PI *src = reinterpret_cast<const PI *>(table + (ok ? id : 0) * ld);
-        PO *dst = reinterpret_cast<PO *>(out + t * out_ld);
+        PO *dst = reinterpret_cast<PO *>(out + at.t * out_ld);
         PI r[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) load_now(r[u], src + s0 + u * kWarp, ok && s0 + u * kWarp < nstep); // (else zeros)
         const float by = ok ? scale : 0.f;
-        const f2 by2 = pack2(__float_as_uint(by), __float_as_uint(by));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            PO o;
-            if constexpr (VE == 1) {
-                o.v[0] = from_f<TO>(__fmul_rn(to_f(r[u].v[0]), by));
-            } else {
-                const PI in[1] = {r[u]};
-                PO to[1];
-                Sums<VE, 1> x;
-#pragma unroll
-                for (int q = 0; q < VE / 2; ++q) x.p[q] = mul2(pair_of<TI, VE, 1>(in, q), by2);
-                unpack(to, x);
-                o = to[0];
-            }
+            const PO o = scaled<TO>(r[u], by);
             if (s0 + u * kWarp < nstep) store_stream(dst + s0 + u * kWarp, o);
         }
-        t += step_t;
-        piece += step_piece;
-        if (piece >= pieces) {
-            piece -= pieces;
-            ++t;
+    }
+}
+
+// BF16 rows of odd length, or that start between two pairs on either side:
+// stores go by the pairs of the output, and the lone elements before the first
+// and after the last pair by the first piece's lanes.  A row of the table that
+// lies the other way is loaded by the pairs that it cuts, each lane's second
+// half from the next lane; the table's first and last row, whose cut pairs
+// reach beyond it, by elements.
+template <int U>
+__global__ void __launch_bounds__(256)
+    k_embed_odd(const bf16_t *__restrict__ table, int64_t V, int64_t ld, const void *__restrict__ ids, bool wide,
+                int64_t T, int H, float scale, bf16_t *__restrict__ out, int64_t out_ld, uint32_t *d_status)
+{
+    pdl_begin();
+    using P1 = Pack<bf16_t, 1>;
+    using P2 = Pack<bf16_t, 2>;
+    const int most = H / 2 > 0 ? H / 2 : 1;
+    for (Pieces at((most + U * kWarp - 1) / (U * kWarp)); at.t < T; at.next()) {
+        const int lane = (int)lane_id(), s0 = at.piece * U * kWarp + lane;
+        const int64_t id = load_id(ids, wide, at.t);
+        const bool ok = id >= 0 && id < V;
+        if (!ok && s0 == 0 && d_status) atomicOr(d_status, AP_FLAG_BAD_INDEX);
+        const P1 *src = reinterpret_cast<const P1 *>(table + (ok ? id : 0) * ld);
+        P1 *dst = reinterpret_cast<P1 *>(out + at.t * out_ld);
+        const int head = reinterpret_cast<uintptr_t>(dst) & 2 ? 1 : 0;
+        const int nstep = (H - head) / 2, rest = H - head - 2 * nstep;
+        P2 r[U];
+        P1 one;
+        const bool cut = reinterpret_cast<uintptr_t>(src + head) & 2;
+        if (cut && id > 0 && id < V - 1) {
+            const P2 *from = reinterpret_cast<const P2 *>(src + head - 1) + s0;
+            P2 a[U + 1];
+#pragma unroll
+            for (int u = 0; u <= U; ++u) load_now(a[u], from + u * kWarp, s0 + u * kWarp <= nstep && (u < U || lane == 0));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                uint32_t own, first;
+                memcpy(&own, &a[u], 4);
+                memcpy(&first, &a[u + 1], 4);
+                const uint32_t next = __shfl_sync(0xffffffffu, lane == 0 ? first : own, (lane + 1) & 31);
+                const uint32_t both = __byte_perm(own, next, 0x5432);
+                memcpy(&r[u], &both, 4);
+            }
+        } else if (cut) {
+            P1 a[U], b[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int s = s0 + u * kWarp;
+                load_now(a[u], src + head + 2 * s, ok && s < nstep);
+                load_now(b[u], src + head + 2 * s + 1, ok && s < nstep);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) r[u] = {a[u].v[0], b[u].v[0]};
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                load_now(r[u], reinterpret_cast<const P2 *>(src + head) + s0 + u * kWarp, ok && s0 + u * kWarp < nstep);
         }
+        const int e = lane < head ? 0 : H - 1;
+        const bool edge = at.piece == 0 && lane < head + rest;
+        load_now(one, src + e, ok && edge);
+        const float by = ok ? scale : 0.f;
+        P2 *to = reinterpret_cast<P2 *>(dst + head);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const P2 o = scaled<bf16_t>(r[u], by);
+            if (s0 + u * kWarp < nstep) store_stream(to + s0 + u * kWarp, o);
+        }
+        if (edge) store_stream(dst + e, scaled<bf16_t>(one, by));
     }
 }
 
@@ -1359,31 +1445,33 @@ int grid_for(int64_t items_per_warp, int resident)
     return (int)(want < 1 ? 1 : want < resident ? want : resident);
 }
 
-template <typename TI, typename TO, int VE, int U>
-void launch_embed(const void *table, int64_t V, int64_t ld, const void *ids, bool wide, int64_t T, int H, float scale,
-                  void *out, int64_t out_ld, uint32_t *d_status, cudaStream_t st)
-{
-    static const int resident = resident_grid((const void *)k_embed<TI, TO, VE, U>, 256);
-    const int64_t items = T * ((H / VE + U * kWarp - 1) / (U * kWarp));
-    launch(k_embed<TI, TO, VE, U>, grid_for(items, resident), 256, 0, st, static_cast<const TI *>(table), V, ld, ids,
-           wide, T, H, scale, static_cast<TO *>(out), out_ld, d_status);
-}
-
 template <typename TI, typename TO>
 void embed_typed(const void *table, int64_t V, int64_t ld, int32_t tt, const void *ids, bool wide, int64_t T, int H,
                  float scale, void *out, int64_t out_ld, int32_t ot, uint32_t *d_status, cudaStream_t st)
 {
-    constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
-    // The widest elements that the rows' alignment allows: 16384 rows of 2048, 2046 and 2047 BF16 take 18.5, 18.6 and
-    // 24.6 us.  UA vectors of a lane in flight: 32768 x 7168 rows 114.3 us (2: 115.3, 8: 114.8), 16384 x 2048 18.5 us
-    // (2: 18.2, 8: 18.2).
-    constexpr int UA = 4;
+    constexpr bool half = sizeof(TI) == 2 && sizeof(TO) == 2;
+    constexpr int VE = half ? 8 : 4;
+    const auto go = [&](auto kernel, int per, int resident) {
+        const int64_t items = T * ((H + per - 1) / per);
+        launch(kernel, grid_for(items, resident), 256, 0, st, static_cast<const TI *>(table), V, ld, ids, wide, T, H,
+               scale, static_cast<TO *>(out), out_ld, d_status);
+    };
+#define AP_EMBED(PER, ...)                                                               \
+    do {                                                                                 \
+        static const int resident = resident_grid((const void *)__VA_ARGS__, 256);       \
+        go(__VA_ARGS__, (PER) * kWarp, resident);                                        \
+    } while (0)
+    // The widest elements that the rows' alignment allows: 16384 rows of 2048, 2046 and 2047 BF16 take 18.5, 18.7 and
+    // 19.6 us (the last by elements: 24.5).  Vectors of a lane in flight: 32768 x 7168 rows 114.3 us (2: 115.3, 8: 114.8).
     if (H % VE == 0 && vec_ok(table, ld, tt, VE) && vec_ok(out, out_ld, ot, VE))
-        launch_embed<TI, TO, VE, UA>(table, V, ld, ids, wide, T, H, scale, out, out_ld, d_status, st);
+        AP_EMBED(VE * 4, k_embed<TI, TO, VE, 4>);
     else if (H % 2 == 0 && vec_ok(table, ld, tt, 2) && vec_ok(out, out_ld, ot, 2))
-        launch_embed<TI, TO, 2, 8>(table, V, ld, ids, wide, T, H, scale, out, out_ld, d_status, st);
+        AP_EMBED(2 * 8, k_embed<TI, TO, 2, 8>);
+    else if constexpr (half)
+        AP_EMBED(2 * 8, k_embed_odd<8>);
     else
-        launch_embed<TI, TO, 1, 16>(table, V, ld, ids, wide, T, H, scale, out, out_ld, d_status, st);
+        AP_EMBED(16, k_embed<TI, TO, 1, 16>);
+#undef AP_EMBED
 }
 
 // What the sums kernels take besides their types.

@@ -80,6 +80,27 @@ def test_embed_matches_plain_form(T, V, H, extra, shift, table, out):
     assert bool((rest == 7.0).all())
 
 
+@pytest.mark.parametrize("extra,to_extra", [(0, 0), (1, 0), (0, 1), (3, 4)])
+@pytest.mark.parametrize("shift,to_shift", [(0, 0), (1, 0), (0, 1), (1, 1), (5, 2)])
+@pytest.mark.parametrize("H", [1, 2, 3, 15, 64, 65, 511, 513, 1025])
+def test_embed_bf16_rows_that_start_between_pairs(H, shift, to_shift, extra, to_extra):
+    """Each row of the table to rows of either parity, its first and last row and bad ids among them."""
+    V = 7
+    ids = np.array([0, 0, V - 1, V - 1, 1, 1, V - 2, V - 2, -1, V, 3, 4, 5, 0, V - 1], np.int64)
+    tab, a, _ = rows(H, V, H, "bf16", extra, shift)
+    o, _, buf = rows(H + 1, len(ids), H, "bf16", to_extra, to_shift)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = bf16_to_host(ap.embed(tab, to_dev(ids), scale=0.37, out=o, status=status))
+    good = (ids >= 0) & (ids < V)
+    exp = a.astype(np.float32)[np.where(good, ids, 0)] * np.float32(0.37) * good[:, None]
+    assert np.array_equal(got[good], inputs.f32_to_bf16_bits(exp)[good]) and not got[~good].any()
+    assert int(host(status)[0]) == ap.FLAG_BAD_INDEX
+    rest = buf.clone()
+    pitch = H + to_extra
+    rest[to_shift:to_shift + len(ids) * pitch].view(len(ids), pitch)[:, :H] = 7.0
+    assert bool((rest == 7.0).all())
+
+
 def test_embed_ids_outside_are_zero_rows_and_flagged():
     tab, a, _ = rows(1, 10, 24, "bf16")
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
