@@ -1584,9 +1584,10 @@ ap_status embed_backward_typed(const SumArgs &a, int32_t dt, int32_t gt, bool ad
                : embed_sums<TD, TG, 1, N, false, kAnywhere>(a, p, st);
 }
 
+// (columns: so that an index of a row and the bytes of a row stay well inside 32 bits)
 bool embed_sizes_ok(int64_t T, int64_t V, int32_t H)
 {
-    return T >= 0 && T < (int64_t(1) << 31) && V >= 1 && V < (int64_t(1) << 31) && H >= 1;
+    return T >= 0 && T < (int64_t(1) << 31) && V >= 1 && V < (int64_t(1) << 31) && H >= 1 && H <= 1 << 28;
 }
 
 } // namespace

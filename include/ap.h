@@ -298,8 +298,9 @@ ap_status ap_route_backward(const float *logits, int64_t T, int32_t E, int32_t k
  *   table   [V, H] of table_dtype, rows table_ld elements apart (device, read)
  *   ids     [T] int32 (id_bytes = 4) or int64 (id_bytes = 8) (device, read)
  *   out     [T, H] of out_dtype, rows out_ld elements apart (device, written)
- * Types: AP_DTYPE_BF16 or AP_DTYPE_F32.  Limits: V >= 1, V < 2^31, H >= 1,
- * 0 <= T < 2^31, row distances >= H, pointers aligned to their elements.
+ * Types: AP_DTYPE_BF16 or AP_DTYPE_F32.  Limits: 1 <= V < 2^31,
+ * 1 <= H <= 2^28, 0 <= T < 2^31, row distances >= H, pointers aligned to their
+ * elements.
  * 16-byte aligned rows are fastest.
  * ========================================================================== */
 ap_status ap_embed(const void *table, int64_t V, int64_t table_ld, int32_t table_dtype, const void *ids,

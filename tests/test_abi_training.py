@@ -144,3 +144,11 @@ def test_binding_refuses_what_it_cannot_pass():
                  lambda: ap.embed_backward(x, torch.zeros(4).long(), 10)):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+def test_embed_refuses_rows_beyond_its_columns(lib):
+    n, H = ctypes.c_int64(0), 2 ** 28 + 1
+    assert lib.ap_embed(None, 2, H, 0, None, 4, 1, H, 1.0, None, H, 0, None, None) == -1
+    assert b"sizes" in lib.ap_last_error()
+    assert lib.ap_embed_scratch_bytes(10, 2, H, ctypes.byref(n)) == -1
+    assert lib.ap_embed_scratch_bytes(10, 2, H - 1, ctypes.byref(n)) == 0
