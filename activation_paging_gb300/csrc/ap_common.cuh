@@ -83,9 +83,13 @@ class NvtxRange {
 // and its blocks then wait in their own pdl_begin() until this grid has
 // finished and its memory is visible.  The chains of small dependent kernels
 // (route, count/rank, scan + plan, copy, pop copy, combine) thereby
-// overlap each launch with the end of the kernel before it; no kernel touches
-// memory before its wait, so results do not change.  After a kernel launched
-// without the attribute, or an event, the wait returns at once.
+// overlap each launch with the end of the kernel before it.  No kernel writes
+// memory, or reads what decides a result, before its wait: that an earlier
+// kernel has ended is not enough, its writes are visible only after the wait.
+// (Before it, k_count_rank, k_route_count_rank and k_embed_sum ask for rows in
+// L2, the last one reading the ids that name them: hints that change no
+// value.)  So results do not change.  After a kernel launched without the
+// attribute, or an event, the wait returns at once.
 template <typename... KArgs, typename... Args>
 inline void launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args &&...args)
 {
@@ -131,8 +135,8 @@ __device__ __forceinline__ void pdl_begin()
 }
 
 // The same, but the next kernel starts only once every block of this one has
-// seen its inputs complete, so what that kernel does before its own wait may
-// read those inputs.
+// seen its inputs complete: of use where that kernel steers hints by them
+// before its own wait.
 __device__ __forceinline__ void pdl_begin_after()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

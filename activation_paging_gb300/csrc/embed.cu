@@ -853,8 +853,8 @@ __global__ void __launch_bounds__(kSumThreads, 2)
                 float *__restrict__ partial, int64_t part_ld, const void *__restrict__ ids, bool wide, int64_t pad,
                 uint32_t *d_status)
 {
-    prefetch_inputs<TD, TG, ADD>(dout, dout_ld, ids, wide, T, V, pad, H, dtable, ld);
-    pdl_begin_after(); // the join's zeros need the sort complete
+    prefetch_inputs<TD, TG, ADD>(dout, dout_ld, ids, wide, T, V, pad, H, dtable, ld); // (hints: they change no value)
+    pdl_begin();
     extern __shared__ __align__(16) uint8_t s_mem[];
     constexpr uint32_t kHead = 1, kThrough = 2, kTail = 4;
     constexpr int kCols = kWarp * VE * NG;
@@ -1057,22 +1057,22 @@ template <typename TG> __device__ __forceinline__ void zero_span(TG *p, int n)
     if (lane < rest) p[n - rest + lane] = from_f<TG>(0.f);
 }
 
-// Zeros the rows of items [first, last) that no id names; an item is `rows`
+// Zeros the rows of the `items` items that no id names; an item is `rows`
 // rows (a power of two, at most 32), taken by one warp of W in a block.  Rows
 // without a gap between them are one span: 139243 rows of 481 FP32 values take
 // 45 us, 78 row by row in single elements.
 // seen_from(r0): bit i says whether row r0 + i is named, for r0 a multiple of `rows`.
 template <typename TG, int W, typename Seen>
-__device__ __forceinline__ void fill_rows(int64_t first, int64_t last, int rows, int64_t V, int H,
-                                          TG *__restrict__ dtable, int64_t ld, Seen seen_from)
+__device__ __forceinline__ void fill_rows(int64_t items, int rows, int64_t V, int H, TG *__restrict__ dtable,
+                                          int64_t ld, Seen seen_from)
 {
     const int64_t warps = (int64_t)gridDim.x * W;
-    int64_t it = first + blockIdx.x + (int64_t)gridDim.x * (threadIdx.x / kWarp);
-    uint32_t next = it < last ? seen_from(it * rows) : 0u;
-    for (; it < last; it += warps) {
+    int64_t it = blockIdx.x + (int64_t)gridDim.x * (threadIdx.x / kWarp);
+    uint32_t next = it < items ? seen_from(it * rows) : 0u;
+    for (; it < items; it += warps) {
         const int64_t r0 = it * rows;
         const uint32_t bits = next;
-        if (it + warps < last) next = seen_from((it + warps) * rows); // on its way while these rows are written
+        if (it + warps < items) next = seen_from((it + warps) * rows); // on its way while these rows are written
         const int n = V - r0 < rows ? (int)(V - r0) : rows;
         for (int r = 0; r < n;) {
             const uint32_t from = bits >> r;
@@ -1091,10 +1091,10 @@ __device__ __forceinline__ void fill_rows(int64_t first, int64_t last, int rows,
 // of the m tiles it goes on through.  A block takes a tile and a slice (most
 // find nothing to do); its warps add up an eighth of the heads each, in tile
 // order, and the first one adds their sums to the tail in warp order.
-// A gradient that is written whole gets its zeros here, by warps that need not
-// wait for the sums (an eighth of them before the sums are complete; the sort
-// is complete then, since the sums kernel lets this one start only after its
-// own wait).
+// A gradient that is written whole gets its zeros here.  They need the sort
+// alone, but start after this kernel's wait for the sums all the same: nothing
+// else makes the sort's `seen` visible to this kernel, and a row that a stale
+// word calls unnamed would lose its sum.
 template <typename TG, int VE, int NG, bool ADD>
 __global__ void __launch_bounds__(kSumThreads)
     k_embed_join(const uint2 *__restrict__ sorted, int64_t T, int64_t V, int H, float scale, int tile_rows,
@@ -1102,17 +1102,13 @@ __global__ void __launch_bounds__(kSumThreads)
                  const float *__restrict__ partial, int64_t part_ld, const uint32_t *__restrict__ seen,
                  int rows_per_fill)
 {
+    pdl_begin();
     constexpr int U = 4;
     constexpr int kCols = kWarp * VE * NG;
     __shared__ __align__(16) float s_part[kSumWarps][kCols];
     const int nstep = H / VE;
     const int lane = (int)lane_id(), w = threadIdx.x / kWarp;
     const Slice<VE, NG> mine{lane, kWarp * NG};
-    const int64_t fills = ADD ? 0 : (V + rows_per_fill - 1) / rows_per_fill;
-    const int64_t ahead = fills / 8;
-    auto seen_from = [&](int64_t r0) { return __ldcg(seen + (r0 >> 5)) >> (r0 & 31); };
-    if (!ADD) fill_rows<TG, kSumWarps>(0, ahead, rows_per_fill, V, H, dtable, ld, seen_from);
-    pdl_begin();
     for (uint32_t it = blockIdx.x; it < items; it += gridDim.x) { // (block-uniform)
         const int64_t c = it / slices;
         const int64_t i0 = c * tile_rows, i1 = i0 + tile_rows;
@@ -1160,7 +1156,16 @@ __global__ void __launch_bounds__(kSumThreads)
         }
         __syncthreads();
     }
-    if (!ADD) fill_rows<TG, kSumWarps>(ahead, fills, rows_per_fill, V, H, dtable, ld, seen_from);
+    if (!ADD) {
+        auto seen_from = [&](int64_t r0) {
+            struct Word {
+                uint32_t bits;
+            } word;
+            load_now(word, reinterpret_cast<const Word *>(seen) + (r0 >> 5), true); // (stays behind the wait)
+            return word.bits >> (r0 & 31);
+        };
+        fill_rows<TG, kSumWarps>((V + rows_per_fill - 1) / rows_per_fill, rows_per_fill, V, H, dtable, ld, seen_from);
+    }
 }
 
 // Up to kSmallTokens tokens in one launch, without work space: every block
@@ -1315,7 +1320,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
         }
         return __ballot_sync(0xffffffffu, lo < T && sorted[lo].x == want);
     };
-    fill_rows<TG, kClWarps>(0, (V + rows_per_fill - 1) / rows_per_fill, rows_per_fill, V, H, dtable, ld, seen_from);
+    fill_rows<TG, kClWarps>((V + rows_per_fill - 1) / rows_per_fill, rows_per_fill, V, H, dtable, ld, seen_from);
 }
 
 // ---- host ------------------------------------------------------------------------
