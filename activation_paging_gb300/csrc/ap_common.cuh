@@ -90,6 +90,9 @@ class NvtxRange {
 // L2, the last one reading the ids that name them: hints that change no
 // value.)  So results do not change.  After a kernel launched without the
 // attribute, or an event, the wait returns at once.
+// Inputs that the kernel ahead may still be writing are not const __restrict__
+// (embed.cu, balance.cu): that promises the compiler data that nobody writes
+// while the kernel runs, which it may read incoherently and before the wait.
 template <typename... KArgs, typename... Args>
 inline void launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args &&...args)
 {

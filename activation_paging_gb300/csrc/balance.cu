@@ -60,9 +60,9 @@ __device__ __forceinline__ float exp_neg(float x)
 // many counted.  Lane l holds the vectors l, l + 32, ... of VEC experts each
 // (N of them).
 template <int VEC, int N>
-__device__ __forceinline__ int route_tokens(const float *__restrict__ logits, int64_t t, int64_t t_end, int64_t step,
-                                            int E, int k, const uint8_t *__restrict__ mask, int32_t *__restrict__ idx,
-                                            float *__restrict__ w, TopkSlots &slots, int *s_cnt, float (&acc)[N][VEC])
+__device__ __forceinline__ int route_tokens(const float *logits, int64_t t, int64_t t_end, int64_t step, int E, int k,
+                                            const uint8_t *mask, int32_t *__restrict__ idx, float *__restrict__ w,
+                                            TopkSlots &slots, int *s_cnt, float (&acc)[N][VEC])
 {
     using Vec = typename Floats<VEC>::T;
     const int lane = (int)lane_id();
@@ -139,8 +139,8 @@ __device__ __forceinline__ void store_sums(float *row, const float (&acc)[N][VEC
 
 template <int VEC, int N, int W>
 __global__ void __launch_bounds__(W *kWarp)
-    k_route_balance(const float *__restrict__ logits, int64_t T, int E, int k, int64_t S, int blocks,
-                    const uint8_t *__restrict__ mask, int32_t *__restrict__ idx, float *__restrict__ w,
+    k_route_balance(const float *logits, int64_t T, int E, int k, int64_t S, int blocks,
+                    const uint8_t *mask, int32_t *__restrict__ idx, float *__restrict__ w,
                     int32_t *__restrict__ part_n, float2 *__restrict__ part, uint32_t *done)
 {
     pdl_begin();
@@ -199,8 +199,8 @@ constexpr int64_t kClusterTokens = 1024, kClusterLogits = 1 << 18;
 bool one_cluster(int64_t T, int32_t E) { return T <= kClusterTokens && T * E <= kClusterLogits; }
 template <int VEC, int N, int W>
 __global__ void __launch_bounds__(W *kWarp)
-    k_balance_cluster(const float *__restrict__ logits, int T, int E, int k, int S, int G, int per,
-                      const uint8_t *__restrict__ mask, float coef, int32_t *__restrict__ idx, float *__restrict__ w,
+    k_balance_cluster(const float *logits, int T, int E, int k, int S, int G, int per,
+                      const uint8_t *mask, float coef, int32_t *__restrict__ idx, float *__restrict__ w,
                       int32_t *__restrict__ counts, float *__restrict__ prob, float *__restrict__ slope,
                       float *__restrict__ loss)
 {
@@ -308,8 +308,8 @@ BalancePlan balance_plan(int64_t T, int32_t E, int64_t group_tokens)
 // ... of its group's blocks in column c; the 128 sums of a column are added in
 // a fixed tree; the last block to finish adds the loss terms up in block order.
 __global__ void __launch_bounds__(kFinThreads)
-    k_balance_finish(int E, int k, int64_t G, int blocks, float coef, const int32_t *__restrict__ part_n,
-                     const float2 *__restrict__ part, float *loss_part, int32_t *__restrict__ counts,
+    k_balance_finish(int E, int k, int64_t G, int blocks, float coef, const int32_t *part_n,
+                     const float2 *part, float *loss_part, int32_t *__restrict__ counts,
                      float *__restrict__ prob, float *__restrict__ slope, float *__restrict__ loss, uint32_t *done)
 {
     pdl_begin();
@@ -405,9 +405,8 @@ __global__ void k_zero_word(float *p)
 // without).
 template <int VEC, int N>
 __global__ void __launch_bounds__(kBalThreads)
-    k_route_backward(const float *logits, int64_t T, int E, int k, const int32_t *__restrict__ idx,
-                     const float *__restrict__ w, const float *__restrict__ dw, const float *__restrict__ slope,
-                     const float *__restrict__ dloss, int64_t S, const uint8_t *__restrict__ mask, float *dlogits,
+    k_route_backward(const float *logits, int64_t T, int E, int k, const int32_t *idx, const float *w, const float *dw,
+                     const float *slope, const float *dloss, int64_t S, const uint8_t *mask, float *dlogits,
                      uint32_t *d_status)
 {
     pdl_begin();

@@ -219,7 +219,7 @@ __device__ __forceinline__ Pack<TO, VE> scaled(const Pack<TI, VE> &v, float by)
 // Rows on the boundaries of VE elements.
 template <typename TI, typename TO, int VE, int U>
 __global__ void __launch_bounds__(256)
-    k_embed(const TI *__restrict__ table, int64_t V, int64_t ld, const void *__restrict__ ids, bool wide, int64_t T,
+    k_embed(const TI *table, int64_t V, int64_t ld, const void *ids, bool wide, int64_t T,
             int H, float scale, TO *__restrict__ out, int64_t out_ld, uint32_t *d_status)
 {
     pdl_begin();
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(256)
 // reach beyond it, by elements.
 template <int U>
 __global__ void __launch_bounds__(256)
-    k_embed_odd(const bf16_t *__restrict__ table, int64_t V, int64_t ld, const void *__restrict__ ids, bool wide,
+    k_embed_odd(const bf16_t *table, int64_t V, int64_t ld, const void *ids, bool wide,
                 int64_t T, int H, float scale, bf16_t *__restrict__ out, int64_t out_ld, uint32_t *d_status)
 {
     pdl_begin();
@@ -517,7 +517,7 @@ __device__ __forceinline__ void sort_passes(int T, int per, int passes, int bits
 
 template <int ITEMS>
 __global__ void __launch_bounds__(kClThreads, 1)
-    k_sort_cluster(const void *__restrict__ ids, bool wide, int T, int per, int64_t V, int64_t pad, int passes,
+    k_sort_cluster(const void *ids, bool wide, int T, int per, int64_t V, int64_t pad, int passes,
                    int bits, uint2 *__restrict__ sorted, uint32_t *__restrict__ seen, uint32_t *d_status)
 {
     cluster_arrive();
@@ -544,7 +544,7 @@ constexpr int kSortTile = kSortThreads * kSortItems;
 // Digit counts of each tile: hist[d * tiles + tile].  The first pass (in ==
 // NULL) reads the ids.
 __global__ void __launch_bounds__(kSortThreads)
-    k_sort_count(const uint2 *__restrict__ in, const void *__restrict__ ids, bool wide, int64_t T, int64_t V,
+    k_sort_count(const uint2 *in, const void *ids, bool wide, int64_t T, int64_t V,
                  int64_t pad, int shift, int bits, uint32_t *__restrict__ hist, uint32_t *__restrict__ seen,
                  uint32_t *d_status)
 {
@@ -618,8 +618,8 @@ __global__ void __launch_bounds__(1024) k_sort_scan(uint32_t *hist, int64_t n)
 // Moves every token of a tile to its place, keeping the order within a digit:
 // warp q ranks its kSortItems * 32 consecutive tokens, 32 at a time.
 __global__ void __launch_bounds__(kSortThreads)
-    k_sort_scatter(const uint2 *__restrict__ in, const void *__restrict__ ids, bool wide, int64_t T, int64_t V,
-                   int64_t pad, int shift, int bits, const uint32_t *__restrict__ hist, uint2 *__restrict__ out,
+    k_sort_scatter(const uint2 *in, const void *ids, bool wide, int64_t T, int64_t V,
+                   int64_t pad, int shift, int bits, const uint32_t *hist, uint2 *__restrict__ out,
                    uint32_t *__restrict__ seen)
 {
     pdl_begin_after(); // as k_sort_cluster
@@ -848,9 +848,9 @@ __device__ __forceinline__ void copy_ends(uint8_t *stage, const Granules &g, uin
 // flight.
 template <typename TD, typename TG, int VE, int NG, bool ADD, Route R>
 __global__ void __launch_bounds__(kSumThreads, 2)
-    k_embed_sum(const TD *__restrict__ dout, int64_t dout_ld, const uint2 *__restrict__ sorted, int64_t T, int64_t V,
+    k_embed_sum(const TD *dout, int64_t dout_ld, const uint2 *sorted, int64_t T, int64_t V,
                 int H, float scale, int rows, uint32_t slices, uint32_t sums, TG *__restrict__ dtable, int64_t ld,
-                float *__restrict__ partial, int64_t part_ld, const void *__restrict__ ids, bool wide, int64_t pad,
+                float *__restrict__ partial, int64_t part_ld, const void *ids, bool wide, int64_t pad,
                 uint32_t *d_status)
 {
     prefetch_inputs<TD, TG, ADD>(dout, dout_ld, ids, wide, T, V, pad, H, dtable, ld); // (hints: they change no value)
@@ -1097,9 +1097,9 @@ __device__ __forceinline__ void fill_rows(int64_t items, int rows, int64_t V, in
 // word calls unnamed would lose its sum.
 template <typename TG, int VE, int NG, bool ADD>
 __global__ void __launch_bounds__(kSumThreads)
-    k_embed_join(const uint2 *__restrict__ sorted, int64_t T, int64_t V, int H, float scale, int tile_rows,
+    k_embed_join(const uint2 *sorted, int64_t T, int64_t V, int H, float scale, int tile_rows,
                  uint32_t slices, uint32_t items, TG *__restrict__ dtable, int64_t ld,
-                 const float *__restrict__ partial, int64_t part_ld, const uint32_t *__restrict__ seen,
+                 const float *partial, int64_t part_ld, const uint32_t *seen,
                  int rows_per_fill)
 {
     pdl_begin();
@@ -1184,7 +1184,7 @@ constexpr int kSmallCols = 128;
 
 template <typename TD, typename TG, int VE, bool ADD>
 __global__ void __launch_bounds__(kClThreads, 1)
-    k_embed_small(const TD *__restrict__ dout, int64_t dout_ld, const void *__restrict__ ids, bool wide, int T,
+    k_embed_small(const TD *dout, int64_t dout_ld, const void *ids, bool wide, int T,
                   int64_t V, int64_t pad, int H, float scale, int passes, int bits, int slices, int groups,
                   TG *__restrict__ dtable, int64_t ld, int rows_per_fill, uint32_t *d_status)
 {

@@ -60,3 +60,12 @@ def test_nothing_but_hints_before_the_wait(file, name, params, body):
     assert at, name + " does not wait"
     before = body[:at.start()]
     assert MAY_STAND_BEFORE.fullmatch(before), (name, before)
+
+
+@pytest.mark.parametrize("file,name,params,body", [k for k in KERNELS if k[0] in ("embed.cu", "balance.cu")],
+                         ids=[k[1] for k in KERNELS if k[0] in ("embed.cu", "balance.cu")])
+def test_inputs_are_not_promised_to_stand_still(file, name, params, body):
+    """const __restrict__ says that nobody writes the data while the kernel runs, which lets the compiler read it through
+    the incoherent cache and before the wait.  A kernel that starts while the one before it still writes its inputs
+    cannot say so."""
+    assert not re.findall(r"const\s+\w+\s*\*\s*__restrict__\s+(\w+)", params)
