@@ -258,7 +258,10 @@ def embed_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: float =
     tokens' rows of dout [T, H] times ``scale`` (FP32 sums), written whole or,
     with ``accumulate``, added to ``dtable``.  Tokens whose id is
     ``padding_idx`` add nothing.  ``scratch``: a uint8 tensor of
-    ``embed_scratch_bytes(T, V, H)`` bytes to reuse."""
+    ``embed_scratch_bytes(T, V, H)`` bytes to reuse.  An id outside [0, V) adds
+    nothing and sets FLAG_BAD_INDEX in ``status``.  FLAG_CORRUPT there says that
+    rows did not arrive in the kernel; the ids that lack them hold NaN then,
+    with ``status`` or without."""
     n, H, ld, kind = _rows(dout, "dout")
     T, size = _ids(ids)
     if n != T:

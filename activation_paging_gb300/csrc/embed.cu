@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 
 #include "ap_common.cuh"
+#include "embed_ring.cuh"
 
 namespace ap {
 namespace {
@@ -684,6 +685,13 @@ template <int VE, int NG> __device__ __forceinline__ void zero(Sums<VE, NG> &a)
     for (int q = 0; q < VE * NG / 2; ++q) a.p[q] = 0;
 }
 
+// Not a number, for sums that lack rows.
+template <int VE, int NG> __device__ __forceinline__ void spoil(Sums<VE, NG> &a)
+{
+#pragma unroll
+    for (int q = 0; q < VE * NG / 2; ++q) a.p[q] = pack2(0x7fffffffu, 0x7fffffffu);
+}
+
 template <typename E, int VE, int NG>
 __device__ __forceinline__ void add_row(Sums<VE, NG> &a, const Pack<E, VE> (&v)[NG])
 {
@@ -846,6 +854,11 @@ __device__ __forceinline__ void copy_ends(uint8_t *stage, const Granules &g, uin
 // latency.  A lane copies the row of its own token.  Loads into registers left
 // 3.3 TB/s at 32768 x 7168 rows, bound by what a warp's registers hold in
 // flight.
+// Should a batch of copies not arrive in the time that bar_wait gives it, the
+// warp sums no staged row any more: every run that it has not ended becomes
+// NaN (a part of one makes the whole NaN where it is joined), the flag is set,
+// and the warp goes on to the block's barriers as ever.  (156.3 us at 32768 x
+// 7168 with a test of the state at every run's begin, 154.4 with spoil_runs.)
 template <typename TD, typename TG, int VE, int NG, bool ADD, Route R>
 __global__ void __launch_bounds__(kSumThreads, 2)
     k_embed_sum(const TD *dout, int64_t dout_ld, const uint2 *sorted, int64_t T, int64_t V,
@@ -904,11 +917,15 @@ __global__ void __launch_bounds__(kSumThreads, 2)
     auto dst_of = [&](const Rows &x, int r) {
         return reinterpret_cast<TG *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x.dst), r));
     };
+    RingState state; // (warp-uniform)
+    auto wait = [&](int slot, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, bar_wait(smem_addr(&s_bar[w][slot]), parity));
+    };
     // kBatch rows of x from r0 on into their stages of the ring: a lane copies its own token's row
     auto fetch = [&](const Rows &x, int r0) {
-        const int rows_left = x.live - r0;
-        if (rows_left <= 0) return;
-        const uint32_t bar = smem_addr(&s_bar[w][r0 / kBatch % (kStages / kBatch)]);
+        const int rows_left = x.live - r0, slot = r0 / kBatch % (kStages / kBatch);
+        if (rows_left <= 0 || !state.arm(slot)) return;
+        const uint32_t bar = smem_addr(&s_bar[w][slot]);
         const uint32_t db = x.cols * sizeof(TD), gb = x.cols * sizeof(TG);
         const uint32_t mask = (rows_left >= kBatch ? (1u << kBatch) - 1 : (1u << rows_left) - 1) << r0;
         const bool on = mask >> lane & 1, both = ADD && on && (x.direct >> lane & 1);
@@ -939,7 +956,6 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         if (R != kAnywhere) return 0;
         return __shfl_sync(0xffffffffu, (uint32_t)reinterpret_cast<uintptr_t>(p), r) & 15;
     };
-    uint32_t phases = 0; // parity of each barrier's phase
     if (lane < kStages / kBatch) bar_init(smem_addr(&s_bar[w][lane]));
     asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -960,11 +976,23 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         if (more) ahead = rows_of(it + gridDim.x);
         Sums<VE, NG> acc;
         zero(acc);
+        // once a batch did not arrive: NaN for the runs that end from row r0 on, and left in acc
+        auto spoil_runs = [&](int r0) {
+            if (lane == 0 && d_status) atomicOr(d_status, AP_FLAG_CORRUPT);
+            spoil(acc);
+            const Pack<TG, VE> none[NG] = {};
+            for (int r = r0; r < live; ++r) {
+                if (direct >> r & 1)
+                    finish_row(dst_of(cur, r), here, acc, none, scale, false);
+                else if (ends >> r & 1)
+                    store_part(s_part(w), mine, acc);
+            }
+        };
         for (int r0 = 0; r0 < live; r0 += kBatch) {
-            const int slot = r0 / kBatch % (kStages / kBatch);
-            if (!bar_wait(smem_addr(&s_bar[w][slot]), phases >> slot & 1) && d_status)
-                atomicOr(d_status, AP_FLAG_CORRUPT);
-            phases ^= 1u << slot;
+            if (!state.take(r0 / kBatch % (kStages / kBatch), wait)) {
+                spoil_runs(r0);
+                break;
+            }
             const uint8_t *at = ring + r0 % kStages * kStage;
             // the batch's rows, those that end a run, and of them those of this warp alone: in uniform registers,
             // by a reduction, so that the branches on them are uniform

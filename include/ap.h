@@ -53,7 +53,8 @@ typedef int32_t ap_status;
 #define AP_FLAG_RECORD_OVERFLOW 0x4u /* a record needed > max_pages_per_record   */
 #define AP_FLAG_BAD_COUNT 0x8u       /* a segment lay outside the given rows     */
 #define AP_FLAG_BAD_INDEX 0x10u      /* an expert id or row index out of range   */
-#define AP_FLAG_CORRUPT 0x20u        /* a page id read back out of range         */
+#define AP_FLAG_CORRUPT 0x20u        /* a page id read back out of range; rows   */
+                                     /* that did not arrive (embed_backward)     */
 
 /* payload types of dispatch_permute (BF16, E4M3); table, row and gradient
  * types of embed and embed_backward (BF16, F32) */
@@ -317,7 +318,10 @@ ap_status ap_embed(const void *table, int64_t V, int64_t table_ld, int32_t table
  * with an id outside [0, V), which set AP_FLAG_BAD_INDEX in *d_status (may be
  * NULL).  The tokens are sorted by id and each id's rows are added up in an
  * order that depends on the ids and sizes alone, without floating-point
- * atomics: equal inputs give equal bits.
+ * atomics: equal inputs give equal bits.  Many tokens' rows are copied to
+ * shared memory first; should a copy not arrive within a bounded wait (no input
+ * leads to that), AP_FLAG_CORRUPT is set, and the ids whose sums lack rows get
+ * NaN, so that it shows without d_status too.
  *
  *   dout    [T, H] of dout_dtype, rows dout_ld elements apart (device, read)
  *   dtable  [V, H] of dtable_dtype, rows dtable_ld apart (device, written;
