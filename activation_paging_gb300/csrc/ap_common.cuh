@@ -23,6 +23,13 @@ void note_launch();
 // bytes) that fit on the whole GPU at once: SMs x resident blocks per SM.
 // Grid-stride kernels launched with this grid run in exactly one wave.
 int resident_grid(const void *kernel, int threads, size_t smem = 0);
+// Largest cluster of `kernel` (launched with `threads` threads and `smem`
+// dynamic shared bytes) that the SMs of the stream take: `most` blocks (a power
+// of two), or the half, the quarter, ... of it.  A stream of an SM partition has
+// only the partition's SMs, and a partition of 8 to 48 SMs takes no cluster of
+// 16.  Asked for each call, since a stream's handle may name another stream
+// later: 0.2 us.
+int cluster_fit(const void *kernel, int threads, size_t smem, int most, cudaStream_t st);
 
 // Dispatch stages shared by the dispatch entry points (dispatch.cu): argument
 // checks, then the count/rank and scan launches that produce counts, live,

@@ -535,6 +535,7 @@ __global__ void __launch_bounds__(kBalThreads)
     }
 }
 
+// (On an SM partition that takes no cluster of 8 the cluster is smaller, and sums add up in another order.)
 template <int VEC, int N, int W>
 ap_status launch_balance_cluster(const float *logits, int T, int E, int k, int S, int G, const uint8_t *mask, float coef,
                                  int32_t *idx, float *w, int32_t *counts, float *prob, float *slope, float *loss,
@@ -543,13 +544,14 @@ ap_status launch_balance_cluster(const float *logits, int T, int E, int k, int S
     const auto kernel = k_balance_cluster<VEC, N, W>;
     constexpr int kMaxE = VEC * N * kWarp;
     constexpr auto smem_of = [](int e, int per) { return (size_t)((W + 1) * e + 1 + 2 * per * e) * 4; };
-    // one token a warp, in blocks of a portable cluster, while the groups and the warps want them
-    int blocks = 1;
-    while (blocks < kClusterBlocks && (blocks * W < T || blocks < G)) blocks *= 2;
-    const int per = G <= blocks ? blocks / G : 1;
     static const cudaError_t attr = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                          (int)smem_of(kMaxE, kClusterBlocks));
     if (attr != cudaSuccess) return cuda_fail(attr, "route_balance");
+    const int most = cluster_fit((const void *)kernel, W * kWarp, smem_of(E, kClusterBlocks), kClusterBlocks, st);
+    // one token a warp, in blocks of one cluster, while the groups and the warps want them
+    int blocks = 1;
+    while (blocks < most && (blocks * W < T || blocks < G)) blocks *= 2;
+    const int per = G <= blocks ? blocks / G : 1;
     launch_cluster(kernel, blocks, W * kWarp, smem_of(E, per), blocks, st, logits, T, E, k, S, G, per, mask, coef, idx,
                    w, counts, prob, slope, loss);
     AP_CHECK_LAUNCH("route_balance launch");

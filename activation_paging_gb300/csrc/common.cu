@@ -89,6 +89,27 @@ int resident_grid(const void *kernel, int threads, size_t smem)
     return per_sm * sm_count();
 }
 
+int cluster_fit(const void *kernel, int threads, size_t smem, int most, cudaStream_t st)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = threads;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    for (; most > 1; most /= 2) {
+        int n = 0;
+        attr[0].val.clusterDim.x = most;
+        cfg.gridDim = most;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) break;
+        (void)cudaGetLastError();
+    }
+    return most;
+}
+
 } // namespace ap
 
 extern "C" const char *ap_status_str(ap_status s)

@@ -370,7 +370,7 @@ __device__ __forceinline__ void mark_seen(uint32_t *seen, uint32_t key, int64_t 
     if ((same >> lane_id()) == 1u && key != (uint32_t)V) atomicOr(seen + (key >> 5), 1u << (key & 31));
 }
 
-// One cluster sorts up to kClusterMax tokens in one launch, in registers and
+// One cluster sorts up to 16 x 8192 tokens in one launch, in registers and
 // (distributed) shared memory.  Block r holds tokens r * per .. r * per + per - 1
 // of the current order, warp q of it a run of 32 * ITEMS.  A pass: every warp
 // ranks its tokens per digit; the warps' counts are added up per digit; every
@@ -382,8 +382,8 @@ __device__ __forceinline__ void mark_seen(uint32_t *seen, uint32_t key, int64_t 
 constexpr int kClThreads = 1024;
 constexpr int kClWarps = kClThreads / kWarp;
 constexpr int kClItemsMax = 8;
-constexpr int kClBlocksMax = 16; // 8 is the largest portable cluster, and what is used where 16 do not fit
-constexpr int64_t kClusterMax = (int64_t)kClBlocksMax * kClThreads * kClItemsMax;
+constexpr int kClBlocksMax = 16; // 8 is the largest portable cluster; fewer are used where 16 do not fit
+constexpr int64_t kClBlockTokens = (int64_t)kClThreads * kClItemsMax;
 
 // Dynamic shared memory: the block's tokens, the warps' counts, the blocks' totals.
 constexpr size_t cluster_smem(int items, int bits, int blocks)
@@ -573,8 +573,8 @@ __global__ void __launch_bounds__(kSortThreads)
 // Exclusive sum of n counts in place, by one cluster: kScanItems counts a
 // thread, the blocks' totals exchanged through shared memory.  (One block took
 // 1.2 us for every 1024 counts: 300 of 490 us at 500000 tokens.)
-constexpr int kScanItems = 16, kScanBlocks = 8;
-__global__ void __launch_bounds__(1024) k_sort_scan(uint32_t *hist, int64_t n)
+constexpr int kScanItems = 16, kScanBlocks = 8, kScanThreads = 1024;
+__global__ void __launch_bounds__(kScanThreads) k_sort_scan(uint32_t *hist, int64_t n)
 {
     cluster_arrive();
     pdl_begin();
@@ -583,8 +583,8 @@ __global__ void __launch_bounds__(1024) k_sort_scan(uint32_t *hist, int64_t n)
     const uint32_t me = blockIdx.x, blocks = gridDim.x; // the grid is one cluster
     uint32_t carry = 0;
     cluster_wait(); // all blocks have started
-    for (int64_t base = 0, turn = 0; base < n; base += (int64_t)blocks * 1024 * kScanItems, ++turn) {
-        const int64_t i0 = base + ((int64_t)me * 1024 + threadIdx.x) * kScanItems;
+    for (int64_t base = 0, turn = 0; base < n; base += (int64_t)blocks * kScanThreads * kScanItems, ++turn) {
+        const int64_t i0 = base + ((int64_t)me * kScanThreads + threadIdx.x) * kScanItems;
         uint32_t v[kScanItems], sum = 0;
 #pragma unroll
         for (int i = 0; i < kScanItems; ++i) v[i] = i0 + i < n ? hist[i0 + i] : 0u;
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(1024) k_sort_scan(uint32_t *hist, int64_t n)
         if (lane == 31) s_warp[wid] = x;
         __syncthreads();
         const uint32_t lower = __reduce_add_sync(0xffffffffu, lane < wid ? s_warp[lane] : 0u);
-        if (threadIdx.x == 1023)
+        if (threadIdx.x == kScanThreads - 1)
             for (uint32_t r = 0; r < blocks; ++r) cluster_store(cluster_addr(smem_addr(&s_tot[turn & 1][me]), r), lower + x);
         cluster_sync(); // (the totals of the turn before are not written again until the next one)
         uint32_t at = carry + lower + x - sum;
@@ -1366,7 +1366,8 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int32_t H)
     while (bits < 32 && (V >> bits)) ++bits; // keys 0 .. V
     p.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
     p.bits = (bits + p.passes - 1) / p.passes;
-    p.tiles = T > kClusterMax / 2 ? (T + kSortTile - 1) / kSortTile : 0; // (half: clusters of 8)
+    // (a call's cluster may have fewer blocks than 16: the passes over memory have room from one block's tokens on)
+    p.tiles = T > kClBlockTokens ? (T + kSortTile - 1) / kSortTile : 0;
     // the longest tiles that still give kWantItems blocks work (pieces of 256 columns): half as long, they take 169 us
     // for 156 at 32768 x 7168 and 29.2 for 28.3 at 8192 x 2048, since the warps of a block wait for one another per tile
     const int64_t pieces = ((int64_t)H + 255) / 256;
@@ -1385,9 +1386,8 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int32_t H)
     return p;
 }
 
-template <int ITEMS>
-ap_status sort_cluster(const void *ids, bool wide, int64_t T, int64_t V, int64_t pad, const EmbedPlan &p, int blocks,
-                       uint2 *sorted, uint32_t *seen, uint32_t *d_status, cudaStream_t st)
+// Lets k_sort_cluster<ITEMS> have its shared memory and clusters of 16.
+template <int ITEMS> cudaError_t sort_attributes()
 {
     static const cudaError_t attr = [] {
         const void *k = (const void *)k_sort_cluster<ITEMS>;
@@ -1395,38 +1395,19 @@ ap_status sort_cluster(const void *ids, bool wide, int64_t T, int64_t V, int64_t
                                                    (int)cluster_smem(ITEMS, kMaxDigitBits, kClBlocksMax));
         return e != cudaSuccess ? e : cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     }();
+    return attr;
+}
+
+template <int ITEMS>
+ap_status sort_cluster(const void *ids, bool wide, int64_t T, int64_t V, int64_t pad, const EmbedPlan &p, int blocks,
+                       uint2 *sorted, uint32_t *seen, uint32_t *d_status, cudaStream_t st)
+{
+    const cudaError_t attr = sort_attributes<ITEMS>();
     if (attr != cudaSuccess) return cuda_fail(attr, "embed_backward sort");
     launch_cluster(k_sort_cluster<ITEMS>, blocks, kClThreads, cluster_smem(ITEMS, p.bits, blocks), blocks, st, ids,
                    wide, (int)T, (int)((T + blocks - 1) / blocks), V, pad, p.passes, p.bits, sorted, seen, d_status);
     AP_CHECK_LAUNCH("embed_backward sort launch");
     return AP_OK;
-}
-
-// The largest cluster that this GPU takes with the sort's largest shared memory.
-int cluster_blocks()
-{
-    static const int most = [] {
-        const void *k = (const void *)k_sort_cluster<kClItemsMax>;
-        const size_t smem = cluster_smem(kClItemsMax, kMaxDigitBits, kClBlocksMax);
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = kClBlocksMax;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = kClBlocksMax;
-        cfg.blockDim = kClThreads;
-        cfg.dynamicSmemBytes = smem;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        const bool ok =
-            cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess &&
-            cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-            cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess && n > 0;
-        if (!ok) (void)cudaGetLastError();
-        return ok ? kClBlocksMax : kClBlocksMax / 2;
-    }();
-    return most;
 }
 
 // Sorts the tokens into one of the two buffers at `sc`; *sorted is set to it.
@@ -1436,8 +1417,11 @@ ap_status sort_tokens(const void *ids, bool wide, int64_t T, int64_t V, int64_t 
 {
     uint2 *buf[2] = {reinterpret_cast<uint2 *>(sc), reinterpret_cast<uint2 *>(sc + p.off_b)};
     *sorted = buf[0];
-    const int most = cluster_blocks();
-    if (T <= (int64_t)most * kClThreads * kClItemsMax) { // 131072 x 512: 87 us in all, with the passes below 137
+    const cudaError_t attr = sort_attributes<kClItemsMax>();
+    if (attr != cudaSuccess) return cuda_fail(attr, "embed_backward sort");
+    const int most = cluster_fit((const void *)k_sort_cluster<kClItemsMax>, kClThreads,
+                                 cluster_smem(kClItemsMax, kMaxDigitBits, kClBlocksMax), kClBlocksMax, st);
+    if (T <= most * kClBlockTokens) { // 131072 x 512: 87 us in all, with the passes below 137
         int blocks = 1;
         while (blocks < most && (int64_t)blocks * kClThreads < T) blocks *= 2;
         const int64_t each = ((T + blocks - 1) / blocks + kClThreads - 1) / kClThreads; // tokens per thread
@@ -1447,12 +1431,13 @@ ap_status sort_tokens(const void *ids, bool wide, int64_t T, int64_t V, int64_t 
         return sort_cluster<8>(ids, wide, T, V, pad, p, blocks, buf[0], seen, d_status, st);
     }
     uint32_t *hist = reinterpret_cast<uint32_t *>(sc + p.off_hist);
+    const int scan = cluster_fit((const void *)k_sort_scan, kScanThreads, 0, kScanBlocks, st);
     for (int q = 0; q < p.passes; ++q) {
         const uint2 *in = q ? buf[(q - 1) & 1] : nullptr;
         launch(k_sort_count, (int)p.tiles, kSortThreads, 0, st, in, ids, wide, T, V, pad, q * p.bits, p.bits, hist,
                q == 0 ? seen : nullptr, d_status);
         AP_CHECK_LAUNCH("embed_backward count launch");
-        launch_cluster(k_sort_scan, kScanBlocks, 1024, 0, kScanBlocks, st, hist, p.tiles << p.bits);
+        launch_cluster(k_sort_scan, scan, kScanThreads, 0, scan, st, hist, p.tiles << p.bits);
         AP_CHECK_LAUNCH("embed_backward scan launch");
         launch(k_sort_scatter, (int)p.tiles, kSortThreads, 0, st, in, ids, wide, T, V, pad, q * p.bits, p.bits, hist,
                buf[q & 1], q + 1 == p.passes ? seen : nullptr);
