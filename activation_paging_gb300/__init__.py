@@ -105,6 +105,18 @@ def _mask(mask: torch.Tensor | None, T: int):
     return _need_shape(mask, mask.dtype, (T,), "mask")
 
 
+def _status(status: torch.Tensor | None):
+    """Address of a status word: 32 bits on the GPU, of whatever type."""
+    if status is None:
+        return None
+    if not status.is_cuda:
+        raise ValueError("status must be a CUDA tensor")
+    p = status.data_ptr()
+    if status.numel() * status.element_size() < 4 or p & 3:
+        raise ValueError("status must hold an aligned 32-bit word")
+    return p
+
+
 @functools.lru_cache(maxsize=1024)
 def route_balance_scratch_bytes(T: int, E: int, group_tokens: int = 0) -> int:
     n = ctypes.c_int64(0)
@@ -145,6 +157,8 @@ def route_balance(logits: torch.Tensor, k: int, coef: float = 1.0, group_tokens:
             else:
                 o[name] = _empty(shape, dtype, dev, stream)
     scratch = o.get("scratch")
+    if scratch is not None:
+        _need(scratch, scratch.dtype, "scratch")
     if sb and (scratch is None or scratch.numel() < sb):
         scratch = o["scratch"] = _empty(sb, torch.uint8, dev, stream)
     check(lib().ap_route_balance(logits.data_ptr(), T, E, k, group_tokens, m, coef, o["idx"].data_ptr(),
@@ -183,7 +197,7 @@ def route_backward(logits: torch.Tensor, idx: torch.Tensor | None = None, w: tor
         dlogits = _empty((T, E), torch.float32, logits.device, stream)
     else:
         _need_shape(dlogits, torch.float32, (T, E), "dlogits")
-    check(lib().ap_route_backward(_p(logits), T, E, k, pi, pw, pdw, ps, pl, group_tokens, m, _p(dlogits), _p(status),
+    check(lib().ap_route_backward(_p(logits), T, E, k, pi, pw, pdw, ps, pl, group_tokens, m, _p(dlogits), _status(status),
                                   _stream(stream)), "route_backward")
     return dlogits
 
@@ -238,7 +252,7 @@ def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, dtype: tor
         n, h, out_ld, out_kind = _rows(out, "out")
         if n != T or h != H:
             raise ValueError(f"out must be {[T, H]}, got {[n, h]}")
-    check(lib().ap_embed(_p(table), V, ld, kind, _p(ids), size, T, H, scale, _p(out), out_ld, out_kind, _p(status),
+    check(lib().ap_embed(_p(table), V, ld, kind, _p(ids), size, T, H, scale, _p(out), out_ld, out_kind, _status(status),
                          _stream(stream)), "embed")
     return out
 
@@ -281,8 +295,8 @@ def embed_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: float =
             scratch = _empty(sb, torch.uint8, dout.device, stream)
     check(lib().ap_embed_backward(_p(dout), ld, kind, _p(ids), size, T, H, V,
                                   -1 if padding_idx is None else padding_idx, scale, 1 if accumulate else 0, _p(dtable),
-                                  g_ld, g_kind, _p(scratch), scratch.numel() if scratch is not None else 0, _p(status),
-                                  _stream(stream)), "embed_backward")
+                                  g_ld, g_kind, _p(scratch), scratch.numel() if scratch is not None else 0,
+                                  _status(status), _stream(stream)), "embed_backward")
     return dtable
 
 
