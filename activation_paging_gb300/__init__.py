@@ -182,6 +182,8 @@ def route_backward(logits: torch.Tensor, idx: torch.Tensor | None = None, w: tor
     if dw is not None:
         if idx is None or w is None:
             raise ValueError("dw needs idx and w")
+        if dw.dim() != 2:
+            raise ValueError(f"dw must be [T, k], got {list(dw.shape)}")
         k = dw.shape[1]
         pdw = _need_shape(dw, torch.float32, (T, k), "dw")
         pi = _need_shape(idx, torch.int32, (T, k), "idx")

@@ -46,3 +46,10 @@ def test_work_space_of_routing():
     for dtype in (torch.uint8, torch.float32):
         kept = torch.empty(n, dtype=dtype, device="cuda")
         assert ap.route_balance(logits, 2, out={"scratch": kept})["scratch"] is kept
+
+
+def test_gradient_of_the_weights_has_two_dimensions():
+    logits = torch.zeros(4, 8, device="cuda")
+    r = ap.route_balance(logits, 1)
+    with pytest.raises(ValueError, match="dw"):
+        ap.route_backward(logits, r["idx"], r["w"], r["w"][:, 0])
