@@ -4,7 +4,9 @@
 // bound by HBM (16384 x 2048 BF16 rows of a 151936-row table: 95 MB in 18 us).
 //
 // Gradient: dtable[v] (+)= scale * sum over the tokens with id v of dout[t].
-// Up to 1024 tokens take one launch (k_embed_small), more take three:
+// Up to 1024 tokens take one launch (k_embed_small), more take three (beyond
+// what one cluster sorts, 131072 tokens as a rule, the sort takes three for
+// each of its one to four digits):
 //   1. The tokens are sorted by id (stable radix sort, least significant digit
 //      first; ids that do not count sort last), so an id's tokens are one run
 //      in token order.
@@ -19,9 +21,10 @@
 // No floating-point atomics: every sum has one order, fixed by ids and sizes.
 // Each row of dout is read once, each row of dtable that an id names read and
 // written once, beside the partial rows (at most 2 of single precision for
-// every 256 rows).  Sums are bound by HBM where there is much to add (32768 x
-// 7168, 30% padding: 154 us, 828 MB); at 8192 x 2048 the sort takes 8 us of
-// the 25, the sums 14 (of which 4 to start and to join), the join 3.
+// every tile, 256 rows where there are many and 32 at the least).  Sums are
+// bound by HBM where there is much to add (32768 x 7168, 30% padding: 154 us,
+// 828 MB); at 8192 x 2048 the sort takes 8 us of the 25, the sums 14 (of which
+// 4 to start and to join), the join 3.
 #include <cuda_bf16.h>
 
 #include "ap_common.cuh"

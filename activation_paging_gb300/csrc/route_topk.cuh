@@ -114,7 +114,8 @@ struct TopkSlots {
 // each, ranked by counting, and put in rank order.  Where more than 32 reach
 // it (ties, or many large logits in one lane) or fewer than k do (NaN,
 // -infinity), the rounds above run instead.  Results are select_token's, bit
-// for bit.  v[i][c]: the logit of expert (lane + 32 i) * VEC + c, -infinity
+// for bit, for rows of numbers (infinities among them); of a row that holds NaN
+// other experts may be chosen.  v[i][c]: the logit of expert (lane + 32 i) * VEC + c, -infinity
 // beyond E.
 template <int VEC, int N>
 __device__ __forceinline__ void select_token_slots(const float (&v)[N][VEC], int E, int k, int lane, TopkSlots &s,

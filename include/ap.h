@@ -231,11 +231,11 @@ ap_status ap_dispatch_backward(const void *dxd, int64_t rows, int32_t H,
 /* ============================================================================
  * route_balance
  *
- * Routing with its balance loss (no counterpart on the pages).  idx and w are
- * exactly those of ap_route_topk.  The T tokens
- * form G = ceil(T / group_tokens) groups of group_tokens consecutive tokens
- * (a batch's sequences; the last group may be shorter; group_tokens = 0: one
- * group of all T).  A token counts when mask is NULL or mask[t] != 0 and its
+ * Routing with its balance loss (no counterpart on the pages).  For finite
+ * logits idx and w are exactly those of ap_route_topk.  The T tokens form
+ * G = ceil(T / group_tokens) groups of group_tokens consecutive tokens (a
+ * batch's sequences; the last group may be shorter; group_tokens = 0: one group
+ * of all T).  A token counts when mask is NULL or mask[t] != 0 and its
  * row holds a number above -infinity.  For group g with n_g such tokens, their
  * softmax rows p[t] over the E experts and their chosen pairs:
  *   counts[g, e] = pairs (t, j) with idx[t, j] = e
@@ -245,8 +245,12 @@ ap_status ap_dispatch_backward(const void *dxd, int64_t rows, int32_t H,
  *                  d loss / d p[t, e] for every such token t of group g
  * (counts are constants of the loss, as usual).  A group without such a token
  * has counts, prob and slope 0 and adds nothing to the loss.  Masked tokens
- * are routed all the same; what their logits hold reaches no sum.  Sums are
- * single precision in an order that depends on the sizes alone, so equal
+ * are routed all the same (ids in [0, E) whatever their logits hold, NaN
+ * included); what their logits hold reaches no sum.  A softmax value whose
+ * logit lies d below its row's largest has a relative error of at most
+ * (2.2 d + 17 + E / 32) 2^-24 (below 2^-126 it may be 0).  Sums are single
+ * precision in an order that depends on the sizes alone (few tokens on an SM
+ * partition without room for a cluster of 8 blocks: on that too), so equal
  * inputs give equal bits.  For a loss over the counts of several calls or
  * GPUs, add up counts and form slope from the sums; prob and loss are this
  * call's.
