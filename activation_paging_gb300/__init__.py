@@ -8,6 +8,8 @@ raises.
 
     embed             rows of an embedding table, scaled (and embed_backward)
     route_topk        softmax -> top-k -> renormalised weights
+    route_scored      top k by softmax or sigmoid scores, a balancing bias and groups
+                      (and route_scored_backward, route_bias_step)
     route_balance     route_topk with a balance loss and per-expert counts
                       (and route_backward, the logits' gradient)
     dispatch_permute  expert-major, capacity-bounded permutation (BF16 / E4M3)
@@ -35,7 +37,7 @@ FLAG_CORRUPT = 0x20
 DTYPE_BF16, DTYPE_E4M3, DTYPE_F32 = 0, 1, 2
 
 __all__ = ["embed", "embed_backward", "embed_scratch_bytes", "route_balance", "route_balance_scratch_bytes",
-           "route_backward", "route_topk", "dispatch_permute", "dispatch_scratch_bytes", "combine_unpermute", "combine_backward",
+           "route_backward", "route_scored", "route_scored_backward", "route_bias_step", "route_topk", "dispatch_permute", "dispatch_scratch_bytes", "combine_unpermute", "combine_backward",
            "dispatch_backward", "cast_e4m3", "Pool", "Arena", "APError", "lib", "launch_count"]
 
 
@@ -202,6 +204,81 @@ def route_backward(logits: torch.Tensor, idx: torch.Tensor | None = None, w: tor
     check(lib().ap_route_backward(_p(logits), T, E, k, pi, pw, pdw, ps, pl, group_tokens, m, _p(dlogits), _status(status),
                                   _stream(stream)), "route_backward")
     return dlogits
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score: str) -> int:
+    kind = _SCORES.get(score)
+    if kind is None:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return kind
+
+
+def route_scored(logits: torch.Tensor, k: int, score: str = "sigmoid", bias: torch.Tensor | None = None, groups: int = 1,
+                 top_groups: int = 1, group_best: int = 2, renorm: bool = True, scale: float = 1.0,
+                 mask: torch.Tensor | None = None, counts: torch.Tensor | None = None, idx: torch.Tensor | None = None,
+                 w: torch.Tensor | None = None, stream=None):
+    """``idx`` [T, k] int32 and ``w`` [T, k] float32 for float32 logits [T, E]:
+    the k largest of score + ``bias`` ([E] float32) in the ``top_groups`` of
+    ``groups`` groups of experts whose ``group_best`` (1 or 2) largest have the
+    largest sum.  The weights are the chosen scores themselves (``softmax`` or
+    ``sigmoid`` of the logits), with ``renorm`` divided by their sum, times
+    ``scale``.  ``counts`` ([E] int32): the pairs of each expert are added to
+    it, of tokens that ``mask`` ([T] bool or uint8) lets count; see
+    ``route_bias_step``."""
+    kind = _score(score)
+    _need(logits, torch.float32, "logits")
+    T, E = logits.shape
+    m = _mask(mask, T)
+    if groups == 1:
+        group_best = 1
+    pb = None if bias is None else _need_shape(bias, torch.float32, (E,), "bias")
+    pc = None if counts is None else _need_shape(counts, torch.int32, (E,), "counts")
+    if idx is None:
+        idx = _empty((T, k), torch.int32, logits.device, stream)
+    if w is None:
+        w = _empty((T, k), torch.float32, logits.device, stream)
+    check(lib().ap_route_scored(logits.data_ptr(), T, E, k, kind, pb, groups, top_groups, group_best, 1 if renorm else 0, scale,
+                                m, _need_shape(idx, torch.int32, (T, k), "idx"), _need_shape(w, torch.float32, (T, k), "w"), pc,
+                                _stream(stream)), "route_scored")
+    return idx, w
+
+
+def route_scored_backward(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Tensor, score: str = "sigmoid",
+                          renorm: bool = True, scale: float = 1.0, dlogits: torch.Tensor | None = None,
+                          status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dlogits [T, E] float32 of ``route_scored`` from the gradient ``dw``
+    [T, k] of its weights."""
+    kind = _score(score)
+    _need(logits, torch.float32, "logits")
+    T, E = logits.shape
+    if dw.dim() != 2:
+        raise ValueError(f"dw must be [T, k], got {list(dw.shape)}")
+    k = dw.shape[1]
+    pw = _need_shape(dw, torch.float32, (T, k), "dw")
+    pi = _need_shape(idx, torch.int32, (T, k), "idx")
+    if dlogits is None:
+        dlogits = _empty((T, E), torch.float32, logits.device, stream)
+    else:
+        _need_shape(dlogits, torch.float32, (T, E), "dlogits")
+    check(lib().ap_route_scored_backward(logits.data_ptr(), T, E, k, pi, pw, kind, 1 if renorm else 0, scale,
+                                         dlogits.data_ptr(), _status(status), _stream(stream)), "route_scored_backward")
+    return dlogits
+
+
+def route_bias_step(bias: torch.Tensor, counts: torch.Tensor, rate: float, reset: bool = False, stream=None) -> torch.Tensor:
+    """Moves ``bias`` ([E] float32) by ``rate`` up where an expert has fewer
+    than its share of ``counts`` ([E] int32), down where more; ``reset`` zeroes
+    the counts."""
+    _need(bias, torch.float32, "bias")
+    if bias.dim() != 1:
+        raise ValueError("bias must be [E]")
+    E = bias.shape[0]
+    check(lib().ap_route_bias_step(bias.data_ptr(), _need_shape(counts, torch.int32, (E,), "counts"), E, rate,
+                                   1 if reset else 0, _stream(stream)), "route_bias_step")
+    return bias
 
 
 _ROW_TYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}

@@ -49,6 +49,9 @@ SIGNATURES = {
     "ap_route_balance_scratch_bytes": (i32, [i64, i32, i64, P]),
     "ap_route_balance": (i32, [P, i64, i32, i32, i64, P, f32, P, P, P, P, P, P, P, i64, P]),
     "ap_route_backward": (i32, [P, i64, i32, i32, P, P, P, P, P, i64, P, P, P, P]),
+    "ap_route_scored": (i32, [P, i64, i32, i32, i32, P, i32, i32, i32, i32, f32, P, P, P, P, P]),
+    "ap_route_scored_backward": (i32, [P, i64, i32, i32, P, P, i32, i32, f32, P, P, P]),
+    "ap_route_bias_step": (i32, [P, P, i32, f32, i32, P]),
     "ap_embed": (i32, [P, i64, i64, i32, P, i32, i64, i32, f32, P, i64, i32, P, P]),
     "ap_embed_scratch_bytes": (i32, [i64, i64, i32, P]),
     "ap_embed_backward": (i32, [P, i64, i32, P, i32, i64, i32, i64, i64, f32, i32, P, i64, i32, P, i64, P, P]),

@@ -42,13 +42,12 @@ __device__ __forceinline__ bool before(uint32_t ka, int ea, uint32_t kb, int eb)
 // redux.sync reductions (max key, then min id among equal keys); the winning
 // lane shifts its list.  All 32 lanes call it with their candidates (a lane
 // without one holds key 0 and id kNoExpert); lane j < k receives the j-th
-// expert in *e and its renormalised weight in *wt, every lane the largest
-// logit in *top.
+// winner's key and id.
 constexpr int kNoExpert = 0x7fffffff;
 
 template <int NV>
-__device__ __forceinline__ void select_token(uint32_t (&key)[NV], int (&ex)[NV], int k, int lane, int *e, float *wt,
-                                             float *top)
+__device__ __forceinline__ void choose_rounds(uint32_t (&key)[NV], int (&ex)[NV], int k, int lane, uint32_t *my_key,
+                                              int *my_e)
 {
 #pragma unroll
     for (int r = 0; r < NV; ++r) {
@@ -64,8 +63,8 @@ __device__ __forceinline__ void select_token(uint32_t (&key)[NV], int (&ex)[NV],
             }
         }
     }
-    uint32_t my_key = 0;
-    int my_e = 0;
+    *my_key = 0;
+    *my_e = 0;
     for (int j = 0; j < k; ++j) {
         const uint32_t m = __reduce_max_sync(0xffffffffu, key[0]);
         const int emin = __reduce_min_sync(0xffffffffu, key[0] == m ? ex[0] : kNoExpert);
@@ -79,18 +78,33 @@ __device__ __forceinline__ void select_token(uint32_t (&key)[NV], int (&ex)[NV],
             ex[NV - 1] = kNoExpert;
         }
         if (lane == j) {
-            my_key = m;
-            my_e = emin;
+            *my_key = m;
+            *my_e = emin;
         }
     }
-    const float mv = key_value(__shfl_sync(0xffffffffu, my_key, 0)); // the largest logit
-    const float z = (lane < k) ? expf(key_value(my_key) - mv) : 0.f;
+}
+
+// The softmax over the chosen logits (lane j < k holds the j-th, top is the
+// largest of all).
+__device__ __forceinline__ float chosen_weight(float logit, float top, int k, int lane)
+{
+    const float z = (lane < k) ? expf(logit - top) : 0.f;
     float s = z;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    *e = my_e;
-    *wt = __fdiv_rn(z, s);
-    *top = mv;
+    return __fdiv_rn(z, s);
+}
+
+// choose_rounds, with lane j's renormalised weight in *wt and the largest logit
+// in every lane's *top.
+template <int NV>
+__device__ __forceinline__ void select_token(uint32_t (&key)[NV], int (&ex)[NV], int k, int lane, int *e, float *wt,
+                                             float *top)
+{
+    uint32_t my_key;
+    choose_rounds<NV>(key, ex, k, lane, &my_key, e);
+    *top = key_value(__shfl_sync(0xffffffffu, my_key, 0));
+    *wt = chosen_weight(key_value(my_key), *top, k, lane);
 }
 
 // The largest of the lanes' values (NaN aside).
@@ -107,19 +121,21 @@ struct TopkSlots {
     float2 sel[kWarp];
 };
 
-// The same selection in about half the instructions for rows of 128 and more
+// The choice of choose_rounds in about half the instructions for rows of 128 and more
 // experts, with a little shared memory.  The k-th largest of the lanes' maxima
 // bounds the k-th largest logit from below, so only logits that reach it can
 // be chosen: little more than k of them as a rule.  They are moved to one lane
 // each, ranked by counting, and put in rank order.  Where more than 32 reach
 // it (ties, or many large logits in one lane) or fewer than k do (NaN,
-// -infinity), the rounds above run instead.  Results are select_token's, bit
+// -infinity), the rounds above run instead.  Results are the rounds', bit
 // for bit, for rows of numbers (infinities among them); of a row that holds NaN
 // other experts may be chosen.  v[i][c]: the logit of expert (lane + 32 i) * VEC + c, -infinity
 // beyond E.
+// Lane j < k receives the j-th value and its id, every lane the
+// largest value in *top.  The slots are free again after a __syncwarp().
 template <int VEC, int N>
-__device__ __forceinline__ void select_token_slots(const float (&v)[N][VEC], int E, int k, int lane, TopkSlots &s,
-                                                   int *e, float *wt, float *top)
+__device__ __forceinline__ void choose_token_slots(const float (&v)[N][VEC], int E, int k, int lane, TopkSlots &s,
+                                                   int *e, float *value, float *top)
 {
     float cur = -INFINITY;
 #pragma unroll
@@ -156,7 +172,10 @@ __device__ __forceinline__ void select_token_slots(const float (&v)[N][VEC], int
                 key[i * VEC + c] = id < E ? order_key(v[i][c]) : 0u;
                 ex[i * VEC + c] = id < E ? id : kNoExpert;
             }
-        select_token<N * VEC>(key, ex, k, lane, e, wt, top);
+        uint32_t my_key;
+        choose_rounds<N * VEC>(key, ex, k, lane, &my_key, e);
+        *value = key_value(my_key);
+        *top = __shfl_sync(0xffffffffu, *value, 0);
         return;
     }
     float2 *at = s.cand + (upto - own);
@@ -183,13 +202,19 @@ __device__ __forceinline__ void select_token_slots(const float (&v)[N][VEC], int
     if (lane < n && rank < k) s.sel[rank] = mine;
     __syncwarp();
     const float2 chosen = s.sel[lane < k ? lane : 0];
-    const float z = (lane < k) ? expf(chosen.x - first) : 0.f;
-    float sum = z;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     *e = __float_as_int(chosen.y);
-    *wt = __fdiv_rn(z, sum);
+    *value = chosen.x;
     *top = first;
+}
+
+// choose_token_slots, with lane j's renormalised weight.
+template <int VEC, int N>
+__device__ __forceinline__ void select_token_slots(const float (&v)[N][VEC], int E, int k, int lane, TopkSlots &s,
+                                                   int *e, float *wt, float *top)
+{
+    float value;
+    choose_token_slots<VEC, N>(v, E, k, lane, s, e, &value, top);
+    *wt = chosen_weight(value, *top, k, lane);
     __syncwarp(); // the slots are free for the next token
 }
 

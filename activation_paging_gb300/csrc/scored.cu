@@ -1,0 +1,614 @@
+// Routing by scores, with a bias that balances the experts and with groups of
+// experts, the gradient of its logits, and the step of the bias.
+//
+// Forward.  Scores s = softmax(l) or sigmoid(l); the choice goes by c = s + bias:
+// of the groups of E / groups consecutive experts the top_groups with the
+// largest sum of their one or two best c, in them the k largest c.  The weights
+// are the scores themselves, without the bias: scale * s_j [/ sum_sel s].
+// One warp per token, one pass: the row stays in registers, its choices go
+// through shared memory for the groups' sums, and the selection is the one of
+// the other routers (route_topk.cuh).
+// Choices that are near one another in single precision are not settled there:
+// where the order of two that matter (neighbours among the k, the border behind
+// them, the border between groups) lies within the error bounds below, the
+// token is chosen again in double precision (choose_exactly), about one token
+// in a thousand.  So ids do not depend on how single precision rounds.  Without
+// a bias, and with groups that go by their best expert, the logits themselves
+// have the scores' order and nothing is near.
+//
+// Backward.  With q the chosen scores and u_j = dw_j - sum_i w_i dw_i / scale:
+//   sigmoid, renormalised   dl_j = scale q_j / S (1 - sigma_j) u_j
+//   sigmoid                 dl_j = scale sigma_j (1 - sigma_j) dw_j
+//   softmax, renormalised   dl_j = scale q_j / S u_j
+//   softmax                 dl_e = p_e (scale dw_e - sum_j p_j scale dw_j), all experts
+// The first three touch k logits of a row and write zeros beside.
+#include "route_topk.cuh"
+
+namespace ap {
+namespace {
+
+constexpr int kScWarps = 8;
+constexpr int kScThreads = kScWarps * kWarp;
+constexpr float kUlp = 5.9604645e-8f; // 2^-24
+
+struct ScoredArgs {
+    const float *logits, *bias;
+    const uint8_t *mask;
+    int32_t *idx;
+    float *w;
+    int32_t *counts;
+    int64_t T;
+    int E, k;
+    int groups, size, top_groups, best; // size: experts of a group
+    uint32_t inv_size;                  // ceil(2^20 / size): e / size = e * inv_size >> 20 for e < 1024
+    float scale;
+    bool sigmoid, renorm;
+};
+
+template <int VEC> struct ScVec;
+template <> struct ScVec<4> { using T = float4; };
+template <> struct ScVec<1> { using T = float; };
+
+// 2^(x log2 e): relative error (1.5 |x| + 4) 2^-24.
+__device__ __forceinline__ float exp_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// Single errors of a choice, with which two of them are near: a sigmoid by
+// exp_fast, an addition and a reciprocal has at most s (1 - s) (1.5 |x| + 4) u
+// + 3 u s <= 4.4 u, a softmax value at most (2.2 d + 17 + E / 32) u of itself,
+// d e^-d <= 1 / e of the largest: 50 u of that one.  Adding the bias rounds by
+// u |c|.  near() bounds the two of a pair.
+__device__ __forceinline__ float near_of(bool sigmoid, float p_top, float c)
+{
+    return (sigmoid ? 16.f * kUlp : 128.f * kUlp * p_top) + 4.f * kUlp * fabsf(c);
+}
+
+// The two largest of a group's values, over the lanes that share the group.
+template <typename F> struct Best2 {
+    F first, second;
+    __device__ __forceinline__ void take(F v)
+    {
+        const F low = v > first ? first : v;
+        second = low > second ? low : second;
+        first = v > first ? v : first;
+    }
+};
+
+// Which groups are in: bit (g * lanes) of the result is set for group g.  `row`
+// holds the warp's choices; every group has `lanes` lanes.  *near: the border
+// between the groups lies within the errors.
+template <typename F>
+__device__ __forceinline__ uint32_t choose_groups(const F *row, const ScoredArgs &a, int lane, int lanes, float p_top,
+                                                  bool *near)
+{
+    const int g = lane / lanes, sub = lane - g * lanes;
+    Best2<F> b = {(F)-INFINITY, (F)-INFINITY};
+    if (g < a.groups) {
+        // the groups begin at different places of theirs, so that groups of 32 experts meet different banks
+        const int n = (a.size - sub + lanes - 1) / lanes;
+        int i = n > 0 ? g % n : 0;
+        for (int c = 0; c < n; ++c) {
+            b.take(row[g * a.size + sub + i * lanes]);
+            if (++i == n) i = 0;
+        }
+    }
+    for (int off = 1; off < lanes; off <<= 1) {
+        const F o1 = __shfl_xor_sync(0xffffffffu, b.first, off), o2 = __shfl_xor_sync(0xffffffffu, b.second, off);
+        b.take(o1);
+        b.take(o2);
+    }
+    F score = a.best == 2 ? b.first + b.second : b.first;
+    if (!(score == score)) score = (F)-INFINITY;
+    int rank = 0;
+    for (int h = 0; h < a.groups; ++h) {
+        const F o = __shfl_sync(0xffffffffu, score, h * lanes);
+        rank += o > score || (o == score && h < g);
+    }
+    const bool in = g < a.groups && rank < a.top_groups;
+    if (near) {
+        float err = a.best == 2 ? near_of(a.sigmoid, p_top, (float)b.first) + near_of(a.sigmoid, p_top, (float)b.second)
+                                : near_of(a.sigmoid, p_top, (float)b.first);
+        if (!(err < INFINITY)) err = 0.f; // of -infinity: nothing rounds
+        const float least = -reduce_max(in ? -((float)score - err) : -INFINITY);
+        const float most = reduce_max(g < a.groups && !in ? (float)score + err : -INFINITY);
+        *near = most >= least && most > -INFINITY;
+    }
+    return __ballot_sync(0xffffffffu, in);
+}
+
+// The choice in double precision: the row's scores anew, the groups, then k
+// rounds over the warp's choices in shared memory.  Lane j < k receives the
+// j-th id, and whether it may be chosen at all.
+__device__ __noinline__ void choose_exactly(const ScoredArgs &a, int64_t t, double *row, int lanes, bool odd, int *e,
+                                            bool *in)
+{
+    const int lane = (int)lane_id();
+    const float *logits = a.logits + t * a.E;
+    double top = 0.0, inv = 0.0;
+    if (!a.sigmoid) {
+        float m = -INFINITY;
+        for (int i = lane; i < a.E; i += kWarp) m = fmaxf(m, logits[i]);
+        m = reduce_max(m);
+        top = m;
+        double sum = 0.0;
+        for (int i = lane; i < a.E; i += kWarp) sum += exp((double)logits[i] - top);
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        inv = sum;
+    }
+    for (int i = lane; i < a.E; i += kWarp) {
+        const double x = logits[i];
+        double c = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / inv;
+        if (a.bias) c += (double)a.bias[i];
+        if (!(c == c) || x == -INFINITY || odd) c = -INFINITY;
+        row[i] = c;
+    }
+    __syncwarp();
+    uint32_t keep = 0xffffffffu;
+    if (a.groups > 1) keep = choose_groups<double>(row, a, lane, lanes, 0.f, nullptr);
+    __syncwarp();
+    if (a.groups > 1)
+        for (int i = lane; i < a.E; i += kWarp)
+            if (!(keep >> ((uint32_t)i * a.inv_size >> 20) * lanes & 1)) row[i] = -INFINITY;
+    __syncwarp();
+    for (int j = 0; j < a.k; ++j) {
+        double best = -INFINITY;
+        int at = kNoExpert; // a chosen expert's place holds NaN
+        for (int i = lane; i < a.E; i += kWarp)
+            if (row[i] > best || (row[i] == best && i < at)) {
+                best = row[i];
+                at = i;
+            }
+        for (int off = 16; off > 0; off >>= 1) {
+            const double o = __shfl_xor_sync(0xffffffffu, best, off);
+            const int oa = __shfl_xor_sync(0xffffffffu, at, off);
+            if (oa != kNoExpert && (at == kNoExpert || o > best || (o == best && oa < at))) {
+                best = o;
+                at = oa;
+            }
+        }
+        if (lane == j) {
+            *e = at;
+            *in = best > -INFINITY;
+        }
+        __syncwarp();
+        if (at % kWarp == lane) row[at] = NAN;
+        __syncwarp();
+    }
+}
+
+// The chosen scores up to a factor that all of them share: of the softmax
+// relative to the largest chosen, of the sigmoid times e^-min(0, largest), so
+// that scores near 0 keep their ratios.
+__device__ __forceinline__ float score_of(bool sigmoid, float l, float shift)
+{
+    if (!sigmoid) return expf(l - shift);
+    return l > 0.f ? __fdiv_rn(1.f, 1.f + expf(-l)) : __fdiv_rn(expf(l - shift), 1.f + expf(l));
+}
+
+// Lane l holds the vectors l, l + 32, ... of VEC experts each (N of them).
+template <int VEC, int N>
+__global__ void __launch_bounds__(kScThreads) k_route_scored(ScoredArgs a)
+{
+    pdl_begin();
+    using Vec = typename ScVec<VEC>::T;
+    extern __shared__ __align__(16) double s_rows[]; // [warps][E], then the counts [E]
+    __shared__ __align__(16) TopkSlots s_slots[kScWarps];
+    const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
+    const int E = a.E, k = a.k, nvec = E / VEC;
+    double *row64 = s_rows + (size_t)wid * E;
+    float *row = reinterpret_cast<float *>(row64);
+    int *s_cnt = reinterpret_cast<int *>(s_rows + (size_t)kScWarps * E);
+    if (a.counts) {
+        for (int e = threadIdx.x; e < E; e += kScThreads) s_cnt[e] = 0;
+        __syncthreads();
+    }
+    // the logits' order is the choices' order
+    const bool direct = !a.bias && (a.groups == 1 || a.best == 1);
+    int lanes = kWarp; // of a group
+    while (lanes * a.groups > kWarp) lanes >>= 1;
+    const int64_t step = (int64_t)gridDim.x * kScWarps;
+    for (int64_t t = (int64_t)blockIdx.x * kScWarps + wid; t < a.T; t += step) {
+        const Vec *src = reinterpret_cast<const Vec *>(a.logits + t * E);
+        float v[N][VEC];
+        float top = -INFINITY;
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) v[i][c] = -INFINITY;
+            if (lane + kWarp * i < nvec) {
+                const Vec x = __ldcs(src + lane + kWarp * i);
+                memcpy(v[i], &x, sizeof(Vec));
+            }
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                odd |= !(v[i][c] == v[i][c]);
+                top = fmaxf(top, v[i][c]);
+            }
+        }
+        top = reduce_max(top);
+        odd = __any_sync(0xffffffffu, odd) || (!a.sigmoid && top == INFINITY);
+        const bool some = top > -INFINITY;
+        float sum = 1.f;
+        if (!a.sigmoid && (!direct || !a.renorm)) {
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) sum += exp_fast(v[i][c] - top);
+            sum = warp_sum(sum);
+        }
+        const float inv = __fdiv_rn(1.f, sum);
+        if (!direct) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = lane + kWarp * i;
+                float b[VEC];
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) b[c] = 0.f;
+                if (a.bias && at < nvec) {
+                    const Vec x = reinterpret_cast<const Vec *>(a.bias)[at];
+                    memcpy(b, &x, sizeof(Vec));
+                }
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    const float x = v[i][c];
+                    const float s = a.sigmoid ? rcp_fast(1.f + exp_fast(-x)) : exp_fast(x - top) * inv;
+                    const float y = s + b[c];
+                    v[i][c] = x > -INFINITY && y == y ? y : -INFINITY;
+                }
+            }
+        }
+        if (odd) { // (warp-uniform) a row that holds NaN has no order: the first k experts
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) v[i][c] = -INFINITY;
+        }
+        bool near = false;
+        if (a.groups > 1) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (lane + kWarp * i < nvec) {
+                    Vec x;
+                    memcpy(&x, v[i], sizeof(Vec));
+                    reinterpret_cast<Vec *>(row)[lane + kWarp * i] = x;
+                }
+            __syncwarp();
+            const uint32_t keep = choose_groups<float>(row, a, lane, lanes, inv, direct ? nullptr : &near);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    const uint32_t e = (lane + kWarp * i) * VEC + c;
+                    if (e < (uint32_t)E && !(keep >> (e * a.inv_size >> 20) * lanes & 1)) v[i][c] = -INFINITY;
+                }
+        }
+        int e;
+        float value, first;
+        bool in;
+        choose_token_slots<VEC, N>(v, E, k, lane, s_slots[wid], &e, &value, &first);
+        in = value > -INFINITY;
+        if (!direct && !near) {
+            // neighbours among the chosen, and what lies at the last one's border
+            const float before = __shfl_up_sync(0xffffffffu, value, 1);
+            const float margin = near_of(a.sigmoid, inv, value);
+            bool close = lane > 0 && lane < k && in && before - value <= margin;
+            const float last = __shfl_sync(0xffffffffu, value, k - 1);
+            const float band = near_of(a.sigmoid, inv, last);
+            int upto = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) upto += v[i][c] >= last - band;
+            upto = __reduce_add_sync(0xffffffffu, upto);
+            const bool border = last > -INFINITY && upto > k;
+            if (__any_sync(0xffffffffu, close) || border) {
+                // equal logits with equal biases have equal choices, whatever the rounding: the lower id is first
+                const float *l = a.logits + t * E;
+                const float mine = lane < k ? l[e] : 0.f, own = a.bias && lane < k ? a.bias[e] : 0.f;
+                const float l1 = __shfl_up_sync(0xffffffffu, mine, 1), b1 = __shfl_up_sync(0xffffffffu, own, 1);
+                close &= !(l1 == mine && b1 == own);
+                const float ll = __shfl_sync(0xffffffffu, mine, k - 1), bl = __shfl_sync(0xffffffffu, own, k - 1);
+                if (border) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+#pragma unroll
+                        for (int c = 0; c < VEC; ++c) {
+                            const int x = (lane + kWarp * i) * VEC + c;
+                            if (v[i][c] >= last - band && v[i][c] <= last + band)
+                                close |= !(l[x] == ll && (!a.bias || a.bias[x] == bl));
+                        }
+                }
+                near = __any_sync(0xffffffffu, close);
+            }
+        }
+        __syncwarp(); // the row and the slots are free
+        if (near) choose_exactly(a, t, row64, lanes, odd, &e, &in);
+        // weights
+        const float l = lane < k ? a.logits[t * E + e] : -INFINITY;
+        in = in && lane < k;
+        float wt = 0.f;
+        if (odd) {
+            wt = NAN;
+        } else if (some) { // (warp-uniform)
+            const float most = reduce_max(in ? l : -INFINITY);
+            if (a.renorm) {
+                const float shift = a.sigmoid ? fminf(most, 0.f) : most;
+                const float q = in ? score_of(a.sigmoid, l, shift) : 0.f;
+                const float all = warp_sum(q);
+                wt = all > 0.f ? __fdiv_rn(q, all) * a.scale : 0.f;
+            } else if (in) {
+                wt = (a.sigmoid ? score_of(true, l, 0.f) : __fdiv_rn(expf(l - top), sum)) * a.scale;
+            }
+        }
+        if (lane < k) {
+            a.idx[t * k + lane] = e;
+            a.w[t * k + lane] = wt;
+            if (a.counts && (odd || some) && (!a.mask || a.mask[t])) atomicAdd(&s_cnt[e], 1);
+        }
+        __syncwarp();
+    }
+    if (a.counts) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < E; e += kScThreads)
+            if (s_cnt[e]) atomicAdd(&a.counts[e], s_cnt[e]);
+    }
+}
+
+// A warp per token: the row's zeros (or its dense term) and the k chosen terms,
+// which go through a row of shared memory per warp, zero between tokens.
+template <int VEC, int N, bool DENSE>
+__global__ void __launch_bounds__(kScThreads)
+    k_route_scored_backward(const float *logits, int64_t T, int E, int k, const int32_t *idx, const float *dw, bool sigmoid,
+                            bool renorm, float scale, float *dlogits, uint32_t *d_status)
+{
+    pdl_begin();
+    using Vec = typename ScVec<VEC>::T;
+    extern __shared__ __align__(16) float s_mem[];
+    const int lane = (int)lane_id(), wid = threadIdx.x / kWarp, nvec = E / VEC;
+    float *s_add = s_mem + wid * ((E + 3) & ~3);
+    for (int e = lane; e < E; e += kWarp) s_add[e] = 0.f;
+    __syncwarp();
+    const int64_t step = (int64_t)gridDim.x * kScWarps;
+    for (int64_t t = (int64_t)blockIdx.x * kScWarps + wid; t < T; t += step) {
+        int e = lane < k ? idx[t * k + lane] : 0;
+        const float g = lane < k ? dw[t * k + lane] * scale : 0.f;
+        const bool in = lane < k && e >= 0 && e < E;
+        if (lane < k && !in && d_status) atomicOr(d_status, AP_FLAG_BAD_INDEX);
+        float v[N][VEC];
+        float add = 0.f, dot = 0.f;
+        if constexpr (DENSE) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) v[i][c] = -INFINITY;
+                if (lane + kWarp * i < nvec) {
+                    const Vec x = reinterpret_cast<const Vec *>(logits + t * E)[lane + kWarp * i];
+                    memcpy(v[i], &x, sizeof(Vec));
+                }
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) top = fmaxf(top, v[i][c]);
+            }
+            const float l = in ? logits[t * E + e] : -INFINITY;
+            top = reduce_max(top);
+            const bool some = top > -INFINITY;
+            if (!some) top = 0.f; // (every exponential is 0 then)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    v[i][c] = exp_fast(v[i][c] - top);
+                    sum += v[i][c];
+                }
+            sum = warp_sum(sum);
+            const float inv = some ? __fdiv_rn(1.f, sum) : 0.f;
+            const float p = in ? exp_fast(l - top) * inv : 0.f;
+            dot = warp_sum(p * g);
+            add = p * g;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) v[i][c] *= -inv * dot;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) v[i][c] = 0.f;
+            const float l = in ? logits[t * E + e] : -INFINITY;
+            const float less = sigmoid ? __fdiv_rn(1.f, 1.f + expf(l)) : 1.f; // 1 - sigma
+            if (renorm) {
+                const float most = reduce_max(l);
+                const float q = l > -INFINITY ? score_of(sigmoid, l, sigmoid ? fminf(most, 0.f) : most) : 0.f;
+                const float all = warp_sum(q);
+                const float w = all > 0.f ? __fdiv_rn(q, all) : all == 0.f ? 0.f : NAN;
+                dot = warp_sum(w * g);
+                add = w * less * (g - dot);
+            } else {
+                add = l > -INFINITY ? score_of(true, l, 0.f) * less * g : l == l ? 0.f : NAN;
+            }
+        }
+        if (in) s_add[e] = add;
+        __syncwarp();
+        Vec *out = reinterpret_cast<Vec *>(dlogits + t * E);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (lane + kWarp * i < nvec) {
+                const Vec x = reinterpret_cast<const Vec *>(s_add)[lane + kWarp * i];
+                float y[VEC];
+                memcpy(y, &x, sizeof(Vec));
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) y[c] += v[i][c];
+                Vec o;
+                memcpy(&o, y, sizeof(Vec));
+                out[lane + kWarp * i] = o;
+            }
+        __syncwarp();
+        if (in) s_add[e] = 0.f;
+        __syncwarp();
+    }
+}
+
+// bias[e] += rate where expert e had fewer than its share of the pairs, -= rate
+// where more.  One block: the share is that of all counts.
+__global__ void __launch_bounds__(1024) k_route_bias_step(float *bias, int32_t *counts, int E, float rate, bool reset)
+{
+    pdl_begin();
+    __shared__ long long s_sum[kWarp];
+    __shared__ long long s_all;
+    const int lane = (int)lane_id(), e = threadIdx.x;
+    const long long n = e < E ? counts[e] : 0;
+    long long sum = n;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) s_sum[e / kWarp] = sum;
+    __syncthreads();
+    if (e < kWarp) {
+        sum = e < (int)blockDim.x / kWarp ? s_sum[e] : 0;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (e == 0) s_all = sum;
+    }
+    __syncthreads();
+    if (e < E) {
+        const long long d = s_all - (long long)E * n;
+        if (d) bias[e] += d > 0 ? rate : -rate;
+        if (reset) counts[e] = 0;
+    }
+}
+
+ap_status scored_sizes(const char *who, int64_t T, int32_t E, int32_t k, int32_t score)
+{
+    if (T < 0 || T >= (int64_t(1) << 31) || E < 1 || E > 1024 || k < 1 || k > E || k > 32)
+        return fail(AP_EINVAL, "%s: bad sizes T=%lld E=%d k=%d", who, (long long)T, E, k);
+    if (score != AP_SCORE_SOFTMAX && score != AP_SCORE_SIGMOID) return fail(AP_EINVAL, "%s: unknown score %d", who, score);
+    return AP_OK;
+}
+
+template <int VEC, int N> ap_status launch_scored(const ScoredArgs &a, cudaStream_t st)
+{
+    const auto kernel = k_route_scored<VEC, N>;
+    constexpr int kMaxE = VEC * N * kWarp;
+    static const cudaError_t attr = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                         (kScWarps * 8 + 4) * kMaxE);
+    if (attr != cudaSuccess) return cuda_fail(attr, "route_scored");
+    static const int resident = resident_grid((const void *)kernel, kScThreads, (kScWarps * 8 + 4) * kMaxE);
+    const int64_t want = (a.T + kScWarps - 1) / kScWarps;
+    launch(kernel, (int)(want < resident ? want : resident), kScThreads, (size_t)(kScWarps * 8 + 4) * a.E, st, a);
+    AP_CHECK_LAUNCH("route_scored launch");
+    return AP_OK;
+}
+
+template <int VEC, int N>
+ap_status launch_scored_backward(bool dense, const float *logits, int64_t T, int E, int k, const int32_t *idx, const float *dw,
+                                 bool sigmoid, bool renorm, float scale, float *dlogits, uint32_t *d_status, cudaStream_t st)
+{
+    const size_t smem = (size_t)kScWarps * ((E + 3) & ~3) * 4;
+    const int64_t want = (T + kScWarps - 1) / kScWarps;
+    auto go = [&](auto *kernel) {
+        static const int resident = resident_grid((const void *)kernel, kScThreads, (size_t)kScWarps * VEC * N * kWarp * 4);
+        launch(kernel, (int)(want < resident ? want : resident), kScThreads, smem, st, logits, T, E, k, idx, dw, sigmoid,
+               renorm, scale, dlogits, d_status);
+    };
+    if (dense)
+        go(k_route_scored_backward<VEC, N, true>);
+    else
+        go(k_route_scored_backward<VEC, N, false>);
+    AP_CHECK_LAUNCH("route_scored_backward launch");
+    return AP_OK;
+}
+
+} // namespace
+} // namespace ap
+
+extern "C" ap_status ap_route_scored(const float *logits, int64_t T, int32_t E, int32_t k, int32_t score, const float *bias,
+                                     int32_t groups, int32_t top_groups, int32_t group_best, int32_t renorm, float scale,
+                                     const uint8_t *mask, int32_t *idx, float *w, int32_t *counts, void *stream)
+{
+    AP_NVTX_RANGE("ap_route_scored");
+    using namespace ap;
+    if (const ap_status s = scored_sizes("route_scored", T, E, k, score); s != AP_OK) return s;
+    if (groups < 1 || groups > 32 || E % groups || top_groups < 1 || top_groups > groups ||
+        (int64_t)top_groups * (E / groups) < k)
+        return fail(AP_EINVAL, "route_scored: bad groups: %d of %d for E=%d k=%d", top_groups, groups, E, k);
+    if (group_best < 1 || group_best > 2 || (groups > 1 && group_best > E / groups))
+        return fail(AP_EINVAL, "route_scored: bad group_best=%d", group_best);
+    if (T == 0) return AP_OK;
+    if (!logits || !idx || !w) return fail(AP_EINVAL, "route_scored: NULL pointer");
+    const int size = E / groups;
+    const ScoredArgs a = {logits, bias, mask, idx,  w,          counts,     T,
+                          E,      k,    groups, size, top_groups, group_best, (uint32_t)(((1 << 20) + size - 1) / size),
+                          scale,  score == AP_SCORE_SIGMOID, renorm != 0};
+    cudaStream_t st = (cudaStream_t)stream;
+    const uintptr_t al = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(bias);
+    if (E >= 128 && E % 4 == 0 && (al & 15) == 0) {
+        if (E <= 128) return launch_scored<4, 1>(a, st);
+        if (E <= 256) return launch_scored<4, 2>(a, st);
+        if (E <= 512) return launch_scored<4, 4>(a, st);
+        return launch_scored<4, 8>(a, st);
+    }
+    if (E <= 32) return launch_scored<1, 1>(a, st);
+    if (E <= 64) return launch_scored<1, 2>(a, st);
+    if (E <= 128) return launch_scored<1, 4>(a, st);
+    if (E <= 256) return launch_scored<1, 8>(a, st);
+    if (E <= 512) return launch_scored<1, 16>(a, st);
+    return launch_scored<1, 32>(a, st);
+}
+
+extern "C" ap_status ap_route_scored_backward(const float *logits, int64_t T, int32_t E, int32_t k, const int32_t *idx,
+                                              const float *dw, int32_t score, int32_t renorm, float scale, float *dlogits,
+                                              uint32_t *d_status, void *stream)
+{
+    AP_NVTX_RANGE("ap_route_scored_backward");
+    using namespace ap;
+    if (const ap_status s = scored_sizes("route_scored_backward", T, E, k, score); s != AP_OK) return s;
+    if (T == 0) return AP_OK;
+    if (!logits || !idx || !dw || !dlogits) return fail(AP_EINVAL, "route_scored_backward: NULL pointer");
+    const bool sigmoid = score == AP_SCORE_SIGMOID, dense = !sigmoid && !renorm;
+    cudaStream_t st = (cudaStream_t)stream;
+    const uintptr_t al = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits);
+#define AP_SCORED_BWD(VEC, N) \
+    return launch_scored_backward<VEC, N>(dense, logits, T, E, k, idx, dw, sigmoid, renorm != 0, scale, dlogits, d_status, st)
+    if (E % 4 == 0 && (al & 15) == 0) {
+        if (E <= 128) AP_SCORED_BWD(4, 1);
+        if (E <= 256) AP_SCORED_BWD(4, 2);
+        if (E <= 512) AP_SCORED_BWD(4, 4);
+        AP_SCORED_BWD(4, 8);
+    }
+    if (E <= 32) AP_SCORED_BWD(1, 1);
+    if (E <= 64) AP_SCORED_BWD(1, 2);
+    if (E <= 128) AP_SCORED_BWD(1, 4);
+    if (E <= 256) AP_SCORED_BWD(1, 8);
+    if (E <= 512) AP_SCORED_BWD(1, 16);
+    AP_SCORED_BWD(1, 32);
+#undef AP_SCORED_BWD
+}
+
+extern "C" ap_status ap_route_bias_step(float *bias, int32_t *counts, int32_t E, float rate, int32_t reset, void *stream)
+{
+    AP_NVTX_RANGE("ap_route_bias_step");
+    using namespace ap;
+    if (E < 1 || E > 1024) return fail(AP_EINVAL, "route_bias_step: bad E=%d", E);
+    if (!bias || !counts) return fail(AP_EINVAL, "route_bias_step: NULL pointer");
+    launch(k_route_bias_step, 1, (E + kWarp - 1) / kWarp * kWarp, 0, (cudaStream_t)stream, bias, counts, E, rate, reset != 0);
+    AP_CHECK_LAUNCH("route_bias_step launch");
+    return AP_OK;
+}

@@ -291,6 +291,72 @@ ap_status ap_route_backward(const float *logits, int64_t T, int32_t E, int32_t k
                             const uint8_t *mask, float *dlogits, uint32_t *d_status, void *stream);
 
 /* ============================================================================
+ * route_scored
+ *
+ * Routing by scores that a bias balances, over groups of experts (no
+ * counterpart on the pages; idx and w feed the dispatch and the combine as
+ * ap_route_topk's do).  Per token, with s = softmax(logits) or sigmoid(logits)
+ * over the E experts and c = s + bias (c = s without one):
+ *   - the experts form `groups` groups of E / groups consecutive ones; a
+ *     group's score is the sum of its group_best (1 or 2) largest c, and the
+ *     top_groups largest groups are kept;
+ *   - the k largest c of the kept groups are chosen, in descending order;
+ *   - w_j = scale * s_j, or with renorm scale * s_j / sum_chosen s.
+ * Ties go to the lower group and the lower expert id.  Choices compare the
+ * values of the formulas in double precision (wherever single precision does
+ * not tell two of them apart), and the logits themselves where there is no bias
+ * and groups go by one expert, so single precision's rounding changes no ids.  An expert whose logit or c is -infinity (or whose bias is NaN) is
+ * chosen only if fewer than k others are left, lowest ids first, with w = 0; a
+ * group with fewer than group_best others has the score -infinity.  A row that
+ * holds NaN (with softmax: or +infinity) gets the experts 0 .. k-1 and w =
+ * NaN.  The relative error of w is at most (2 d + E / 32 + 40) 2^-24 with d the
+ * distance of the logit from the row's largest (renorm: from the largest
+ * chosen; sigmoid without renorm: d = 0); below 2^-120 w may be 0.
+ *
+ *   logits  [T, E] float32, row-major (device, read)
+ *   bias    [E] float32 (device, read) or NULL
+ *   mask    [T] bytes (device, read) or NULL: tokens with 0 are routed all the
+ *           same, but not counted
+ *   idx, w  [T, k] as ap_route_topk (device, written)
+ *   counts  [E] int32 (device, added to) or NULL: pairs per expert of the
+ *           tokens that mask lets count and whose row is not all -infinity
+ * Limits: as ap_route_topk; 1 <= groups <= 32, E % groups = 0,
+ * 1 <= top_groups <= groups, top_groups * E / groups >= k,
+ * group_best <= E / groups.
+ * ========================================================================== */
+#define AP_SCORE_SOFTMAX 0
+#define AP_SCORE_SIGMOID 1
+ap_status ap_route_scored(const float *logits, int64_t T, int32_t E, int32_t k, int32_t score, const float *bias,
+                          int32_t groups, int32_t top_groups, int32_t group_best, int32_t renorm, float scale,
+                          const uint8_t *mask, int32_t *idx, float *w, int32_t *counts, void *stream);
+
+/* Gradient of route_scored's logits from the gradient dw of w, for the chosen
+ * idx (the choice itself has no derivative; the bias has none either):
+ *   softmax, no renorm  dlogits[e] = p_e (scale g_e - sum_j p_j scale g_j), with
+ *                       g_e the dw of expert e (0 where it was not chosen)
+ *   otherwise           only chosen experts have a gradient: with r_j = s_j /
+ *                       sum_chosen s, u_j = dw_j - sum_i r_i dw_i and
+ *                       s' = s (1 - s):
+ *                       softmax scale r_j u_j; sigmoid scale r_j (1 - s_j) u_j,
+ *                       without renorm scale s_j' dw_j
+ *   idx      [T, k] (device, read): ids distinct in a row.  An id outside
+ *            [0, E) adds nothing and sets AP_FLAG_BAD_INDEX in *d_status (may
+ *            be NULL)
+ *   dw       [T, k] float32 (device, read)
+ *   dlogits  [T, E] float32 (device, written whole); may be logits itself
+ * logits, score, renorm, scale and limits as ap_route_scored. */
+ap_status ap_route_scored_backward(const float *logits, int64_t T, int32_t E, int32_t k, const int32_t *idx, const float *dw,
+                                   int32_t score, int32_t renorm, float scale, float *dlogits, uint32_t *d_status,
+                                   void *stream);
+
+/* The bias's step towards balance: with n = counts[e] and N their sum over all
+ * experts, bias[e] += rate where n < N / E, -= rate where n > N / E.
+ *   bias [E] float32, counts [E] int32 (device, read and written): with
+ *   reset = 1 the counts are zeroed for the next step
+ * Limits: 1 <= E <= 1024. */
+ap_status ap_route_bias_step(float *bias, int32_t *counts, int32_t E, float rate, int32_t reset, void *stream);
+
+/* ============================================================================
  * embed
  *
  * Token rows from an embedding table (no counterpart on the pages: the rows x
