@@ -16,6 +16,8 @@ raises.
     Pool              paged stash: push / pop / reset / overflow read-out,
                       calibration and lazy growth (over an Arena)
     Arena             device memory that grows in place
+    AdamW             the weights' update: gradient norm and clipping, a step over
+                      many tensors, moments in 32 or 8 bits
     combine_unpermute top-k weighted un-permute to dense BF16 [T, H]
 """
 from __future__ import annotations
@@ -37,8 +39,8 @@ FLAG_CORRUPT = 0x20
 DTYPE_BF16, DTYPE_E4M3, DTYPE_F32 = 0, 1, 2
 
 __all__ = ["embed", "embed_backward", "embed_scratch_bytes", "route_balance", "route_balance_scratch_bytes",
-           "route_backward", "route_scored", "route_scored_backward", "route_bias_step", "route_topk", "dispatch_permute", "dispatch_scratch_bytes", "combine_unpermute", "combine_backward",
-           "dispatch_backward", "cast_e4m3", "Pool", "Arena", "APError", "lib", "launch_count"]
+           "route_backward", "route_scored", "route_scored_backward", "route_bias_step", "route_topk", "dispatch_permute",
+           "dispatch_scratch_bytes", "combine_unpermute", "combine_backward", "dispatch_backward", "cast_e4m3", "AdamW", "Pool", "Arena", "APError", "lib", "launch_count"]
 
 
 def lib():
@@ -377,6 +379,155 @@ def embed_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: float =
                                   g_ld, g_kind, _p(scratch), scratch.numel() if scratch is not None else 0,
                                   _status(status), _stream(stream)), "embed_backward")
     return dtable
+
+
+class AdamW:
+    """AdamW over many tensors at once: one launch for the step, whatever their
+    number (up to 440), with the step's number, the clipping factor and what
+    skips the step on the GPU, so that steps are captured and replayed.
+
+    ``params`` (BF16 or FP32, one type) and ``grads`` (BF16 or FP32, one type):
+    lists of contiguous CUDA tensors; the optimizer keeps them, reads the
+    gradients and writes the parameters at each step (``bind`` changes the
+    gradients).  ``master``: FP32 copies of BF16 parameters, as a list or True
+    (made here).  ``state_bits`` 32 or 8 (see ``ap_adamw_step``).  Moments are
+    flat buffers in which tensor i begins at element ``parts[i][0]``, a multiple
+    of 256; ``state`` gives them with the step words (a checkpoint, or buffers
+    to use): ``m``, ``v`` (float32, or int8 and uint8 with float32 ``m_scale``
+    and ``v_scale``, one for each 256 elements) and ``step`` (int32 [2]: steps
+    taken, 0)."""
+
+    BLOCK = 256
+
+    def __init__(self, params, grads, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+                 master=None, state_bits: int = 32, state: dict | None = None, seed: int = 0):
+        self.params, self.lr = list(params), lr
+        if not self.params:
+            raise ValueError("params is empty")
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+        kind, dev = self.params[0].dtype, self.params[0].device
+        if kind not in _ROW_TYPES:
+            raise ValueError(f"params must be bfloat16 or float32, got {kind}")
+        for i, p in enumerate(self.params):
+            _need(p, kind, f"params[{i}]")
+        if master is True:
+            master = [p.float() for p in self.params]
+        self.master = None if master is None or master is False else list(master)
+        if self.master is not None:
+            if kind != torch.bfloat16:
+                raise ValueError("master copies are of bfloat16 params")
+            if len(self.master) != len(self.params):
+                raise ValueError(f"{len(self.master)} master copies for {len(self.params)} params")
+            for i, (p, q) in enumerate(zip(self.params, self.master)):
+                _need_shape(q, torch.float32, p.shape, f"master[{i}]")
+        self._apart(self.params + (self.master or []))
+        self.parts, at = [], 0
+        for p in self.params:
+            self.parts.append((at, p.numel()))
+            at += -(-p.numel() // self.BLOCK) * self.BLOCK
+        self.state, self.state_bits, eight = dict(state or {}), state_bits, state_bits == 8
+        need = {"m": (torch.int8 if eight else torch.float32, (at,)), "v": (torch.uint8 if eight else torch.float32, (at,)),
+                "step": (torch.int32, (2,))}
+        if eight:
+            need |= {n: (torch.float32, (at // self.BLOCK,)) for n in ("m_scale", "v_scale")}
+        for name, (dtype, shape) in need.items():
+            if name in self.state:
+                _need_shape(self.state[name], dtype, shape, "state " + name)
+            else:
+                self.state[name] = torch.zeros(shape, dtype=dtype, device=dev)
+        self._apart([self.state[n] for n in need])
+        self._table = (_lib.AdamWTensor * len(self.params))()
+        size = self.state["m"].element_size()
+        at = {n: self.state[n].data_ptr() for n in need}
+        for i, (p, (off, n)) in enumerate(zip(self.params, self.parts)):
+            e = self._table[i]
+            e.param, e.n, e.m, e.v = p.data_ptr(), n, at["m"] + off * size, at["v"] + off * size
+            if eight:
+                e.m_scale, e.v_scale = at["m_scale"] + off // self.BLOCK * 4, at["v_scale"] + off // self.BLOCK * 4
+            if self.master is not None:
+                e.master = self.master[i].data_ptr()
+        self._cfg = _lib.AdamWConfig(lr=lr, beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
+                                     param_dtype=_ROW_TYPES[kind], master=1 if self.master is not None else 0,
+                                     state_bits=state_bits, seed=seed & 0xFFFFFFFF, d_step=at["step"])
+        self._cfg_ref = ctypes.byref(self._cfg)
+        self.bind(grads)
+        n = ctypes.c_int64(0)
+        check(lib().ap_grad_norm_scratch_bytes(self._table, len(self._table), ctypes.byref(n)), "grad_norm_scratch_bytes")
+        self._scratch_bytes = n.value
+        self._scratch = torch.empty(n.value, dtype=torch.uint8, device=dev)
+
+    @staticmethod
+    def _apart(tensors):
+        """Refuses tensors that share memory: each is written by threads of its own."""
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors if t.numel())
+        for (_, end), (start, _) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError("params, master copies and moments must not share memory")
+
+    def bind(self, grads):
+        """The gradients of later steps: contiguous tensors of the parameters' shapes."""
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} grads for {len(self.params)} params")
+        kind = grads[0].dtype
+        if kind not in _ROW_TYPES:
+            raise ValueError(f"grads must be bfloat16 or float32, got {kind}")
+        for i, (p, g) in enumerate(zip(self.params, grads)):
+            _need_shape(g, kind, p.shape, f"grads[{i}]")
+        for e, g in zip(self._table, grads):
+            e.grad = g.data_ptr()
+        self.grads, self._cfg.grad_dtype = grads, _ROW_TYPES[kind]
+
+    @staticmethod
+    def _word(t, name: str):
+        """Address of one float32 on the GPU."""
+        if t is None:
+            return None
+        if t.dtype != torch.float32 or not t.is_cuda or t.numel() != 1:
+            raise ValueError(f"{name} must be one float32 on the GPU")
+        return t.data_ptr()
+
+    def grad_norm(self, max_norm: float | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """[norm of all gradients, factor that clips it to ``max_norm``] (float32 [2]; the factor is 1 without clipping,
+        NaN where the norm is not finite): pass ``out[1:]`` as ``scale`` to ``step``."""
+        if max_norm is not None and not max_norm > 0:
+            raise ValueError(f"max_norm must be positive, got {max_norm}")
+        if out is None:
+            out = _empty((2,), torch.float32, self.params[0].device, stream)
+        else:
+            _need_shape(out, torch.float32, (2,), "out")
+        check(lib().ap_grad_norm(self._table, len(self._table), self._cfg.grad_dtype, max_norm or 0.0, out.data_ptr(),
+                                 self._scratch.data_ptr(), self._scratch_bytes, _stream(stream)), "grad_norm")
+        return out
+
+    def step(self, lr=None, scale: torch.Tensor | None = None, skip=None, stream=None):
+        """One step.  ``lr``: a number or one float32 on the GPU (default: the optimizer's); ``scale``: one float32 on
+        the GPU that multiplies the gradients, and skips the step where it is not finite; ``skip``: a 32-bit word on the
+        GPU, or a ``Pool`` (its sticky flags): not 0 skips the step.  A skipped step changes nothing."""
+        c = self._cfg
+        if isinstance(lr, torch.Tensor):
+            c.d_lr = self._word(lr, "lr")
+        else:
+            c.d_lr, c.lr = None, self.lr if lr is None else lr
+        c.d_scale = self._word(scale, "scale")
+        c.d_skip = skip.flags_device_ptr() if isinstance(skip, Pool) else _status(skip)
+        check(lib().ap_adamw_step(self._table, len(self._table), self._cfg_ref, _stream(stream)), "adamw_step")
+
+    def moments(self, dtype: torch.dtype = torch.float32, out=None, stream=None):
+        """(m, v): the moments' values as flat float32 (or bfloat16) tensors; ``state``'s own where they are that already."""
+        s, n = self.state, self.state["m"].numel()
+        if self.state_bits == 32:
+            if dtype != torch.float32 or out is not None:
+                raise ValueError("moments of 32 bits are state['m'] and state['v']")
+            return s["m"], s["v"]
+        if dtype not in _ROW_TYPES:
+            raise ValueError(f"dtype must be bfloat16 or float32, got {dtype}")
+        m, v = out if out is not None else (_empty((n,), dtype, s["m"].device, stream) for _ in range(2))
+        check(lib().ap_adamw_moments(s["m"].data_ptr(), s["v"].data_ptr(), s["m_scale"].data_ptr(), s["v_scale"].data_ptr(), n,
+                                     _ROW_TYPES[dtype], _need_shape(m, dtype, (n,), "m"), _need_shape(v, dtype, (n,), "v"),
+                                     _stream(stream)), "adamw_moments")
+        return m, v
 
 
 def launch_count() -> int:

@@ -33,6 +33,17 @@ class RecordInfo(ctypes.Structure):
                 ("nspill", i64), ("nlost", i64)]
 
 
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", P), ("grad", P), ("master", P), ("m", P), ("v", P), ("m_scale", P), ("v_scale", P), ("n", i64)]
+
+
+class AdamWConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("param_dtype", i32), ("grad_dtype", i32), ("master", i32),
+                ("state_bits", i32), ("seed", u32), ("reserved", u32), ("d_lr", P), ("d_scale", P), ("d_skip", P),
+                ("d_step", P)]
+
+
 # name -> (restype, argtypes); every ap_* symbol the header declares
 SIGNATURES = {
     "ap_status_str": (ctypes.c_char_p, [i32]),
@@ -55,6 +66,10 @@ SIGNATURES = {
     "ap_embed": (i32, [P, i64, i64, i32, P, i32, i64, i32, f32, P, i64, i32, P, P]),
     "ap_embed_scratch_bytes": (i32, [i64, i64, i32, P]),
     "ap_embed_backward": (i32, [P, i64, i32, P, i32, i64, i32, i64, i64, f32, i32, P, i64, i32, P, i64, P, P]),
+    "ap_adamw_step": (i32, [P, i32, P, P]),
+    "ap_grad_norm_scratch_bytes": (i32, [P, i32, P]),
+    "ap_grad_norm": (i32, [P, i32, i32, f32, P, P, i64, P]),
+    "ap_adamw_moments": (i32, [P, P, P, P, i64, i32, P, P, P]),
     "ap_pool_required_bytes": (i32, [P, P, P, P]),
     "ap_pool_init": (i32, [P, P, P, P, P, P]),
     "ap_pool_reset": (i32, [P, P]),

@@ -57,7 +57,8 @@ typedef int32_t ap_status;
                                      /* that did not arrive (embed_backward)     */
 
 /* payload types of dispatch_permute (BF16, E4M3); table, row and gradient
- * types of embed and embed_backward (BF16, F32) */
+ * types of embed and embed_backward, parameters and gradients of adamw_step
+ * (BF16, F32) */
 #define AP_DTYPE_BF16 0
 #define AP_DTYPE_E4M3 1
 #define AP_DTYPE_F32 2
@@ -405,6 +406,84 @@ ap_status ap_embed_backward(const void *dout, int64_t dout_ld, int32_t dout_dtyp
                             int64_t T, int32_t H, int64_t V, int64_t padding_idx, float scale, int32_t accumulate,
                             void *dtable, int64_t dtable_ld, int32_t dtable_dtype, void *scratch,
                             int64_t scratch_bytes, uint32_t *d_status, void *stream);
+
+/* ============================================================================
+ * adamw_step
+ *
+ * The weights' update from the path's gradients (no counterpart on the pages;
+ * the pool's flag word, ap_pool_flags_device_ptr, lets a step skip itself on
+ * overflow): an AdamW step over many tensors at once, one launch for each 440
+ * of them.  Per element, with t the number of the step:
+ *   g' = scale * g;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   p  = (1 - lr weight_decay) p - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in single precision, p rounded once to its type.  With master copies p is
+ * read from and written to the FP32 copy, and the BF16 parameter is its
+ * rounding.
+ *
+ * Moments of 8 bits: elements 256 i .. 256 i + 255 of a tensor share two
+ * scales; m = m_scale c |c| with the int8 code c in -127 .. 127, and sqrt(v) =
+ * v_scale c^2 with the uint8 code c.  The step decodes, updates in single
+ * precision (p from these), and codes again: m_scale = max |m| / 127^2, v_scale
+ * = max sqrt(v) / 255^2, codes floor(sqrt(|m| / m_scale) + r) and floor(sqrt(
+ * sqrt(v) / v_scale) + r'), the latter at least 1 where v > 0.  r and r' are the
+ * low and the high 16 bits of u / 65536, u = mix(e * 0x9E3779B9 + mix(i +
+ * mix(seed + 0x9E3779B9 t))) for element e of the call's tensor i, all modulo
+ * 2^32, with mix the finalizer of MurmurHash3.  A block with a moment that is not
+ * finite becomes NaN whole.
+ *
+ *   tensors  host array of n: device addresses and elements of each.  param of
+ *            param_dtype, grad of grad_dtype, master float32 (config.master = 1,
+ *            param_dtype BF16; else ignored), m and v float32, or codes whose
+ *            buffers hold the elements rounded up to a multiple of 256, and
+ *            m_scale, v_scale float32, one for each 256 elements
+ *   d_step   int32[2] (device): steps taken, a work word that is 0 between
+ *            calls.  The call's step is t = d_step[0] + 1, which it writes back
+ *   d_lr     float32 (device) or NULL: lr, in place of config.lr
+ *   d_scale  float32 (device) or NULL: 1.  One that is not finite skips the step
+ *   d_skip   uint32 (device) or NULL: not 0 skips the step.  A skipped step
+ *            changes nothing, d_step included
+ * The calls of one optimizer (one d_step) must not overlap; parameters, masters
+ * and moments must not overlap one another.  Addresses of 16 (BF16: 8) bytes'
+ * alignment are fastest.  0 <= beta1, beta2 < 1, eps >= 0.
+ * ========================================================================== */
+#define AP_ADAMW_BLOCK 256
+typedef struct {
+    void *param;
+    const void *grad;
+    void *master;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    int64_t n;
+} ap_adamw_tensor;
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int32_t param_dtype, grad_dtype, master, state_bits; /* state_bits: 8 or 32 */
+    uint32_t seed;
+    uint32_t reserved;
+    const float *d_lr, *d_scale;
+    const uint32_t *d_skip;
+    int32_t *d_step;
+} ap_adamw_config;
+ap_status ap_adamw_step(const ap_adamw_tensor *tensors, int32_t n, const ap_adamw_config *cfg, void *stream);
+
+/* The 2-norm over all gradients of the tensors (only grad and n are used), and
+ * what clips it: out[0] = norm, out[1] = max_norm / norm where max_norm > 0 and
+ * norm > max_norm, else 1; NaN where the norm is not finite, so that
+ * ap_adamw_step with d_scale = out + 1 skips the step.  Squares are single
+ * precision, their sums as exact as double, in an order that depends on the
+ * sizes alone: equal inputs give equal bits.
+ *   out     [2] float32 (device, written)
+ *   scratch device work space of ap_grad_norm_scratch_bytes() bytes, 16-byte
+ *           aligned; its contents need no initialisation */
+ap_status ap_grad_norm_scratch_bytes(const ap_adamw_tensor *tensors, int32_t n, int64_t *bytes);
+ap_status ap_grad_norm(const ap_adamw_tensor *tensors, int32_t n, int32_t grad_dtype, float max_norm, float *out,
+                       void *scratch, int64_t scratch_bytes, void *stream);
+
+/* What 8-bit moments stand for, as BF16 or FP32 (a checkpoint's plain types):
+ * n codes (a multiple of 256) of m and v with their scales into m_out and v_out
+ * [n] of out_dtype (device). */
+ap_status ap_adamw_moments(const void *m, const void *v, const float *m_scale, const float *v_scale, int64_t n,
+                           int32_t out_dtype, void *m_out, void *v_out, void *stream);
 
 /* ============================================================================
  * Paged activation stash (torchtitan pull 5541, "AI-Generated Details":

@@ -81,3 +81,49 @@ def route_scored_backward(logits, idx, dw, score="sigmoid", renorm=True, scale=1
 def route_bias_step(bias, counts, rate):
     n = counts.astype(np.int64)
     return (bias + np.float32(rate) * np.sign(n.sum() - n.size * n).astype(np.float32)).astype(np.float32)
+
+
+# ---- the weights' update ---------------------------------------------------------
+
+BLOCK = 256
+
+
+def _mix(x):
+    x = (x ^ (x >> 16)) * 0x85EBCA6B & 0xFFFFFFFF
+    x = (x ^ (x >> 13)) * 0xC2B2AE35 & 0xFFFFFFFF
+    return x ^ (x >> 16)
+
+
+def adamw_noise(seed: int, t: int, tensor: int, n: int):
+    """The low and high 16 bits, as fractions, that round the codes of m and v."""
+    key = _mix((tensor + _mix((seed + 0x9E3779B9 * t) & 0xFFFFFFFF)) & 0xFFFFFFFF)
+    e = np.arange(n, dtype=np.uint64) * np.uint64(0x9E3779B9)
+    x = (e + np.uint64(key)) & np.uint64(0xFFFFFFFF)
+    m32 = np.uint64(0xFFFFFFFF)
+    x = (x ^ (x >> np.uint64(16))) * np.uint64(0x85EBCA6B) & m32
+    x = (x ^ (x >> np.uint64(13))) * np.uint64(0xC2B2AE35) & m32
+    x = (x ^ (x >> np.uint64(16))).astype(np.int64)
+    return (x & 0xFFFF) / 65536.0, (x >> 16) / 65536.0
+
+
+def adamw_decode(cm, cv, sm, sv):
+    """(m, v) of codes and scales."""
+    n = cm.size
+    each = lambda s: np.repeat(s.astype(np.float64), BLOCK)[:n]  # noqa: E731
+    c, r = cm.astype(np.float64), cv.astype(np.float64) ** 2 * each(sv)
+    return c * np.abs(c) * each(sm), r * r
+
+
+def block_max(x):
+    pad = np.zeros(-(-x.size // BLOCK) * BLOCK)
+    pad[:x.size] = np.abs(x)
+    return pad.reshape(-1, BLOCK).max(1)
+
+
+def adamw_step(p, g, m, v, t, lr, betas, eps, weight_decay, scale=1.0):
+    """(p, m, v, the step's change) after step t, in 64 bits, from 64-bit moments."""
+    g = g.astype(np.float64) * scale
+    m = betas[0] * m + (1 - betas[0]) * g
+    v = betas[1] * v + (1 - betas[1]) * g * g
+    change = lr * (m / (1 - betas[0] ** t)) / (np.sqrt(v / (1 - betas[1] ** t)) + eps)
+    return p.astype(np.float64) * (1 - lr * weight_decay) - change, m, v, change

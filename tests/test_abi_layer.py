@@ -45,3 +45,66 @@ def test_route_bias_step_refusals(lib):
     assert lib.ap_route_bias_step(None, P, 8, 1.0, 0, None) == -1
     assert lib.ap_route_bias_step(P, None, 8, 1.0, 0, None) == -1
     assert lib.ap_launch_count() == n0
+
+
+def adamw(lib, tensor=(), **over):
+    from activation_paging_gb300._lib import AdamWConfig, AdamWTensor
+    t = (AdamWTensor * 2)()
+    for e in t:
+        e.param = e.grad = e.master = e.m = e.v = e.m_scale = e.v_scale = 4096
+        e.n = 1000
+    for name, value in tensor:
+        setattr(t[1], name, value)
+    c = AdamWConfig(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, param_dtype=0, grad_dtype=2, master=1, state_bits=8, d_step=4096)
+    n = over.pop("n", 2)
+    for name, value in over.items():
+        setattr(c, name, value)
+    return lib.ap_adamw_step(t, n, ctypes.byref(c), None)
+
+
+def test_adamw_step_refusals(lib):
+    n0 = lib.ap_launch_count()
+    for over in (dict(n=-1), dict(param_dtype=1), dict(grad_dtype=3), dict(state_bits=16), dict(master=2),
+                 dict(param_dtype=2), dict(beta1=1.0), dict(beta2=-0.1), dict(eps=-1.0), dict(beta1=float("nan")),
+                 dict(d_step=0), dict(d_step=4098)):
+        assert adamw(lib, **over) == -1, over
+    for name in ("param", "grad", "master", "m", "v", "m_scale", "v_scale"):
+        assert adamw(lib, [(name, 0)]) == -1, name
+        assert adamw(lib, [(name, 4097)]) == -1, name
+    assert adamw(lib, [("n", -5)]) == -1
+    assert adamw(lib, [("n", 2 ** 39)]) == -1
+    assert lib.ap_adamw_step(None, 0, None, None) == -1
+    assert lib.ap_launch_count() == n0
+
+
+def test_grad_norm_refusals(lib):
+    from activation_paging_gb300._lib import AdamWTensor
+    t = (AdamWTensor * 2)()
+    for e in t:
+        e.grad, e.n = 4096, 1000
+    n = ctypes.c_int64()
+    assert lib.ap_grad_norm_scratch_bytes(t, 2, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.ap_grad_norm_scratch_bytes(t, 2, None) == -1
+    n0 = lib.ap_launch_count()
+
+    def call(tensors=t, count=2, dtype=2, out=P, scratch=P, sb=n.value):
+        return lib.ap_grad_norm(tensors, count, dtype, 1.0, out, scratch, sb, None)
+    for bad in (dict(count=-1), dict(tensors=None), dict(dtype=1), dict(out=None), dict(scratch=None), dict(sb=n.value - 1),
+                dict(scratch=ctypes.c_void_p(4100))):
+        assert call(**bad) == -1, bad
+    t[1].grad = 4098
+    assert call() == -1
+    t[1].grad = 0
+    assert call() == -1
+    assert lib.ap_launch_count() == n0
+
+
+def test_adamw_moments_refusals(lib):
+    def call(m=P, v=P, ms=P, vs=P, n=512, dtype=0, mo=P, vo=P):
+        return lib.ap_adamw_moments(m, v, ms, vs, n, dtype, mo, vo, None)
+    n0 = lib.ap_launch_count()
+    for bad in (dict(n=-256), dict(n=100), dict(dtype=1), dict(m=None), dict(v=None), dict(ms=None), dict(vs=None), dict(mo=None),
+                dict(vo=None), dict(m=ctypes.c_void_p(4097)), dict(mo=ctypes.c_void_p(4100))):
+        assert call(**bad) == -1, bad
+    assert call(n=0, m=None) == 0
+    assert lib.ap_launch_count() == n0
