@@ -12,6 +12,8 @@ raises.
                       (and route_scored_backward, route_bias_step)
     route_balance     route_topk with a balance loss and per-expert counts
                       (and route_backward, the logits' gradient)
+    expert_linear     the experts' products on dispatched rows, with bias,
+                      activation and residual (and expert_linear_dx, _dw)
     dispatch_permute  expert-major, capacity-bounded permutation (BF16 / E4M3)
     Pool              paged stash: push / pop / reset / overflow read-out,
                       calibration and lazy growth (over an Arena)
@@ -40,7 +42,8 @@ DTYPE_BF16, DTYPE_E4M3, DTYPE_F32 = 0, 1, 2
 
 __all__ = ["embed", "embed_backward", "embed_scratch_bytes", "route_balance", "route_balance_scratch_bytes",
            "route_backward", "route_scored", "route_scored_backward", "route_bias_step", "route_topk", "dispatch_permute",
-           "dispatch_scratch_bytes", "combine_unpermute", "combine_backward", "dispatch_backward", "cast_e4m3", "AdamW", "Pool", "Arena", "APError", "lib", "launch_count"]
+           "dispatch_scratch_bytes", "combine_unpermute", "combine_backward", "dispatch_backward", "cast_e4m3", "expert_linear",
+           "expert_linear_dx", "expert_linear_dw", "AdamW", "Pool", "Arena", "APError", "lib", "launch_count"]
 
 
 def lib():
@@ -528,6 +531,136 @@ class AdamW:
                                      _ROW_TYPES[dtype], _need_shape(m, dtype, (n,), "m"), _need_shape(v, dtype, (n,), "v"),
                                      _stream(stream)), "adamw_moments")
         return m, v
+
+
+_ACTS = {None: 0, "silu": 1, "gelu": 2, "swiglu": 3}
+
+
+def _act(act) -> int:
+    kind = _ACTS.get(act)
+    if kind is None:
+        raise ValueError(f"act must be None, 'silu', 'gelu' or 'swiglu', got {act!r}")
+    return kind
+
+
+def _rows16(t: torch.Tensor, name: str, shape: tuple | None = None):
+    """(address, distance of rows) of BF16 rows that may lie apart."""
+    n, H, pitch, kind = _rows(t, name)
+    if kind != DTYPE_BF16:
+        raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
+    if shape is not None and (n, H) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {[n, H]}")
+    return t.data_ptr(), pitch
+
+
+def _segments(seg_off: torch.Tensor, live: torch.Tensor):
+    _need(seg_off, torch.int32, "seg_off")
+    if seg_off.dim() != 1:
+        raise ValueError("seg_off must be [E]")
+    E = seg_off.shape[0]
+    return E, seg_off.data_ptr(), _need_shape(live, torch.int32, (E,), "live")
+
+
+def _weights(W: torch.Tensor, E: int):
+    """(N, K, distance of rows, distance of experts) of BF16 weights [E, N, K]."""
+    if W.dtype != torch.bfloat16 or not W.is_cuda:
+        raise ValueError(f"W must be a bfloat16 CUDA tensor, got {W.dtype}")
+    if W.dim() != 3 or W.shape[0] != E:
+        raise ValueError(f"W must be [{E}, N, K], got {list(W.shape)}")
+    (_, N, K), (apart, pitch, step) = W.shape, W.stride()
+    if step != 1 and K > 1:
+        raise ValueError("W must have contiguous rows")
+    return N, K, max(pitch, K) if N == 1 else pitch, apart
+
+
+def _out_rows(out, rows: int, cols: int, dtype, device, stream, name: str):
+    """(tensor, distance of rows, type) of BF16 or FP32 result rows, made here if not given."""
+    if out is None:
+        kind = DTYPE_BF16 if dtype is None else _ROW_TYPES.get(dtype)
+        if kind is None:
+            raise ValueError(f"dtype must be bfloat16 or float32, got {dtype}")
+        return _empty((rows, cols), torch.bfloat16 if dtype is None else dtype, device, stream), cols, kind
+    n, H, pitch, kind = _rows(out, name)
+    if (n, H) != (rows, cols):
+        raise ValueError(f"{name} must be {[rows, cols]}, got {[n, H]}")
+    return out, pitch, kind
+
+
+def expert_linear(x: torch.Tensor, W: torch.Tensor, seg_off: torch.Tensor, live: torch.Tensor,
+                  bias: torch.Tensor | None = None, act: str | None = None, residual: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, pre: torch.Tensor | None = None, dtype: torch.dtype | None = None,
+                  status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[r] = act(x[r] W[e]^T + bias[e]) + residual[r] for the rows r of each
+    expert e: ``live[e]`` rows from ``seg_off[e]`` ([E] int32 on the GPU, as the
+    dispatch leaves them; the counts are read there).  x [rows, K] BF16, W [E, N, K]
+    BF16, bias [E, N] float32, residual [rows, N] BF16, out [rows, N] BF16 (or
+    float32: ``dtype``).  ``act``: None, 'silu', 'gelu', or 'swiglu' with W
+    [E, 2 N, K], silu of the first N columns times the others.  ``pre``: a BF16
+    tensor that receives the values before the activation, for
+    ``expert_linear_dx``.  Rows may lie apart; rows of no expert are not written."""
+    E, ps, pl = _segments(seg_off, live)
+    wide, K, ldw, lde = _weights(W, E)
+    kind = _act(act)
+    rows = x.shape[0]
+    px, ldx = _rows16(x, "x", (rows, K))
+    if kind == 3 and wide % 2:
+        raise ValueError(f"W must have an even number of rows for swiglu, got {wide}")
+    N = wide // 2 if kind == 3 else wide
+    pb = None if bias is None else _need_shape(bias, torch.float32, (E, wide), "bias")
+    pr, ldr = (None, 0) if residual is None else _rows16(residual, "residual", (rows, N))
+    pp, ldp = (None, 0) if pre is None else _rows16(pre, "pre", (rows, wide))
+    out, ldo, okind = _out_rows(out, rows, N, dtype, x.device, stream, "out")
+    check(lib().ap_expert_linear(px, ldx, rows, E, N, K, ps, pl, W.data_ptr(), ldw, lde, pb, kind, pr, ldr, pp, ldp,
+                                 out.data_ptr(), ldo, okind, _status(status), _stream(stream)), "expert_linear")
+    return out
+
+
+def expert_linear_dx(dy: torch.Tensor, W: torch.Tensor, seg_off: torch.Tensor, live: torch.Tensor, act: str | None = None,
+                     pre: torch.Tensor | None = None, residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     dtype: torch.dtype | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of ``expert_linear``'s rows: (dy[r] W[e] + residual[r]) times the
+    derivative of the activation ``act`` that made them, at ``pre``, from which
+    they were made ([rows, K] BF16; 'swiglu': [rows, 2 K], as the result then)."""
+    E, ps, pl = _segments(seg_off, live)
+    N, K, ldw, lde = _weights(W, E)
+    kind = _act(act)
+    rows = dy.shape[0]
+    py, ldy = _rows16(dy, "dy", (rows, N))
+    wide = 2 * K if kind == 3 else K
+    if kind and pre is None:
+        raise ValueError("act needs pre")
+    pp, ldp = _rows16(pre, "pre", (rows, wide)) if kind else (None, 0)
+    pr, ldr = (None, 0) if residual is None else _rows16(residual, "residual", (rows, K))
+    out, ldo, okind = _out_rows(out, rows, wide, dtype, dy.device, stream, "out")
+    check(lib().ap_expert_linear_dx(py, ldy, rows, E, N, K, ps, pl, W.data_ptr(), ldw, lde, kind, pp, ldp, pr, ldr,
+                                    out.data_ptr(), ldo, okind, _status(status), _stream(stream)), "expert_linear_dx")
+    return out
+
+
+def expert_linear_dw(dy: torch.Tensor, x: torch.Tensor, seg_off: torch.Tensor, live: torch.Tensor,
+                     dW: torch.Tensor | None = None, dbias: torch.Tensor | None = None, accumulate: bool = False,
+                     dtype: torch.dtype = torch.float32, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of ``expert_linear``'s weights: dW[e] = the sum of dy[r]^T x[r]
+    over the expert's rows ([E, N, K] float32 or BF16), written whole or, with
+    ``accumulate``, added to ``dW``; likewise ``dbias`` ([E, N] float32) where
+    given."""
+    E, ps, pl = _segments(seg_off, live)
+    rows, N, ldy, kind = _rows(dy, "dy")
+    py, ldy = _rows16(dy, "dy")
+    K = x.shape[1] if x.dim() == 2 else -1
+    px, ldx = _rows16(x, "x", (rows, K))
+    if dW is None:
+        if accumulate:
+            raise ValueError("accumulate needs dW")
+        dW = _empty((E, N, K), dtype, dy.device, stream)
+    wkind = _ROW_TYPES.get(dW.dtype)
+    if wkind is None:
+        raise ValueError(f"dW must be bfloat16 or float32, got {dW.dtype}")
+    pw = _need_shape(dW, dW.dtype, (E, N, K), "dW")
+    pb = None if dbias is None else _need_shape(dbias, torch.float32, (E, N), "dbias")
+    check(lib().ap_expert_linear_dw(py, ldy, px, ldx, rows, E, N, K, ps, pl, 1 if accumulate else 0, pw, wkind, pb,
+                                    _status(status), _stream(stream)), "expert_linear_dw")
+    return dW
 
 
 def launch_count() -> int:

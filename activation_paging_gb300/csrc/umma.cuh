@@ -1,0 +1,139 @@
+// Tensor-core building blocks of the experts' products: barriers with bounded
+// waits, tensor maps and their copies, operand descriptors, and the products
+// and read-out of accumulators in tensor memory.
+#pragma once
+
+#include <cuda.h>
+
+#include "ap_common.cuh"
+
+namespace ap {
+namespace umma {
+
+// ---- barriers in shared memory ---------------------------------------------------
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_init_done()
+{
+    asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Waits for the phase of this parity to end; gives up after a number of tries
+// (each of which may sleep for a while), or once another wait of the block gave
+// up (*dead).  A million tries take some ten milliseconds at the least.
+constexpr uint32_t kTries = 1u << 20;
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *dead)
+{
+    uint32_t ok = 0;
+    for (uint32_t i = 0; i < kTries; ++i) {
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+        if (ok) return true;
+        if ((i & 255) == 255 && *dead) return false;
+    }
+    *dead = 1;
+    return false;
+}
+
+// ---- copies by tensor map ---------------------------------------------------------
+__device__ __forceinline__ void tma_2d(uint32_t to, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                     to),
+                 "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+// What threads wrote to shared memory becomes visible to the tensor cores.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ---- tensor memory ------------------------------------------------------------------
+// (one whole warp each)
+__device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t columns)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Operands lie in shared memory as lines of 128 bytes, eight lines to a
+// swizzled atom of 1024 bytes.
+// Contiguous along the contraction ("K"): a line is 64 values of one row; the
+// next eight rows lie `next` = 1024 bytes on.  16 values further along the
+// contraction: 32 bytes.
+// Contiguous along the rows ("MN"): a line is 64 rows' values at one place of
+// the contraction; eight places on: 1024 bytes; 64 rows on: `chunk` bytes.  16
+// places further: 2048 bytes.
+__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t chunk)
+{
+    return (uint64_t)((at & 0x3ffff) >> 4) | (uint64_t)(chunk >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// BF16 operands, FP32 accumulators, m x n.
+__device__ __forceinline__ uint32_t shape_of(int m, int n, bool a_mn, bool b_mn)
+{
+    return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 | (uint32_t)(n >> 3) << 17 |
+           (uint32_t)(m >> 4) << 24;
+}
+// acc (+)= A B^T over 16 places of the contraction (one thread).
+__device__ __forceinline__ void mma(uint32_t acc, uint64_t a, uint64_t b, uint32_t shape, bool add)
+{
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(acc), "l"(a),
+                 "l"(b), "r"(shape), "r"((uint32_t)add)
+                 : "memory");
+}
+// The barrier gets one arrival when all products that this thread asked for are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// 32 columns of the warp's 32 lanes.
+__device__ __forceinline__ void acc_load(uint32_t at, float (&v)[32])
+{
+    uint32_t r[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+                   "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+                   "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(at)
+                 : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ---- host ---------------------------------------------------------------------------
+// A map of BF16 values, innermost first, with lines of 64 values swizzled in
+// 128 bytes; pitches in elements for the dimensions after the first.
+bool make_map(CUtensorMap *map, const void *base, int dims, const uint64_t *extent, const uint64_t *pitch, const uint32_t *box);
+
+} // namespace umma
+} // namespace ap

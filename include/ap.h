@@ -54,7 +54,8 @@ typedef int32_t ap_status;
 #define AP_FLAG_BAD_COUNT 0x8u       /* a segment lay outside the given rows     */
 #define AP_FLAG_BAD_INDEX 0x10u      /* an expert id or row index out of range   */
 #define AP_FLAG_CORRUPT 0x20u        /* a page id read back out of range; rows   */
-                                     /* that did not arrive (embed_backward)     */
+                                     /* that did not arrive (embed_backward,     */
+                                     /* expert_linear)                           */
 
 /* payload types of dispatch_permute (BF16, E4M3); table, row and gradient
  * types of embed and embed_backward, parameters and gradients of adamw_step
@@ -356,6 +357,76 @@ ap_status ap_route_scored_backward(const float *logits, int64_t T, int32_t E, in
  *   reset = 1 the counts are zeroed for the next step
  * Limits: 1 <= E <= 1024. */
 ap_status ap_route_bias_step(float *bias, int32_t *counts, int32_t E, float rate, int32_t reset, void *stream);
+
+/* ============================================================================
+ * expert_linear
+ *
+ * The experts' products between the dispatch and the combine, on rows as the
+ * dispatch leaves them (no counterpart on the pages).  Expert e's rows are
+ * seg_off[e] .. seg_off[e] + live[e] - 1, with both read on the device, so
+ * counts may change between CUDA-graph replays.  For each such row r:
+ *   z[r] = x[r] W[e]^T + bias[e]       (FP32 accumulation; also stored to pre)
+ *   out[r] = act(z[r]) + residual[r]   (z not rounded before; one rounding)
+ * with act: none; SILU z sigmoid(z); GELU z Phi(z) (the normal distribution's,
+ * no approximation of it); SWIGLU: W[e] has 2 N rows and z = [g, u] 2 N columns,
+ * act(z) = silu(g) u.  Rows of no expert are neither read for a result nor
+ * written.  A segment with live < 0, seg_off < 0 or seg_off + live > rows is
+ * left out and sets AP_FLAG_BAD_COUNT in *d_status (may be NULL); segments must
+ * not overlap.  Sums have one order for given sizes and counts: equal inputs
+ * give equal bits.  Should operands not arrive within a bounded wait (no input
+ * leads to that), AP_FLAG_CORRUPT is set and the rows that lack them get NaN.
+ *
+ *   x        [rows, K] bf16, ldx elements apart (device, read)
+ *   W        [E, N, K] bf16 (SWIGLU: [E, 2 N, K]), rows ldw and experts lde
+ *            elements apart (device, read)
+ *   bias     [E, N] ([E, 2 N]) float32, contiguous (device, read) or NULL
+ *   residual [rows, N] bf16, ldres apart (device, read) or NULL; may be out
+ *   pre      [rows, N] ([rows, 2 N]) bf16, ldpre apart (device, written) or NULL
+ *   out      [rows, N] of out_dtype (BF16 or F32), ldo apart (device, written)
+ * Limits: 0 <= rows < 2^31, 1 <= E <= 1024, 1 <= N, K <= 2^20.  Bases of x and W
+ * on 16 bytes and pitches that are multiples of 8 elements are many times
+ * faster than others.
+ * ========================================================================== */
+#define AP_ACT_NONE 0
+#define AP_ACT_SILU 1
+#define AP_ACT_GELU 2
+#define AP_ACT_SWIGLU 3
+ap_status ap_expert_linear(const void *x, int64_t ldx, int64_t rows, int32_t E, int32_t N, int32_t K,
+                           const int32_t *d_seg_off, const int32_t *d_live, const void *W, int64_t ldw, int64_t lde,
+                           const float *bias, int32_t act, const void *residual, int64_t ldres, void *pre, int64_t ldpre,
+                           void *out, int64_t ldo, int32_t out_dtype, uint32_t *d_status, void *stream);
+
+/* Gradient of the rows: for each row r of expert e
+ *   d[r]  = dy[r] W[e] + residual[r]                 (K columns)
+ *   dx[r] = d[r] * act'(pre[r])                      (none: d[r])
+ * where act is the activation that made x, and pre what it was made from (the
+ * forward call's output of that name): so the call goes back through a product
+ * and the activation ahead of it.  SWIGLU: pre and dx have 2 K columns [g, u],
+ * dx = [d u silu'(g), d silu(g)].
+ *   dy       [rows, N] bf16, ldy apart; W [E, N, K] as above (device, read)
+ *   pre      [rows, K] ([rows, 2 K]) bf16, ldpre apart (device, read); unused
+ *            without an activation
+ *   residual [rows, K] bf16, ldres apart (device, read) or NULL: further
+ *            gradients of x; may be dx where there is no SWIGLU
+ *   dx       [rows, K] ([rows, 2 K]) of dx_dtype, ldx apart (device, written);
+ *            BF16 dx may be pre
+ * Segments, limits and the rest as ap_expert_linear. */
+ap_status ap_expert_linear_dx(const void *dy, int64_t ldy, int64_t rows, int32_t E, int32_t N, int32_t K,
+                              const int32_t *d_seg_off, const int32_t *d_live, const void *W, int64_t ldw, int64_t lde,
+                              int32_t act, const void *pre, int64_t ldpre, const void *residual, int64_t ldres, void *dx,
+                              int64_t ldx, int32_t dx_dtype, uint32_t *d_status, void *stream);
+
+/* Gradients of weights and bias:
+ *   dW[e] = sum over rows r of expert e of dy[r]^T x[r]    dbias[e] = sum dy[r]
+ * accumulate = 1: added to what is there (one rounding), else written whole
+ * (zeros for an expert without rows).
+ *   dW    [E, N, K] of dw_dtype (BF16 or F32), contiguous (device) or NULL
+ *   dbias [E, N] float32, contiguous (device) or NULL; not both NULL
+ *   dy    [rows, N] bf16, ldy apart; x [rows, K] bf16, ldx apart (device, read)
+ * Segments, limits and the rest as ap_expert_linear. */
+ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void *x, int64_t ldx, int64_t rows, int32_t E, int32_t N,
+                              int32_t K, const int32_t *d_seg_off, const int32_t *d_live, int32_t accumulate, void *dW,
+                              int32_t dw_dtype, float *dbias, uint32_t *d_status, void *stream);
 
 /* ============================================================================
  * embed

@@ -127,3 +127,74 @@ def adamw_step(p, g, m, v, t, lr, betas, eps, weight_decay, scale=1.0):
     v = betas[1] * v + (1 - betas[1]) * g * g
     change = lr * (m / (1 - betas[0] ** t)) / (np.sqrt(v / (1 - betas[1] ** t)) + eps)
     return p.astype(np.float64) * (1 - lr * weight_decay) - change, m, v, change
+
+
+# ---- the experts' products ---------------------------------------------------------
+
+def _cdf(z):
+    from math import erfc, sqrt
+    return 0.5 * np.vectorize(erfc, otypes=[np.float64])(-z / sqrt(2.0)) if z.size else z
+
+
+def act(kind, z):
+    """act(z); swiglu: of the halves of z's columns."""
+    if kind == "swiglu":
+        n = z.shape[1] // 2
+        return z[:, :n] * sigmoid(z[:, :n]) * z[:, n:]
+    return z * sigmoid(z) if kind == "silu" else z * _cdf(z) if kind == "gelu" else z
+
+
+def act_backward(kind, z, d):
+    """d act(z) / dz times d."""
+    if kind is None:
+        return d
+    if kind == "gelu":
+        return d * (_cdf(z) + z * np.exp(-0.5 * z * z) / np.sqrt(2.0 * np.pi))
+    n = d.shape[1]
+    g = z[:, :n]
+    s = sigmoid(g)
+    slope = s * (1.0 + g * (1.0 - s))
+    return d * slope if kind == "silu" else np.concatenate([d * z[:, n:] * slope, d * g * s], 1)
+
+
+def expert_rows(seg, live, rows):
+    """(expert, its rows) of every valid segment."""
+    for e, (a, n) in enumerate(zip(seg.tolist(), live.tolist())):
+        if a >= 0 and n > 0 and a + n <= rows:
+            yield e, slice(a, a + n)
+
+
+def expert_linear(x, W, seg, live, bias=None, kind=None, residual=None):
+    """(z, out, and for error bounds the sums of magnitudes of z's terms): NaN in rows of no expert."""
+    wide = W.shape[1]
+    z, size = np.full((x.shape[0], wide), np.nan), np.zeros((x.shape[0], wide))
+    for e, at in expert_rows(seg, live, x.shape[0]):
+        b = 0.0 if bias is None else bias[e].astype(np.float64)
+        z[at] = x[at] @ W[e].T + b
+        size[at] = np.abs(x[at]) @ np.abs(W[e]).T + np.abs(b)
+    out = np.full((x.shape[0], wide // 2 if kind == "swiglu" else wide), np.nan)
+    for e, at in expert_rows(seg, live, x.shape[0]):
+        out[at] = act(kind, z[at]) + (0.0 if residual is None else residual[at])
+    return z, out, size
+
+
+def expert_linear_dx(dy, W, seg, live, kind=None, pre=None, residual=None):
+    """(dx, sums of magnitudes before the activation's slope)"""
+    cols = W.shape[2]
+    dx = np.full((dy.shape[0], 2 * cols if kind == "swiglu" else cols), np.nan)
+    size = np.zeros((dy.shape[0], cols))
+    for e, at in expert_rows(seg, live, dy.shape[0]):
+        d = dy[at] @ W[e] + (0.0 if residual is None else residual[at])
+        size[at] = np.abs(dy[at]) @ np.abs(W[e]) + (0.0 if residual is None else np.abs(residual[at]))
+        dx[at] = act_backward(kind, None if kind is None else pre[at], d)
+    return dx, size
+
+
+def expert_linear_dw(dy, x, seg, live, E):
+    """(dW, dbias, sums of magnitudes of both)"""
+    dW, db = np.zeros((E, dy.shape[1], x.shape[1])), np.zeros((E, dy.shape[1]))
+    sW, sb = np.zeros_like(dW), np.zeros_like(db)
+    for e, at in expert_rows(seg, live, x.shape[0]):
+        dW[e], db[e] = dy[at].T @ x[at], dy[at].sum(0)
+        sW[e], sb[e] = np.abs(dy[at]).T @ np.abs(x[at]), np.abs(dy[at]).sum(0)
+    return dW, db, sW, sb
