@@ -15,6 +15,9 @@
 // A block per SM walks the tiles: one warp fetches operands through a ring of
 // stages, one issues the products, four read the accumulator and write the
 // outputs while the next tile's products run into a second accumulator.
+// Outputs and what the epilogue reads (residual, pre-activations) pass through
+// shared memory as 8 x 8 matrices, transposed, so that memory sees rows' pieces
+// of 32 and 64 bytes.
 // Operands come by tensor map where base and pitch are multiples of 16 bytes;
 // else (odd row lengths) three warps bring them element by element.
 #include <cuda_bf16.h>
@@ -28,16 +31,17 @@ namespace {
 using bf16_t = __nv_bfloat16;
 using namespace umma;
 
-constexpr int kExThreads = 256;    // warps: 0 fetches, 1 multiplies, 2 and 3 fetch odd rows, 4 to 7 write
+constexpr int kExThreads = 384;    // warps: 0 fetches, 1 multiplies, 2 and 3 fetch odd rows, 4 to 11 write
 constexpr int kFetchers = 96;      // threads of warps 0, 2 and 3
-constexpr int kWriters = 128;
+constexpr int kWriters = 8;        // warps: two for each quarter of the lanes, with every other 32 columns
 constexpr int kLanes = 128;        // features of a tile
 constexpr int kDepth = 64;         // contraction of a stage: one line of 128 bytes
 constexpr int kPanel = kDepth * 128; // 64 lines
 constexpr int kMaxStages = 10;
 constexpr int kMaxSmem = 232448;
 constexpr int kMaxExperts = 1024;
-constexpr int kSwapPitch = 33;     // of the gate's and the up product's exchange
+constexpr int kPassPitch = 80;     // bytes of 32 lanes' values on their way, with what keeps banks apart
+constexpr int kPass = 32 * kPassPitch; // of a writer
 
 enum Op { kForward, kRows, kWeights };
 
@@ -55,7 +59,8 @@ struct ExArgs {
     int E, F, K;           // features of the output (of each half of a gated product), contraction
     int tiles_f, columns, stages, act;
     bool out_f32, add;     // add: kWeights, to what is there
-    bool vec;              // kWeights: rows of the output on 32-byte boundaries
+    bool by16;             // a gated product's map takes 16 features of either half in turn
+    bool vec_out, vec_pre, vec_res; // rows on 16-byte boundaries (kWeights: 32), of whole pieces
 };
 
 // ---- activations -----------------------------------------------------------------
@@ -72,12 +77,6 @@ __device__ __forceinline__ float sigmoid_fast(float x)
     return y;
 }
 __device__ __forceinline__ float normal_cdf(float x) { return 0.5f * erfcf(-0.70710678f * x); }
-__device__ __forceinline__ float act_of(int act, float z)
-{
-    if (act == AP_ACT_SILU) return z * sigmoid_fast(z);
-    if (act == AP_ACT_GELU) return z * normal_cdf(z);
-    return z;
-}
 __device__ __forceinline__ float act_slope(int act, float z)
 {
     if (act == AP_ACT_GELU) return normal_cdf(z) + z * 0.39894228f * ex_fast(-0.5f * z * z);
@@ -183,41 +182,56 @@ __device__ __forceinline__ void fill_panel(uint8_t *to, const bf16_t *src, int64
     }
 }
 
-// A stage: the features' operand (two panels, 16 KB), then the columns'.
+// A stage: the features' operand (16 KB), then the columns'.  A gated product's
+// features alternate by 16 between the gate's and the up product's, so that a
+// writing lane finds both.
 template <Op OP, bool MAPS>
 __device__ __forceinline__ void fetch(const ExArgs &a, const Tile &t, int step, uint8_t *stage, const CUtensorMap *mx,
-                                      const CUtensorMap *mw, uint32_t full, int thread)
+                                      const CUtensorMap *mw, const CUtensorMap *whole, uint32_t full, int thread)
 {
     const int k0 = step * kDepth;
     const bool gated = OP == kForward && a.act == AP_ACT_SWIGLU;
-    const int half = gated ? a.F : 64; // where the second panel's features begin, behind the first's
     uint8_t *col = stage + 2 * kPanel;
     const int n = OP == kWeights ? ceil_div(t.n, 64) : ceil_div(t.n, 32);
     if constexpr (MAPS) {
         const uint32_t sa = smem_addr(stage), sb = smem_addr(col);
-        bar_expect(full, 2 * kPanel + n * (OP == kWeights ? kPanel : kPanel / 2));
+        const bool all = OP != kWeights && t.n > a.columns - 32; // the tile's rows in one copy
+        bar_expect(full, 2 * kPanel + (all ? a.columns * 128 : n * (OP == kWeights ? kPanel : kPanel / 2)));
+        if (gated && a.by16) {
+            tma_5d(sa, mw, k0, 0, 0, t.f0 >> 4, t.e, full);
+        } else if (gated) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (OP == kForward) tma_3d(sa + h * kPanel, mw, k0, t.f0 + h * half, t.e, full);
-            if (OP == kRows) tma_3d(sa + h * kPanel, mw, t.f0 + h * 64, k0, t.e, full);
-            if (OP == kWeights) tma_2d(sa + h * kPanel, mx, t.f0 + h * 64, t.row0 + k0, full);
+            for (int b = 0; b < 8; ++b) tma_3d(sa + b * 2048, mw, k0, t.f0 + (b >> 1) * 16 + (b & 1) * a.F, t.e, full);
+        } else if (OP == kForward) {
+            tma_3d(sa, mw, k0, t.f0, t.e, full);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (OP == kRows) tma_3d(sa + h * kPanel, mw, t.f0 + h * 64, k0, t.e, full);
+                if (OP == kWeights) tma_2d(sa + h * kPanel, mx, t.f0 + h * 64, t.row0 + k0, full);
+            }
         }
-        for (int i = 0; i < n; ++i) {
+        if (all) tma_2d(sb, whole, k0, t.row0, full);
+        for (int i = 0; i < n && !all; ++i) {
             if (OP == kWeights)
                 tma_2d(sb + i * kPanel, mw, t.c0 + i * 64, t.row0 + k0, full);
             else
                 tma_2d(sb + i * (kPanel / 2), mx, k0, t.row0 + i * 32, full);
         }
     } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int f = t.f0 + h * half;
-            if (OP == kForward)
-                fill_panel(stage + h * kPanel, a.W + t.e * a.lde + f * a.ldw + k0, a.ldw, 64, (gated ? 2 : 1) * a.F - f, a.K - k0,
-                           thread);
-            if (OP == kRows) fill_panel(stage + h * kPanel, a.W + t.e * a.lde + k0 * a.ldw + f, a.ldw, 64, a.K - k0, a.F - f, thread);
-            if (OP == kWeights)
-                fill_panel(stage + h * kPanel, a.x + (int64_t)(t.row0 + k0) * a.ldx + f, a.ldx, 64, t.live - k0, a.F - f, thread);
+        if (gated) {
+            for (int b = 0; b < 8; ++b) {
+                const int f = t.f0 + (b >> 1) * 16;
+                fill_panel(stage + b * 2048, a.W + t.e * a.lde + (f + (b & 1) * a.F) * a.ldw + k0, a.ldw, 16, a.F - f, a.K - k0, thread);
+            }
+        } else {
+            for (int h = 0; h < 2; ++h) {
+                const int f = t.f0 + h * 64;
+                uint8_t *to = stage + h * kPanel;
+                if (OP == kForward) fill_panel(to, a.W + t.e * a.lde + f * a.ldw + k0, a.ldw, 64, a.F - f, a.K - k0, thread);
+                if (OP == kRows) fill_panel(to, a.W + t.e * a.lde + k0 * a.ldw + f, a.ldw, 64, a.K - k0, a.F - f, thread);
+                if (OP == kWeights) fill_panel(to, a.x + (int64_t)(t.row0 + k0) * a.ldx + f, a.ldx, 64, t.live - k0, a.F - f, thread);
+            }
         }
         for (int i = 0; i < n; ++i) {
             if (OP == kWeights)
@@ -232,143 +246,436 @@ __device__ __forceinline__ void fetch(const ExArgs &a, const Tile &t, int step, 
     }
 }
 
-__device__ __forceinline__ void writers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWriters) : "memory"); }
-
 template <typename T> __device__ __forceinline__ void put(T *p, float v);
 template <> __device__ __forceinline__ void put<float>(float *p, float v) { *p = v; }
 template <> __device__ __forceinline__ void put<bf16_t>(bf16_t *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// 32 rows' values of a feature (lane), rows c .. c + count - 1 from row on.
-template <typename T>
-__device__ __forceinline__ void write_rows(const ExArgs &a, const Tile &t, int c, float (&v)[32], int f, int lane_row, float *swap)
+__device__ __forceinline__ uint32_t pack(float lo, float hi)
 {
-    const int64_t row = (int64_t)t.row0 + c;
-    const int count = min(32, t.n - c);
-    const bool on = f < a.F;
-    T *out = static_cast<T *>(a.out) + row * a.ldo + f;
-    const bf16_t *res = a.residual + row * a.ldres + f;
-    bf16_t *pre = a.pre + row * a.ldpre + f;
-    const bool up = lane_row >= kLanes / 2;
-    if (a.act == AP_ACT_SWIGLU) { // lanes 64 on hold the up product of the features of the lanes before
-        if (a.bias && on) {
-            const float b = a.bias[(int64_t)t.e * 2 * a.F + (up ? a.F : 0) + f];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] += b;
-        }
-        if (a.pre && on) {
-            bf16_t *p = pre + (up ? a.F : 0);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < count) p[j * a.ldpre] = __float2bfloat16_rn(v[j]);
-        }
-        float *mine = swap + (lane_row & (kLanes / 2 - 1)) * kSwapPitch;
-        if (up)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) mine[j] = v[j];
-        writers_sync();
-        if (!up && on)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < count) {
-                    float h = v[j] * sigmoid_fast(v[j]) * mine[j];
-                    if (a.residual) h += __bfloat162float(res[j * a.ldres]);
-                    put(out + j * a.ldo, h);
-                }
-        writers_sync();
-        return;
-    }
-    if (!on) return;
-    if (a.bias) {
-        const float b = a.bias[(int64_t)t.e * a.F + f];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += b;
-    }
-    if (a.pre)
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < count) pre[j * a.ldpre] = __float2bfloat16_rn(v[j]);
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (j < count) {
-            float h = act_of(a.act, v[j]);
-            if (a.residual) h += __bfloat162float(res[j * a.ldres]);
-            put(out + j * a.ldo, h);
-        }
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
 }
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-template <typename T>
-__device__ __forceinline__ void write_slopes(const ExArgs &a, const Tile &t, int c, float (&v)[32], int f)
+// A writer's 32 rows (columns of the accumulator) of 32 features (lanes) from f
+// on, of which those below F count.  Values in the tiles' layout of
+// acc_load_tiles: v[h][4 i + 2 s + c] is feature f + 16 h + 8 s + lane / 4 of row
+// 8 i + 2 (lane % 4) + c; as 16-bit pairs: p[i][2 h + s].
+using Frag = float[2][16];
+using Pairs = uint32_t[4][4];
+
+// Memory's rows of 32 features: lane l holds 16 bytes of row 8 q + l / 4, piece l % 4.
+struct Piece {
+    uint4 w[4];
+};
+// Which of the 32 features count: those below `left` of the first 16 and below
+// `left2` of the others, which begin `second` elements on (16, or a gated product's other half).
+struct Span {
+    int left, left2;
+    int64_t second;
+};
+__device__ __forceinline__ Span together(int left) { return {left, left - 16, 16}; }
+__device__ __forceinline__ void piece_load(Piece &x, const bf16_t *rows, int64_t ld, int count, const Span &n, bool vec)
 {
-    if (f >= a.F) return;
-    const int64_t row = (int64_t)t.row0 + c;
-    const int count = min(32, t.n - c);
-    T *out = static_cast<T *>(a.out) + row * a.ldo + f;
-    if (a.residual) {
-        const bf16_t *res = a.residual + row * a.ldres + f;
+    const int lane = (int)lane_id();
+    const int at = (lane & 1) * 8; // of the 16 features of a half
+    const int64_t off = (lane & 2 ? n.second : 0) + at;
+    const int in = (lane & 2 ? n.left2 : n.left) - at; // features from this piece on that count
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < count) v[j] += __bfloat162float(res[j * a.ldres]);
+    for (int q = 0; q < 4; ++q) {
+        const int r = q * 8 + (lane >> 2);
+        x.w[q] = make_uint4(0, 0, 0, 0);
+        if (r >= count) continue;
+        const bf16_t *p = rows + r * ld + off;
+        if (vec) {
+            if (in > 0) x.w[q] = *reinterpret_cast<const uint4 *>(p);
+        } else {
+            const unsigned short *s = reinterpret_cast<const unsigned short *>(p);
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < in) w[j / 2] |= (uint32_t)s[j] << 16 * (j & 1);
+            x.w[q] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
-    const bf16_t *pre = a.pre + row * a.ldpre + f;
-    if (a.act == AP_ACT_SWIGLU) {
+}
+__device__ __forceinline__ void piece_to_pairs(const Piece &x, uint8_t *pass, Pairs &p)
+{
+    const int lane = (int)lane_id();
+    __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < count) {
-                const float g = __bfloat162float(pre[j * a.ldpre]), u = __bfloat162float(pre[j * a.ldpre + a.F]);
-                put(out + j * a.ldo, v[j] * u * act_slope(AP_ACT_SILU, g));
-                put(out + j * a.ldo + a.F, v[j] * g * sigmoid_fast(g));
-            }
+    for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4 *>(pass + (q * 8 + (lane >> 2)) * kPassPitch + (lane & 3) * 16) = x.w[q];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) matrices_load(smem_addr(pass) + (i * 8 + (lane & 7)) * kPassPitch + (lane >> 3) * 16, p[i]);
+}
+__device__ __forceinline__ void pairs_store(const Pairs &p, uint8_t *pass, bf16_t *rows, int64_t ld, int count, const Span &n, bool vec)
+{
+    const int lane = (int)lane_id();
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) matrices_store(smem_addr(pass) + (i * 8 + (lane & 7)) * kPassPitch + (lane >> 3) * 16, p[i]);
+    __syncwarp();
+    if (vec) {
+        const int at = (lane & 1) * 8;
+        const int64_t off = (lane & 2 ? n.second : 0) + at;
+        const int in = (lane & 2 ? n.left2 : n.left) - at;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int r = q * 8 + (lane >> 2);
+            const uint4 w = *reinterpret_cast<const uint4 *>(pass + r * kPassPitch + (lane & 3) * 16);
+            if (r < count && in > 0) *reinterpret_cast<uint4 *>(rows + r * ld + off) = w;
+        }
+    } else { // a row at a time, a feature a lane
+        const int in = (lane < 16 ? n.left : n.left2) - (lane & 15);
+        unsigned short *to = reinterpret_cast<unsigned short *>(rows) + (lane & 15) + (lane < 16 ? 0 : n.second);
+        for (int r = 0; r < count; ++r)
+            if (in > 0) to[r * ld] = *reinterpret_cast<const unsigned short *>(pass + r * kPassPitch + lane * 2);
+    }
+}
+// The first halves alone (16 features).
+__device__ __forceinline__ void half_store(const uint32_t (&p)[4][2], uint8_t *pass, bf16_t *rows, int64_t ld, int count, int left,
+                                           bool vec)
+{
+    const int lane = (int)lane_id();
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t r[4] = {p[2 * i][0], p[2 * i][1], p[2 * i + 1][0], p[2 * i + 1][1]};
+        matrices_store(smem_addr(pass) + ((2 * i + (lane >> 4)) * 8 + (lane & 7)) * kPassPitch + (lane >> 3 & 1) * 16, r);
+    }
+    __syncwarp();
+    if (vec) {
+        const int at = (lane & 1) * 8;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int r = q * 16 + (lane >> 1);
+            const uint4 w = *reinterpret_cast<const uint4 *>(pass + r * kPassPitch + (lane & 1) * 16);
+            if (r < count && left > at) *reinterpret_cast<uint4 *>(rows + r * ld + at) = w;
+        }
     } else {
+        unsigned short *to = reinterpret_cast<unsigned short *>(rows) + (lane & 15);
+        for (int r = lane >> 4; r < count; r += 2)
+            if (left > (lane & 15)) to[r * ld] = *reinterpret_cast<const unsigned short *>(pass + r * kPassPitch + (lane & 15) * 2);
+    }
+}
+// FP32 results go straight to memory: eight lanes hold 32 bytes of a row.
+__device__ __forceinline__ void floats_store(const float (&v)[16], float *rows, int64_t ld, int count, int left)
+{
+    const int lane = (int)lane_id();
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < count) {
-                const float d = a.act == AP_ACT_NONE ? v[j] : v[j] * act_slope(a.act, __bfloat162float(pre[j * a.ldpre]));
-                put(out + j * a.ldo, d);
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int r = 8 * i + 2 * (lane & 3) + c, f = 8 * s + (lane >> 2);
+                if (r < count && f < left) rows[r * ld + f] = v[4 * i + 2 * s + c];
             }
+}
+__device__ __forceinline__ void to_pairs(const Frag &v, Pairs &p)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) p[i][2 * h + s] = pack(v[h][4 * i + 2 * s], v[h][4 * i + 2 * s + 1]);
+}
+// fn(value, what the pairs hold there) for all 32 values.
+template <typename Fn> __device__ __forceinline__ void with_pairs(Frag &v, const Pairs &p, Fn fn)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                v[h][4 * i + 2 * s] = fn(v[h][4 * i + 2 * s], low(p[i][2 * h + s]));
+                v[h][4 * i + 2 * s + 1] = fn(v[h][4 * i + 2 * s + 1], high(p[i][2 * h + s]));
+            }
+}
+__device__ __forceinline__ void result_store(const ExArgs &a, const Frag &v, uint8_t *pass, int64_t at, int count, int left)
+{
+    if (a.out_f32) {
+        float *out = static_cast<float *>(a.out) + at;
+        floats_store(v[0], out, a.ldo, count, left);
+        floats_store(v[1], out + 16, a.ldo, count, left - 16);
+    } else {
+        Pairs p;
+        to_pairs(v, p);
+        pairs_store(p, pass, static_cast<bf16_t *>(a.out) + at, a.ldo, count, together(left), a.vec_out);
     }
 }
 
-// 32 places of a weight's row (lane), one after the other in memory.
-template <typename T> __device__ __forceinline__ void write_weights(const ExArgs &a, const Tile &t, int c, float (&v)[32], int f)
+// What the epilogue reads of 32 rows, on its way while the products still run.
+struct Ahead {
+    Piece residual, first, second;
+};
+template <Op OP>
+__device__ __forceinline__ void read_ahead(const ExArgs &a, const Tile &t, int c, int part, Ahead &x)
+{
+    if (c >= t.n) return;
+    const int64_t row = (int64_t)t.row0 + c;
+    const int count = min(32, t.n - c);
+    const bool gated = a.act == AP_ACT_SWIGLU;
+    const int f = t.f0 + part * (OP == kForward && gated ? 16 : 32), left = a.F - f;
+    if (a.residual) piece_load(x.residual, a.residual + row * a.ldres + f, a.ldres, count,
+                               together(OP == kForward && gated ? min(left, 16) : left), a.vec_res);
+    if (OP == kRows && a.act != AP_ACT_NONE) {
+        piece_load(x.first, a.pre + row * a.ldpre + f, a.ldpre, count, together(left), a.vec_pre);
+        if (gated) piece_load(x.second, a.pre + row * a.ldpre + f + a.F, a.ldpre, count, together(left), a.vec_pre);
+    }
+}
+
+// The epilogue of 32 rows from c on: forwards.
+__device__ __forceinline__ void write_rows(const ExArgs &a, const Tile &t, int c, int part, Frag &v, const Ahead &x, uint8_t *pass)
+{
+    const int lane = (int)lane_id();
+    const int64_t row = (int64_t)t.row0 + c;
+    const int count = min(32, t.n - c);
+    const bool gated = a.act == AP_ACT_SWIGLU;
+    const int f = t.f0 + part * (gated ? 16 : 32), left = a.F - f;
+    if (left <= 0) return;
+    if (a.bias) {
+        const float *b = a.bias + (int64_t)t.e * (gated ? 2 : 1) * a.F + f + (lane >> 2);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const bool in = (gated ? 0 : 16 * h) + 8 * s + (lane >> 2) < left;
+                const float add = in ? b[(gated ? h * a.F : 16 * h) + 8 * s] : 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[h][4 * i + 2 * s] += add;
+                    v[h][4 * i + 2 * s + 1] += add;
+                }
+            }
+    }
+    Pairs p;
+    if (a.pre) {
+        to_pairs(v, p);
+        pairs_store(p, pass, a.pre + row * a.ldpre + f, a.ldpre, count, gated ? Span{left, left, a.F} : together(left), a.vec_pre);
+    }
+    if (gated) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[0][i] = v[0][i] * sigmoid_fast(v[0][i]) * v[1][i];
+    } else if (a.act == AP_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i / 16][i % 16] *= sigmoid_fast(v[i / 16][i % 16]);
+    } else if (a.act == AP_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i / 16][i % 16] *= normal_cdf(v[i / 16][i % 16]);
+    }
+    if (a.residual) {
+        piece_to_pairs(x.residual, pass, p);
+        with_pairs(v, p, [](float y, float r) { return y + r; });
+    }
+    const int64_t at = row * a.ldo + f;
+    if (!gated) {
+        result_store(a, v, pass, at, count, left);
+    } else if (a.out_f32) {
+        floats_store(v[0], static_cast<float *>(a.out) + at, a.ldo, count, left);
+    } else {
+        uint32_t q[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) q[i][s] = pack(v[0][4 * i + 2 * s], v[0][4 * i + 2 * s + 1]);
+        half_store(q, pass, static_cast<bf16_t *>(a.out) + at, a.ldo, count, left, a.vec_out);
+    }
+}
+
+// Backwards to the rows.
+__device__ __forceinline__ void write_slopes(const ExArgs &a, const Tile &t, int c, int part, Frag &v, const Ahead &x, uint8_t *pass)
+{
+    const int64_t row = (int64_t)t.row0 + c;
+    const int count = min(32, t.n - c);
+    const int f = t.f0 + part * 32, left = a.F - f;
+    if (left <= 0) return;
+    Pairs p;
+    if (a.residual) {
+        piece_to_pairs(x.residual, pass, p);
+        with_pairs(v, p, [](float y, float r) { return y + r; });
+    }
+    const int64_t at = row * a.ldo + f;
+    if (a.act == AP_ACT_SWIGLU) {
+        Pairs u;
+        piece_to_pairs(x.first, pass, p);
+        piece_to_pairs(x.second, pass, u);
+        Frag d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float g = e ? high(p[i][2 * h + s]) : low(p[i][2 * h + s]);
+                        const float w = e ? high(u[i][2 * h + s]) : low(u[i][2 * h + s]);
+                        const float q = sigmoid_fast(g), y = v[h][4 * i + 2 * s + e];
+                        v[h][4 * i + 2 * s + e] = y * w * (q * (1.f + g * (1.f - q)));
+                        d[h][4 * i + 2 * s + e] = y * g * q;
+                    }
+        result_store(a, v, pass, at, count, left);
+        result_store(a, d, pass, at + a.F, count, left);
+        return;
+    }
+    if (a.act == AP_ACT_SILU) {
+        piece_to_pairs(x.first, pass, p);
+        with_pairs(v, p, [](float y, float z) { return y * act_slope(AP_ACT_SILU, z); });
+    } else if (a.act == AP_ACT_GELU) {
+        piece_to_pairs(x.first, pass, p);
+        with_pairs(v, p, [](float y, float z) { return y * act_slope(AP_ACT_GELU, z); });
+    }
+    result_store(a, v, pass, at, count, left);
+}
+
+// 32 bytes in one go.
+struct alignas(32) Wide {
+    uint32_t w[8];
+};
+__device__ __forceinline__ Wide wide_load(const void *p)
+{
+    Wide x;
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]), "=r"(x.w[6]), "=r"(x.w[7])
+                 : "l"(p)
+                 : "memory");
+    return x;
+}
+__device__ __forceinline__ void wide_store(void *p, const Wide &x)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x.w[0]), "r"(x.w[1]), "r"(x.w[2]), "r"(x.w[3]),
+                 "r"(x.w[4]), "r"(x.w[5]), "r"(x.w[6]), "r"(x.w[7])
+                 : "memory");
+}
+
+// Weights: 32 places of a row (lane), one after the other in memory.  What is
+// there already is read while the products run.
+template <typename T> struct Kept {
+    Wide w[32 * sizeof(T) / 32];
+};
+template <typename T> __device__ __forceinline__ T *weights_at(const ExArgs &a, const Tile &t, int c, int f)
+{
+    return static_cast<T *>(a.out) + ((int64_t)t.e * a.F + f) * a.K + t.c0 + c;
+}
+template <typename T> __device__ __forceinline__ void read_weights(const ExArgs &a, const Tile &t, int c, int f, Kept<T> &x)
+{
+    if (!a.add || !a.vec_out || f >= a.F || c + 32 > t.n) return;
+    const T *p = weights_at<T>(a, t, c, f);
+#pragma unroll
+    for (int q = 0; q < (int)sizeof(T); ++q) x.w[q] = wide_load(p + q * (32 / sizeof(T)));
+}
+template <typename T> __device__ __forceinline__ void write_weights(const ExArgs &a, const Tile &t, int c, int f, float (&v)[32], const Kept<T> &x)
 {
     if (f >= a.F) return;
-    const int count = min(32, t.n - c);
-    T *out = static_cast<T *>(a.out) + ((int64_t)t.e * a.F + f) * a.K + t.c0 + c;
-    if (a.vec && count == 32) {
-        constexpr int kPer = 16 / sizeof(T);
+    T *out = weights_at<T>(a, t, c, f);
+    if (a.vec_out && c + 32 <= t.n) {
+        constexpr int kPer = 32 / sizeof(T);
 #pragma unroll
-        for (int j = 0; j < 32; j += kPer) {
-            uint4 *p = reinterpret_cast<uint4 *>(out + j);
-            T x[kPer];
-            if (a.add) {
-                const uint4 old = *p;
-                memcpy(x, &old, 16);
-            }
+        for (int q = 0; q < (int)sizeof(T); ++q) {
+            Wide n;
 #pragma unroll
-            for (int q = 0; q < kPer; ++q) {
-                float s = v[j + q];
-                if (a.add) s += (float)x[q];
-                put(x + q, s);
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (sizeof(T) == 4) {
+                    const float y = v[q * kPer + j];
+                    n.w[j] = __float_as_uint(a.add ? __uint_as_float(x.w[q].w[j]) + y : y);
+                } else {
+                    const float lo = v[q * kPer + 2 * j], hi = v[q * kPer + 2 * j + 1];
+                    n.w[j] = a.add ? pack(low(x.w[q].w[j]) + lo, high(x.w[q].w[j]) + hi) : pack(lo, hi);
+                }
             }
-            uint4 n;
-            memcpy(&n, x, 16);
-            *p = n;
+            wide_store(out + q * kPer, n);
         }
         return;
     }
+    const int count = min(32, t.n - c);
 #pragma unroll
     for (int j = 0; j < 32; ++j)
         if (j < count) put(out + j, a.add ? (float)out[j] + v[j] : v[j]);
 }
 
+// One writer: two for each quarter of the accumulator's lanes.
+template <Op OP, typename T>
+__device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int writer, uint32_t tmem, uint64_t *s_done, uint64_t *s_free,
+                                            uint8_t *pass, volatile int *dead)
+{
+    const int part = writer & 3, lane = (int)lane_id();
+    uint32_t count = 0;
+    bool ok = true;
+    for (; w.find(a.E); w.next()) {
+        const Tile t = tile_of<OP>(a, w);
+        const uint32_t acc = count & 1, at = tmem + acc * 256 + ((uint32_t)part * kWarp << 16);
+        const int f = t.f0 + part * kWarp + lane; // (of weights)
+        int c = (writer >> 2) * 32;
+        Ahead x;
+        Kept<T> kept;
+        if constexpr (OP == kWeights)
+            read_weights<T>(a, t, c, f, kept);
+        else
+            read_ahead<OP>(a, t, c, part, x);
+        if (t.steps > 0) {
+            ok = __all_sync(0xffffffffu, ok && bar_wait(smem_addr(&s_done[acc]), count >> 1 & 1, dead));
+            ++count;
+        }
+        fence_after();
+        const bool some = c < t.n;
+        for (; c < t.n; c += 64) {
+            const bool last = c + 64 >= t.n;
+            float v[32];
+            Frag y;
+            if (t.steps > 0 && ok) {
+                if constexpr (OP == kWeights)
+                    acc_load(at + c, v);
+                else
+                    acc_load_tiles(at + c, y);
+            } else { // nothing to add up, or products that did not come
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    v[j] = t.steps > 0 ? NAN : 0.f;
+                    y[j / 16][j % 16] = NAN;
+                }
+            }
+            if (last) { // the accumulator is read
+                fence_before();
+                __syncwarp();
+                if (lane == 0 && t.steps > 0) bar_arrive(smem_addr(&s_free[acc]));
+            }
+            if constexpr (OP == kWeights) {
+                const Kept<T> now = kept;
+                if (!last) read_weights<T>(a, t, c + 64, f, kept);
+                write_weights<T>(a, t, c, f, v, now);
+            } else {
+                const Ahead now = x;
+                if (!last) read_ahead<OP>(a, t, c + 64, part, x);
+                if constexpr (OP == kForward)
+                    write_rows(a, t, c, part, y, now, pass);
+                else
+                    write_slopes(a, t, c, part, y, now, pass);
+            }
+        }
+        if (!some && t.steps > 0) {
+            __syncwarp();
+            if (lane == 0) bar_arrive(smem_addr(&s_free[acc]));
+        }
+    }
+    if (!ok && a.d_status && lane == 0) atomicOr(a.d_status, AP_FLAG_CORRUPT);
+}
+
 template <Op OP, bool MAPS>
 __global__ void __launch_bounds__(kExThreads, 1)
-    k_experts(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const ExArgs a)
+    k_experts(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap whole,
+              const ExArgs a)
 {
     pdl_begin();
     extern __shared__ __align__(1024) uint8_t s_mem[];
     __shared__ Table s_tab;
-    __shared__ float s_swap[OP == kForward ? kLanes / 2 * kSwapPitch : 1];
+    __shared__ __align__(16) uint8_t s_pass[OP == kWeights ? 16 : kWriters * kPass];
     __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_done[2], s_free[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
@@ -382,7 +689,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(smem_addr(&s_done[s]), 1);
-            bar_init(smem_addr(&s_free[s]), kWriters / kWarp);
+            bar_init(smem_addr(&s_free[s]), kWriters);
         }
         bar_init(smem_addr(&s_drain), 1);
         bar_init_done();
@@ -414,7 +721,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
                         ok = false;
                         break;
                     }
-                    fetch<OP, MAPS>(a, t, step, stages + (size_t)s * stage_bytes, &mx, &mw, smem_addr(&s_full[s]), thread);
+                    fetch<OP, MAPS>(a, t, step, stages + (size_t)s * stage_bytes, &mx, &mw, &whole, smem_addr(&s_full[s]), thread);
                     ++count;
                     if (++s == (uint32_t)a.stages) {
                         s = 0;
@@ -486,44 +793,11 @@ __global__ void __launch_bounds__(kExThreads, 1)
         }
     } else if (wid >= 4) {
         // ---- write
-        const int part = wid & 3, lane_row = part * kWarp + lane;
-        uint32_t count = 0;
-        bool ok = true;
-        for (; w.find(a.E); w.next()) {
-            const Tile t = tile_of<OP>(a, w);
-            const uint32_t acc = count & 1;
-            if (t.steps > 0) {
-                if (ok && !bar_wait(smem_addr(&s_done[acc]), count >> 1 & 1, dead)) ok = false;
-                ++count;
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            fence_after();
-            const int f = t.f0 + (OP == kForward && a.act == AP_ACT_SWIGLU ? lane_row & (kLanes / 2 - 1) : lane_row);
-            for (int c = 0; c < t.n; c += 32) {
-                float v[32];
-                if (t.steps > 0 && ok) {
-                    acc_load(tmem + acc * 256 + c + ((uint32_t)part * kWarp << 16), v);
-                } else { // nothing to add up, or products that did not come
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = t.steps > 0 ? NAN : 0.f;
-                }
-                if (c + 32 >= t.n) { // the accumulator is read
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0 && t.steps > 0) bar_arrive(smem_addr(&s_free[acc]));
-                }
-                if (a.out_f32) {
-                    if (OP == kForward) write_rows<float>(a, t, c, v, f, lane_row, s_swap);
-                    if (OP == kRows) write_slopes<float>(a, t, c, v, f);
-                    if (OP == kWeights) write_weights<float>(a, t, c, v, f);
-                } else {
-                    if (OP == kForward) write_rows<bf16_t>(a, t, c, v, f, lane_row, s_swap);
-                    if (OP == kRows) write_slopes<bf16_t>(a, t, c, v, f);
-                    if (OP == kWeights) write_weights<bf16_t>(a, t, c, v, f);
-                }
-            }
-        }
-        if (!ok && a.d_status && lane == 0) atomicOr(a.d_status, AP_FLAG_CORRUPT);
+        uint8_t *pass = s_pass + (OP == kWeights ? 0 : (wid - 4) * kPass);
+        if (OP == kWeights && !a.out_f32)
+            write_tiles<OP, bf16_t>(a, w, wid - 4, tmem, s_done, s_free, pass, dead);
+        else
+            write_tiles<OP, float>(a, w, wid - 4, tmem, s_done, s_free, pass, dead);
     }
     __syncwarp();
     fence_before();
@@ -575,7 +849,8 @@ bool mappable(const void *p, int64_t ld, int64_t more = 0)
 }
 
 template <Op OP, bool MAPS>
-ap_status launch_experts(const char *who, const CUtensorMap &mx, const CUtensorMap &mw, ExArgs a, int64_t tiles, cudaStream_t st)
+ap_status launch_experts(const char *who, const CUtensorMap &mx, const CUtensorMap &mw, const CUtensorMap &whole, ExArgs a, int64_t tiles,
+                         cudaStream_t st)
 {
     const auto kernel = k_experts<OP, MAPS>;
     cudaFuncAttributes attr;
@@ -587,7 +862,7 @@ ap_status launch_experts(const char *who, const CUtensorMap &mx, const CUtensorM
     const int stage = 2 * kPanel + a.columns * 128, room = kMaxSmem - fixed - 1024;
     a.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
     const int sms = sm_count();
-    launch(kernel, (int)(tiles < sms ? tiles : sms), kExThreads, (size_t)a.stages * stage + 1024, st, mx, mw, a);
+    launch(kernel, (int)(tiles < sms ? tiles : sms), kExThreads, (size_t)a.stages * stage + 1024, st, mx, mw, whole, a);
     AP_CHECK_LAUNCH(who);
     return AP_OK;
 }
@@ -615,22 +890,36 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, cudaStream_
 {
     if (a.E == 1) a.lde = a.ldw * (op == kForward ? a.F * halves : a.K); // (of no account)
     a.columns = columns_for(a.rows, a.E);
+    a.vec_out = !odd_address(a.out, 16) && a.ldo % 8 == 0 && a.F % 8 == 0;
+    a.vec_pre = !odd_address(a.pre, 16) && a.ldpre % 8 == 0 && a.F % 8 == 0;
+    a.vec_res = !odd_address(a.residual, 16) && a.ldres % 8 == 0 && a.F % 8 == 0;
     const int per = op == kForward && halves == 2 ? kLanes / 2 : kLanes;
     a.tiles_f = (a.F + per - 1) / per;
     const int64_t tiles = (a.rows / a.columns + a.E) * (int64_t)a.tiles_f;
     if (tiles >= INT32_MAX) return fail(AP_EINVAL, "%s: %lld tiles are more than one launch takes", who, (long long)tiles);
-    CUtensorMap mx = {}, mw = {};
+    CUtensorMap mx = {}, mw = {}, whole = {};
     if (!mappable(a.x, a.ldx) || !mappable(a.W, a.ldw, a.lde))
-        return op == kForward ? launch_experts<kForward, false>(who, mx, mw, a, tiles, st)
-                              : launch_experts<kRows, false>(who, mx, mw, a, tiles, st);
+        return op == kForward ? launch_experts<kForward, false>(who, mx, mw, whole, a, tiles, st)
+                              : launch_experts<kRows, false>(who, mx, mw, whole, a, tiles, st);
     const int wide = op == kForward ? a.F * halves : a.K, deep = op == kForward ? a.K : a.F; // of W[e]
     const uint64_t ex[2] = {(uint64_t)a.K, (uint64_t)a.rows}, px[1] = {(uint64_t)a.ldx};
-    const uint64_t ew[3] = {(uint64_t)deep, (uint64_t)wide, (uint64_t)a.E}, pw[2] = {(uint64_t)a.ldw, (uint64_t)a.lde};
-    const uint32_t bx[2] = {64, 32}, bw[3] = {64, 64, 1};
-    if (!make_map(&mx, a.x, 2, ex, px, bx) || !make_map(&mw, a.W, 3, ew, pw, bw))
-        return fail(AP_ENOTSUP, "%s: no tensor map of these sizes", who);
-    return op == kForward ? launch_experts<kForward, true>(who, mx, mw, a, tiles, st)
-                          : launch_experts<kRows, true>(who, mx, mw, a, tiles, st);
+    const uint32_t bx[2] = {64, 32}, ball[2] = {64, (uint32_t)a.columns};
+    bool ok = make_map(&mx, a.x, 2, ex, px, bx) && make_map(&whole, a.x, 2, ex, px, ball);
+    // One copy for a gated product's features needs whole sixteens: 8 copies of 16 lines took 957 us where one takes ... us
+    a.by16 = op == kForward && halves == 2 && a.F % 16 == 0;
+    if (a.by16) {
+        const uint64_t ew[5] = {(uint64_t)deep, 16, 2, (uint64_t)a.F / 16, (uint64_t)a.E};
+        const uint64_t pw[4] = {(uint64_t)a.ldw, (uint64_t)(a.F * a.ldw), (uint64_t)(16 * a.ldw), (uint64_t)a.lde};
+        const uint32_t bw[5] = {64, 16, 2, 4, 1};
+        ok = ok && make_map(&mw, a.W, 5, ew, pw, bw);
+    } else {
+        const uint64_t ew[3] = {(uint64_t)deep, (uint64_t)wide, (uint64_t)a.E}, pw[2] = {(uint64_t)a.ldw, (uint64_t)a.lde};
+        const uint32_t bw[3] = {64, op == kRows ? 64u : halves == 2 ? 16u : 128u, 1};
+        ok = ok && make_map(&mw, a.W, 3, ew, pw, bw);
+    }
+    if (!ok) return fail(AP_ENOTSUP, "%s: no tensor map of these sizes", who);
+    return op == kForward ? launch_experts<kForward, true>(who, mx, mw, whole, a, tiles, st)
+                          : launch_experts<kRows, true>(who, mx, mw, whole, a, tiles, st);
 }
 
 } // namespace
@@ -650,8 +939,8 @@ bool umma::make_map(CUtensorMap *map, const void *base, int dims, const uint64_t
         return reinterpret_cast<Encode>(p);
     }();
     if (!encode) return false;
-    cuuint64_t strides[2], sizes[3];
-    cuuint32_t ones[3] = {1, 1, 1};
+    cuuint64_t strides[4], sizes[5];
+    cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < dims; ++i) sizes[i] = extent[i];
     for (int i = 0; i + 1 < dims; ++i) strides[i] = pitch[i] * 2;
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void *>(base), sizes, strides, box, ones,
@@ -738,10 +1027,10 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
         a.out_f32 = dw_dtype == AP_DTYPE_F32, a.add = accumulate != 0;
         a.columns = K > 128 ? 256 : K > 64 ? 128 : 64;
         a.tiles_f = (N + kLanes - 1) / kLanes;
-        a.vec = !odd_address(dW, 16) && K % (a.out_f32 ? 4 : 8) == 0;
+        a.vec_out = !odd_address(dW, 32) && K % (a.out_f32 ? 8 : 16) == 0;
         const int64_t tiles = (int64_t)E * a.tiles_f * ((K + a.columns - 1) / a.columns);
         if (tiles >= INT32_MAX) return fail(AP_EINVAL, "%s: %lld tiles are more than one launch takes", who, (long long)tiles);
-        CUtensorMap mx = {}, mw = {};
+        CUtensorMap mx = {}, mw = {}, whole = {};
         ap_status s;
         if (rows > 0 && mappable(dy, ldy) && mappable(x, ldx)) {
             const uint64_t ey[2] = {(uint64_t)N, (uint64_t)rows}, py[1] = {(uint64_t)ldy};
@@ -749,9 +1038,9 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
             const uint32_t box[2] = {64, 64};
             if (!make_map(&mx, dy, 2, ey, py, box) || !make_map(&mw, x, 2, ex, px, box))
                 return fail(AP_ENOTSUP, "%s: no tensor map of these sizes", who);
-            s = launch_experts<kWeights, true>(who, mx, mw, a, tiles, st);
+            s = launch_experts<kWeights, true>(who, mx, mw, whole, a, tiles, st);
         } else {
-            s = launch_experts<kWeights, false>(who, mx, mw, a, tiles, st);
+            s = launch_experts<kWeights, false>(who, mx, mw, whole, a, tiles, st);
         }
         if (s != AP_OK) return s;
     }

@@ -61,6 +61,13 @@ __device__ __forceinline__ void tma_3d(uint32_t to, const CUtensorMap *map, int 
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void tma_5d(uint32_t to, const CUtensorMap *map, int x, int y, int z, int u, int v, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+                 "[%7];" ::"r"(to),
+                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
+                 : "memory");
+}
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -128,6 +135,45 @@ __device__ __forceinline__ void acc_load(uint32_t at, float (&v)[32])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The same 32 lanes and columns as two halves of 16 lanes in the layout of 8 x 8
+// matrices: v[h][4 i + 2 s + c] is lane 16 h + 8 s + l / 4 and column 8 i +
+// 2 (l % 4) + c of the warp's lane l.
+__device__ __forceinline__ void acc_load_tiles(uint32_t at, float (&v)[2][16])
+{
+    uint32_t r[2][16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                     "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                     : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3]), "=r"(r[h][4]), "=r"(r[h][5]), "=r"(r[h][6]),
+                       "=r"(r[h][7]), "=r"(r[h][8]), "=r"(r[h][9]), "=r"(r[h][10]), "=r"(r[h][11]), "=r"(r[h][12]),
+                       "=r"(r[h][13]), "=r"(r[h][14]), "=r"(r[h][15])
+                     : "r"(at + ((uint32_t)h << 20))
+                     : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[h][i] = __uint_as_float(r[h][i]);
+}
+
+// ---- 8 x 8 matrices of 16-bit values, transposed on their way --------------------------
+// Lane l gives the address of row l % 8 of matrix l / 8 in memory; a lane holds
+// two neighbours of a column there.
+__device__ __forceinline__ void matrices_store(uint32_t at, const uint32_t (&r)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3])
+                 : "memory");
+}
+__device__ __forceinline__ void matrices_load(uint32_t at, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
 }
 
 // ---- host ---------------------------------------------------------------------------

@@ -176,6 +176,14 @@ def test_forward(K, N, act):
     check_forward(Rows(RAGGED, gap=3), K, N, act, bias=True, residual=True)
 
 
+@pytest.mark.parametrize("N", [8, 15, 16, 17, 24, 32, 48, 64])
+@pytest.mark.parametrize("residual", [True, False])
+def test_gated_halves_of_any_width(N, residual):
+    """Widths at which a writer's 16 features of either half end."""
+    check_forward(Rows([40, 3]), 64, N, "swiglu", bias=True, residual=residual)
+    check_rows(Rows([40, 3]), 64, N, "swiglu", residual=residual)
+
+
 @pytest.mark.parametrize("K,N", [(1, 1), (63, 65), (65, 127), (203, 517), (1003, 130)])
 @pytest.mark.parametrize("act", [None, "gelu", "swiglu"])
 def test_forward_of_odd_rows(K, N, act):
