@@ -30,6 +30,8 @@ int resident_grid(const void *kernel, int threads, size_t smem = 0);
 // 16.  Asked for each call, since a stream's handle may name another stream
 // later: 0.2 us.
 int cluster_fit(const void *kernel, int threads, size_t smem, int most, cudaStream_t st);
+// Clusters of `cluster` blocks of `kernel` that the stream's SMs take at once (0: none).
+int cluster_count(const void *kernel, int threads, size_t smem, int cluster, cudaStream_t st);
 
 // Dispatch stages shared by the dispatch entry points (dispatch.cu): argument
 // checks, then the count/rank and scan launches that produce counts, live,

@@ -89,24 +89,28 @@ int resident_grid(const void *kernel, int threads, size_t smem)
     return per_sm * sm_count();
 }
 
-int cluster_fit(const void *kernel, int threads, size_t smem, int most, cudaStream_t st)
+int cluster_count(const void *kernel, int threads, size_t smem, int cluster, cudaStream_t st)
 {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = cluster;
     cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    for (; most > 1; most /= 2) {
-        int n = 0;
-        attr[0].val.clusterDim.x = most;
-        cfg.gridDim = most;
-        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) break;
-        (void)cudaGetLastError();
-    }
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) return n;
+    (void)cudaGetLastError();
+    return 0;
+}
+
+int cluster_fit(const void *kernel, int threads, size_t smem, int most, cudaStream_t st)
+{
+    while (most > 1 && cluster_count(kernel, threads, smem, most, st) < 1) most /= 2;
     return most;
 }
 

@@ -91,15 +91,15 @@ struct Table { // in shared memory
 };
 struct Walk {
     const Table &tab;
-    int t, e;
-    __device__ __forceinline__ Walk(const Table &table) : tab(table), t((int)blockIdx.x), e(0) {}
+    int t, e, step;
+    __device__ __forceinline__ Walk(const Table &table, int from, int by) : tab(table), t(from), e(0), step(by) {}
     __device__ __forceinline__ bool find(int E)
     {
         if (t >= tab.first[E]) return false;
         while (t >= tab.first[e + 1]) ++e;
         return true;
     }
-    __device__ __forceinline__ void next() { t += (int)gridDim.x; }
+    __device__ __forceinline__ void next() { t += step; }
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -142,12 +142,13 @@ template <Op OP> __device__ void count_tiles(const ExArgs &a, Table &tab)
     if (bad && a.d_status && blockIdx.x == 0) atomicOr(a.d_status, AP_FLAG_BAD_COUNT);
 }
 
-// What a tile is: features from f0, columns (rows of the output, or kWeights:
-// places of a weight's row) from c0, n of them; the contraction's steps.
+// What a tile is: features from f0 (this block's, of a pair's), columns (rows of
+// the output, or kWeights: places of a weight's row) from c0, n of them; the
+// contraction's steps.  An expert's rows are shared out evenly among its tiles.
 struct Tile {
     int e, f0, c0, n, steps, row0, live;
 };
-template <Op OP> __device__ __forceinline__ Tile tile_of(const ExArgs &a, const Walk &w)
+template <Op OP, bool PAIR> __device__ __forceinline__ Tile tile_of(const ExArgs &a, const Walk &w, int rank)
 {
     Tile t;
     t.e = w.e;
@@ -156,9 +157,10 @@ template <Op OP> __device__ __forceinline__ Tile tile_of(const ExArgs &a, const 
     const int width = OP == kWeights ? a.K : t.live;
     const int across = ceil_div(width, a.columns);
     const int f = at / across, c = at - f * across;
-    t.f0 = f * (OP == kForward && a.act == AP_ACT_SWIGLU ? kLanes / 2 : kLanes);
-    t.c0 = c * a.columns;
-    t.n = min(a.columns, width - t.c0);
+    const int each = OP == kWeights ? a.columns : (ceil_div(width, across) + 31) & ~31;
+    t.f0 = ((PAIR ? 2 : 1) * f + rank) * (OP == kForward && a.act == AP_ACT_SWIGLU ? kLanes / 2 : kLanes);
+    t.c0 = c * each;
+    t.n = min(each, width - t.c0);
     t.row0 = w.tab.seg[w.e] + (OP == kWeights ? 0 : t.c0);
     t.steps = OP == kWeights ? ceil_div(t.live, kDepth) : ceil_div(a.K, kDepth);
     return t;
@@ -185,9 +187,9 @@ __device__ __forceinline__ void fill_panel(uint8_t *to, const bf16_t *src, int64
 // A stage: the features' operand (16 KB), then the columns'.  A gated product's
 // features alternate by 16 between the gate's and the up product's, so that a
 // writing lane finds both.
-template <Op OP, bool MAPS>
+template <Op OP, bool MAPS, bool PAIR>
 __device__ __forceinline__ void fetch(const ExArgs &a, const Tile &t, int step, uint8_t *stage, const CUtensorMap *mx,
-                                      const CUtensorMap *mw, const CUtensorMap *whole, uint32_t full, int thread)
+                                      const CUtensorMap *mw, const CUtensorMap *whole, uint32_t full, int rank, int thread)
 {
     const int k0 = step * kDepth;
     const bool gated = OP == kForward && a.act == AP_ACT_SWIGLU;
@@ -195,28 +197,35 @@ __device__ __forceinline__ void fetch(const ExArgs &a, const Tile &t, int step, 
     const int n = OP == kWeights ? ceil_div(t.n, 64) : ceil_div(t.n, 32);
     if constexpr (MAPS) {
         const uint32_t sa = smem_addr(stage), sb = smem_addr(col);
-        const bool all = OP != kWeights && t.n > a.columns - 32; // the tile's rows in one copy
-        bar_expect(full, 2 * kPanel + (all ? a.columns * 128 : n * (OP == kWeights ? kPanel : kPanel / 2)));
+        // a pair's blocks bring half of the tile's rows each, and all tell the first one's barrier
+        const int half = (t.n + 31) / 32 * 16, rows = PAIR ? half : t.n, most = PAIR ? a.columns / 2 : a.columns;
+        const int small = a.columns >= 128 ? 64 : 32, boxes = ceil_div(rows, small);
+        const bool all = rows > most - small; // in one copy
+        const int bytes = 2 * kPanel + (OP == kWeights ? n * kPanel : all ? most * 128 : boxes * small * 128);
+        if (rank == 0) bar_expect(full, PAIR ? 2 * bytes : bytes);
+        const uint32_t bar = PAIR ? cluster_addr(full, 0) : full;
         if (gated && a.by16) {
-            tma_5d(sa, mw, k0, 0, 0, t.f0 >> 4, t.e, full);
+            tma_5d<PAIR>(sa, mw, k0, 0, 0, t.f0 >> 4, t.e, bar);
         } else if (gated) {
 #pragma unroll
-            for (int b = 0; b < 8; ++b) tma_3d(sa + b * 2048, mw, k0, t.f0 + (b >> 1) * 16 + (b & 1) * a.F, t.e, full);
+            for (int b = 0; b < 8; ++b) tma_3d<PAIR>(sa + b * 2048, mw, k0, t.f0 + (b >> 1) * 16 + (b & 1) * a.F, t.e, bar);
         } else if (OP == kForward) {
-            tma_3d(sa, mw, k0, t.f0, t.e, full);
+            tma_3d<PAIR>(sa, mw, k0, t.f0, t.e, bar);
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (OP == kRows) tma_3d(sa + h * kPanel, mw, t.f0 + h * 64, k0, t.e, full);
-                if (OP == kWeights) tma_2d(sa + h * kPanel, mx, t.f0 + h * 64, t.row0 + k0, full);
+                if (OP == kRows) tma_3d<PAIR>(sa + h * kPanel, mw, t.f0 + h * 64, k0, t.e, bar);
+                if (OP == kWeights) tma_2d<PAIR>(sa + h * kPanel, mx, t.f0 + h * 64, t.row0 + k0, bar);
             }
         }
-        if (all) tma_2d(sb, whole, k0, t.row0, full);
-        for (int i = 0; i < n && !all; ++i) {
-            if (OP == kWeights)
-                tma_2d(sb + i * kPanel, mw, t.c0 + i * 64, t.row0 + k0, full);
+        if (OP == kWeights) {
+            for (int i = 0; i < n; ++i) tma_2d<PAIR>(sb + i * kPanel, mw, t.c0 + i * 64, t.row0 + k0, bar);
+        } else {
+            const int row = t.row0 + (PAIR ? rank * half : 0);
+            if (all)
+                tma_2d<PAIR>(sb, whole, k0, row, bar);
             else
-                tma_2d(sb + i * (kPanel / 2), mx, k0, t.row0 + i * 32, full);
+                for (int i = 0; i < boxes; ++i) tma_2d<PAIR>(sb + i * small * 128, mx, k0, row + i * small, bar);
         }
     } else {
         if (gated) {
@@ -601,15 +610,21 @@ template <typename T> __device__ __forceinline__ void write_weights(const ExArgs
 }
 
 // One writer: two for each quarter of the accumulator's lanes.
-template <Op OP, typename T>
-__device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int writer, uint32_t tmem, uint64_t *s_done, uint64_t *s_free,
-                                            uint8_t *pass, volatile int *dead)
+template <Op OP, bool PAIR, typename T>
+__device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, int writer, uint32_t tmem, uint64_t *s_done,
+                                            uint64_t *s_free, uint8_t *pass, volatile int *dead)
 {
+    const auto release = [&](uint32_t acc) { // the accumulator is read
+        if (PAIR)
+            bar_arrive_at(cluster_addr(smem_addr(&s_free[acc]), 0));
+        else
+            bar_arrive(smem_addr(&s_free[acc]));
+    };
     const int part = writer & 3, lane = (int)lane_id();
     uint32_t count = 0;
     bool ok = true;
     for (; w.find(a.E); w.next()) {
-        const Tile t = tile_of<OP>(a, w);
+        const Tile t = tile_of<OP, PAIR>(a, w, rank);
         const uint32_t acc = count & 1, at = tmem + acc * 256 + ((uint32_t)part * kWarp << 16);
         const int f = t.f0 + part * kWarp + lane; // (of weights)
         int c = (writer >> 2) * 32;
@@ -641,10 +656,10 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int writer
                     y[j / 16][j % 16] = NAN;
                 }
             }
-            if (last) { // the accumulator is read
+            if (last) {
                 fence_before();
                 __syncwarp();
-                if (lane == 0 && t.steps > 0) bar_arrive(smem_addr(&s_free[acc]));
+                if (lane == 0 && t.steps > 0) release(acc);
             }
             if constexpr (OP == kWeights) {
                 const Kept<T> now = kept;
@@ -661,13 +676,13 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int writer
         }
         if (!some && t.steps > 0) {
             __syncwarp();
-            if (lane == 0) bar_arrive(smem_addr(&s_free[acc]));
+            if (lane == 0) release(acc);
         }
     }
     if (!ok && a.d_status && lane == 0) atomicOr(a.d_status, AP_FLAG_CORRUPT);
 }
 
-template <Op OP, bool MAPS>
+template <Op OP, bool MAPS, bool PAIR>
 __global__ void __launch_bounds__(kExThreads, 1)
     k_experts(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap whole,
               const ExArgs a)
@@ -680,7 +695,8 @@ __global__ void __launch_bounds__(kExThreads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
     const int wid = threadIdx.x / kWarp, lane = (int)lane_id();
-    const int stage_bytes = 2 * kPanel + a.columns * 128;
+    const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
+    const int stage_bytes = 2 * kPanel + a.columns * (PAIR ? 64 : 128);
     uint8_t *stages = s_mem + ((1024 - (smem_addr(s_mem) & 1023)) & 1023);
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
@@ -689,20 +705,21 @@ __global__ void __launch_bounds__(kExThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(smem_addr(&s_done[s]), 1);
-            bar_init(smem_addr(&s_free[s]), kWriters);
+            bar_init(smem_addr(&s_free[s]), (PAIR ? 2 : 1) * kWriters);
         }
         bar_init(smem_addr(&s_drain), 1);
         bar_init_done();
         s_dead = 0;
     }
-    if (wid == 1) tmem_alloc(smem_addr(&s_tmem), 512);
+    if (wid == 1) tmem_alloc<PAIR>(smem_addr(&s_tmem), 512);
     if (wid == 2) count_tiles<OP>(a, s_tab);
     fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync(); // the other block's barriers are ready, and it has the table of its own
     fence_after();
     const uint32_t tmem = s_tmem;
     volatile int *dead = &s_dead;
-    Walk w(s_tab);
+    Walk w(s_tab, (int)blockIdx.x / (PAIR ? 2 : 1), (int)gridDim.x / (PAIR ? 2 : 1));
 
     if (wid == 0 || (!MAPS && (wid == 2 || wid == 3))) {
         // ---- fetch: stage by stage, as they fall empty
@@ -711,17 +728,19 @@ __global__ void __launch_bounds__(kExThreads, 1)
             if (MAPS) {
                 tma_prefetch_map(&mx);
                 tma_prefetch_map(&mw);
+                if (OP != kWeights) tma_prefetch_map(&whole);
             }
             uint32_t count = 0, s = 0, turn = 0; // stages fetched; ring position and its turn
             bool ok = true;
             for (; ok && w.find(a.E); w.next()) {
-                const Tile t = tile_of<OP>(a, w);
+                const Tile t = tile_of<OP, PAIR>(a, w, rank);
                 for (int step = 0; step < t.steps; ++step) {
                     if (count >= (uint32_t)a.stages && !bar_wait(smem_addr(&s_empty[s]), (turn & 1) ^ 1, dead)) {
                         ok = false;
                         break;
                     }
-                    fetch<OP, MAPS>(a, t, step, stages + (size_t)s * stage_bytes, &mx, &mw, &whole, smem_addr(&s_full[s]), thread);
+                    fetch<OP, MAPS, PAIR>(a, t, step, stages + (size_t)s * stage_bytes, &mx, &mw, &whole, smem_addr(&s_full[s]), rank,
+                                          thread);
                     ++count;
                     if (++s == (uint32_t)a.stages) {
                         s = 0;
@@ -729,26 +748,32 @@ __global__ void __launch_bounds__(kExThreads, 1)
                     }
                 }
             }
-            if (MAPS && !ok) { // copies on their way end before the block does
+            if (MAPS && (PAIR || !ok)) {
+                // Copies on their way end before the block does (a pair's are told to the first block, which the second
+                // waits for below), and so do the arrivals that the other block's products send here.
                 volatile int none = 0;
                 for (uint32_t i = 0; i < (uint32_t)a.stages && i < count; ++i) {
-                    const uint32_t c = count - 1 - i;
+                    const uint32_t c = count - 1 - i, at = c % a.stages, parity = c / a.stages & 1;
                     none = 0;
-                    (void)bar_wait(smem_addr(&s_full[c % a.stages]), c / a.stages & 1, &none);
+                    if (ok)
+                        (void)bar_wait(smem_addr(&s_empty[at]), parity, dead);
+                    else if (rank == 0)
+                        (void)bar_wait(smem_addr(&s_full[at]), parity, &none);
                 }
             }
         }
-    } else if (wid == 1) {
+    } else if (wid == 1 && rank == 0) {
         // ---- multiply
         uint32_t s = 0, turn = 0, count = 0; // ring; tiles so far
         bool ok = true;
         for (; ok && w.find(a.E); w.next()) {
-            const Tile t = tile_of<OP>(a, w);
+            const Tile t = tile_of<OP, PAIR>(a, w, rank);
             if (t.steps == 0) continue;
             const uint32_t acc = count & 1;
             if (count >= 2 && !__all_sync(0xffffffffu, bar_wait(smem_addr(&s_free[acc]), (count >> 1 & 1) ^ 1, dead))) break;
             fence_after();
-            const uint32_t shape = shape_of(kLanes, (t.n + 15) & ~15, OP != kForward, OP == kWeights);
+            const uint32_t shape = shape_of(PAIR ? 2 * kLanes : kLanes, PAIR ? (t.n + 31) & ~31 : (t.n + 15) & ~15, OP != kForward,
+                                            OP == kWeights);
             for (int step = 0; step < t.steps; ++step) {
                 if (!__all_sync(0xffffffffu, bar_wait(smem_addr(&s_full[s]), turn & 1, dead))) {
                     ok = false;
@@ -769,9 +794,9 @@ __global__ void __launch_bounds__(kExThreads, 1)
                     const uint32_t sa = smem_addr(stage), sb = sa + 2 * kPanel;
 #pragma unroll
                     for (int k = 0; k < kDepth / 16; ++k)
-                        mma(tmem + acc * 256, operand(sa + k * (OP == kForward ? 32 : 2048), kPanel),
-                            operand(sb + k * (OP == kWeights ? 2048 : 32), kPanel), shape, step > 0 || k > 0);
-                    mma_commit(smem_addr(&s_empty[s]));
+                        mma<PAIR>(tmem + acc * 256, operand(sa + k * (OP == kForward ? 32 : 2048), kPanel),
+                                  operand(sb + k * (OP == kWeights ? 2048 : 32), kPanel), shape, step > 0 || k > 0);
+                    mma_commit<PAIR>(smem_addr(&s_empty[s]));
                 }
                 __syncwarp();
                 if (++s == (uint32_t)a.stages) {
@@ -779,14 +804,14 @@ __global__ void __launch_bounds__(kExThreads, 1)
                     ++turn;
                 }
             }
-            if (ok && lane == 0) mma_commit(smem_addr(&s_done[acc]));
+            if (ok && lane == 0) mma_commit<PAIR>(smem_addr(&s_done[acc]));
             __syncwarp();
             ++count;
         }
         if (__any_sync(0xffffffffu, *dead)) { // products on their way end before tensor memory is freed
             volatile int none = 0;
             if (lane == 0) {
-                mma_commit(smem_addr(&s_drain));
+                mma_commit<PAIR>(smem_addr(&s_drain));
                 (void)bar_wait(smem_addr(&s_drain), 0, &none);
             }
             __syncwarp();
@@ -795,16 +820,17 @@ __global__ void __launch_bounds__(kExThreads, 1)
         // ---- write
         uint8_t *pass = s_pass + (OP == kWeights ? 0 : (wid - 4) * kPass);
         if (OP == kWeights && !a.out_f32)
-            write_tiles<OP, bf16_t>(a, w, wid - 4, tmem, s_done, s_free, pass, dead);
+            write_tiles<OP, PAIR, bf16_t>(a, w, rank, wid - 4, tmem, s_done, s_free, pass, dead);
         else
-            write_tiles<OP, float>(a, w, wid - 4, tmem, s_done, s_free, pass, dead);
+            write_tiles<OP, PAIR, float>(a, w, rank, wid - 4, tmem, s_done, s_free, pass, dead);
     }
     __syncwarp();
     fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync(); // neither block's memory is used by the other any more
     if (wid == 1) {
         fence_after();
-        tmem_free(tmem, 512);
+        tmem_free<PAIR>(tmem, 512);
     }
 }
 
@@ -848,21 +874,28 @@ bool mappable(const void *p, int64_t ld, int64_t more = 0)
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && more % 8 == 0;
 }
 
-template <Op OP, bool MAPS>
+template <Op OP, bool MAPS, bool PAIR = false>
 ap_status launch_experts(const char *who, const CUtensorMap &mx, const CUtensorMap &mw, const CUtensorMap &whole, ExArgs a, int64_t tiles,
                          cudaStream_t st)
 {
-    const auto kernel = k_experts<OP, MAPS>;
+    const auto kernel = k_experts<OP, MAPS, PAIR>;
     cudaFuncAttributes attr;
     static const int fixed = cudaFuncGetAttributes(&attr, (const void *)kernel) == cudaSuccess ? (int)attr.sharedSizeBytes : -1;
     if (fixed < 0) return cuda_fail(cudaGetLastError(), who);
     static const cudaError_t set =
         cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - fixed);
     if (set != cudaSuccess) return cuda_fail(set, who);
-    const int stage = 2 * kPanel + a.columns * 128, room = kMaxSmem - fixed - 1024;
+    const int stage = 2 * kPanel + a.columns * (PAIR ? 64 : 128), room = kMaxSmem - fixed - 1024;
     a.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
-    const int sms = sm_count();
-    launch(kernel, (int)(tiles < sms ? tiles : sms), kExThreads, (size_t)a.stages * stage + 1024, st, mx, mw, whole, a);
+    const size_t smem = (size_t)a.stages * stage + 1024;
+    if constexpr (PAIR) {
+        const int pairs = cluster_count((const void *)kernel, kExThreads, smem, 2, st);
+        if (pairs < 1) return fail(AP_ENOTSUP, "%s: the stream's SMs take no pair of blocks", who);
+        launch_cluster(kernel, 2 * (int)(tiles < pairs ? tiles : pairs), kExThreads, smem, 2, st, mx, mw, whole, a);
+    } else {
+        const int sms = sm_count();
+        launch(kernel, (int)(tiles < sms ? tiles : sms), kExThreads, smem, st, mx, mw, whole, a);
+    }
     AP_CHECK_LAUNCH(who);
     return AP_OK;
 }
@@ -893,17 +926,20 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, cudaStream_
     a.vec_out = !odd_address(a.out, 16) && a.ldo % 8 == 0 && a.F % 8 == 0;
     a.vec_pre = !odd_address(a.pre, 16) && a.ldpre % 8 == 0 && a.F % 8 == 0;
     a.vec_res = !odd_address(a.residual, 16) && a.ldres % 8 == 0 && a.F % 8 == 0;
-    const int per = op == kForward && halves == 2 ? kLanes / 2 : kLanes;
+    const bool maps = mappable(a.x, a.ldx) && mappable(a.W, a.ldw, a.lde);
+    // Two blocks to a tile of 256 features share its rows' operand: 32 KB from L2 for 48 a product.
+    const bool pair = maps && a.columns == 256 && a.F * (op == kForward ? halves : 1) > kLanes;
+    const int per = (op == kForward && halves == 2 ? kLanes / 2 : kLanes) * (pair ? 2 : 1);
     a.tiles_f = (a.F + per - 1) / per;
     const int64_t tiles = (a.rows / a.columns + a.E) * (int64_t)a.tiles_f;
     if (tiles >= INT32_MAX) return fail(AP_EINVAL, "%s: %lld tiles are more than one launch takes", who, (long long)tiles);
     CUtensorMap mx = {}, mw = {}, whole = {};
-    if (!mappable(a.x, a.ldx) || !mappable(a.W, a.ldw, a.lde))
+    if (!maps)
         return op == kForward ? launch_experts<kForward, false>(who, mx, mw, whole, a, tiles, st)
                               : launch_experts<kRows, false>(who, mx, mw, whole, a, tiles, st);
     const int wide = op == kForward ? a.F * halves : a.K, deep = op == kForward ? a.K : a.F; // of W[e]
     const uint64_t ex[2] = {(uint64_t)a.K, (uint64_t)a.rows}, px[1] = {(uint64_t)a.ldx};
-    const uint32_t bx[2] = {64, 32}, ball[2] = {64, (uint32_t)a.columns};
+    const uint32_t bx[2] = {64, a.columns >= 128 ? 64u : 32u}, ball[2] = {64, (uint32_t)(pair ? a.columns / 2 : a.columns)};
     bool ok = make_map(&mx, a.x, 2, ex, px, bx) && make_map(&whole, a.x, 2, ex, px, ball);
     // One copy for a gated product's features needs whole sixteens: 8 copies of 16 lines took 957 us where one takes ... us
     a.by16 = op == kForward && halves == 2 && a.F % 16 == 0;
@@ -918,6 +954,9 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, cudaStream_
         ok = ok && make_map(&mw, a.W, 3, ew, pw, bw);
     }
     if (!ok) return fail(AP_ENOTSUP, "%s: no tensor map of these sizes", who);
+    if (pair)
+        return op == kForward ? launch_experts<kForward, true, true>(who, mx, mw, whole, a, tiles, st)
+                              : launch_experts<kRows, true, true>(who, mx, mw, whole, a, tiles, st);
     return op == kForward ? launch_experts<kForward, true>(who, mx, mw, whole, a, tiles, st)
                           : launch_experts<kRows, true>(who, mx, mw, whole, a, tiles, st);
 }

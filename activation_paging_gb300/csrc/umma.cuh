@@ -46,27 +46,53 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return false;
 }
 
+// The same barrier in another block of the cluster: its address, and an arrival there.
+__device__ __forceinline__ void bar_arrive_at(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 // ---- copies by tensor map ---------------------------------------------------------
-__device__ __forceinline__ void tma_2d(uint32_t to, const CUtensorMap *map, int x, int y, uint32_t bar)
+// PAIR: the barrier may be the other block's of a pair (a cluster address).
+template <bool PAIR> __device__ __forceinline__ void tma_2d(uint32_t to, const CUtensorMap *map, int x, int y, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                     to),
-                 "l"(map), "r"(x), "r"(y), "r"(bar)
-                 : "memory");
+    if constexpr (PAIR)
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                     "[%0], [%1, {%2, %3}], [%4];" ::"r"(to),
+                     "l"(map), "r"(x), "r"(y), "r"(bar)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                         to),
+                     "l"(map), "r"(x), "r"(y), "r"(bar)
+                     : "memory");
 }
-__device__ __forceinline__ void tma_3d(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+template <bool PAIR> __device__ __forceinline__ void tma_3d(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                     "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
+                     "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
+                     "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                     : "memory");
 }
+template <bool PAIR>
 __device__ __forceinline__ void tma_5d(uint32_t to, const CUtensorMap *map, int x, int y, int z, int u, int v, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
-                 "[%7];" ::"r"(to),
-                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
-                 : "memory");
+    if constexpr (PAIR)
+        asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                     "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(to),
+                     "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(to),
+                     "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
+                     : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map)
 {
@@ -76,15 +102,23 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map)
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---- tensor memory ------------------------------------------------------------------
-// (one whole warp each)
-__device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t columns)
+// (one whole warp each; PAIR: of both blocks of a pair, which do it together)
+template <bool PAIR> __device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t columns)
 {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
 }
-__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns)
+template <bool PAIR> __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns)
 {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -107,17 +141,29 @@ __device__ __forceinline__ uint32_t shape_of(int m, int n, bool a_mn, bool b_mn)
     return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 | (uint32_t)(n >> 3) << 17 |
            (uint32_t)(m >> 4) << 24;
 }
-// acc (+)= A B^T over 16 places of the contraction (one thread).
-__device__ __forceinline__ void mma(uint32_t acc, uint64_t a, uint64_t b, uint32_t shape, bool add)
+// acc (+)= A B^T over 16 places of the contraction (one thread).  PAIR: the first
+// block of a pair multiplies for both: each has half of A's rows and the
+// accumulator's lanes for them, and half of B's.
+template <bool PAIR> __device__ __forceinline__ void mma(uint32_t acc, uint64_t a, uint64_t b, uint32_t shape, bool add)
 {
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(acc), "l"(a),
-                 "l"(b), "r"(shape), "r"((uint32_t)add)
-                 : "memory");
+    if constexpr (PAIR)
+        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(acc),
+                     "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+                     : "memory");
+    else
+        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(acc),
+                     "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+                     : "memory");
 }
-// The barrier gets one arrival when all products that this thread asked for are done.
-__device__ __forceinline__ void mma_commit(uint32_t bar)
+// The barrier (PAIR: of both blocks) gets one arrival when all products that this thread asked for are done.
+template <bool PAIR> __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if constexpr (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                     "h"((uint16_t)3)
+                     : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 // 32 columns of the warp's 32 lanes.
 __device__ __forceinline__ void acc_load(uint32_t at, float (&v)[32])

@@ -166,6 +166,14 @@ def test_one_product_of_a_gradient():
     check_rows(Rows([128]), 64, 128)
 
 
+def test_one_product_of_a_pair_of_blocks():
+    check_forward(Rows([256]), 64, 256, pre=False)
+
+
+def test_one_product_of_a_gradient_by_a_pair_of_blocks():
+    check_rows(Rows([256]), 64, 256)
+
+
 def test_one_gradient_of_weights():
     check_weights(Rows([64]), 128, 64, bias=False)
 
@@ -182,6 +190,19 @@ def test_gated_halves_of_any_width(N, residual):
     """Widths at which a writer's 16 features of either half end."""
     check_forward(Rows([40, 3]), 64, N, "swiglu", bias=True, residual=residual)
     check_rows(Rows([40, 3]), 64, N, "swiglu", residual=residual)
+
+
+MANY = [0, 1, 31, 32, 33, 255, 256, 257, 511, 513, 700, 16, 17, 0]
+
+
+@pytest.mark.parametrize("K,N", [(64, 136), (256, 384), (72, 200), (1000, 264), (520, 1000)])
+@pytest.mark.parametrize("act", [None, "silu", "swiglu"])
+def test_many_rows(K, N, act):
+    """Tiles of 256 rows, shared out evenly; pairs of blocks."""
+    r = Rows(MANY, gap=2)
+    check_forward(r, K, N, act, bias=True, residual=True)
+    check_rows(r, K, N, act, residual=True)
+    check_weights(r, N, K, False)
 
 
 @pytest.mark.parametrize("K,N", [(1, 1), (63, 65), (65, 127), (203, 517), (1003, 130)])
