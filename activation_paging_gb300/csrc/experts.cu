@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     extern __shared__ __align__(1024) uint8_t s_mem[];
     __shared__ Table s_tab;
     __shared__ __align__(16) uint8_t s_pass[OP == kWeights ? 16 : kWriters * kPass];
-    __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_done[2], s_free[2], s_drain;
+    __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_done[2], s_free[2], s_drain, s_ask, s_tail;
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
     const int wid = threadIdx.x / kWarp, lane = (int)lane_id();
@@ -708,6 +708,8 @@ __global__ void __launch_bounds__(kExThreads, 1)
             bar_init(smem_addr(&s_free[s]), (PAIR ? 2 : 1) * kWriters);
         }
         bar_init(smem_addr(&s_drain), 1);
+        bar_init(smem_addr(&s_ask), 1);
+        bar_init(smem_addr(&s_tail), 2 * kWarp);
         bar_init_done();
         s_dead = 0;
     }
@@ -724,7 +726,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     if (wid == 0 || (!MAPS && (wid == 2 || wid == 3))) {
         // ---- fetch: stage by stage, as they fall empty
         const int thread = wid == 0 ? lane : threadIdx.x - kWarp;
-        if (!MAPS || lane == 0) {
+        if (!MAPS || elect_one()) {
             if (MAPS) {
                 tma_prefetch_map(&mx);
                 tma_prefetch_map(&mw);
@@ -762,59 +764,64 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 }
             }
         }
-    } else if (wid == 1 && rank == 0) {
-        // ---- multiply
-        uint32_t s = 0, turn = 0, count = 0; // ring; tiles so far
-        bool ok = true;
-        for (; ok && w.find(a.E); w.next()) {
-            const Tile t = tile_of<OP, PAIR>(a, w, rank);
-            if (t.steps == 0) continue;
-            const uint32_t acc = count & 1;
-            if (count >= 2 && !__all_sync(0xffffffffu, bar_wait(smem_addr(&s_free[acc]), (count >> 1 & 1) ^ 1, dead))) break;
-            fence_after();
-            const uint32_t shape = shape_of(PAIR ? 2 * kLanes : kLanes, PAIR ? (t.n + 31) & ~31 : (t.n + 15) & ~15, OP != kForward,
-                                            OP == kWeights);
-            for (int step = 0; step < t.steps; ++step) {
-                if (!__all_sync(0xffffffffu, bar_wait(smem_addr(&s_full[s]), turn & 1, dead))) {
-                    ok = false;
-                    break;
-                }
+    } else if (wid == 1) {
+        // ---- multiply (a pair's first block for both)
+        if (rank == 0 && elect_one()) {
+            uint32_t s = 0, turn = 0, count = 0, tails = 0; // ring; tiles and tiles with a tail so far
+            bool ok = true;
+            for (; ok && w.find(a.E); w.next()) {
+                const Tile t = tile_of<OP, PAIR>(a, w, rank);
+                if (t.steps == 0) continue;
+                const uint32_t acc = count & 1;
+                if (count >= 2 && !bar_wait(smem_addr(&s_free[acc]), (count >> 1 & 1) ^ 1, dead)) break;
                 fence_after();
-                uint8_t *stage = stages + (size_t)s * stage_bytes;
-                if (OP == kWeights && MAPS && t.live - step * kDepth < kDepth) {
-                    // the lines behind the expert's last row are others' rows: zeros
-                    const int from = (t.live - step * kDepth) * 128, panels = 2 + ceil_div(t.n, 64);
-                    for (int p = 0; p < panels; ++p)
-                        for (int b = from + lane * 16; b < kPanel; b += kWarp * 16)
-                            *reinterpret_cast<uint4 *>(stage + p * kPanel + b) = make_uint4(0, 0, 0, 0);
-                    fence_async();
-                    __syncwarp();
-                }
-                if (lane == 0) {
-                    const uint32_t sa = smem_addr(stage), sb = sa + 2 * kPanel;
+                const uint32_t shape = shape_of(PAIR ? 2 * kLanes : kLanes, PAIR ? (t.n + 31) & ~31 : (t.n + 15) & ~15,
+                                                OP != kForward, OP == kWeights);
+                for (int step = 0; step < t.steps; ++step) {
+                    const bool tail = OP == kWeights && MAPS && step + 1 == t.steps && t.live % kDepth;
+                    ok = bar_wait(smem_addr(&s_full[s]), turn & 1, dead);
+                    if (ok && tail) { // (asks, and waits until it is done)
+                        bar_arrive(smem_addr(&s_ask));
+                        ok = bar_wait(smem_addr(&s_tail), tails++ & 1, dead);
+                    }
+                    if (!ok) break;
+                    fence_after();
+                    const uint32_t sa = smem_addr(stages) + s * stage_bytes, sb = sa + 2 * kPanel;
 #pragma unroll
                     for (int k = 0; k < kDepth / 16; ++k)
                         mma<PAIR>(tmem + acc * 256, operand(sa + k * (OP == kForward ? 32 : 2048), kPanel),
                                   operand(sb + k * (OP == kWeights ? 2048 : 32), kPanel), shape, step > 0 || k > 0);
                     mma_commit<PAIR>(smem_addr(&s_empty[s]));
+                    if (++s == (uint32_t)a.stages) {
+                        s = 0;
+                        ++turn;
+                    }
                 }
-                __syncwarp();
-                if (++s == (uint32_t)a.stages) {
-                    s = 0;
-                    ++turn;
-                }
+                if (ok) mma_commit<PAIR>(smem_addr(&s_done[acc]));
+                ++count;
             }
-            if (ok && lane == 0) mma_commit<PAIR>(smem_addr(&s_done[acc]));
-            __syncwarp();
-            ++count;
-        }
-        if (__any_sync(0xffffffffu, *dead)) { // products on their way end before tensor memory is freed
-            volatile int none = 0;
-            if (lane == 0) {
+            if (*dead) { // products on their way end before tensor memory is freed
+                volatile int none = 0;
                 mma_commit<PAIR>(smem_addr(&s_drain));
                 (void)bar_wait(smem_addr(&s_drain), 0, &none);
             }
-            __syncwarp();
+        }
+    } else if (OP == kWeights && MAPS && wid < 4) {
+        // ---- the lines behind an expert's last row are others' rows: zeros
+        uint32_t fetched = 0, tails = 0;
+        for (; w.find(a.E); w.next()) {
+            const Tile t = tile_of<OP, PAIR>(a, w, rank);
+            fetched += t.steps;
+            const int left = t.live % kDepth;
+            if (t.steps == 0 || left == 0) continue;
+            if (!__all_sync(0xffffffffu, bar_wait(smem_addr(&s_ask), tails++ & 1, dead))) break;
+            uint8_t *stage = stages + (size_t)((fetched - 1) % a.stages) * stage_bytes;
+            const int panels = 2 + ceil_div(t.n, 64);
+            for (int p = 0; p < panels; ++p)
+                for (int b = left * 128 + (threadIdx.x - 2 * kWarp) * 16; b < kPanel; b += 2 * kWarp * 16)
+                    *reinterpret_cast<uint4 *>(stage + p * kPanel + b) = make_uint4(0, 0, 0, 0);
+            fence_async();
+            bar_arrive(smem_addr(&s_tail));
         }
     } else if (wid >= 4) {
         // ---- write

@@ -46,6 +46,13 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return false;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+    return one;
+}
 // The same barrier in another block of the cluster: its address, and an arrival there.
 __device__ __forceinline__ void bar_arrive_at(uint32_t cluster_bar)
 {
