@@ -42,6 +42,7 @@ constexpr int kMaxSmem = 232448;
 constexpr int kMaxExperts = 1024;
 constexpr int kPassPitch = 80;     // bytes of 32 lanes' values on their way, with what keeps banks apart
 constexpr int kPass = 32 * kPassPitch; // of a writer
+constexpr int kSend = 32 * 128;    // a writer's 32 x 32 weights on their way, two of them
 
 enum Op { kForward, kRows, kWeights };
 
@@ -59,6 +60,7 @@ struct ExArgs {
     int E, F, K;           // features of the output (of each half of a gated product), contraction
     int tiles_f, columns, stages, act;
     bool out_f32, add;     // add: kWeights, to what is there
+    bool send;             // kWeights: FP32 results go by tensor map (`whole`)
     bool by16;             // a gated product's map takes 16 features of either half in turn
     bool vec_out, vec_pre, vec_res; // rows on 16-byte boundaries (kWeights: 32), of whole pieces
 };
@@ -575,7 +577,7 @@ template <typename T> __device__ __forceinline__ T *weights_at(const ExArgs &a, 
 }
 template <typename T> __device__ __forceinline__ void read_weights(const ExArgs &a, const Tile &t, int c, int f, Kept<T> &x)
 {
-    if (!a.add || !a.vec_out || f >= a.F || c + 32 > t.n) return;
+    if (!a.add || a.send || !a.vec_out || f >= a.F || c + 32 > t.n) return;
     const T *p = weights_at<T>(a, t, c, f);
 #pragma unroll
     for (int q = 0; q < (int)sizeof(T); ++q) x.w[q] = wide_load(p + q * (32 / sizeof(T)));
@@ -612,8 +614,9 @@ template <typename T> __device__ __forceinline__ void write_weights(const ExArgs
 // One writer: two for each quarter of the accumulator's lanes.
 template <Op OP, bool PAIR, typename T>
 __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, int writer, uint32_t tmem, uint64_t *s_done,
-                                            uint64_t *s_free, uint8_t *pass, volatile int *dead)
+                                            uint64_t *s_free, uint8_t *pass, const CUtensorMap *map, volatile int *dead)
 {
+    int sent = 0;
     const auto release = [&](uint32_t acc) { // the accumulator is read
         if (PAIR)
             bar_arrive_at(cluster_addr(smem_addr(&s_free[acc]), 0));
@@ -661,7 +664,20 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
                 __syncwarp();
                 if (lane == 0 && t.steps > 0) release(acc);
             }
-            if constexpr (OP == kWeights) {
+            if (OP == kWeights && a.send) {
+                // Lines of a row's 32 weights, in swizzled pieces of 16 bytes; memory itself adds them to what is there.
+                uint8_t *to = pass + (sent++ & 1) * kSend;
+                if (lane == 0) tma_store_read<1>();
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    *reinterpret_cast<float4 *>(to + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                fence_async();
+                __syncwarp();
+                if (lane == 0 && t.f0 + part * kWarp < a.F)
+                    tma_store_3d(map, t.c0 + c, t.f0 + part * kWarp, t.e, smem_addr(to), a.add);
+            } else if constexpr (OP == kWeights) {
                 const Kept<T> now = kept;
                 if (!last) read_weights<T>(a, t, c + 64, f, kept);
                 write_weights<T>(a, t, c, f, v, now);
@@ -679,6 +695,7 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
             if (lane == 0) release(acc);
         }
     }
+    if (OP == kWeights && a.send && lane == 0) tma_store_done();
     if (!ok && a.d_status && lane == 0) atomicOr(a.d_status, AP_FLAG_CORRUPT);
 }
 
@@ -690,6 +707,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     pdl_begin();
     extern __shared__ __align__(1024) uint8_t s_mem[];
     __shared__ Table s_tab;
+    // (FP32 weights: in front of the stages, which lie on the boundaries that their swizzle wants)
     __shared__ __align__(16) uint8_t s_pass[OP == kWeights ? 16 : kWriters * kPass];
     __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_done[2], s_free[2], s_drain, s_ask, s_tail;
     __shared__ uint32_t s_tmem;
@@ -697,7 +715,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     const int wid = threadIdx.x / kWarp, lane = (int)lane_id();
     const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
     const int stage_bytes = 2 * kPanel + a.columns * (PAIR ? 64 : 128);
-    uint8_t *stages = s_mem + ((1024 - (smem_addr(s_mem) & 1023)) & 1023);
+    uint8_t *stages = s_mem + ((1024 - (smem_addr(s_mem) & 1023)) & 1023) + (OP == kWeights && a.send ? kWriters * 2 * kSend : 0);
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             bar_init(smem_addr(&s_full[s]), MAPS ? 1 : kFetchers);
@@ -825,11 +843,11 @@ __global__ void __launch_bounds__(kExThreads, 1)
         }
     } else if (wid >= 4) {
         // ---- write
-        uint8_t *pass = s_pass + (OP == kWeights ? 0 : (wid - 4) * kPass);
+        uint8_t *pass = OP == kWeights ? stages - (kWriters - (wid - 4)) * 2 * kSend : s_pass + (wid - 4) * kPass;
         if (OP == kWeights && !a.out_f32)
-            write_tiles<OP, PAIR, bf16_t>(a, w, rank, wid - 4, tmem, s_done, s_free, pass, dead);
+            write_tiles<OP, PAIR, bf16_t>(a, w, rank, wid - 4, tmem, s_done, s_free, pass, &whole, dead);
         else
-            write_tiles<OP, PAIR, float>(a, w, rank, wid - 4, tmem, s_done, s_free, pass, dead);
+            write_tiles<OP, PAIR, float>(a, w, rank, wid - 4, tmem, s_done, s_free, pass, &whole, dead);
     }
     __syncwarp();
     fence_before();
@@ -892,9 +910,10 @@ ap_status launch_experts(const char *who, const CUtensorMap &mx, const CUtensorM
     static const cudaError_t set =
         cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - fixed);
     if (set != cudaSuccess) return cuda_fail(set, who);
-    const int stage = 2 * kPanel + a.columns * (PAIR ? 64 : 128), room = kMaxSmem - fixed - 1024;
+    const int stage = 2 * kPanel + a.columns * (PAIR ? 64 : 128), send = a.send ? kWriters * 2 * kSend : 0;
+    const int room = kMaxSmem - fixed - 1024 - send;
     a.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
-    const size_t smem = (size_t)a.stages * stage + 1024;
+    const size_t smem = (size_t)a.stages * stage + 1024 + send;
     if constexpr (PAIR) {
         const int pairs = cluster_count((const void *)kernel, kExThreads, smem, 2, st);
         if (pairs < 1) return fail(AP_ENOTSUP, "%s: the stream's SMs take no pair of blocks", who);
@@ -970,7 +989,8 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, cudaStream_
 
 } // namespace
 
-bool umma::make_map(CUtensorMap *map, const void *base, int dims, const uint64_t *extent, const uint64_t *pitch, const uint32_t *box)
+bool umma::make_map(CUtensorMap *map, const void *base, int dims, const uint64_t *extent, const uint64_t *pitch, const uint32_t *box,
+                    bool f32)
 {
     using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -988,8 +1008,8 @@ bool umma::make_map(CUtensorMap *map, const void *base, int dims, const uint64_t
     cuuint64_t strides[4], sizes[5];
     cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < dims; ++i) sizes[i] = extent[i];
-    for (int i = 0; i + 1 < dims; ++i) strides[i] = pitch[i] * 2;
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void *>(base), sizes, strides, box, ones,
+    for (int i = 0; i + 1 < dims; ++i) strides[i] = pitch[i] * (f32 ? 4 : 2);
+    return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void *>(base), sizes, strides, box, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1077,6 +1097,12 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
         const int64_t tiles = (int64_t)E * a.tiles_f * ((K + a.columns - 1) / a.columns);
         if (tiles >= INT32_MAX) return fail(AP_EINVAL, "%s: %lld tiles are more than one launch takes", who, (long long)tiles);
         CUtensorMap mx = {}, mw = {}, whole = {};
+        // (sums of FP32 weights to what is there: reading them here took 587 us where memory adds in ... us)
+        if (a.out_f32 && !odd_address(dW, 16) && K % 4 == 0) {
+            const uint64_t eo[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)E}, po[2] = {(uint64_t)K, (uint64_t)N * K};
+            const uint32_t box[3] = {32, 32, 1};
+            a.send = make_map(&whole, dW, 3, eo, po, box, true);
+        }
         ap_status s;
         if (rows > 0 && mappable(dy, ldy) && mappable(x, ldx)) {
             const uint64_t ey[2] = {(uint64_t)N, (uint64_t)rows}, py[1] = {(uint64_t)ldy};
