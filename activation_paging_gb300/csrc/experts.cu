@@ -60,9 +60,16 @@ struct ExArgs {
     int E, F, K;           // features of the output (of each half of a gated product), contraction
     int tiles_f, columns, stages, act;
     bool out_f32, add;     // add: kWeights, to what is there
-    bool send;             // kWeights: FP32 results go by tensor map (`whole`)
+    bool send;             // kWeights: FP32 results go by tensor map
+    bool chunk_x, chunk_w; // kWeights: rows of whole 64s, two of them in a copy
     bool by16;             // a gated product's map takes 16 features of either half in turn
     bool vec_out, vec_pre, vec_res; // rows on 16-byte boundaries (kWeights: 32), of whole pieces
+};
+
+// Where operands come from: x in small and in large copies, the weights (kWeights:
+// x is dy, w is x); where FP32 weights' gradients go.
+struct ExMaps {
+    CUtensorMap x, xx, w, ww, out;
 };
 
 // ---- activations -----------------------------------------------------------------
@@ -190,44 +197,54 @@ __device__ __forceinline__ void fill_panel(uint8_t *to, const bf16_t *src, int64
 // features alternate by 16 between the gate's and the up product's, so that a
 // writing lane finds both.
 template <Op OP, bool MAPS, bool PAIR>
-__device__ __forceinline__ void fetch(const ExArgs &a, const Tile &t, int step, uint8_t *stage, const CUtensorMap *mx,
-                                      const CUtensorMap *mw, const CUtensorMap *whole, uint32_t full, int rank, int thread)
+__device__ __forceinline__ void fetch(const ExArgs &a, const Tile &t, int step, uint8_t *stage, const ExMaps &m, uint32_t full, int rank,
+                                      int thread)
 {
     const int k0 = step * kDepth;
     const bool gated = OP == kForward && a.act == AP_ACT_SWIGLU;
     uint8_t *col = stage + 2 * kPanel;
-    const int n = OP == kWeights ? ceil_div(t.n, 64) : ceil_div(t.n, 32);
     if constexpr (MAPS) {
         const uint32_t sa = smem_addr(stage), sb = smem_addr(col);
-        // a pair's blocks bring half of the tile's rows each, and all tell the first one's barrier
-        const int half = (t.n + 31) / 32 * 16, rows = PAIR ? half : t.n, most = PAIR ? a.columns / 2 : a.columns;
-        const int small = a.columns >= 128 ? 64 : 32, boxes = ceil_div(rows, small);
-        const bool all = rows > most - small; // in one copy
-        const int bytes = 2 * kPanel + (OP == kWeights ? n * kPanel : all ? most * 128 : boxes * small * 128);
+        // a pair's blocks bring half of the tile's columns each, and all tell the first one's barrier
+        const int half = (t.n + 31) / 32 * 16, most = PAIR ? a.columns / 2 : a.columns, cols = PAIR ? half : t.n;
+        const int from = PAIR ? rank * half : 0; // of the tile's columns
+        const int small = a.columns >= 128 ? 64 : 32, boxes = ceil_div(cols, small);
+        const bool all = OP == kWeights || cols > most - small; // as many as there may be
+        const int bytes = 2 * kPanel + (all ? most : boxes * small) * 128;
         if (rank == 0) bar_expect(full, PAIR ? 2 * bytes : bytes);
         const uint32_t bar = PAIR ? cluster_addr(full, 0) : full;
-        if (gated && a.by16) {
-            tma_5d<PAIR>(sa, mw, k0, 0, 0, t.f0 >> 4, t.e, bar);
-        } else if (gated) {
-#pragma unroll
-            for (int b = 0; b < 8; ++b) tma_3d<PAIR>(sa + b * 2048, mw, k0, t.f0 + (b >> 1) * 16 + (b & 1) * a.F, t.e, bar);
-        } else if (OP == kForward) {
-            tma_3d<PAIR>(sa, mw, k0, t.f0, t.e, bar);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (OP == kRows) tma_3d<PAIR>(sa + h * kPanel, mw, t.f0 + h * 64, k0, t.e, bar);
-                if (OP == kWeights) tma_2d<PAIR>(sa + h * kPanel, mx, t.f0 + h * 64, t.row0 + k0, bar);
-            }
-        }
-        if (OP == kWeights) {
-            for (int i = 0; i < n; ++i) tma_2d<PAIR>(sb + i * kPanel, mw, t.c0 + i * 64, t.row0 + k0, bar);
-        } else {
-            const int row = t.row0 + (PAIR ? rank * half : 0);
-            if (all)
-                tma_2d<PAIR>(sb, whole, k0, row, bar);
+        if constexpr (OP == kForward) {
+            if (!gated)
+                tma_3d<PAIR>(sa, &m.w, k0, t.f0, t.e, bar);
+            else if (a.by16)
+                tma_5d<PAIR>(sa, &m.w, k0, 0, 0, t.f0 >> 4, t.e, bar);
             else
-                for (int i = 0; i < boxes; ++i) tma_2d<PAIR>(sb + i * small * 128, mx, k0, row + i * small, bar);
+                for (int b = 0; b < 8; ++b) tma_3d<PAIR>(sa + b * 2048, &m.w, k0, t.f0 + (b >> 1) * 16 + (b & 1) * a.F, t.e, bar);
+        } else if constexpr (OP == kRows) {
+            tma_3d<PAIR>(sa, &m.w, t.f0, k0, t.e, bar);
+            tma_3d<PAIR>(sa + kPanel, &m.w, t.f0 + 64, k0, t.e, bar);
+        }
+        if constexpr (OP == kWeights) {
+            const int row = t.row0 + k0, c = t.c0 + from;
+            if (a.chunk_x) {
+                tma_3d<PAIR>(sa, &m.xx, 0, row, t.f0 >> 6, bar);
+            } else {
+                tma_2d<PAIR>(sa, &m.x, t.f0, row, bar);
+                tma_2d<PAIR>(sa + kPanel, &m.x, t.f0 + 64, row, bar);
+            }
+            for (int i = 0; i < most; i += 128) {
+                const uint32_t to = sb + i * 128;
+                if (a.chunk_w && most >= 128 && c % 64 == 0) {
+                    tma_3d<PAIR>(to, &m.ww, 0, row, (c + i) >> 6, bar);
+                } else {
+                    tma_2d<PAIR>(to, &m.w, c + i, row, bar);
+                    if (most >= 128) tma_2d<PAIR>(to + kPanel, &m.w, c + i + 64, row, bar);
+                }
+            }
+        } else if (all) {
+            tma_2d<PAIR>(sb, &m.xx, k0, t.row0 + from, bar);
+        } else {
+            for (int i = 0; i < boxes; ++i) tma_2d<PAIR>(sb + i * small * 128, &m.x, k0, t.row0 + from + i * small, bar);
         }
     } else {
         if (gated) {
@@ -244,6 +261,7 @@ __device__ __forceinline__ void fetch(const ExArgs &a, const Tile &t, int step, 
                 if (OP == kWeights) fill_panel(to, a.x + (int64_t)(t.row0 + k0) * a.ldx + f, a.ldx, 64, t.live - k0, a.F - f, thread);
             }
         }
+        const int n = OP == kWeights ? ceil_div(t.n, 64) : ceil_div(t.n, 32);
         for (int i = 0; i < n; ++i) {
             if (OP == kWeights)
                 fill_panel(col + i * kPanel, a.W + (int64_t)(t.row0 + k0) * a.ldw + t.c0 + i * 64, a.ldw, 64, t.live - k0,
@@ -611,6 +629,11 @@ template <typename T> __device__ __forceinline__ void write_weights(const ExArgs
         if (j < count) put(out + j, a.add ? (float)out[j] + v[j] : v[j]);
 }
 
+__device__ __forceinline__ void add_vector(float *p, float4 v)
+{
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
 // One writer: two for each quarter of the accumulator's lanes.
 template <Op OP, bool PAIR, typename T>
 __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, int writer, uint32_t tmem, uint64_t *s_done,
@@ -665,18 +688,28 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
                 if (lane == 0 && t.steps > 0) release(acc);
             }
             if (OP == kWeights && a.send) {
-                // Lines of a row's 32 weights, in swizzled pieces of 16 bytes; memory itself adds them to what is there.
+                // Lines of a row's 32 weights, in swizzled pieces of 16 bytes.
                 uint8_t *to = pass + (sent++ & 1) * kSend;
-                if (lane == 0) tma_store_read<1>();
+                if (lane == 0 && !a.add) tma_store_read<1>();
                 __syncwarp();
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     *reinterpret_cast<float4 *>(to + lane * 128 + ((q ^ (lane & 7)) << 4)) =
                         make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                fence_async();
-                __syncwarp();
-                if (lane == 0 && t.f0 + part * kWarp < a.F)
-                    tma_store_3d(map, t.c0 + c, t.f0 + part * kWarp, t.e, smem_addr(to), a.add);
+                if (a.add) { // memory itself adds them to what is there, a line of 128 bytes by eight lanes
+                    __syncwarp();
+                    const int k = c + (lane & 7) * 4;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int r = q * 4 + (lane >> 3), row = t.f0 + part * kWarp + r;
+                        const float4 x = *reinterpret_cast<const float4 *>(to + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                        if (row < a.F && k < t.n) add_vector(weights_at<float>(a, t, k, row), x);
+                    }
+                } else {
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0 && t.f0 + part * kWarp < a.F) tma_store_3d(map, t.c0 + c, t.f0 + part * kWarp, t.e, smem_addr(to));
+                }
             } else if constexpr (OP == kWeights) {
                 const Kept<T> now = kept;
                 if (!last) read_weights<T>(a, t, c + 64, f, kept);
@@ -701,15 +734,15 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
 
 template <Op OP, bool MAPS, bool PAIR>
 __global__ void __launch_bounds__(kExThreads, 1)
-    k_experts(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap whole,
-              const ExArgs a)
+    k_experts(const __grid_constant__ ExMaps m, const ExArgs a)
 {
     pdl_begin();
+    constexpr bool kPass2 = OP == kWeights && MAPS; // two warps pass stages on to the products
     extern __shared__ __align__(1024) uint8_t s_mem[];
     __shared__ Table s_tab;
     // (FP32 weights: in front of the stages, which lie on the boundaries that their swizzle wants)
     __shared__ __align__(16) uint8_t s_pass[OP == kWeights ? 16 : kWriters * kPass];
-    __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_done[2], s_free[2], s_drain, s_ask, s_tail;
+    __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_ready[kPass2 ? kMaxStages : 1], s_done[2], s_free[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
     const int wid = threadIdx.x / kWarp, lane = (int)lane_id();
@@ -720,14 +753,13 @@ __global__ void __launch_bounds__(kExThreads, 1)
         for (int s = 0; s < a.stages; ++s) {
             bar_init(smem_addr(&s_full[s]), MAPS ? 1 : kFetchers);
             bar_init(smem_addr(&s_empty[s]), 1);
+            if (kPass2) bar_init(smem_addr(&s_ready[s]), 2);
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(smem_addr(&s_done[s]), 1);
             bar_init(smem_addr(&s_free[s]), (PAIR ? 2 : 1) * kWriters);
         }
         bar_init(smem_addr(&s_drain), 1);
-        bar_init(smem_addr(&s_ask), 1);
-        bar_init(smem_addr(&s_tail), 2 * kWarp);
         bar_init_done();
         s_dead = 0;
     }
@@ -746,9 +778,8 @@ __global__ void __launch_bounds__(kExThreads, 1)
         const int thread = wid == 0 ? lane : threadIdx.x - kWarp;
         if (!MAPS || elect_one()) {
             if (MAPS) {
-                tma_prefetch_map(&mx);
-                tma_prefetch_map(&mw);
-                if (OP != kWeights) tma_prefetch_map(&whole);
+                tma_prefetch_map(&m.xx);
+                tma_prefetch_map(OP == kWeights ? &m.ww : &m.w);
             }
             uint32_t count = 0, s = 0, turn = 0; // stages fetched; ring position and its turn
             bool ok = true;
@@ -759,8 +790,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
                         ok = false;
                         break;
                     }
-                    fetch<OP, MAPS, PAIR>(a, t, step, stages + (size_t)s * stage_bytes, &mx, &mw, &whole, smem_addr(&s_full[s]), rank,
-                                          thread);
+                    fetch<OP, MAPS, PAIR>(a, t, step, stages + (size_t)s * stage_bytes, m, smem_addr(&s_full[s]), rank, thread);
                     ++count;
                     if (++s == (uint32_t)a.stages) {
                         s = 0;
@@ -785,7 +815,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     } else if (wid == 1) {
         // ---- multiply (a pair's first block for both)
         if (rank == 0 && elect_one()) {
-            uint32_t s = 0, turn = 0, count = 0, tails = 0; // ring; tiles and tiles with a tail so far
+            uint32_t s = 0, turn = 0, count = 0; // ring; tiles so far
             bool ok = true;
             for (; ok && w.find(a.E); w.next()) {
                 const Tile t = tile_of<OP, PAIR>(a, w, rank);
@@ -796,13 +826,10 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 const uint32_t shape = shape_of(PAIR ? 2 * kLanes : kLanes, PAIR ? (t.n + 31) & ~31 : (t.n + 15) & ~15,
                                                 OP != kForward, OP == kWeights);
                 for (int step = 0; step < t.steps; ++step) {
-                    const bool tail = OP == kWeights && MAPS && step + 1 == t.steps && t.live % kDepth;
-                    ok = bar_wait(smem_addr(&s_full[s]), turn & 1, dead);
-                    if (ok && tail) { // (asks, and waits until it is done)
-                        bar_arrive(smem_addr(&s_ask));
-                        ok = bar_wait(smem_addr(&s_tail), tails++ & 1, dead);
+                    if (!bar_wait(smem_addr(kPass2 ? &s_ready[s] : &s_full[s]), turn & 1, dead)) {
+                        ok = false;
+                        break;
                     }
-                    if (!ok) break;
                     fence_after();
                     const uint32_t sa = smem_addr(stages) + s * stage_bytes, sb = sa + 2 * kPanel;
 #pragma unroll
@@ -824,30 +851,39 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 (void)bar_wait(smem_addr(&s_drain), 0, &none);
             }
         }
-    } else if (OP == kWeights && MAPS && wid < 4) {
-        // ---- the lines behind an expert's last row are others' rows: zeros
-        uint32_t fetched = 0, tails = 0;
-        for (; w.find(a.E); w.next()) {
+    } else if (kPass2 && wid < 4) {
+        // ---- pass stages on, with zeros for the lines behind an expert's last row, which are others' rows
+        uint32_t s = 0, turn = 0;
+        bool ok = true;
+        for (; ok && w.find(a.E); w.next()) {
             const Tile t = tile_of<OP, PAIR>(a, w, rank);
-            fetched += t.steps;
-            const int left = t.live % kDepth;
-            if (t.steps == 0 || left == 0) continue;
-            if (!__all_sync(0xffffffffu, bar_wait(smem_addr(&s_ask), tails++ & 1, dead))) break;
-            uint8_t *stage = stages + (size_t)((fetched - 1) % a.stages) * stage_bytes;
-            const int panels = 2 + ceil_div(t.n, 64);
-            for (int p = 0; p < panels; ++p)
-                for (int b = left * 128 + (threadIdx.x - 2 * kWarp) * 16; b < kPanel; b += 2 * kWarp * 16)
-                    *reinterpret_cast<uint4 *>(stage + p * kPanel + b) = make_uint4(0, 0, 0, 0);
-            fence_async();
-            bar_arrive(smem_addr(&s_tail));
+            for (int step = 0; step < t.steps; ++step) {
+                ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&s_full[s]), turn & 1, dead));
+                if (!ok) break;
+                const int left = t.live - step * kDepth;
+                if (left < kDepth) {
+                    uint8_t *stage = stages + (size_t)s * stage_bytes;
+                    const int panels = 2 + a.columns / 64;
+                    for (int p = wid - 2; p < panels; p += 2)
+                        for (int b = left * 128 + lane * 16; b < kPanel; b += kWarp * 16)
+                            *reinterpret_cast<uint4 *>(stage + p * kPanel + b) = make_uint4(0, 0, 0, 0);
+                    fence_async();
+                    __syncwarp();
+                }
+                if (lane == 0) bar_arrive(smem_addr(&s_ready[s]));
+                if (++s == (uint32_t)a.stages) {
+                    s = 0;
+                    ++turn;
+                }
+            }
         }
     } else if (wid >= 4) {
         // ---- write
         uint8_t *pass = OP == kWeights ? stages - (kWriters - (wid - 4)) * 2 * kSend : s_pass + (wid - 4) * kPass;
         if (OP == kWeights && !a.out_f32)
-            write_tiles<OP, PAIR, bf16_t>(a, w, rank, wid - 4, tmem, s_done, s_free, pass, &whole, dead);
+            write_tiles<OP, PAIR, bf16_t>(a, w, rank, wid - 4, tmem, s_done, s_free, pass, &m.out, dead);
         else
-            write_tiles<OP, PAIR, float>(a, w, rank, wid - 4, tmem, s_done, s_free, pass, &whole, dead);
+            write_tiles<OP, PAIR, float>(a, w, rank, wid - 4, tmem, s_done, s_free, pass, &m.out, dead);
     }
     __syncwarp();
     fence_before();
@@ -900,8 +936,7 @@ bool mappable(const void *p, int64_t ld, int64_t more = 0)
 }
 
 template <Op OP, bool MAPS, bool PAIR = false>
-ap_status launch_experts(const char *who, const CUtensorMap &mx, const CUtensorMap &mw, const CUtensorMap &whole, ExArgs a, int64_t tiles,
-                         cudaStream_t st)
+ap_status launch_experts(const char *who, const ExMaps &m, ExArgs a, int64_t tiles, cudaStream_t st)
 {
     const auto kernel = k_experts<OP, MAPS, PAIR>;
     cudaFuncAttributes attr;
@@ -917,10 +952,10 @@ ap_status launch_experts(const char *who, const CUtensorMap &mx, const CUtensorM
     if constexpr (PAIR) {
         const int pairs = cluster_count((const void *)kernel, kExThreads, smem, 2, st);
         if (pairs < 1) return fail(AP_ENOTSUP, "%s: the stream's SMs take no pair of blocks", who);
-        launch_cluster(kernel, 2 * (int)(tiles < pairs ? tiles : pairs), kExThreads, smem, 2, st, mx, mw, whole, a);
+        launch_cluster(kernel, 2 * (int)(tiles < pairs ? tiles : pairs), kExThreads, smem, 2, st, m, a);
     } else {
         const int sms = sm_count();
-        launch(kernel, (int)(tiles < sms ? tiles : sms), kExThreads, smem, st, mx, mw, whole, a);
+        launch(kernel, (int)(tiles < sms ? tiles : sms), kExThreads, smem, st, m, a);
     }
     AP_CHECK_LAUNCH(who);
     return AP_OK;
@@ -959,32 +994,32 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, cudaStream_
     a.tiles_f = (a.F + per - 1) / per;
     const int64_t tiles = (a.rows / a.columns + a.E) * (int64_t)a.tiles_f;
     if (tiles >= INT32_MAX) return fail(AP_EINVAL, "%s: %lld tiles are more than one launch takes", who, (long long)tiles);
-    CUtensorMap mx = {}, mw = {}, whole = {};
+    ExMaps m = {};
     if (!maps)
-        return op == kForward ? launch_experts<kForward, false>(who, mx, mw, whole, a, tiles, st)
-                              : launch_experts<kRows, false>(who, mx, mw, whole, a, tiles, st);
+        return op == kForward ? launch_experts<kForward, false>(who, m, a, tiles, st)
+                              : launch_experts<kRows, false>(who, m, a, tiles, st);
     const int wide = op == kForward ? a.F * halves : a.K, deep = op == kForward ? a.K : a.F; // of W[e]
     const uint64_t ex[2] = {(uint64_t)a.K, (uint64_t)a.rows}, px[1] = {(uint64_t)a.ldx};
     const uint32_t bx[2] = {64, a.columns >= 128 ? 64u : 32u}, ball[2] = {64, (uint32_t)(pair ? a.columns / 2 : a.columns)};
-    bool ok = make_map(&mx, a.x, 2, ex, px, bx) && make_map(&whole, a.x, 2, ex, px, ball);
+    bool ok = make_map(&m.x, a.x, 2, ex, px, bx) && make_map(&m.xx, a.x, 2, ex, px, ball);
     // One copy for a gated product's features needs whole sixteens: 8 copies of 16 lines took 957 us where one takes ... us
     a.by16 = op == kForward && halves == 2 && a.F % 16 == 0;
     if (a.by16) {
         const uint64_t ew[5] = {(uint64_t)deep, 16, 2, (uint64_t)a.F / 16, (uint64_t)a.E};
         const uint64_t pw[4] = {(uint64_t)a.ldw, (uint64_t)(a.F * a.ldw), (uint64_t)(16 * a.ldw), (uint64_t)a.lde};
         const uint32_t bw[5] = {64, 16, 2, 4, 1};
-        ok = ok && make_map(&mw, a.W, 5, ew, pw, bw);
+        ok = ok && make_map(&m.w, a.W, 5, ew, pw, bw);
     } else {
         const uint64_t ew[3] = {(uint64_t)deep, (uint64_t)wide, (uint64_t)a.E}, pw[2] = {(uint64_t)a.ldw, (uint64_t)a.lde};
         const uint32_t bw[3] = {64, op == kRows ? 64u : halves == 2 ? 16u : 128u, 1};
-        ok = ok && make_map(&mw, a.W, 3, ew, pw, bw);
+        ok = ok && make_map(&m.w, a.W, 3, ew, pw, bw);
     }
     if (!ok) return fail(AP_ENOTSUP, "%s: no tensor map of these sizes", who);
     if (pair)
-        return op == kForward ? launch_experts<kForward, true, true>(who, mx, mw, whole, a, tiles, st)
-                              : launch_experts<kRows, true, true>(who, mx, mw, whole, a, tiles, st);
-    return op == kForward ? launch_experts<kForward, true>(who, mx, mw, whole, a, tiles, st)
-                          : launch_experts<kRows, true>(who, mx, mw, whole, a, tiles, st);
+        return op == kForward ? launch_experts<kForward, true, true>(who, m, a, tiles, st)
+                              : launch_experts<kRows, true, true>(who, m, a, tiles, st);
+    return op == kForward ? launch_experts<kForward, true>(who, m, a, tiles, st)
+                          : launch_experts<kRows, true>(who, m, a, tiles, st);
 }
 
 } // namespace
@@ -1091,28 +1126,35 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
         a.x = (const bf16_t *)dy, a.W = (const bf16_t *)x, a.ldx = ldy, a.ldw = ldx;
         a.seg = d_seg_off, a.live = d_live, a.out = dW, a.d_status = d_status, a.rows = rows, a.E = E, a.F = N, a.K = K;
         a.out_f32 = dw_dtype == AP_DTYPE_F32, a.add = accumulate != 0;
+        const bool maps = rows > 0 && mappable(dy, ldy) && mappable(x, ldx);
         a.columns = K > 128 ? 256 : K > 64 ? 128 : 64;
         a.tiles_f = (N + kLanes - 1) / kLanes;
+        auto tiles_of = [&] { return (int64_t)E * a.tiles_f * ((K + a.columns - 1) / a.columns); };
+        if (tiles_of() < 2 * sm_count()) a.columns = K > 64 ? 128 : 64; // few tiles: smaller ones, for more SMs
         a.vec_out = !odd_address(dW, 32) && K % (a.out_f32 ? 8 : 16) == 0;
-        const int64_t tiles = (int64_t)E * a.tiles_f * ((K + a.columns - 1) / a.columns);
+        const int64_t tiles = tiles_of();
         if (tiles >= INT32_MAX) return fail(AP_EINVAL, "%s: %lld tiles are more than one launch takes", who, (long long)tiles);
-        CUtensorMap mx = {}, mw = {}, whole = {};
-        // (sums of FP32 weights to what is there: reading them here took 587 us where memory adds in ... us)
+        ExMaps m = {};
+        // (FP32 sums to what is there: 587 us where the writers read it, 471 where memory adds, at 65536 rows, 128 x 2048 x 1024)
         if (a.out_f32 && !odd_address(dW, 16) && K % 4 == 0) {
             const uint64_t eo[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)E}, po[2] = {(uint64_t)K, (uint64_t)N * K};
             const uint32_t box[3] = {32, 32, 1};
-            a.send = make_map(&whole, dW, 3, eo, po, box, true);
+            a.send = make_map(&m.out, dW, 3, eo, po, box, true);
         }
         ap_status s;
-        if (rows > 0 && mappable(dy, ldy) && mappable(x, ldx)) {
-            const uint64_t ey[2] = {(uint64_t)N, (uint64_t)rows}, py[1] = {(uint64_t)ldy};
-            const uint64_t ex[2] = {(uint64_t)K, (uint64_t)rows}, px[1] = {(uint64_t)ldx};
-            const uint32_t box[2] = {64, 64};
-            if (!make_map(&mx, dy, 2, ey, py, box) || !make_map(&mw, x, 2, ex, px, box))
+        if (maps) {
+            // two chunks of 64 columns in a copy where rows are whole chunks: a row's end is no border to such a map
+            a.chunk_x = N % 64 == 0, a.chunk_w = K % 64 == 0;
+            const uint64_t ey[3] = {a.chunk_x ? 64 : (uint64_t)N, (uint64_t)rows, (uint64_t)N / 64}, py[2] = {(uint64_t)ldy, 64};
+            const uint64_t ex[3] = {a.chunk_w ? 64 : (uint64_t)K, (uint64_t)rows, (uint64_t)K / 64}, px[2] = {(uint64_t)ldx, 64};
+            const uint32_t box[3] = {64, 64, 2};
+            const uint64_t e1[2] = {(uint64_t)N, (uint64_t)rows}, e2[2] = {(uint64_t)K, (uint64_t)rows};
+            if (!make_map(&m.x, dy, 2, e1, py, box) || !make_map(&m.w, x, 2, e2, px, box) ||
+                (a.chunk_x && !make_map(&m.xx, dy, 3, ey, py, box)) || (a.chunk_w && !make_map(&m.ww, x, 3, ex, px, box)))
                 return fail(AP_ENOTSUP, "%s: no tensor map of these sizes", who);
-            s = launch_experts<kWeights, true>(who, mx, mw, whole, a, tiles, st);
+            s = launch_experts<kWeights, true>(who, m, a, tiles, st);
         } else {
-            s = launch_experts<kWeights, false>(who, mx, mw, whole, a, tiles, st);
+            s = launch_experts<kWeights, false>(who, m, a, tiles, st);
         }
         if (s != AP_OK) return s;
     }

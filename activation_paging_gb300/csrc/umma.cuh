@@ -101,18 +101,12 @@ __device__ __forceinline__ void tma_5d(uint32_t to, const CUtensorMap *map, int 
                      "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
                      : "memory");
 }
-// From shared memory, stored or added (FP32) to what is there; a thread's copies
-// come in groups.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int y, int z, uint32_t from, bool add)
+// From shared memory; a thread's copies come in groups.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int y, int z, uint32_t from)
 {
-    if (add)
-        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
-                     "r"(y), "r"(z), "r"(from)
-                     : "memory");
-    else
-        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y),
-                     "r"(z), "r"(from)
-                     : "memory");
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y), "r"(z),
+                 "r"(from)
+                 : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 template <int N> __device__ __forceinline__ void tma_store_read() // all groups but the last N have read shared memory

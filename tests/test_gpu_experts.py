@@ -195,7 +195,7 @@ def test_gated_halves_of_any_width(N, residual):
 MANY = [0, 1, 31, 32, 33, 255, 256, 257, 511, 513, 700, 16, 17, 0]
 
 
-@pytest.mark.parametrize("K,N", [(64, 136), (256, 384), (72, 200), (1000, 264), (520, 1000)])
+@pytest.mark.parametrize("K,N", [(64, 136), (256, 384), (72, 200), (1000, 264), (520, 1000), (512, 640)])
 @pytest.mark.parametrize("act", [None, "silu", "swiglu"])
 def test_many_rows(K, N, act):
     """Tiles of 256 rows, shared out evenly; pairs of blocks."""
