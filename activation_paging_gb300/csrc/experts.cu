@@ -19,7 +19,8 @@
 // shared memory as 8 x 8 matrices, transposed, so that memory sees rows' pieces
 // of 32 and 64 bytes.
 // Operands come by tensor map where base and pitch are multiples of 16 bytes;
-// else (odd row lengths) three warps bring them element by element.
+// else (odd row lengths) seven warps cut them out of the 16-byte granules that
+// hold them.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -31,8 +32,10 @@ namespace {
 using bf16_t = __nv_bfloat16;
 using namespace umma;
 
-constexpr int kExThreads = 384;    // warps: 0 fetches, 1 multiplies, 2 and 3 fetch odd rows, 4 to 11 write
-constexpr int kFetchers = 96;      // threads of warps 0, 2 and 3
+// Warps: 0 fetches, 1 multiplies, 2 and 3 pass stages on, 4 to 11 write; without
+// tensor maps 0, 2, 3 and 12 to 15 fetch.
+constexpr int ex_threads(bool maps) { return maps ? 384 : 512; }
+constexpr int kFetchers = 7 * 32;
 constexpr int kWriters = 8;        // warps: two for each quarter of the lanes, with every other 32 columns
 constexpr int kLanes = 128;        // features of a tile
 constexpr int kDepth = 64;         // contraction of a stage: one line of 128 bytes
@@ -42,7 +45,7 @@ constexpr int kMaxSmem = 232448;
 constexpr int kMaxExperts = 1024;
 constexpr int kPassPitch = 80;     // bytes of 32 lanes' values on their way, with what keeps banks apart
 constexpr int kPass = 32 * kPassPitch; // of a writer
-constexpr int kSend = 32 * 128;    // a writer's 32 x 32 weights on their way, two of them
+constexpr int kHalf = 16 * 128;    // (of weights: 16 rows of 32 FP32)
 
 enum Op { kForward, kRows, kWeights };
 
@@ -59,17 +62,17 @@ struct ExArgs {
     int64_t rows;
     int E, F, K;           // features of the output (of each half of a gated product), contraction
     int tiles_f, columns, stages, act;
+    const char *x_end, *W_end; // where their buffers end
     bool out_f32, add;     // add: kWeights, to what is there
-    bool send;             // kWeights: FP32 results go by tensor map
     bool chunk_x, chunk_w; // kWeights: rows of whole 64s, two of them in a copy
     bool by16;             // a gated product's map takes 16 features of either half in turn
-    bool vec_out, vec_pre, vec_res; // rows on 16-byte boundaries (kWeights: 32), of whole pieces
+    bool vec_out, vec_pre, vec_res; // rows on 16-byte boundaries, of whole pieces
 };
 
 // Where operands come from: x in small and in large copies, the weights (kWeights:
-// x is dy, w is x); where FP32 weights' gradients go.
+// x is dy, w is x).
 struct ExMaps {
-    CUtensorMap x, xx, w, ww, out;
+    CUtensorMap x, xx, w, ww;
 };
 
 // ---- activations -----------------------------------------------------------------
@@ -175,21 +178,104 @@ template <Op OP, bool PAIR> __device__ __forceinline__ Tile tile_of(const ExArgs
     return t;
 }
 
-// One panel of lines by plain loads: line r holds 64 values of row r of src from
-// column c0 on, in swizzled pieces of 16 bytes; zeros outside rows and columns.
-__device__ __forceinline__ void fill_panel(uint8_t *to, const bf16_t *src, int64_t ld, int lines, int64_t rows, int64_t columns,
-                                           int thread)
+// 16 bytes from an address between granules: of the two granules a and b those
+// from byte `off` (even) on.
+__device__ __forceinline__ uint4 cut(uint4 a, uint4 b, uint32_t off)
 {
-    for (int i = thread; i < lines * 8; i += kFetchers) {
-        const int r = i >> 3, c = i & 7;
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (r < rows) {
-            const unsigned short *p = reinterpret_cast<const unsigned short *>(src) + r * ld + c * 8;
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c * 8 + j < columns) w[j / 2] |= (uint32_t)p[j] << 16 * (j & 1);
+    for (int i = 0; i < 6; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+    if (off & 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// `lines` lines of 64 values from p on, `ld` values apart, of which the first
+// `rows` and in each the first `n` values are there: cut into swizzled pieces of
+// 16 bytes, zeros elsewhere.  Granules that lie inside the operand's buffer
+// (begin to end) are read whole, the ones that its ends cut element by element.
+__device__ __forceinline__ void fetch_lines(uint8_t *to, const bf16_t *p, int64_t ld, int lines, int rows, int n, const char *begin,
+                                            const char *end, int thread)
+{
+    constexpr int kEach = 5, kStep = kFetchers / 8; // lines of a thread on their way, and how far apart
+    const int c = thread & 7;
+    n = min(max(n - c * 8, 0), 8);
+    const char *from = reinterpret_cast<const char *>(p + c * 8 + (int64_t)(thread >> 3) * ld);
+    const int64_t step = ld * 2 * kStep;
+    for (int l0 = thread >> 3; l0 < lines; l0 += kEach * kStep) {
+        uint4 lo[kEach], hi[kEach];
+        bool cut_off[kEach];
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+            const char *q = from + u * step;
+            const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(q) & 15;
+            const char *at = q - off;
+            const bool on = n > 0 && l0 + u * kStep < rows, second = off + 2 * n > 16;
+            cut_off[u] = at < begin || at + (second ? 32 : 16) > end;
+            lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
+            if (on && !cut_off[u]) {
+                lo[u] = *reinterpret_cast<const uint4 *>(at);
+                if (second) hi[u] = *reinterpret_cast<const uint4 *>(at + 16);
+            }
         }
-        *reinterpret_cast<uint4 *>(to + r * 128 + ((c ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int u = 0; u < kEach; ++u, from += step) {
+            const int l = l0 + u * kStep;
+            if (l >= lines) continue;
+            uint4 w = cut(lo[u], hi[u], (uint32_t)reinterpret_cast<uintptr_t>(from) & 15);
+            if (n > 0 && l < rows && cut_off[u]) {
+                uint32_t v[4] = {0, 0, 0, 0};
+                const unsigned short *e = reinterpret_cast<const unsigned short *>(from);
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t x = (uint32_t)e[j] << 16 * (j & 1);
+                    v[0] |= j < 2 ? x : 0, v[1] |= j >> 1 == 1 ? x : 0, v[2] |= j >> 1 == 2 ? x : 0, v[3] |= j >> 1 == 3 ? x : 0;
+                }
+                w = make_uint4(v[0], v[1], v[2], v[3]);
+            } else if (n < 8) { // a row's end
+                w.x &= n >= 2 ? ~0u : n == 1 ? 0xffffu : 0u;
+                w.y &= n >= 4 ? ~0u : n == 3 ? 0xffffu : 0u;
+                w.z &= n >= 6 ? ~0u : n == 5 ? 0xffffu : 0u;
+                w.w &= n == 7 ? 0xffffu : 0u;
+            }
+            *reinterpret_cast<uint4 *>(to + l * 128 + ((c ^ (l & 7)) << 4)) = w;
+        }
+    }
+}
+
+// A stage by plain loads.
+template <Op OP>
+__device__ __forceinline__ void fetch_plain(const ExArgs &a, const Tile &t, int k0, uint8_t *stage, int thread)
+{
+    const char *x0 = reinterpret_cast<const char *>(a.x), *w0 = reinterpret_cast<const char *>(a.W);
+    uint8_t *col = stage + 2 * kPanel;
+    if constexpr (OP == kForward) {
+        const bf16_t *W = a.W + t.e * a.lde + k0;
+        if (a.act == AP_ACT_SWIGLU)
+            for (int b = 0; b < 8; ++b) {
+                const int f = t.f0 + (b >> 1) * 16;
+                fetch_lines(stage + b * 2048, W + (f + (b & 1) * a.F) * a.ldw, a.ldw, 16, a.F - f, a.K - k0, w0, a.W_end, thread);
+            }
+        else
+            fetch_lines(stage, W + t.f0 * a.ldw, a.ldw, kLanes, a.F - t.f0, a.K - k0, w0, a.W_end, thread);
+    } else {
+        for (int h = 0; h < 2; ++h) {
+            const int f = t.f0 + h * 64;
+            if (OP == kRows)
+                fetch_lines(stage + h * kPanel, a.W + t.e * a.lde + k0 * a.ldw + f, a.ldw, 64, a.K - k0, a.F - f, w0, a.W_end, thread);
+            else
+                fetch_lines(stage + h * kPanel, a.x + (int64_t)(t.row0 + k0) * a.ldx + f, a.ldx, 64, t.live - k0, a.F - f, x0, a.x_end,
+                            thread);
+        }
+    }
+    if constexpr (OP == kWeights) {
+        for (int c = 0; c < t.n; c += 64)
+            fetch_lines(col + c * 128, a.W + (int64_t)(t.row0 + k0) * a.ldw + t.c0 + c, a.ldw, 64, t.live - k0, a.K - t.c0 - c, w0, a.W_end,
+                        thread);
+    } else {
+        fetch_lines(col, a.x + (int64_t)t.row0 * a.ldx + k0, a.ldx, (t.n + 31) & ~31, t.n, a.K - k0, x0, a.x_end, thread);
     }
 }
 
@@ -247,37 +333,11 @@ __device__ __forceinline__ void fetch(const ExArgs &a, const Tile &t, int step, 
             for (int i = 0; i < boxes; ++i) tma_2d<PAIR>(sb + i * small * 128, &m.x, k0, t.row0 + from + i * small, bar);
         }
     } else {
-        if (gated) {
-            for (int b = 0; b < 8; ++b) {
-                const int f = t.f0 + (b >> 1) * 16;
-                fill_panel(stage + b * 2048, a.W + t.e * a.lde + (f + (b & 1) * a.F) * a.ldw + k0, a.ldw, 16, a.F - f, a.K - k0, thread);
-            }
-        } else {
-            for (int h = 0; h < 2; ++h) {
-                const int f = t.f0 + h * 64;
-                uint8_t *to = stage + h * kPanel;
-                if (OP == kForward) fill_panel(to, a.W + t.e * a.lde + f * a.ldw + k0, a.ldw, 64, a.F - f, a.K - k0, thread);
-                if (OP == kRows) fill_panel(to, a.W + t.e * a.lde + k0 * a.ldw + f, a.ldw, 64, a.K - k0, a.F - f, thread);
-                if (OP == kWeights) fill_panel(to, a.x + (int64_t)(t.row0 + k0) * a.ldx + f, a.ldx, 64, t.live - k0, a.F - f, thread);
-            }
-        }
-        const int n = OP == kWeights ? ceil_div(t.n, 64) : ceil_div(t.n, 32);
-        for (int i = 0; i < n; ++i) {
-            if (OP == kWeights)
-                fill_panel(col + i * kPanel, a.W + (int64_t)(t.row0 + k0) * a.ldw + t.c0 + i * 64, a.ldw, 64, t.live - k0,
-                           a.K - t.c0 - i * 64, thread);
-            else
-                fill_panel(col + i * (kPanel / 2), a.x + (int64_t)(t.row0 + i * 32) * a.ldx + k0, a.ldx, 32, t.n - i * 32, a.K - k0,
-                           thread);
-        }
+        fetch_plain<OP>(a, t, k0, stage, thread);
         fence_async();
         bar_arrive(full);
     }
 }
-
-template <typename T> __device__ __forceinline__ void put(T *p, float v);
-template <> __device__ __forceinline__ void put<float>(float *p, float v) { *p = v; }
-template <> __device__ __forceinline__ void put<bf16_t>(bf16_t *p, float v) { *p = __float2bfloat16_rn(v); }
 
 __device__ __forceinline__ uint32_t pack(float lo, float hi)
 {
@@ -564,100 +624,125 @@ __device__ __forceinline__ void write_slopes(const ExArgs &a, const Tile &t, int
     result_store(a, v, pass, at, count, left);
 }
 
-// 32 bytes in one go.
-struct alignas(32) Wide {
-    uint32_t w[8];
-};
-__device__ __forceinline__ Wide wide_load(const void *p)
-{
-    Wide x;
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]), "=r"(x.w[6]), "=r"(x.w[7])
-                 : "l"(p)
-                 : "memory");
-    return x;
-}
-__device__ __forceinline__ void wide_store(void *p, const Wide &x)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x.w[0]), "r"(x.w[1]), "r"(x.w[2]), "r"(x.w[3]),
-                 "r"(x.w[4]), "r"(x.w[5]), "r"(x.w[6]), "r"(x.w[7])
-                 : "memory");
-}
-
-// Weights: 32 places of a row (lane), one after the other in memory.  What is
-// there already is read while the products run.
-template <typename T> struct Kept {
-    Wide w[32 * sizeof(T) / 32];
-};
-template <typename T> __device__ __forceinline__ T *weights_at(const ExArgs &a, const Tile &t, int c, int f)
-{
-    return static_cast<T *>(a.out) + ((int64_t)t.e * a.F + f) * a.K + t.c0 + c;
-}
-template <typename T> __device__ __forceinline__ void read_weights(const ExArgs &a, const Tile &t, int c, int f, Kept<T> &x)
-{
-    if (!a.add || a.send || !a.vec_out || f >= a.F || c + 32 > t.n) return;
-    const T *p = weights_at<T>(a, t, c, f);
-#pragma unroll
-    for (int q = 0; q < (int)sizeof(T); ++q) x.w[q] = wide_load(p + q * (32 / sizeof(T)));
-}
-template <typename T> __device__ __forceinline__ void write_weights(const ExArgs &a, const Tile &t, int c, int f, float (&v)[32], const Kept<T> &x)
-{
-    if (f >= a.F) return;
-    T *out = weights_at<T>(a, t, c, f);
-    if (a.vec_out && c + 32 <= t.n) {
-        constexpr int kPer = 32 / sizeof(T);
-#pragma unroll
-        for (int q = 0; q < (int)sizeof(T); ++q) {
-            Wide n;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if constexpr (sizeof(T) == 4) {
-                    const float y = v[q * kPer + j];
-                    n.w[j] = __float_as_uint(a.add ? __uint_as_float(x.w[q].w[j]) + y : y);
-                } else {
-                    const float lo = v[q * kPer + 2 * j], hi = v[q * kPer + 2 * j + 1];
-                    n.w[j] = a.add ? pack(low(x.w[q].w[j]) + lo, high(x.w[q].w[j]) + hi) : pack(lo, hi);
-                }
-            }
-            wide_store(out + q * kPer, n);
-        }
-        return;
-    }
-    const int count = min(32, t.n - c);
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (j < count) put(out + j, a.add ? (float)out[j] + v[j] : v[j]);
-}
-
+// Weights: rows are the lanes, 32 of their places the columns.  Sixteen rows at a
+// time pass through shared memory (lines of 128 bytes, swizzled in pieces of 16),
+// so that memory sees pieces of 128 bytes (BF16: 64) of a row.  FP32 sums to what
+// is there are left to memory: its vector reductions need no answer.
 __device__ __forceinline__ void add_vector(float *p, float4 v)
 {
     asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
+__device__ __forceinline__ void add_one(float *p, float v) { asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory"); }
+
+template <typename T> __device__ __forceinline__ T *weights_at(const ExArgs &a, const Tile &t, int c, int f)
+{
+    return static_cast<T *>(a.out) + ((int64_t)t.e * a.F + f) * a.K + t.c0 + c;
+}
+// BF16 weights that are there, read while the products run: 8 of row 8 q + lane / 4.
+struct Kept {
+    uint4 w[4];
+};
+__device__ __forceinline__ void read_weights(const ExArgs &a, const Tile &t, int c, int f, Kept &x)
+{
+    const int lane = (int)lane_id(), k = c + (lane & 3) * 8;
+    if (!a.add || a.out_f32 || !a.vec_out || k >= t.n) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int row = f + q * 8 + (lane >> 2);
+        if (row < a.F) x.w[q] = *reinterpret_cast<const uint4 *>(weights_at<bf16_t>(a, t, k, row));
+    }
+}
+__device__ __forceinline__ void write_weights(const ExArgs &a, const Tile &t, int c, int f, const float (&v)[32], const Kept &kept,
+                                              uint8_t *pass)
+{
+    const int lane = (int)lane_id();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int f0 = f + h * 16;
+        __syncwarp();
+        if (lane >> 4 == h)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<float4 *>(pass + (lane & 15) * 128 + ((q ^ (lane & 7)) << 4)) =
+                    make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        __syncwarp();
+        const auto piece = [&](int r, int q) { return *reinterpret_cast<const float4 *>(pass + r * 128 + ((q ^ (r & 7)) << 4)); };
+        if (a.vec_out && a.out_f32) {
+            const int k = c + (lane & 7) * 4;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = q * 4 + (lane >> 3);
+                const float4 x = piece(r, lane & 7);
+                if (f0 + r < a.F && k < t.n) {
+                    float *p = weights_at<float>(a, t, k, f0 + r);
+                    if (a.add)
+                        add_vector(p, x);
+                    else
+                        *reinterpret_cast<float4 *>(p) = x;
+                }
+            }
+        } else if (a.vec_out) {
+            const int k = c + (lane & 3) * 8;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int r = q * 8 + (lane >> 2);
+                float4 x = piece(r, (lane & 3) * 2), y = piece(r, (lane & 3) * 2 + 1);
+                if (a.add) {
+                    const uint4 o = kept.w[h * 2 + q];
+                    x.x += low(o.x), x.y += high(o.x), x.z += low(o.y), x.w += high(o.y);
+                    y.x += low(o.z), y.y += high(o.z), y.z += low(o.w), y.w += high(o.w);
+                }
+                if (f0 + r < a.F && k < t.n)
+                    *reinterpret_cast<uint4 *>(weights_at<bf16_t>(a, t, k, f0 + r)) =
+                        make_uint4(pack(x.x, x.y), pack(x.z, x.w), pack(y.x, y.y), pack(y.z, y.w));
+            }
+        } else { // a row at a time, a place a lane
+            const int rows = min(16, a.F - f0);
+            if (c + lane < t.n)
+#pragma unroll 4
+                for (int r = 0; r < rows; ++r) {
+                    const float x = *reinterpret_cast<const float *>(pass + r * 128 + ((lane >> 2 ^ (r & 7)) << 4) + (lane & 3) * 4);
+                    if (a.out_f32) {
+                        float *p = weights_at<float>(a, t, c + lane, f0 + r);
+                        if (a.add)
+                            add_one(p, x);
+                        else
+                            *p = x;
+                    } else {
+                        bf16_t *p = weights_at<bf16_t>(a, t, c + lane, f0 + r);
+                        *p = __float2bfloat16_rn(a.add ? __bfloat162float(*p) + x : x);
+                    }
+                }
+        }
+    }
+}
 
 // One writer: two for each quarter of the accumulator's lanes.
-template <Op OP, bool PAIR, typename T>
+template <Op OP, bool PAIR>
 __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, int writer, uint32_t tmem, uint64_t *s_done,
-                                            uint64_t *s_free, uint8_t *pass, const CUtensorMap *map, volatile int *dead)
+                                            uint64_t *s_free, uint8_t *pass, volatile int *dead)
 {
-    int sent = 0;
-    const auto release = [&](uint32_t acc) { // the accumulator is read
-        if (PAIR)
-            bar_arrive_at(cluster_addr(smem_addr(&s_free[acc]), 0));
-        else
-            bar_arrive(smem_addr(&s_free[acc]));
-    };
     const int part = writer & 3, lane = (int)lane_id();
     uint32_t count = 0;
     bool ok = true;
+    const auto release = [&](uint32_t acc) { // the accumulator is read
+        __syncwarp();
+        if (lane == 0) {
+            if (PAIR)
+                bar_arrive_at(cluster_addr(smem_addr(&s_free[acc]), 0));
+            else
+                bar_arrive(smem_addr(&s_free[acc]));
+        }
+    };
     for (; w.find(a.E); w.next()) {
         const Tile t = tile_of<OP, PAIR>(a, w, rank);
         const uint32_t acc = count & 1, at = tmem + acc * 256 + ((uint32_t)part * kWarp << 16);
-        const int f = t.f0 + part * kWarp + lane; // (of weights)
+        const int f = t.f0 + part * kWarp; // (of weights)
         int c = (writer >> 2) * 32;
         Ahead x;
-        Kept<T> kept;
+        Kept kept;
         if constexpr (OP == kWeights)
-            read_weights<T>(a, t, c, f, kept);
+            read_weights(a, t, c, f, kept);
         else
             read_ahead<OP>(a, t, c, part, x);
         if (t.steps > 0) {
@@ -665,7 +750,7 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
             ++count;
         }
         fence_after();
-        const bool some = c < t.n;
+        if (c >= t.n && t.steps > 0) release(acc);
         for (; c < t.n; c += 64) {
             const bool last = c + 64 >= t.n;
             float v[32];
@@ -684,36 +769,12 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
             }
             if (last) {
                 fence_before();
-                __syncwarp();
-                if (lane == 0 && t.steps > 0) release(acc);
+                if (t.steps > 0) release(acc);
             }
-            if (OP == kWeights && a.send) {
-                // Lines of a row's 32 weights, in swizzled pieces of 16 bytes.
-                uint8_t *to = pass + (sent++ & 1) * kSend;
-                if (lane == 0 && !a.add) tma_store_read<1>();
-                __syncwarp();
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    *reinterpret_cast<float4 *>(to + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                if (a.add) { // memory itself adds them to what is there, a line of 128 bytes by eight lanes
-                    __syncwarp();
-                    const int k = c + (lane & 7) * 4;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const int r = q * 4 + (lane >> 3), row = t.f0 + part * kWarp + r;
-                        const float4 x = *reinterpret_cast<const float4 *>(to + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-                        if (row < a.F && k < t.n) add_vector(weights_at<float>(a, t, k, row), x);
-                    }
-                } else {
-                    fence_async();
-                    __syncwarp();
-                    if (lane == 0 && t.f0 + part * kWarp < a.F) tma_store_3d(map, t.c0 + c, t.f0 + part * kWarp, t.e, smem_addr(to));
-                }
-            } else if constexpr (OP == kWeights) {
-                const Kept<T> now = kept;
-                if (!last) read_weights<T>(a, t, c + 64, f, kept);
-                write_weights<T>(a, t, c, f, v, now);
+            if constexpr (OP == kWeights) {
+                const Kept now = kept;
+                if (!last) read_weights(a, t, c + 64, f, kept);
+                if (f < a.F) write_weights(a, t, c, f, v, now, pass);
             } else {
                 const Ahead now = x;
                 if (!last) read_ahead<OP>(a, t, c + 64, part, x);
@@ -723,32 +784,27 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
                     write_slopes(a, t, c, part, y, now, pass);
             }
         }
-        if (!some && t.steps > 0) {
-            __syncwarp();
-            if (lane == 0) release(acc);
-        }
     }
-    if (OP == kWeights && a.send && lane == 0) tma_store_done();
     if (!ok && a.d_status && lane == 0) atomicOr(a.d_status, AP_FLAG_CORRUPT);
 }
 
 template <Op OP, bool MAPS, bool PAIR>
-__global__ void __launch_bounds__(kExThreads, 1)
+__global__ void __launch_bounds__(ex_threads(MAPS), 1)
     k_experts(const __grid_constant__ ExMaps m, const ExArgs a)
 {
     pdl_begin();
     constexpr bool kPass2 = OP == kWeights && MAPS; // two warps pass stages on to the products
     extern __shared__ __align__(1024) uint8_t s_mem[];
     __shared__ Table s_tab;
-    // (FP32 weights: in front of the stages, which lie on the boundaries that their swizzle wants)
-    __shared__ __align__(16) uint8_t s_pass[OP == kWeights ? 16 : kWriters * kPass];
+    constexpr int kPassOf = OP == kWeights ? kHalf : kPass;
+    __shared__ __align__(16) uint8_t s_pass[kWriters * kPassOf];
     __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_ready[kPass2 ? kMaxStages : 1], s_done[2], s_free[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
     const int wid = threadIdx.x / kWarp, lane = (int)lane_id();
     const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
     const int stage_bytes = 2 * kPanel + a.columns * (PAIR ? 64 : 128);
-    uint8_t *stages = s_mem + ((1024 - (smem_addr(s_mem) & 1023)) & 1023) + (OP == kWeights && a.send ? kWriters * 2 * kSend : 0);
+    uint8_t *stages = s_mem + ((1024 - (smem_addr(s_mem) & 1023)) & 1023);
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             bar_init(smem_addr(&s_full[s]), MAPS ? 1 : kFetchers);
@@ -773,9 +829,9 @@ __global__ void __launch_bounds__(kExThreads, 1)
     volatile int *dead = &s_dead;
     Walk w(s_tab, (int)blockIdx.x / (PAIR ? 2 : 1), (int)gridDim.x / (PAIR ? 2 : 1));
 
-    if (wid == 0 || (!MAPS && (wid == 2 || wid == 3))) {
+    if (wid == 0 || (!MAPS && (wid == 2 || wid == 3 || wid >= 12))) {
         // ---- fetch: stage by stage, as they fall empty
-        const int thread = wid == 0 ? lane : threadIdx.x - kWarp;
+        const int thread = lane + kWarp * (wid == 0 ? 0 : wid < 4 ? wid - 1 : wid - 9);
         if (!MAPS || elect_one()) {
             if (MAPS) {
                 tma_prefetch_map(&m.xx);
@@ -879,11 +935,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
         }
     } else if (wid >= 4) {
         // ---- write
-        uint8_t *pass = OP == kWeights ? stages - (kWriters - (wid - 4)) * 2 * kSend : s_pass + (wid - 4) * kPass;
-        if (OP == kWeights && !a.out_f32)
-            write_tiles<OP, PAIR, bf16_t>(a, w, rank, wid - 4, tmem, s_done, s_free, pass, &m.out, dead);
-        else
-            write_tiles<OP, PAIR, float>(a, w, rank, wid - 4, tmem, s_done, s_free, pass, &m.out, dead);
+        write_tiles<OP, PAIR>(a, w, rank, wid - 4, tmem, s_done, s_free, s_pass + (wid - 4) * kPassOf, dead);
     }
     __syncwarp();
     fence_before();
@@ -945,17 +997,17 @@ ap_status launch_experts(const char *who, const ExMaps &m, ExArgs a, int64_t til
     static const cudaError_t set =
         cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - fixed);
     if (set != cudaSuccess) return cuda_fail(set, who);
-    const int stage = 2 * kPanel + a.columns * (PAIR ? 64 : 128), send = a.send ? kWriters * 2 * kSend : 0;
-    const int room = kMaxSmem - fixed - 1024 - send;
+    const int stage = 2 * kPanel + a.columns * (PAIR ? 64 : 128);
+    const int room = kMaxSmem - fixed - 1024;
     a.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
-    const size_t smem = (size_t)a.stages * stage + 1024 + send;
+    const size_t smem = (size_t)a.stages * stage + 1024;
     if constexpr (PAIR) {
-        const int pairs = cluster_count((const void *)kernel, kExThreads, smem, 2, st);
+        const int pairs = cluster_count((const void *)kernel, ex_threads(MAPS), smem, 2, st);
         if (pairs < 1) return fail(AP_ENOTSUP, "%s: the stream's SMs take no pair of blocks", who);
-        launch_cluster(kernel, 2 * (int)(tiles < pairs ? tiles : pairs), kExThreads, smem, 2, st, m, a);
+        launch_cluster(kernel, 2 * (int)(tiles < pairs ? tiles : pairs), ex_threads(MAPS), smem, 2, st, m, a);
     } else {
         const int sms = sm_count();
-        launch(kernel, (int)(tiles < sms ? tiles : sms), kExThreads, smem, st, m, a);
+        launch(kernel, (int)(tiles < sms ? tiles : sms), ex_threads(MAPS), smem, st, m, a);
     }
     AP_CHECK_LAUNCH(who);
     return AP_OK;
@@ -977,12 +1029,15 @@ bool odd_address(const void *p, unsigned bytes) { return (reinterpret_cast<uintp
 int columns_for(int64_t rows, int32_t E)
 {
     const int64_t each = rows / E;
-    return each >= 96 ? 256 : each >= 24 ? 128 : 64;
+    return each > 128 ? 256 : each > 32 ? 128 : 64;
 }
 
 ap_status rows_product(const char *who, Op op, ExArgs a, int halves, cudaStream_t st)
 {
     if (a.E == 1) a.lde = a.ldw * (op == kForward ? a.F * halves : a.K); // (of no account)
+    a.x_end = reinterpret_cast<const char *>(a.x + (a.rows - 1) * a.ldx + a.K);
+    a.W_end = reinterpret_cast<const char *>(a.W + (a.E - 1) * a.lde +
+                                             (op == kForward ? (a.F * halves - 1) * a.ldw + a.K : (a.K - 1) * a.ldw + a.F));
     a.columns = columns_for(a.rows, a.E);
     a.vec_out = !odd_address(a.out, 16) && a.ldo % 8 == 0 && a.F % 8 == 0;
     a.vec_pre = !odd_address(a.pre, 16) && a.ldpre % 8 == 0 && a.F % 8 == 0;
@@ -1002,7 +1057,7 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, cudaStream_
     const uint64_t ex[2] = {(uint64_t)a.K, (uint64_t)a.rows}, px[1] = {(uint64_t)a.ldx};
     const uint32_t bx[2] = {64, a.columns >= 128 ? 64u : 32u}, ball[2] = {64, (uint32_t)(pair ? a.columns / 2 : a.columns)};
     bool ok = make_map(&m.x, a.x, 2, ex, px, bx) && make_map(&m.xx, a.x, 2, ex, px, ball);
-    // One copy for a gated product's features needs whole sixteens: 8 copies of 16 lines took 957 us where one takes ... us
+    // One copy for a gated product's features needs whole sixteens: 8 copies of 16 lines took 957 us where one takes 590
     a.by16 = op == kForward && halves == 2 && a.F % 16 == 0;
     if (a.by16) {
         const uint64_t ew[5] = {(uint64_t)deep, 16, 2, (uint64_t)a.F / 16, (uint64_t)a.E};
@@ -1024,8 +1079,7 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, cudaStream_
 
 } // namespace
 
-bool umma::make_map(CUtensorMap *map, const void *base, int dims, const uint64_t *extent, const uint64_t *pitch, const uint32_t *box,
-                    bool f32)
+bool umma::make_map(CUtensorMap *map, const void *base, int dims, const uint64_t *extent, const uint64_t *pitch, const uint32_t *box)
 {
     using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -1043,8 +1097,8 @@ bool umma::make_map(CUtensorMap *map, const void *base, int dims, const uint64_t
     cuuint64_t strides[4], sizes[5];
     cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < dims; ++i) sizes[i] = extent[i];
-    for (int i = 0; i + 1 < dims; ++i) strides[i] = pitch[i] * (f32 ? 4 : 2);
-    return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void *>(base), sizes, strides, box, ones,
+    for (int i = 0; i + 1 < dims; ++i) strides[i] = pitch[i] * 2;
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void *>(base), sizes, strides, box, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1126,21 +1180,17 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
         a.x = (const bf16_t *)dy, a.W = (const bf16_t *)x, a.ldx = ldy, a.ldw = ldx;
         a.seg = d_seg_off, a.live = d_live, a.out = dW, a.d_status = d_status, a.rows = rows, a.E = E, a.F = N, a.K = K;
         a.out_f32 = dw_dtype == AP_DTYPE_F32, a.add = accumulate != 0;
+        a.x_end = reinterpret_cast<const char *>(a.x + (rows - 1) * ldy + N);
+        a.W_end = reinterpret_cast<const char *>(a.W + (rows - 1) * ldx + K);
         const bool maps = rows > 0 && mappable(dy, ldy) && mappable(x, ldx);
         a.columns = K > 128 ? 256 : K > 64 ? 128 : 64;
         a.tiles_f = (N + kLanes - 1) / kLanes;
         auto tiles_of = [&] { return (int64_t)E * a.tiles_f * ((K + a.columns - 1) / a.columns); };
         if (tiles_of() < 2 * sm_count()) a.columns = K > 64 ? 128 : 64; // few tiles: smaller ones, for more SMs
-        a.vec_out = !odd_address(dW, 32) && K % (a.out_f32 ? 8 : 16) == 0;
+        a.vec_out = !odd_address(dW, 16) && K % (a.out_f32 ? 4 : 8) == 0;
         const int64_t tiles = tiles_of();
         if (tiles >= INT32_MAX) return fail(AP_EINVAL, "%s: %lld tiles are more than one launch takes", who, (long long)tiles);
         ExMaps m = {};
-        // (FP32 sums to what is there: 587 us where the writers read it, 471 where memory adds, at 65536 rows, 128 x 2048 x 1024)
-        if (a.out_f32 && !odd_address(dW, 16) && K % 4 == 0) {
-            const uint64_t eo[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)E}, po[2] = {(uint64_t)K, (uint64_t)N * K};
-            const uint32_t box[3] = {32, 32, 1};
-            a.send = make_map(&m.out, dW, 3, eo, po, box, true);
-        }
         ap_status s;
         if (maps) {
             // two chunks of 64 columns in a copy where rows are whole chunks: a row's end is no border to such a map

@@ -101,19 +101,6 @@ __device__ __forceinline__ void tma_5d(uint32_t to, const CUtensorMap *map, int 
                      "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
                      : "memory");
 }
-// From shared memory; a thread's copies come in groups.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int y, int z, uint32_t from)
-{
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y), "r"(z),
-                 "r"(from)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-template <int N> __device__ __forceinline__ void tma_store_read() // all groups but the last N have read shared memory
-{
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -243,10 +230,9 @@ __device__ __forceinline__ void matrices_load(uint32_t at, uint32_t (&r)[4])
 }
 
 // ---- host ---------------------------------------------------------------------------
-// A map of BF16 (or FP32) values, innermost first, with lines of 128 bytes,
-// swizzled; pitches in elements for the dimensions after the first.
-bool make_map(CUtensorMap *map, const void *base, int dims, const uint64_t *extent, const uint64_t *pitch, const uint32_t *box,
-              bool f32 = false);
+// A map of BF16 values, innermost first, with lines of 128 bytes, swizzled;
+// pitches in elements for the dimensions after the first.
+bool make_map(CUtensorMap *map, const void *base, int dims, const uint64_t *extent, const uint64_t *pitch, const uint32_t *box);
 
 } // namespace umma
 } // namespace ap
