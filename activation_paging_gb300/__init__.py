@@ -586,10 +586,23 @@ def _out_rows(out, rows: int, cols: int, dtype, device, stream, name: str):
     return out, pitch, kind
 
 
+def _expert_scratch(scratch, a, lda, rows_a, cols_a, b, ldb, lde, rows_b, cols_b, device, stream):
+    """(tensor, bytes) of the work space for operands that do not lie on 16-byte boundaries: none, as a rule."""
+    if scratch is not None:
+        _need(scratch, torch.uint8, "scratch")
+        return scratch, scratch.numel()
+    if not ((a | b) & 15 or (lda | ldb | lde) & 7):
+        return None, 0
+    n = ctypes.c_int64(0)
+    check(lib().ap_expert_linear_scratch_bytes(a, lda, rows_a, cols_a, b, ldb, lde, rows_b, cols_b, ctypes.byref(n)),
+          "expert_linear_scratch_bytes")
+    return (_empty((n.value,), torch.uint8, device, stream), n.value) if n.value else (None, 0)
+
+
 def expert_linear(x: torch.Tensor, W: torch.Tensor, seg_off: torch.Tensor, live: torch.Tensor,
                   bias: torch.Tensor | None = None, act: str | None = None, residual: torch.Tensor | None = None,
                   out: torch.Tensor | None = None, pre: torch.Tensor | None = None, dtype: torch.dtype | None = None,
-                  status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                  scratch: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """out[r] = act(x[r] W[e]^T + bias[e]) + residual[r] for the rows r of each
     expert e: ``live[e]`` rows from ``seg_off[e]`` ([E] int32 on the GPU, as the
     dispatch leaves them; the counts are read there).  x [rows, K] BF16, W [E, N, K]
@@ -597,7 +610,9 @@ def expert_linear(x: torch.Tensor, W: torch.Tensor, seg_off: torch.Tensor, live:
     float32: ``dtype``).  ``act``: None, 'silu', 'gelu', or 'swiglu' with W
     [E, 2 N, K], silu of the first N columns times the others.  ``pre``: a BF16
     tensor that receives the values before the activation, for
-    ``expert_linear_dx``.  Rows may lie apart; rows of no expert are not written."""
+    ``expert_linear_dx``.  Rows may lie apart; rows of no expert are not written.
+    ``scratch``: a uint8 tensor to reuse where rows do not lie on 16-byte
+    boundaries (they are copied to such)."""
     E, ps, pl = _segments(seg_off, live)
     wide, K, ldw, lde = _weights(W, E)
     kind = _act(act)
@@ -610,14 +625,17 @@ def expert_linear(x: torch.Tensor, W: torch.Tensor, seg_off: torch.Tensor, live:
     pr, ldr = (None, 0) if residual is None else _rows16(residual, "residual", (rows, N))
     pp, ldp = (None, 0) if pre is None else _rows16(pre, "pre", (rows, wide))
     out, ldo, okind = _out_rows(out, rows, N, dtype, x.device, stream, "out")
-    check(lib().ap_expert_linear(px, ldx, rows, E, N, K, ps, pl, W.data_ptr(), ldw, lde, pb, kind, pr, ldr, pp, ldp,
-                                 out.data_ptr(), ldo, okind, _status(status), _stream(stream)), "expert_linear")
+    pw = W.data_ptr()
+    scratch, sb = _expert_scratch(scratch, px, ldx, rows, K, pw, ldw, lde, E * wide, K, x.device, stream)
+    check(lib().ap_expert_linear(px, ldx, rows, E, N, K, ps, pl, pw, ldw, lde, pb, kind, pr, ldr, pp, ldp, out.data_ptr(), ldo,
+                                 okind, _p(scratch), sb, _status(status), _stream(stream)), "expert_linear")
     return out
 
 
 def expert_linear_dx(dy: torch.Tensor, W: torch.Tensor, seg_off: torch.Tensor, live: torch.Tensor, act: str | None = None,
                      pre: torch.Tensor | None = None, residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                     dtype: torch.dtype | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                     dtype: torch.dtype | None = None, scratch: torch.Tensor | None = None,
+                     status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient of ``expert_linear``'s rows: (dy[r] W[e] + residual[r]) times the
     derivative of the activation ``act`` that made them, at ``pre``, from which
     they were made ([rows, K] BF16; 'swiglu': [rows, 2 K], as the result then)."""
@@ -632,14 +650,17 @@ def expert_linear_dx(dy: torch.Tensor, W: torch.Tensor, seg_off: torch.Tensor, l
     pp, ldp = _rows16(pre, "pre", (rows, wide)) if kind else (None, 0)
     pr, ldr = (None, 0) if residual is None else _rows16(residual, "residual", (rows, K))
     out, ldo, okind = _out_rows(out, rows, wide, dtype, dy.device, stream, "out")
-    check(lib().ap_expert_linear_dx(py, ldy, rows, E, N, K, ps, pl, W.data_ptr(), ldw, lde, kind, pp, ldp, pr, ldr,
-                                    out.data_ptr(), ldo, okind, _status(status), _stream(stream)), "expert_linear_dx")
+    pw = W.data_ptr()
+    scratch, sb = _expert_scratch(scratch, py, ldy, rows, N, pw, ldw, lde, E * N, K, dy.device, stream)
+    check(lib().ap_expert_linear_dx(py, ldy, rows, E, N, K, ps, pl, pw, ldw, lde, kind, pp, ldp, pr, ldr, out.data_ptr(), ldo,
+                                    okind, _p(scratch), sb, _status(status), _stream(stream)), "expert_linear_dx")
     return out
 
 
 def expert_linear_dw(dy: torch.Tensor, x: torch.Tensor, seg_off: torch.Tensor, live: torch.Tensor,
                      dW: torch.Tensor | None = None, dbias: torch.Tensor | None = None, accumulate: bool = False,
-                     dtype: torch.dtype = torch.float32, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                     dtype: torch.dtype = torch.float32, scratch: torch.Tensor | None = None,
+                     status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient of ``expert_linear``'s weights: dW[e] = the sum of dy[r]^T x[r]
     over the expert's rows ([E, N, K] float32 or BF16), written whole or, with
     ``accumulate``, added to ``dW``; likewise ``dbias`` ([E, N] float32) where
@@ -658,7 +679,8 @@ def expert_linear_dw(dy: torch.Tensor, x: torch.Tensor, seg_off: torch.Tensor, l
         raise ValueError(f"dW must be bfloat16 or float32, got {dW.dtype}")
     pw = _need_shape(dW, dW.dtype, (E, N, K), "dW")
     pb = None if dbias is None else _need_shape(dbias, torch.float32, (E, N), "dbias")
-    check(lib().ap_expert_linear_dw(py, ldy, px, ldx, rows, E, N, K, ps, pl, 1 if accumulate else 0, pw, wkind, pb,
+    scratch, sb = _expert_scratch(scratch, py, ldy, rows, N, px, ldx, 0, rows, K, dy.device, stream)
+    check(lib().ap_expert_linear_dw(py, ldy, px, ldx, rows, E, N, K, ps, pl, 1 if accumulate else 0, pw, wkind, pb, _p(scratch), sb,
                                     _status(status), _stream(stream)), "expert_linear_dw")
     return dW
 

@@ -63,9 +63,10 @@ SIGNATURES = {
     "ap_route_scored": (i32, [P, i64, i32, i32, i32, P, i32, i32, i32, i32, f32, P, P, P, P, P]),
     "ap_route_scored_backward": (i32, [P, i64, i32, i32, P, P, i32, i32, f32, P, P, P]),
     "ap_route_bias_step": (i32, [P, P, i32, f32, i32, P]),
-    "ap_expert_linear": (i32, [P, i64, i64, i32, i32, i32, P, P, P, i64, i64, P, i32, P, i64, P, i64, P, i64, i32, P, P]),
-    "ap_expert_linear_dx": (i32, [P, i64, i64, i32, i32, i32, P, P, P, i64, i64, i32, P, i64, P, i64, P, i64, i32, P, P]),
-    "ap_expert_linear_dw": (i32, [P, i64, P, i64, i64, i32, i32, i32, P, P, i32, P, i32, P, P, P]),
+    "ap_expert_linear_scratch_bytes": (i32, [P, i64, i64, i32, P, i64, i64, i64, i32, P]),
+    "ap_expert_linear": (i32, [P, i64, i64, i32, i32, i32, P, P, P, i64, i64, P, i32, P, i64, P, i64, P, i64, i32, P, i64, P, P]),
+    "ap_expert_linear_dx": (i32, [P, i64, i64, i32, i32, i32, P, P, P, i64, i64, i32, P, i64, P, i64, P, i64, i32, P, i64, P, P]),
+    "ap_expert_linear_dw": (i32, [P, i64, P, i64, i64, i32, i32, i32, P, P, i32, P, i32, P, P, i64, P, P]),
     "ap_embed": (i32, [P, i64, i64, i32, P, i32, i64, i32, f32, P, i64, i32, P, P]),
     "ap_embed_scratch_bytes": (i32, [i64, i64, i32, P]),
     "ap_embed_backward": (i32, [P, i64, i32, P, i32, i64, i32, i64, i64, f32, i32, P, i64, i32, P, i64, P, P]),

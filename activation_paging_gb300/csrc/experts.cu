@@ -18,9 +18,9 @@
 // Outputs and what the epilogue reads (residual, pre-activations) pass through
 // shared memory as 8 x 8 matrices, transposed, so that memory sees rows' pieces
 // of 32 and 64 bytes.
-// Operands come by tensor map where base and pitch are multiples of 16 bytes;
-// else (odd row lengths) seven warps cut them out of the 16-byte granules that
-// hold them.
+// Operands come by tensor map, which wants bases and pitches that are multiples
+// of 16 bytes.  Others (odd row lengths) are copied to rows that begin on such
+// boundaries first (k_repitch).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -32,10 +32,7 @@ namespace {
 using bf16_t = __nv_bfloat16;
 using namespace umma;
 
-// Warps: 0 fetches, 1 multiplies, 2 and 3 pass stages on, 4 to 11 write; without
-// tensor maps 0, 2, 3 and 12 to 15 fetch.
-constexpr int ex_threads(bool maps) { return maps ? 384 : 512; }
-constexpr int kFetchers = 7 * 32;
+constexpr int kExThreads = 384;    // warps: 0 fetches, 1 multiplies, 2 and 3 pass stages on, 4 to 11 write
 constexpr int kWriters = 8;        // warps: two for each quarter of the lanes, with every other 32 columns
 constexpr int kLanes = 128;        // features of a tile
 constexpr int kDepth = 64;         // contraction of a stage: one line of 128 bytes
@@ -62,7 +59,6 @@ struct ExArgs {
     int64_t rows;
     int E, F, K;           // features of the output (of each half of a gated product), contraction
     int tiles_f, columns, stages, act;
-    const char *x_end, *W_end; // where their buffers end
     bool out_f32, add;     // add: kWeights, to what is there
     bool chunk_x, chunk_w; // kWeights: rows of whole 64s, two of them in a copy
     bool by16;             // a gated product's map takes 16 features of either half in turn
@@ -178,164 +174,56 @@ template <Op OP, bool PAIR> __device__ __forceinline__ Tile tile_of(const ExArgs
     return t;
 }
 
-// 16 bytes from an address between granules: of the two granules a and b those
-// from byte `off` (even) on.
-__device__ __forceinline__ uint4 cut(uint4 a, uint4 b, uint32_t off)
-{
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
-    if (off & 2)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// `lines` lines of 64 values from p on, `ld` values apart, of which the first
-// `rows` and in each the first `n` values are there: cut into swizzled pieces of
-// 16 bytes, zeros elsewhere.  Granules that lie inside the operand's buffer
-// (begin to end) are read whole, the ones that its ends cut element by element.
-__device__ __forceinline__ void fetch_lines(uint8_t *to, const bf16_t *p, int64_t ld, int lines, int rows, int n, const char *begin,
-                                            const char *end, int thread)
-{
-    constexpr int kEach = 5, kStep = kFetchers / 8; // lines of a thread on their way, and how far apart
-    const int c = thread & 7;
-    n = min(max(n - c * 8, 0), 8);
-    const char *from = reinterpret_cast<const char *>(p + c * 8 + (int64_t)(thread >> 3) * ld);
-    const int64_t step = ld * 2 * kStep;
-    for (int l0 = thread >> 3; l0 < lines; l0 += kEach * kStep) {
-        uint4 lo[kEach], hi[kEach];
-        bool cut_off[kEach];
-#pragma unroll
-        for (int u = 0; u < kEach; ++u) {
-            const char *q = from + u * step;
-            const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(q) & 15;
-            const char *at = q - off;
-            const bool on = n > 0 && l0 + u * kStep < rows, second = off + 2 * n > 16;
-            cut_off[u] = at < begin || at + (second ? 32 : 16) > end;
-            lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
-            if (on && !cut_off[u]) {
-                lo[u] = *reinterpret_cast<const uint4 *>(at);
-                if (second) hi[u] = *reinterpret_cast<const uint4 *>(at + 16);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kEach; ++u, from += step) {
-            const int l = l0 + u * kStep;
-            if (l >= lines) continue;
-            uint4 w = cut(lo[u], hi[u], (uint32_t)reinterpret_cast<uintptr_t>(from) & 15);
-            if (n > 0 && l < rows && cut_off[u]) {
-                uint32_t v[4] = {0, 0, 0, 0};
-                const unsigned short *e = reinterpret_cast<const unsigned short *>(from);
-                for (int j = 0; j < n; ++j) {
-                    const uint32_t x = (uint32_t)e[j] << 16 * (j & 1);
-                    v[0] |= j < 2 ? x : 0, v[1] |= j >> 1 == 1 ? x : 0, v[2] |= j >> 1 == 2 ? x : 0, v[3] |= j >> 1 == 3 ? x : 0;
-                }
-                w = make_uint4(v[0], v[1], v[2], v[3]);
-            } else if (n < 8) { // a row's end
-                w.x &= n >= 2 ? ~0u : n == 1 ? 0xffffu : 0u;
-                w.y &= n >= 4 ? ~0u : n == 3 ? 0xffffu : 0u;
-                w.z &= n >= 6 ? ~0u : n == 5 ? 0xffffu : 0u;
-                w.w &= n == 7 ? 0xffffu : 0u;
-            }
-            *reinterpret_cast<uint4 *>(to + l * 128 + ((c ^ (l & 7)) << 4)) = w;
-        }
-    }
-}
-
-// A stage by plain loads.
-template <Op OP>
-__device__ __forceinline__ void fetch_plain(const ExArgs &a, const Tile &t, int k0, uint8_t *stage, int thread)
-{
-    const char *x0 = reinterpret_cast<const char *>(a.x), *w0 = reinterpret_cast<const char *>(a.W);
-    uint8_t *col = stage + 2 * kPanel;
-    if constexpr (OP == kForward) {
-        const bf16_t *W = a.W + t.e * a.lde + k0;
-        if (a.act == AP_ACT_SWIGLU)
-            for (int b = 0; b < 8; ++b) {
-                const int f = t.f0 + (b >> 1) * 16;
-                fetch_lines(stage + b * 2048, W + (f + (b & 1) * a.F) * a.ldw, a.ldw, 16, a.F - f, a.K - k0, w0, a.W_end, thread);
-            }
-        else
-            fetch_lines(stage, W + t.f0 * a.ldw, a.ldw, kLanes, a.F - t.f0, a.K - k0, w0, a.W_end, thread);
-    } else {
-        for (int h = 0; h < 2; ++h) {
-            const int f = t.f0 + h * 64;
-            if (OP == kRows)
-                fetch_lines(stage + h * kPanel, a.W + t.e * a.lde + k0 * a.ldw + f, a.ldw, 64, a.K - k0, a.F - f, w0, a.W_end, thread);
-            else
-                fetch_lines(stage + h * kPanel, a.x + (int64_t)(t.row0 + k0) * a.ldx + f, a.ldx, 64, t.live - k0, a.F - f, x0, a.x_end,
-                            thread);
-        }
-    }
-    if constexpr (OP == kWeights) {
-        for (int c = 0; c < t.n; c += 64)
-            fetch_lines(col + c * 128, a.W + (int64_t)(t.row0 + k0) * a.ldw + t.c0 + c, a.ldw, 64, t.live - k0, a.K - t.c0 - c, w0, a.W_end,
-                        thread);
-    } else {
-        fetch_lines(col, a.x + (int64_t)t.row0 * a.ldx + k0, a.ldx, (t.n + 31) & ~31, t.n, a.K - k0, x0, a.x_end, thread);
-    }
-}
-
 // A stage: the features' operand (16 KB), then the columns'.  A gated product's
 // features alternate by 16 between the gate's and the up product's, so that a
 // writing lane finds both.
-template <Op OP, bool MAPS, bool PAIR>
-__device__ __forceinline__ void fetch(const ExArgs &a, const Tile &t, int step, uint8_t *stage, const ExMaps &m, uint32_t full, int rank,
-                                      int thread)
+template <Op OP, bool PAIR>
+__device__ __forceinline__ void fetch(const ExArgs &a, const Tile &t, int step, uint8_t *stage, const ExMaps &m, uint32_t full, int rank)
 {
     const int k0 = step * kDepth;
     const bool gated = OP == kForward && a.act == AP_ACT_SWIGLU;
     uint8_t *col = stage + 2 * kPanel;
-    if constexpr (MAPS) {
-        const uint32_t sa = smem_addr(stage), sb = smem_addr(col);
-        // a pair's blocks bring half of the tile's columns each, and all tell the first one's barrier
-        const int half = (t.n + 31) / 32 * 16, most = PAIR ? a.columns / 2 : a.columns, cols = PAIR ? half : t.n;
-        const int from = PAIR ? rank * half : 0; // of the tile's columns
-        const int small = a.columns >= 128 ? 64 : 32, boxes = ceil_div(cols, small);
-        const bool all = OP == kWeights || cols > most - small; // as many as there may be
-        const int bytes = 2 * kPanel + (all ? most : boxes * small) * 128;
-        if (rank == 0) bar_expect(full, PAIR ? 2 * bytes : bytes);
-        const uint32_t bar = PAIR ? cluster_addr(full, 0) : full;
-        if constexpr (OP == kForward) {
-            if (!gated)
-                tma_3d<PAIR>(sa, &m.w, k0, t.f0, t.e, bar);
-            else if (a.by16)
-                tma_5d<PAIR>(sa, &m.w, k0, 0, 0, t.f0 >> 4, t.e, bar);
-            else
-                for (int b = 0; b < 8; ++b) tma_3d<PAIR>(sa + b * 2048, &m.w, k0, t.f0 + (b >> 1) * 16 + (b & 1) * a.F, t.e, bar);
-        } else if constexpr (OP == kRows) {
-            tma_3d<PAIR>(sa, &m.w, t.f0, k0, t.e, bar);
-            tma_3d<PAIR>(sa + kPanel, &m.w, t.f0 + 64, k0, t.e, bar);
-        }
-        if constexpr (OP == kWeights) {
-            const int row = t.row0 + k0, c = t.c0 + from;
-            if (a.chunk_x) {
-                tma_3d<PAIR>(sa, &m.xx, 0, row, t.f0 >> 6, bar);
-            } else {
-                tma_2d<PAIR>(sa, &m.x, t.f0, row, bar);
-                tma_2d<PAIR>(sa + kPanel, &m.x, t.f0 + 64, row, bar);
-            }
-            for (int i = 0; i < most; i += 128) {
-                const uint32_t to = sb + i * 128;
-                if (a.chunk_w && most >= 128 && c % 64 == 0) {
-                    tma_3d<PAIR>(to, &m.ww, 0, row, (c + i) >> 6, bar);
-                } else {
-                    tma_2d<PAIR>(to, &m.w, c + i, row, bar);
-                    if (most >= 128) tma_2d<PAIR>(to + kPanel, &m.w, c + i + 64, row, bar);
-                }
-            }
-        } else if (all) {
-            tma_2d<PAIR>(sb, &m.xx, k0, t.row0 + from, bar);
+    const uint32_t sa = smem_addr(stage), sb = smem_addr(col);
+    // a pair's blocks bring half of the tile's columns each, and all tell the first one's barrier
+    const int half = (t.n + 31) / 32 * 16, most = PAIR ? a.columns / 2 : a.columns, cols = PAIR ? half : t.n;
+    const int from = PAIR ? rank * half : 0; // of the tile's columns
+    const int small = a.columns >= 128 ? 64 : 32, boxes = ceil_div(cols, small);
+    const bool all = OP == kWeights || cols > most - small; // as many as there may be
+    const int bytes = 2 * kPanel + (all ? most : boxes * small) * 128;
+    if (rank == 0) bar_expect(full, PAIR ? 2 * bytes : bytes);
+    const uint32_t bar = PAIR ? cluster_addr(full, 0) : full;
+    if constexpr (OP == kForward) {
+        if (!gated)
+            tma_3d<PAIR>(sa, &m.w, k0, t.f0, t.e, bar);
+        else if (a.by16)
+            tma_5d<PAIR>(sa, &m.w, k0, 0, 0, t.f0 >> 4, t.e, bar);
+        else
+            for (int b = 0; b < 8; ++b) tma_3d<PAIR>(sa + b * 2048, &m.w, k0, t.f0 + (b >> 1) * 16 + (b & 1) * a.F, t.e, bar);
+    } else if constexpr (OP == kRows) {
+        tma_3d<PAIR>(sa, &m.w, t.f0, k0, t.e, bar);
+        tma_3d<PAIR>(sa + kPanel, &m.w, t.f0 + 64, k0, t.e, bar);
+    }
+    if constexpr (OP == kWeights) {
+        const int row = t.row0 + k0, c = t.c0 + from;
+        if (a.chunk_x) {
+            tma_3d<PAIR>(sa, &m.xx, 0, row, t.f0 >> 6, bar);
         } else {
-            for (int i = 0; i < boxes; ++i) tma_2d<PAIR>(sb + i * small * 128, &m.x, k0, t.row0 + from + i * small, bar);
+            tma_2d<PAIR>(sa, &m.x, t.f0, row, bar);
+            tma_2d<PAIR>(sa + kPanel, &m.x, t.f0 + 64, row, bar);
         }
+        for (int i = 0; i < most; i += 128) {
+            const uint32_t to = sb + i * 128;
+            if (a.chunk_w && most >= 128 && c % 64 == 0) {
+                tma_3d<PAIR>(to, &m.ww, 0, row, (c + i) >> 6, bar);
+            } else {
+                tma_2d<PAIR>(to, &m.w, c + i, row, bar);
+                if (most >= 128) tma_2d<PAIR>(to + kPanel, &m.w, c + i + 64, row, bar);
+            }
+        }
+    } else if (all) {
+        tma_2d<PAIR>(sb, &m.xx, k0, t.row0 + from, bar);
     } else {
-        fetch_plain<OP>(a, t, k0, stage, thread);
-        fence_async();
-        bar_arrive(full);
+        for (int i = 0; i < boxes; ++i) tma_2d<PAIR>(sb + i * small * 128, &m.x, k0, t.row0 + from + i * small, bar);
     }
 }
 
@@ -788,12 +676,12 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
     if (!ok && a.d_status && lane == 0) atomicOr(a.d_status, AP_FLAG_CORRUPT);
 }
 
-template <Op OP, bool MAPS, bool PAIR>
-__global__ void __launch_bounds__(ex_threads(MAPS), 1)
+template <Op OP, bool PAIR>
+__global__ void __launch_bounds__(kExThreads, 1)
     k_experts(const __grid_constant__ ExMaps m, const ExArgs a)
 {
     pdl_begin();
-    constexpr bool kPass2 = OP == kWeights && MAPS; // two warps pass stages on to the products
+    constexpr bool kPass2 = OP == kWeights; // two warps pass stages on to the products
     extern __shared__ __align__(1024) uint8_t s_mem[];
     __shared__ Table s_tab;
     constexpr int kPassOf = OP == kWeights ? kHalf : kPass;
@@ -807,7 +695,7 @@ __global__ void __launch_bounds__(ex_threads(MAPS), 1)
     uint8_t *stages = s_mem + ((1024 - (smem_addr(s_mem) & 1023)) & 1023);
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
-            bar_init(smem_addr(&s_full[s]), MAPS ? 1 : kFetchers);
+            bar_init(smem_addr(&s_full[s]), 1);
             bar_init(smem_addr(&s_empty[s]), 1);
             if (kPass2) bar_init(smem_addr(&s_ready[s]), 2);
         }
@@ -829,14 +717,11 @@ __global__ void __launch_bounds__(ex_threads(MAPS), 1)
     volatile int *dead = &s_dead;
     Walk w(s_tab, (int)blockIdx.x / (PAIR ? 2 : 1), (int)gridDim.x / (PAIR ? 2 : 1));
 
-    if (wid == 0 || (!MAPS && (wid == 2 || wid == 3 || wid >= 12))) {
+    if (wid == 0) {
         // ---- fetch: stage by stage, as they fall empty
-        const int thread = lane + kWarp * (wid == 0 ? 0 : wid < 4 ? wid - 1 : wid - 9);
-        if (!MAPS || elect_one()) {
-            if (MAPS) {
-                tma_prefetch_map(&m.xx);
-                tma_prefetch_map(OP == kWeights ? &m.ww : &m.w);
-            }
+        if (elect_one()) {
+            tma_prefetch_map(&m.xx);
+            tma_prefetch_map(OP == kWeights ? &m.ww : &m.w);
             uint32_t count = 0, s = 0, turn = 0; // stages fetched; ring position and its turn
             bool ok = true;
             for (; ok && w.find(a.E); w.next()) {
@@ -846,7 +731,7 @@ __global__ void __launch_bounds__(ex_threads(MAPS), 1)
                         ok = false;
                         break;
                     }
-                    fetch<OP, MAPS, PAIR>(a, t, step, stages + (size_t)s * stage_bytes, m, smem_addr(&s_full[s]), rank, thread);
+                    fetch<OP, PAIR>(a, t, step, stages + (size_t)s * stage_bytes, m, smem_addr(&s_full[s]), rank);
                     ++count;
                     if (++s == (uint32_t)a.stages) {
                         s = 0;
@@ -854,7 +739,7 @@ __global__ void __launch_bounds__(ex_threads(MAPS), 1)
                     }
                 }
             }
-            if (MAPS && (PAIR || !ok)) {
+            if (PAIR || !ok) {
                 // Copies on their way end before the block does (a pair's are told to the first block, which the second
                 // waits for below), and so do the arrivals that the other block's products send here.
                 volatile int none = 0;
@@ -947,6 +832,75 @@ __global__ void __launch_bounds__(ex_threads(MAPS), 1)
     }
 }
 
+// 16 bytes from an address between granules: of the two granules a and b those
+// from byte `off` (even) on.
+__device__ __forceinline__ uint4 cut(uint4 a, uint4 b, uint32_t off)
+{
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+    if (off & 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Rows of `cols` values, ld apart (per of them to an expert, experts lde apart),
+// to rows that begin on 16-byte boundaries; experts without rows are left out.  A
+// warp per row, a lane per 16 bytes there: it cuts them out of the granules that
+// hold them, which are read whole where they lie inside the buffer, and by
+// elements where its ends cut them.  Bound by HBM.
+__global__ void __launch_bounds__(256) k_repitch(const bf16_t *src, int64_t ld, int64_t lde, int64_t per, int64_t rows, int cols,
+                                                 const int32_t *live, bf16_t *dst, int64_t pitch)
+{
+    pdl_begin();
+    const int lane = (int)lane_id(), pieces = (cols + 7) / 8;
+    const char *begin = reinterpret_cast<const char *>(src);
+    const char *end = reinterpret_cast<const char *>(src + (rows - 1) / per * lde + (rows - 1) % per * ld + cols);
+    const int64_t step = (int64_t)gridDim.x * 8;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / kWarp; r < rows; r += step) {
+        const int64_t e = r / per;
+        if (live && live[e] <= 0) continue;
+        const char *row = reinterpret_cast<const char *>(src + e * lde + (r - e * per) * ld);
+        uint4 *to = reinterpret_cast<uint4 *>(dst + r * pitch);
+        const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(row) & 15; // of every piece
+        constexpr int kEach = 4;
+        for (int c0 = lane; c0 < pieces; c0 += kEach * kWarp) {
+            uint4 lo[kEach], hi[kEach];
+            bool whole[kEach];
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                const int c = c0 + u * kWarp, n = min(cols - c * 8, 8);
+                const char *at = row + c * 16 - off;
+                const bool second = (int)off + 2 * n > 16;
+                lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
+                whole[u] = at >= begin && at + (second ? 32 : 16) <= end;
+                if (n > 0 && whole[u]) {
+                    lo[u] = *reinterpret_cast<const uint4 *>(at);
+                    if (second) hi[u] = *reinterpret_cast<const uint4 *>(at + 16);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                const int c = c0 + u * kWarp, n = min(cols - c * 8, 8);
+                if (n <= 0) continue;
+                uint4 w = cut(lo[u], hi[u], off);
+                if (!whole[u]) {
+                    const unsigned short *p = reinterpret_cast<const unsigned short *>(row) + c * 8;
+                    uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < n) v[j / 2] |= (uint32_t)p[j] << 16 * (j & 1);
+                    w = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+                to[c] = w; // (what lies behind the last value is no part of a row to the tensor maps)
+            }
+        }
+    }
+}
+
 // db[e] (+)= the sum of the expert's rows of dy: a block takes 64 columns of an
 // expert, eight warps every eighth row, two columns a lane.
 __global__ void __launch_bounds__(256) k_expert_bias(const bf16_t *dy, int64_t ld, const int32_t *seg, const int32_t *live, int64_t rows,
@@ -987,10 +941,10 @@ bool mappable(const void *p, int64_t ld, int64_t more = 0)
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && more % 8 == 0;
 }
 
-template <Op OP, bool MAPS, bool PAIR = false>
+template <Op OP, bool PAIR = false>
 ap_status launch_experts(const char *who, const ExMaps &m, ExArgs a, int64_t tiles, cudaStream_t st)
 {
-    const auto kernel = k_experts<OP, MAPS, PAIR>;
+    const auto kernel = k_experts<OP, PAIR>;
     cudaFuncAttributes attr;
     static const int fixed = cudaFuncGetAttributes(&attr, (const void *)kernel) == cudaSuccess ? (int)attr.sharedSizeBytes : -1;
     if (fixed < 0) return cuda_fail(cudaGetLastError(), who);
@@ -1002,12 +956,12 @@ ap_status launch_experts(const char *who, const ExMaps &m, ExArgs a, int64_t til
     a.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
     const size_t smem = (size_t)a.stages * stage + 1024;
     if constexpr (PAIR) {
-        const int pairs = cluster_count((const void *)kernel, ex_threads(MAPS), smem, 2, st);
+        const int pairs = cluster_count((const void *)kernel, kExThreads, smem, 2, st);
         if (pairs < 1) return fail(AP_ENOTSUP, "%s: the stream's SMs take no pair of blocks", who);
-        launch_cluster(kernel, 2 * (int)(tiles < pairs ? tiles : pairs), ex_threads(MAPS), smem, 2, st, m, a);
+        launch_cluster(kernel, 2 * (int)(tiles < pairs ? tiles : pairs), kExThreads, smem, 2, st, m, a);
     } else {
         const int sms = sm_count();
-        launch(kernel, (int)(tiles < sms ? tiles : sms), ex_threads(MAPS), smem, st, m, a);
+        launch(kernel, (int)(tiles < sms ? tiles : sms), kExThreads, smem, st, m, a);
     }
     AP_CHECK_LAUNCH(who);
     return AP_OK;
@@ -1023,6 +977,36 @@ ap_status check_rows(const char *who, int64_t rows, int32_t E, int32_t N, int32_
         return fail(AP_EINVAL, "%s: bad pitches %lld, %lld, %lld", who, (long long)ldx, (long long)ldw, (long long)lde);
     return AP_OK;
 }
+int64_t repitch_bytes(const void *p, int64_t ld, int64_t lde, int64_t rows, int cols)
+{
+    return mappable(p, ld, lde) ? 0 : (rows * ((cols + 7) / 8 * 16) + 255) / 256 * 256;
+}
+// Copies operands that tensor maps do not take into the work space, one after the other.
+struct Repitch {
+    const char *who;
+    void *scratch;
+    int64_t left;
+    cudaStream_t st;
+    // `count` lots of `per` rows, *lde apart (nullptr: one lot)
+    ap_status take(const bf16_t **p, int64_t *ld, int64_t *lde, int64_t per, int count, int cols, const int32_t *live)
+    {
+        const int64_t rows = per * count, need = repitch_bytes(*p, *ld, lde ? *lde : 0, rows, cols), pitch = (cols + 7) / 8 * 8;
+        if (!need) return AP_OK;
+        if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 15)) return fail(AP_EINVAL, "%s: scratch is NULL or not aligned", who);
+        if (left < need)
+            return fail(AP_EINVAL, "%s: %lld bytes of scratch left, %lld needed", who, (long long)left, (long long)need);
+        bf16_t *to = static_cast<bf16_t *>(scratch);
+        const int64_t want = (rows + 7) / 8, most = (int64_t)sm_count() * 8;
+        launch(k_repitch, (int)(want < most ? want : most), 256, 0, st, *p, *ld, lde ? *lde : 0, per, rows, cols, live, to, pitch);
+        AP_CHECK_LAUNCH(who);
+        scratch = static_cast<char *>(scratch) + need;
+        left -= need;
+        *p = to;
+        *ld = pitch;
+        if (lde) *lde = per * pitch;
+        return AP_OK;
+    }
+};
 bool odd_address(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
 // Columns of a tile: rows of the output at most, by what an expert has on the average.
@@ -1032,28 +1016,24 @@ int columns_for(int64_t rows, int32_t E)
     return each > 128 ? 256 : each > 32 ? 128 : 64;
 }
 
-ap_status rows_product(const char *who, Op op, ExArgs a, int halves, cudaStream_t st)
+ap_status rows_product(const char *who, Op op, ExArgs a, int halves, void *scratch, int64_t scratch_bytes, cudaStream_t st)
 {
     if (a.E == 1) a.lde = a.ldw * (op == kForward ? a.F * halves : a.K); // (of no account)
-    a.x_end = reinterpret_cast<const char *>(a.x + (a.rows - 1) * a.ldx + a.K);
-    a.W_end = reinterpret_cast<const char *>(a.W + (a.E - 1) * a.lde +
-                                             (op == kForward ? (a.F * halves - 1) * a.ldw + a.K : (a.K - 1) * a.ldw + a.F));
+    const int wide = op == kForward ? a.F * halves : a.K, deep = op == kForward ? a.K : a.F; // of W[e]
+    Repitch re = {who, scratch, scratch_bytes, st};
+    if (const ap_status r = re.take(&a.x, &a.ldx, nullptr, a.rows, 1, a.K, nullptr); r != AP_OK) return r;
+    if (const ap_status r = re.take(&a.W, &a.ldw, &a.lde, wide, a.E, deep, a.live); r != AP_OK) return r;
     a.columns = columns_for(a.rows, a.E);
     a.vec_out = !odd_address(a.out, 16) && a.ldo % 8 == 0 && a.F % 8 == 0;
     a.vec_pre = !odd_address(a.pre, 16) && a.ldpre % 8 == 0 && a.F % 8 == 0;
     a.vec_res = !odd_address(a.residual, 16) && a.ldres % 8 == 0 && a.F % 8 == 0;
-    const bool maps = mappable(a.x, a.ldx) && mappable(a.W, a.ldw, a.lde);
     // Two blocks to a tile of 256 features share its rows' operand: 32 KB from L2 for 48 a product.
-    const bool pair = maps && a.columns == 256 && a.F * (op == kForward ? halves : 1) > kLanes;
+    const bool pair = a.columns == 256 && a.F * (op == kForward ? halves : 1) > kLanes;
     const int per = (op == kForward && halves == 2 ? kLanes / 2 : kLanes) * (pair ? 2 : 1);
     a.tiles_f = (a.F + per - 1) / per;
     const int64_t tiles = (a.rows / a.columns + a.E) * (int64_t)a.tiles_f;
     if (tiles >= INT32_MAX) return fail(AP_EINVAL, "%s: %lld tiles are more than one launch takes", who, (long long)tiles);
     ExMaps m = {};
-    if (!maps)
-        return op == kForward ? launch_experts<kForward, false>(who, m, a, tiles, st)
-                              : launch_experts<kRows, false>(who, m, a, tiles, st);
-    const int wide = op == kForward ? a.F * halves : a.K, deep = op == kForward ? a.K : a.F; // of W[e]
     const uint64_t ex[2] = {(uint64_t)a.K, (uint64_t)a.rows}, px[1] = {(uint64_t)a.ldx};
     const uint32_t bx[2] = {64, a.columns >= 128 ? 64u : 32u}, ball[2] = {64, (uint32_t)(pair ? a.columns / 2 : a.columns)};
     bool ok = make_map(&m.x, a.x, 2, ex, px, bx) && make_map(&m.xx, a.x, 2, ex, px, ball);
@@ -1071,10 +1051,9 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, cudaStream_
     }
     if (!ok) return fail(AP_ENOTSUP, "%s: no tensor map of these sizes", who);
     if (pair)
-        return op == kForward ? launch_experts<kForward, true, true>(who, m, a, tiles, st)
-                              : launch_experts<kRows, true, true>(who, m, a, tiles, st);
-    return op == kForward ? launch_experts<kForward, true>(who, m, a, tiles, st)
-                          : launch_experts<kRows, true>(who, m, a, tiles, st);
+        return op == kForward ? launch_experts<kForward, true>(who, m, a, tiles, st)
+                              : launch_experts<kRows, true>(who, m, a, tiles, st);
+    return op == kForward ? launch_experts<kForward>(who, m, a, tiles, st) : launch_experts<kRows>(who, m, a, tiles, st);
 }
 
 } // namespace
@@ -1105,10 +1084,22 @@ bool umma::make_map(CUtensorMap *map, const void *base, int dims, const uint64_t
 
 } // namespace ap
 
+extern "C" ap_status ap_expert_linear_scratch_bytes(const void *a, int64_t lda, int64_t rows_a, int32_t cols_a, const void *b,
+                                                    int64_t ldb, int64_t lde, int64_t rows_b, int32_t cols_b, int64_t *bytes)
+{
+    using namespace ap;
+    if (!bytes || rows_a < 0 || rows_b < 0 || cols_a < 1 || cols_b < 1 || cols_a > (1 << 20) || cols_b > (1 << 20) ||
+        rows_a >= (int64_t(1) << 31) || rows_b >= (int64_t(1) << 32))
+        return fail(AP_EINVAL, "expert_linear_scratch_bytes: bad sizes");
+    *bytes = repitch_bytes(a, lda, 0, rows_a, cols_a) + repitch_bytes(b, ldb, lde, rows_b, cols_b);
+    return AP_OK;
+}
+
 extern "C" ap_status ap_expert_linear(const void *x, int64_t ldx, int64_t rows, int32_t E, int32_t N, int32_t K,
                                       const int32_t *d_seg_off, const int32_t *d_live, const void *W, int64_t ldw, int64_t lde,
                                       const float *bias, int32_t act, const void *residual, int64_t ldres, void *pre,
-                                      int64_t ldpre, void *out, int64_t ldo, int32_t out_dtype, uint32_t *d_status, void *stream)
+                                      int64_t ldpre, void *out, int64_t ldo, int32_t out_dtype, void *scratch, int64_t scratch_bytes,
+                                      uint32_t *d_status, void *stream)
 {
     AP_NVTX_RANGE("ap_expert_linear");
     using namespace ap;
@@ -1129,13 +1120,14 @@ extern "C" ap_status ap_expert_linear(const void *x, int64_t ldx, int64_t rows, 
     a.seg = d_seg_off, a.live = d_live, a.bias = bias, a.residual = (const bf16_t *)residual, a.pre = (bf16_t *)pre, a.out = out;
     a.ldres = ldres, a.ldpre = ldpre, a.ldo = ldo, a.d_status = d_status, a.rows = rows, a.E = E, a.F = N, a.K = K, a.act = act;
     a.out_f32 = out_dtype == AP_DTYPE_F32;
-    return rows_product(who, kForward, a, halves, (cudaStream_t)stream);
+    return rows_product(who, kForward, a, halves, scratch, scratch_bytes, (cudaStream_t)stream);
 }
 
 extern "C" ap_status ap_expert_linear_dx(const void *dy, int64_t ldy, int64_t rows, int32_t E, int32_t N, int32_t K,
                                          const int32_t *d_seg_off, const int32_t *d_live, const void *W, int64_t ldw, int64_t lde,
                                          int32_t act, const void *pre, int64_t ldpre, const void *residual, int64_t ldres, void *dx,
-                                         int64_t ldx, int32_t dx_dtype, uint32_t *d_status, void *stream)
+                                         int64_t ldx, int32_t dx_dtype, void *scratch, int64_t scratch_bytes, uint32_t *d_status,
+                                         void *stream)
 {
     AP_NVTX_RANGE("ap_expert_linear_dx");
     using namespace ap;
@@ -1158,12 +1150,13 @@ extern "C" ap_status ap_expert_linear_dx(const void *dy, int64_t ldy, int64_t ro
     a.pre = const_cast<bf16_t *>((const bf16_t *)pre);
     a.ldres = ldres, a.ldpre = ldpre, a.ldo = ldx, a.d_status = d_status, a.rows = rows, a.E = E, a.F = K, a.K = N, a.act = act;
     a.out_f32 = dx_dtype == AP_DTYPE_F32;
-    return rows_product(who, kRows, a, halves, (cudaStream_t)stream);
+    return rows_product(who, kRows, a, halves, scratch, scratch_bytes, (cudaStream_t)stream);
 }
 
 extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void *x, int64_t ldx, int64_t rows, int32_t E, int32_t N,
                                          int32_t K, const int32_t *d_seg_off, const int32_t *d_live, int32_t accumulate, void *dW,
-                                         int32_t dw_dtype, float *dbias, uint32_t *d_status, void *stream)
+                                         int32_t dw_dtype, float *dbias, void *scratch, int64_t scratch_bytes, uint32_t *d_status,
+                                         void *stream)
 {
     AP_NVTX_RANGE("ap_expert_linear_dw");
     using namespace ap;
@@ -1180,9 +1173,11 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
         a.x = (const bf16_t *)dy, a.W = (const bf16_t *)x, a.ldx = ldy, a.ldw = ldx;
         a.seg = d_seg_off, a.live = d_live, a.out = dW, a.d_status = d_status, a.rows = rows, a.E = E, a.F = N, a.K = K;
         a.out_f32 = dw_dtype == AP_DTYPE_F32, a.add = accumulate != 0;
-        a.x_end = reinterpret_cast<const char *>(a.x + (rows - 1) * ldy + N);
-        a.W_end = reinterpret_cast<const char *>(a.W + (rows - 1) * ldx + K);
-        const bool maps = rows > 0 && mappable(dy, ldy) && mappable(x, ldx);
+        if (rows > 0) {
+            Repitch re = {who, scratch, scratch_bytes, st};
+            if (const ap_status r = re.take(&a.x, &a.ldx, nullptr, rows, 1, N, nullptr); r != AP_OK) return r;
+            if (const ap_status r = re.take(&a.W, &a.ldw, nullptr, rows, 1, K, nullptr); r != AP_OK) return r;
+        }
         a.columns = K > 128 ? 256 : K > 64 ? 128 : 64;
         a.tiles_f = (N + kLanes - 1) / kLanes;
         auto tiles_of = [&] { return (int64_t)E * a.tiles_f * ((K + a.columns - 1) / a.columns); };
@@ -1191,22 +1186,18 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
         const int64_t tiles = tiles_of();
         if (tiles >= INT32_MAX) return fail(AP_EINVAL, "%s: %lld tiles are more than one launch takes", who, (long long)tiles);
         ExMaps m = {};
-        ap_status s;
-        if (maps) {
+        if (rows > 0) {
             // two chunks of 64 columns in a copy where rows are whole chunks: a row's end is no border to such a map
             a.chunk_x = N % 64 == 0, a.chunk_w = K % 64 == 0;
-            const uint64_t ey[3] = {a.chunk_x ? 64 : (uint64_t)N, (uint64_t)rows, (uint64_t)N / 64}, py[2] = {(uint64_t)ldy, 64};
-            const uint64_t ex[3] = {a.chunk_w ? 64 : (uint64_t)K, (uint64_t)rows, (uint64_t)K / 64}, px[2] = {(uint64_t)ldx, 64};
+            const uint64_t ey[3] = {a.chunk_x ? 64 : (uint64_t)N, (uint64_t)rows, (uint64_t)N / 64}, py[2] = {(uint64_t)a.ldx, 64};
+            const uint64_t ex[3] = {a.chunk_w ? 64 : (uint64_t)K, (uint64_t)rows, (uint64_t)K / 64}, px[2] = {(uint64_t)a.ldw, 64};
             const uint32_t box[3] = {64, 64, 2};
             const uint64_t e1[2] = {(uint64_t)N, (uint64_t)rows}, e2[2] = {(uint64_t)K, (uint64_t)rows};
-            if (!make_map(&m.x, dy, 2, e1, py, box) || !make_map(&m.w, x, 2, e2, px, box) ||
-                (a.chunk_x && !make_map(&m.xx, dy, 3, ey, py, box)) || (a.chunk_w && !make_map(&m.ww, x, 3, ex, px, box)))
+            if (!make_map(&m.x, a.x, 2, e1, py, box) || !make_map(&m.w, a.W, 2, e2, px, box) ||
+                (a.chunk_x && !make_map(&m.xx, a.x, 3, ey, py, box)) || (a.chunk_w && !make_map(&m.ww, a.W, 3, ex, px, box)))
                 return fail(AP_ENOTSUP, "%s: no tensor map of these sizes", who);
-            s = launch_experts<kWeights, true>(who, m, a, tiles, st);
-        } else {
-            s = launch_experts<kWeights, false>(who, m, a, tiles, st);
         }
-        if (s != AP_OK) return s;
+        if (const ap_status s = launch_experts<kWeights>(who, m, a, tiles, st); s != AP_OK) return s;
     }
     if (dbias) {
         launch(k_expert_bias, dim3((unsigned)((N + 63) / 64), (unsigned)E), 256, 0, st, (const bf16_t *)dy, ldy, d_seg_off, d_live, rows,

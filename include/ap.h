@@ -383,18 +383,27 @@ ap_status ap_route_bias_step(float *bias, int32_t *counts, int32_t E, float rate
  *   residual [rows, N] bf16, ldres apart (device, read) or NULL; may be out
  *   pre      [rows, N] ([rows, 2 N]) bf16, ldpre apart (device, written) or NULL
  *   out      [rows, N] of out_dtype (BF16 or F32), ldo apart (device, written)
- * Limits: 0 <= rows < 2^31, 1 <= E <= 1024, 1 <= N, K <= 2^20.  Bases of x and W
- * on 16 bytes and pitches that are multiples of 8 elements are many times
- * faster than others.
+ *   scratch  device work space of ap_expert_linear_scratch_bytes() bytes, 16-byte
+ *            aligned; its contents need no initialisation.  Operands whose bases
+ *            lie on 16 bytes and whose pitches are multiples of 8 elements need 0
+ *            bytes (NULL); others are copied to such rows first
+ * Limits: 0 <= rows < 2^31, 1 <= E <= 1024, 1 <= N, K <= 2^20.
  * ========================================================================== */
 #define AP_ACT_NONE 0
 #define AP_ACT_SILU 1
 #define AP_ACT_GELU 2
 #define AP_ACT_SWIGLU 3
+/* The work space of a call by its two BF16 operands: a of rows_a rows of cols_a
+ * values, lda apart, and b likewise, whose experts lie lde apart (0 for rows):
+ * (x, W with E N (SWIGLU: E 2 N) rows) forwards, (dy, W) for the rows' gradient,
+ * (dy, x) for the weights'.  The addresses are not read. */
+ap_status ap_expert_linear_scratch_bytes(const void *a, int64_t lda, int64_t rows_a, int32_t cols_a, const void *b, int64_t ldb,
+                                         int64_t lde, int64_t rows_b, int32_t cols_b, int64_t *bytes);
 ap_status ap_expert_linear(const void *x, int64_t ldx, int64_t rows, int32_t E, int32_t N, int32_t K,
                            const int32_t *d_seg_off, const int32_t *d_live, const void *W, int64_t ldw, int64_t lde,
                            const float *bias, int32_t act, const void *residual, int64_t ldres, void *pre, int64_t ldpre,
-                           void *out, int64_t ldo, int32_t out_dtype, uint32_t *d_status, void *stream);
+                           void *out, int64_t ldo, int32_t out_dtype, void *scratch, int64_t scratch_bytes,
+                           uint32_t *d_status, void *stream);
 
 /* Gradient of the rows: for each row r of expert e
  *   d[r]  = dy[r] W[e] + residual[r]                 (K columns)
@@ -414,7 +423,8 @@ ap_status ap_expert_linear(const void *x, int64_t ldx, int64_t rows, int32_t E, 
 ap_status ap_expert_linear_dx(const void *dy, int64_t ldy, int64_t rows, int32_t E, int32_t N, int32_t K,
                               const int32_t *d_seg_off, const int32_t *d_live, const void *W, int64_t ldw, int64_t lde,
                               int32_t act, const void *pre, int64_t ldpre, const void *residual, int64_t ldres, void *dx,
-                              int64_t ldx, int32_t dx_dtype, uint32_t *d_status, void *stream);
+                              int64_t ldx, int32_t dx_dtype, void *scratch, int64_t scratch_bytes, uint32_t *d_status,
+                              void *stream);
 
 /* Gradients of weights and bias:
  *   dW[e] = sum over rows r of expert e of dy[r]^T x[r]    dbias[e] = sum dy[r]
@@ -426,7 +436,8 @@ ap_status ap_expert_linear_dx(const void *dy, int64_t ldy, int64_t rows, int32_t
  * Segments, limits and the rest as ap_expert_linear. */
 ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void *x, int64_t ldx, int64_t rows, int32_t E, int32_t N,
                               int32_t K, const int32_t *d_seg_off, const int32_t *d_live, int32_t accumulate, void *dW,
-                              int32_t dw_dtype, float *dbias, uint32_t *d_status, void *stream);
+                              int32_t dw_dtype, float *dbias, void *scratch, int64_t scratch_bytes, uint32_t *d_status,
+                              void *stream);
 
 /* ============================================================================
  * embed

@@ -112,9 +112,9 @@ def test_adamw_moments_refusals(lib):
 
 def test_expert_linear_refusals(lib):
     def fwd(x=P, ldx=64, rows=100, E=4, N=32, K=64, seg=P, live=P, W=P, ldw=64, lde=64 * 64, bias=None, act=0, res=None, ldr=32,
-            pre=None, ldp=32, out=P, ldo=32, dt=0):
-        return lib.ap_expert_linear(x, ldx, rows, E, N, K, seg, live, W, ldw, lde, bias, act, res, ldr, pre, ldp, out, ldo, dt, None,
-                                    None)
+            pre=None, ldp=32, out=P, ldo=32, dt=0, scratch=None, sb=0):
+        return lib.ap_expert_linear(x, ldx, rows, E, N, K, seg, live, W, ldw, lde, bias, act, res, ldr, pre, ldp, out, ldo, dt, scratch,
+                                    sb, None, None)
     odd, half = ctypes.c_void_p(4097), ctypes.c_void_p(4098)
     n0 = lib.ap_launch_count()
     for bad in (dict(rows=-1), dict(rows=2 ** 31), dict(E=0), dict(E=1025), dict(N=0), dict(K=0), dict(N=2 ** 20 + 1), dict(K=2 ** 21),
@@ -124,16 +124,31 @@ def test_expert_linear_refusals(lib):
                 dict(dt=2, out=half), dict(rows=2 ** 31 - 1, N=2 ** 20, ldo=2 ** 20, lde=2 ** 27, ldw=64)):
         assert fwd(**bad) == -1, bad
     assert fwd(rows=0, x=None, out=None) == 0
+    # operands off the 16-byte boundaries need work space
+    n = ctypes.c_int64(-1)
+    assert lib.ap_expert_linear_scratch_bytes(P, 64, 100, 64, P, 64, 4096, 128, 64, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.ap_expert_linear_scratch_bytes(P, 65, 100, 63, P, 64, 4096, 128, 64, ctypes.byref(n)) == 0
+    assert n.value == 100 * 128
+    assert lib.ap_expert_linear_scratch_bytes(half, 64, 100, 64, P, 64, 4097, 128, 63, ctypes.byref(n)) == 0
+    assert n.value == 100 * 128 + 128 * 128
+    assert lib.ap_expert_linear_scratch_bytes(P, 64, -1, 64, P, 64, 0, 128, 64, ctypes.byref(n)) == -1
+    assert lib.ap_expert_linear_scratch_bytes(P, 64, 1, 0, P, 64, 0, 128, 64, ctypes.byref(n)) == -1
+    assert lib.ap_expert_linear_scratch_bytes(P, 64, 1, 64, P, 64, 0, 128, 64, None) == -1
+    for bad in (dict(x=half), dict(ldx=65), dict(W=half), dict(ldw=65, lde=4224), dict(x=half, scratch=P, sb=100 * 128 - 1),
+                dict(x=half, scratch=ctypes.c_void_p(4104), sb=100 * 128)):
+        assert fwd(**bad) == -1, bad
+        assert b"scratch" in lib.ap_last_error()
 
     def dx(dy=P, ldy=32, rows=100, E=4, N=32, K=64, seg=P, live=P, W=P, ldw=64, lde=32 * 64, act=0, pre=None, ldp=64, res=None, ldr=64,
            out=P, ldo=64, dt=0):
-        return lib.ap_expert_linear_dx(dy, ldy, rows, E, N, K, seg, live, W, ldw, lde, act, pre, ldp, res, ldr, out, ldo, dt, None, None)
+        return lib.ap_expert_linear_dx(dy, ldy, rows, E, N, K, seg, live, W, ldw, lde, act, pre, ldp, res, ldr, out, ldo, dt, None, 0,
+                                       None, None)
     for bad in (dict(rows=-1), dict(E=0), dict(ldy=31), dict(ldw=63), dict(lde=30 * 64), dict(act=1), dict(act=3, pre=P, ldp=127, ldo=128),
                 dict(act=3, pre=P, ldp=128), dict(res=P, ldr=63), dict(dt=1), dict(dy=None), dict(out=None), dict(act=9)):
         assert dx(**bad) == -1, bad
 
     def dw(dy=P, ldy=32, x=P, ldx=64, rows=100, E=4, N=32, K=64, seg=P, live=P, add=0, dW=P, dt=2, db=None):
-        return lib.ap_expert_linear_dw(dy, ldy, x, ldx, rows, E, N, K, seg, live, add, dW, dt, db, None, None)
+        return lib.ap_expert_linear_dw(dy, ldy, x, ldx, rows, E, N, K, seg, live, add, dW, dt, db, None, 0, None, None)
     for bad in (dict(rows=-1), dict(E=1025), dict(ldy=31), dict(ldx=63), dict(add=2), dict(dt=1), dict(dW=None), dict(dy=None),
                 dict(x=None), dict(seg=None), dict(live=None), dict(dW=half), dict(db=half), dict(x=odd)):
         assert dw(**bad) == -1, bad
