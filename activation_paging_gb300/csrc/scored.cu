@@ -11,10 +11,12 @@
 // Choices that are near one another in single precision are not settled there:
 // where the order of two that matter (neighbours among the k, the border behind
 // them, the border between groups) lies within the error bounds below, the
-// token is chosen again in double precision (choose_exactly), about one token
+// few experts in question are compared in double precision, for about one token
 // in a thousand.  So ids do not depend on how single precision rounds.  Without
 // a bias, and with groups that go by their best expert, the logits themselves
-// have the scores' order and nothing is near.
+// have the scores' order and nothing is near.  (All of a row's choices in double
+// precision, 8 exponentials a lane one after the other, made the slowest warp
+// take 25 us longer.)
 //
 // Backward.  With q the chosen scores and u_j = dw_j - sum_i w_i dw_i / scale:
 //   sigmoid, renormalised   dl_j = scale q_j / S (1 - sigma_j) u_j
@@ -91,88 +93,159 @@ template <typename F> struct Best2 {
     }
 };
 
-// Which groups are in: bit (g * lanes) of the result is set for group g.  `row`
-// holds the warp's choices; every group has `lanes` lanes.  *near: the border
-// between the groups lies within the errors.
-template <typename F>
-__device__ __forceinline__ uint32_t choose_groups(const F *row, const ScoredArgs &a, int lane, int lanes, float p_top,
-                                                  bool *near)
+// The choice in double precision of an expert with logit x and bias b.  Without
+// a bias softmax values keep their order undivided by the row's sum.
+__device__ __noinline__ double exact_choice(bool sigmoid, bool biased, float x, float b, float top, double sum)
 {
-    const int g = lane / lanes, sub = lane - g * lanes;
-    Best2<F> b = {(F)-INFINITY, (F)-INFINITY};
+    double c = sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)top);
+    if (biased) c = (sigmoid ? c : c / sum) + (double)b;
+    return c == c && x > -INFINITY ? c : -INFINITY;
+}
+__device__ __noinline__ double exact_sum(const float *logits, int E, float top)
+{
+    double sum = 0.0;
+    for (int i = (int)lane_id(); i < E; i += kWarp) sum += exp((double)logits[i] - (double)top);
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    return sum;
+}
+// What exact comparisons of a token need.
+struct Exact {
+    const ScoredArgs &a;
+    const float *logits;
+    float top;
+    double sum;
+    __device__ __forceinline__ Exact(const ScoredArgs &args, int64_t t, float row_top)
+        : a(args), logits(args.logits + t * args.E), top(row_top), sum(1.0)
+    {
+        if (!a.sigmoid && a.bias) sum = exact_sum(logits, a.E, top);
+    }
+    __device__ __forceinline__ double of(int e) const
+    {
+        return exact_choice(a.sigmoid, a.bias != nullptr, logits[e], a.bias ? a.bias[e] : 0.f, top, sum);
+    }
+};
+
+// Which groups are in: bit g of the result is set for group g.  `row` holds the
+// warp's choices; every group has `lanes` lanes.
+__device__ __forceinline__ uint32_t choose_groups(const float *row, const ScoredArgs &a, int64_t t, int lane, int lanes, float top,
+                                                  float p_top, bool direct)
+{
+    const int g = lane / lanes, sub = lane - g * lanes; // (lanes is a power of two)
+    Best2<float> b = {-INFINITY, -INFINITY};
     if (g < a.groups) {
         // the groups begin at different places of theirs, so that groups of 32 experts meet different banks
         const int n = (a.size - sub + lanes - 1) / lanes;
-        int i = n > 0 ? g % n : 0;
+        int i = g < n ? g : 0;
         for (int c = 0; c < n; ++c) {
             b.take(row[g * a.size + sub + i * lanes]);
             if (++i == n) i = 0;
         }
     }
     for (int off = 1; off < lanes; off <<= 1) {
-        const F o1 = __shfl_xor_sync(0xffffffffu, b.first, off), o2 = __shfl_xor_sync(0xffffffffu, b.second, off);
+        const float o1 = __shfl_xor_sync(0xffffffffu, b.first, off), o2 = __shfl_xor_sync(0xffffffffu, b.second, off);
         b.take(o1);
         b.take(o2);
     }
-    F score = a.best == 2 ? b.first + b.second : b.first;
-    if (!(score == score)) score = (F)-INFINITY;
+    float score = a.best == 2 ? b.first + b.second : b.first;
+    if (!(score == score)) score = -INFINITY;
+    // lane g takes over group g's
+    const int from = lane < a.groups ? lane * lanes : 0;
+    score = __shfl_sync(0xffffffffu, score, from);
     int rank = 0;
     for (int h = 0; h < a.groups; ++h) {
-        const F o = __shfl_sync(0xffffffffu, score, h * lanes);
-        rank += o > score || (o == score && h < g);
+        const float o = __shfl_sync(0xffffffffu, score, h);
+        rank += o > score || (o == score && h < lane);
     }
-    const bool in = g < a.groups && rank < a.top_groups;
-    if (near) {
-        float err = a.best == 2 ? near_of(a.sigmoid, p_top, (float)b.first) + near_of(a.sigmoid, p_top, (float)b.second)
-                                : near_of(a.sigmoid, p_top, (float)b.first);
+    const bool is = lane < a.groups;
+    bool in = is && rank < a.top_groups;
+    if (!direct) {
+        const float first = __shfl_sync(0xffffffffu, b.first, from), second = __shfl_sync(0xffffffffu, b.second, from);
+        float err = near_of(a.sigmoid, p_top, first) + (a.best == 2 ? near_of(a.sigmoid, p_top, second) : 0.f);
         if (!(err < INFINITY)) err = 0.f; // of -infinity: nothing rounds
-        const float least = -reduce_max(in ? -((float)score - err) : -INFINITY);
-        const float most = reduce_max(g < a.groups && !in ? (float)score + err : -INFINITY);
-        *near = most >= least && most > -INFINITY;
+        const float least = -reduce_max(in ? err - score : -INFINITY), most = reduce_max(is && !in ? score + err : -INFINITY);
+        if (most >= least && most > -INFINITY) {
+            // groups at the border, by the exact sums of those experts that may be among their best
+            const bool open = is && (in ? score - err <= most : score + err >= least);
+            const uint32_t opens = __ballot_sync(0xffffffffu, open);
+            const Exact x(a, t, top);
+            double mine = -INFINITY;
+            for (uint32_t left = opens; left; left &= left - 1) {
+                const int h = __ffs(left) - 1;
+                float low = __shfl_sync(0xffffffffu, a.best == 2 ? second : first, h);
+                low -= near_of(a.sigmoid, p_top, low); // (-infinity: all)
+                Best2<double> d = {-INFINITY, -INFINITY};
+                for (int i = lane; i < a.size; i += kWarp) {
+                    const float v = row[h * a.size + i];
+                    if (v > -INFINITY && !(v < low)) d.take(x.of(h * a.size + i));
+                }
+                for (int off = 1; off < kWarp; off <<= 1) {
+                    const double o1 = __shfl_xor_sync(0xffffffffu, d.first, off), o2 = __shfl_xor_sync(0xffffffffu, d.second, off);
+                    d.take(o1);
+                    d.take(o2);
+                }
+                if (lane == h) mine = a.best == 2 ? d.first + d.second : d.first;
+            }
+            int place = 0;
+            for (uint32_t left = opens; left; left &= left - 1) {
+                const int h = __ffs(left) - 1;
+                const double o = __shfl_sync(0xffffffffu, mine, h);
+                place += o > mine || (o == mine && h < lane);
+            }
+            const int room = a.top_groups - __popc(__ballot_sync(0xffffffffu, in && !open));
+            if (open) in = place < room;
+        }
     }
     return __ballot_sync(0xffffffffu, in);
 }
 
-// The choice in double precision: the row's scores anew, the groups, then k
-// rounds over the warp's choices in shared memory.  Lane j < k receives the
-// j-th id, and whether it may be chosen at all.
-__device__ __noinline__ void choose_exactly(const ScoredArgs &a, int64_t t, double *row, int lanes, bool odd, int *e,
-                                            bool *in)
+// The choice among the experts that `row` (the warp's choices) puts at or above
+// `low`, in double precision: n <= 32 of them, a lane each.
+__device__ __noinline__ void choose_few(const ScoredArgs &a, int64_t t, float top, const float *row, float low, int n, int *list, int *e)
 {
     const int lane = (int)lane_id();
-    const float *logits = a.logits + t * a.E;
-    double top = 0.0, inv = 0.0;
-    if (!a.sigmoid) {
-        float m = -INFINITY;
-        for (int i = lane; i < a.E; i += kWarp) m = fmaxf(m, logits[i]);
-        m = reduce_max(m);
-        top = m;
-        double sum = 0.0;
-        for (int i = lane; i < a.E; i += kWarp) sum += exp((double)logits[i] - top);
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        inv = sum;
-    }
-    for (int i = lane; i < a.E; i += kWarp) {
-        const double x = logits[i];
-        double c = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / inv;
-        if (a.bias) c += (double)a.bias[i];
-        if (!(c == c) || x == -INFINITY || odd) c = -INFINITY;
-        row[i] = c;
+    int at = 0;
+    for (int i0 = 0; i0 < a.E; i0 += kWarp) {
+        const bool on = i0 + lane < a.E && row[i0 + lane] >= low;
+        const uint32_t who = __ballot_sync(0xffffffffu, on);
+        if (on) list[at + __popc(who & lanemask_lt())] = i0 + lane;
+        at += __popc(who);
     }
     __syncwarp();
-    uint32_t keep = 0xffffffffu;
-    if (a.groups > 1) keep = choose_groups<double>(row, a, lane, lanes, 0.f, nullptr);
+    const Exact x(a, t, top);
+    const int mine = lane < n ? list[lane] : -1;
+    const double c = lane < n ? x.of(mine) : -INFINITY;
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+        const double o = __shfl_sync(0xffffffffu, c, j);
+        rank += o > c || (o == c && j < lane); // (the list rises)
+    }
     __syncwarp();
-    if (a.groups > 1)
-        for (int i = lane; i < a.E; i += kWarp)
-            if (!(keep >> ((uint32_t)i * a.inv_size >> 20) * lanes & 1)) row[i] = -INFINITY;
+    if (lane < n) list[rank] = mine;
     __syncwarp();
+    if (lane < a.k) *e = list[lane];
+}
+
+// The same where more are at the border: the row's choices anew in double
+// precision, k rounds over them.  Lane j < k receives the j-th id.
+__device__ __noinline__ void choose_many(const ScoredArgs &a, int64_t t, float top, double *wide, const float *row, int *e)
+{
+    const int lane = (int)lane_id();
+    const Exact x(a, t, top);
+    // from the end, as the row lies in the same memory
+    for (int i0 = (a.E - 1) / kWarp * kWarp; i0 >= 0; i0 -= kWarp) {
+        const int i = i0 + lane;
+        const float v = i < a.E ? row[i] : -INFINITY;
+        const double c = v > -INFINITY ? x.of(i) : -INFINITY;
+        __syncwarp();
+        if (i < a.E) wide[i] = c;
+        __syncwarp();
+    }
     for (int j = 0; j < a.k; ++j) {
         double best = -INFINITY;
         int at = kNoExpert; // a chosen expert's place holds NaN
         for (int i = lane; i < a.E; i += kWarp)
-            if (row[i] > best || (row[i] == best && i < at)) {
-                best = row[i];
+            if (wide[i] > best || (wide[i] == best && i < at)) {
+                best = wide[i];
                 at = i;
             }
         for (int off = 16; off > 0; off >>= 1) {
@@ -183,12 +256,9 @@ __device__ __noinline__ void choose_exactly(const ScoredArgs &a, int64_t t, doub
                 at = oa;
             }
         }
-        if (lane == j) {
-            *e = at;
-            *in = best > -INFINITY;
-        }
+        if (lane == j) *e = at;
         __syncwarp();
-        if (at % kWarp == lane) row[at] = NAN;
+        if (at % kWarp == lane) wide[at] = NAN;
         __syncwarp();
     }
 }
@@ -204,7 +274,7 @@ __device__ __forceinline__ float score_of(bool sigmoid, float l, float shift)
 
 // Lane l holds the vectors l, l + 32, ... of VEC experts each (N of them).
 template <int VEC, int N>
-__global__ void __launch_bounds__(kScThreads) k_route_scored(ScoredArgs a)
+__global__ void __launch_bounds__(kScThreads, VEC * N <= 8 ? 4 : VEC * N <= 16 ? 2 : 1) k_route_scored(ScoredArgs a)
 {
     pdl_begin();
     using Vec = typename ScVec<VEC>::T;
@@ -282,8 +352,7 @@ __global__ void __launch_bounds__(kScThreads) k_route_scored(ScoredArgs a)
 #pragma unroll
                 for (int c = 0; c < VEC; ++c) v[i][c] = -INFINITY;
         }
-        bool near = false;
-        if (a.groups > 1) {
+        const auto row_store = [&] {
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 if (lane + kWarp * i < nvec) {
@@ -292,34 +361,38 @@ __global__ void __launch_bounds__(kScThreads) k_route_scored(ScoredArgs a)
                     reinterpret_cast<Vec *>(row)[lane + kWarp * i] = x;
                 }
             __syncwarp();
-            const uint32_t keep = choose_groups<float>(row, a, lane, lanes, inv, direct ? nullptr : &near);
+        };
+        if (a.groups > 1) {
+            row_store();
+            const uint32_t keep = choose_groups(row, a, t, lane, lanes, top, inv, direct);
 #pragma unroll
             for (int i = 0; i < N; ++i)
 #pragma unroll
                 for (int c = 0; c < VEC; ++c) {
                     const uint32_t e = (lane + kWarp * i) * VEC + c;
-                    if (e < (uint32_t)E && !(keep >> (e * a.inv_size >> 20) * lanes & 1)) v[i][c] = -INFINITY;
+                    if (e < (uint32_t)E && !(keep >> (e * a.inv_size >> 20) & 1)) v[i][c] = -INFINITY;
                 }
+            __syncwarp();
         }
         int e;
         float value, first;
-        bool in;
         choose_token_slots<VEC, N>(v, E, k, lane, s_slots[wid], &e, &value, &first);
-        in = value > -INFINITY;
-        if (!direct && !near) {
+        const float last = __shfl_sync(0xffffffffu, value, k - 1);
+        // (chosen with a choice of -infinity: none of those that may be chosen)
+        const bool in = lane < k && value > -INFINITY;
+        if (!direct) {
             // neighbours among the chosen, and what lies at the last one's border
             const float before = __shfl_up_sync(0xffffffffu, value, 1);
-            const float margin = near_of(a.sigmoid, inv, value);
-            bool close = lane > 0 && lane < k && in && before - value <= margin;
-            const float last = __shfl_sync(0xffffffffu, value, k - 1);
-            const float band = near_of(a.sigmoid, inv, last);
+            bool close = lane > 0 && in && before - value <= near_of(a.sigmoid, inv, value);
+            // (fewer than k that may be chosen: there is no border behind them)
+            const float low = last > -INFINITY ? last - near_of(a.sigmoid, inv, last) : -FLT_MAX;
             int upto = 0;
 #pragma unroll
             for (int i = 0; i < N; ++i)
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) upto += v[i][c] >= last - band;
+                for (int c = 0; c < VEC; ++c) upto += v[i][c] >= low;
             upto = __reduce_add_sync(0xffffffffu, upto);
-            const bool border = last > -INFINITY && upto > k;
+            const bool border = upto > k;
             if (__any_sync(0xffffffffu, close) || border) {
                 // equal logits with equal biases have equal choices, whatever the rounding: the lower id is first
                 const float *l = a.logits + t * E;
@@ -333,18 +406,26 @@ __global__ void __launch_bounds__(kScThreads) k_route_scored(ScoredArgs a)
 #pragma unroll
                         for (int c = 0; c < VEC; ++c) {
                             const int x = (lane + kWarp * i) * VEC + c;
-                            if (v[i][c] >= last - band && v[i][c] <= last + band)
+                            if (v[i][c] >= low && v[i][c] <= last + (last - low))
                                 close |= !(l[x] == ll && (!a.bias || a.bias[x] == bl));
                         }
                 }
-                near = __any_sync(0xffffffffu, close);
+                if (__any_sync(0xffffffffu, close)) { // (warp-uniform)
+                    __syncwarp();
+                    row_store();
+                    // those that may be chosen keep their places in front of those that may not
+                    int again = e;
+                    if (upto <= kWarp)
+                        choose_few(a, t, top, row, low, upto, reinterpret_cast<int *>(&s_slots[wid]), &again);
+                    else
+                        choose_many(a, t, top, row64, row, &again);
+                    if (in) e = again;
+                }
             }
         }
         __syncwarp(); // the row and the slots are free
-        if (near) choose_exactly(a, t, row64, lanes, odd, &e, &in);
         // weights
         const float l = lane < k ? a.logits[t * E + e] : -INFINITY;
-        in = in && lane < k;
         float wt = 0.f;
         if (odd) {
             wt = NAN;
