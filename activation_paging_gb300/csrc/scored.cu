@@ -42,6 +42,7 @@ struct ScoredArgs {
     int64_t T;
     int E, k;
     int groups, size, top_groups, best; // size: experts of a group
+    int shift;                          // groups of 4 << shift experts, as long as a warp's lanes hold one; else -1
     uint32_t inv_size;                  // ceil(2^20 / size): e / size = e * inv_size >> 20 for e < 1024
     float scale;
     bool sigmoid, renorm;
@@ -125,12 +126,33 @@ struct Exact {
     }
 };
 
-// Which groups are in: bit g of the result is set for group g.  `row` holds the
-// warp's choices; every group has `lanes` lanes.
-__device__ __forceinline__ uint32_t choose_groups(const float *row, const ScoredArgs &a, int64_t t, int lane, int lanes, float top,
-                                                  float p_top, bool direct)
+// The score of a group by its best experts, and how far single precision may be off.
+struct GroupScore {
+    float score, err;
+};
+__device__ __forceinline__ GroupScore group_score(const ScoredArgs &a, const Best2<float> &b, float p_top)
 {
-    const int g = lane / lanes, sub = lane - g * lanes; // (lanes is a power of two)
+    GroupScore g;
+    g.score = a.best == 2 ? b.first + b.second : b.first;
+    if (!(g.score == g.score)) g.score = -INFINITY;
+    g.err = near_of(a.sigmoid, p_top, b.first) + (a.best == 2 ? near_of(a.sigmoid, p_top, b.second) : 0.f);
+    if (!(g.err < INFINITY)) g.err = 0.f; // of -infinity: nothing rounds
+    return g;
+}
+__device__ __forceinline__ void best_of_lanes(Best2<float> &b, int from, int to) // over lanes that differ in these bits
+{
+    for (int off = from; off < to; off <<= 1) {
+        const float o1 = __shfl_xor_sync(0xffffffffu, b.first, off), o2 = __shfl_xor_sync(0xffffffffu, b.second, off);
+        b.second = fmaxf(fminf(b.first, o1), fmaxf(b.second, o2));
+        b.first = fmaxf(b.first, o1);
+    }
+}
+
+// Lane g's score of group g from the warp's choices in shared memory; every
+// group has `lanes` lanes (a power of two).
+__device__ __forceinline__ GroupScore scan_groups(const float *row, const ScoredArgs &a, int lane, int lanes, float p_top)
+{
+    const int g = lane / lanes, sub = lane - g * lanes;
     Best2<float> b = {-INFINITY, -INFINITY};
     if (g < a.groups) {
         // the groups begin at different places of theirs, so that groups of 32 experts meet different banks
@@ -141,61 +163,41 @@ __device__ __forceinline__ uint32_t choose_groups(const float *row, const Scored
             if (++i == n) i = 0;
         }
     }
-    for (int off = 1; off < lanes; off <<= 1) {
-        const float o1 = __shfl_xor_sync(0xffffffffu, b.first, off), o2 = __shfl_xor_sync(0xffffffffu, b.second, off);
-        b.take(o1);
-        b.take(o2);
-    }
-    float score = a.best == 2 ? b.first + b.second : b.first;
-    if (!(score == score)) score = -INFINITY;
-    // lane g takes over group g's
+    best_of_lanes(b, 1, lanes);
+    GroupScore s = group_score(a, b, p_top);
     const int from = lane < a.groups ? lane * lanes : 0;
-    score = __shfl_sync(0xffffffffu, score, from);
-    int rank = 0;
-    for (int h = 0; h < a.groups; ++h) {
-        const float o = __shfl_sync(0xffffffffu, score, h);
-        rank += o > score || (o == score && h < lane);
-    }
-    const bool is = lane < a.groups;
-    bool in = is && rank < a.top_groups;
-    if (!direct) {
-        const float first = __shfl_sync(0xffffffffu, b.first, from), second = __shfl_sync(0xffffffffu, b.second, from);
-        float err = near_of(a.sigmoid, p_top, first) + (a.best == 2 ? near_of(a.sigmoid, p_top, second) : 0.f);
-        if (!(err < INFINITY)) err = 0.f; // of -infinity: nothing rounds
-        const float least = -reduce_max(in ? err - score : -INFINITY), most = reduce_max(is && !in ? score + err : -INFINITY);
-        if (most >= least && most > -INFINITY) {
-            // groups at the border, by the exact sums of those experts that may be among their best
-            const bool open = is && (in ? score - err <= most : score + err >= least);
-            const uint32_t opens = __ballot_sync(0xffffffffu, open);
-            const Exact x(a, t, top);
-            double mine = -INFINITY;
-            for (uint32_t left = opens; left; left &= left - 1) {
-                const int h = __ffs(left) - 1;
-                float low = __shfl_sync(0xffffffffu, a.best == 2 ? second : first, h);
-                low -= near_of(a.sigmoid, p_top, low); // (-infinity: all)
-                Best2<double> d = {-INFINITY, -INFINITY};
-                for (int i = lane; i < a.size; i += kWarp) {
-                    const float v = row[h * a.size + i];
-                    if (v > -INFINITY && !(v < low)) d.take(x.of(h * a.size + i));
-                }
-                for (int off = 1; off < kWarp; off <<= 1) {
-                    const double o1 = __shfl_xor_sync(0xffffffffu, d.first, off), o2 = __shfl_xor_sync(0xffffffffu, d.second, off);
-                    d.take(o1);
-                    d.take(o2);
-                }
-                if (lane == h) mine = a.best == 2 ? d.first + d.second : d.first;
-            }
-            int place = 0;
-            for (uint32_t left = opens; left; left &= left - 1) {
-                const int h = __ffs(left) - 1;
-                const double o = __shfl_sync(0xffffffffu, mine, h);
-                place += o > mine || (o == mine && h < lane);
-            }
-            const int room = a.top_groups - __popc(__ballot_sync(0xffffffffu, in && !open));
-            if (open) in = place < room;
+    s.score = __shfl_sync(0xffffffffu, s.score, from);
+    s.err = __shfl_sync(0xffffffffu, s.err, from);
+    return s;
+}
+
+// The exact scores of the groups `opens`, lane g of group g: by those experts
+// that may be among their best.
+__device__ __noinline__ double exact_groups(const ScoredArgs &a, int64_t t, const float *row, float top, float p_top, uint32_t opens)
+{
+    const int lane = (int)lane_id();
+    const Exact x(a, t, top);
+    double mine = -INFINITY;
+    for (uint32_t left = opens; left; left &= left - 1) {
+        const int h = __ffs(left) - 1;
+        Best2<float> b = {-INFINITY, -INFINITY};
+        for (int i = lane; i < a.size; i += kWarp) b.take(row[h * a.size + i]);
+        best_of_lanes(b, 1, kWarp);
+        float low = a.best == 2 ? b.second : b.first;
+        low -= near_of(a.sigmoid, p_top, low); // (-infinity: all)
+        Best2<double> d = {-INFINITY, -INFINITY};
+        for (int i = lane; i < a.size; i += kWarp) {
+            const float v = row[h * a.size + i];
+            if (v > -INFINITY && !(v < low)) d.take(x.of(h * a.size + i));
         }
+        for (int off = 1; off < kWarp; off <<= 1) {
+            const double o1 = __shfl_xor_sync(0xffffffffu, d.first, off), o2 = __shfl_xor_sync(0xffffffffu, d.second, off);
+            d.take(o1);
+            d.take(o2);
+        }
+        if (lane == h) mine = a.best == 2 ? d.first + d.second : d.first;
     }
-    return __ballot_sync(0xffffffffu, in);
+    return mine;
 }
 
 // The choice among the experts that `row` (the warp's choices) puts at or above
@@ -273,8 +275,9 @@ __device__ __forceinline__ float score_of(bool sigmoid, float l, float shift)
 }
 
 // Lane l holds the vectors l, l + 32, ... of VEC experts each (N of them).
-template <int VEC, int N>
-__global__ void __launch_bounds__(kScThreads, VEC * N <= 8 ? 4 : VEC * N <= 16 ? 2 : 1) k_route_scored(ScoredArgs a)
+template <int VEC, int N, bool GROUPS>
+__global__ void __launch_bounds__(kScThreads, VEC * N <= 8 ? 4 : VEC * N <= 16 ? 2 : 1)
+    k_route_scored(const __grid_constant__ ScoredArgs a)
 {
     pdl_begin();
     using Vec = typename ScVec<VEC>::T;
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kScThreads, VEC * N <= 8 ? 4 : VEC * N <= 16 ?
         __syncthreads();
     }
     // the logits' order is the choices' order
-    const bool direct = !a.bias && (a.groups == 1 || a.best == 1);
+    const bool direct = !a.bias && (!GROUPS || a.best == 1);
     int lanes = kWarp; // of a group
     while (lanes * a.groups > kWarp) lanes >>= 1;
     const int64_t step = (int64_t)gridDim.x * kScWarps;
@@ -362,15 +365,67 @@ __global__ void __launch_bounds__(kScThreads, VEC * N <= 8 ? 4 : VEC * N <= 16 ?
                 }
             __syncwarp();
         };
-        if (a.groups > 1) {
-            row_store();
-            const uint32_t keep = choose_groups(row, a, t, lane, lanes, top, inv, direct);
+        if constexpr (GROUPS) {
+            // lane g: group g's score
+            GroupScore mine = {-INFINITY, 0.f};
+            if (VEC == 4 && a.shift >= 0) { // (warp-uniform) groups of 4 << shift experts: whole lanes, a power of two of them
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    Best2<float> b = {fmaxf(v[i][0], v[i][VEC > 1]), fminf(v[i][0], v[i][VEC > 1])};
+#pragma unroll
+                    for (int c = 2; c < VEC; ++c) {
+                        b.second = fmaxf(b.second, fminf(b.first, v[i][c]));
+                        b.first = fmaxf(b.first, v[i][c]);
+                    }
+                    best_of_lanes(b, 1, 1 << a.shift);
+                    const GroupScore g = group_score(a, b, inv);
+                    const int at = lane << a.shift; // group `lane` begins with this vector
+                    const float s = __shfl_sync(0xffffffffu, g.score, at & 31), r = __shfl_sync(0xffffffffu, g.err, at & 31);
+                    if (at >> 5 == i) mine = {s, r};
+                }
+            } else {
+                row_store();
+                mine = scan_groups(row, a, lane, lanes, inv);
+            }
+            const bool is = lane < a.groups;
+            if (!is) mine = {-INFINITY, 0.f};
+            int rank = 0;
+            for (int h = 0; h < a.groups; ++h) {
+                const float o = __shfl_sync(0xffffffffu, mine.score, h);
+                rank += o > mine.score || (o == mine.score && h < lane);
+            }
+            bool in_group = is && rank < a.top_groups;
+            if (!direct) {
+                const float least = -reduce_max(in_group ? mine.err - mine.score : -INFINITY);
+                const float most = reduce_max(is && !in_group ? mine.score + mine.err : -INFINITY);
+                if (most >= least && most > -INFINITY) { // (warp-uniform) the groups at the border
+                    const bool open = is && (in_group ? mine.score - mine.err <= most : mine.score + mine.err >= least);
+                    const uint32_t opens = __ballot_sync(0xffffffffu, open);
+                    row_store();
+                    const double exact = exact_groups(a, t, row, top, inv, opens);
+                    int place = 0;
+                    for (uint32_t left = opens; left; left &= left - 1) {
+                        const int h = __ffs(left) - 1;
+                        const double o = __shfl_sync(0xffffffffu, exact, h);
+                        place += o > exact || (o == exact && h < lane);
+                    }
+                    const int room = a.top_groups - __popc(__ballot_sync(0xffffffffu, in_group && !open));
+                    if (open) in_group = place < room;
+                }
+            }
+            const uint32_t keep = __ballot_sync(0xffffffffu, in_group);
 #pragma unroll
             for (int i = 0; i < N; ++i)
+                if (VEC == 4 && a.shift >= 0) {
+                    if (!(keep >> ((lane + kWarp * i >> a.shift) & 31) & 1))
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) {
-                    const uint32_t e = (lane + kWarp * i) * VEC + c;
-                    if (e < (uint32_t)E && !(keep >> (e * a.inv_size >> 20) & 1)) v[i][c] = -INFINITY;
+                        for (int c = 0; c < VEC; ++c) v[i][c] = -INFINITY;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < VEC; ++c) {
+                        const uint32_t e = (lane + kWarp * i) * VEC + c;
+                        if (e < (uint32_t)E && !(keep >> (e * a.inv_size >> 20) & 1)) v[i][c] = -INFINITY;
+                    }
                 }
             __syncwarp();
         }
@@ -584,9 +639,9 @@ ap_status scored_sizes(const char *who, int64_t T, int32_t E, int32_t k, int32_t
     return AP_OK;
 }
 
-template <int VEC, int N> ap_status launch_scored(const ScoredArgs &a, cudaStream_t st)
+template <int VEC, int N, bool GROUPS> ap_status launch_scored_form(const ScoredArgs &a, cudaStream_t st)
 {
-    const auto kernel = k_route_scored<VEC, N>;
+    const auto kernel = k_route_scored<VEC, N, GROUPS>;
     constexpr int kMaxE = VEC * N * kWarp;
     static const cudaError_t attr = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                          (kScWarps * 8 + 4) * kMaxE);
@@ -596,6 +651,11 @@ template <int VEC, int N> ap_status launch_scored(const ScoredArgs &a, cudaStrea
     launch(kernel, (int)(want < resident ? want : resident), kScThreads, (size_t)(kScWarps * 8 + 4) * a.E, st, a);
     AP_CHECK_LAUNCH("route_scored launch");
     return AP_OK;
+}
+
+template <int VEC, int N> ap_status launch_scored(const ScoredArgs &a, cudaStream_t st)
+{
+    return a.groups > 1 ? launch_scored_form<VEC, N, true>(a, st) : launch_scored_form<VEC, N, false>(a, st);
 }
 
 template <int VEC, int N>
@@ -635,8 +695,11 @@ extern "C" ap_status ap_route_scored(const float *logits, int64_t T, int32_t E, 
     if (T == 0) return AP_OK;
     if (!logits || !idx || !w) return fail(AP_EINVAL, "route_scored: NULL pointer");
     const int size = E / groups;
+    int shift = -1;
+    for (int q = 0; q <= 5; ++q)
+        if (size == 4 << q) shift = q;
     const ScoredArgs a = {logits, bias, mask, idx,  w,          counts,     T,
-                          E,      k,    groups, size, top_groups, group_best, (uint32_t)(((1 << 20) + size - 1) / size),
+                          E,      k,    groups, size, top_groups, group_best, shift, (uint32_t)(((1 << 20) + size - 1) / size),
                           scale,  score == AP_SCORE_SIGMOID, renorm != 0};
     cudaStream_t st = (cudaStream_t)stream;
     const uintptr_t al = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(bias);
