@@ -21,6 +21,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "ap_common.cuh"
 
 namespace ap {
@@ -137,15 +139,34 @@ __device__ __forceinline__ void store_codes(void *p, int64_t at, const uint32_t 
     __stcs(w, c[0]);
     __stcs(w + kBlock / 8, c[1]);
 }
-__device__ __forceinline__ float code_m(uint32_t w, int j) // c |c| of byte j
+// Integers below 2^23 sit in the last bits of 2^23 plus them, so bytes become
+// numbers, and numbers their integer parts, without the conversion unit (which
+// six conversions an element keep as busy as HBM).
+constexpr float kBig = 8388608.f; // 2^23
+constexpr uint32_t kBigBits = 0x4b000000u;
+__device__ __forceinline__ float byte_of(uint32_t w, int j) // byte j, not signed
 {
-    const float c = (float)(int8_t)(w >> 8 * j);
+    return __uint_as_float(__byte_perm(w, kBigBits, 0x7440 | j)) - kBig;
+}
+__device__ __forceinline__ float code_m(uint32_t w, int j) // c |c| of byte j (the caller flips the sign bits: c + 128)
+{
+    const float c = __uint_as_float(__byte_perm(w, kBigBits, 0x7440 | j)) - (kBig + 128.f);
     return c * fabsf(c);
 }
 __device__ __forceinline__ float code_v(uint32_t w, int j) // c^2
 {
-    const float c = (float)(w >> 8 * j & 0xff);
+    const float c = byte_of(w, j);
     return c * c;
+}
+constexpr uint32_t kSigns = 0x80808080u;
+// floor(x - 1) in the last bits
+__device__ __forceinline__ uint32_t floor_bits(float x) { return __float_as_uint(__fadd_rd(x, kBig - 1.f)); }
+// 1 and the low or high 16 bits as a fraction
+__device__ __forceinline__ float low_fraction(uint32_t u) { return __uint_as_float((u << 7 & 0x7fff80u) | 0x3f800000u); }
+__device__ __forceinline__ float high_fraction(uint32_t u) { return __uint_as_float((u >> 9 & 0x7fff80u) | 0x3f800000u); }
+__device__ __forceinline__ uint32_t four_bytes(const uint32_t (&c)[8], int h)
+{
+    return __byte_perm(__byte_perm(c[4 * h], c[4 * h + 1], 0x0040), __byte_perm(c[4 * h + 2], c[4 * h + 3], 0x0040), 0x5410);
 }
 
 // The finalizer of MurmurHash3 (Appleby), a mixing of 32 bits.
@@ -159,13 +180,20 @@ __device__ __forceinline__ uint32_t mix(uint32_t x)
 }
 constexpr uint32_t kGolden = 0x9E3779B9u;
 
-__device__ __forceinline__ float sqrt_fast(float x) // within 2^-22 of its value, also below the normal numbers
+// Single instructions, within 2^-22 of the values; what is below the normal
+// numbers counts as 0.
+__device__ __forceinline__ float sqrt_fast(float x)
 {
     float y;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float div_fast(float a, float b) { return __fdividef(a, b); }
+__device__ __forceinline__ float div_fast(float a, float b)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(b));
+    return a * y;
+}
 
 // 1 - b^t from ln b: expm1 keeps its precision for few steps.
 __device__ __forceinline__ float correction(const float (&ln_b)[2], float t)
@@ -192,100 +220,170 @@ template <int CAP> __device__ __forceinline__ int tensor_of(const UpTable<CAP> &
     return lo;
 }
 
+// A lane's 8 elements of a block as they lie in memory.
+template <typename E> struct Raw;
+template <> struct Raw<float> {
+    float4 w[2];
+    __device__ __forceinline__ float at(int j) const
+    {
+        const float4 &x = w[j / 4];
+        return j % 4 == 0 ? x.x : j % 4 == 1 ? x.y : j % 4 == 2 ? x.z : x.w;
+    }
+};
+template <> struct Raw<bf16_t> {
+    uint2 w[2];
+    __device__ __forceinline__ float at(int j) const
+    {
+        const uint32_t x = j % 4 < 2 ? w[j / 4].x : w[j / 4].y;
+        return __uint_as_float(j & 1 ? x & 0xffff0000u : x << 16);
+    }
+};
+template <typename E> __device__ __forceinline__ void load_raw(const E *p, int64_t at, int64_t n, bool vec, Raw<E> &x)
+{
+    using Vec = decltype(x.w[0]);
+    const int lane = (int)lane_id();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t i = at + h * (kBlock / 2) + lane * 4;
+        if (vec) {
+            x.w[h] = __ldcs(reinterpret_cast<std::remove_reference_t<Vec> *>(const_cast<E *>(p + i)));
+        } else {
+            E y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                put(y + j, 0.f);
+                if (i + j < n) y[j] = p[i + j];
+            }
+            memcpy(&x.w[h], y, sizeof(y));
+        }
+    }
+}
+template <int BITS> constexpr bool kAheadOf = BITS == 8;
+template <int BITS> constexpr int kUpBlocksOf = BITS == 8 ? 3 : 1;
+// What a lane has of a block: parameters, gradients and moments.
+template <typename P, typename G, int BITS> struct UpBlock {
+    Raw<P> p;
+    Raw<G> g;
+    Raw<float> m, v;
+    uint32_t cm[2], cv[2];
+    float sm, sv;
+    int i; // the tensor
+    int64_t at;
+    bool vec;
+};
+
 template <int CAP, typename P, typename G, bool MASTER, int BITS>
-__global__ void __launch_bounds__(kUpThreads) k_adamw(const __grid_constant__ UpTable<CAP> tab, const UpStep s)
+__global__ void __launch_bounds__(kUpThreads, kUpBlocksOf<BITS>) k_adamw(const __grid_constant__ UpTable<CAP> tab, const UpStep s)
 {
     pdl_begin();
-    if ((s.d_skip && *s.d_skip) || (s.d_scale && !(fabsf(*s.d_scale) < INFINITY))) return; // (the same for all blocks)
     const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
-    const int t = *s.d_step + 1;
+    const int32_t taken = *s.d_step;
+    const uint32_t skip = s.d_skip ? *s.d_skip : 0u;
     const float scale = s.d_scale ? *s.d_scale : 1.f, lr = s.d_lr ? *s.d_lr : s.lr;
+    const uint32_t blocks = tab.first[tab.count];
+    using Q = std::conditional_t<MASTER, float, P>;
+    using Block = UpBlock<Q, G, BITS>;
+    uint32_t b = blockIdx.x * kUpWarps + wid;
+    int i = tensor_of(tab, b);
+    const auto load = [&](Block &x) { // block b
+        while (b >= tab.first[i + 1]) ++i;
+        const UpTensor &q = tab.t[i];
+        x.i = i;
+        x.at = (int64_t)(b - tab.first[i]) * kBlock;
+        x.vec = tab.vec && x.at + kBlock <= q.n;
+        load_raw(MASTER ? reinterpret_cast<const Q *>(q.master) : static_cast<const Q *>(q.param), x.at, q.n, x.vec, x.p);
+        load_raw(static_cast<const G *>(q.grad), x.at, q.n, x.vec, x.g);
+        if constexpr (BITS == 8) {
+            load_codes(q.m, x.at, x.cm);
+            load_codes(q.v, x.at, x.cv);
+            x.sm = q.m_scale[x.at / kBlock];
+            x.sv = q.v_scale[x.at / kBlock];
+        } else {
+            load_raw(static_cast<const float *>(q.m), x.at, q.n, x.vec, x.m);
+            load_raw(static_cast<const float *>(q.v), x.at, q.n, x.vec, x.v);
+        }
+    };
+    constexpr bool kAhead = kAheadOf<BITS>; // the next block is on its way while one is worked on
+    Block next;
+    if (b < blocks) load(next); // (on its way while the step's constants are formed)
+    const int t = taken + 1;
     const float keep = 1.f - lr * s.decay;
     const float rate = __fdiv_rn(lr, correction(s.ln_b1, (float)t));
     const float root = __frsqrt_rn(correction(s.ln_b2, (float)t));
     const uint32_t seeded = mix(s.seed + kGolden * (uint32_t)t);
-    const uint32_t blocks = tab.first[tab.count];
-    uint32_t b = blockIdx.x * kUpWarps + wid;
-    int i = tensor_of(tab, b);
-    for (; b < blocks; b += gridDim.x * kUpWarps) {
-        while (b >= tab.first[i + 1]) ++i;
-        const UpTensor &x = tab.t[i];
-        const int64_t at = (int64_t)(b - tab.first[i]) * kBlock, n = x.n;
-        const bool vec = tab.vec && at + kBlock <= n;
-        float p[8], g[8], m[8], v[8];
-        uint32_t cm[2], cv[2];
-        float sm = 0.f, sv = 0.f;
-        if constexpr (MASTER)
-            load8(x.master, at, n, vec, p);
-        else
-            load8(static_cast<const P *>(x.param), at, n, vec, p);
-        load8(static_cast<const G *>(x.grad), at, n, vec, g);
+    if (skip || !(fabsf(scale) < INFINITY)) return; // (the same for all blocks)
+    while (b < blocks) {
+        const Block x = next;
+        b += gridDim.x * kUpWarps;
+        if (kAhead && b < blocks) load(next);
+        const UpTensor &q = tab.t[x.i];
+        const int64_t n = q.n, at = x.at;
+        const bool vec = x.vec;
+        float p[8], m[8], v[8], r[8];
         if constexpr (BITS == 8) {
-            load_codes(x.m, at, cm);
-            load_codes(x.v, at, cv);
-            sm = x.m_scale[at / kBlock];
-            sv = x.v_scale[at / kBlock];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                m[j] = code_m(cm[j / 4], j % 4) * sm;
-                const float r = code_v(cv[j / 4], j % 4) * sv;
-                v[j] = r * r;
+                m[j] = code_m(x.cm[j / 4] ^ kSigns, j % 4) * x.sm;
+                const float y = code_v(x.cv[j / 4], j % 4) * x.sv;
+                v[j] = y * y;
             }
             if (at + kBlock > n) // what the codes behind the last element hold is of no account
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (at + (j / 4) * (kBlock / 2) + lane * 4 + j % 4 >= n) m[j] = v[j] = 0.f;
         } else {
-            load8(static_cast<const float *>(x.m), at, n, vec, m);
-            load8(static_cast<const float *>(x.v), at, n, vec, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                m[j] = x.m.at(j);
+                v[j] = x.v.at(j);
+            }
         }
-        float r[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float gj = g[j] * scale;
-            m[j] = fmaf(s.b1, m[j], s.one_b1 * gj);
-            v[j] = fmaf(s.b2, v[j], s.one_b2 * gj * gj);
+            const float g = x.g.at(j) * scale;
+            m[j] = fmaf(s.b1, m[j], s.one_b1 * g);
+            v[j] = fmaf(s.b2, v[j], s.one_b2 * g * g);
             r[j] = sqrt_fast(v[j]);
-            p[j] = fmaf(keep, p[j], -rate * div_fast(m[j], fmaf(r[j], root, s.eps)));
+            p[j] = fmaf(keep, x.p.at(j), -rate * div_fast(m[j], fmaf(r[j], root, s.eps)));
         }
-        if constexpr (MASTER) store8(x.master, at, n, vec, p);
-        store8(static_cast<P *>(x.param), at, n, vec, p);
+        if constexpr (MASTER) store8(q.master, at, n, vec, p);
+        store8(static_cast<P *>(q.param), at, n, vec, p);
         if constexpr (BITS == 32) {
-            store8(static_cast<float *>(x.m), at, n, vec, m);
-            store8(static_cast<float *>(x.v), at, n, vec, v);
+            store8(static_cast<float *>(q.m), at, n, vec, m);
+            store8(static_cast<float *>(q.v), at, n, vec, v);
         } else {
             float top_m = 0.f, top_r = 0.f; // (elements beyond n are 0; max that keeps NaN)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 top_m = __uint_as_float(max(__float_as_uint(top_m), __float_as_uint(fabsf(m[j]))));
-                top_r = __uint_as_float(max(__float_as_uint(top_r), __float_as_uint(fabsf(r[j]))));
+                top_r = __uint_as_float(max(__float_as_uint(top_r), __float_as_uint(r[j])));
             }
             top_m = block_max(top_m);
             top_r = block_max(top_r);
             // a block with a value that is no number becomes NaN whole
-            sm = top_m < INFINITY ? top_m * (1.f / (127.f * 127.f)) : NAN;
-            sv = top_r < INFINITY ? top_r * (1.f / (255.f * 255.f)) : NAN;
+            const float sm = top_m < INFINITY ? top_m * (1.f / (127.f * 127.f)) : NAN;
+            const float sv = top_r < INFINITY ? top_r * (1.f / (255.f * 255.f)) : NAN;
             const float im = sm > 0.f ? __fdiv_rn(1.f, sm) : 0.f, iv = sv > 0.f ? __fdiv_rn(1.f, sv) : 0.f;
-            const uint32_t key = mix((uint32_t)(tab.base + i) + seeded);
-            cm[0] = cm[1] = cv[0] = cv[1] = 0;
+            const uint32_t key = mix((uint32_t)(tab.base + x.i) + seeded);
+            uint32_t cm[8], cv[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t e = (uint32_t)at + (j / 4) * (kBlock / 2) + lane * 4 + j % 4;
                 const uint32_t u = mix(e * kGolden + key);
-                int c = (int)fminf(sqrt_fast(fabsf(m[j]) * im) + (float)(u & 0xffff) * (1.f / 65536), 127.f);
-                c = m[j] < 0.f ? -c : c;
-                cm[j / 4] |= (uint32_t)(c & 0xff) << 8 * (j % 4);
-                const float q = fminf(sqrt_fast(r[j] * iv) + (float)(u >> 16) * (1.f / 65536), 255.f);
-                const uint32_t w = r[j] > 0.f ? (uint32_t)fmaxf(q, 1.f) : 0u;
-                cv[j / 4] |= w << 8 * (j % 4);
+                const uint32_t c = floor_bits(fminf(sqrt_fast(fabsf(m[j]) * im) + low_fraction(u), 128.f));
+                cm[j] = m[j] < 0.f ? 0u - c : c; // (last byte)
+                const float y = fminf(sqrt_fast(r[j] * iv) + high_fraction(u), 256.f);
+                cv[j] = r[j] > 0.f ? floor_bits(fmaxf(y, 2.f)) : 0u;
             }
-            store_codes(x.m, at, cm);
-            store_codes(x.v, at, cv);
+            const uint32_t wm[2] = {four_bytes(cm, 0), four_bytes(cm, 1)}, wv[2] = {four_bytes(cv, 0), four_bytes(cv, 1)};
+            store_codes(q.m, at, wm);
+            store_codes(q.v, at, wv);
             if (lane == 0) {
-                x.m_scale[at / kBlock] = sm;
-                x.v_scale[at / kBlock] = sv;
+                q.m_scale[at / kBlock] = sm;
+                q.v_scale[at / kBlock] = sv;
             }
         }
+        if (!kAhead && b < blocks) load(next);
     }
     // the last block of the last launch moves the step on; the work word is 0 again then
     if (s.last) {
@@ -300,62 +398,87 @@ __global__ void __launch_bounds__(kUpThreads) k_adamw(const __grid_constant__ Up
     }
 }
 
-// Sums of squares: a lane adds 8 squares, and those sums with what each
-// addition rounds away; blocks leave one double each.
-template <int CAP, typename G>
-__global__ void __launch_bounds__(kUpThreads) k_norm(const __grid_constant__ UpTable<CAP> tab, double *part)
+// Sums of squares as pairs of FP32: the sum, and what its additions rounded away.
+struct Pair {
+    float sum, rest;
+};
+__device__ __forceinline__ void add_to(Pair &a, float x)
 {
-    pdl_begin();
-    __shared__ double s_sum[kUpWarps];
-    const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
-    const uint32_t blocks = tab.first[tab.count];
-    uint32_t b = blockIdx.x * kUpWarps + wid;
-    int i = tensor_of(tab, b);
-    float sum = 0.f, rest = 0.f;
-    for (; b < blocks; b += gridDim.x * kUpWarps) {
-        while (b >= tab.first[i + 1]) ++i;
-        const UpTensor &x = tab.t[i];
-        const int64_t at = (int64_t)(b - tab.first[i]) * kBlock, n = x.n;
-        float g[8], q = 0.f;
-        load8(static_cast<const G *>(x.grad), at, n, tab.vec && at + kBlock <= n, g);
+    const float to = __fadd_rn(a.sum, x), back = __fsub_rn(to, a.sum);
+    a.rest += __fadd_rn(__fsub_rn(a.sum, __fsub_rn(to, back)), __fsub_rn(x, back));
+    a.sum = to;
+}
+__device__ __forceinline__ void add_lanes(Pair &a)
+{
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q = fmaf(g[j], g[j], q);
-        const float to = __fadd_rn(sum, q), back = __fsub_rn(to, sum);
-        rest += __fadd_rn(__fsub_rn(sum, __fsub_rn(to, back)), __fsub_rn(q, back));
-        sum = to;
+    for (int off = 16; off > 0; off >>= 1) {
+        const float s = __shfl_xor_sync(0xffffffffu, a.sum, off), r = __shfl_xor_sync(0xffffffffu, a.rest, off);
+        add_to(a, s);
+        a.rest += r;
     }
-    double d = sum < INFINITY ? (double)sum + (double)rest : (double)sum;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-    if (lane == 0) s_sum[wid] = d;
+}
+template <int WARPS> __device__ __forceinline__ void add_block(Pair &a) // (warp 0 receives it)
+{
+    __shared__ Pair s_sum[WARPS];
+    const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
+    add_lanes(a);
+    if (lane == 0) s_sum[wid] = a;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int q = 1; q < kUpWarps; ++q) d += s_sum[q];
-        part[blockIdx.x] = d;
+    if (wid == 0) {
+        a = lane < WARPS ? s_sum[lane] : Pair{0.f, 0.f};
+        add_lanes(a);
     }
 }
 
-constexpr int kNormThreads = 1024;
-__global__ void __launch_bounds__(kNormThreads) k_norm_finish(const double *part, int n, float max_norm, float *out)
+// The gradients' squares: four blocks of elements at a time, 8 of each a lane.
+constexpr int kNormBlocks4 = 4;
+template <int CAP, typename G>
+__global__ void __launch_bounds__(kUpThreads) k_norm(const __grid_constant__ UpTable<CAP> tab, Pair *part)
 {
     pdl_begin();
-    __shared__ double s_sum[kNormThreads / kWarp];
-    const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
-    double d = 0.0;
-    for (int i = threadIdx.x; i < n; i += kNormThreads) d += part[i];
+    const uint32_t blocks = tab.first[tab.count];
+    uint32_t b = blockIdx.x * kUpWarps + threadIdx.x / kWarp;
+    int i = tensor_of(tab, b);
+    Pair a = {0.f, 0.f};
+    for (; b < blocks; b += gridDim.x * kUpWarps) {
+        while (b >= tab.first[i + 1]) ++i;
+        const UpTensor &x = tab.t[i];
+        const int64_t at = (int64_t)(b - tab.first[i]) * (kNormBlocks4 * kBlock), n = x.n;
+        float g[kNormBlocks4][8];
+        if (tab.vec && at + kNormBlocks4 * kBlock <= n) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-    if (lane == 0) s_sum[wid] = d;
-    __syncthreads();
-    if (wid == 0) {
-        d = s_sum[lane];
+            for (int q = 0; q < kNormBlocks4; ++q) load8(static_cast<const G *>(x.grad), at + q * kBlock, n, true, g[q]);
+        } else {
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-        if (lane == 0) {
-            const float norm = (float)sqrt(d);
-            out[0] = norm;
-            out[1] = !(norm < INFINITY) ? NAN : max_norm > 0.f && norm > max_norm ? __fdiv_rn(max_norm, norm) : 1.f;
+            for (int q = 0; q < kNormBlocks4; ++q) load8(static_cast<const G *>(x.grad), at + q * kBlock, n, false, g[q]);
         }
+#pragma unroll
+        for (int q = 0; q < kNormBlocks4; ++q) {
+            float y = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y = fmaf(g[q][j], g[q][j], y);
+            add_to(a, y);
+        }
+    }
+    add_block<kUpWarps>(a);
+    if (threadIdx.x == 0) part[blockIdx.x] = a;
+}
+
+constexpr int kNormThreads = 1024;
+__global__ void __launch_bounds__(kNormThreads) k_norm_finish(const Pair *part, int n, float max_norm, float *out)
+{
+    pdl_begin();
+    Pair a = {0.f, 0.f};
+    for (int i = threadIdx.x; i < n; i += kNormThreads) {
+        const Pair p = part[i];
+        add_to(a, p.sum);
+        a.rest += p.rest;
+    }
+    add_block<kNormThreads / kWarp>(a);
+    if (threadIdx.x == 0) {
+        const float norm = __fsqrt_rn(a.sum < INFINITY ? a.sum + a.rest : a.sum);
+        out[0] = norm;
+        out[1] = !(norm < INFINITY) ? NAN : max_norm > 0.f && norm > max_norm ? __fdiv_rn(max_norm, norm) : 1.f;
     }
 }
 
@@ -374,7 +497,7 @@ __global__ void __launch_bounds__(kUpThreads) k_moments(const void *m, const voi
         float x[8], y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            x[j] = code_m(cm[j / 4], j % 4) * sm;
+            x[j] = code_m(cm[j / 4] ^ kSigns, j % 4) * sm;
             y[j] = code_v(cv[j / 4], j % 4) * sv;
             y[j] *= y[j];
         }
@@ -394,6 +517,7 @@ int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
 template <int CAP> void fill(UpTable<CAP> &tab, const ap_adamw_tensor *t, int from, int to, unsigned psize, unsigned gsize,
                              bool grads_only)
 {
+    const int unit = grads_only ? kNormBlocks4 : 1; // blocks of elements that a warp takes at a time
     tab.count = to - from;
     tab.base = from;
     tab.vec = 1;
@@ -401,7 +525,7 @@ template <int CAP> void fill(UpTable<CAP> &tab, const ap_adamw_tensor *t, int fr
     for (int i = from; i < to; ++i) {
         const ap_adamw_tensor &x = t[i];
         tab.first[i - from] = at;
-        at += (uint32_t)blocks_of(x.n);
+        at += (uint32_t)((blocks_of(x.n) + unit - 1) / unit);
         tab.t[i - from] = {x.param, x.grad, (float *)x.master, x.m, x.v, x.m_scale, x.v_scale, x.n};
         if (!x.n) continue;
         bool ok = aligned(x.grad, 4 * gsize);
@@ -488,7 +612,7 @@ int norm_launches(const ap_adamw_tensor *t, int32_t n)
 }
 
 template <int CAP>
-ap_status norm_launch_all(const ap_adamw_tensor *t, int32_t n, int32_t dtype, float max_norm, float *out, double *part,
+ap_status norm_launch_all(const ap_adamw_tensor *t, int32_t n, int32_t dtype, float max_norm, float *out, Pair *part,
                           cudaStream_t st)
 {
     int from = 0, parts = 0;
@@ -537,7 +661,7 @@ extern "C" ap_status ap_grad_norm(const ap_adamw_tensor *tensors, int32_t n, int
         return fail(AP_EINVAL, "grad_norm: scratch of %lld bytes, %lld needed", (long long)scratch_bytes, (long long)need);
     for (int i = 0; i < n; ++i)
         if (!aligned(tensors[i].grad, size_of(grad_dtype))) return fail(AP_EINVAL, "grad_norm: tensor %d not aligned", i);
-    double *part = static_cast<double *>(scratch);
+    Pair *part = static_cast<Pair *>(scratch);
     cudaStream_t st = (cudaStream_t)stream;
     return n <= kFew ? norm_launch_all<kFew>(tensors, n, grad_dtype, max_norm, out, part, st)
                      : norm_launch_all<kMany>(tensors, n, grad_dtype, max_norm, out, part, st);

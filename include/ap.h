@@ -552,8 +552,8 @@ ap_status ap_adamw_step(const ap_adamw_tensor *tensors, int32_t n, const ap_adam
  * what clips it: out[0] = norm, out[1] = max_norm / norm where max_norm > 0 and
  * norm > max_norm, else 1; NaN where the norm is not finite, so that
  * ap_adamw_step with d_scale = out + 1 skips the step.  Squares are single
- * precision, their sums as exact as double, in an order that depends on the
- * sizes alone: equal inputs give equal bits.
+ * precision, eight of them added up as such, their sums in pairs of numbers, in
+ * an order that depends on the sizes alone: equal inputs give equal bits.
  *   out     [2] float32 (device, written)
  *   scratch device work space of ap_grad_norm_scratch_bytes() bytes, 16-byte
  *           aligned; its contents need no initialisation */
