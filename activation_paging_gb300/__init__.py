@@ -241,13 +241,17 @@ def route_scored(logits: torch.Tensor, k: int, score: str = "sigmoid", bias: tor
         group_best = 1
     pb = None if bias is None else _need_shape(bias, torch.float32, (E,), "bias")
     pc = None if counts is None else _need_shape(counts, torch.int32, (E,), "counts")
+    pairs = (T, k)
     if idx is None:
-        idx = _empty((T, k), torch.int32, logits.device, stream)
+        idx = _empty(pairs, torch.int32, logits.device, stream)
+    else:
+        _need_shape(idx, torch.int32, pairs, "idx")
     if w is None:
-        w = _empty((T, k), torch.float32, logits.device, stream)
+        w = _empty(pairs, torch.float32, logits.device, stream)
+    else:
+        _need_shape(w, torch.float32, pairs, "w")
     check(lib().ap_route_scored(logits.data_ptr(), T, E, k, kind, pb, groups, top_groups, group_best, 1 if renorm else 0, scale,
-                                m, _need_shape(idx, torch.int32, (T, k), "idx"), _need_shape(w, torch.float32, (T, k), "w"), pc,
-                                _stream(stream)), "route_scored")
+                                m, idx.data_ptr(), w.data_ptr(), pc, _stream(stream)), "route_scored")
     return idx, w
 
 
@@ -459,6 +463,7 @@ class AdamW:
         check(lib().ap_grad_norm_scratch_bytes(self._table, len(self._table), ctypes.byref(n)), "grad_norm_scratch_bytes")
         self._scratch_bytes = n.value
         self._scratch = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        self._norm = torch.empty(2, dtype=torch.float32, device=dev)
 
     @staticmethod
     def _apart(tensors):
@@ -493,11 +498,12 @@ class AdamW:
 
     def grad_norm(self, max_norm: float | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """[norm of all gradients, factor that clips it to ``max_norm``] (float32 [2]; the factor is 1 without clipping,
-        NaN where the norm is not finite): pass ``out[1:]`` as ``scale`` to ``step``."""
+        NaN where the norm is not finite): pass ``out[1:]`` as ``scale`` to ``step``.  Without ``out`` the tensor is the
+        optimizer's own, which the next call writes again."""
         if max_norm is not None and not max_norm > 0:
             raise ValueError(f"max_norm must be positive, got {max_norm}")
         if out is None:
-            out = _empty((2,), torch.float32, self.params[0].device, stream)
+            out = self._norm
         else:
             _need_shape(out, torch.float32, (2,), "out")
         check(lib().ap_grad_norm(self._table, len(self._table), self._cfg.grad_dtype, max_norm or 0.0, out.data_ptr(),

@@ -192,6 +192,7 @@ def test_norm(kind, sizes, offset):
         assert host(o.grad_norm(e * 3))[1] == 1.0
     again = torch.empty(2, device="cuda")
     assert torch.equal(o.grad_norm(out=again), o.grad_norm())
+    assert o.grad_norm() is o.grad_norm()
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), 3e38])

@@ -174,6 +174,16 @@ def test_one_product_of_a_gradient_by_a_pair_of_blocks():
     check_rows(Rows([256]), 64, 256)
 
 
+def test_one_product_of_two_tiles_of_a_pair():
+    check_forward(Rows([256]), 64, 512, pre=False)
+    check_forward(Rows([200]), 64, 512, pre=False)
+
+
+def test_one_product_of_a_gradient_by_two_tiles_of_a_pair():
+    check_rows(Rows([256]), 64, 512)
+    check_rows(Rows([30, 300]), 64, 512)
+
+
 def test_one_gradient_of_weights():
     check_weights(Rows([64]), 128, 64, bias=False)
 
