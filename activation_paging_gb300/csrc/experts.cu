@@ -38,6 +38,11 @@ constexpr int kLanes = 128;        // features of a tile
 constexpr int kDepth = 64;         // contraction of a stage: one line of 128 bytes
 constexpr int kPanel = kDepth * 128; // 64 lines
 constexpr int kMaxStages = 10;
+// The tensor cores cut what they add to an accumulator: its error grows with the
+// contraction, 1.1e-9 of it for each place (9.2e-6 at 8192).  FP32 weights'
+// gradients are therefore added up over sections of 2048 rows, which the writers
+// add with rounding (2.1e-6, and the products still hide the writing).
+constexpr int kSection = 32; // stages
 constexpr int kMaxSmem = 232448;
 constexpr int kMaxExperts = 1024;
 constexpr int kPassPitch = 80;     // bytes of 32 lanes' values on their way, with what keeps banks apart
@@ -154,7 +159,7 @@ template <Op OP> __device__ void count_tiles(const ExArgs &a, Table &tab)
 // the output, or kWeights: places of a weight's row) from c0, n of them; the
 // contraction's steps.  An expert's rows are shared out evenly among its tiles.
 struct Tile {
-    int e, f0, c0, n, steps, row0, live;
+    int e, f0, c0, n, steps, row0, live, sections;
 };
 template <Op OP, bool PAIR> __device__ __forceinline__ Tile tile_of(const ExArgs &a, const Walk &w, int rank)
 {
@@ -171,6 +176,7 @@ template <Op OP, bool PAIR> __device__ __forceinline__ Tile tile_of(const ExArgs
     t.n = min(each, width - t.c0);
     t.row0 = w.tab.seg[w.e] + (OP == kWeights ? 0 : t.c0);
     t.steps = OP == kWeights ? ceil_div(t.live, kDepth) : ceil_div(a.K, kDepth);
+    t.sections = OP == kWeights && a.out_f32 ? ceil_div(t.steps, kSection) : t.steps > 0;
     return t;
 }
 
@@ -541,7 +547,7 @@ __device__ __forceinline__ void read_weights(const ExArgs &a, const Tile &t, int
     }
 }
 __device__ __forceinline__ void write_weights(const ExArgs &a, const Tile &t, int c, int f, const float (&v)[32], const Kept &kept,
-                                              uint8_t *pass)
+                                              bool add, uint8_t *pass)
 {
     const int lane = (int)lane_id();
 #pragma unroll
@@ -563,7 +569,7 @@ __device__ __forceinline__ void write_weights(const ExArgs &a, const Tile &t, in
                 const float4 x = piece(r, lane & 7);
                 if (f0 + r < a.F && k < t.n) {
                     float *p = weights_at<float>(a, t, k, f0 + r);
-                    if (a.add)
+                    if (add)
                         add_vector(p, x);
                     else
                         *reinterpret_cast<float4 *>(p) = x;
@@ -575,7 +581,7 @@ __device__ __forceinline__ void write_weights(const ExArgs &a, const Tile &t, in
             for (int q = 0; q < 2; ++q) {
                 const int r = q * 8 + (lane >> 2);
                 float4 x = piece(r, (lane & 3) * 2), y = piece(r, (lane & 3) * 2 + 1);
-                if (a.add) {
+                if (add) {
                     const uint4 o = kept.w[h * 2 + q];
                     x.x += low(o.x), x.y += high(o.x), x.z += low(o.y), x.w += high(o.y);
                     y.x += low(o.z), y.y += high(o.z), y.z += low(o.w), y.w += high(o.w);
@@ -592,13 +598,13 @@ __device__ __forceinline__ void write_weights(const ExArgs &a, const Tile &t, in
                     const float x = *reinterpret_cast<const float *>(pass + r * 128 + ((lane >> 2 ^ (r & 7)) << 4) + (lane & 3) * 4);
                     if (a.out_f32) {
                         float *p = weights_at<float>(a, t, c + lane, f0 + r);
-                        if (a.add)
+                        if (add)
                             add_one(p, x);
                         else
                             *p = x;
                     } else {
                         bf16_t *p = weights_at<bf16_t>(a, t, c + lane, f0 + r);
-                        *p = __float2bfloat16_rn(a.add ? __bfloat162float(*p) + x : x);
+                        *p = __float2bfloat16_rn(add ? __bfloat162float(*p) + x : x);
                     }
                 }
         }
@@ -624,52 +630,54 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
     };
     for (; w.find(a.E); w.next()) {
         const Tile t = tile_of<OP, PAIR>(a, w, rank);
-        const uint32_t acc = count & 1, at = tmem + acc * 256 + ((uint32_t)part * kWarp << 16);
         const int f = t.f0 + part * kWarp; // (of weights)
-        int c = (writer >> 2) * 32;
-        Ahead x;
-        Kept kept;
-        if constexpr (OP == kWeights)
-            read_weights(a, t, c, f, kept);
-        else
-            read_ahead<OP>(a, t, c, part, x);
-        if (t.steps > 0) {
-            ok = __all_sync(0xffffffffu, ok && bar_wait(smem_addr(&s_done[acc]), count >> 1 & 1, dead));
-            ++count;
-        }
-        fence_after();
-        if (c >= t.n && t.steps > 0) release(acc);
-        for (; c < t.n; c += 64) {
-            const bool last = c + 64 >= t.n;
-            float v[32];
-            Frag y;
-            if (t.steps > 0 && ok) {
-                if constexpr (OP == kWeights)
-                    acc_load(at + c, v);
-                else
-                    acc_load_tiles(at + c, y);
-            } else { // nothing to add up, or products that did not come
+        for (int section = 0; section == 0 || section < t.sections; ++section) {
+            const uint32_t acc = count & 1, at = tmem + acc * 256 + ((uint32_t)part * kWarp << 16);
+            int c = (writer >> 2) * 32;
+            Ahead x;
+            Kept kept;
+            if constexpr (OP == kWeights)
+                read_weights(a, t, c, f, kept);
+            else
+                read_ahead<OP>(a, t, c, part, x);
+            if (t.steps > 0) {
+                ok = __all_sync(0xffffffffu, ok && bar_wait(smem_addr(&s_done[acc]), count >> 1 & 1, dead));
+                ++count;
+            }
+            fence_after();
+            if (c >= t.n && t.steps > 0) release(acc);
+            for (; c < t.n; c += 64) {
+                const bool last = c + 64 >= t.n;
+                float v[32];
+                Frag y;
+                if (t.steps > 0 && ok) {
+                    if constexpr (OP == kWeights)
+                        acc_load(at + c, v);
+                    else
+                        acc_load_tiles(at + c, y);
+                } else { // nothing to add up, or products that did not come
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    v[j] = t.steps > 0 ? NAN : 0.f;
-                    y[j / 16][j % 16] = NAN;
+                    for (int j = 0; j < 32; ++j) {
+                        v[j] = t.steps > 0 ? NAN : 0.f;
+                        y[j / 16][j % 16] = NAN;
+                    }
                 }
-            }
-            if (last) {
-                fence_before();
-                if (t.steps > 0) release(acc);
-            }
-            if constexpr (OP == kWeights) {
-                const Kept now = kept;
-                if (!last) read_weights(a, t, c + 64, f, kept);
-                if (f < a.F) write_weights(a, t, c, f, v, now, pass);
-            } else {
-                const Ahead now = x;
-                if (!last) read_ahead<OP>(a, t, c + 64, part, x);
-                if constexpr (OP == kForward)
-                    write_rows(a, t, c, part, y, now, pass);
-                else
-                    write_slopes(a, t, c, part, y, now, pass);
+                if (last) {
+                    fence_before();
+                    if (t.steps > 0) release(acc);
+                }
+                if constexpr (OP == kWeights) {
+                    const Kept now = kept;
+                    if (!last) read_weights(a, t, c + 64, f, kept);
+                    if (f < a.F) write_weights(a, t, c, f, v, now, a.add || section > 0, pass);
+                } else {
+                    const Ahead now = x;
+                    if (!last) read_ahead<OP>(a, t, c + 64, part, x);
+                    if constexpr (OP == kForward)
+                        write_rows(a, t, c, part, y, now, pass);
+                    else
+                        write_slopes(a, t, c, part, y, now, pass);
+                }
             }
         }
     }
@@ -761,30 +769,31 @@ __global__ void __launch_bounds__(kExThreads, 1)
             for (; ok && w.find(a.E); w.next()) {
                 const Tile t = tile_of<OP, PAIR>(a, w, rank);
                 if (t.steps == 0) continue;
-                const uint32_t acc = count & 1;
-                if (count >= 2 && !bar_wait(smem_addr(&s_free[acc]), (count >> 1 & 1) ^ 1, dead)) break;
-                fence_after();
                 const uint32_t shape = shape_of(PAIR ? 2 * kLanes : kLanes, PAIR ? (t.n + 31) & ~31 : (t.n + 15) & ~15,
                                                 OP != kForward, OP == kWeights);
-                for (int step = 0; step < t.steps; ++step) {
-                    if (!bar_wait(smem_addr(kPass2 ? &s_ready[s] : &s_full[s]), turn & 1, dead)) {
-                        ok = false;
-                        break;
-                    }
+                const int section = t.sections > 1 ? kSection : t.steps;
+                for (int from = 0; ok && from < t.steps; from += section, ++count) {
+                    const uint32_t acc = count & 1;
+                    ok = count < 2 || bar_wait(smem_addr(&s_free[acc]), (count >> 1 & 1) ^ 1, dead);
                     fence_after();
-                    const uint32_t sa = smem_addr(stages) + s * stage_bytes, sb = sa + 2 * kPanel;
+                    const int end = min(from + section, t.steps);
+                    for (int step = from; ok && step < end; ++step) {
+                        ok = bar_wait(smem_addr(kPass2 ? &s_ready[s] : &s_full[s]), turn & 1, dead);
+                        if (!ok) break;
+                        fence_after();
+                        const uint32_t sa = smem_addr(stages) + s * stage_bytes, sb = sa + 2 * kPanel;
 #pragma unroll
-                    for (int k = 0; k < kDepth / 16; ++k)
-                        mma<PAIR>(tmem + acc * 256, operand(sa + k * (OP == kForward ? 32 : 2048), kPanel),
-                                  operand(sb + k * (OP == kWeights ? 2048 : 32), kPanel), shape, step > 0 || k > 0);
-                    mma_commit<PAIR>(smem_addr(&s_empty[s]));
-                    if (++s == (uint32_t)a.stages) {
-                        s = 0;
-                        ++turn;
+                        for (int k = 0; k < kDepth / 16; ++k)
+                            mma<PAIR>(tmem + acc * 256, operand(sa + k * (OP == kForward ? 32 : 2048), kPanel),
+                                      operand(sb + k * (OP == kWeights ? 2048 : 32), kPanel), shape, step > from || k > 0);
+                        mma_commit<PAIR>(smem_addr(&s_empty[s]));
+                        if (++s == (uint32_t)a.stages) {
+                            s = 0;
+                            ++turn;
+                        }
                     }
+                    if (ok) mma_commit<PAIR>(smem_addr(&s_done[acc]));
                 }
-                if (ok) mma_commit<PAIR>(smem_addr(&s_done[acc]));
-                ++count;
             }
             if (*dead) { // products on their way end before tensor memory is freed
                 volatile int none = 0;

@@ -260,6 +260,26 @@ def test_long_contractions():
     check_weights(Rows([5000, 64, 65]), 128, 256)
 
 
+@pytest.mark.parametrize("add", [True, False])
+@pytest.mark.parametrize("N,K", [(128, 256), (130, 67)])
+def test_long_sums_of_weights(N, K, add):
+    """FP32 gradients are added up by sections of 2048 rows: an error of 1.1e-9 of the result for each row of a section,
+    and for numbers of one sign (each addition cuts up to 2 u of the sum so far, half of it on the average) up to
+    2048 / 16 u = 128 u, whatever the number of rows; additions of sections round by u each."""
+    r = Rows([2048, 9000, 0, 2049, 4096])
+    for positive in (False, True):
+        x, dy = r.make(K), r.make(N)
+        if positive:
+            x, dy = x.abs(), dy.abs()
+        dW = torch.ones(r.E, N, K, device="cuda")
+        ap.expert_linear_dw(dy, x, *r.args, dW=dW, accumulate=add)
+        e, _, _, _ = layer.expert_linear_dw(f64(dy), f64(x), r.seg, r.live, r.E)
+        e = e + (1.0 if add else 0.0)
+        for q in range(r.E):
+            size = np.linalg.norm(e[q])
+            assert np.linalg.norm(f64(dW[q]) - e[q]) <= ((128 + 8) * U if positive else 4e-6) * size
+
+
 @pytest.mark.parametrize("N,K", [(64, 128), (256, 384), (8, 8), (72, 200), (1000, 136)])
 @pytest.mark.parametrize("act", [None, "silu", "gelu", "swiglu"])
 def test_gradient_of_rows(N, K, act):
