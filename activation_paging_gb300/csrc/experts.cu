@@ -273,7 +273,11 @@ __device__ __forceinline__ void piece_load(Piece &x, const bf16_t *rows, int64_t
         if (r >= count) continue;
         const bf16_t *p = rows + r * ld + off;
         if (vec) {
-            if (in > 0) x.w[q] = *reinterpret_cast<const uint4 *>(p);
+            // (volatile: the load stays here, ahead of the work on the rows before)
+            asm volatile("{ .reg .pred q; setp.gt.s32 q, %5, 0; @q ld.global.v4.u32 {%0, %1, %2, %3}, [%4]; }"
+                         : "+r"(x.w[q].x), "+r"(x.w[q].y), "+r"(x.w[q].z), "+r"(x.w[q].w)
+                         : "l"(p), "r"(in)
+                         : "memory");
         } else {
             const unsigned short *s = reinterpret_cast<const unsigned short *>(p);
             uint32_t w[4] = {0, 0, 0, 0};
