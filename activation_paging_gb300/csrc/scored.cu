@@ -267,11 +267,14 @@ __device__ __noinline__ void choose_many(const ScoredArgs &a, int64_t t, float t
 
 // The chosen scores up to a factor that all of them share: of the softmax
 // relative to the largest chosen, of the sigmoid times e^-min(0, largest), so
-// that scores near 0 keep their ratios.
+// that scores near 0 keep their ratios: e^(l - shift) / (1 + e^l) below 0.  The
+// relative error is (1.5 d + 10) u with d = |l - shift|.
 __device__ __forceinline__ float score_of(bool sigmoid, float l, float shift)
 {
-    if (!sigmoid) return expf(l - shift);
-    return l > 0.f ? __fdiv_rn(1.f, 1.f + expf(-l)) : __fdiv_rn(expf(l - shift), 1.f + expf(l));
+    const float e = exp_fast(sigmoid && l > 0.f ? -l : l - shift);
+    if (!sigmoid) return e;
+    const float below = shift == 0.f ? e : exp_fast(l); // (l > 0 only with shift = 0)
+    return (l > 0.f ? 1.f : e) * rcp_fast(1.f + below);
 }
 
 // Lane l holds the vectors l, l + 32, ... of VEC experts each (N of them).
@@ -333,20 +336,23 @@ __global__ void __launch_bounds__(kScThreads, VEC * N <= 8 ? 4 : VEC * N <= 16 ?
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int at = lane + kWarp * i;
-                float b[VEC];
+                float b[VEC], y[VEC];
 #pragma unroll
                 for (int c = 0; c < VEC; ++c) b[c] = 0.f;
                 if (a.bias && at < nvec) {
                     const Vec x = reinterpret_cast<const Vec *>(a.bias)[at];
                     memcpy(b, &x, sizeof(Vec));
                 }
+                if (a.sigmoid) {
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) {
-                    const float x = v[i][c];
-                    const float s = a.sigmoid ? rcp_fast(1.f + exp_fast(-x)) : exp_fast(x - top) * inv;
-                    const float y = s + b[c];
-                    v[i][c] = x > -INFINITY && y == y ? y : -INFINITY;
+                    for (int c = 0; c < VEC; ++c) y[c] = rcp_fast(1.f + exp_fast(-v[i][c]));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < VEC; ++c) y[c] = exp_fast(v[i][c] - top) * inv;
                 }
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) // (the larger of NaN and -infinity is -infinity)
+                    v[i][c] = v[i][c] > -INFINITY ? fmaxf(y[c] + b[c], -INFINITY) : -INFINITY;
             }
         }
         if (odd) { // (warp-uniform) a row that holds NaN has no order: the first k experts
@@ -490,9 +496,9 @@ __global__ void __launch_bounds__(kScThreads, VEC * N <= 8 ? 4 : VEC * N <= 16 ?
                 const float shift = a.sigmoid ? fminf(most, 0.f) : most;
                 const float q = in ? score_of(a.sigmoid, l, shift) : 0.f;
                 const float all = warp_sum(q);
-                wt = all > 0.f ? __fdiv_rn(q, all) * a.scale : 0.f;
+                wt = all > 0.f ? q * (rcp_fast(all) * a.scale) : 0.f;
             } else if (in) {
-                wt = (a.sigmoid ? score_of(true, l, 0.f) : __fdiv_rn(expf(l - top), sum)) * a.scale;
+                wt = (a.sigmoid ? score_of(true, l, 0.f) : exp_fast(l - top) * inv) * a.scale;
             }
         }
         if (lane < k) {
