@@ -89,10 +89,41 @@ __device__ __forceinline__ float sigmoid_fast(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + ex_fast(-x)));
     return y;
 }
-__device__ __forceinline__ float normal_cdf(float x) { return 0.5f * erfcf(-0.70710678f * x); }
+// The normal distribution: its value Phi(x) and e^(-x^2 / 2).  Of the smaller
+// tail, Phi(-|x|) = t P(t) e^(-x^2 / 2) with t = 1 / (1 + |x| / sqrt 8): a
+// least-squares fit of P to erfc's scaled form, reweighted to even errors of
+// 4.3e-8; with FP32's roundings 2e-7 and (0.75 x^2 + 4) 2^-24 of the exponential,
+// relative to the tail.  (erfc in its place: 44.5 us for 32
+// at 5994 rows of 1000 to 520, whose epilogue bounds them.)
+struct Normal {
+    float cdf, bell;
+};
+__device__ __forceinline__ Normal normal_of(float x)
+{
+    float t;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(fabsf(x), 0.353553391f, 1.f)));
+    float p = -0.0295344745f;
+    p = fmaf(p, t, 0.142287454f);
+    p = fmaf(p, t, -0.243599892f);
+    p = fmaf(p, t, 0.139033515f);
+    p = fmaf(p, t, -0.0133127892f);
+    p = fmaf(p, t, 0.101343417f);
+    p = fmaf(p, t, 0.121551885f);
+    p = fmaf(p, t, 0.141187654f);
+    p = fmaf(p, t, 0.141043209f);
+    Normal n;
+    n.bell = ex_fast(-0.5f * x * x);
+    const float tail = t * p * n.bell;
+    n.cdf = x < 0.f ? tail : 1.f - tail;
+    return n;
+}
+__device__ __forceinline__ float gelu_of(float x) { return x * normal_of(x).cdf; }
 __device__ __forceinline__ float act_slope(int act, float z)
 {
-    if (act == AP_ACT_GELU) return normal_cdf(z) + z * 0.39894228f * ex_fast(-0.5f * z * z);
+    if (act == AP_ACT_GELU) {
+        const Normal n = normal_of(z);
+        return fmaf(z * 0.39894228f, n.bell, n.cdf);
+    }
     const float s = sigmoid_fast(z);
     return s * (1.f + z * (1.f - s));
 }
@@ -455,7 +486,7 @@ __device__ __forceinline__ void write_rows(const ExArgs &a, const Tile &t, int c
         for (int i = 0; i < 32; ++i) v[i / 16][i % 16] *= sigmoid_fast(v[i / 16][i % 16]);
     } else if (a.act == AP_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i / 16][i % 16] *= normal_cdf(v[i / 16][i % 16]);
+        for (int i = 0; i < 32; ++i) v[i / 16][i % 16] = gelu_of(v[i / 16][i % 16]);
     }
     if (a.residual) {
         piece_to_pairs(x.residual, pass, p);

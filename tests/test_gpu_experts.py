@@ -5,7 +5,8 @@ Products of BF16 values are exact; the tensor cores add 16 of them to the FP32
 accumulator at a time, each addend cut to the largest one's last bits: at most 17
 x 2^-23 of the sum of magnitudes S a step, so (C / 16 + 1) 17 x 2^-23 S over a
 contraction of C.  Bias and residual round by 2^-24 each (in S), 2^x and its
-reciprocal make sigmoid good to (1.5 |z| + 8) 2^-24, erfc to some 2^-21; a result
+reciprocal make sigmoid good to (1.5 |z| + 8) 2^-24, the normal distribution's tail to
+2e-7 + (0.75 z^2 + 4) 2^-24 of itself; a result
 rounds by 2^-8 to BF16.  Errors of z reach the result through |act'| <= 1.13 (for
 the gated product: times the other half, and the other way).
 """
@@ -160,6 +161,34 @@ RAGGED = [0, 1, 15, 16, 17, 0, 255, 256, 257, 31, 33, 300, 0]
 
 def test_one_plain_product():
     check_forward(Rows([128]), 64, 128, pre=False)
+
+
+def test_gelu_of_all_sizes():
+    """z from -20 to 20 through a unit weight: the smaller tail within 2e-7 + (0.75 z^2 + 8) u of itself (below 2^-120: 0),
+    the value z Phi(z) with one rounding more, 1 - tail another."""
+    z = torch.linspace(-20, 20, 4001, device="cuda").bfloat16()
+    n = z.numel()
+    x = torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = z
+    W = torch.zeros(1, 8, 8, dtype=torch.bfloat16, device="cuda")
+    W[0, :, 0] = 1
+    seg = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1,), n, dtype=torch.int32, device="cuda")
+    f = f64(z)
+    got = f64(ap.expert_linear(x, W, *seg, act="gelu", dtype=torch.float32))[:, 3]
+    e = layer.act("gelu", f)
+    tail = np.abs(f) * layer._cdf(-np.abs(f))
+    rel = 2e-7 + (0.75 * f * f + 8) * U
+    assert np.all(np.abs(got - e) <= rel * tail + 2 * U * np.abs(e) + 20 * 2.0 ** -120)
+    pre = torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda")
+    pre[:, 0] = z
+    dy = torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda")
+    dy[:, 0] = 1
+    W = torch.zeros(1, 8, 8, dtype=torch.bfloat16, device="cuda")
+    W[0, 0, :] = 1
+    got = f64(ap.expert_linear_dx(dy, W, *seg, act="gelu", pre=pre, dtype=torch.float32))[:, 0]
+    e = layer.act_backward("gelu", f, np.ones_like(f))
+    bell = np.abs(f) * np.exp(-0.5 * f * f) / np.sqrt(2 * np.pi)
+    assert np.all(np.abs(got - e) <= rel * (layer._cdf(-np.abs(f)) + 2 * bell) + 2 * U * np.abs(e) + 20 * 2.0 ** -120)
 
 
 def test_one_product_of_a_gradient():
