@@ -985,23 +985,37 @@ bool mappable(const void *p, int64_t ld, int64_t more = 0)
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && more % 8 == 0;
 }
 
-template <Op OP, bool PAIR = false>
-ap_status launch_experts(const char *who, const ExMaps &m, ExArgs a, int64_t tiles, cudaStream_t st)
+// The stages that fit the shared memory, and its bytes: as many as the kernel's attribute allows (0: an error).
+template <Op OP, bool PAIR> size_t stages_of(ExArgs &a)
 {
     const auto kernel = k_experts<OP, PAIR>;
-    cudaFuncAttributes attr;
-    static const int fixed = cudaFuncGetAttributes(&attr, (const void *)kernel) == cudaSuccess ? (int)attr.sharedSizeBytes : -1;
-    if (fixed < 0) return cuda_fail(cudaGetLastError(), who);
-    static const cudaError_t set =
-        cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - fixed);
-    if (set != cudaSuccess) return cuda_fail(set, who);
-    const int stage = 2 * kPanel + a.columns * (PAIR ? 64 : 128);
-    const int room = kMaxSmem - fixed - 1024;
+    static const int fixed = [&] {
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, (const void *)kernel) != cudaSuccess) return -1;
+        const int n = (int)attr.sharedSizeBytes;
+        return cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - n) == cudaSuccess ? n
+                                                                                                                                    : -1;
+    }();
+    if (fixed < 0) return 0;
+    const int stage = 2 * kPanel + a.columns * (PAIR ? 64 : 128), room = kMaxSmem - fixed - 1024;
     a.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
-    const size_t smem = (size_t)a.stages * stage + 1024;
+    return (size_t)a.stages * stage + 1024;
+}
+// Pairs of blocks that the stream's SMs take at once (a partition may take none).
+template <Op OP> int pairs_of(ExArgs a, cudaStream_t st)
+{
+    const size_t smem = stages_of<OP, true>(a);
+    return smem ? cluster_count((const void *)k_experts<OP, true>, kExThreads, smem, 2, st) : 0;
+}
+
+// `pairs`: that many at most, of two blocks each; 0: single blocks
+template <Op OP, bool PAIR = false>
+ap_status launch_experts(const char *who, const ExMaps &m, ExArgs a, int64_t tiles, int pairs, cudaStream_t st)
+{
+    const auto kernel = k_experts<OP, PAIR>;
+    const size_t smem = stages_of<OP, PAIR>(a);
+    if (!smem) return cuda_fail(cudaGetLastError(), who);
     if constexpr (PAIR) {
-        const int pairs = cluster_count((const void *)kernel, kExThreads, smem, 2, st);
-        if (pairs < 1) return fail(AP_ENOTSUP, "%s: the stream's SMs take no pair of blocks", who);
         launch_cluster(kernel, 2 * (int)(tiles < pairs ? tiles : pairs), kExThreads, smem, 2, st, m, a);
     } else {
         const int sms = sm_count();
@@ -1028,29 +1042,31 @@ int64_t repitch_bytes(const void *p, int64_t ld, int64_t lde, int64_t rows, int 
 // Copies operands that tensor maps do not take into the work space, one after the other.
 struct Repitch {
     const char *who;
-    void *scratch;
-    int64_t left;
+    char *scratch;
     cudaStream_t st;
     // `count` lots of `per` rows, *lde apart (nullptr: one lot)
     ap_status take(const bf16_t **p, int64_t *ld, int64_t *lde, int64_t per, int count, int cols, const int32_t *live)
     {
         const int64_t rows = per * count, need = repitch_bytes(*p, *ld, lde ? *lde : 0, rows, cols), pitch = (cols + 7) / 8 * 8;
         if (!need) return AP_OK;
-        if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 15)) return fail(AP_EINVAL, "%s: scratch is NULL or not aligned", who);
-        if (left < need)
-            return fail(AP_EINVAL, "%s: %lld bytes of scratch left, %lld needed", who, (long long)left, (long long)need);
-        bf16_t *to = static_cast<bf16_t *>(scratch);
+        bf16_t *to = reinterpret_cast<bf16_t *>(scratch);
         const int64_t want = (rows + 7) / 8, most = (int64_t)sm_count() * 8;
         launch(k_repitch, (int)(want < most ? want : most), 256, 0, st, *p, *ld, lde ? *lde : 0, per, rows, cols, live, to, pitch);
         AP_CHECK_LAUNCH(who);
-        scratch = static_cast<char *>(scratch) + need;
-        left -= need;
+        scratch += need;
         *p = to;
         *ld = pitch;
         if (lde) *lde = per * pitch;
         return AP_OK;
     }
 };
+ap_status scratch_ok(const char *who, const void *scratch, int64_t have, int64_t need)
+{
+    if (!need) return AP_OK;
+    if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 15)) return fail(AP_EINVAL, "%s: scratch is NULL or not aligned", who);
+    if (have < need) return fail(AP_EINVAL, "%s: scratch of %lld bytes, %lld needed", who, (long long)have, (long long)need);
+    return AP_OK;
+}
 bool odd_address(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
 // Columns of a tile: rows of the output at most, by what an expert has on the average.
@@ -1064,22 +1080,30 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, void *scrat
 {
     if (a.E == 1) a.lde = a.ldw * (op == kForward ? a.F * halves : a.K); // (of no account)
     const int wide = op == kForward ? a.F * halves : a.K, deep = op == kForward ? a.K : a.F; // of W[e]
-    Repitch re = {who, scratch, scratch_bytes, st};
-    if (const ap_status r = re.take(&a.x, &a.ldx, nullptr, a.rows, 1, a.K, nullptr); r != AP_OK) return r;
-    if (const ap_status r = re.take(&a.W, &a.ldw, &a.lde, wide, a.E, deep, a.live); r != AP_OK) return r;
+    if (const ap_status r = scratch_ok(who, scratch, scratch_bytes,
+                                       repitch_bytes(a.x, a.ldx, 0, a.rows, a.K) +
+                                           repitch_bytes(a.W, a.ldw, a.lde, (int64_t)wide * a.E, deep));
+        r != AP_OK)
+        return r;
     a.columns = columns_for(a.rows, a.E);
     a.vec_out = !odd_address(a.out, 16) && a.ldo % 8 == 0 && a.F % 8 == 0;
     a.vec_pre = !odd_address(a.pre, 16) && a.ldpre % 8 == 0 && a.F % 8 == 0;
     a.vec_res = !odd_address(a.residual, 16) && a.ldres % 8 == 0 && a.F % 8 == 0;
-    // Two blocks to a tile of 256 features share its rows' operand: 32 KB from L2 for 48 a product.
-    const bool pair = a.columns == 256 && a.F * (op == kForward ? halves : 1) > kLanes;
-    const int per = (op == kForward && halves == 2 ? kLanes / 2 : kLanes) * (pair ? 2 : 1);
+    // Two blocks to a tile of 256 features share its rows' operand: 32 KB from L2 for 48 a product (65536 rows of 2048 over
+    // 128 experts: 476 us for 545).
+    int pairs = 0;
+    if (a.columns == 256 && a.F * (op == kForward ? halves : 1) > kLanes)
+        pairs = op == kForward ? pairs_of<kForward>(a, st) : pairs_of<kRows>(a, st);
+    const int per = (op == kForward && halves == 2 ? kLanes / 2 : kLanes) * (pairs ? 2 : 1);
     a.tiles_f = (a.F + per - 1) / per;
     const int64_t tiles = (a.rows / a.columns + a.E) * (int64_t)a.tiles_f;
     if (tiles >= INT32_MAX) return fail(AP_EINVAL, "%s: %lld tiles are more than one launch takes", who, (long long)tiles);
+    Repitch re = {who, static_cast<char *>(scratch), st};
+    if (const ap_status r = re.take(&a.x, &a.ldx, nullptr, a.rows, 1, a.K, nullptr); r != AP_OK) return r;
+    if (const ap_status r = re.take(&a.W, &a.ldw, &a.lde, wide, a.E, deep, a.live); r != AP_OK) return r;
     ExMaps m = {};
     const uint64_t ex[2] = {(uint64_t)a.K, (uint64_t)a.rows}, px[1] = {(uint64_t)a.ldx};
-    const uint32_t bx[2] = {64, a.columns >= 128 ? 64u : 32u}, ball[2] = {64, (uint32_t)(pair ? a.columns / 2 : a.columns)};
+    const uint32_t bx[2] = {64, a.columns >= 128 ? 64u : 32u}, ball[2] = {64, (uint32_t)(pairs ? a.columns / 2 : a.columns)};
     bool ok = make_map(&m.x, a.x, 2, ex, px, bx) && make_map(&m.xx, a.x, 2, ex, px, ball);
     // One copy for a gated product's features needs whole sixteens: 8 copies of 16 lines took 957 us where one takes 590
     a.by16 = op == kForward && halves == 2 && a.F % 16 == 0;
@@ -1094,10 +1118,10 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, void *scrat
         ok = ok && make_map(&m.w, a.W, 3, ew, pw, bw);
     }
     if (!ok) return fail(AP_ENOTSUP, "%s: no tensor map of these sizes", who);
-    if (pair)
-        return op == kForward ? launch_experts<kForward, true>(who, m, a, tiles, st)
-                              : launch_experts<kRows, true>(who, m, a, tiles, st);
-    return op == kForward ? launch_experts<kForward>(who, m, a, tiles, st) : launch_experts<kRows>(who, m, a, tiles, st);
+    if (pairs)
+        return op == kForward ? launch_experts<kForward, true>(who, m, a, tiles, pairs, st)
+                              : launch_experts<kRows, true>(who, m, a, tiles, pairs, st);
+    return op == kForward ? launch_experts<kForward>(who, m, a, tiles, 0, st) : launch_experts<kRows>(who, m, a, tiles, 0, st);
 }
 
 } // namespace
@@ -1217,11 +1241,6 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
         a.x = (const bf16_t *)dy, a.W = (const bf16_t *)x, a.ldx = ldy, a.ldw = ldx;
         a.seg = d_seg_off, a.live = d_live, a.out = dW, a.d_status = d_status, a.rows = rows, a.E = E, a.F = N, a.K = K;
         a.out_f32 = dw_dtype == AP_DTYPE_F32, a.add = accumulate != 0;
-        if (rows > 0) {
-            Repitch re = {who, scratch, scratch_bytes, st};
-            if (const ap_status r = re.take(&a.x, &a.ldx, nullptr, rows, 1, N, nullptr); r != AP_OK) return r;
-            if (const ap_status r = re.take(&a.W, &a.ldw, nullptr, rows, 1, K, nullptr); r != AP_OK) return r;
-        }
         a.columns = K > 128 ? 256 : K > 64 ? 128 : 64;
         a.tiles_f = (N + kLanes - 1) / kLanes;
         auto tiles_of = [&] { return (int64_t)E * a.tiles_f * ((K + a.columns - 1) / a.columns); };
@@ -1231,6 +1250,13 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
         if (tiles >= INT32_MAX) return fail(AP_EINVAL, "%s: %lld tiles are more than one launch takes", who, (long long)tiles);
         ExMaps m = {};
         if (rows > 0) {
+            if (const ap_status r = scratch_ok(who, scratch, scratch_bytes,
+                                               repitch_bytes(dy, ldy, 0, rows, N) + repitch_bytes(x, ldx, 0, rows, K));
+                r != AP_OK)
+                return r;
+            Repitch re = {who, static_cast<char *>(scratch), st};
+            if (const ap_status r = re.take(&a.x, &a.ldx, nullptr, rows, 1, N, nullptr); r != AP_OK) return r;
+            if (const ap_status r = re.take(&a.W, &a.ldw, nullptr, rows, 1, K, nullptr); r != AP_OK) return r;
             // two chunks of 64 columns in a copy where rows are whole chunks: a row's end is no border to such a map
             a.chunk_x = N % 64 == 0, a.chunk_w = K % 64 == 0;
             const uint64_t ey[3] = {a.chunk_x ? 64 : (uint64_t)N, (uint64_t)rows, (uint64_t)N / 64}, py[2] = {(uint64_t)a.ldx, 64};
@@ -1241,7 +1267,7 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
                 (a.chunk_x && !make_map(&m.xx, a.x, 3, ey, py, box)) || (a.chunk_w && !make_map(&m.ww, a.W, 3, ex, px, box)))
                 return fail(AP_ENOTSUP, "%s: no tensor map of these sizes", who);
         }
-        if (const ap_status s = launch_experts<kWeights>(who, m, a, tiles, st); s != AP_OK) return s;
+        if (const ap_status s = launch_experts<kWeights>(who, m, a, tiles, 0, st); s != AP_OK) return s;
     }
     if (dbias) {
         launch(k_expert_bias, dim3((unsigned)((N + 63) / 64), (unsigned)E), 256, 0, st, (const bf16_t *)dy, ldy, d_seg_off, d_live, rows,

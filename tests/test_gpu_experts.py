@@ -509,3 +509,39 @@ def test_refusals():
             ("status", lambda: ap.expert_linear(x, W, n, n, status=torch.zeros(1)))):
         with pytest.raises(ValueError, match=match):
             call()
+
+
+@pytest.mark.parametrize("sms", [8, 24])
+def test_on_partitions(sms):
+    """Streams of SM partitions, which take fewer pairs of blocks or none: the bits of an ordinary stream."""
+    import ctypes
+    from activation_paging_gb300 import build as cuda_build
+    lib = ctypes.CDLL(cuda_build.BENCH_LIB)
+    vp, ip = ctypes.c_void_p, ctypes.c_int
+    s1, s2, c1, c2, n1, n2 = vp(), vp(), vp(), vp(), ip(), ip()
+    lib.apb_green_split.restype = ip
+    lib.apb_green_split.argtypes = [ip, ip] + [ctypes.POINTER(vp)] * 2 + [ctypes.POINTER(ip)] * 2 + [ctypes.POINTER(vp)] * 2
+    lib.apb_green_destroy.restype = ip
+    lib.apb_green_destroy.argtypes = [vp] * 4
+    rc = lib.apb_green_split(torch.cuda.current_device(), sms, *(ctypes.byref(t) for t in (s1, s2, n1, n2, c1, c2)))
+    if rc < 0:
+        pytest.skip(f"the driver lacks green-context entry point {-rc} of apb_green_split")
+    assert rc == 0
+    r = Rows([513, 3, 900, 64])
+    x, W, dy, z = r.make(256), r.weights(512, 256), r.make(512), r.make(512)
+    logits = torch.randn(3000, 64, generator=r.g, device="cuda")
+
+    def calls():
+        return [ap.expert_linear(x, W, *r.args, act="swiglu"), ap.expert_linear_dx(dy, W, *r.args, act="swiglu", pre=z),
+                ap.expert_linear_dw(dy, x, *r.args), *ap.route_scored(logits, 8, groups=8, top_groups=4)]
+    first = calls()
+    for h in (s1, s2):
+        s = torch.cuda.ExternalStream(h.value)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got = calls()
+        torch.cuda.synchronize()
+        for a, b in zip(first, got):
+            assert torch.equal(a, b)  # (every row is some expert's)
+    torch.cuda.synchronize()
+    assert lib.apb_green_destroy(s1, s2, c1, c2) == 0
