@@ -402,7 +402,8 @@ class AdamW:
     of 256; ``state`` gives them with the step words (a checkpoint, or buffers
     to use): ``m``, ``v`` (float32, or int8 and uint8 with float32 ``m_scale``
     and ``v_scale``, one for each 256 elements) and ``step`` (int32 [2]: steps
-    taken, 0)."""
+    taken, 0).  The calls of one optimizer are to follow one another (one stream,
+    or events between)."""
 
     BLOCK = 256
 

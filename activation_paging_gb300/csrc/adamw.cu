@@ -19,6 +19,7 @@
 // nearest would never let it move.  A positive v never gets code 0, so no
 // division by eps alone comes from the coding.
 #include <cuda_bf16.h>
+#include <float.h>
 #include <math.h>
 
 #include <type_traits>
@@ -363,7 +364,8 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocksOf<BITS>) k_adamw(const _
             // a block with a value that is no number becomes NaN whole
             const float sm = top_m < INFINITY ? top_m * (1.f / (127.f * 127.f)) : NAN;
             const float sv = top_r < INFINITY ? top_r * (1.f / (255.f * 255.f)) : NAN;
-            const float im = sm > 0.f ? __fdiv_rn(1.f, sm) : 0.f, iv = sv > 0.f ? __fdiv_rn(1.f, sv) : 0.f;
+            // (scales below the normal numbers, of moments below 2^-112, give codes of 0)
+            const float im = sm >= FLT_MIN ? div_fast(1.f, sm) : 0.f, iv = sv >= FLT_MIN ? div_fast(1.f, sv) : 0.f;
             const uint32_t key = mix((uint32_t)(tab.base + x.i) + seeded);
             uint32_t cm[8], cv[8];
 #pragma unroll

@@ -763,8 +763,10 @@ __global__ void __launch_bounds__(kExThreads, 1)
     if (wid == 0) {
         // ---- fetch: stage by stage, as they fall empty
         if (elect_one()) {
-            tma_prefetch_map(&m.xx);
-            tma_prefetch_map(OP == kWeights ? &m.ww : &m.w);
+            if (a.rows > 0) {
+                tma_prefetch_map(OP == kWeights && !a.chunk_x ? &m.x : &m.xx);
+                tma_prefetch_map(OP == kWeights && a.chunk_w ? &m.ww : &m.w);
+            }
             uint32_t count = 0, s = 0, turn = 0; // stages fetched; ring position and its turn
             bool ok = true;
             for (; ok && w.find(a.E); w.next()) {

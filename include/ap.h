@@ -3,7 +3,9 @@
  * a paged activation stash (libap.so).
  *
  * The path: route_topk -> dispatch_permute -> stash_push ... stash_pop ->
- * combine_unpermute, all on one GPU.  Every call is asynchronous on the CUDA
+ * combine_unpermute, all on one GPU; around it the operators of a layer's
+ * training step: embed, route_balance and route_scored, expert_linear,
+ * adamw_step, and their gradients.  Every call is asynchronous on the CUDA
  * stream it is given (passed as `void *`, a cudaStream_t; NULL = legacy
  * default stream) and launches only this library's kernels.  No call
  * allocates device memory: the caller owns every buffer (device pointers
@@ -385,7 +387,8 @@ ap_status ap_route_bias_step(float *bias, int32_t *counts, int32_t E, float rate
  *   bias     [E, N] ([E, 2 N]) float32, contiguous (device, read) or NULL
  *   residual [rows, N] bf16, ldres apart (device, read) or NULL; may be out
  *   pre      [rows, N] ([rows, 2 N]) bf16, ldpre apart (device, written) or NULL
- *   out      [rows, N] of out_dtype (BF16 or F32), ldo apart (device, written)
+ *   out      [rows, N] of out_dtype (BF16 or F32), ldo apart (device, written);
+ *            neither out nor pre may overlap x, W, bias or one another
  *   scratch  device work space of ap_expert_linear_scratch_bytes() bytes, 16-byte
  *            aligned; its contents need no initialisation.  Operands whose bases
  *            lie on 16 bytes and whose pitches are multiples of 8 elements need 0
@@ -421,7 +424,7 @@ ap_status ap_expert_linear(const void *x, int64_t ldx, int64_t rows, int32_t E, 
  *   residual [rows, K] bf16, ldres apart (device, read) or NULL: further
  *            gradients of x; may be dx where there is no SWIGLU
  *   dx       [rows, K] ([rows, 2 K]) of dx_dtype, ldx apart (device, written);
- *            BF16 dx may be pre
+ *            BF16 dx may be pre, else it may overlap no other argument
  * Segments, limits and the rest as ap_expert_linear. */
 ap_status ap_expert_linear_dx(const void *dy, int64_t ldy, int64_t rows, int32_t E, int32_t N, int32_t K,
                               const int32_t *d_seg_off, const int32_t *d_live, const void *W, int64_t ldw, int64_t lde,
@@ -513,8 +516,8 @@ ap_status ap_embed_backward(const void *dout, int64_t dout_ld, int32_t dout_dtyp
  * sqrt(v) / v_scale) + r'), the latter at least 1 where v > 0.  r and r' are the
  * low and the high 16 bits of u / 65536, u = mix(e * 0x9E3779B9 + mix(i +
  * mix(seed + 0x9E3779B9 t))) for element e of the call's tensor i, all modulo
- * 2^32, with mix the finalizer of MurmurHash3.  A block with a moment that is not
- * finite becomes NaN whole.
+ * 2^32, with mix the finalizer of MurmurHash3.  A scale below 2^-126 counts as 0.
+ * A block with a moment that is not finite becomes NaN whole.
  *
  *   tensors  host array of n: device addresses and elements of each.  param of
  *            param_dtype, grad of grad_dtype, master float32 (config.master = 1,
