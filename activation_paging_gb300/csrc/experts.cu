@@ -13,7 +13,7 @@
 // that are not there (with rows on the lanes: by 128).  It also makes the
 // epilogue's lanes neighbours in a row of the output.
 // A block per SM walks the tiles: one warp fetches operands through a ring of
-// stages, one issues the products, four read the accumulator and write the
+// stages, one issues the products, eight read the accumulator and write the
 // outputs while the next tile's products run into a second accumulator.
 // Outputs and what the epilogue reads (residual, pre-activations) pass through
 // shared memory as 8 x 8 matrices, transposed, so that memory sees rows' pieces
@@ -57,6 +57,7 @@ struct ExArgs {
     const int32_t *seg, *live;
     const float *bias;
     const bf16_t *residual;
+    float *db;             // kWeights: the bias's gradient or nullptr
     bf16_t *pre;           // z: written forwards, read backwards
     void *out;
     int64_t ldres, ldpre, ldo;
@@ -739,7 +740,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             bar_init(smem_addr(&s_full[s]), 1);
-            bar_init(smem_addr(&s_empty[s]), 1);
+            bar_init(smem_addr(&s_empty[s]), kPass2 && a.db ? 3 : 1);
             if (kPass2) bar_init(smem_addr(&s_ready[s]), 2);
         }
         for (int s = 0; s < 2; ++s) {
@@ -839,11 +840,18 @@ __global__ void __launch_bounds__(kExThreads, 1)
             }
         }
     } else if (kPass2 && wid < 4) {
-        // ---- pass stages on, with zeros for the lines behind an expert's last row, which are others' rows
+        // ---- pass stages on, with zeros for the lines behind an expert's last row, which are others' rows; and add up the
+        // bias's gradient, each row of tiles in one of them: always the first would be the same SMs' wherever `across` and the
+        // grid have a factor in common, so it moves on from round to round of the grid, or else from row to row (65536 rows, 128
+        // experts, 2048 x 1024: 463 us for 546; without a bias 462). A warp takes a panel of 64 features, a lane 8 of them of
+        // every fourth line, in two sums a stage
         uint32_t s = 0, turn = 0;
         bool ok = true;
         for (; ok && w.find(a.E); w.next()) {
             const Tile t = tile_of<OP, PAIR>(a, w, rank);
+            const uint32_t across = ceil_div(a.K, a.columns), c = t.c0 / a.columns, first = w.t - c, by = w.step;
+            const bool adds = a.db && c == first / (by % across ? across : by) % across;
+            float sum[8] = {};
             for (int step = 0; step < t.steps; ++step) {
                 ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&s_full[s]), turn & 1, dead));
                 if (!ok) break;
@@ -858,11 +866,41 @@ __global__ void __launch_bounds__(kExThreads, 1)
                     __syncwarp();
                 }
                 if (lane == 0) bar_arrive(smem_addr(&s_ready[s]));
+                if (a.db) {
+                    if (adds) {
+                        const uint8_t *panel = stages + (size_t)s * stage_bytes + (wid - 2) * kPanel;
+                        float part[2][8] = {};
+#pragma unroll
+                        for (int i = 0; i < kDepth / 4; ++i) {
+                            const int r = 4 * i + (lane >> 3);
+                            const uint4 x = *reinterpret_cast<const uint4 *>(panel + r * 128 + (((lane ^ r) & 7) << 4));
+                            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                part[i & 1][2 * j] += low(y[j]);
+                                part[i & 1][2 * j + 1] += high(y[j]);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sum[j] += part[0][j] + part[1][j];
+                    }
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(smem_addr(&s_empty[s])); // (the stage is read)
+                }
                 if (++s == (uint32_t)a.stages) {
                     s = 0;
                     ++turn;
                 }
             }
+            if (adds)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
+                    sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
+                    const int f = t.f0 + (wid - 2) * 64 + lane * 8 + j;
+                    float *to = a.db + (int64_t)t.e * a.F + f;
+                    if (lane < 8 && f < a.F) *to = ok ? a.add ? *to + sum[j] : sum[j] : NAN;
+                }
         }
     } else if (wid >= 4) {
         // ---- write
@@ -947,7 +985,8 @@ __global__ void __launch_bounds__(256) k_repitch(const bf16_t *src, int64_t ld, 
     }
 }
 
-// db[e] (+)= the sum of the expert's rows of dy: a block takes 64 columns of an
+// db[e] (+)= the sum of the expert's rows of dy, where the weights' gradient is
+// not wanted (with it, its stages are added up): a block takes 64 columns of an
 // expert, eight warps every eighth row, two columns a lane.
 __global__ void __launch_bounds__(256) k_expert_bias(const bf16_t *dy, int64_t ld, const int32_t *seg, const int32_t *live, int64_t rows,
                                                      int N, float *db, bool add)
@@ -1242,7 +1281,7 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
         ExArgs a = {};
         a.x = (const bf16_t *)dy, a.W = (const bf16_t *)x, a.ldx = ldy, a.ldw = ldx;
         a.seg = d_seg_off, a.live = d_live, a.out = dW, a.d_status = d_status, a.rows = rows, a.E = E, a.F = N, a.K = K;
-        a.out_f32 = dw_dtype == AP_DTYPE_F32, a.add = accumulate != 0;
+        a.out_f32 = dw_dtype == AP_DTYPE_F32, a.add = accumulate != 0, a.db = dbias;
         a.columns = K > 128 ? 256 : K > 64 ? 128 : 64;
         a.tiles_f = (N + kLanes - 1) / kLanes;
         auto tiles_of = [&] { return (int64_t)E * a.tiles_f * ((K + a.columns - 1) / a.columns); };
@@ -1271,7 +1310,7 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
         }
         if (const ap_status s = launch_experts<kWeights>(who, m, a, tiles, 0, st); s != AP_OK) return s;
     }
-    if (dbias) {
+    if (dbias && !dW) {
         launch(k_expert_bias, dim3((unsigned)((N + 63) / 64), (unsigned)E), 256, 0, st, (const bf16_t *)dy, ldy, d_seg_off, d_live, rows,
                N, dbias, accumulate != 0);
         AP_CHECK_LAUNCH("expert_linear_dw bias launch");

@@ -338,6 +338,26 @@ def test_gradient_of_odd_weights(N, K, add):
     check_weights(Rows([3, 130]), 64, 72, xp=73, add=add, dtype=torch.bfloat16)
 
 
+@pytest.mark.parametrize("N", [8, 64, 100, 128, 130, 512])
+@pytest.mark.parametrize("add", [True, False])
+def test_gradient_of_the_bias_alone(N, add):
+    """The C call without dW: the same sums up to their order."""
+    import ctypes
+    r = Rows(RAGGED, gap=2)
+    dy = r.make(N)
+    db = torch.randn(r.E, N, generator=r.g, device="cuda")
+    old = f64(db)
+    rc = ap.lib().ap_expert_linear_dw(ctypes.c_void_p(dy.data_ptr()), N, None, 8, r.rows, r.E, N, 8, ctypes.c_void_p(r.args[0].data_ptr()),
+                                      ctypes.c_void_p(r.args[1].data_ptr()), int(add), None, 2, ctypes.c_void_p(db.data_ptr()), None, 0,
+                                      None, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == 0
+    torch.cuda.synchronize()
+    _, e, _, size = layer.expert_linear_dw(zeros_off(f64(dy), r.on), np.zeros((r.rows, 8)), r.seg, r.live, r.E)
+    if add:
+        e, size = e + old, size + np.abs(old)
+    assert np.all(np.abs(f64(db) - e) <= (300 / 8 + 10) * U * size)
+
+
 def test_neighbours_do_not_leak():
     """NaN in another expert's weights and rows, and in rows of no expert, stays there."""
     for K in (96, 99):
