@@ -309,10 +309,11 @@ ap_status ap_route_backward(const float *logits, int64_t T, int32_t E, int32_t k
  * Ties go to the lower group and the lower expert id.  Choices compare the
  * values of the formulas in double precision (wherever single precision does
  * not tell two of them apart), and the logits themselves where there is no bias
- * and groups go by one expert, so single precision's rounding changes no ids.  An expert whose logit or c is -infinity (or whose bias is NaN) is
- * chosen only if fewer than k others are left, lowest ids first, with w = 0; a
- * group with fewer than group_best others has the score -infinity.  A row that
- * holds NaN (with softmax: or +infinity) gets the experts 0 .. k-1 and w =
+ * and groups go by one expert, so single precision's rounding changes no ids.
+ * An expert whose logit or c is -infinity (or whose bias is NaN) is chosen only
+ * if fewer than k others are left, lowest ids first, with w = 0; a group with
+ * fewer than group_best others has the score -infinity.  A row that holds NaN
+ * (with softmax: or +infinity) gets the experts 0 .. k-1 and w =
  * NaN.  The relative error of w is at most (2 d + E / 32 + 40) 2^-24 with d the
  * distance of the logit from the row's largest (renorm: from the largest
  * chosen; sigmoid without renorm: d = 0); below 2^-120 w may be 0.
@@ -378,8 +379,9 @@ ap_status ap_route_bias_step(float *bias, int32_t *counts, int32_t E, float rate
  * give equal bits.  The tensor cores' FP32 sums cut instead of rounding: their
  * error is about 1.1e-9 of the result's size for each place of the contraction
  * (for numbers of one sign up to 5e-9), below the rounding to BF16 up to some
- * 10^6 places; FP32 weights' gradients are added up by sections of 2048 rows.  Should operands not arrive within a bounded wait (no input
- * leads to that), AP_FLAG_CORRUPT is set and the rows that lack them get NaN.
+ * 10^6 places; FP32 weights' gradients are added up by sections of 2048 rows.
+ * Should operands not arrive within a bounded wait (no input leads to that),
+ * AP_FLAG_CORRUPT is set and the rows that lack them get NaN.
  *
  *   x        [rows, K] bf16, ldx elements apart (device, read)
  *   W        [E, N, K] bf16 (SWIGLU: [E, 2 N, K]), rows ldw and experts lde
