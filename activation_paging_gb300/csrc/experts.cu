@@ -41,7 +41,8 @@ constexpr int kMaxStages = 10;
 // The tensor cores cut what they add to an accumulator: its error grows with the
 // contraction, 1.1e-9 of it for each place (9.2e-6 at 8192).  FP32 weights'
 // gradients are therefore added up over sections of 2048 rows, which the writers
-// add with rounding (2.1e-6, and the products still hide the writing).
+// add with rounding (2.1e-6; by 1024 1.1e-6, but then the products do not hide the
+// writing: 262144 rows over 128 experts, 1024 x 2048 1135 us for 1011).
 constexpr int kSection = 32; // stages
 constexpr int kMaxSmem = 232448;
 constexpr int kMaxExperts = 1024;
@@ -1301,12 +1302,14 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
         a.x = (const bf16_t *)dy, a.W = (const bf16_t *)x, a.ldx = ldy, a.ldw = ldx;
         a.seg = d_seg_off, a.live = d_live, a.out = dW, a.d_status = d_status, a.rows = rows, a.E = E, a.F = N, a.K = K;
         a.out_f32 = dw_dtype == AP_DTYPE_F32, a.add = accumulate != 0, a.db = dbias;
-        a.columns = K > 128 ? 256 : K > 64 ? 128 : 64;
         a.tiles_f = (N + kLanes - 1) / kLanes;
-        auto tiles_of = [&] { return (int64_t)E * a.tiles_f * ((K + a.columns - 1) / a.columns); };
-        if (tiles_of() < 2 * sm_count()) a.columns = K > 64 ? 128 : 64; // few tiles: smaller ones, for more SMs
+        const auto tiles_of = [&](int columns) { return (int64_t)E * a.tiles_f * ((K + columns - 1) / columns); };
+        const auto rounds = [&](int columns) { return (tiles_of(columns) + sm_count() - 1) / sm_count(); };
+        // A stage of 256 columns takes 0.43 us, of 128 or 64 0.34 (issuing bounds these): by rounds of tiles over the SMs. 8
+        // experts of 4096 rows, 1024 x 1024 (256 or 512 tiles): 79 us by 256, 96 by 128; of 8192, 512 x 512 (64 or 128): 99 and 75.
+        a.columns = K <= 64 ? 64 : K > 128 && 4 * rounds(256) <= 3 * rounds(128) ? 256 : 128;
         a.vec_out = !odd_address(dW, 16) && K % (a.out_f32 ? 4 : 8) == 0;
-        const int64_t tiles = tiles_of();
+        const int64_t tiles = tiles_of(a.columns);
         if (tiles >= INT32_MAX) return fail(AP_EINVAL, "%s: %lld tiles are more than one launch takes", who, (long long)tiles);
         ExMaps m = {};
         if (rows > 0) {
