@@ -402,8 +402,12 @@ class AdamW:
     of 256; ``state`` gives them with the step words (a checkpoint, or buffers
     to use): ``m``, ``v`` (float32, or int8 and uint8 with float32 ``m_scale``
     and ``v_scale``, one for each 256 elements) and ``step`` (int32 [2]: steps
-    taken, 0).  The calls of one optimizer are to follow one another (one stream,
-    or events between)."""
+    taken, 0).  All of them are used where they were when the optimizer was made
+    (gradients: when they were bound): a call refuses tensors that have moved
+    since (``p.data = ...``, another tensor in ``state``), so copy into them, or
+    make a new optimizer with ``state``.  A captured graph does not look again.
+    The calls of one optimizer are to follow one another (one stream, or events
+    between)."""
 
     BLOCK = 256
 
@@ -445,6 +449,8 @@ class AdamW:
             else:
                 self.state[name] = torch.zeros(shape, dtype=dtype, device=dev)
         self._apart([self.state[n] for n in need])
+        self._names = list(need)
+        self._held = self._hold(self._written())
         self._table = (_lib.AdamWTensor * len(self.params))()
         size = self.state["m"].element_size()
         at = {n: self.state[n].data_ptr() for n in need}
@@ -465,6 +471,29 @@ class AdamW:
         self._scratch_bytes = n.value
         self._scratch = torch.empty(n.value, dtype=torch.uint8, device=dev)
         self._norm = torch.empty(2, dtype=torch.float32, device=dev)
+
+    def _written(self):
+        """What a step writes."""
+        return [*self.params, *(self.master or ()), *map(self.state.__getitem__, self._names)]
+
+    @staticmethod
+    def _hold(tensors):
+        """(addresses, their indices, storages): as long as these are held, an address stays that of the same memory."""
+        return list(map(torch.Tensor.data_ptr, tensors)), list(range(len(tensors))), [t.untyped_storage() for t in tensors]
+
+    @staticmethod
+    def _stay(tensors, held, what: str):
+        """Refuses tensors that are not where the table has them (one call compares all: 32 ns each, 61 by data_ptr())."""
+        at, all_of, _ = held
+        if len(tensors) != len(at) or not torch._C._tensors_data_ptrs_at_indices_equal(tensors, at, all_of):
+            raise ValueError(what)
+
+    def _stay_written(self):
+        self._stay(self._written(), self._held, "params, master copies or state have moved since the optimizer was made: "
+                                                "copy into them, or make a new optimizer")
+
+    def _stay_grads(self):
+        self._stay(self.grads, self._grads_held, "grads have moved since they were bound: bind them again")
 
     @staticmethod
     def _apart(tensors):
@@ -487,6 +516,7 @@ class AdamW:
         for e, g in zip(self._table, grads):
             e.grad = g.data_ptr()
         self.grads, self._cfg.grad_dtype = grads, _ROW_TYPES[kind]
+        self._grads_held = self._hold(grads)
 
     @staticmethod
     def _word(t, name: str):
@@ -501,6 +531,7 @@ class AdamW:
         """[norm of all gradients, factor that clips it to ``max_norm``] (float32 [2]; the factor is 1 without clipping,
         NaN where the norm is not finite): pass ``out[1:]`` as ``scale`` to ``step``.  Without ``out`` the tensor is the
         optimizer's own, which the next call writes again."""
+        self._stay_grads()
         if max_norm is not None and not max_norm > 0:
             raise ValueError(f"max_norm must be positive, got {max_norm}")
         if out is None:
@@ -515,6 +546,8 @@ class AdamW:
         """One step.  ``lr``: a number or one float32 on the GPU (default: the optimizer's); ``scale``: one float32 on
         the GPU that multiplies the gradients, and skips the step where it is not finite; ``skip``: a 32-bit word on the
         GPU, or a ``Pool`` (its sticky flags): not 0 skips the step.  A skipped step changes nothing."""
+        self._stay_grads()
+        self._stay_written()
         c = self._cfg
         if isinstance(lr, torch.Tensor):
             c.d_lr = self._word(lr, "lr")
@@ -526,6 +559,7 @@ class AdamW:
 
     def moments(self, dtype: torch.dtype = torch.float32, out=None, stream=None):
         """(m, v): the moments' values as flat float32 (or bfloat16) tensors; ``state``'s own where they are that already."""
+        self._stay_written()
         s, n = self.state, self.state["m"].numel()
         if self.state_bits == 32:
             if dtype != torch.float32 or out is not None:

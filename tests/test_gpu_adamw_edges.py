@@ -1,0 +1,85 @@
+"""GPU: the optimizer at the edges of what a program does with it.
+
+u = 2^-24, a rounding of single precision."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import host
+
+pytestmark = pytest.mark.gpu
+
+ap = pytest.importorskip("activation_paging_gb300")
+
+U = 2.0 ** -24
+
+
+def small(bits=32, master=False, n=600):
+    kind = torch.bfloat16 if master else torch.float32
+    params = [torch.full((n,), 0.5, device="cuda", dtype=kind), torch.zeros(7, device="cuda", dtype=kind)]
+    grads = [torch.full((n,), 1e-2, device="cuda"), torch.ones(7, device="cuda")]
+    return ap.AdamW(params, grads, master=master, state_bits=bits)
+
+
+def move_param(o):
+    o.params[1].data = o.params[1].data.clone()
+
+
+def move_master(o):
+    o.master[0].data = o.master[0].data.clone()
+
+
+def load_state(o):
+    o.state.update({n: t.clone() for n, t in o.state.items()})
+
+
+def replace_scale(o):
+    o.state["v_scale"] = torch.zeros(1, device="cuda")
+
+
+def free_state(o):
+    o.state["m"].untyped_storage().resize_(0)
+
+
+@pytest.mark.parametrize("move", [move_param, move_master, load_state, replace_scale, free_state])
+def test_tensors_that_moved_are_refused(move):
+    """A step writes where its tensors were when the optimizer was made, so it refuses those that are elsewhere now."""
+    o = small(8, True)
+    o.step()
+    kept = [t.clone() for t in o.params + o.master]
+    move(o)
+    n0 = ap.launch_count()
+    for call in (o.step, o.moments):
+        with pytest.raises(ValueError, match="moved"):
+            call()
+    assert ap.launch_count() == n0
+    assert all(torch.equal(a, b) for a, b in zip(kept, o.params + o.master))
+
+
+def test_gradients_that_moved_are_refused_until_bound_again():
+    o = small()
+    o.grads[0].data = torch.full((600,), -1e-2, device="cuda")
+    n0 = ap.launch_count()
+    for call in (o.step, o.grad_norm):
+        with pytest.raises(ValueError, match="bind"):
+            call()
+    assert ap.launch_count() == n0
+    o.bind(o.grads)
+    before = float(o.params[0][0])
+    o.step()
+    assert float(o.params[0][0]) > before  # down the new gradient
+
+
+def test_loaded_state_is_copied_in_or_given_anew():
+    a, b = small(8), small(8)
+    a.step()
+    for name, t in b.state.items():
+        t.copy_(a.state[name])
+    for x, y in zip(a.params, b.params):
+        y.copy_(x)
+    c = ap.AdamW([p.clone() for p in a.params], a.grads, state_bits=8, state={n: t.clone() for n, t in a.state.items()})
+    for o in (a, b, c):
+        o.step()
+    for o in (b, c):
+        assert all(torch.equal(x, y) for x, y in zip(a.params + list(a.state.values()), o.params + list(o.state.values())))
+    assert host(a.state["step"]).tolist() == [2, 0] and np.isfinite(host(a.params[0])).all()
