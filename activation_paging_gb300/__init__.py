@@ -545,7 +545,9 @@ class AdamW:
     def step(self, lr=None, scale: torch.Tensor | None = None, skip=None, stream=None):
         """One step.  ``lr``: a number or one float32 on the GPU (default: the optimizer's); ``scale``: one float32 on
         the GPU that multiplies the gradients, and skips the step where it is not finite; ``skip``: a 32-bit word on the
-        GPU, or a ``Pool`` (its sticky flags): not 0 skips the step.  A skipped step changes nothing."""
+        GPU, or a ``Pool`` (its sticky flags): not 0 skips the step.  A skipped step changes nothing.  The word is read
+        once for the whole step; to see the overflow of a pool's pushes, come after them (``stream=pool.stream``, or an
+        event)."""
         self._stay_grads()
         self._stay_written()
         c = self._cfg

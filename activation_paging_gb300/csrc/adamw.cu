@@ -273,13 +273,16 @@ template <typename P, typename G, int BITS> struct UpBlock {
     bool vec;
 };
 
+// The work word while a call runs: blocks that are done, and what the first block to ask found, which all blocks of all
+// launches go by, since the word that skips a step may change at any time.
+constexpr int kGoes = 1 << 30, kSkips = 1 << 29;
+
 template <int CAP, typename P, typename G, bool MASTER, int BITS>
 __global__ void __launch_bounds__(kUpThreads, kUpBlocksOf<BITS>) k_adamw(const __grid_constant__ UpTable<CAP> tab, const UpStep s)
 {
     pdl_begin();
     const int lane = (int)lane_id(), wid = threadIdx.x / kWarp;
     const int32_t taken = *s.d_step;
-    const uint32_t skip = s.d_skip ? *s.d_skip : 0u;
     const float scale = s.d_scale ? *s.d_scale : 1.f, lr = s.d_lr ? *s.d_lr : s.lr;
     const uint32_t blocks = tab.first[tab.count];
     using Q = std::conditional_t<MASTER, float, P>;
@@ -312,7 +315,18 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocksOf<BITS>) k_adamw(const _
     const float rate = __fdiv_rn(lr, correction(s.ln_b1, (float)t));
     const float root = __frsqrt_rn(correction(s.ln_b2, (float)t));
     const uint32_t seeded = mix(s.seed + kGolden * (uint32_t)t);
-    if (skip || !(fabsf(scale) < INFINITY)) return; // (the same for all blocks)
+    bool skips = !(fabsf(scale) < INFINITY);
+    if (s.d_skip) { // (the same for all blocks)
+        __shared__ int s_skips;
+        if (threadIdx.x == 0) {
+            const int mine = skips || *reinterpret_cast<const volatile uint32_t *>(s.d_skip) ? kSkips : kGoes;
+            const int first = atomicCAS(s.d_step + 1, 0, mine);
+            s_skips = (first ? first : mine) & kSkips;
+        }
+        __syncthreads();
+        skips = s_skips != 0;
+    }
+    if (skips) b = blocks;
     while (b < blocks) {
         const Block x = next;
         b += gridDim.x * kUpWarps;
@@ -392,8 +406,8 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocksOf<BITS>) k_adamw(const _
         __syncthreads();
         if (threadIdx.x == 0) {
             __threadfence();
-            if (atomicAdd(s.d_step + 1, 1) == (int)gridDim.x - 1) {
-                s.d_step[0] = t;
+            if ((atomicAdd(s.d_step + 1, 1) & (kSkips - 1)) == (int)gridDim.x - 1) {
+                if (!skips) s.d_step[0] = t;
                 s.d_step[1] = 0;
             }
         }

@@ -531,7 +531,11 @@ ap_status ap_embed_backward(const void *dout, int64_t dout_ld, int32_t dout_dtyp
  *   d_lr     float32 (device) or NULL: lr, in place of config.lr
  *   d_scale  float32 (device) or NULL: 1.  One that is not finite skips the step
  *   d_skip   uint32 (device) or NULL: not 0 skips the step.  A skipped step
- *            changes nothing, d_step included
+ *            changes nothing, d_step included.  The word may change while the
+ *            call runs (a pool's flags, by pushes on another stream): it is read
+ *            once for all blocks and launches.  A call that is to see a push's
+ *            overflow has to come after that push, on its stream or by an event.
+ *            d_lr and d_scale stay as they are until the call is done
  * The calls of one optimizer (one d_step) must not overlap; parameters, masters
  * and moments must not overlap one another.  Addresses of 16 (BF16: 8) bytes'
  * alignment are fastest.  0 <= beta1, beta2 < 1, eps >= 0.

@@ -83,3 +83,37 @@ def test_loaded_state_is_copied_in_or_given_anew():
     for o in (b, c):
         assert all(torch.equal(x, y) for x, y in zip(a.params + list(a.state.values()), o.params + list(o.state.values())))
     assert host(a.state["step"]).tolist() == [2, 0] and np.isfinite(host(a.params[0])).all()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_skip_word_that_changes_during_the_call_is_read_once(bits):
+    """441 tensors are two launches.  Another stream flips the word all the while: a step is taken whole or not at all, and
+    the work word is 0 after it."""
+    n = 40_000
+    params = [torch.ones(n, device="cuda") for _ in range(441)]
+    o = ap.AdamW(params, [torch.ones(n, device="cuda") for _ in range(441)], weight_decay=0.0, state_bits=bits)
+    word, side = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.cuda.Stream()
+    steps, ends = 0, torch.stack([p[i] for p in params for i in (0, -1)])
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for q in range(40):
+            with torch.cuda.stream(side):
+                word.fill_(q & 1)
+            if q == 20:
+                o.step(skip=word)
+        torch.cuda.synchronize()
+        now, work = host(o.state["step"]).tolist()
+        was, ends = ends, torch.stack([p[i] for p in params for i in (0, -1)])
+        assert work == 0 and now - steps in (0, 1)
+        moved = ends != was  # (a step of gradients of 1 moves each element by about lr)
+        assert bool(moved.all()) if now > steps else not bool(moved.any())
+        steps = now
+
+
+def test_a_step_after_a_skipped_one_counts_from_the_start():
+    o, word = small(), torch.ones(1, dtype=torch.int32, device="cuda")
+    for skip, steps in ((word, 0), (None, 1), (word, 1), (word, 1), (torch.zeros_like(word), 2), (None, 3)):
+        o.step(skip=skip)
+        assert host(o.state["step"]).tolist() == [steps, 0]
+    o.step(scale=torch.full((1,), float("nan"), device="cuda"), skip=torch.zeros_like(word))
+    assert host(o.state["step"]).tolist() == [3, 0]
