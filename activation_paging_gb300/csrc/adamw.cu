@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocksOf<BITS>) k_adamw(const _
     Block next;
     if (b < blocks) load(next); // (on its way while the step's constants are formed)
     const int t = taken + 1;
-    const float keep = 1.f - lr * s.decay;
+    const float less = -(lr * s.decay); // (1 - lr decay as a factor would round the decay to multiples of 2^-24)
     const float rate = __fdiv_rn(lr, correction(s.ln_b1, (float)t));
     const float root = __frsqrt_rn(correction(s.ln_b2, (float)t));
     const uint32_t seeded = mix(s.seed + kGolden * (uint32_t)t);
@@ -359,7 +359,8 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocksOf<BITS>) k_adamw(const _
             m[j] = fmaf(s.b1, m[j], s.one_b1 * g);
             v[j] = fmaf(s.b2, v[j], s.one_b2 * g * g);
             r[j] = sqrt_fast(v[j]);
-            p[j] = fmaf(keep, x.p.at(j), -rate * div_fast(m[j], fmaf(r[j], root, s.eps)));
+            const float at_p = x.p.at(j);
+            p[j] = at_p + fmaf(less, at_p, -rate * div_fast(m[j], fmaf(r[j], root, s.eps)));
         }
         if constexpr (MASTER) store8(q.master, at, n, vec, p);
         store8(static_cast<P *>(q.param), at, n, vec, p);

@@ -117,3 +117,26 @@ def test_a_step_after_a_skipped_one_counts_from_the_start():
         assert host(o.state["step"]).tolist() == [steps, 0]
     o.step(scale=torch.full((1,), float("nan"), device="cuda"), skip=torch.zeros_like(word))
     assert host(o.state["step"]).tolist() == [3, 0]
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lr,decay", [(1e-2, 0.1), (1e-5, 0.01), (3e-6, 0.01), (2e-6, 0.01)])
+def test_small_decays_are_whole(kind, lr, decay):
+    """The end of a schedule, lr * decay down to 2e-8: over many elements the change is the formula's.  Parameters in [1, 2)
+    round to multiples of 2 u: by u at the most, either way alike, as the changes (of deviation lr, 16 such steps and more)
+    spread over many.  So the mean of n has a deviation of u / sqrt(3 n); six of them, and 64 u of the mean change (of lr, rate,
+    product and quotient).  The decay is 0.5 u and more."""
+    n = 1 << 22
+    g = torch.Generator(device="cuda").manual_seed(3)
+    p = torch.rand(n, generator=g, device="cuda") + 1.0
+    state = {"m": torch.randn(n, generator=g, device="cuda"), "v": torch.ones(n, device="cuda"),
+             "step": torch.tensor([10 ** 6, 0], dtype=torch.int32, device="cuda")}
+    grad = torch.randn(n, generator=g, device="cuda")
+    before, m, v = p.double(), state["m"].double(), state["v"].double()
+    o = ap.AdamW([p.to(kind)], [grad], lr=lr, weight_decay=decay, state=state, master=[p] if kind == torch.bfloat16 else None)
+    o.step()
+    after = (o.master or o.params)[0].double()
+    m, v = 0.9 * m + 0.1 * grad.double(), 0.999 * v + 0.001 * grad.double() ** 2
+    change = -lr * decay * before - lr * m / (v.sqrt() + 1e-8)  # (the corrections are 1 by then)
+    off = float((after - before - change).mean())
+    assert abs(off) <= 6 * U / (3 * n) ** 0.5 + 64 * U * abs(float(change.mean()))
