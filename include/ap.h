@@ -538,7 +538,9 @@ ap_status ap_embed_backward(const void *dout, int64_t dout_ld, int32_t dout_dtyp
  *            d_lr and d_scale stay as they are until the call is done
  * The calls of one optimizer (one d_step) must not overlap; parameters, masters
  * and moments must not overlap one another.  Addresses of 16 (BF16: 8) bytes'
- * alignment are fastest.  0 <= beta1, beta2 < 1, eps >= 0.
+ * alignment are fastest.  0 <= beta1, beta2 < 1, eps >= 0.  With eps = 0 an
+ * element whose v is 0 (no gradient yet, or a square below single precision's
+ * numbers) divides by 0.
  * ========================================================================== */
 #define AP_ADAMW_BLOCK 256
 typedef struct {

@@ -140,3 +140,28 @@ def test_small_decays_are_whole(kind, lr, decay):
     change = -lr * decay * before - lr * m / (v.sqrt() + 1e-8)  # (the corrections are 1 by then)
     off = float((after - before - change).mean())
     assert abs(off) <= 6 * U / (3 * n) ** 0.5 + 64 * U * abs(float(change.mean()))
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-30])
+def test_squares_below_the_normal_numbers_have_roots(eps):
+    """v near 1e-40: the change is the formula's, for eps = 0 too.  v = b2 v rounds by 2^-150 (of 1e-40: 7e-6 u', half of that
+    in its root), the rest by 32 u."""
+    n = 1024
+    state = {"m": torch.linspace(-1e-22, 1e-22, n, device="cuda"), "v": torch.linspace(1e-40, 3e-40, n, device="cuda"),
+             "step": torch.tensor([10 ** 6, 0], dtype=torch.int32, device="cuda")}
+    m, v = state["m"].double() * 0.9, state["v"].double() * 0.999
+    o = ap.AdamW([torch.zeros(n, device="cuda")], [torch.zeros(n, device="cuda")], lr=1.0, eps=eps, weight_decay=0.0, state=state)
+    o.step()
+    want = -m / (v.sqrt() + eps)
+    assert bool((o.state["v"] > 0).all())
+    assert bool(((o.params[0].double() - want).abs() <= (0.5 * 2.0 ** -150 / 1e-40 + 32 * U) * want.abs()).all())
+
+
+def test_codes_of_positive_squares_are_positive():
+    """Gradients of 1e-20 to 1e-19: (1 - b2) g^2 is 1e-43 and more, below the normal numbers but positive."""
+    n = 512
+    o = ap.AdamW([torch.zeros(n, device="cuda")], [torch.logspace(-20, -19, n, device="cuda")], lr=1.0, eps=0.0, state_bits=8)
+    o.step()
+    assert bool((o.state["v"] > 0).all()) and bool(torch.isfinite(o.params[0]).all())
+    m, v = o.moments()
+    assert bool((v > 0).all()) and bool((o.params[0] < 0).all())
