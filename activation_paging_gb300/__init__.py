@@ -388,6 +388,9 @@ def embed_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: float =
     return dtable
 
 
+_ROUNDINGS = {"codes": 0, "values": 1}
+
+
 class AdamW:
     """AdamW over many tensors at once: one launch for the step, whatever their
     number (up to 440), with the step's number, the clipping factor and what
@@ -397,7 +400,10 @@ class AdamW:
     lists of contiguous CUDA tensors; the optimizer keeps them, reads the
     gradients and writes the parameters at each step (``bind`` changes the
     gradients).  ``master``: FP32 copies of BF16 parameters, as a list or True
-    (made here).  ``state_bits`` 32 or 8 (see ``ap_adamw_step``).  Moments are
+    (made here).  ``state_bits`` 32 or 8 (see ``ap_adamw_step``).  ``rounding`` of
+    8-bit moments, at random: 'codes', fair between codes, which keeps moments
+    far below their block's largest too large (of 1e-4 of it by a fifth), or
+    'values', whose expectations are the moments.  Moments are
     flat buffers in which tensor i begins at element ``parts[i][0]``, a multiple
     of 256; ``state`` gives them with the step words (a checkpoint, or buffers
     to use): ``m``, ``v`` (float32, or int8 and uint8 with float32 ``m_scale``
@@ -412,12 +418,14 @@ class AdamW:
     BLOCK = 256
 
     def __init__(self, params, grads, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
-                 master=None, state_bits: int = 32, state: dict | None = None, seed: int = 0):
+                 master=None, state_bits: int = 32, state: dict | None = None, seed: int = 0, rounding: str = "codes"):
         self.params, self.lr = list(params), lr
         if not self.params:
             raise ValueError("params is empty")
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+        if rounding not in _ROUNDINGS:
+            raise ValueError(f"rounding must be 'codes' or 'values', got {rounding!r}")
         kind, dev = self.params[0].dtype, self.params[0].device
         if kind not in _ROW_TYPES:
             raise ValueError(f"params must be bfloat16 or float32, got {kind}")
@@ -463,7 +471,7 @@ class AdamW:
                 e.master = self.master[i].data_ptr()
         self._cfg = _lib.AdamWConfig(lr=lr, beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
                                      param_dtype=_ROW_TYPES[kind], master=1 if self.master is not None else 0,
-                                     state_bits=state_bits, seed=seed & 0xFFFFFFFF, d_step=at["step"])
+                                     state_bits=state_bits, seed=seed & 0xFFFFFFFF, rounding=_ROUNDINGS[rounding], d_step=at["step"])
         self._cfg_ref = ctypes.byref(self._cfg)
         self.bind(grads)
         n = ctypes.c_int64(0)

@@ -40,7 +40,7 @@ class AdamWTensor(ctypes.Structure):
 class AdamWConfig(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
                 ("weight_decay", ctypes.c_double), ("param_dtype", i32), ("grad_dtype", i32), ("master", i32),
-                ("state_bits", i32), ("seed", u32), ("reserved", u32), ("d_lr", P), ("d_scale", P), ("d_skip", P),
+                ("state_bits", i32), ("seed", u32), ("rounding", u32), ("d_lr", P), ("d_scale", P), ("d_skip", P),
                 ("d_step", P)]
 
 

@@ -14,10 +14,16 @@
 // c in 0 .. 255, s from the block's largest.  The square law spends the codes
 // where moments of a block lie: steps of 1.6% (0.8% of sqrt(v)) at the largest,
 // 16% at a hundredth of it, down to 6e-5 (1.5e-5) of it.  Codes are rounded up or
-// down at random in proportion (16 bits of a counter-based mix of seed, step,
-// tensor and element): v moves by less than a code a step, and rounding to
-// nearest would never let it move.  A positive v never gets code 0, so no
-// division by eps alone comes from the coding.
+// down at random (16 bits of a counter-based mix of seed, step, tensor and
+// element): v moves by less than a code a step, and rounding to nearest would
+// never let it move.  A positive v never gets code 0, so no division by eps alone
+// comes from the coding.
+// Up with the code's own fraction f (ROUND_CODES), the value's expectation is too
+// large by s f (1 - f) a step, which is nothing for large codes; a steady m or
+// sqrt(v) of 1e-3 of its block's largest is kept 0.2% and 0.6% too large, of 1e-4
+// 24% and 20%, m of 1e-5 4.6 times.  With the value's place between the values of
+// the two codes (ROUND_VALUES) the expectations of m and v are exact, but for v
+// below code 1.  134 M elements: 367 us and VALUES_US.
 #include <cuda_bf16.h>
 #include <float.h>
 #include <math.h>
@@ -205,6 +211,16 @@ __device__ __forceinline__ float div_fast(float a, float b)
     return a * y;
 }
 
+// The code of x in units of its square (last byte; x <= the largest code's square), up from the root's floor where the
+// fraction, 1 + that and half a place, is below the place of value(x) between those of the two squares.  The root may be off
+// by a rounding: a code that is one too small for it goes up always, one too large never.
+template <typename Fn> __device__ __forceinline__ uint32_t between_codes(float x, float fraction, Fn value)
+{
+    const float at = __fadd_rd(sqrt_code(x), kBig), c = at - kBig, low = c * c, high = low + (2.f * c + 1.f);
+    const float place = fraction - (1.f - 0.5f / 65536.f);
+    return __float_as_uint(at) + (place * (value(high) - value(low)) < value(x) - value(low));
+}
+
 // 1 - b^t from ln b: expm1 keeps its precision for few steps.
 __device__ __forceinline__ float correction(const float (&ln_b)[2], float t)
 {
@@ -268,8 +284,10 @@ template <typename E> __device__ __forceinline__ void load_raw(const E *p, int64
         }
     }
 }
-template <int BITS> constexpr bool kAheadOf = BITS == 8;
-template <int BITS> constexpr int kUpBlocksOf = BITS == 8 ? 3 : 1;
+// What a kernel is made for: moments of 32 bits, or of 8 with either rounding.
+enum Moments { k32, kCodes, kValues };
+template <int BITS> constexpr bool kAheadOf = BITS != k32;
+template <int BITS> constexpr int kUpBlocksOf = BITS == k32 ? 1 : 3;
 // What a lane has of a block: parameters, gradients and moments.
 template <typename P, typename G, int BITS> struct UpBlock {
     Raw<P> p;
@@ -306,7 +324,7 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocksOf<BITS>) k_adamw(const _
         x.vec = tab.vec && x.at + kBlock <= q.n;
         load_raw(MASTER ? reinterpret_cast<const Q *>(q.master) : static_cast<const Q *>(q.param), x.at, q.n, x.vec, x.p);
         load_raw(static_cast<const G *>(q.grad), x.at, q.n, x.vec, x.g);
-        if constexpr (BITS == 8) {
+        if constexpr (BITS != k32) {
             load_codes(q.m, x.at, x.cm);
             load_codes(q.v, x.at, x.cv);
             x.sm = q.m_scale[x.at / kBlock];
@@ -344,7 +362,7 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocksOf<BITS>) k_adamw(const _
         const int64_t n = q.n, at = x.at;
         const bool vec = x.vec;
         float p[8], m[8], v[8], r[8];
-        if constexpr (BITS == 8) {
+        if constexpr (BITS != k32) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 m[j] = code_m(x.cm[j / 4] ^ kSigns, j % 4) * x.sm;
@@ -373,7 +391,7 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocksOf<BITS>) k_adamw(const _
         }
         if constexpr (MASTER) store8(q.master, at, n, vec, p);
         store8(static_cast<P *>(q.param), at, n, vec, p);
-        if constexpr (BITS == 32) {
+        if constexpr (BITS == k32) {
             store8(static_cast<float *>(q.m), at, n, vec, m);
             store8(static_cast<float *>(q.v), at, n, vec, v);
         } else {
@@ -396,10 +414,18 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocksOf<BITS>) k_adamw(const _
             for (int j = 0; j < 8; ++j) {
                 const uint32_t e = (uint32_t)at + (j / 4) * (kBlock / 2) + lane * 4 + j % 4;
                 const uint32_t u = mix(e * kGolden + key);
-                const uint32_t c = floor_bits(fminf(sqrt_code(fabsf(m[j]) * im) + low_fraction(u), 128.f));
+                const float xm = fabsf(m[j]) * im, xv = r[j] * iv;
+                uint32_t c, d;
+                if constexpr (BITS == kCodes) {
+                    c = floor_bits(fminf(sqrt_code(xm) + low_fraction(u), 128.f));
+                    d = floor_bits(fmaxf(fminf(sqrt_code(xv) + high_fraction(u), 256.f), 2.f));
+                } else {
+                    c = between_codes(fminf(xm, 127.f * 127.f), low_fraction(u), [](float q) { return q; });
+                    d = between_codes(fminf(xv, 255.f * 255.f), high_fraction(u), [](float q) { return q * q; });
+                    d = max(d & 255u, 1u);
+                }
                 cm[j] = m[j] < 0.f ? 0u - c : c; // (last byte)
-                const float y = fminf(sqrt_code(r[j] * iv) + high_fraction(u), 256.f);
-                cv[j] = r[j] > 0.f ? floor_bits(fmaxf(y, 2.f)) : 0u;
+                cv[j] = r[j] > 0.f ? d : 0u;
             }
             const uint32_t wm[2] = {four_bytes(cm, 0), four_bytes(cm, 1)}, wv[2] = {four_bytes(cv, 0), four_bytes(cv, 1)};
             store_codes(q.m, at, wm);
@@ -605,7 +631,9 @@ template <int CAP> ap_status adamw_launches(const ap_adamw_tensor *t, int32_t n,
         s.last = to == n;
         ap_status r;
 #define AP_ADAMW(P, G, M) \
-    r = c.state_bits == 8 ? launch_adamw<CAP, P, G, M, 8>(tab, s, st) : launch_adamw<CAP, P, G, M, 32>(tab, s, st)
+    r = c.state_bits == 32 ? launch_adamw<CAP, P, G, M, k32>(tab, s, st)                  \
+        : c.rounding == AP_ADAMW_ROUND_CODES ? launch_adamw<CAP, P, G, M, kCodes>(tab, s, st) \
+                                             : launch_adamw<CAP, P, G, M, kValues>(tab, s, st)
         const bool g16 = c.grad_dtype == AP_DTYPE_BF16;
         if (c.param_dtype == AP_DTYPE_F32) {
             if (g16)
@@ -703,6 +731,8 @@ extern "C" ap_status ap_adamw_step(const ap_adamw_tensor *tensors, int32_t n, co
     if (!float_type(c.param_dtype) || !float_type(c.grad_dtype))
         return fail(AP_EINVAL, "adamw_step: types %d, %d", c.param_dtype, c.grad_dtype);
     if (c.state_bits != 8 && c.state_bits != 32) return fail(AP_EINVAL, "adamw_step: state_bits=%d", c.state_bits);
+    if (c.rounding != AP_ADAMW_ROUND_CODES && c.rounding != AP_ADAMW_ROUND_VALUES)
+        return fail(AP_EINVAL, "adamw_step: rounding=%u", c.rounding);
     if (c.master != 0 && (c.master != 1 || c.param_dtype != AP_DTYPE_BF16))
         return fail(AP_EINVAL, "adamw_step: master=%d with parameters of type %d", c.master, c.param_dtype);
     if (!(c.beta1 >= 0.0 && c.beta1 < 1.0 && c.beta2 >= 0.0 && c.beta2 < 1.0 && c.eps >= 0.0))

@@ -114,6 +114,16 @@ def adamw_decode(cm, cv, sm, sv):
     return c * np.abs(c) * each(sm), r * r
 
 
+def adamw_codes(x, r, top, power, rounding="codes"):
+    """Codes of magnitudes x in units of their scale (sqrt(v)'s too), with the fractions r; power: of the values that
+    count, 1 for m, 2 for v."""
+    c = np.floor(np.sqrt(x))
+    if rounding == "codes":
+        return np.minimum(np.floor(np.sqrt(x) + r), top)
+    low, high = c ** (2 * power), (c + 1) ** (2 * power)
+    return np.minimum(c + ((r + 0.5 / 65536) * (high - low) < x ** power - low), top)
+
+
 def block_max(x):
     pad = np.zeros(-(-x.size // BLOCK) * BLOCK)
     pad[:x.size] = np.abs(x)

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from gpu_util import host
+from oracle import layer
 
 pytestmark = pytest.mark.gpu
 
@@ -165,3 +166,66 @@ def test_codes_of_positive_squares_are_positive():
     assert bool((o.state["v"] > 0).all()) and bool(torch.isfinite(o.params[0]).all())
     m, v = o.moments()
     assert bool((v > 0).all()) and bool((o.params[0] < 0).all())
+
+
+@pytest.mark.parametrize("ratio", [1e-2, 1e-3, 1e-4, 1e-5])
+def test_small_moments_in_codes_keep_their_size(ratio):
+    """Elements far below their block's largest, of one gradient: coded moments rounded by values keep the mean.  A code's
+    expectation is the value, to half of 2^-17 of a step between codes (below the value itself, but for codes near 0: of
+    2^-17 scales, 7.6e-6 of m = 0.16 scales); the mean of n elements is off by its standard deviation, six of them.  v of
+    1e-5 lies below its scale's first code, which it is kept at."""
+    n, steps = 1 << 20, 60
+    grad = torch.full((n,), ratio, device="cuda")
+    grad[::256] = 1.0
+    o = ap.AdamW([torch.zeros(n, device="cuda")], [grad], betas=(0.9, 0.95), state_bits=8, rounding="values", seed=5)
+    for _ in range(steps):
+        o.step()
+    for name, moment, want, b in (("m", o.moments()[0], ratio, 0.9), ("v", o.moments()[1], ratio ** 2, 0.95)):
+        x = moment.view(-1, 256)[:, 1:].double()
+        want *= 1 - b ** steps
+        if name == "v" and ratio == 1e-5:
+            assert bool((o.state["v"].view(-1, 256)[:, 1:] == 1).all())
+            continue
+        assert abs(float(x.mean()) - want) <= 6 * float(x.std()) / x.numel() ** 0.5 + (2e-4 + 64 * U) * want
+
+
+@pytest.mark.parametrize("rounding", ["codes", "values"])
+def test_codes_are_the_documented_ones(rounding):
+    """Of a first step, whose moments are (1 - b) g and (1 - b) g^2: x = |m| / m_scale takes 8 u of itself, and a code
+    rises with x.  The place between two values takes 8 u more of the values, which is a fraction of the step between
+    them of 8 u x / (2 c + 1) < 8 u 128 at most (v: half its power's): covered by 1024 u of x."""
+    n = 256 * 64 + 100
+    g = torch.Generator(device="cuda").manual_seed(9)
+    grad = torch.randn(n, generator=g, device="cuda") * torch.logspace(-4, 0, n, device="cuda")[torch.randperm(n, generator=g, device="cuda")]
+    grad[:256] = 0.0
+    o = ap.AdamW([torch.zeros(n, device="cuda")], [grad], betas=(0.9, 0.95), state_bits=8, rounding=rounding, seed=7)
+    o.step()
+    low, high = layer.adamw_noise(7, 1, 0, n)
+    gf = host(grad).astype(np.float64)
+    for name, x, top, r, power in (("m", np.abs(gf) * 0.1, 127, low, 1), ("v", np.abs(gf) * np.sqrt(0.05), 255, high, 2)):
+        scale = np.repeat(layer.block_max(x) / top ** 2, 256)[:n]
+        on = scale > 0
+        y = np.where(on, x / np.where(on, scale, 1.0), 0.0)
+        code = np.abs(host(o.state[name])[:n].astype(np.int64))
+        lo, hi = (layer.adamw_codes(y * (1 + d), r + d, top, power, rounding) for d in (-1024 * U, 1024 * U))
+        if name == "v":
+            lo, hi = np.maximum(lo, y > 0), np.maximum(hi, y > 0)
+        if rounding == "values":  # (r is compared with the place, which falls with it)
+            lo = np.minimum(lo, layer.adamw_codes(y * (1 - 1024 * U), r + 1024 * U, top, power, rounding))
+            hi = np.maximum(hi, layer.adamw_codes(y * (1 + 1024 * U), r - 1024 * U, top, power, rounding))
+            if name == "v":
+                lo = np.maximum(lo, y > 0)
+        assert np.all((code >= lo) & (code <= hi))
+        assert (lo == hi).mean() > 0.98  # (the bounds leave few codes open)
+        assert not code[~on].any()
+
+
+def test_rounding_by_values_is_seeded_and_repeats():
+    def run(seed):
+        o = ap.AdamW([torch.zeros(1000, device="cuda")], [torch.linspace(-1, 1, 1000, device="cuda")], state_bits=8, rounding="values",
+                     seed=seed)
+        for _ in range(3):
+            o.step()
+        return list(o.state.values()) + o.params
+    a, b, c = run(1), run(1), run(2)
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and not torch.equal(a[1], c[1])
