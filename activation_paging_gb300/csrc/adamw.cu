@@ -23,7 +23,7 @@
 // sqrt(v) of 1e-3 of its block's largest is kept 0.2% and 0.6% too large, of 1e-4
 // 24% and 20%, m of 1e-5 4.6 times.  With the value's place between the values of
 // the two codes (ROUND_VALUES) the expectations of m and v are exact, but for v
-// below code 1.  134 M elements: 367 us and VALUES_US.
+// below code 1.  134 M elements, BF16 with masters: 368 us and 438.
 #include <cuda_bf16.h>
 #include <float.h>
 #include <math.h>
