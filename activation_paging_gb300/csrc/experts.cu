@@ -651,7 +651,7 @@ __device__ __forceinline__ void write_weights(const ExArgs &a, const Tile &t, in
 // One writer: two for each quarter of the accumulator's lanes.
 template <Op OP, bool PAIR>
 __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, int writer, uint32_t tmem, uint64_t *s_done,
-                                            uint64_t *s_free, uint8_t *pass, volatile int *dead)
+                                            uint64_t *s_free, uint8_t *pass, volatile int *dead, const volatile uint32_t *fetched)
 {
     const int part = writer & 3, lane = (int)lane_id();
     uint32_t count = 0;
@@ -678,7 +678,8 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
             else
                 read_ahead<OP>(a, t, c, part, x);
             if (t.steps > 0) {
-                ok = __all_sync(0xffffffffu, ok && bar_wait(smem_addr(&s_done[acc]), count >> 1 & 1, dead));
+                // (for all of a section, which may be a whole expert's rows: as long as stages come)
+                ok = __all_sync(0xffffffffu, ok && bar_wait(smem_addr(&s_done[acc]), count >> 1 & 1, dead, fetched));
                 ++count;
             }
             fence_after();
@@ -734,6 +735,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_ready[kPass2 ? kMaxStages : 1], s_done[2], s_free[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
+    __shared__ uint32_t s_fetched; // stages so far
     const int wid = threadIdx.x / kWarp, lane = (int)lane_id();
     const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
     const int stage_bytes = 2 * kPanel + a.columns * (PAIR ? 64 : 128);
@@ -751,6 +753,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
         bar_init(smem_addr(&s_drain), 1);
         bar_init_done();
         s_dead = 0;
+        s_fetched = 0;
     }
     if (wid == 1) tmem_alloc<PAIR>(smem_addr(&s_tmem), 512);
     if (wid == 2) count_tiles<OP>(a, s_tab);
@@ -779,7 +782,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
                         break;
                     }
                     fetch<OP, PAIR>(a, t, step, stages + (size_t)s * stage_bytes, m, smem_addr(&s_full[s]), rank);
-                    ++count;
+                    *(volatile uint32_t *)&s_fetched = ++count;
                     if (++s == (uint32_t)a.stages) {
                         s = 0;
                         ++turn;
@@ -905,7 +908,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
         }
     } else if (wid >= 4) {
         // ---- write
-        write_tiles<OP, PAIR>(a, w, rank, wid - 4, tmem, s_done, s_free, s_pass + (wid - 4) * kPassOf, dead);
+        write_tiles<OP, PAIR>(a, w, rank, wid - 4, tmem, s_done, s_free, s_pass + (wid - 4) * kPassOf, dead, &s_fetched);
     }
     __syncwarp();
     fence_before();

@@ -29,18 +29,26 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
 }
 // Waits for the phase of this parity to end; gives up after a number of tries
 // (each of which may sleep for a while), or once another wait of the block gave
-// up (*dead).  A million tries take some ten milliseconds at the least.
+// up (*dead).  A million tries take some ten milliseconds at the least, which is
+// no limit to a wait for work whose length the sizes give: such a wait names a
+// count that moves while the work does (*moved), and the tries are those without
+// a move.
 constexpr uint32_t kTries = 1u << 20;
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *dead)
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *dead, const volatile uint32_t *moved = nullptr)
 {
-    uint32_t ok = 0;
+    uint32_t ok = 0, seen = moved ? *moved : 0;
     for (uint32_t i = 0; i < kTries; ++i) {
         asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
                      : "=r"(ok)
                      : "r"(bar), "r"(parity)
                      : "memory");
         if (ok) return true;
-        if ((i & 255) == 255 && *dead) return false;
+        if ((i & 255) != 255) continue;
+        if (*dead) return false;
+        if (moved && *moved != seen) {
+            seen = *moved;
+            i = 0;
+        }
     }
     *dead = 1;
     return false;

@@ -1,0 +1,56 @@
+"""GPU: the experts' products at the edges of what a call may ask for.
+
+Operands of small whole numbers: products and sums below 2^24 are exact in single precision, whatever their order, so
+results are the exact ones (rounded once to BF16: by 2^-8 of themselves at most).  u = 2^-24."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import host, to_dev
+from oracle import layer
+
+pytestmark = pytest.mark.gpu
+
+ap = pytest.importorskip("activation_paging_gb300")
+
+U = 2.0 ** -24
+HALF = 2.0 ** -8
+
+
+def whole(shape, low, high, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(low, high + 1, shape, generator=g, device="cuda", dtype=torch.int8).bfloat16()
+
+
+def one(rows):
+    return torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1,), rows, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_weights_gradient_of_millions_of_rows(dtype):
+    """One expert of 4 million rows: 65536 stages, in one section for BF16 results."""
+    rows = (1 << 22) - 5
+    dy, x, status = whole((rows, 64), 0, 1, 1), whole((rows, 64), -1, 1, 2), torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = ap.expert_linear_dw(dy, x, *one(rows), dtype=dtype, status=status)[0].double()
+    want = sum(a.double().t() @ b.double() for a, b in zip(dy.split(1 << 18), x.split(1 << 18)))
+    assert int(status) == 0
+    assert float(want.abs().max()) < 2 ** 24
+    assert bool(((got - want).abs() <= (HALF * want.abs() if dtype == torch.bfloat16 else 0.0)).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [40, 300])
+def test_products_of_the_longest_contraction(dtype, rows):
+    """K = 2^20: 16384 stages of a tile (300 rows: pairs of blocks)."""
+    K, N = 1 << 20, 160
+    x, W, status = whole((rows, K), -1, 1, 3), whole((1, N, K), 0, 1, 4), torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = ap.expert_linear(x, W, *one(rows), dtype=dtype, status=status).double()
+    want = sum(a.double() @ b.double().t() for a, b in zip(x.split(1 << 17, 1), W[0].split(1 << 17, 1)))
+    assert int(status) == 0
+    assert bool(((got - want).abs() <= (HALF * want.abs() if dtype == torch.bfloat16 else 0.0)).all())
+    # and back: a contraction over 2^20 features
+    back = ap.expert_linear_dx(whole((rows, K), -1, 1, 5), whole((1, K, 72), 0, 1, 6), *one(rows), dtype=dtype, status=status).double()
+    dy, V = whole((rows, K), -1, 1, 5), whole((1, K, 72), 0, 1, 6)[0]
+    want = sum(a.double() @ b.double() for a, b in zip(dy.split(1 << 17, 1), V.split(1 << 17)))
+    assert int(status) == 0
+    assert bool(((back - want).abs() <= (HALF * want.abs() if dtype == torch.bfloat16 else 0.0)).all())

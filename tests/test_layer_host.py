@@ -1,5 +1,7 @@
 """Host logic of a layer's operators (no GPU is touched)."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -60,3 +62,28 @@ def test_codes_rounded_by_values_are_fair_to_them():
             assert abs((c ** (2 * power)).mean() - x ** power) <= step * 2.0 ** -17 * 1.001
     c = layer.adamw_codes(np.full(65536, 2.25), r, 255, 1)
     assert abs((c * c).mean() - 2.5) < 1e-9
+
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "activation_paging_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*|/\*.*?\*/", " ", f.read(), flags=re.S)
+
+
+def test_waits_for_whole_sections_go_by_progress():
+    """A wait gives up after 2^20 tries, ten milliseconds at the least.  The writers' wait is for all stages of a section, of
+    0.34 us and more each: of one expert's 2^31 rows, 11 s.  So it has to start anew as stages are fetched; what is left behind
+    the last one fetched is the ring, and no other wait is for more than the ring and an epilogue."""
+    text, least_s, stage_s = source("experts.cu"), 0.01, 0.43e-6
+    assert (2 ** 31 // 64) * 0.34e-6 > least_s
+    wait = re.search(r"bool bar_wait\(.*?\n}", source("umma.cuh"), flags=re.S).group(0)
+    assert re.search(r"if \(moved && \*moved != seen\) \{\s*seen = \*moved;\s*i = 0;", wait)
+    assert "kTries = 1u << 20" in source("umma.cuh")
+    waits = re.findall(r"bar_wait\(((?:[^()]|\([^()]*\))*)\)", text)
+    done = [w for w in waits if "s_done" in w]
+    assert len(done) == 1 and done[0].rstrip().endswith("dead, fetched")
+    assert re.search(r"fetch<OP, PAIR>\([^;]*;\s*\*\(volatile uint32_t \*\)&s_fetched = \+\+count;", text)
+    ring = int(re.search(r"kMaxStages = (\d+)", text).group(1))
+    assert 1000 * ring * stage_s < least_s
