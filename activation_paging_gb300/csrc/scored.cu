@@ -59,6 +59,17 @@ __device__ __forceinline__ float exp_fast(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
     return y;
 }
+// The same without the growth in |x|, for x <= 0: what the product rounds away,
+// and the constant's rest, as a first-order correction.  6 2^-24.
+__device__ __forceinline__ float exp_near(float x)
+{
+    x = x < -200.f ? -200.f : x; // (the power is 0 there already; -infinity has no rest)
+    constexpr float kLog2e = 1.44269504f, kRest = 1.92596299e-8f, kLn2 = 0.693147181f;
+    const float y = x * kLog2e, rest = fmaf(x, kRest, fmaf(x, kLog2e, -y));
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
+    return fmaf(e, rest * kLn2, e);
+}
 __device__ __forceinline__ float rcp_fast(float x)
 {
     float y;
@@ -268,12 +279,13 @@ __device__ __noinline__ void choose_many(const ScoredArgs &a, int64_t t, float t
 // The chosen scores up to a factor that all of them share: of the softmax
 // relative to the largest chosen, of the sigmoid times e^-min(0, largest), so
 // that scores near 0 keep their ratios: e^(l - shift) / (1 + e^l) below 0.  The
-// relative error is (1.5 d + 10) u with d = |l - shift|.
+// relative error is (d + 18) u with d = |l - shift|, which its difference rounds
+// by; without a shift 18 u.
 __device__ __forceinline__ float score_of(bool sigmoid, float l, float shift)
 {
-    const float e = exp_fast(sigmoid && l > 0.f ? -l : l - shift);
+    const float e = exp_near(sigmoid && l > 0.f ? -l : l - shift);
     if (!sigmoid) return e;
-    const float below = shift == 0.f ? e : exp_fast(l); // (l > 0 only with shift = 0)
+    const float below = shift == 0.f ? e : exp_near(l); // (l > 0 only with shift = 0)
     return (l > 0.f ? 1.f : e) * rcp_fast(1.f + below);
 }
 
@@ -498,7 +510,7 @@ __global__ void __launch_bounds__(kScThreads, VEC * N <= 8 ? 4 : VEC * N <= 16 ?
                 const float all = warp_sum(q);
                 wt = all > 0.f ? q * (rcp_fast(all) * a.scale) : 0.f;
             } else if (in) {
-                wt = (a.sigmoid ? score_of(true, l, 0.f) : exp_fast(l - top) * inv) * a.scale;
+                wt = (a.sigmoid ? score_of(true, l, 0.f) : exp_near(l - top) * inv) * a.scale;
             }
         }
         if (lane < k) {
