@@ -257,9 +257,11 @@ def route_scored(logits: torch.Tensor, k: int, score: str = "sigmoid", bias: tor
 
 def route_scored_backward(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Tensor, score: str = "sigmoid",
                           renorm: bool = True, scale: float = 1.0, dlogits: torch.Tensor | None = None,
-                          status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                          status: torch.Tensor | None = None, stream=None, w: torch.Tensor | None = None) -> torch.Tensor:
     """dlogits [T, E] float32 of ``route_scored`` from the gradient ``dw``
-    [T, k] of its weights."""
+    [T, k] of its weights.  ``w``: the weights themselves, needed where rows may
+    have fewer than k experts to choose from (logits or biases of -infinity):
+    those chosen for want of others have weight 0, and no gradient."""
     kind = _score(score)
     _need(logits, torch.float32, "logits")
     T, E = logits.shape
@@ -268,12 +270,13 @@ def route_scored_backward(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Ten
     k = dw.shape[1]
     pw = _need_shape(dw, torch.float32, (T, k), "dw")
     pi = _need_shape(idx, torch.int32, (T, k), "idx")
+    p = None if w is None else _need_shape(w, torch.float32, (T, k), "w")
     if dlogits is None:
         dlogits = _empty((T, E), torch.float32, logits.device, stream)
     else:
         _need_shape(dlogits, torch.float32, (T, E), "dlogits")
-    check(lib().ap_route_scored_backward(logits.data_ptr(), T, E, k, pi, pw, kind, 1 if renorm else 0, scale,
-                                         dlogits.data_ptr(), _status(status), _stream(stream)), "route_scored_backward")
+    check(lib().ap_route_scored_backward_weighted(logits.data_ptr(), T, E, k, pi, pw, p, kind, 1 if renorm else 0, scale,
+                                                  dlogits.data_ptr(), _status(status), _stream(stream)), "route_scored_backward")
     return dlogits
 
 

@@ -62,6 +62,7 @@ SIGNATURES = {
     "ap_route_backward": (i32, [P, i64, i32, i32, P, P, P, P, P, i64, P, P, P, P]),
     "ap_route_scored": (i32, [P, i64, i32, i32, i32, P, i32, i32, i32, i32, f32, P, P, P, P, P]),
     "ap_route_scored_backward": (i32, [P, i64, i32, i32, P, P, i32, i32, f32, P, P, P]),
+    "ap_route_scored_backward_weighted": (i32, [P, i64, i32, i32, P, P, P, i32, i32, f32, P, P, P]),
     "ap_route_bias_step": (i32, [P, P, i32, f32, i32, P]),
     "ap_expert_linear_scratch_bytes": (i32, [P, i64, i64, i32, P, i64, i64, i64, i32, P]),
     "ap_expert_linear": (i32, [P, i64, i64, i32, i32, i32, P, P, P, i64, i64, P, i32, P, i64, P, i64, P, i64, i32, P, i64, P, P]),

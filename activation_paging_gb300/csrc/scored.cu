@@ -23,7 +23,9 @@
 //   sigmoid                 dl_j = scale sigma_j (1 - sigma_j) dw_j
 //   softmax, renormalised   dl_j = scale q_j / S u_j
 //   softmax                 dl_e = p_e (scale dw_e - sum_j p_j scale dw_j), all experts
-// The first three touch k logits of a row and write zeros beside.
+// The first three touch k logits of a row and write zeros beside.  Experts that
+// were chosen for want of others (w = 0 forwards) are no part of the sums; which
+// these are the logits do not say, so the weights are read for it.
 #include "route_topk.cuh"
 
 namespace ap {
@@ -531,8 +533,8 @@ __global__ void __launch_bounds__(kScThreads, VEC * N <= 8 ? 4 : VEC * N <= 16 ?
 // which go through a row of shared memory per warp, zero between tokens.
 template <int VEC, int N, bool DENSE>
 __global__ void __launch_bounds__(kScThreads)
-    k_route_scored_backward(const float *logits, int64_t T, int E, int k, const int32_t *idx, const float *dw, bool sigmoid,
-                            bool renorm, float scale, float *dlogits, uint32_t *d_status)
+    k_route_scored_backward(const float *logits, int64_t T, int E, int k, const int32_t *idx, const float *dw, const float *w,
+                            bool sigmoid, bool renorm, float scale, float *dlogits, uint32_t *d_status)
 {
     pdl_begin();
     using Vec = typename ScVec<VEC>::T;
@@ -544,9 +546,14 @@ __global__ void __launch_bounds__(kScThreads)
     const int64_t step = (int64_t)gridDim.x * kScWarps;
     for (int64_t t = (int64_t)blockIdx.x * kScWarps + wid; t < T; t += step) {
         int e = lane < k ? idx[t * k + lane] : 0;
-        const float g = lane < k ? dw[t * k + lane] * scale : 0.f;
-        const bool in = lane < k && e >= 0 && e < E;
+        float g = lane < k ? dw[t * k + lane] * scale : 0.f;
+        bool in = lane < k && e >= 0 && e < E;
         if (lane < k && !in && d_status) atomicOr(d_status, AP_FLAG_BAD_INDEX);
+        if (w) { // chosen for want of others: w = 0, whatever the logits
+            const float was = lane < k ? w[t * k + lane] : 0.f;
+            in = in && was != 0.f;
+            g = !in ? 0.f : was == was ? g : NAN;
+        }
         float v[N][VEC];
         float add = 0.f, dot = 0.f;
         if constexpr (DENSE) {
@@ -678,13 +685,13 @@ template <int VEC, int N> ap_status launch_scored(const ScoredArgs &a, cudaStrea
 
 template <int VEC, int N>
 ap_status launch_scored_backward(bool dense, const float *logits, int64_t T, int E, int k, const int32_t *idx, const float *dw,
-                                 bool sigmoid, bool renorm, float scale, float *dlogits, uint32_t *d_status, cudaStream_t st)
+                                 const float *w, bool sigmoid, bool renorm, float scale, float *dlogits, uint32_t *d_status, cudaStream_t st)
 {
     const size_t smem = (size_t)kScWarps * ((E + 3) & ~3) * 4;
     const int64_t want = (T + kScWarps - 1) / kScWarps;
     auto go = [&](auto *kernel) {
         static const int resident = resident_grid((const void *)kernel, kScThreads, (size_t)kScWarps * VEC * N * kWarp * 4);
-        launch(kernel, (int)(want < resident ? want : resident), kScThreads, smem, st, logits, T, E, k, idx, dw, sigmoid,
+        launch(kernel, (int)(want < resident ? want : resident), kScThreads, smem, st, logits, T, E, k, idx, dw, w, sigmoid,
                renorm, scale, dlogits, d_status);
     };
     if (dense)
@@ -739,6 +746,13 @@ extern "C" ap_status ap_route_scored_backward(const float *logits, int64_t T, in
                                               const float *dw, int32_t score, int32_t renorm, float scale, float *dlogits,
                                               uint32_t *d_status, void *stream)
 {
+    return ap_route_scored_backward_weighted(logits, T, E, k, idx, dw, nullptr, score, renorm, scale, dlogits, d_status, stream);
+}
+
+extern "C" ap_status ap_route_scored_backward_weighted(const float *logits, int64_t T, int32_t E, int32_t k, const int32_t *idx,
+                                                       const float *dw, const float *w, int32_t score, int32_t renorm,
+                                                       float scale, float *dlogits, uint32_t *d_status, void *stream)
+{
     AP_NVTX_RANGE("ap_route_scored_backward");
     using namespace ap;
     if (const ap_status s = scored_sizes("route_scored_backward", T, E, k, score); s != AP_OK) return s;
@@ -748,7 +762,7 @@ extern "C" ap_status ap_route_scored_backward(const float *logits, int64_t T, in
     cudaStream_t st = (cudaStream_t)stream;
     const uintptr_t al = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits);
 #define AP_SCORED_BWD(VEC, N) \
-    return launch_scored_backward<VEC, N>(dense, logits, T, E, k, idx, dw, sigmoid, renorm != 0, scale, dlogits, d_status, st)
+    return launch_scored_backward<VEC, N>(dense, logits, T, E, k, idx, dw, w, sigmoid, renorm != 0, scale, dlogits, d_status, st)
     if (E % 4 == 0 && (al & 15) == 0) {
         if (E <= 128) AP_SCORED_BWD(4, 1);
         if (E <= 256) AP_SCORED_BWD(4, 2);

@@ -91,7 +91,7 @@ class Layer:
         ap.expert_linear_dw(dzz, back, seg, live, dW=q["gate_up"], accumulate=True, status=st, stream=s)
         dxd = ap.expert_linear_dx(dzz, p["gate_up"], seg, live, status=st, stream=s)
         dx = ap.dispatch_backward(dxd, d["dest"], status=st, stream=s).float()
-        dlogits = ap.route_scored_backward(logits, idx, dw, scale=2.0, status=st, stream=s)
+        dlogits = ap.route_scored_backward(logits, idx, dw, scale=2.0, status=st, stream=s, w=w)
         q["router"] += dlogits.t() @ x.float()
         dx += dlogits @ p["router"].float()
         ap.embed_backward(dx, ids, self.V, scale=self.scale, padding_idx=PAD, dtable=q["table"], accumulate=True, status=st, stream=s)

@@ -349,10 +349,21 @@ ap_status ap_route_scored(const float *logits, int64_t T, int32_t E, int32_t k, 
  *            be NULL)
  *   dw       [T, k] float32 (device, read)
  *   dlogits  [T, E] float32 (device, written whole); may be logits itself
- * logits, score, renorm, scale and limits as ap_route_scored. */
+ * logits, score, renorm, scale and limits as ap_route_scored.  The formulas take
+ * every pair for one whose score counts: where rows may have fewer than k experts
+ * to choose from (logits or biases of -infinity), call
+ * ap_route_scored_backward_weighted. */
 ap_status ap_route_scored_backward(const float *logits, int64_t T, int32_t E, int32_t k, const int32_t *idx, const float *dw,
                                    int32_t score, int32_t renorm, float scale, float *dlogits, uint32_t *d_status,
                                    void *stream);
+
+/* The same with the weights that ap_route_scored wrote ([T, k] float32, device,
+ * read; NULL: as above): a pair of weight 0, whose expert was chosen for want of
+ * others, has no gradient and no part in the sums; one of weight NaN makes its
+ * own gradient, and with renorm or softmax its row's, NaN. */
+ap_status ap_route_scored_backward_weighted(const float *logits, int64_t T, int32_t E, int32_t k, const int32_t *idx,
+                                            const float *dw, const float *w, int32_t score, int32_t renorm, float scale,
+                                            float *dlogits, uint32_t *d_status, void *stream);
 
 /* The bias's step towards balance: with n = counts[e] and N their sum over all
  * experts, bias[e] += rate where n < N / E, -= rate where n > N / E.

@@ -55,9 +55,12 @@ def route_scored(logits, k, score="sigmoid", bias=None, groups=1, top_groups=1, 
     return idx.astype(np.int32), w, counts.astype(np.int32), eligible
 
 
-def route_scored_backward(logits, idx, dw, score="sigmoid", renorm=True, scale=1.0):
+def route_scored_backward(logits, idx, dw, score="sigmoid", renorm=True, scale=1.0, eligible=None):
+    """eligible: the pairs that count (route_scored's last result); all without it."""
     T, E = logits.shape
     x, dw = logits.astype(np.float64), dw.astype(np.float64)
+    if eligible is not None:
+        idx = np.where(eligible, idx, -1)
     d = np.zeros((T, E))
     ok = (idx >= 0) & (idx < E)
     at = np.where(ok, idx, 0).astype(np.int64)

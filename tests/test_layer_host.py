@@ -87,3 +87,24 @@ def test_waits_for_whole_sections_go_by_progress():
     assert re.search(r"fetch<OP, PAIR>\([^;]*;\s*\*\(volatile uint32_t \*\)&s_fetched = \+\+count;", text)
     ring = int(re.search(r"kMaxStages = (\d+)", text).group(1))
     assert 1000 * ring * stage_s < least_s
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_plain_gradient_leaves_out_pairs_that_do_not_count(score, renorm):
+    """Against torch's own, of weights that are 0 for such pairs."""
+    g = np.random.default_rng(1)
+    logits = g.standard_normal((30, 8)).astype(np.float32)
+    logits[g.random((30, 8)) < 0.4] = -np.inf
+    logits[:, 2] = 0.5
+    idx, w, _, eligible = layer.route_scored(logits, 4, score, None, 4, 2, 2, renorm, 1.5)
+    assert not eligible.all() and not w[~eligible].any()
+    dw = g.standard_normal((30, 4))
+    x = torch.tensor(logits, dtype=torch.float64, requires_grad=True)
+    s = (torch.sigmoid(x) if score == "sigmoid" else torch.softmax(x, 1)).gather(1, torch.from_numpy(idx).long())
+    s = torch.where(torch.from_numpy(eligible), s, torch.zeros((), dtype=torch.float64))
+    v = 1.5 * (s / s.sum(1, keepdim=True) if renorm else s)
+    np.testing.assert_allclose(v.detach().numpy(), w, rtol=1e-6)
+    (v * torch.from_numpy(dw)).sum().backward()
+    got = layer.route_scored_backward(logits, idx, dw, score, renorm, 1.5, eligible)
+    np.testing.assert_allclose(got, np.nan_to_num(x.grad.numpy()), rtol=1e-9, atol=1e-13)
