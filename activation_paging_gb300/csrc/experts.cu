@@ -1007,14 +1007,17 @@ __global__ void __launch_bounds__(256) k_repitch(const Lot first, const Lot seco
 // not wanted (with it, its stages are added up): a block takes 64 columns of an
 // expert, eight warps every eighth row, two columns a lane.
 __global__ void __launch_bounds__(256) k_expert_bias(const bf16_t *dy, int64_t ld, const int32_t *seg, const int32_t *live, int64_t rows,
-                                                     int N, float *db, bool add)
+                                                     int N, float *db, bool add, uint32_t *d_status)
 {
     pdl_begin();
     __shared__ float s_sum[8][64];
     const int e = blockIdx.y, wid = threadIdx.x / kWarp, lane = (int)lane_id();
     const int at = seg[e];
     int n = live[e];
-    if (n < 0 || at < 0 || (int64_t)at + n > rows) n = 0;
+    if (n < 0 || at < 0 || (int64_t)at + n > rows) {
+        n = 0;
+        if (d_status && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(d_status, AP_FLAG_BAD_COUNT);
+    }
     const int c = blockIdx.x * 64 + lane;
     float s[2] = {0.f, 0.f};
     for (int r = wid; r < n; r += 8) {
@@ -1338,7 +1341,7 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
     }
     if (dbias && !dW) {
         launch(k_expert_bias, dim3((unsigned)((N + 63) / 64), (unsigned)E), 256, 0, st, (const bf16_t *)dy, ldy, d_seg_off, d_live, rows,
-               N, dbias, accumulate != 0);
+               N, dbias, accumulate != 0, d_status);
         AP_CHECK_LAUNCH("expert_linear_dw bias launch");
     }
     return AP_OK;

@@ -54,3 +54,22 @@ def test_products_of_the_longest_contraction(dtype, rows):
     want = sum(a.double() @ b.double() for a, b in zip(dy.split(1 << 17, 1), V.split(1 << 17)))
     assert int(status) == 0
     assert bool(((back - want).abs() <= (HALF * want.abs() if dtype == torch.bfloat16 else 0.0)).all())
+
+
+@pytest.mark.parametrize("N", [8, 200])
+@pytest.mark.parametrize("seg,live", [([0, 10, 31], [10, 20, 30]), ([0, 10, -1], [10, 20, 30]), ([0, 10, 30], [10, 20, -4]),
+                                      ([0, 10, 30], [10, 20, 2 ** 31 - 1]), ([0, 10, 30], [10, 20, 30])])
+def test_bad_segments_of_the_bias_alone(N, seg, live):
+    """The C call without dW says so too, and leaves their experts at 0."""
+    import ctypes
+    dy = whole((60, N), -3, 3, 1)
+    s, n = to_dev(np.array(seg, np.int32)), to_dev(np.array(live, np.int32))
+    db, status = torch.full((3, N), 7.0, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    at = [ctypes.c_void_p(t.data_ptr()) for t in (dy, s, n, db, status)]
+    rc = ap.lib().ap_expert_linear_dw(at[0], N, None, 8, 60, 3, N, 8, at[1], at[2], 0, None, 2, at[3], None, 0, at[4],
+                                      ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == 0
+    good = live[2] == 30 and seg[2] == 30
+    assert int(status) == (0 if good else ap.FLAG_BAD_COUNT)
+    want = torch.stack([dy[:10].float().sum(0), dy[10:30].float().sum(0), dy[30:].float().sum(0) * good])
+    assert torch.equal(db, want)
