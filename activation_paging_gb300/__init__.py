@@ -711,17 +711,25 @@ def expert_linear_dx(dy: torch.Tensor, W: torch.Tensor, seg_off: torch.Tensor, l
     return out
 
 
-def expert_linear_dw(dy: torch.Tensor, x: torch.Tensor, seg_off: torch.Tensor, live: torch.Tensor,
-                     dW: torch.Tensor | None = None, dbias: torch.Tensor | None = None, accumulate: bool = False,
+def expert_linear_dw(dy: torch.Tensor, x: torch.Tensor | None, seg_off: torch.Tensor, live: torch.Tensor,
+                     dW: torch.Tensor | bool | None = None, dbias: torch.Tensor | None = None, accumulate: bool = False,
                      dtype: torch.dtype = torch.float32, scratch: torch.Tensor | None = None,
                      status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient of ``expert_linear``'s weights: dW[e] = the sum of dy[r]^T x[r]
     over the expert's rows ([E, N, K] float32 or BF16), written whole or, with
     ``accumulate``, added to ``dW``; likewise ``dbias`` ([E, N] float32) where
-    given."""
+    given.  ``dW=False``: the gradient of the bias alone, which is returned then
+    (``x`` is of no account)."""
     E, ps, pl = _segments(seg_off, live)
     rows, N, ldy, kind = _rows(dy, "dy")
     py, ldy = _rows16(dy, "dy")
+    if dW is False:
+        if dbias is None:
+            raise ValueError("dW=False needs dbias")
+        check(lib().ap_expert_linear_dw(py, ldy, None, 1, rows, E, N, 1, ps, pl, 1 if accumulate else 0, None, DTYPE_F32,
+                                        _need_shape(dbias, torch.float32, (E, N), "dbias"), None, 0, _status(status),
+                                        _stream(stream)), "expert_linear_dw")
+        return dbias
     K = x.shape[1] if x.dim() == 2 else -1
     px, ldx = _rows16(x, "x", (rows, K))
     if dW is None:

@@ -73,3 +73,21 @@ def test_bad_segments_of_the_bias_alone(N, seg, live):
     assert int(status) == (0 if good else ap.FLAG_BAD_COUNT)
     want = torch.stack([dy[:10].float().sum(0), dy[10:30].float().sum(0), dy[30:].float().sum(0) * good])
     assert torch.equal(db, want)
+
+
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("offset", [0, 3])
+def test_bias_alone_from_python(add, offset):
+    dy = whole((60, 96), -3, 3, 1)[:, offset:offset + 70]
+    s, n = to_dev(np.array([0, 10, 30], np.int32)), to_dev(np.array([10, 0, 25], np.int32))
+    db, status = torch.ones(3, 70, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert ap.expert_linear_dw(dy, None, s, n, dW=False, dbias=db, accumulate=add, status=status) is db
+    want = torch.stack([dy[:10].float().sum(0), torch.zeros(70, device="cuda"), dy[30:55].float().sum(0)]) + (1.0 if add else 0.0)
+    assert torch.equal(db, want) and int(status) == 0
+    again = torch.ones(3, 70, device="cuda")
+    ap.expert_linear_dw(dy, dy, s, n, dbias=again, accumulate=add, dW=torch.zeros(3, 70, 70, device="cuda"))
+    assert torch.equal(db, again)
+    for match, call in (("dbias", lambda: ap.expert_linear_dw(dy, None, s, n, dW=False)),
+                        ("dbias must", lambda: ap.expert_linear_dw(dy, None, s, n, dW=False, dbias=db[:2]))):
+        with pytest.raises(ValueError, match=match):
+            call()
