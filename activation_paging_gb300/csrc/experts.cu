@@ -44,6 +44,14 @@ constexpr int kMaxStages = 10;
 // add with rounding (2.1e-6; by 1024 1.1e-6, but then the products do not hide the
 // writing: 262144 rows over 128 experts, 1024 x 2048 1135 us for 1011).
 constexpr int kSection = 32; // stages
+// FP32 results of the other two (PARTS) likewise, over 1024 places, where the
+// contraction is longer: error 1e-6 whatever its length, for 2.1e-6 at 2048 and
+// 4.4e-6 at 4096.  The writers add a section to the sums so far, which stand in
+// place of the second accumulator, while the products wait: 65536 rows of 2048 to
+// 1024 over 128 experts 229 us for 198, 8192 of 4096 to 4096 over 8 215 for 180.
+// (By 512 4.7e-7, 275 and 244 us; by 2048 199 and 218.  Two accumulators of 160
+// columns beside the sums, by 512: 320 and 249.)
+constexpr int kPart = 16; // stages
 constexpr int kMaxSmem = 232448;
 constexpr int kMaxExperts = 1024;
 constexpr int kPassPitch = 80;     // bytes of 32 lanes' values on their way, with what keeps banks apart
@@ -194,7 +202,7 @@ template <Op OP> __device__ void count_tiles(const ExArgs &a, Table &tab)
 struct Tile {
     int e, f0, c0, n, steps, row0, live, sections;
 };
-template <Op OP, bool PAIR> __device__ __forceinline__ Tile tile_of(const ExArgs &a, const Walk &w, int rank)
+template <Op OP, bool PAIR, bool PARTS> __device__ __forceinline__ Tile tile_of(const ExArgs &a, const Walk &w, int rank)
 {
     Tile t;
     t.e = w.e;
@@ -209,7 +217,7 @@ template <Op OP, bool PAIR> __device__ __forceinline__ Tile tile_of(const ExArgs
     t.n = min(each, width - t.c0);
     t.row0 = w.tab.seg[w.e] + (OP == kWeights ? 0 : t.c0);
     t.steps = OP == kWeights ? ceil_div(t.live, kDepth) : ceil_div(a.K, kDepth);
-    t.sections = OP == kWeights && a.out_f32 ? ceil_div(t.steps, kSection) : t.steps > 0;
+    t.sections = PARTS ? ceil_div(t.steps, kPart) : OP == kWeights && a.out_f32 ? ceil_div(t.steps, kSection) : t.steps > 0;
     return t;
 }
 
@@ -649,7 +657,7 @@ __device__ __forceinline__ void write_weights(const ExArgs &a, const Tile &t, in
 }
 
 // One writer: two for each quarter of the accumulator's lanes.
-template <Op OP, bool PAIR>
+template <Op OP, bool PAIR, bool PARTS>
 __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, int writer, uint32_t tmem, uint64_t *s_done,
                                             uint64_t *s_free, uint8_t *pass, volatile int *dead, const volatile uint32_t *fetched)
 {
@@ -666,10 +674,24 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
         }
     };
     for (; w.find(a.E); w.next()) {
-        const Tile t = tile_of<OP, PAIR>(a, w, rank);
+        const Tile t = tile_of<OP, PAIR, PARTS>(a, w, rank);
         const int f = t.f0 + part * kWarp; // (of weights)
-        for (int section = 0; section == 0 || section < t.sections; ++section) {
-            const uint32_t acc = count & 1, at = tmem + acc * 256 + ((uint32_t)part * kWarp << 16);
+        const uint32_t own = tmem + ((uint32_t)part * kWarp << 16);
+        if constexpr (PARTS) { // sections to their sums, which the epilogue takes
+            for (int section = 0; section < t.sections; ++section, ++count) {
+                ok = __all_sync(0xffffffffu, ok && bar_wait(smem_addr(&s_done[0]), count & 1, dead, fetched));
+                fence_after();
+                if (ok) {
+                    for (int c = (writer >> 2) * 32; c < t.n; c += 64) acc_fold(own + c, own + 256 + c, section > 0);
+                    acc_folded();
+                }
+                fence_before();
+                release(0);
+            }
+        }
+        for (int section = 0; section == 0 || (!PARTS && section < t.sections); ++section) {
+            const uint32_t acc = count & 1, at = own + (PARTS ? 1 : acc) * 256;
+            const bool waits = t.steps > 0 && !PARTS;
             int c = (writer >> 2) * 32;
             Ahead x;
             Kept kept;
@@ -677,13 +699,13 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
                 read_weights(a, t, c, f, kept);
             else
                 read_ahead<OP>(a, t, c, part, x);
-            if (t.steps > 0) {
+            if (waits) {
                 // (for all of a section, which may be a whole expert's rows: as long as stages come)
                 ok = __all_sync(0xffffffffu, ok && bar_wait(smem_addr(&s_done[acc]), count >> 1 & 1, dead, fetched));
                 ++count;
             }
             fence_after();
-            if (c >= t.n && t.steps > 0) release(acc);
+            if (c >= t.n && waits) release(acc);
             for (; c < t.n; c += 64) {
                 const bool last = c + 64 >= t.n;
                 float v[32];
@@ -702,7 +724,7 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
                 }
                 if (last) {
                     fence_before();
-                    if (t.steps > 0) release(acc);
+                    if (waits) release(acc);
                 }
                 if constexpr (OP == kWeights) {
                     const Kept now = kept;
@@ -722,7 +744,7 @@ __device__ __forceinline__ void write_tiles(const ExArgs &a, Walk &w, int rank, 
     if (!ok && a.d_status && lane == 0) atomicOr(a.d_status, AP_FLAG_CORRUPT);
 }
 
-template <Op OP, bool PAIR>
+template <Op OP, bool PAIR, bool PARTS>
 __global__ void __launch_bounds__(kExThreads, 1)
     k_experts(const __grid_constant__ ExMaps m, const ExArgs a)
 {
@@ -775,7 +797,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
             uint32_t count = 0, s = 0, turn = 0; // stages fetched; ring position and its turn
             bool ok = true;
             for (; ok && w.find(a.E); w.next()) {
-                const Tile t = tile_of<OP, PAIR>(a, w, rank);
+                const Tile t = tile_of<OP, PAIR, PARTS>(a, w, rank);
                 for (int step = 0; step < t.steps; ++step) {
                     if (count >= (uint32_t)a.stages && !bar_wait(smem_addr(&s_empty[s]), (turn & 1) ^ 1, dead)) {
                         ok = false;
@@ -809,14 +831,15 @@ __global__ void __launch_bounds__(kExThreads, 1)
             uint32_t s = 0, turn = 0, count = 0; // ring; tiles so far
             bool ok = true;
             for (; ok && w.find(a.E); w.next()) {
-                const Tile t = tile_of<OP, PAIR>(a, w, rank);
+                const Tile t = tile_of<OP, PAIR, PARTS>(a, w, rank);
                 if (t.steps == 0) continue;
                 const uint32_t shape = shape_of(PAIR ? 2 * kLanes : kLanes, PAIR ? (t.n + 31) & ~31 : (t.n + 15) & ~15,
                                                 OP != kForward, OP == kWeights);
-                const int section = t.sections > 1 ? kSection : t.steps;
+                const int section = t.sections <= 1 ? t.steps : PARTS ? kPart : kSection;
+                constexpr int two = !PARTS; // accumulators in turn, or one
                 for (int from = 0; ok && from < t.steps; from += section, ++count) {
-                    const uint32_t acc = count & 1;
-                    ok = count < 2 || bar_wait(smem_addr(&s_free[acc]), (count >> 1 & 1) ^ 1, dead);
+                    const uint32_t acc = two ? count & 1 : 0;
+                    ok = count < 1u + two || bar_wait(smem_addr(&s_free[acc]), (count >> two & 1) ^ 1, dead);
                     fence_after();
                     const int end = min(from + section, t.steps);
                     for (int step = from; ok && step < end; ++step) {
@@ -852,7 +875,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
         uint32_t s = 0, turn = 0;
         bool ok = true;
         for (; w.find(a.E); w.next()) {
-            const Tile t = tile_of<OP, PAIR>(a, w, rank);
+            const Tile t = tile_of<OP, PAIR, PARTS>(a, w, rank);
             const uint32_t across = ceil_div(a.K, a.columns), c = t.c0 / a.columns, first = w.t - c, by = w.step;
             const bool adds = a.db && c == first / (by % across ? across : by) % across;
             float sum[8] = {};
@@ -908,7 +931,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
         }
     } else if (wid >= 4) {
         // ---- write
-        write_tiles<OP, PAIR>(a, w, rank, wid - 4, tmem, s_done, s_free, s_pass + (wid - 4) * kPassOf, dead, &s_fetched);
+        write_tiles<OP, PAIR, PARTS>(a, w, rank, wid - 4, tmem, s_done, s_free, s_pass + (wid - 4) * kPassOf, dead, &s_fetched);
     }
     __syncwarp();
     fence_before();
@@ -1048,9 +1071,9 @@ bool mappable(const void *p, int64_t ld, int64_t more = 0)
 }
 
 // The stages that fit the shared memory, and its bytes: as many as the kernel's attribute allows (0: an error).
-template <Op OP, bool PAIR> size_t stages_of(ExArgs &a)
+template <Op OP, bool PAIR, bool PARTS> size_t stages_of(ExArgs &a)
 {
-    const auto kernel = k_experts<OP, PAIR>;
+    const auto kernel = k_experts<OP, PAIR, PARTS>;
     static const int fixed = [&] {
         cudaFuncAttributes attr;
         if (cudaFuncGetAttributes(&attr, (const void *)kernel) != cudaSuccess) return -1;
@@ -1064,18 +1087,18 @@ template <Op OP, bool PAIR> size_t stages_of(ExArgs &a)
     return (size_t)a.stages * stage + 1024;
 }
 // Pairs of blocks that the stream's SMs take at once (a partition may take none).
-template <Op OP> int pairs_of(ExArgs a, cudaStream_t st)
+template <Op OP, bool PARTS> int pairs_of(ExArgs a, cudaStream_t st)
 {
-    const size_t smem = stages_of<OP, true>(a);
-    return smem ? cluster_count((const void *)k_experts<OP, true>, kExThreads, smem, 2, st) : 0;
+    const size_t smem = stages_of<OP, true, PARTS>(a);
+    return smem ? cluster_count((const void *)k_experts<OP, true, PARTS>, kExThreads, smem, 2, st) : 0;
 }
 
 // `pairs`: that many at most, of two blocks each; 0: single blocks
-template <Op OP, bool PAIR = false>
+template <Op OP, bool PAIR, bool PARTS>
 ap_status launch_experts(const char *who, const ExMaps &m, ExArgs a, int64_t tiles, int pairs, cudaStream_t st)
 {
-    const auto kernel = k_experts<OP, PAIR>;
-    const size_t smem = stages_of<OP, PAIR>(a);
+    const auto kernel = k_experts<OP, PAIR, PARTS>;
+    const size_t smem = stages_of<OP, PAIR, PARTS>(a);
     if (!smem) return cuda_fail(cudaGetLastError(), who);
     if constexpr (PAIR) {
         launch_cluster(kernel, 2 * (int)(tiles < pairs ? tiles : pairs), kExThreads, smem, 2, st, m, a);
@@ -1142,6 +1165,12 @@ int columns_for(int64_t rows, int32_t E)
     return each > 128 ? 256 : each > 32 ? 128 : 64;
 }
 
+template <Op OP, bool PARTS>
+ap_status rows_launch(const char *who, const ExMaps &m, const ExArgs &a, int64_t tiles, int pairs, cudaStream_t st)
+{
+    return pairs ? launch_experts<OP, true, PARTS>(who, m, a, tiles, pairs, st) : launch_experts<OP, false, PARTS>(who, m, a, tiles, 0, st);
+}
+
 ap_status rows_product(const char *who, Op op, ExArgs a, int halves, void *scratch, int64_t scratch_bytes, cudaStream_t st)
 {
     if (a.E == 1) a.lde = a.ldw * (op == kForward ? a.F * halves : a.K); // (of no account)
@@ -1152,6 +1181,7 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, void *scrat
         r != AP_OK)
         return r;
     a.columns = columns_for(a.rows, a.E);
+    const bool parts = a.out_f32 && a.K > kPart * kDepth;
     a.vec_out = !odd_address(a.out, 16) && a.ldo % 8 == 0 && a.F % 8 == 0;
     a.vec_pre = !odd_address(a.pre, 16) && a.ldpre % 8 == 0 && a.F % 8 == 0;
     a.vec_res = !odd_address(a.residual, 16) && a.ldres % 8 == 0 && a.F % 8 == 0;
@@ -1159,7 +1189,8 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, void *scrat
     // 128 experts: 476 us for 545).
     int pairs = 0;
     if (a.columns == 256 && a.F * (op == kForward ? halves : 1) > kLanes)
-        pairs = op == kForward ? pairs_of<kForward>(a, st) : pairs_of<kRows>(a, st);
+        pairs = op == kForward ? (parts ? pairs_of<kForward, true>(a, st) : pairs_of<kForward, false>(a, st))
+                               : (parts ? pairs_of<kRows, true>(a, st) : pairs_of<kRows, false>(a, st));
     const int per = (op == kForward && halves == 2 ? kLanes / 2 : kLanes) * (pairs ? 2 : 1);
     a.tiles_f = (a.F + per - 1) / per;
     const int64_t tiles = (a.rows / a.columns + a.E) * (int64_t)a.tiles_f;
@@ -1185,10 +1216,9 @@ ap_status rows_product(const char *who, Op op, ExArgs a, int halves, void *scrat
         ok = ok && make_map(&m.w, a.W, 3, ew, pw, bw);
     }
     if (!ok) return fail(AP_ENOTSUP, "%s: no tensor map of these sizes", who);
-    if (pairs)
-        return op == kForward ? launch_experts<kForward, true>(who, m, a, tiles, pairs, st)
-                              : launch_experts<kRows, true>(who, m, a, tiles, pairs, st);
-    return op == kForward ? launch_experts<kForward>(who, m, a, tiles, 0, st) : launch_experts<kRows>(who, m, a, tiles, 0, st);
+    if (op == kForward)
+        return parts ? rows_launch<kForward, true>(who, m, a, tiles, pairs, st) : rows_launch<kForward, false>(who, m, a, tiles, pairs, st);
+    return parts ? rows_launch<kRows, true>(who, m, a, tiles, pairs, st) : rows_launch<kRows, false>(who, m, a, tiles, pairs, st);
 }
 
 } // namespace
@@ -1337,7 +1367,7 @@ extern "C" ap_status ap_expert_linear_dw(const void *dy, int64_t ldy, const void
                 (a.chunk_x && !make_map(&m.xx, a.x, 3, ey, py, box)) || (a.chunk_w && !make_map(&m.ww, a.W, 3, ex, px, box)))
                 return fail(AP_ENOTSUP, "%s: no tensor map of these sizes", who);
         }
-        if (const ap_status s = launch_experts<kWeights>(who, m, a, tiles, 0, st); s != AP_OK) return s;
+        if (const ap_status s = launch_experts<kWeights, false, false>(who, m, a, tiles, 0, st); s != AP_OK) return s;
     }
     if (dbias && !dW) {
         launch(k_expert_bias, dim3((unsigned)((N + 63) / 64), (unsigned)E), 256, 0, st, (const bf16_t *)dy, ldy, d_seg_off, d_live, rows,

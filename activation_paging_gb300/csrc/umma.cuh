@@ -220,6 +220,41 @@ __device__ __forceinline__ void acc_load_tiles(uint32_t at, float (&v)[2][16])
         for (int i = 0; i < 16; ++i) v[h][i] = __uint_as_float(r[h][i]);
 }
 
+// The same 32 lanes and columns of one place added to those of another (add) or
+// put there: columns that no product writes.  acc_folded() ends the stores.
+__device__ __forceinline__ void acc_fold(uint32_t from, uint32_t to, bool add)
+{
+    uint32_t r[32], q[32];
+    if (add) {
+        asm volatile(
+                     "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%64];\n\t"
+                     "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%65];\n\t"
+                     "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47}, [%66];\n\t"
+                     "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%67];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                       "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+                       "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]), "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15]),
+                       "=r"(q[16]), "=r"(q[17]), "=r"(q[18]), "=r"(q[19]), "=r"(q[20]), "=r"(q[21]), "=r"(q[22]), "=r"(q[23]), "=r"(q[24]), "=r"(q[25]), "=r"(q[26]), "=r"(q[27]), "=r"(q[28]), "=r"(q[29]), "=r"(q[30]), "=r"(q[31])
+                     : "r"(from), "r"(from + (1u << 20)), "r"(to), "r"(to + (1u << 20))
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(q[i]));
+    } else {
+        float v[2][16];
+        acc_load_tiles(from, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i / 16][i % 16]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+                     "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(to + ((uint32_t)h << 20)),
+                     "r"(r[h * 16 + 0]), "r"(r[h * 16 + 1]), "r"(r[h * 16 + 2]), "r"(r[h * 16 + 3]), "r"(r[h * 16 + 4]), "r"(r[h * 16 + 5]), "r"(r[h * 16 + 6]), "r"(r[h * 16 + 7]), "r"(r[h * 16 + 8]), "r"(r[h * 16 + 9]), "r"(r[h * 16 + 10]), "r"(r[h * 16 + 11]), "r"(r[h * 16 + 12]), "r"(r[h * 16 + 13]), "r"(r[h * 16 + 14]), "r"(r[h * 16 + 15])
+                     : "memory");
+}
+__device__ __forceinline__ void acc_folded() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // ---- 8 x 8 matrices of 16-bit values, transposed on their way --------------------------
 // Lane l gives the address of row l % 8 of matrix l / 8 in memory; a lane holds
 // two neighbours of a column there.

@@ -390,7 +390,8 @@ ap_status ap_route_bias_step(float *bias, int32_t *counts, int32_t E, float rate
  * give equal bits.  The tensor cores' FP32 sums cut instead of rounding: their
  * error is about 1.1e-9 of the result's size for each place of the contraction
  * (for numbers of one sign up to 5e-9), below the rounding to BF16 up to some
- * 10^6 places; FP32 weights' gradients are added up by sections of 2048 rows.
+ * 10^6 places; FP32 weights' gradients are added up by sections of 2048 rows,
+ * other FP32 results by sections of 1024 places (error 1e-6 at any length).
  * Should operands not arrive within a bounded wait (no input leads to that),
  * AP_FLAG_CORRUPT is set and the rows that lack them get NaN.
  *

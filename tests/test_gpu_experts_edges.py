@@ -91,3 +91,53 @@ def test_bias_alone_from_python(add, offset):
                         ("dbias must", lambda: ap.expert_linear_dw(dy, None, s, n, dW=False, dbias=db[:2]))):
         with pytest.raises(ValueError, match=match):
             call()
+
+
+def section_bound(C):
+    """FP32 results of a contraction of C places: sections of 1024 in the tensor cores, 17 x 2^-23 of the sum of magnitudes
+    for each 16 places and once more, and a rounding for each section added up."""
+    return (1024 / 16 + 1) * 17 * 2 * U + (C / 1024 + 1) * U
+
+
+@pytest.mark.parametrize("live", [[200, 0, 90], [3, 1, 0], [700, 161, 33]])
+@pytest.mark.parametrize("act", [None, "silu", "swiglu"])
+@pytest.mark.parametrize("K", [65536, 8200])
+def test_float_results_of_long_contractions(live, act, K):
+    """Numbers of one sign, whose cut sums are all off the same way: at 65536 places by 3e-4 if they were added up in one."""
+    E, N = len(live), 136 if K == 65536 else 300
+    wide = 2 * N if act == "swiglu" else N
+    seg = np.concatenate([[0], np.cumsum(live)[:-1] + 2]).astype(np.int32)
+    n, rows = np.array(live, np.int32), int(sum(live)) + 5
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = (torch.rand(rows, K, generator=g, device="cuda") + 0.5).bfloat16()
+    W = (torch.rand(E, wide, K, generator=g, device="cuda") + 0.5).mul_(1 / K).bfloat16()
+    res, bias = torch.randn(rows, N, generator=g, device="cuda").bfloat16(), torch.randn(E, wide, generator=g, device="cuda")
+    out = ap.expert_linear(x, W, to_dev(seg), to_dev(n), bias=bias, act=act, residual=res, dtype=torch.float32,
+                           out=torch.full((rows, N), 7.0, device="cuda"))
+    again = ap.expert_linear(x, W, to_dev(seg), to_dev(n), bias=bias, act=act, residual=res, dtype=torch.float32,
+                             out=torch.full((rows, N), 7.0, device="cuda"))
+    assert torch.equal(out, again)
+    back = ap.expert_linear_dx(x, W.transpose(1, 2).contiguous(), to_dev(seg), to_dev(n), dtype=torch.float32,
+                               out=torch.full((rows, wide), 7.0, device="cuda"))
+    on = np.zeros(rows, bool)
+    for e, at in layer.expert_rows(seg, n, rows):
+        on[torch.arange(rows).numpy()[at]] = True
+        z = x[at].double() @ W[e].double().t()
+        off = section_bound(K) * z  # (all terms are positive)
+        assert bool(((back[at].double() - z).abs() <= off + U * z).all())
+        b = bias[e].double()
+        z, off = z + b, off + U * ((z + b).abs() + b.abs())
+        if act == "swiglu":
+            zg, zu, dg, du = z[:, :N], z[:, N:], off[:, :N], off[:, N:]
+            want = torch.nn.functional.silu(zg) * zu
+            # silu' <= 1.1, its own error (1.5 |z| + 12) u of itself
+            off = 1.1 * dg * (zu.abs() + du) + zg.abs() * du + (1.5 * zg.abs() + 14) * U * want.abs()
+        elif act == "silu":
+            want = torch.nn.functional.silu(z)
+            off = 1.1 * off + (1.5 * z.abs() + 12) * U * want.abs()
+        else:
+            want = z
+        want = want + res[at].double()
+        off = off + 2 * U * (want.abs() + res[at].double().abs())
+        assert bool(((out[at].double() - want).abs() <= off).all())
+    assert bool((out[torch.from_numpy(~on).cuda()] == 7.0).all()) and bool((back[torch.from_numpy(~on).cuda()] == 7.0).all())
