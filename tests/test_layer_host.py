@@ -83,7 +83,7 @@ def test_waits_for_whole_sections_go_by_progress():
     assert "kTries = 1u << 20" in source("umma.cuh")
     waits = re.findall(r"bar_wait\(((?:[^()]|\([^()]*\))*)\)", text)
     done = [w for w in waits if "s_done" in w]
-    assert len(done) == 1 and done[0].rstrip().endswith("dead, fetched")
+    assert done and all(w.rstrip().endswith("dead, fetched") for w in done)
     assert re.search(r"fetch<OP, PAIR>\([^;]*;\s*\*\(volatile uint32_t \*\)&s_fetched = \+\+count;", text)
     ring = int(re.search(r"kMaxStages = (\d+)", text).group(1))
     assert 1000 * ring * stage_s < least_s
