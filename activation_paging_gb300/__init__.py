@@ -433,7 +433,8 @@ class AdamW:
         if kind not in _ROW_TYPES:
             raise ValueError(f"params must be bfloat16 or float32, got {kind}")
         for i, p in enumerate(self.params):
-            _need(p, kind, f"params[{i}]")
+            if p.dtype != kind or not p.is_cuda or not p.is_contiguous():
+                _need(p, kind, f"params[{i}]")
         if master is True:
             master = [p.float() for p in self.params]
         self.master = None if master is None or master is False else list(master)
@@ -467,7 +468,7 @@ class AdamW:
         at = {n: self.state[n].data_ptr() for n in need}
         for i, (p, (off, n)) in enumerate(zip(self.params, self.parts)):
             e = self._table[i]
-            e.param, e.n, e.m, e.v = p.data_ptr(), n, at["m"] + off * size, at["v"] + off * size
+            e.param, e.n, e.m, e.v = self._held[0][i], n, at["m"] + off * size, at["v"] + off * size
             if eight:
                 e.m_scale, e.v_scale = at["m_scale"] + off // self.BLOCK * 4, at["v_scale"] + off // self.BLOCK * 4
             if self.master is not None:
@@ -493,18 +494,19 @@ class AdamW:
         return list(map(torch.Tensor.data_ptr, tensors)), list(range(len(tensors))), [t.untyped_storage() for t in tensors]
 
     @staticmethod
-    def _stay(tensors, held, what: str):
-        """Refuses tensors that are not where the table has them (one call compares all: 32 ns each, 61 by data_ptr())."""
+    def _stay(tensors, held) -> bool:
+        """Whether tensors are where the table has them (one call compares all: 32 ns each, 61 by data_ptr())."""
         at, all_of, _ = held
-        if len(tensors) != len(at) or not torch._C._tensors_data_ptrs_at_indices_equal(tensors, at, all_of):
-            raise ValueError(what)
+        return len(tensors) == len(at) and torch._C._tensors_data_ptrs_at_indices_equal(tensors, at, all_of)
 
     def _stay_written(self):
-        self._stay(self._written(), self._held, "params, master copies or state have moved since the optimizer was made: "
-                                                "copy into them, or make a new optimizer")
+        if not self._stay(self._written(), self._held):
+            raise ValueError("params, master copies or state have moved since the optimizer was made: copy into them, or make "
+                             "a new optimizer")
 
     def _stay_grads(self):
-        self._stay(self.grads, self._grads_held, "grads have moved since they were bound: bind them again")
+        if not self._stay(self.grads, self._grads_held):
+            raise ValueError("grads have moved since they were bound: bind them again")
 
     @staticmethod
     def _apart(tensors):
@@ -523,11 +525,13 @@ class AdamW:
         if kind not in _ROW_TYPES:
             raise ValueError(f"grads must be bfloat16 or float32, got {kind}")
         for i, (p, g) in enumerate(zip(self.params, grads)):
-            _need_shape(g, kind, p.shape, f"grads[{i}]")
-        for e, g in zip(self._table, grads):
-            e.grad = g.data_ptr()
+            if g.shape != p.shape or g.dtype != kind or not g.is_cuda or not g.is_contiguous():
+                _need_shape(g, kind, p.shape, f"grads[{i}]")
+        held = self._hold(grads)
+        for e, p in zip(self._table, held[0]):
+            e.grad = p
         self.grads, self._cfg.grad_dtype = grads, _ROW_TYPES[kind]
-        self._grads_held = self._hold(grads)
+        self._grads_held = held
 
     @staticmethod
     def _word(t, name: str):
