@@ -448,7 +448,8 @@ ap_status ap_expert_linear_dx(const void *dy, int64_t ldy, int64_t rows, int32_t
 
 /* Gradients of weights and bias:
  *   dW[e] = sum over rows r of expert e of dy[r]^T x[r]    dbias[e] = sum dy[r]
- * accumulate = 1: added to what is there (one rounding), else written whole
+ * accumulate = 1: added to what is there (BF16: one rounding; FP32: one for each
+ * section of 2048 rows), else written whole
  * (zeros for an expert without rows).
  *   dW    [E, N, K] of dw_dtype (BF16 or F32), contiguous (device) or NULL
  *   dbias [E, N] float32, contiguous (device) or NULL; not both NULL
@@ -589,8 +590,9 @@ ap_status ap_adamw_step(const ap_adamw_tensor *tensors, int32_t n, const ap_adam
  * what clips it: out[0] = norm, out[1] = max_norm / norm where max_norm > 0 and
  * norm > max_norm, else 1; NaN where the norm is not finite, so that
  * ap_adamw_step with d_scale = out + 1 skips the step.  Squares are single
- * precision, eight of them added up as such, their sums in pairs of numbers, in
- * an order that depends on the sizes alone: equal inputs give equal bits.
+ * precision (so a gradient above 1.8e19 counts as not finite, one below 1e-23 as
+ * 0), eight of them added up as such, their sums in pairs of numbers, in an order
+ * that depends on the sizes alone: equal inputs give equal bits.
  *   out     [2] float32 (device, written)
  *   scratch device work space of ap_grad_norm_scratch_bytes() bytes, 16-byte
  *           aligned; its contents need no initialisation */
