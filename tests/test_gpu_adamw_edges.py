@@ -229,3 +229,27 @@ def test_rounding_by_values_is_seeded_and_repeats():
         return list(o.state.values()) + o.params
     a, b, c = run(1), run(1), run(2)
     assert all(torch.equal(x, y) for x, y in zip(a, b)) and not torch.equal(a[1], c[1])
+
+
+@pytest.mark.parametrize("rounding", ["codes", "values"])
+def test_captured_steps_read_the_skip_word_at_each_replay(rounding):
+    def make():
+        g = torch.Generator(device="cuda").manual_seed(2)
+        params = [torch.randn(n, generator=g, device="cuda").bfloat16() for n in (700, 3, 5000)]
+        grads = [torch.randn(n, generator=g, device="cuda") for n in (700, 3, 5000)]
+        return ap.AdamW(params, grads, master=True, state_bits=8, rounding=rounding, seed=3)
+    a, b = make(), make()
+    word, side = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        a.step(skip=word)
+    steps = 0
+    for skip in (0, 1, 1, 0, 2 ** 31 - 1, 0):
+        word.fill_(skip)
+        graph.replay()
+        b.step(skip=word)
+        steps += skip == 0
+        assert host(a.state["step"]).tolist() == host(b.state["step"]).tolist() == [steps, 0]
+    for x, y in zip(a.params + a.master + list(a.state.values()), b.params + b.master + list(b.state.values())):
+        assert torch.equal(x, y)

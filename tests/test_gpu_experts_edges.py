@@ -141,3 +141,33 @@ def test_float_results_of_long_contractions(live, act, K):
         off = off + 2 * U * (want.abs() + res[at].double().abs())
         assert bool(((out[at].double() - want).abs() <= off).all())
     assert bool((out[torch.from_numpy(~on).cuda()] == 7.0).all()) and bool((back[torch.from_numpy(~on).cuda()] == 7.0).all())
+
+
+def test_float_results_in_a_graph_and_on_another_stream():
+    """Sections of a long contraction, with counts that change between replays."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, W = torch.randn(600, 3000, generator=g, device="cuda").bfloat16(), torch.randn(2, 260, 3000, generator=g, device="cuda").bfloat16()
+    seg, live = to_dev(np.array([0, 300], np.int32)), to_dev(np.array([300, 300], np.int32))
+    out, side, graph = torch.empty(600, 130, device="cuda"), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        ap.expert_linear(x, W, seg, live, act="swiglu", out=out)
+    for counts in ((300, 300), (1, 299), (0, 17), (257, 0)):
+        live.copy_(torch.tensor(counts, dtype=torch.int32))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = torch.full_like(out, 7.0)
+        with torch.cuda.stream(side):
+            ap.expert_linear(x, W, seg, live, act="swiglu", out=want, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert bool((out[counts[0]:300] == 7.0).all()) and bool((out[300 + counts[1]:] == 7.0).all())
+        for e, n in enumerate(counts):
+            z = x[300 * e:300 * e + n].double() @ W[e].double().t()
+            size = x[300 * e:300 * e + n].double().abs() @ W[e].double().abs().t()
+            off, zg, zu = section_bound(3000) * size, z[:, :130], z[:, 130:]
+            h = torch.nn.functional.silu(zg)
+            got = out[300 * e:300 * e + n].double()
+            bound = 1.1 * off[:, :130] * (zu.abs() + off[:, 130:]) + h.abs() * off[:, 130:] + (1.5 * zg.abs() + 14) * U * (h * zu).abs()
+            assert bool(((got - h * zu).abs() <= bound + 1e-30).all())

@@ -92,3 +92,21 @@ def test_weights_of_the_gradient_are_checked():
     for bad in (w[:2], w.double(), w.cpu(), w.t().contiguous().t()):
         with pytest.raises(ValueError, match="w must"):
             ap.route_scored_backward(logits, idx, w, w=bad)
+
+
+def test_gradient_with_weights_in_a_graph_and_in_place():
+    logits = torch.from_numpy(short_rows(300, 64, 4)).cuda()
+    idx, w = ap.route_scored(logits, 8, groups=4, top_groups=2)
+    dw, d, graph = torch.randn_like(w), torch.empty_like(logits), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        ap.route_scored(logits, 8, groups=4, top_groups=2, idx=idx, w=w)
+        ap.route_scored_backward(logits, idx, dw, dlogits=d, w=w)
+    logits.copy_(logits.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    i, we = ap.route_scored(logits, 8, groups=4, top_groups=2)
+    assert torch.equal(i, idx) and torch.equal(we, w)
+    same = logits.clone()
+    ap.route_scored_backward(same, i, dw, dlogits=same, w=we)
+    assert torch.equal(same, d) and bool(torch.isfinite(d).all())
