@@ -1274,7 +1274,7 @@ extern "C" ap_status ap_expert_linear(const void *x, int64_t ldx, int64_t rows, 
     if (const ap_status s = check_rows(who, rows, E, N, K, ldx, K, ldw, K, lde, 0); s != AP_OK) return s;
     if (out_dtype != AP_DTYPE_BF16 && out_dtype != AP_DTYPE_F32) return fail(AP_EINVAL, "%s: type %d", who, out_dtype);
     if (ldo < N || (residual && ldres < N) || (pre && ldpre < (int64_t)halves * N)) return fail(AP_EINVAL, "%s: bad pitches", who);
-    if (E > 1 && lde < ((int64_t)halves * N - 1) * ldw + K) return fail(AP_EINVAL, "%s: experts' weights overlap", who);
+    if (E > 1 && lde < ((int64_t)halves * N - 1) * ldw + K) return fail(AP_EINVAL, "%s: experts' weights overlap or interleave", who);
     if (rows == 0) return AP_OK;
     if (!x || !d_seg_off || !d_live || !W || !out) return fail(AP_EINVAL, "%s: NULL pointer", who);
     if (odd_address(x, 2) || odd_address(W, 2) || odd_address(residual, 2) || odd_address(pre, 2) || odd_address(bias, 4) ||
@@ -1303,7 +1303,7 @@ extern "C" ap_status ap_expert_linear_dx(const void *dy, int64_t ldy, int64_t ro
     if (dx_dtype != AP_DTYPE_BF16 && dx_dtype != AP_DTYPE_F32) return fail(AP_EINVAL, "%s: type %d", who, dx_dtype);
     if (ldx < (int64_t)halves * K || (residual && ldres < K) || (act != AP_ACT_NONE && ldpre < (int64_t)halves * K))
         return fail(AP_EINVAL, "%s: bad pitches", who);
-    if (E > 1 && lde < ((int64_t)N - 1) * ldw + K) return fail(AP_EINVAL, "%s: experts' weights overlap", who);
+    if (E > 1 && lde < ((int64_t)N - 1) * ldw + K) return fail(AP_EINVAL, "%s: experts' weights overlap or interleave", who);
     if (rows == 0) return AP_OK;
     if (!dy || !d_seg_off || !d_live || !W || !dx || (act != AP_ACT_NONE && !pre)) return fail(AP_EINVAL, "%s: NULL pointer", who);
     if (odd_address(dy, 2) || odd_address(W, 2) || odd_address(residual, 2) || odd_address(pre, 2) ||

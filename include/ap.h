@@ -407,7 +407,8 @@ ap_status ap_route_bias_step(float *bias, int32_t *counts, int32_t E, float rate
  *            aligned; its contents need no initialisation.  Operands whose bases
  *            lie on 16 bytes and whose pitches are multiples of 8 elements need 0
  *            bytes (NULL); others are copied to such rows first
- * Limits: 0 <= rows < 2^31, 1 <= E <= 1024, 1 <= N, K <= 2^20.
+ * Limits: 0 <= rows < 2^31, 1 <= E <= 1024, 1 <= N, K <= 2^20; an expert's weights
+ * lie behind the one before's (E > 1: lde >= (rows of W[e] - 1) ldw + K).
  * ========================================================================== */
 #define AP_ACT_NONE 0
 #define AP_ACT_SILU 1
